@@ -27,7 +27,8 @@
  *    any CUDA call; a failed check returns PISA_EINVAL / PISA_EUNSUPPORTED /
  *    PISA_EWORKSPACE and enqueues nothing. A launch failure returns PISA_ECUDA. The text
  *    of the last error of the calling thread is returned by pisa_last_error().
- *  - Supported in this build: d in {64,128}, C = 64, g in {2,4} (4 for the entry points
+ *  - Supported by the selection, the selected blocks' attention and its decode step (the window
+ *    attention and the query/key norm state their own): d in {64,128}, C = 64, g in {2,4} (4 for the entry points
  *    named under pisa_shape_t), 1 <= K <= 32 with gK <= 64, G in {1,2,4,8},
  *    1 <= N <= 2^24, B*U*N*gK < 2^31 (U = Hkv, or Hq for a per-head selection) and
  *    B*N*Hq < 2^31. Anything else returns PISA_EUNSUPPORTED.
@@ -42,7 +43,7 @@
 extern "C" {
 #endif
 
-#define PISA_VERSION 4
+#define PISA_VERSION 5
 #define PISA_MAX_LEVELS 32
 
 enum {
@@ -277,6 +278,118 @@ int pisa_decode_step(const pisa_decode_shape_t* shape, const int32_t* pos, void*
                      void* Vcache, float* pyr_sum, const void* q, const void* k_new,
                      const void* v_new, void* o, int32_t* idx, float* score, int32_t* status,
                      void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Sliding-window attention with sinks: the local attention that stands beside the selected
+ * blocks' attention (the digest's and the explainer's pages have no counterpart; layers of a
+ * model alternate the two). Row i of Q sits at position p = i + N - Nq (Nq < N: the queries
+ * are the last ones, a chunk of a prompt against the keys so far) and sees key j iff
+ *     j <= p,  j < L,  p < L  and  (p - j < window  or  j < sinks),
+ * L = len[b] clamped to [0, N] (N where len is NULL): a right-padded batch. window >= N is
+ * full causal attention. A row at p >= L sees nothing: O = 0, lse = -inf, dQ = 0; dK and dV
+ * of keys that no row sees are 0. Every output element is written.
+ *
+ * Q [B,Nq,Hq,d], K, V [B,N,Hkv,d] bf16 with d and the heads contiguous; *_stride is the
+ * distance between consecutive tokens in elements (0: contiguous, H*d; a multiple of 8, at
+ * least H*d), batches follow one another (B*N equally spaced tokens), so slices of a fused
+ * projection need no copy. O, dO, dQ [B,Nq,Hq,d], dK, dV [B,N,Hkv,d] bf16 and lse [B,Hq,Nq]
+ * fp32 are contiguous. Any group size G = Hq / Hkv <= 64; d in {64, 128}; 1 <= Nq <= N <= 2^24;
+ * B*N*Hq < 2^31. scale as in pisa_shape_t.
+ * Values at tokens j >= L (an uninitialised cache, padding) are never used, whatever they
+ * are. Non-finite values at tokens j < L can reach the rows of any query near them, masked
+ * or not. */
+typedef struct {
+  int32_t B, Nq, N, Hq, Hkv, d, window, sinks;
+  float scale;
+  int32_t q_stride, k_stride, v_stride;
+} pisa_window_shape_t;
+
+/* pisa_window_workspace_size's `op`. */
+enum { PISA_WINDOW_FWD = 0, PISA_WINDOW_BWD = 1 };
+
+/* Bytes of workspace of the window attention's calls (host-only). The first 256 bytes are the
+ * status block. */
+int pisa_window_workspace_size(const pisa_window_shape_t* shape, int op, size_t* bytes);
+
+/* O = softmax over the visible keys of (s q.k) times V, lse = log sum exp(s q.k). len: device
+ * [B] int32, may be NULL. A bounded wait that gives up poisons the rows it leaves unfinished
+ * (O = NaN, lse = NaN) and sets PISA_STATUS_TIMEOUT. Workspace: PISA_WINDOW_FWD. */
+int pisa_window_attn_fwd(const pisa_window_shape_t* shape, const void* Q, const void* K, const void* V,
+                         const int32_t* len, void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* With P = exp(s q.k - lse), D = dO.O and dS = P (dO.v - D) on the visible pairs:
+ * dQ = s dS K, dK = s dS^T Q, dV = P^T dO; dK and dV sum over the group's heads. O and lse from
+ * the forward of the same inputs. The sums' order is fixed: the same call gives the same bits.
+ * A bounded wait that gives up poisons the gradients it leaves unfinished (NaN).
+ * Workspace: PISA_WINDOW_BWD. */
+int pisa_window_attn_bwd(const pisa_window_shape_t* shape, const void* Q, const void* K, const void* V,
+                         const void* O, const float* lse, const void* dO, const int32_t* len, void* dQ,
+                         void* dK, void* dV, void* ws, size_t ws_bytes, void* stream);
+
+/* Decode shape of the window attention. Ncap: cache capacity in tokens per sequence. */
+typedef struct {
+  int32_t B, Ncap, Hq, Hkv, d, window, sinks;
+  float scale;
+} pisa_window_decode_shape_t;
+
+/* One decode step of the window attention for every sequence, in one launch: writes k_new and
+ * v_new into the cache at the slot of p = pos[b] and attends from q over the keys that p sees.
+ * Rolling cache: position j lives in slot j for j < Ncap, and from there on the slots behind
+ * the sinks are reused in turn: slot(j) = j < sinks ? j : sinks + (j - sinks) % (Ncap - sinks)
+ * (which is j itself up to Ncap). Ncap >= sinks + window never drops a visible key; a smaller
+ * Ncap > sinks holds positions below Ncap only.
+ *   pos device [B] int32 (read, not advanced); Kcache, Vcache [B,Ncap,Hkv,d] bf16 (read, one
+ *   slot per sequence and KV head written); q [B,Hq,d], k_new, v_new [B,Hkv,d] bf16 (read);
+ *   o [B,Hq,d] bf16, lse [B,Hq] fp32 (may be NULL) (written).
+ *   status: device int32 word; PISA_STATUS_POS_RANGE is ORed in when some pos[b] is negative,
+ *   or at or past Ncap with Ncap < sinks + window; that sequence is then left untouched.
+ * G <= 64, d in {64, 128}, Ncap <= 2^24. Keys at slots that p does not see are never used,
+ * whatever their values. */
+int pisa_window_decode_step(const pisa_window_decode_shape_t* shape, const int32_t* pos, void* Kcache,
+                            void* Vcache, const void* q, const void* k_new, const void* v_new, void* o,
+                            float* lse, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Queries and keys made ready for the selection, the attentions and the decode steps: the
+ * RMS norm of every head and the rotation by position, in one pass (no counterpart on the
+ * pages; every Q and K above is such an output). Per row x (a token's head, d elements):
+ *     h = x / sqrt(mean(x^2) + eps)  (norm = 1; h = x with norm = 0),   y = h * w,
+ * then pair c < rot/2 of y's first `rot` elements, (2c, 2c+1) with interleaved = 1 or
+ * (c, c + rot/2) with interleaved = 0, turns by the angle pos * inv_freq[c] and is multiplied
+ * by rot_scale:
+ *     (a, b) -> rot_scale (a cos - b sin, a sin + b cos);
+ * elements rot .. d-1 pass unturned. pos * inv_freq is formed exactly (fixed point, modulo a
+ * turn) for every int32 position, so far positions lose nothing.
+ * d in {64, 128}; rot a multiple of 16 in [0, d]; B*N*(Hq+Hkv) < 2^31. q_stride, k_stride: the
+ * distance between consecutive tokens in elements, as in pisa_window_shape_t. rot_scale 0
+ * selects 1. */
+typedef struct {
+  int32_t B, N, Hq, Hkv, d, rot, interleaved, norm;
+  float eps, rot_scale;
+  int32_t q_stride, k_stride;
+} pisa_rope_shape_t;
+
+/* Q [B,N,Hq,d], K [B,N,Hkv,d] bf16 (read, strided); inv_freq device [rot/2] fp32 radians per
+ * position (finite; may be NULL with rot = 0); q_weight, k_weight device [d] fp32 (NULL: ones;
+ * ignored with norm = 0); pos device [B,N] int32 (NULL: token i of every sequence at i).
+ * Qr [B,N,Hq,d], Kr [B,N,Hkv,d] bf16 contiguous (written); Qr may be Q itself and Kr K where
+ * those are contiguous. */
+int pisa_qk_norm_rope(const pisa_rope_shape_t* shape, const void* Q, const void* K, const float* inv_freq,
+                      const float* q_weight, const float* k_weight, const int32_t* pos, void* Qr, void* Kr,
+                      void* stream);
+
+/* Bytes of workspace of pisa_qk_norm_rope_bwd (host-only). */
+int pisa_qk_norm_rope_workspace_size(const pisa_rope_shape_t* shape, size_t* bytes);
+
+/* Its backward: with g the gradient turned back (times rot_scale), dw = sum over rows of g h,
+ * dx = r (g w - h mean(g w h)), r = 1 / sqrt(mean(x^2) + eps) (dx = g with norm = 0).
+ * Q, K the forward's inputs; dQr, dKr contiguous bf16 (read); dQ [B,N,Hq,d], dK [B,N,Hkv,d]
+ * bf16 contiguous (written; may be dQr and dKr themselves); dq_weight, dk_weight [d] fp32
+ * (written; NULL: not wanted; with norm = 0 they must be NULL). The sums' order is fixed. */
+int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const void* K, const void* dQr,
+                          const void* dKr, const float* inv_freq, const float* q_weight,
+                          const float* k_weight, const int32_t* pos, void* dQ, void* dK, float* dq_weight,
+                          float* dk_weight, void* ws, size_t ws_bytes, void* stream);
 
 /* Per-kernel timing (no counterpart on the pages: a measurement aid). After
  * pisa_profile_start(), every kernel that the library launches is bracketed by two CUDA

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -17,10 +18,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpisa.so")
 
 PISA_OK, PISA_EINVAL, PISA_EUNSUPPORTED, PISA_EWORKSPACE, PISA_ECUDA, PISA_ETIMEOUT = range(6)
+WINDOW_FWD, WINDOW_BWD = range(2)
 OP_SELECT, OP_SELECT_FLAT, OP_ATTN_FWD, OP_ATTN_BWD, OP_SELECT_MEAN, OP_SELECT_MEANVAR = range(6)
 STATUS_POS_RANGE, STATUS_TIMEOUT = 1, 2
 MAX_LEVELS = 32
-ABI_VERSION = 4          # PISA_VERSION of the header these argument lists follow
+ABI_VERSION = 5          # PISA_VERSION of the header these argument lists follow
 
 EXPORTS = (
     "pisa_version", "pisa_last_error", "pisa_pyramid_layout", "pisa_workspace_size",
@@ -28,7 +30,8 @@ EXPORTS = (
     "pisa_sparse_attn_bwd", "pisa_decode_pyramid_layout", "pisa_decode_build_pyramid",
     "pisa_decode_step", "pisa_profile_start", "pisa_profile_stop", "pisa_profile_read",
     "pisa_select_noalloc", "pisa_select_mean", "pisa_set_wait_limit", "pisa_test_stall",
-    "pisa_select_meanvar",
+    "pisa_select_meanvar", "pisa_window_workspace_size", "pisa_window_attn_fwd", "pisa_window_attn_bwd",
+    "pisa_window_decode_step", "pisa_qk_norm_rope", "pisa_qk_norm_rope_workspace_size", "pisa_qk_norm_rope_bwd",
 )
 
 
@@ -50,6 +53,23 @@ class ProfileEntry(ctypes.Structure):
 class DecodeShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "Ncap", "Hq", "Hkv", "d", "C", "K", "g")] + \
                [("scale", ctypes.c_float)]
+
+
+class WindowShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Nq", "N", "Hq", "Hkv", "d", "window", "sinks")] + \
+               [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class WindowDecodeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Ncap", "Hq", "Hkv", "d", "window", "sinks")] + \
+               [("scale", ctypes.c_float)]
+
+
+class RopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "Hq", "Hkv", "d", "rot", "interleaved", "norm")] + \
+               [("eps", ctypes.c_float), ("rot_scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("q_stride", "k_stride")]
 
 
 _lib = None
@@ -81,6 +101,13 @@ def lib() -> ctypes.CDLL:
         L.pisa_decode_pyramid_layout.argtypes = [P(DecodeShape), P(i32), P(i64), P(i64)]
         L.pisa_decode_build_pyramid.argtypes = [P(DecodeShape), vp, vp, vp, vp]
         L.pisa_decode_step.argtypes = [P(DecodeShape)] + [vp] * 11 + [vp]
+        L.pisa_window_workspace_size.argtypes = [P(WindowShape), ctypes.c_int, P(sz)]
+        L.pisa_window_attn_fwd.argtypes = [P(WindowShape)] + [vp] * 7 + [sz, vp]
+        L.pisa_window_attn_bwd.argtypes = [P(WindowShape)] + [vp] * 11 + [sz, vp]
+        L.pisa_window_decode_step.argtypes = [P(WindowDecodeShape)] + [vp] * 10
+        L.pisa_qk_norm_rope.argtypes = [P(RopeShape)] + [vp] * 9
+        L.pisa_qk_norm_rope_workspace_size.argtypes = [P(RopeShape), P(sz)]
+        L.pisa_qk_norm_rope_bwd.argtypes = [P(RopeShape)] + [vp] * 13 + [sz, vp]
         L.pisa_profile_start.argtypes = []
         L.pisa_profile_stop.argtypes = []
         L.pisa_profile_read.argtypes = [P(ProfileEntry), i32, P(i32)]
@@ -291,9 +318,14 @@ def decode_build_pyramid(Kcache, length, shape: DecodeShape) -> torch.Tensor:
 
 
 def decode_step(shape: DecodeShape, pos, Kcache, Vcache, pyr, q, k_new, v_new, o=None, idx=None,
-                score=None, status=None):
-    """One fused decode step (append + ancestor update + select + attend) for all sequences."""
+                score=None, status=None, rope: Rope | None = None):
+    """One fused decode step (append + ancestor update + select + attend) for all sequences.
+
+    With `rope`, q and k_new are raw projections: they are normed and rotated at `pos` first
+    (qk_norm_rope, one more launch)."""
     dev = q.device
+    if rope is not None:
+        q, k_new = _ready_token(rope, q, k_new, pos)
     o = o if o is not None else torch.empty_like(q)
     idx = idx if idx is not None else torch.empty(shape.B, shape.Hkv, shape.K, dtype=torch.int32, device=dev)
     status = status if status is not None else torch.zeros(4, dtype=torch.int32, device=dev)
@@ -301,6 +333,285 @@ def decode_step(shape: DecodeShape, pos, Kcache, Vcache, pyr, q, k_new, v_new, o
                                   _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(o), _ptr(idx), _ptr(score),
                                   _ptr(status), _stream(dev)))
     return o, idx, score, status
+
+
+# ---------------------------------------------------------------------------------------
+# Sliding-window attention with sinks; query/key norm with rotation
+
+def _on(dev, fn, *args) -> None:
+    """Call fn(*args, stream) on dev's current stream, with dev the current device."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _need_shaped(t, dtype, size, dev, name: str) -> None:
+    """A contiguous tensor of this type and size on `dev`."""
+    if t.dtype != dtype or t.device != dev or not t.is_cuda or t.shape != size or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(size)} on {dev} "
+                         f"(got {t.dtype}, {tuple(t.shape)}, {t.device}, contiguous={t.is_contiguous()})")
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between consecutive tokens of [B, N, H, d] (0: contiguous), d and the heads contiguous."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, H, d] (got {tuple(t.shape)})")
+    if t.is_contiguous():
+        return 0
+    B, N, H, d = t.shape
+    sb, sn, sh, sd = t.stride()
+    step = sn if N > 1 else sb
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (N > 1 and B > 1 and sb != N * sn):
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens (strides {tuple(t.stride())})")
+    return step if B * N > 1 else 0
+
+
+def _need_tokens(t, size, stride: int, dev, name: str) -> None:
+    if t.dtype != torch.bfloat16 or t.device != dev or not t.is_cuda or t.shape != size:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor {tuple(size)} on {dev} "
+                         f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
+    if not t.is_contiguous() or stride not in (0, size[2] * size[3]):
+        if size[0] * size[1] > 1 and (_token_stride(t, name) or size[2] * size[3]) != (stride or size[2] * size[3]):
+            raise ValueError(f"{name} has strides {tuple(t.stride())}, the shape says {stride} elements a token")
+
+
+def make_window_shape(B, Nq, N, Hq, Hkv, d, window, sinks=0, scale=0.0, q_stride=0, k_stride=0,
+                      v_stride=0) -> WindowShape:
+    return WindowShape(B, Nq, N, Hq, Hkv, d, window, sinks, float(scale), q_stride, k_stride, v_stride)
+
+
+def window_shape_of(Q, K, V, window, sinks=0, scale=0.0) -> WindowShape:
+    """The shape of Q [B,Nq,Hq,d], K, V [B,N,Hkv,d], which may be slices of a fused projection."""
+    B, Nq, Hq, d = Q.shape
+    return make_window_shape(B, Nq, K.shape[1], Hq, K.shape[2], d, window, sinks, scale, _token_stride(Q, "Q"),
+                             _token_stride(K, "K"), _token_stride(V, "V"))
+
+
+def window_workspace_size(shape: WindowShape, op: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().pisa_window_workspace_size(ctypes.byref(shape), op, ctypes.byref(b)))
+    return b.value
+
+
+def window_workspace(shape: WindowShape, op: int, device) -> torch.Tensor:
+    """A device workspace of the size `op` (WINDOW_FWD, WINDOW_BWD) needs (uint8 tensor)."""
+    return torch.empty(window_workspace_size(shape, op), dtype=torch.uint8, device=device)
+
+
+def _need_window(Q, K, V, shape, lens) -> None:
+    dev = Q.device
+    kv = (shape.B, shape.N, shape.Hkv, shape.d)
+    _need_tokens(Q, (shape.B, shape.Nq, shape.Hq, shape.d), shape.q_stride, dev, "Q")
+    _need_tokens(K, kv, shape.k_stride, dev, "K")
+    _need_tokens(V, kv, shape.v_stride, dev, "V")
+    if lens is not None:
+        _need_shaped(lens, torch.int32, (shape.B,), dev, "lens")
+
+
+def window_attn_fwd(Q, K, V, shape: WindowShape, lens=None, ws=None, out=None, lse=None):
+    """Causal sliding-window attention with sinks: O [B,Nq,Hq,d] bf16, lse [B,Hq,Nq] fp32.
+
+    lens: valid tokens of each sequence, [B] int32 (None: all); rows past them get O = 0, lse = -inf."""
+    _need_window(Q, K, V, shape, lens)
+    dev = Q.device
+    size = (shape.B, shape.Nq, shape.Hq, shape.d)
+    if out is None:
+        out = torch.empty(size, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shaped(out, torch.bfloat16, size, dev, "out")
+    if lse is None:
+        lse = torch.empty((shape.B, shape.Hq, shape.Nq), dtype=torch.float32, device=dev)
+    else:
+        _need_shaped(lse, torch.float32, (shape.B, shape.Hq, shape.Nq), dev, "lse")
+    if ws is None:
+        ws = window_workspace(shape, WINDOW_FWD, dev)
+    _on(dev, lib().pisa_window_attn_fwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(lens),
+        out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return out, lse
+
+
+def window_attn_bwd(Q, K, V, O, lse, dO, shape: WindowShape, lens=None, ws=None):
+    """Gradients of window_attn_fwd: dQ, dK, dV (bf16), from its O and lse."""
+    _need_window(Q, K, V, shape, lens)
+    dev = Q.device
+    size = (shape.B, shape.Nq, shape.Hq, shape.d)
+    _need_shaped(O, torch.bfloat16, size, dev, "O")
+    _need_shaped(dO, torch.bfloat16, size, dev, "dO")
+    _need_shaped(lse, torch.float32, (shape.B, shape.Hq, shape.Nq), dev, "lse")
+    dQ = torch.empty(size, dtype=torch.bfloat16, device=dev)
+    dK = torch.empty((shape.B, shape.N, shape.Hkv, shape.d), dtype=torch.bfloat16, device=dev)
+    dV = torch.empty_like(dK)
+    if ws is None:
+        ws = window_workspace(shape, WINDOW_BWD, dev)
+    _on(dev, lib().pisa_window_attn_bwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+        lse.data_ptr(), dO.data_ptr(), _ptr(lens), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(),
+        ws.numel())
+    return dQ, dK, dV
+
+
+def make_window_decode_shape(B, Ncap, Hq, Hkv, d, window, sinks=0, scale=0.0) -> WindowDecodeShape:
+    return WindowDecodeShape(B, Ncap, Hq, Hkv, d, window, sinks, float(scale))
+
+
+def window_decode_step(shape: WindowDecodeShape, pos, Kcache, Vcache, q, k_new, v_new, o=None, lse=None,
+                       status=None, rope: Rope | None = None):
+    """One decode step of the window attention: append at the slot of pos, attend. Returns o, lse, status.
+
+    The cache rolls once positions reach its capacity (see pisa.h). With `rope`, q and k_new are
+    raw projections: they are normed and rotated at `pos` first (qk_norm_rope, one more launch)."""
+    dev = q.device
+    B, H = shape.B, (shape.B, shape.Hkv, shape.d)
+    cache = (B, shape.Ncap, shape.Hkv, shape.d)
+    _need_shaped(pos, torch.int32, (B,), dev, "pos")
+    _need_shaped(Kcache, torch.bfloat16, cache, dev, "Kcache")
+    _need_shaped(Vcache, torch.bfloat16, cache, dev, "Vcache")
+    if rope is not None:
+        q, k_new = _ready_token(rope, q, k_new, pos)
+    _need_shaped(q, torch.bfloat16, (B, shape.Hq, shape.d), dev, "q")
+    _need_shaped(k_new, torch.bfloat16, H, dev, "k_new")
+    _need_shaped(v_new, torch.bfloat16, H, dev, "v_new")
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _need_shaped(o, torch.bfloat16, (B, shape.Hq, shape.d), dev, "o")
+    if lse is None:
+        lse = torch.empty((B, shape.Hq), dtype=torch.float32, device=dev)
+    else:
+        _need_shaped(lse, torch.float32, (B, shape.Hq), dev, "lse")
+    if status is None:
+        status = torch.zeros(4, dtype=torch.int32, device=dev)
+    _on(dev, lib().pisa_window_decode_step, ctypes.byref(shape), pos.data_ptr(), Kcache.data_ptr(), Vcache.data_ptr(),
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), o.data_ptr(), lse.data_ptr(), status.data_ptr())
+    return o, lse, status
+
+
+def make_rope_shape(B, N, Hq, Hkv, d, rot, interleaved=False, norm=True, eps=1e-6, rot_scale=1.0, q_stride=0,
+                    k_stride=0) -> RopeShape:
+    return RopeShape(B, N, Hq, Hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, float(eps), float(rot_scale),
+                     q_stride, k_stride)
+
+
+def rope_shape_of(Q, K, rot, interleaved=False, norm=True, eps=1e-6, rot_scale=1.0) -> RopeShape:
+    """The shape of Q [B,N,Hq,d], K [B,N,Hkv,d], which may be slices of a fused projection."""
+    B, N, Hq, d = Q.shape
+    return make_rope_shape(B, N, Hq, K.shape[2], d, rot, interleaved, norm, eps, rot_scale, _token_stride(Q, "Q"),
+                           _token_stride(K, "K"))
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained_len: int = 0, slow: float = 1.0, fast: float = 32.0):
+    """Rotary frequencies (inv_freq [rot/2] fp32 on the CPU, radians per position) and rot_scale.
+
+    scaling, for contexts `factor` times longer than the trained_len tokens of training:
+      "none"    base ** (-2 c / rot)
+      "linear"  every frequency divided by factor (position interpolation)
+      "ntk"     the base raised by factor ** (rot / (rot - 2)): the lowest frequency is divided by
+                factor, the highest stays
+      "yarn"    by parts (YaRN): pairs that turn more than `fast` times within trained_len stay, those
+                under `slow` turns are divided by factor, a linear ramp in the turns between; and
+                rot_scale = 0.1 ln(factor) + 1
+    """
+    if rot < 2 or rot % 2 or factor < 1 or base <= 0:
+        raise ValueError(f"rot={rot} must be even and positive, factor={factor} at least 1, base={base} positive")
+    c = torch.arange(0, rot, 2, dtype=torch.float64) / rot
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** -c
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if trained_len < 1 or not 0 <= slow < fast:
+            raise ValueError(f"yarn scaling needs trained_len and 0 <= slow < fast (got {trained_len}, {slow}, {fast})")
+        keep = ((trained_len * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f / factor * (1 - keep) + f * keep
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(torch.float32), 0.1 * math.log(factor) + 1 if scaling == "yarn" and factor > 1 else 1.0
+
+
+class Rope(NamedTuple):
+    """What turns raw query and key projections into the heads the attentions take: device tensors
+    (inv_freq [rot/2] fp32, the norm's weights [d] fp32 or None) and pisa_rope_shape_t's settings."""
+    inv_freq: torch.Tensor | None
+    rot: int
+    interleaved: bool = False
+    norm: bool = True
+    eps: float = 1e-6
+    rot_scale: float = 1.0
+    q_weight: torch.Tensor | None = None
+    k_weight: torch.Tensor | None = None
+
+
+def _ready_token(rope: Rope, q, k_new, pos):
+    """q [B,Hq,d] and k_new [B,Hkv,d] of one token per sequence, normed and rotated at pos [B]."""
+    q4, k4 = q[:, None], k_new[:, None]
+    shape = rope_shape_of(q4, k4, rope.rot, rope.interleaved, rope.norm, rope.eps, rope.rot_scale)
+    q4, k4 = qk_norm_rope(q4, k4, rope.inv_freq, shape, rope.q_weight, rope.k_weight, pos[:, None])
+    return q4[:, 0], k4[:, 0]
+
+
+def _need_rope(Q, K, inv_freq, shape, q_weight, k_weight, pos) -> None:
+    dev = Q.device
+    _need_tokens(Q, (shape.B, shape.N, shape.Hq, shape.d), shape.q_stride, dev, "Q")
+    _need_tokens(K, (shape.B, shape.N, shape.Hkv, shape.d), shape.k_stride, dev, "K")
+    if inv_freq is not None:
+        _need_shaped(inv_freq, torch.float32, (shape.rot // 2,), dev, "inv_freq")
+    if q_weight is not None:
+        _need_shaped(q_weight, torch.float32, (shape.d,), dev, "q_weight")
+    if k_weight is not None:
+        _need_shaped(k_weight, torch.float32, (shape.d,), dev, "k_weight")
+    if pos is not None:
+        _need_shaped(pos, torch.int32, (shape.B, shape.N), dev, "pos")
+
+
+def qk_norm_rope(Q, K, inv_freq, shape: RopeShape, q_weight=None, k_weight=None, pos=None, q_out=None, k_out=None):
+    """RMS norm of every head and rotation by position: Qr [B,N,Hq,d], Kr [B,N,Hkv,d] bf16.
+
+    pos: [B,N] int32 (None: 0 .. N-1). q_out / k_out may be Q / K themselves where contiguous."""
+    _need_rope(Q, K, inv_freq, shape, q_weight, k_weight, pos)
+    dev = Q.device
+    sizes = (shape.B, shape.N, shape.Hq, shape.d), (shape.B, shape.N, shape.Hkv, shape.d)
+    if q_out is None:
+        q_out = torch.empty(sizes[0], dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shaped(q_out, torch.bfloat16, sizes[0], dev, "q_out")
+    if k_out is None:
+        k_out = torch.empty(sizes[1], dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shaped(k_out, torch.bfloat16, sizes[1], dev, "k_out")
+    _on(dev, lib().pisa_qk_norm_rope, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), _ptr(inv_freq), _ptr(q_weight),
+        _ptr(k_weight), _ptr(pos), q_out.data_ptr(), k_out.data_ptr())
+    return q_out, k_out
+
+
+def qk_norm_rope_workspace(shape: RopeShape, device) -> torch.Tensor:
+    """A device workspace for qk_norm_rope_bwd (uint8 tensor)."""
+    b = ctypes.c_size_t()
+    _check(lib().pisa_qk_norm_rope_workspace_size(ctypes.byref(shape), ctypes.byref(b)))
+    return torch.empty(b.value, dtype=torch.uint8, device=device)
+
+
+def qk_norm_rope_bwd(Q, K, dQr, dKr, inv_freq, shape: RopeShape, q_weight=None, k_weight=None, pos=None, ws=None):
+    """Gradients of qk_norm_rope: dQ, dK (bf16) and the weights' dwq, dwk ([d] fp32; None without the norm)."""
+    _need_rope(Q, K, inv_freq, shape, q_weight, k_weight, pos)
+    dev = Q.device
+    _need_shaped(dQr, torch.bfloat16, (shape.B, shape.N, shape.Hq, shape.d), dev, "dQr")
+    _need_shaped(dKr, torch.bfloat16, (shape.B, shape.N, shape.Hkv, shape.d), dev, "dKr")
+    dQ, dK = torch.empty_like(dQr), torch.empty_like(dKr)
+    dwq = dwk = None
+    if shape.norm:
+        dwq = torch.empty(shape.d, dtype=torch.float32, device=dev)
+        dwk = torch.empty(shape.d, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = qk_norm_rope_workspace(shape, dev)
+    _on(dev, lib().pisa_qk_norm_rope_bwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), dQr.data_ptr(),
+        dKr.data_ptr(), _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(pos), dQ.data_ptr(), dK.data_ptr(),
+        _ptr(dwq), _ptr(dwk), ws.data_ptr(), ws.numel())
+    return dQ, dK, dwq, dwk
 
 
 def workspace_status(ws: torch.Tensor) -> int:

@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "internal.h"
+#include "window.h"
 
 namespace {
 
@@ -147,6 +148,111 @@ int check_ws_bytes(size_t need, const void* ws, size_t ws_bytes) {
 
 int check_ws(const pisa::Dims& d, const pisa::Geo& g, int op, const void* ws, size_t ws_bytes) {
   return check_ws_bytes(ws_bytes_for(d, g, op), ws, ws_bytes);
+}
+
+// ---- sliding-window attention, query/key norm with rotation
+
+int check_heads(int Hq, int Hkv, int d) {
+  if (Hq % Hkv != 0) return fail(PISA_EINVAL, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+  if (d != 64 && d != 128) return fail(PISA_EUNSUPPORTED, "head dim d=%d (supported: 64, 128)", d);
+  return PISA_OK;
+}
+
+int check_scale(float scale, const char* name) {
+  if (!(scale >= 0.f) || std::isinf(scale)) return fail(PISA_EINVAL, "%s must be finite and >= 0", name);
+  return PISA_OK;
+}
+
+// Token stride in elements: 0 means contiguous.
+int check_stride(int32_t stride, int H, int d, const char* name, int64_t* out) {
+  const int64_t row = static_cast<int64_t>(H) * d;
+  if (stride != 0 && (stride < row || stride % 8 != 0))
+    return fail(PISA_EINVAL, "%s=%d must be 0 or a multiple of 8 of at least H*d=%lld", name, stride,
+                static_cast<long long>(row));
+  *out = stride ? stride : row;
+  return PISA_OK;
+}
+
+float scale_or_default(float scale, int d) { return scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d)); }
+
+int window_dims(const pisa_window_shape_t* s, pisa::WinDims* o) {
+  if (!s) return fail(PISA_EINVAL, "shape is NULL");
+  if (s->B < 1 || s->Nq < 1 || s->N < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1 || s->window < 1)
+    return fail(PISA_EINVAL, "sizes must be positive (B=%d Nq=%d N=%d Hq=%d Hkv=%d d=%d window=%d)", s->B, s->Nq,
+                s->N, s->Hq, s->Hkv, s->d, s->window);
+  if (s->sinks < 0) return fail(PISA_EINVAL, "sinks=%d is negative", s->sinks);
+  if (s->Nq > s->N) return fail(PISA_EINVAL, "Nq=%d exceeds N=%d", s->Nq, s->N);
+  PISA_CHECK(check_heads(s->Hq, s->Hkv, s->d));
+  if (s->Hq / s->Hkv > 64) return fail(PISA_EUNSUPPORTED, "GQA group G=%d (supported: at most 64)", s->Hq / s->Hkv);
+  if (s->N > (1 << 24)) return fail(PISA_EUNSUPPORTED, "N=%d exceeds 2^24", s->N);
+  const int64_t bn = static_cast<int64_t>(s->B) * s->N;
+  if (bn >= (int64_t(1) << 31) || bn * s->Hq >= (int64_t(1) << 31))
+    return fail(PISA_EUNSUPPORTED, "B*N*Hq=%lld exceeds 2^31", static_cast<long long>(bn * s->Hq));
+  PISA_CHECK(check_scale(s->scale, "scale"));
+  pisa::WinDims d{};
+  PISA_CHECK(check_stride(s->q_stride, s->Hq, s->d, "q_stride", &d.qs));
+  PISA_CHECK(check_stride(s->k_stride, s->Hkv, s->d, "k_stride", &d.ks));
+  PISA_CHECK(check_stride(s->v_stride, s->Hkv, s->d, "v_stride", &d.vs));
+  d.B = s->B; d.Nq = s->Nq; d.N = s->N; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d;
+  d.G = s->Hq / s->Hkv;
+  d.off = s->N - s->Nq;
+  d.window = s->window < s->N ? s->window : s->N;     // the same keys, and no sum of positions overflows
+  d.sinks = s->sinks < s->N ? s->sinks : s->N;
+  d.scale = scale_or_default(s->scale, s->d);
+  *o = d;
+  return PISA_OK;
+}
+
+size_t window_ws_bytes(const pisa::WinDims& d, int op) {
+  return op == PISA_WINDOW_FWD ? 256 : pisa::window_bwd_ws(d).total;
+}
+
+int window_decode_dims(const pisa_window_decode_shape_t* s, pisa::WinDecodeDims* o) {
+  if (!s) return fail(PISA_EINVAL, "shape is NULL");
+  if (s->B < 1 || s->Ncap < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1 || s->window < 1)
+    return fail(PISA_EINVAL, "sizes must be positive (B=%d Ncap=%d Hq=%d Hkv=%d d=%d window=%d)", s->B, s->Ncap,
+                s->Hq, s->Hkv, s->d, s->window);
+  if (s->sinks < 0) return fail(PISA_EINVAL, "sinks=%d is negative", s->sinks);
+  if (s->Ncap <= s->sinks) return fail(PISA_EINVAL, "Ncap=%d must exceed sinks=%d", s->Ncap, s->sinks);
+  PISA_CHECK(check_heads(s->Hq, s->Hkv, s->d));
+  if (s->Hq / s->Hkv > 64) return fail(PISA_EUNSUPPORTED, "GQA group G=%d (supported: at most 64)", s->Hq / s->Hkv);
+  if (s->Ncap > (1 << 24)) return fail(PISA_EUNSUPPORTED, "Ncap=%d exceeds 2^24", s->Ncap);
+  if (s->B > 65535 || s->Hq > 65535) return fail(PISA_EUNSUPPORTED, "B=%d or Hq=%d exceeds 65535", s->B, s->Hq);
+  PISA_CHECK(check_scale(s->scale, "scale"));
+  pisa::WinDecodeDims d{};
+  d.B = s->B; d.Ncap = s->Ncap; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d;
+  d.G = s->Hq / s->Hkv;
+  d.window = s->window;
+  d.sinks = s->sinks;
+  d.scale = scale_or_default(s->scale, s->d);
+  *o = d;
+  return PISA_OK;
+}
+
+int rope_dims(const pisa_rope_shape_t* s, pisa::RopeDims* o) {
+  if (!s) return fail(PISA_EINVAL, "shape is NULL");
+  if (s->B < 1 || s->N < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1)
+    return fail(PISA_EINVAL, "sizes must be positive (B=%d N=%d Hq=%d Hkv=%d d=%d)", s->B, s->N, s->Hq, s->Hkv, s->d);
+  if (s->d != 64 && s->d != 128) return fail(PISA_EUNSUPPORTED, "head dim d=%d (supported: 64, 128)", s->d);
+  if (s->rot < 0 || s->rot > s->d) return fail(PISA_EINVAL, "rot=%d is outside [0, d=%d]", s->rot, s->d);
+  if (s->rot % 16 != 0) return fail(PISA_EUNSUPPORTED, "rot=%d (supported: multiples of 16)", s->rot);
+  if ((s->interleaved != 0 && s->interleaved != 1) || (s->norm != 0 && s->norm != 1))
+    return fail(PISA_EINVAL, "interleaved=%d and norm=%d must be 0 or 1", s->interleaved, s->norm);
+  PISA_CHECK(check_scale(s->eps, "eps"));
+  PISA_CHECK(check_scale(s->rot_scale, "rot_scale"));
+  const int64_t bn = static_cast<int64_t>(s->B) * s->N, H = static_cast<int64_t>(s->Hq) + s->Hkv;
+  if (bn >= (int64_t(1) << 31) || H >= (int64_t(1) << 31) || bn * H >= (int64_t(1) << 31))
+    return fail(PISA_EUNSUPPORTED, "B*N*(Hq+Hkv) exceeds 2^31");
+  pisa::RopeDims d{};
+  PISA_CHECK(check_stride(s->q_stride, s->Hq, s->d, "q_stride", &d.qs));
+  PISA_CHECK(check_stride(s->k_stride, s->Hkv, s->d, "k_stride", &d.ks));
+  d.B = s->B; d.N = s->N; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d; d.rot = s->rot;
+  d.interleaved = s->interleaved;
+  d.norm = s->norm;
+  d.eps = s->eps;
+  d.rot_scale = s->rot_scale > 0.f ? s->rot_scale : 1.f;
+  *o = d;
+  return PISA_OK;
 }
 
 }  // namespace
@@ -353,6 +459,104 @@ int pisa_decode_step(const pisa_decode_shape_t* shape, const int32_t* pos, void*
   return cuda_rc(pisa::launch_decode_step(d, shape->Ncap, g, pos, Kcache, Vcache, pyr_sum, q, k_new,
                                           v_new, o, idx, score, status, stream),
                  "pisa_decode_step");
+}
+
+int pisa_window_workspace_size(const pisa_window_shape_t* shape, int op, size_t* bytes) {
+  pisa::WinDims d;
+  PISA_CHECK(window_dims(shape, &d));
+  if (!bytes) return fail(PISA_EINVAL, "bytes is NULL");
+  if (op != PISA_WINDOW_FWD && op != PISA_WINDOW_BWD) return fail(PISA_EINVAL, "unknown op %d", op);
+  *bytes = window_ws_bytes(d, op);
+  return PISA_OK;
+}
+
+int pisa_window_attn_fwd(const pisa_window_shape_t* shape, const void* Q, const void* K, const void* V,
+                         const int32_t* len, void* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  pisa::WinDims d;
+  PISA_CHECK(window_dims(shape, &d));
+  PISA_CHECK(check_ptr(Q, "Q"));
+  PISA_CHECK(check_ptr(K, "K"));
+  PISA_CHECK(check_ptr(V, "V"));
+  PISA_CHECK(check_ptr(len, "len", true));
+  PISA_CHECK(check_ptr(O, "O"));
+  PISA_CHECK(check_ptr(lse, "lse"));
+  PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_FWD), ws, ws_bytes));
+  return cuda_rc(pisa::launch_window_fwd(d, Q, K, V, len, O, lse, static_cast<char*>(ws), stream),
+                 "pisa_window_attn_fwd");
+}
+
+int pisa_window_attn_bwd(const pisa_window_shape_t* shape, const void* Q, const void* K, const void* V,
+                         const void* O, const float* lse, const void* dO, const int32_t* len, void* dQ,
+                         void* dK, void* dV, void* ws, size_t ws_bytes, void* stream) {
+  pisa::WinDims d;
+  PISA_CHECK(window_dims(shape, &d));
+  const void* in[] = {Q, K, V, O, lse, dO, dQ, dK, dV};
+  const char* names[] = {"Q", "K", "V", "O", "lse", "dO", "dQ", "dK", "dV"};
+  for (int k = 0; k < 9; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(len, "len", true));
+  PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_BWD), ws, ws_bytes));
+  return cuda_rc(pisa::launch_window_bwd(d, Q, K, V, O, lse, dO, len, dQ, dK, dV, static_cast<char*>(ws), stream),
+                 "pisa_window_attn_bwd");
+}
+
+int pisa_window_decode_step(const pisa_window_decode_shape_t* shape, const int32_t* pos, void* Kcache,
+                            void* Vcache, const void* q, const void* k_new, const void* v_new, void* o,
+                            float* lse, int32_t* status, void* stream) {
+  pisa::WinDecodeDims d;
+  PISA_CHECK(window_decode_dims(shape, &d));
+  const void* in[] = {pos, Kcache, Vcache, q, k_new, v_new, o, status};
+  const char* names[] = {"pos", "Kcache", "Vcache", "q", "k_new", "v_new", "o", "status"};
+  for (int k = 0; k < 8; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(lse, "lse", true));
+  return cuda_rc(pisa::launch_window_decode(d, pos, Kcache, Vcache, q, k_new, v_new, o, lse, status, stream),
+                 "pisa_window_decode_step");
+}
+
+int pisa_qk_norm_rope(const pisa_rope_shape_t* shape, const void* Q, const void* K, const float* inv_freq,
+                      const float* q_weight, const float* k_weight, const int32_t* pos, void* Qr, void* Kr,
+                      void* stream) {
+  pisa::RopeDims d;
+  PISA_CHECK(rope_dims(shape, &d));
+  PISA_CHECK(check_ptr(Q, "Q"));
+  PISA_CHECK(check_ptr(K, "K"));
+  PISA_CHECK(check_ptr(inv_freq, "inv_freq", d.rot == 0));
+  PISA_CHECK(check_ptr(q_weight, "q_weight", true));
+  PISA_CHECK(check_ptr(k_weight, "k_weight", true));
+  PISA_CHECK(check_ptr(pos, "pos", true));
+  PISA_CHECK(check_ptr(Qr, "Qr"));
+  PISA_CHECK(check_ptr(Kr, "Kr"));
+  if ((Qr == Q && d.qs != static_cast<int64_t>(d.Hq) * d.d) || (Kr == K && d.ks != static_cast<int64_t>(d.Hkv) * d.d))
+    return fail(PISA_EINVAL, "in place needs a contiguous Q and K");
+  return cuda_rc(pisa::launch_rope(d, Q, K, inv_freq, q_weight, k_weight, pos, Qr, Kr, stream), "pisa_qk_norm_rope");
+}
+
+int pisa_qk_norm_rope_workspace_size(const pisa_rope_shape_t* shape, size_t* bytes) {
+  pisa::RopeDims d;
+  PISA_CHECK(rope_dims(shape, &d));
+  if (!bytes) return fail(PISA_EINVAL, "bytes is NULL");
+  *bytes = pisa::rope_bwd_ws(d);
+  return PISA_OK;
+}
+
+int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const void* K, const void* dQr,
+                          const void* dKr, const float* inv_freq, const float* q_weight,
+                          const float* k_weight, const int32_t* pos, void* dQ, void* dK, float* dq_weight,
+                          float* dk_weight, void* ws, size_t ws_bytes, void* stream) {
+  pisa::RopeDims d;
+  PISA_CHECK(rope_dims(shape, &d));
+  const void* in[] = {Q, K, dQr, dKr, dQ, dK};
+  const char* names[] = {"Q", "K", "dQr", "dKr", "dQ", "dK"};
+  for (int k = 0; k < 6; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(inv_freq, "inv_freq", d.rot == 0));
+  const void* opt[] = {q_weight, k_weight, pos, dq_weight, dk_weight};
+  const char* opt_names[] = {"q_weight", "k_weight", "pos", "dq_weight", "dk_weight"};
+  for (int k = 0; k < 5; ++k) PISA_CHECK(check_ptr(opt[k], opt_names[k], true));
+  if (!d.norm && (dq_weight || dk_weight)) return fail(PISA_EINVAL, "norm=0 has no weight gradients");
+  if (dQ == Q || dK == K) return fail(PISA_EINVAL, "dQ and dK must not be Q and K");
+  PISA_CHECK(check_ws_bytes(pisa::rope_bwd_ws(d), ws, ws_bytes));
+  return cuda_rc(pisa::launch_rope_bwd(d, Q, K, dQr, dKr, inv_freq, q_weight, k_weight, pos, dQ, dK, dq_weight,
+                                       dk_weight, static_cast<char*>(ws), stream),
+                 "pisa_qk_norm_rope_bwd");
 }
 
 }  // extern "C"
