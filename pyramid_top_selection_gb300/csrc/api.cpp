@@ -193,6 +193,9 @@ int window_dims(const pisa_window_shape_t* s, pisa::WinDims* o) {
   PISA_CHECK(check_stride(s->q_stride, s->Hq, s->d, "q_stride", &d.qs));
   PISA_CHECK(check_stride(s->k_stride, s->Hkv, s->d, "k_stride", &d.ks));
   PISA_CHECK(check_stride(s->v_stride, s->Hkv, s->d, "v_stride", &d.vs));
+  const int64_t strides[] = {d.qs, d.ks, d.vs};      // TMA: less than 2^40 bytes between batches
+  for (const int64_t st : strides)
+    if (st * s->N >= (int64_t(1) << 39)) return fail(PISA_EUNSUPPORTED, "token stride %lld at N=%d", static_cast<long long>(st), s->N);
   d.B = s->B; d.Nq = s->Nq; d.N = s->N; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d;
   d.G = s->Hq / s->Hkv;
   d.off = s->N - s->Nq;

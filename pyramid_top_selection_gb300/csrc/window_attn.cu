@@ -1,45 +1,474 @@
-// Sliding-window attention with sinks, forward: one warp per (query, head) row, keys in order
-// with the running maximum and sum of the softmax.
+// Sliding-window attention with sinks, forward, on the fifth-generation tensor cores.
+//
+// Per row: O = softmax over the visible keys of (s q.k) times V, in one pass over the keys with the
+// running maximum and sum of the softmax. P = 2^(c s_j - m) with c = scale log2 e; m follows the
+// running maximum only when that grows by more than 2^8 (P, its sum and O then stay within fp32
+// and bf16 range, and O is rescaled rarely); lse = (m + log2 l) ln 2.
+//
+// Persistent, one CTA per SM; a work item is 256 rows of one KV head: two 128-row tiles of (token,
+// head) rows, P heads of the group together (window_tc.cuh), so the keys are read once for two tiles
+// and the window's edges mask few columns. Items with the most keys come first. Roles:
+//   * loader (warp 9, one thread): Q tiles, then the item's key and value tiles of 128 columns
+//     (KeyList: sinks and window as one list) by TMA into a ring of stages;
+//   * MMA (warp 8, one thread): per key tile and row tile, O += P V (P from tensor memory, V
+//     as stored, MN-major), then the next S = Q K^T into the columns P has left. A tile's P V and
+//     the next S alternate between the two row tiles, so one tile's softmax runs under the other's
+//     products;
+//   * softmax (warps 0-3 and 4-7, one row tile each, one row a thread): S row from tensor
+//     memory into registers, masks where the tile touches an edge, maximum, exponentials, sum, P
+//     as bf16 over the first half of S's columns; at the item's end O / l to bf16 through a
+//     staging tile and TMA stores;
+//   * scrub (warp 10): zeroes value rows at tokens >= len in the tile that holds the sequence's
+//     end, so that padding's values (NaN, say) do not meet P = 0.
+// TMEM: S (and P) of row tile t at 128 t, O at 256 + d t: all 512 columns at d = 128.
+// P is rounded to bf16 for the product (2^-8 relative at most); the sum l takes it unrounded.
+// Every wait is bounded; one that gives up sets the CTA's abort flag, every role leaves, copies and
+// MMAs in flight are drained, and the rows of the items left are poisoned.
+#include <algorithm>
+
 #include "device.cuh"
+#include "internal.h"
 #include "profile.h"
-#include "window.h"
+#include "tmap.h"
+#include "window_tc.cuh"
 
 namespace pisa {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 384;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;                  // log2 growth of the maximum that O is rescaled for
+constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) window_fwd_kernel(const WinDims s, const __nv_bfloat16* Q,
-                                                                 const __nv_bfloat16* K, const __nv_bfloat16* V,
-                                                                 const int32_t* len, __nv_bfloat16* O, float* lse) {
-  constexpr int E = D / 32;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(s.B) * s.Nq * s.Hq) return;
-  const int lane = threadIdx.x & 31, h = static_cast<int>(row % s.Hq);
-  const int64_t tok = row / s.Hq;
-  const int i = static_cast<int>(tok % s.Nq), b = static_cast<int>(tok / s.Nq), kv = h / s.G;
-  const int L = len ? max(0, min(len[b], s.N)) : s.N, p = i + s.off;
-  float q[E], o[E] = {}, m = neg_inf(), l = 0.f;
-  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(Q[tok * s.qs + h * D + lane * E + e]) * s.scale;
-  if (p < L) {
-    const int lo = max(0, p - s.window + 1);
-    auto key = [&](int j) {
-      const int64_t kr = static_cast<int64_t>(b) * s.N + j;
-      float x = 0.f;
-      for (int e = 0; e < E; ++e) x += q[e] * __bfloat162float(K[kr * s.ks + kv * D + lane * E + e]);
-      x = warp_sum(x);
-      const float mn = fmaxf(m, x), c = __expf(m - mn), w = __expf(x - mn);
-      l = l * c + w;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * c + w * __bfloat162float(V[kr * s.vs + kv * D + lane * E + e]);
-      m = mn;
-    };
-    for (int j = 0; j < min(s.sinks, lo); ++j) key(j);
-    for (int j = lo; j <= p; ++j) key(j);
+struct FwdSmem {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * 128 * 128;        // 128 rows x D bf16, SW128 blocks of 64 columns
+  static constexpr int NST = 256 / D * 2;            // K / V stages: 128 KB in all
+  static constexpr int oQ = 0, oKV = 2 * TILE, oStage = oKV + NST * TILE;
+  static constexpr int STG = 32 * 128;               // a warp's 32 rows x 64 bf16
+  static constexpr int bytes = oStage + 8 * STG + 1024;
+};
+
+struct FwdArgs {
+  WinDims s;
+  const int32_t* len;
+  __nv_bfloat16* O;
+  float* lse;
+  int32_t* status;
+  uint64_t wait_ns;
+  int stall;
+  int P, tok;              // heads of a tile, tokens of a tile (128 / P)
+  int n_tiles, n_heads, n_items;   // token tile pairs, (b, kv, head set) combinations
+};
+
+struct FwdItem {
+  int b, kv, h0, t0;       // batch, KV head, first query head, first token
+  __device__ __forceinline__ FwdItem(const FwdArgs& a, int w) {
+    const int tile = a.n_tiles - 1 - w / a.n_heads, hh = w % a.n_heads, sets = a.s.G / a.P;
+    b = hh / (a.s.Hkv * sets);
+    kv = hh / sets % a.s.Hkv;
+    h0 = kv * a.s.G + hh % sets * a.P;
+    t0 = tile * 2 * a.tok;
   }
-  for (int e = 0; e < E; ++e) O[row * D + lane * E + e] = __float2bfloat16_rn(l > 0.f ? o[e] / l : 0.f);
-  if (lane == 0) lse[(static_cast<int64_t>(b) * s.Hq + h) * s.Nq + i] = l > 0.f ? m + logf(l) : neg_inf();
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kmap32,
+                  const __grid_constant__ CUtensorMap vmap32, const __grid_constant__ CUtensorMap omap) {
+  using M = FwdSmem<D>;
+  extern __shared__ unsigned char smraw[];
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[M::NST], kv_empty[M::NST], s_full[2], p_full[2],
+      pv_done[2], o_empty[2], scrubbed, drain, never;
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_abort;
+
+  const WinDims& s = a.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned char* sm = smraw + ((1024 - (tc::su32(smraw) & 1023)) & 1023);
+  const uint32_t aQ = tc::su32(sm + M::oQ), aKV = tc::su32(sm + M::oKV), aStage = tc::su32(sm + M::oStage);
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      tc::bar_init(&q_full[t], 1);
+      tc::bar_init(&q_empty[t], 1);
+      tc::bar_init(&s_full[t], 1);
+      tc::bar_init(&p_full[t], 128);
+      tc::bar_init(&pv_done[t], 1);
+      tc::bar_init(&o_empty[t], 128);
+    }
+    for (int k = 0; k < M::NST; ++k) {
+      tc::bar_init(&kv_full[k], 1);
+      tc::bar_init(&kv_empty[k], 1);
+    }
+    tc::bar_init(&scrubbed, 1);
+    tc::bar_init(&drain, 1);
+    tc::bar_init(&never, 1);
+    tc::fence_bar_init();
+    s_abort = 0;
+  }
+  if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
+  tc::before_sync();
+  __syncthreads();
+  tc::after_sync();
+  const uint32_t tm = tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
+  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+  // positions of row tile t of an item: [p0, p1)
+  auto tile_p0 = [&](const FwdItem& it, int t) { return s.off + it.t0 + t * a.tok; };
+  auto tile_p1 = [&](const FwdItem& it, int t) { return s.off + min(s.Nq, it.t0 + (t + 1) * a.tok); };
+
+  if (warp >= 8) {
+    win::regs_dec<88>();
+    if (warp == 9) {
+      // ---------------------------------------------------------------- loader
+      if (lane == 0) {
+        int n_kv = 0, n_q[2] = {0, 0};         // loads issued
+        for (int w = blockIdx.x; w < a.n_items && !aborted(); w += gridDim.x) {
+          const FwdItem it(a, w);
+          const int L = win::valid_len(a.len, it.b, s.N);
+          const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
+          auto load_q = [&](int t) -> bool {
+            if (min(tile_p1(it, t), L) <= tile_p0(it, t)) return true;
+            if (!wait(&q_empty[t], (n_q[t] & 1) ^ 1)) return false;
+            ++n_q[t];
+            tc::bar_expect_tx(&q_full[t], M::TILE);
+#pragma unroll
+            for (int kb = 0; kb < M::KB; ++kb)
+              tc::tma_load4(aQ + t * M::TILE + kb * (128 * 128), &qmap, kb * 64, it.h0, it.t0 + t * a.tok, it.b, &q_full[t]);
+            return true;
+          };
+          auto load_kv = [&](int v0, const CUtensorMap* big, const CUtensorMap* small) -> bool {
+            const int st = n_kv % M::NST;
+            if (!wait(&kv_empty[st], ((n_kv / M::NST) & 1) ^ 1)) return false;
+            ++n_kv;
+            tc::bar_expect_tx(&kv_full[st], M::TILE);
+            const uint32_t dst = aKV + st * M::TILE;
+            if (v0 >= kl.SP) {
+#pragma unroll
+              for (int kb = 0; kb < M::KB; ++kb)
+                tc::tma_load4(dst + kb * (128 * 128), big, kb * 64, it.kv, kl.key(v0), it.b, &kv_full[st]);
+            } else {
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int kb = 0; kb < M::KB; ++kb)
+                  tc::tma_load4(dst + kb * (128 * 128) + r * (32 * 128), small, kb * 64, it.kv, kl.key(v0 + 32 * r), it.b,
+                                &kv_full[st]);
+            }
+            return true;
+          };
+          if (kl.n_cols == 0) continue;
+          bool ok = load_q(0) && load_kv(0, &kmap, &kmap32) && load_q(1) && load_kv(0, &vmap, &vmap32);
+          for (int v0 = 128; ok && v0 < kl.n_cols; v0 += 128)
+            ok = load_kv(v0, &kmap, &kmap32) && load_kv(v0, &vmap, &vmap32);
+          if (!ok) break;
+        }
+        // whatever is still in flight lands before the CTA leaves
+        for (int k = max(0, n_kv - M::NST); k < n_kv; ++k) tc::bar_wait(&kv_full[k % M::NST], (k / M::NST) & 1, kDrainNs);
+        for (int t = 0; t < 2; ++t)
+          if (n_q[t]) tc::bar_wait(&q_full[t], (n_q[t] - 1) & 1, kDrainNs);
+      }
+    } else if (warp == 8) {
+      // ---------------------------------------------------------------- MMA
+      if (lane == 0) {
+        constexpr uint32_t idS = tc::idesc_bf16(128, 128);
+        constexpr uint32_t idO = tc::idesc_bf16_major(128, D, false, true);
+        int n_kv = 0, n_scrub = 0;
+        int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, first P Vs so far
+        bool issued = false, ok = true;
+        for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
+          const FwdItem it(a, w);
+          const int L = win::valid_len(a.len, it.b, s.N);
+          const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
+          const int n = (kl.n_cols + 127) / 128;
+          if (n == 0) continue;
+          if (a.stall && !wait(&never, 0)) { ok = false; break; }
+          bool q_ready[2] = {false, false}, first[2] = {true, true};
+          auto active = [&](int t, int j) { return win::tile_active(s, kl, L, tile_p0(it, t), tile_p1(it, t), 128 * j); };
+          // stage of key tile j of this item: n_kv + 2 j, of its values one more
+          auto issue_s = [&](int t, int j) -> bool {
+            if (!q_ready[t]) {
+              if (!wait(&q_full[t], n_q[t] & 1)) return false;
+              ++n_q[t];
+              q_ready[t] = true;
+            }
+            const int k = n_kv + 2 * j, st = k % M::NST;
+            if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
+            if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
+            tc::after_sync();
+            issued = true;
+#pragma unroll
+            for (int k2 = 0; k2 < D / 16; ++k2) {
+              const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
+              tc::mma(tm + 128 * t, tc::desc(aQ + t * M::TILE + o), tc::desc(aKV + st * M::TILE + o), idS, k2 > 0);
+            }
+            tc::commit(&s_full[t]);
+            if (j == win::last_tile(kl, L, tile_p0(it, t), tile_p1(it, t))) tc::commit(&q_empty[t]);
+            return true;
+          };
+          auto issue_pv = [&](int t, int j) -> bool {
+            const int k = n_kv + 2 * j + 1, st = k % M::NST;
+            if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
+            if (first[t] && !wait(&o_empty[t], (n_o[t] & 1) ^ 1)) return false;
+            if (!wait(&p_full[t], n_p[t] & 1)) return false;
+            tc::after_sync();
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * kk, tc::desc_mn(aKV + st * M::TILE + kk * 2048, 128 * 128), idO,
+                         !first[t] || kk > 0);
+            tc::commit(&pv_done[t]);
+            if (first[t]) ++n_o[t];
+            first[t] = false;
+            ++n_p[t];
+            return true;
+          };
+          for (int t = 0; ok && t < 2; ++t)
+            if (active(t, 0)) ok = issue_s(t, 0);
+          if (ok) tc::commit(&kv_empty[n_kv % M::NST]);
+          for (int j = 0; ok && j < n && !aborted(); ++j) {
+            // the values of the tile that holds the sequence's end have their padding zeroed
+            if (kl.key(128 * j + 127) >= L && L < s.N) ok = wait(&scrubbed, n_scrub++ & 1);
+            for (int t = 0; ok && t < 2; ++t) {
+              if (active(t, j)) ok = issue_pv(t, j);
+              if (ok && t == 1) tc::commit(&kv_empty[(n_kv + 2 * j + 1) % M::NST]);
+              if (ok && j + 1 < n && active(t, j + 1)) ok = issue_s(t, j + 1);
+            }
+            if (ok && j + 1 < n) tc::commit(&kv_empty[(n_kv + 2 * j + 2) % M::NST]);
+          }
+          n_kv += 2 * n;
+        }
+        if (issued) {
+          tc::commit(&drain);
+          tc::bar_wait(&drain, 0, kDrainNs);
+        }
+      }
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- scrub
+      int n_kv = 0;
+      for (int w = blockIdx.x; a.len && w < a.n_items && !aborted(); w += gridDim.x) {
+        const FwdItem it(a, w);
+        const int L = win::valid_len(a.len, it.b, s.N);
+        const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
+        const int n = (kl.n_cols + 127) / 128;
+        if (n && L < s.N && kl.key(128 * n - 1) >= L) {      // only the last tile can reach the end
+          const int k = n_kv + 2 * n - 1, st = k % M::NST, v0 = 128 * (n - 1);
+          if (!__all_sync(0xffffffffu, wait(&kv_full[st], (k / M::NST) & 1))) break;
+          for (int c = 0; c < 128; ++c)
+            if (v0 + c >= kl.SP && kl.key(v0 + c) >= L)
+              for (int x = lane; x < M::KB * 8; x += 32)
+                *reinterpret_cast<uint4*>(sm + M::oKV + st * M::TILE + (x >> 3) * (128 * 128) + c * 128 + (x & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(&scrubbed);
+        }
+        n_kv += 2 * n;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, output
+    win::regs_inc<208>();
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tm + 128 * t + lane_off, tO = tm + 256 + D * t + lane_off;
+    const float c1 = s.scale * kLog2e;
+    int n_s = 0;                               // key tiles done by this row tile
+    int w = blockIdx.x;
+    for (; w < a.n_items && !aborted(); w += gridDim.x) {
+      const FwdItem it(a, w);
+      const int L = win::valid_len(a.len, it.b, s.N);
+      const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
+      const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
+      const int p = p0 + r / a.P, h = it.h0 + r % a.P;
+      const bool row = p < p1 && p < L;
+      const int n = (kl.n_cols + 127) / 128;
+      float m = neg_inf(), l = 0.f;
+      int done = 0;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        const int v0 = 128 * j;
+        if (!win::tile_active(s, kl, L, p0, p1, v0)) continue;
+        ok = wait(&s_full[t], n_s & 1);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc::after_sync();
+        float x[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float y[32];
+          tc::tmem_ld32(tS + 32 * q, y);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[32 * q + c] = y[c];
+        }
+        // column c is key kb + c (or sink v0 + c): visible iff c <= hi and (c >= lo or c < sk)
+        const int kb = kl.lo + v0 - kl.SP;
+        const int hi = row ? p - kb : -1, lo = max(p - s.window + 1, kl.lo) - kb, sk = s.sinks - v0;
+        const bool all = hi >= 127 && (lo <= 0 || sk >= 128);
+        if (!__all_sync(0xffffffffu, all)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t see = win::bit_range(0, hi - 32 * q) & (win::bit_range(lo - 32 * q, 31) | win::bit_range(0, sk - 1 - 32 * q));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[32 * q + c] = (see >> c) & 1 ? x[32 * q + c] : neg_inf();
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(x[q], x[4 + q]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = tc::max3(mx[q], x[c + q], x[c + 4 + q]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+        const bool grow = top > m + kSlack;                  // also from m = -inf
+        const bool fix = grow && m > neg_inf();              // something has been accumulated
+        float f = 1.f;
+        if (grow) {
+          f = fix ? tc::ex2(m - top) : 1.f;
+          m = top;
+          l *= f;
+        }
+        if (__any_sync(0xffffffffu, fix)) {                  // O waits for the product before, then follows
+          ok = wait(&pv_done[t], (n_s - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc::after_sync();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            float y[32];
+            tc::tmem_ld32(tO + 32 * q, y);
+            uint32_t u[16];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(y[16 * hh + c] * f);
+              tc::tmem_st16(tO + 32 * q + 16 * hh, u);
+            }
+          }
+        }
+        const float mm = m > neg_inf() ? m : 0.f;
+        const uint64_t cc = tc::pack2(c1, c1), nm = tc::pack2(-mm, -mm);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t u[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float y0, y1;
+            tc::unpack2(tc::fma2(tc::pack2(x[16 * q + 2 * c], x[16 * q + 2 * c + 1]), cc, nm), y0, y1);
+            y0 = tc::ex2(y0);
+            y1 = tc::ex2(y1);
+            sum[c & 1] = tc::add2(sum[c & 1], tc::pack2(y0, y1));
+            u[c] = pack_bf16(y0, y1);
+          }
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tS + 8 * q), "r"(u[0]),
+                       "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                       : "memory");
+        }
+        tc::tmem_wait_st();
+        tc::before_sync();
+        tc::bar_arrive(&p_full[t]);
+        float s0, s1;
+        tc::unpack2(tc::add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        ++n_s;
+        ++done;
+      }
+      if (!ok) break;
+      if (p0 >= s.off + s.Nq) continue;                      // a tile past the last query
+      if (done) {
+        ok = wait(&pv_done[t], (n_s - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc::after_sync();
+      }
+      if (p < p1)
+        a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + p - s.off] = l == 0.f ? neg_inf() : (m + log2f(l)) * kLn2;
+      const float inv = 1.f / l;                             // l = 0: an empty row, whose output is 0
+      unsigned char* stg = sm + M::oStage + warp * M::STG;
+      const int tk = it.t0 + t * a.tok + (warp & 3) * 32 / a.P;   // the warp's first token
+#pragma unroll 1
+      for (int kb = 0; kb < M::KB; ++kb) {
+        uint32_t u[32];
+        if (done) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float y[32];
+            tc::tmem_ld32(tO + 64 * kb + 32 * q, y);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) u[16 * q + c] = l == 0.f ? 0u : pack_bf16(y[2 * c] * inv, y[2 * c + 1] * inv);
+          }
+          if (kb == M::KB - 1) {
+            tc::before_sync();
+            tc::bar_arrive(&o_empty[t]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) u[c] = 0u;
+        }
+        if (lane == 0) tc::bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (tk < s.Nq) win::tma_store4(&omap, 64 * kb, it.h0, tk, it.b, aStage + warp * M::STG);
+          tc::bulk_commit();
+        }
+      }
+    }
+    if (lane == 0) tc::bulk_wait<0>();
+    if (aborted()) {                                         // the rows of the item at hand and of those left
+      for (; w < a.n_items; w += gridDim.x) {
+        const FwdItem it(a, w);
+        const int i = it.t0 + t * a.tok + r / a.P, h = it.h0 + r % a.P;
+        if (i >= s.Nq) continue;
+        a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + i] = __int_as_float(0x7fc00000);
+        uint4* o = reinterpret_cast<uint4*>(a.O + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
+        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+      }
+    }
+  }
+  tc::before_sync();
+  __syncthreads();
+  if (tid == 0 && s_abort) atomicOr(a.status, PISA_STATUS_TIMEOUT);
+  if (warp == 0) {
+    tc::after_sync();
+    tc::tmem_free(tm, 512);
+  }
+}
+
+// Map of [B, N, H, d] bf16 with `stride` elements between tokens; boxes of 64 elements x `heads` x `tokens`.
+int token_map(CUtensorMap* m, const void* p, int B, int N, int H, int d, int64_t stride, int heads, int tokens) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(H), static_cast<uint64_t>(N),
+                            static_cast<uint64_t>(B)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2,
+                               static_cast<uint64_t>(stride) * 2 * N};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(heads), static_cast<uint32_t>(tokens), 1};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box);
+}
+
+// The softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread.
+template <int D>
+bool registers_fit() {
+  static const bool fit = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, window_fwd_kernel<D>) == cudaSuccess && f.numRegs >= 168;
+  }();
+  return fit;
+}
+
+template <int D>
+int fwd_launch(const FwdArgs& a, const CUtensorMap* m, int grid, cudaStream_t st) {
+  if (!registers_fit<D>()) return static_cast<int>(cudaErrorInvalidKernelImage);
+  cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdSmem<D>::bytes);
+  if (e != cudaSuccess) return e;
+  ProfScope ps(st, "window_fwd");
+  window_fwd_kernel<D><<<grid, kThreads, FwdSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -47,15 +476,31 @@ __global__ void __launch_bounds__(32 * kWarps) window_fwd_kernel(const WinDims s
 int launch_window_fwd(const WinDims& s, const void* Q, const void* K, const void* V, const int32_t* len, void* O,
                       float* lse, char* ws, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  FwdArgs a{};
+  a.s = s;
+  a.len = len;
+  a.O = static_cast<__nv_bfloat16*>(O);
+  a.lse = lse;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.wait_ns = wait_limit_ns();
+  a.stall = test_stall();
+  a.P = win::packed_heads(s.G);
+  a.tok = 128 / a.P;
+  a.n_tiles = (s.Nq + 2 * a.tok - 1) / (2 * a.tok);
+  a.n_heads = s.B * s.Hkv * (s.G / a.P);
+  const int64_t items = static_cast<int64_t>(a.n_tiles) * a.n_heads;   // < B N Hq
+  a.n_items = static_cast<int>(items);
+  CUtensorMap m[6];
+  if (int e = token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
+  if (int e = token_map(&m[1], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
+  if (int e = token_map(&m[2], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 128)) return e;
+  if (int e = token_map(&m[3], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
+  if (int e = token_map(&m[4], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
+  if (int e = token_map(&m[5], O, s.B, s.Nq, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
   if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(s.B) * s.Nq * s.Hq;
-  const unsigned blocks = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-  auto k = s.d == 128 ? window_fwd_kernel<128> : window_fwd_kernel<64>;
-  ProfScope ps(st, "window_fwd");
-  k<<<blocks, 32 * kWarps, 0, st>>>(s, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(K),
-                                    static_cast<const __nv_bfloat16*>(V), len, static_cast<__nv_bfloat16*>(O), lse);
-  return cudaGetLastError();
+  const int grid = static_cast<int>(std::min<int64_t>(items, sm_count()));
+  return s.d == 128 ? fwd_launch<128>(a, m, grid, st) : fwd_launch<64>(a, m, grid, st);
 }
 
 }  // namespace pisa

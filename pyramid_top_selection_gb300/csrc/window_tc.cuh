@@ -1,0 +1,100 @@
+// What the tensor-core kernels of the window attention share: bounded waits that sleep, register
+// moves between warpgroups, and the walk over a query tile's keys.
+#pragma once
+
+#include "tc.cuh"
+#include "window.h"
+
+namespace pisa {
+namespace win {
+
+// Wait for the phase of `bar` with this parity: sleeps in try_wait, gives up (and sets the CTA's
+// abort flag) after limit_ns nanoseconds, or at once when the CTA has aborted.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint64_t limit_ns) {
+  const uint32_t a = tc::su32(bar);
+  uint64_t t0 = 0;
+  for (int it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = tc::global_ns();
+    if ((it & 15) == 15) {
+      if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+      if (tc::global_ns() - t0 > limit_ns) break;
+    }
+  }
+  atomicOr(abort_flag, 1);
+  return false;
+}
+
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// TMA store of a shared-memory box into a 4-D tensor map at (c0, c1, c2, c3); what lies outside the
+// tensor is not written.
+__device__ __forceinline__ void tma_store4(const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+               : "memory");
+}
+
+// Heads of a group that share a 128-row tile: the largest power of two dividing G, at most 16. A
+// tile's rows are (token, head), heads fastest, so it covers 128 / P tokens and keys are read
+// once for its P heads; fewer tokens a tile also means fewer masked keys at a window's edges.
+inline int packed_heads(int G) {
+  int p = 1;
+  while (p < 16 && G % (2 * p) == 0) p *= 2;
+  return p;
+}
+
+// Bits a .. b (inclusive, any integers) of a 32-bit mask.
+__device__ __forceinline__ uint32_t bit_range(int a, int b) {
+  const uint32_t up = b < 0 ? 0u : b >= 31 ? 0xffffffffu : (2u << b) - 1;
+  const uint32_t lo = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : ~((1u << a) - 1);
+  return up & lo;
+}
+
+// Valid tokens of sequence b.
+__device__ __forceinline__ int valid_len(const int32_t* len, int b, int N) {
+  return len ? max(0, min(__ldg(len + b), N)) : N;
+}
+
+// The keys of a run of query positions [p0, p1) of one sequence as one list of columns: first the
+// sinks (padded to SP columns, a multiple of 32) when all of these lie before the window's first
+// key, then keys lo ... Column v holds key v (v < SP) or lo + v - SP. Otherwise the list simply
+// starts at key 0. So every padding column holds a key below lo, one of the sequence's.
+struct KeyList {
+  int lo, SP, n_cols;
+  __device__ __forceinline__ KeyList(const WinDims& s, int L, int p0, int p1) {
+    const int last = min(p1, L) - 1;
+    lo = max(0, p0 - s.window + 1);
+    SP = (s.sinks + 31) & ~31;
+    if (lo < SP) lo = SP = 0;
+    n_cols = last >= p0 ? SP + last - lo + 1 : 0;
+  }
+  __device__ __forceinline__ int key(int v) const { return v < SP ? v : lo + v - SP; }
+};
+
+// The last 128-column tile with keys that a position in [p0, p1) sees (-1: none).
+__device__ __forceinline__ int last_tile(const KeyList& kl, int L, int p0, int p1) {
+  const int last = min(p1, L) - 1;
+  return last < p0 ? -1 : (kl.SP + last - kl.lo) >> 7;
+}
+
+// Whether the 128 columns at v0 hold a key that some position in [p0, p1) sees.
+__device__ __forceinline__ bool tile_active(const WinDims& s, const KeyList& kl, int L, int p0, int p1, int v0) {
+  const int last = min(p1, L) - 1;
+  if (last < p0) return false;
+  const int vend = kl.SP + last - kl.lo + 1, vbeg = kl.SP + max(kl.lo, p0 - s.window + 1) - kl.lo;
+  return v0 < vend && (v0 + 128 > vbeg || v0 < s.sinks);
+}
+
+}  // namespace win
+}  // namespace pisa
