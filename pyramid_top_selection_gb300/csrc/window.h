@@ -16,7 +16,7 @@ struct WinDims {
 };
 
 struct WinBwdWs {
-  size_t status, delta, total;
+  size_t status, nlse, delta, part, total;
 };
 WinBwdWs window_bwd_ws(const WinDims& s);
 

@@ -17,9 +17,8 @@
 //   * softmax (warps 0-3 and 4-7, one row tile each, one row a thread): S row from tensor
 //     memory into registers, masks where the tile touches an edge, maximum, exponentials, sum, P
 //     as bf16 over the first half of S's columns; at the item's end O / l to bf16 through a
-//     staging tile and TMA stores;
-//   * scrub (warp 10): zeroes value rows at tokens >= len in the tile that holds the sequence's
-//     end, so that padding's values (NaN, say) do not meet P = 0.
+//     staging tile and TMA stores. In the tile that holds the sequence's end they also zero the
+//     value rows at tokens >= len, so that padding's values (NaN, say) do not meet P = 0.
 // TMEM: S (and P) of row tile t at 128 t, O at 256 + d t: all 512 columns at d = 128.
 // P is rounded to bf16 for the product (2^-8 relative at most); the sum l takes it unrounded.
 // Every wait is bounded; one that gives up sets the CTA's abort flag, every role leaves, copies and
@@ -48,7 +47,7 @@ struct FwdSmem {
   static constexpr int NST = 256 / D * 2;            // K / V stages: 128 KB in all
   static constexpr int oQ = 0, oKV = 2 * TILE, oStage = oKV + NST * TILE;
   static constexpr int STG = 32 * 128;               // a warp's 32 rows x 64 bf16
-  static constexpr int bytes = oStage + 8 * STG + 1024;
+  static constexpr int bytes = oStage + 8 * STG;
 };
 
 struct FwdArgs {
@@ -80,15 +79,14 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kmap32,
                   const __grid_constant__ CUtensorMap vmap32, const __grid_constant__ CUtensorMap omap) {
   using M = FwdSmem<D>;
-  extern __shared__ unsigned char smraw[];
+  extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[M::NST], kv_empty[M::NST], s_full[2], p_full[2],
-      pv_done[2], o_empty[2], scrubbed, drain, never;
+      pv_done[2], o_empty[2], drain, never;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
 
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned char* sm = smraw + ((1024 - (tc::su32(smraw) & 1023)) & 1023);
   const uint32_t aQ = tc::su32(sm + M::oQ), aKV = tc::su32(sm + M::oKV), aStage = tc::su32(sm + M::oStage);
 
   if (tid == 0) {
@@ -104,7 +102,6 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       tc::bar_init(&kv_full[k], 1);
       tc::bar_init(&kv_empty[k], 1);
     }
-    tc::bar_init(&scrubbed, 1);
     tc::bar_init(&drain, 1);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
@@ -176,7 +173,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       if (lane == 0) {
         constexpr uint32_t idS = tc::idesc_bf16(128, 128);
         constexpr uint32_t idO = tc::idesc_bf16_major(128, D, false, true);
-        int n_kv = 0, n_scrub = 0;
+        int n_kv = 0;
         int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, first P Vs so far
         bool issued = false, ok = true;
         for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
@@ -229,8 +226,6 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
             if (active(t, 0)) ok = issue_s(t, 0);
           if (ok) tc::commit(&kv_empty[n_kv % M::NST]);
           for (int j = 0; ok && j < n && !aborted(); ++j) {
-            // the values of the tile that holds the sequence's end have their padding zeroed
-            if (kl.key(128 * j + 127) >= L && L < s.N) ok = wait(&scrubbed, n_scrub++ & 1);
             for (int t = 0; ok && t < 2; ++t) {
               if (active(t, j)) ok = issue_pv(t, j);
               if (ok && t == 1) tc::commit(&kv_empty[(n_kv + 2 * j + 1) % M::NST]);
@@ -245,28 +240,6 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           tc::bar_wait(&drain, 0, kDrainNs);
         }
       }
-    } else if (warp == 10) {
-      // ---------------------------------------------------------------- scrub
-      int n_kv = 0;
-      for (int w = blockIdx.x; a.len && w < a.n_items && !aborted(); w += gridDim.x) {
-        const FwdItem it(a, w);
-        const int L = win::valid_len(a.len, it.b, s.N);
-        const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
-        const int n = (kl.n_cols + 127) / 128;
-        if (n && L < s.N && kl.key(128 * n - 1) >= L) {      // only the last tile can reach the end
-          const int k = n_kv + 2 * n - 1, st = k % M::NST, v0 = 128 * (n - 1);
-          if (!__all_sync(0xffffffffu, wait(&kv_full[st], (k / M::NST) & 1))) break;
-          for (int c = 0; c < 128; ++c)
-            if (v0 + c >= kl.SP && kl.key(v0 + c) >= L)
-              for (int x = lane; x < M::KB * 8; x += 32)
-                *reinterpret_cast<uint4*>(sm + M::oKV + st * M::TILE + (x >> 3) * (128 * 128) + c * 128 + (x & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-          tc::fence_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::bar_arrive(&scrubbed);
-        }
-        n_kv += 2 * n;
-      }
     }
   } else {
     // ------------------------------------------------------------------ softmax, output
@@ -275,16 +248,16 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tm + 128 * t + lane_off, tO = tm + 256 + D * t + lane_off;
     const float c1 = s.scale * kLog2e;
-    int n_s = 0;                               // key tiles done by this row tile
+    int n_s = 0, n_kv = 0;                     // key tiles done by this row tile; stages used by earlier items
     int w = blockIdx.x;
-    for (; w < a.n_items && !aborted(); w += gridDim.x) {
+    for (int n = 0; w < a.n_items && !aborted(); w += gridDim.x, n_kv += 2 * n) {
       const FwdItem it(a, w);
       const int L = win::valid_len(a.len, it.b, s.N);
       const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
       const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
+      n = (kl.n_cols + 127) / 128;
       const int p = p0 + r / a.P, h = it.h0 + r % a.P;
       const bool row = p < p1 && p < L;
-      const int n = (kl.n_cols + 127) / 128;
       float m = neg_inf(), l = 0.f;
       int done = 0;
       bool ok = true;
@@ -366,6 +339,19 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
                        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                        : "memory");
         }
+        // padding's values (only the last tile can reach past the sequence) become zero; of two row
+        // tiles that use the tile, the first, whose product the MMA thread issues first, does it
+        if (L < s.N && kl.key(v0 + 127) >= L &&
+            (t == 0 || !win::tile_active(s, kl, L, tile_p0(it, 0), tile_p1(it, 0), v0))) {
+          const int k = n_kv + 2 * j + 1, st = k % M::NST;
+          ok = wait(&kv_full[st], (k / M::NST) & 1);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          if (v0 + r >= kl.SP && kl.key(v0 + r) >= L)
+            for (int c = 0; c < M::KB * 8; ++c)
+              *reinterpret_cast<uint4*>(sm + M::oKV + st * M::TILE + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          tc::fence_async_smem();
+        }
         tc::tmem_wait_st();
         tc::before_sync();
         tc::bar_arrive(&p_full[t]);
@@ -441,16 +427,6 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   }
 }
 
-// Map of [B, N, H, d] bf16 with `stride` elements between tokens; boxes of 64 elements x `heads` x `tokens`.
-int token_map(CUtensorMap* m, const void* p, int B, int N, int H, int d, int64_t stride, int heads, int tokens) {
-  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(H), static_cast<uint64_t>(N),
-                            static_cast<uint64_t>(B)};
-  const uint64_t strides[3] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2,
-                               static_cast<uint64_t>(stride) * 2 * N};
-  const uint32_t box[4] = {64, static_cast<uint32_t>(heads), static_cast<uint32_t>(tokens), 1};
-  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box);
-}
-
 // The softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread.
 template <int D>
 bool registers_fit() {
@@ -491,12 +467,12 @@ int launch_window_fwd(const WinDims& s, const void* Q, const void* K, const void
   const int64_t items = static_cast<int64_t>(a.n_tiles) * a.n_heads;   // < B N Hq
   a.n_items = static_cast<int>(items);
   CUtensorMap m[6];
-  if (int e = token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
-  if (int e = token_map(&m[1], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
-  if (int e = token_map(&m[2], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 128)) return e;
-  if (int e = token_map(&m[3], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
-  if (int e = token_map(&m[4], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
-  if (int e = token_map(&m[5], O, s.B, s.Nq, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
+  if (int e = win::token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
+  if (int e = win::token_map(&m[1], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
+  if (int e = win::token_map(&m[2], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 128)) return e;
+  if (int e = win::token_map(&m[3], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
+  if (int e = win::token_map(&m[4], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
+  if (int e = win::token_map(&m[5], O, s.B, s.Nq, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
   if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(std::min<int64_t>(items, sm_count()));

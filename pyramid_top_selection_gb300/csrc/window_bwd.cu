@@ -1,9 +1,25 @@
-// Sliding-window attention with sinks, backward: D = dO . O per row, then dQ with one warp per
-// (query, head) row over its keys, and dK, dV with one warp per (key, KV head) over the rows
-// that see it (no atomics: the order of every sum is fixed).
+// Sliding-window attention with sinks, backward, on the fifth-generation tensor cores.
+//
+// P = exp(s q.k - lse), D = dO . O, dS = P (dO . v - D):  dQ = s dS K,  dK = s dS^T Q,  dV = P^T dO.
+// Two kernels, each with its sums in tensor memory and no atomics, so the order of every sum is
+// fixed: one walks the keys of a row tile (dQ: S, dP and dQ products), one the rows of a key tile
+// (dK, dV: S^T, dP^T, dV and dK products). S and dP are formed twice, 7 products instead of 5; one
+// kernel for all three would have to add dQ tiles into an fp32 buffer in memory, whose reductions
+// bound the selected blocks' backward kernel (attn_bwd_tc.cu), in an order that changes.
+//
+// Rows are packed as in the forward (window_tc.cuh): a 128-row tile is (token, head) rows, P heads
+// of the group together. dQ's kernel also writes -lse log2 e and D per row, in tile order, for the
+// second kernel.
+//
+// P and dS are rounded to bf16 for their products (2^-8 relative at most), sums are fp32. Every wait
+// is bounded; one that gives up poisons what its CTA leaves unfinished.
+#include <algorithm>
+
 #include "device.cuh"
+#include "internal.h"
 #include "profile.h"
-#include "window.h"
+#include "tmap.h"
+#include "window_tc.cuh"
 
 namespace pisa {
 
@@ -11,129 +27,893 @@ size_t align256(size_t x);
 
 namespace {
 
-constexpr int kWarps = 8;
 using bf16 = __nv_bfloat16;
+constexpr int kThreads = 320;                  // warps 0-7 softmax and output, 8 MMA, 9 loader
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
+constexpr uint32_t kNaN2 = 0x7fc07fc0u;        // two bf16 NaNs
 
-struct WinBwdArgs {
+struct BwdArgs {
   WinDims s;
-  const bf16 *Q, *K, *V, *O, *dO;
-  const float* lse;
   const int32_t* len;
-  float* delta;    // [B, Nq, Hq]
+  const bf16* O;
+  const float* lse;
+  float *nlse, *delta;     // [B][Hkv][sets][Nqp][P]: -lse log2 e and D
   bf16 *dQ, *dK, *dV;
+  float* part;             // fp32 partial sums of dV, dK: [slot][2][128][D]
+  int32_t* status;
+  uint64_t wait_ns;
+  int stall;
+  int P, tok, sets, Nqp;   // heads and tokens of a row tile, head sets of a group, padded Nq
+  int n_tiles, n_heads, n_items;           // dQ: token tiles, (b, kv, set), items
+  // dK, dV: key tiles, (b, kv), key tiles with sinks, token tiles of a chunk, chunks of a band and
+  // of a sink tile, items of the bands
+  int n_kt, n_bh, n_st, ct, nck, ncs, n_reg;
 };
 
+// ------------------------------------------------------------------------------------------ dQ
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) window_dq_kernel(const WinBwdArgs a) {
-  constexpr int E = D / 32;
+struct DqSmem {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * 128 * 128;
+  static constexpr int NK = 3, NV = 2;               // a key tile is held from S to dQ, its values only for dP
+  static constexpr int oQ = 0, oO = TILE, oK = 2 * TILE, oV = oK + NK * TILE;
+  static constexpr int bytes = oV + NV * TILE;
+};
+
+struct DqItem {
+  int b, kv, set, t0;
+  __device__ __forceinline__ DqItem(const BwdArgs& a, int w) {
+    const int tile = a.n_tiles - 1 - w / a.n_heads, hh = w % a.n_heads;
+    b = hh / (a.s.Hkv * a.sets);
+    kv = hh / a.sets % a.s.Hkv;
+    set = hh % a.sets;
+    t0 = tile * a.tok;
+  }
+};
+
+// TMEM: S (and dS in its place) of key tile n at 128 (n & 1), dP at 256, dQ at 384. Per key tile the
+// MMA thread issues the next S, then (dS ready) the next dP, then dQ += dS K, so that the tensor
+// cores work on two products while the softmax warps turn S and dP into dS.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ CUtensorMap kmap32, const __grid_constant__ CUtensorMap vmap32,
+                 const __grid_constant__ CUtensorMap dqmap) {
+  using M = DqSmem<D>;
+  extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
+  __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
+      s_full[2], dp_full, ds_full, dq_done, dq_last, dq_empty, exch, drain, never;
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_abort;
+  __shared__ float s_dot[2][128];
+
   const WinDims& s = a.s;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(s.B) * s.Nq * s.Hq) return;
-  const int lane = threadIdx.x & 31, h = static_cast<int>(row % s.Hq);
-  const int64_t tok = row / s.Hq;
-  const int i = static_cast<int>(tok % s.Nq), b = static_cast<int>(tok / s.Nq), kv = h / s.G;
-  const int L = a.len ? max(0, min(a.len[b], s.N)) : s.N, p = i + s.off;
-  float q[E], g[E], acc[E] = {}, dl = 0.f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.Q[tok * s.qs + h * D + lane * E + e]);
-    g[e] = __bfloat162float(a.dO[row * D + lane * E + e]);
-    dl += g[e] * __bfloat162float(a.O[row * D + lane * E + e]);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t aQ = tc::su32(sm + M::oQ), aO = tc::su32(sm + M::oO), aK = tc::su32(sm + M::oK), aV = tc::su32(sm + M::oV);
+
+  if (tid == 0) {
+    tc::bar_init(&q_full, 1);
+    tc::bar_init(&q_empty, 8);
+    for (int k = 0; k < M::NK; ++k) {
+      tc::bar_init(&k_full[k], 1);
+      tc::bar_init(&k_empty[k], 1);
+    }
+    for (int k = 0; k < M::NV; ++k) {
+      tc::bar_init(&v_full[k], 1);
+      tc::bar_init(&v_empty[k], 1);
+    }
+    tc::bar_init(&s_full[0], 1);
+    tc::bar_init(&s_full[1], 1);
+    tc::bar_init(&dp_full, 1);
+    tc::bar_init(&ds_full, 256);
+    tc::bar_init(&dq_done, 1);
+    tc::bar_init(&dq_last, 1);
+    tc::bar_init(&dq_empty, 256);
+    tc::bar_init(&exch, 256);
+    tc::bar_init(&drain, 1);
+    tc::bar_init(&never, 1);
+    tc::fence_bar_init();
+    s_abort = 0;
   }
-  dl = warp_sum(dl);
-  if (lane == 0) a.delta[row] = dl;
-  if (p < L) {
-    const float ls = a.lse[(static_cast<int64_t>(b) * s.Hq + h) * s.Nq + i];
-    const int lo = max(0, p - s.window + 1);
-    auto key = [&](int j) {
-      const int64_t kr = static_cast<int64_t>(b) * s.N + j;
-      float x = 0.f, y = 0.f, k[E];
-      for (int e = 0; e < E; ++e) {
-        k[e] = __bfloat162float(a.K[kr * s.ks + kv * D + lane * E + e]);
-        x += q[e] * k[e];
-        y += g[e] * __bfloat162float(a.V[kr * s.vs + kv * D + lane * E + e]);
+  if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
+  tc::before_sync();
+  __syncthreads();
+  tc::after_sync();
+  const uint32_t tm = tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
+  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+
+  if (warp == 9) {
+    // ------------------------------------------------------------------ loader
+    if (lane == 0) {
+      int n_k = 0, n_v = 0, n_q = 0;           // loads issued
+      for (int w = blockIdx.x; w < a.n_items && !aborted(); w += gridDim.x) {
+        const DqItem it(a, w);
+        const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
+        const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
+        if (kl.n_cols == 0) continue;
+        auto load = [&](int& k, uint64_t* full, uint64_t* empty, int ns, uint32_t base, int v0, const CUtensorMap* big,
+                        const CUtensorMap* small) -> bool {
+          const int st = k % ns;
+          if (!wait(&empty[st], ((k / ns) & 1) ^ 1)) return false;
+          ++k;
+          tc::bar_expect_tx(&full[st], M::TILE);
+          const uint32_t dst = base + st * M::TILE;
+          if (v0 >= kl.SP) {
+#pragma unroll
+            for (int kb = 0; kb < M::KB; ++kb)
+              tc::tma_load4(dst + kb * (128 * 128), big, kb * 64, it.kv, kl.key(v0), it.b, &full[st]);
+          } else {
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int kb = 0; kb < M::KB; ++kb)
+                tc::tma_load4(dst + kb * (128 * 128) + r * (32 * 128), small, kb * 64, it.kv, kl.key(v0 + 32 * r), it.b, &full[st]);
+          }
+          return true;
+        };
+        if (!wait(&q_empty, (n_q & 1) ^ 1)) break;
+        ++n_q;
+        tc::bar_expect_tx(&q_full, 2 * M::TILE);
+#pragma unroll
+        for (int kb = 0; kb < M::KB; ++kb) {
+          tc::tma_load4(aQ + kb * (128 * 128), &qmap, kb * 64, it.kv * s.G + it.set * a.P, it.t0, it.b, &q_full);
+          tc::tma_load4(aO + kb * (128 * 128), &domap, kb * 64, it.kv * s.G + it.set * a.P, it.t0, it.b, &q_full);
+        }
+        bool ok = true;
+        for (int v0 = 0; ok && v0 < kl.n_cols; v0 += 128)
+          ok = load(n_k, k_full, k_empty, M::NK, aK, v0, &kmap, &kmap32) &&
+               load(n_v, v_full, v_empty, M::NV, aV, v0, &vmap, &vmap32);
+        if (!ok) break;
       }
-      const float ds = __expf(s.scale * warp_sum(x) - ls) * (warp_sum(y) - dl) * s.scale;
-      for (int e = 0; e < E; ++e) acc[e] += ds * k[e];
-    };
-    for (int j = 0; j < min(s.sinks, lo); ++j) key(j);
-    for (int j = lo; j <= p; ++j) key(j);
+      // whatever is still in flight lands before the CTA leaves
+      for (int k = max(0, n_k - M::NK); k < n_k; ++k) tc::bar_wait(&k_full[k % M::NK], (k / M::NK) & 1, kDrainNs);
+      for (int k = max(0, n_v - M::NV); k < n_v; ++k) tc::bar_wait(&v_full[k % M::NV], (k / M::NV) & 1, kDrainNs);
+      if (n_q) tc::bar_wait(&q_full, (n_q - 1) & 1, kDrainNs);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idS = tc::idesc_bf16(128, 128);
+      constexpr uint32_t idQ = tc::idesc_bf16_major(128, D, false, true);
+      int n_q = 0, n_k = 0;
+      bool issued = false, ok = true;
+      for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
+        const DqItem it(a, w);
+        const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
+        const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
+        const int n = (kl.n_cols + 127) / 128;
+        if (n == 0) continue;
+        if (a.stall && !wait(&never, 0)) { ok = false; break; }
+        // g: key tiles so far. The dS that was in S's place has been read: that of two tiles ago, or,
+        // at an item's start, where all earlier products may be done, the last one's
+        auto issue_s = [&](int g, int before) -> bool {
+          const int st = g % M::NK;
+          if (!wait(&k_full[st], (g / M::NK) & 1)) return false;
+          if (before >= 0 && !wait(&dq_done, before & 1)) return false;
+          tc::after_sync();
+          issued = true;
+#pragma unroll
+          for (int k2 = 0; k2 < D / 16; ++k2) {
+            const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
+            tc::mma(tm + 128 * (g & 1), tc::desc(aQ + o), tc::desc(aK + st * M::TILE + o), idS, k2 > 0);
+          }
+          tc::commit(&s_full[g & 1]);
+          return true;
+        };
+        auto issue_dp = [&](int g) -> bool {
+          const int st = g % M::NV;
+          if (!wait(&v_full[st], (g / M::NV) & 1)) return false;
+          tc::after_sync();
+#pragma unroll
+          for (int k2 = 0; k2 < D / 16; ++k2) {
+            const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
+            tc::mma(tm + 256, tc::desc(aO + o), tc::desc(aV + st * M::TILE + o), idS, k2 > 0);
+          }
+          tc::commit(&dp_full);
+          tc::commit(&v_empty[st]);
+          return true;
+        };
+        ok = wait(&q_full, n_q & 1) && issue_s(n_k, n_k - 1) && issue_dp(n_k);
+        for (int j = 0; ok && j < n && !aborted(); ++j) {
+          const int g = n_k + j;
+          if (j + 1 < n && !issue_s(g + 1, g - 1)) { ok = false; break; }
+          if (!wait(&ds_full, g & 1)) { ok = false; break; }
+          if (j + 1 < n && !issue_dp(g + 1)) { ok = false; break; }
+          if (j == 0 && !wait(&dq_empty, (n_q & 1) ^ 1)) { ok = false; break; }
+          tc::after_sync();
+          const int st = g % M::NK;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_ts(tm + 384, tm + 128 * (g & 1) + 64 * (kk >> 2) + 8 * (kk & 3),
+                       tc::desc_mn(aK + st * M::TILE + kk * 2048, 128 * 128), idQ, j > 0 || kk > 0);
+          tc::commit(&dq_done);
+          tc::commit(&k_empty[st]);
+          if (j + 1 == n) tc::commit(&dq_last);   // (dq_done may be two phases behind the softmax warps)
+        }
+        ++n_q;
+        n_k += n;
+      }
+      if (issued) {
+        tc::commit(&drain);
+        tc::bar_wait(&drain, 0, kDrainNs);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ softmax: row r, columns 64 g ..
+    const int g = warp >> 2, r = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float c1 = s.scale * kLog2e;
+    int n_k = 0, n_q = 0, w = blockIdx.x;
+    for (; w < a.n_items && !aborted(); w += gridDim.x) {
+      const DqItem it(a, w);
+      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0, p1 = s.off + min(s.Nq, it.t0 + a.tok);
+      const win::KeyList kl(s, L, p0, p1);
+      const int n = (kl.n_cols + 127) / 128;
+      const int hp = r % a.P, i = it.t0 + r / a.P, p = s.off + i, h = it.kv * s.G + it.set * a.P + hp;
+      const bool row = p < p1 && p < L;
+      if (n == 0) {                                          // no row sees anything: dQ = 0
+        if (g == 0 && i < s.Nq) {
+          uint4* o = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
+          for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      // D = dO . O, half a row each; the halves meet in shared memory
+      bool ok = wait(&q_full, n_q & 1);
+      float nl = 0.f, dl = 0.f;
+      if (row) {
+        const bf16* o = a.O + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D + g * (D / 2);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint4 u = ldg_u4(o + 8 * c);
+          const int col = g * (D / 2) + 8 * c;
+          const uint4 v = *reinterpret_cast<const uint4*>(sm + M::oO + (col >> 6) * (128 * 128) + tc::sw128(r, col & 63));
+          const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            dl = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(vv[k] << 16), dl);
+            dl = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(vv[k] & 0xffff0000u), dl);
+          }
+        }
+        nl = -a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + i] * kLog2e;
+      }
+      s_dot[g][r] = dl;
+      tc::bar_arrive(&exch);
+      ok = ok && wait(&exch, n_q & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      dl = s_dot[0][r] + s_dot[1][r];
+      if (g == 0 && i < s.Nq) {
+        const int64_t at = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + it.set) * a.Nqp + i) * a.P + hp;
+        a.nlse[at] = nl;
+        a.delta[at] = dl;
+      }
+      for (int j = 0; j < n; ++j, ++n_k) {
+        const int v0 = 128 * j + 64 * g;
+        ok = wait(&s_full[n_k & 1], (n_k >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc::after_sync();
+        float x[64], y[64];
+        const uint32_t tS = tm + 128 * (n_k & 1) + 64 * g + lane_off;
+        tc::tmem_ld64(tS, x);
+        const int kb = kl.lo + v0 - kl.SP;
+        const int hi = row ? p - kb : -1, lo = max(p - s.window + 1, kl.lo) - kb, sk = s.sinks - v0;
+        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+        const bool masked = !__all_sync(0xffffffffu, hi >= 63 && (lo <= 0 || sk >= 64));
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            see[q] = win::bit_range(0, hi - 32 * q) & (win::bit_range(lo - 32 * q, 31) | win::bit_range(0, sk - 1 - 32 * q));
+        }
+        const uint64_t cc = tc::pack2(c1, c1), ll = tc::pack2(nl, nl), dd = tc::pack2(-dl, -dl);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float y0, y1;
+          tc::unpack2(tc::fma2(tc::pack2(x[c], x[c + 1]), cc, ll), y0, y1);
+          x[c] = tc::ex2(y0);
+          x[c + 1] = tc::ex2(y1);
+        }
+        ok = wait(&dp_full, n_k & 1);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc::after_sync();
+        tc::tmem_ld64(tm + 256 + 64 * g + lane_off, y);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float e0, e1;
+          tc::unpack2(tc::add2(tc::pack2(y[c], y[c + 1]), dd), e0, e1);
+          x[c] *= e0;
+          x[c + 1] *= e1;
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t u[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) u[c] = pack_bf16(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
+          tc::tmem_st16(tS + 16 * q, u);
+        }
+        // keys at tokens >= len (the last tile's; S has read them) become zero: dS = 0 there, and dQ
+        // must not meet what padding holds
+        if (g == 0 && L < s.N && kl.key(128 * j + 127) >= L) {
+          if (128 * j + r >= kl.SP && kl.key(128 * j + r) >= L)
+            for (int c = 0; c < M::KB * 8; ++c)
+              *reinterpret_cast<uint4*>(sm + M::oK + (n_k % M::NK) * M::TILE + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          tc::fence_async_smem();
+        }
+        tc::tmem_wait_st();
+        tc::before_sync();
+        tc::bar_arrive(&ds_full);
+      }
+      if (!ok) break;
+      // dQ of the item, scaled, through Q's shared memory (nothing reads that any more)
+      ok = wait(&dq_last, n_q & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc::after_sync();
+      ++n_q;
+      if (g < M::KB) {
+        float x[64];
+        tc::tmem_ld64(tm + 384 + 64 * g + lane_off, x);
+        unsigned char* stg = sm + M::oQ + g * (128 * 128);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[k] = pack_bf16(s.scale * x[8 * c + 2 * k], s.scale * x[8 * c + 2 * k + 1]);
+          *reinterpret_cast<uint4*>(stg + tc::sw128(r, 8 * c)) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        const int tk = it.t0 + (warp & 3) * 32 / a.P;
+        if (lane == 0) {
+          if (tk < s.Nq)
+            win::tma_store4(&dqmap, 64 * g, it.kv * s.G + it.set * a.P, tk, it.b, aQ + g * (128 * 128) + (warp & 3) * (32 * 128));
+          tc::bulk_commit();
+          tc::bulk_wait_read<0>();
+        }
+        __syncwarp();
+      }
+      tc::before_sync();
+      tc::bar_arrive(&dq_empty);
+      if (lane == 0) tc::bar_arrive(&q_empty);
+    }
+    if (lane == 0) tc::bulk_wait<0>();
+    if (aborted() && g == 0) {                               // the rows of the item at hand and of those left
+      for (; w < a.n_items; w += gridDim.x) {
+        const DqItem it(a, w);
+        const int i = it.t0 + r / a.P, h = it.kv * s.G + it.set * a.P + r % a.P;
+        if (i >= s.Nq) continue;
+        uint4* o = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
+        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(kNaN2, kNaN2, kNaN2, kNaN2);
+      }
+    }
   }
-  for (int e = 0; e < E; ++e) a.dQ[row * D + lane * E + e] = __float2bfloat16_rn(acc[e]);
+  tc::before_sync();
+  __syncthreads();
+  if (tid == 0 && s_abort) atomicOr(a.status, PISA_STATUS_TIMEOUT);
+  if (warp == 0) {
+    tc::after_sync();
+    tc::tmem_free(tm, 512);
+  }
+}
+
+// --------------------------------------------------------------------------------------- dK, dV
+template <int D>
+struct DkvSmem {
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = KB * 128 * 128;
+  static constexpr int NQ = 3, NO = 2;               // Q is held from S^T to dK, dO from dP^T to dV
+  static constexpr int oK = 0, oV = TILE, oQ = 2 * TILE, oO = oQ + NQ * TILE, oStat = oO + NO * TILE;
+  static constexpr int oBar = oStat + 2 * 1024;      // per stage: 128 x -lse log2 e, 128 x D
+  static constexpr int bytes = oBar + 256;           // d = 128: 231,680 of the 232,448 there are
+};
+
+struct DkvBars {
+  uint64_t kv_full, q_full[3], q_empty[3], o_full[2], o_empty[2], st_full[2], st_empty[2], s_full, dp_full, p_full, ds_full,
+      dv_done, dk_done, drain, never;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(DkvBars) <= 256, "barrier block");
+
+// The token tiles of key tile kt: the first token and how many tiles, for L valid tokens.
+struct TokenRange {
+  int i0, n;
+  __host__ __device__ TokenRange(const WinDims& s, int tok, int L, int kt) {
+    const int kb = 128 * kt;
+    const int64_t see = static_cast<int64_t>(kb) + 127 + s.window;      // one past the last position of the band
+    const int end = kb < s.sinks || see > L ? L : static_cast<int>(see);
+    const int first = kb > s.off ? kb - s.off : 0;
+    i0 = first & ~3;                                                    // 16-byte rows of the statistics
+    const int last = kb < L ? end - s.off : 0;                          // a tile past the end has no key
+    n = last > first ? (last - i0 + tok - 1) / tok : 0;
+  }
+};
+
+struct DkvItem {
+  int b, kv, kt, c, chunks;        // chunk c of the key tile's `chunks`
+  int64_t slot;                    // partial sums' slot, -1: the only chunk, written as it is
+  __host__ __device__ DkvItem(const BwdArgs& a, int w) {
+    int bh;
+    if (w < a.n_reg) {
+      c = w / (a.n_kt * a.n_bh);
+      const int x = w % (a.n_kt * a.n_bh);
+      kt = x / a.n_bh;
+      bh = x % a.n_bh;
+    } else {
+      const int x = w - a.n_reg;
+      c = a.nck + x / (a.n_st * a.n_bh);
+      kt = x / a.n_bh % a.n_st;
+      bh = x % a.n_bh;
+    }
+    b = bh / a.s.Hkv;
+    kv = bh % a.s.Hkv;
+    chunks = kt < a.n_st ? a.ncs : a.nck;
+    slot = chunks == 1 ? -1 : slot_of(a, kt, bh, c);
+  }
+  // slots: sink tiles first ([kt][bh][ncs]), then the others ([kt][bh][nck])
+  static __host__ __device__ int64_t slot_of(const BwdArgs& a, int kt, int bh, int c) {
+    if (kt < a.n_st) return (static_cast<int64_t>(kt) * a.n_bh + bh) * a.ncs + c;
+    return static_cast<int64_t>(a.n_st) * a.n_bh * a.ncs + (static_cast<int64_t>(kt - a.n_st) * a.n_bh + bh) * a.nck + c;
+  }
+};
+
+// One CTA per item: a tile of 128 keys of one KV head and a run of the row tiles that see it. TMEM:
+// S^T (keys x rows; P^T in its place) at 0, dP^T (dS^T) at 128, dV at 256, dK at 256 + d. Per row
+// tile n the MMA thread issues dV(n), S^T(n + 1), dK(n), dP^T(n + 1): the exponentials of one tile
+// run under the dK and dP^T products, its dS under the next tile's dV and S^T.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap dkmap, const __grid_constant__ CUtensorMap dvmap) {
+  using M = DkvSmem<D>;
+  extern __shared__ __align__(1024) unsigned char sm[];      // the only shared memory: SW128 tiles first
+  DkvBars& bar = *reinterpret_cast<DkvBars*>(sm + M::oBar);
+  auto &kv_full = bar.kv_full, &s_full = bar.s_full, &dp_full = bar.dp_full, &p_full = bar.p_full, &ds_full = bar.ds_full,
+       &dv_done = bar.dv_done, &dk_done = bar.dk_done, &drain = bar.drain, &never = bar.never;
+  auto &q_full = bar.q_full, &q_empty = bar.q_empty;
+  auto &o_full = bar.o_full, &o_empty = bar.o_empty, &st_full = bar.st_full, &st_empty = bar.st_empty;
+  uint32_t& tmem_base = bar.tmem_base;
+  int& s_abort = bar.abort;
+
+  const WinDims& s = a.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t aK = tc::su32(sm + M::oK), aV = tc::su32(sm + M::oV), aQ = tc::su32(sm + M::oQ), aO = tc::su32(sm + M::oO);
+
+  const DkvItem it(a, blockIdx.x);
+  const int kb = 128 * it.kt, L = win::valid_len(a.len, it.b, s.N);
+  const TokenRange tr(s, a.tok, L, it.kt);
+  // this chunk's row tiles: token tile n / sets, head set n % sets
+  const int tile0 = it.c * a.ct, n = max(0, min(a.ct, tr.n - tile0)) * a.sets;
+  if (n == 0 && it.slot >= 0) return;                        // the reduction knows which chunks are empty
+  auto tile_tok = [&](int k) { return tr.i0 + (tile0 + k / a.sets) * a.tok; };
+  auto tile_end = [&](int k) { return s.off + tile_tok(k) + a.tok; };    // one past its last position
+
+  if (tid == 0) {
+    tc::bar_init(&kv_full, 1);
+    for (int k = 0; k < M::NQ; ++k) {
+      tc::bar_init(&q_full[k], 1);
+      tc::bar_init(&q_empty[k], 1);
+    }
+    for (int k = 0; k < M::NO; ++k) {
+      tc::bar_init(&o_full[k], 1);
+      tc::bar_init(&o_empty[k], 1);
+      tc::bar_init(&st_full[k], 1);
+      tc::bar_init(&st_empty[k], 8);
+    }
+    tc::bar_init(&s_full, 1);
+    tc::bar_init(&dp_full, 1);
+    tc::bar_init(&p_full, 256);
+    tc::bar_init(&ds_full, 256);
+    tc::bar_init(&dv_done, 1);
+    tc::bar_init(&dk_done, 1);
+    tc::bar_init(&drain, 1);
+    tc::bar_init(&never, 1);
+    tc::fence_bar_init();
+    s_abort = 0;
+  }
+  if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
+  tc::before_sync();
+  __syncthreads();
+  tc::after_sync();
+  const uint32_t tm = tmem_base;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
+  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
+
+  if (warp == 9) {
+    // ------------------------------------------------------------------ loader
+    if (lane == 0 && n > 0) {
+      tc::bar_expect_tx(&kv_full, 2 * M::TILE);
+#pragma unroll
+      for (int x = 0; x < M::KB; ++x) {
+        tc::tma_load4(aK + x * (128 * 128), &kmap, x * 64, it.kv, kb, it.b, &kv_full);
+        tc::tma_load4(aV + x * (128 * 128), &vmap, x * 64, it.kv, kb, it.b, &kv_full);
+      }
+      int n_q = 0, n_o = 0, n_st = 0;          // loads issued
+      for (int k = 0; k < n && !aborted(); ++k) {
+        const int i0 = tile_tok(k), set = k % a.sets, h0 = it.kv * s.G + set * a.P;
+        const int sq = k % M::NQ, so = k % M::NO, ss = k & 1;
+        if (!wait(&q_empty[sq], ((k / M::NQ) & 1) ^ 1)) break;
+        ++n_q;
+        tc::bar_expect_tx(&q_full[sq], M::TILE);
+#pragma unroll
+        for (int x = 0; x < M::KB; ++x)
+          tc::tma_load4(aQ + sq * M::TILE + x * (128 * 128), &qmap, x * 64, h0, i0, it.b, &q_full[sq]);
+        if (!wait(&o_empty[so], ((k / M::NO) & 1) ^ 1)) break;
+        ++n_o;
+        tc::bar_expect_tx(&o_full[so], M::TILE);
+#pragma unroll
+        for (int x = 0; x < M::KB; ++x)
+          tc::tma_load4(aO + so * M::TILE + x * (128 * 128), &domap, x * 64, h0, i0, it.b, &o_full[so]);
+        if (!wait(&st_empty[ss], ((k >> 1) & 1) ^ 1)) break;
+        ++n_st;
+        const int64_t at = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + set) * a.Nqp + i0) * a.P;
+        const uint32_t stat = tc::su32(sm + M::oStat) + ss * 1024;
+        tc::bar_expect_tx(&st_full[ss], 1024);
+        win::bulk_load(stat, a.nlse + at, 512, &st_full[ss]);
+        win::bulk_load(stat + 512, a.delta + at, 512, &st_full[ss]);
+      }
+      // whatever is still in flight lands before the CTA leaves
+      tc::bar_wait(&kv_full, 0, kDrainNs);
+      for (int x = max(0, n_q - M::NQ); x < n_q; ++x) tc::bar_wait(&q_full[x % M::NQ], (x / M::NQ) & 1, kDrainNs);
+      for (int x = max(0, n_o - M::NO); x < n_o; ++x) tc::bar_wait(&o_full[x % M::NO], (x / M::NO) & 1, kDrainNs);
+      for (int x = max(0, n_st - 2); x < n_st; ++x) tc::bar_wait(&st_full[x & 1], (x >> 1) & 1, kDrainNs);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idS = tc::idesc_bf16(128, 128);
+      constexpr uint32_t idA = tc::idesc_bf16_major(128, D, false, true);
+      bool ok = wait(&kv_full, 0);
+      if (ok && a.stall) ok = wait(&never, 0);
+      const bool issued = ok;
+      auto issue_s = [&](int k) -> bool {                    // S^T of row tile k
+        const int sq = k % M::NQ;
+        if (!wait(&q_full[sq], (k / M::NQ) & 1)) return false;
+        if (k > 0 && !wait(&dv_done, (k - 1) & 1)) return false;        // P^T has been read
+        tc::after_sync();
+#pragma unroll
+        for (int k2 = 0; k2 < D / 16; ++k2) {
+          const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
+          tc::mma(tm, tc::desc(aK + o), tc::desc(aQ + sq * M::TILE + o), idS, k2 > 0);
+        }
+        tc::commit(&s_full);
+        return true;
+      };
+      auto issue_dp = [&](int k) -> bool {
+        const int so = k % M::NO;
+        if (!wait(&o_full[so], (k / M::NO) & 1)) return false;
+        if (k > 0 && !wait(&dk_done, (k - 1) & 1)) return false;        // dS^T has been read
+        tc::after_sync();
+#pragma unroll
+        for (int k2 = 0; k2 < D / 16; ++k2) {
+          const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
+          tc::mma(tm + 128, tc::desc(aV + o), tc::desc(aO + so * M::TILE + o), idS, k2 > 0);
+        }
+        tc::commit(&dp_full);
+        return true;
+      };
+      ok = ok && issue_s(0) && issue_dp(0);
+      for (int k = 0; ok && k < n && !aborted(); ++k) {
+        const int sq = k % M::NQ, so = k % M::NO;
+        if (!wait(&p_full, k & 1)) { ok = false; break; }
+        tc::after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ts(tm + 256, tm + 64 * (kk >> 2) + 8 * (kk & 3), tc::desc_mn(aO + so * M::TILE + kk * 2048, 128 * 128), idA,
+                     k > 0 || kk > 0);
+        tc::commit(&dv_done);
+        tc::commit(&o_empty[so]);
+        if (k + 1 < n && !issue_s(k + 1)) { ok = false; break; }
+        if (!wait(&ds_full, k & 1)) { ok = false; break; }
+        tc::after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ts(tm + 256 + D, tm + 128 + 64 * (kk >> 2) + 8 * (kk & 3),
+                     tc::desc_mn(aQ + sq * M::TILE + kk * 2048, 128 * 128), idA, k > 0 || kk > 0);
+        tc::commit(&dk_done);
+        tc::commit(&q_empty[sq]);
+        if (k + 1 < n && !issue_dp(k + 1)) { ok = false; break; }
+      }
+      if (issued) {
+        tc::commit(&drain);
+        tc::bar_wait(&drain, 0, kDrainNs);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ softmax: key (lane) r, rows 64 g ..
+    const int g = warp >> 2, r = tid & 127, key = kb + r;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float c1 = s.scale * kLog2e;
+    // positions that see this key: [key, see_end)
+    const int64_t see_end = key >= L ? 0 : key < s.sinks ? L : min(static_cast<int64_t>(L), static_cast<int64_t>(key) + s.window);
+    bool ok = true;
+    for (int k = 0; k < n; ++k) {
+      const int sq = k % M::NQ, ss = k & 1, pt0 = s.off + tile_tok(k);
+      ok = wait(&st_full[ss], (k >> 1) & 1) && wait(&s_full, k & 1);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc::after_sync();
+      float x[64];
+      const uint32_t tS = tm + 64 * g + lane_off;
+      tc::tmem_ld64(tS, x);
+      // column c is a row at position pt0 + c / P: visible iff lo <= c <= hi
+      const int lo = max(-1, min(128, key - pt0)) * a.P - 64 * g;
+      const int hi = static_cast<int>(max(int64_t(0), min(int64_t(128), see_end - pt0))) * a.P - 1 - 64 * g;
+      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 63);
+      if (masked) {
+        see[0] = win::bit_range(lo, hi);
+        see[1] = win::bit_range(lo - 32, hi - 32);
+      }
+      const float4* nl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 256 * g);
+      const float4* dl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 512 + 256 * g);
+      const uint64_t cc = tc::pack2(c1, c1);
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l4 = nl[c / 4];
+        float y0, y1;
+        tc::unpack2(tc::fma2(tc::pack2(x[c], x[c + 1]), cc, tc::pack2(l4.x, l4.y)), y0, y1);
+        x[c] = tc::ex2(y0);
+        x[c + 1] = tc::ex2(y1);
+        tc::unpack2(tc::fma2(tc::pack2(x[c + 2], x[c + 3]), cc, tc::pack2(l4.z, l4.w)), y0, y1);
+        x[c + 2] = tc::ex2(y0);
+        x[c + 3] = tc::ex2(y1);
+      }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t u[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) u[c] = pack_bf16(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
+        tc::tmem_st16(tS + 16 * q, u);
+      }
+      // rows at positions >= len become zero in both tiles once S^T and dP^T have read them: P and dS
+      // are 0 there, and dV and dK must not meet what padding holds
+      if (L < s.N && tile_end(k) > L) {
+        ok = wait(&dp_full, k & 1);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        const int base = g ? M::oO + k % M::NO * M::TILE : M::oQ + sq * M::TILE;
+        if (pt0 + r / a.P >= L)
+          for (int c = 0; c < M::KB * 8; ++c)
+            *reinterpret_cast<uint4*>(sm + base + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+        tc::fence_async_smem();
+      }
+      tc::tmem_wait_st();
+      tc::before_sync();
+      tc::bar_arrive(&p_full);
+      ok = wait(&dp_full, k & 1);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc::after_sync();
+      const uint32_t tD = tm + 128 + 64 * g + lane_off;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float y[32];
+        tc::tmem_ld32(tD + 32 * q, y);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 d4 = dl[8 * q + c / 4];
+          x[32 * q + c] *= y[c] - d4.x;
+          x[32 * q + c + 1] *= y[c + 1] - d4.y;
+          x[32 * q + c + 2] *= y[c + 2] - d4.z;
+          x[32 * q + c + 3] *= y[c + 3] - d4.w;
+        }
+        if (masked) {                                        // what is not visible may be NaN in dP or D
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[32 * q + c] = (see[q] >> c) & 1 ? x[32 * q + c] : 0.f;
+        }
+        uint32_t u[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) u[c] = pack_bf16(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
+        tc::tmem_st16(tD + 16 * q, u);
+      }
+      tc::tmem_wait_st();
+      tc::before_sync();
+      tc::bar_arrive(&ds_full);
+      if (lane == 0) tc::bar_arrive(&st_empty[ss]);
+    }
+    if (ok && n > 0) {
+      ok = wait(&dk_done, (n - 1) & 1) && wait(&dv_done, (n - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::after_sync();
+    }
+    ok = !__any_sync(0xffffffffu, !ok || aborted());
+    // output: warps 0-3 dV, 4-7 dK (scaled), key r
+    const float f = g ? s.scale : 1.f;
+    const uint32_t tA = tm + 256 + D * g + lane_off;
+    const float nan = __int_as_float(0x7fc00000);
+    if (it.slot >= 0) {
+      float4* o = reinterpret_cast<float4*>(a.part + ((it.slot * 2 + g) * 128 + r) * D);
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float x[32];
+        if (ok) tc::tmem_ld32(tA + 32 * q, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          o[8 * q + c] = ok ? make_float4(f * x[4 * c], f * x[4 * c + 1], f * x[4 * c + 2], f * x[4 * c + 3])
+                            : make_float4(nan, nan, nan, nan);
+      }
+    } else if (!ok || n == 0) {
+      const uint32_t v = ok ? 0u : kNaN2;
+      if (key < s.N) {
+        uint4* o = reinterpret_cast<uint4*>((g ? a.dK : a.dV) + ((static_cast<int64_t>(it.b) * s.N + key) * s.Hkv + it.kv) * D);
+        for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(v, v, v, v);
+      }
+    } else {                                                 // through V's and K's shared memory
+      const int base = g ? M::oK : M::oV;
+#pragma unroll 1
+      for (int x2 = 0; x2 < M::KB; ++x2) {
+        float x[64];
+        tc::tmem_ld64(tA + 64 * x2, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) u[k] = pack_bf16(f * x[8 * c + 2 * k], f * x[8 * c + 2 * k + 1]);
+          *reinterpret_cast<uint4*>(sm + base + x2 * (128 * 128) + tc::sw128(r, 8 * c)) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const int k0 = kb + 32 * (warp & 3);
+          if (k0 < s.N)
+            win::tma_store4(g ? &dkmap : &dvmap, 64 * x2, it.kv, k0, it.b,
+                            tc::su32(sm + base) + x2 * (128 * 128) + (warp & 3) * (32 * 128));
+          tc::bulk_commit();
+        }
+      }
+      if (lane == 0) tc::bulk_wait<0>();
+    }
+  }
+  tc::before_sync();
+  __syncthreads();
+  if (tid == 0 && s_abort) atomicOr(a.status, PISA_STATUS_TIMEOUT);
+  if (warp == 0) {
+    tc::after_sync();
+    tc::tmem_free(tm, 512);
+  }
+}
+
+// dK, dV of the key tiles that were cut into chunks: the chunks' partial sums in order.
+// grid: (tiles x b kv, D / 4); a thread sums 4 elements.
+template <int D>
+__global__ void __launch_bounds__(256) window_dkv_sum_kernel(const BwdArgs a, int first_kt) {
+  const WinDims& s = a.s;
+  const int kt = first_kt + blockIdx.x / a.n_bh, bh = blockIdx.x % a.n_bh, b = bh / s.Hkv, kv = bh % s.Hkv;
+  const int L = win::valid_len(a.len, b, s.N);
+  const TokenRange tr(s, a.tok, L, kt);
+  const int chunks = (tr.n + a.ct - 1) / a.ct;
+  const int e = (blockIdx.y * 256 + threadIdx.x) * 4, which = e / (128 * D), r = e / D % 128, col = e % D;
+  const int key = 128 * kt + r;
+  if (key >= s.N) return;
+  const float* p = a.part + (DkvItem::slot_of(a, kt, bh, 0) * 2 * 128) * D + e;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < chunks; ++c) {
+    const float4 x = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(c) * 2 * 128 * D);
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  bf16* o = (which ? a.dK : a.dV) + ((static_cast<int64_t>(b) * s.N + key) * s.Hkv + kv) * D + col;
+  *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// The sizes that follow from a shape. Chunks: a key tile's rows are one item where the key tiles
+// alone fill the GPU six times over; else (few heads, wide windows) and for the rows that only
+// sinks see, runs of `ct` token tiles, whose partial sums a last kernel adds.
+void plan(BwdArgs& a) {
+  const WinDims& s = a.s;
+  a.P = win::packed_heads(s.G);
+  a.tok = 128 / a.P;
+  a.sets = s.G / a.P;
+  a.Nqp = (s.Nq + 3) & ~3;
+  a.n_tiles = (s.Nq + a.tok - 1) / a.tok;
+  a.n_heads = s.B * s.Hkv * a.sets;
+  a.n_items = a.n_tiles * a.n_heads;
+  a.n_kt = (s.N + 127) / 128;
+  a.n_bh = s.B * s.Hkv;
+  a.n_st = std::min(a.n_kt, (s.sinks + 127) / 128);
+  const int64_t all = (s.Nq + 3 + a.tok - 1) / a.tok;                       // token tiles of every row
+  const int64_t band = std::min(all, (int64_t(s.window) + 130 + a.tok - 1) / a.tok);
+  const int64_t total = band * a.sets * a.n_kt * a.n_bh;
+  const int64_t want = std::max<int64_t>(16, total / (152 * 6));            // row tiles of an item
+  a.ct = static_cast<int>(std::min(band, (want + a.sets - 1) / a.sets));
+  a.nck = static_cast<int>((band + a.ct - 1) / a.ct);
+  a.ncs = a.n_st ? static_cast<int>((all + a.ct - 1) / a.ct) : a.nck;
+  a.n_reg = a.n_kt * a.n_bh * a.nck;
+}
+
+int64_t part_slots(const BwdArgs& a) {
+  const int64_t sink = a.ncs > 1 ? static_cast<int64_t>(a.n_st) * a.n_bh * a.ncs : 0;
+  const int64_t rest = a.nck > 1 ? static_cast<int64_t>(a.n_kt - a.n_st) * a.n_bh * a.nck : 0;
+  return sink + rest;
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) window_dkv_kernel(const WinBwdArgs a) {
-  constexpr int E = D / 32;
-  const WinDims& s = a.s;
-  const int64_t kr = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (kr >= static_cast<int64_t>(s.B) * s.N * s.Hkv) return;
-  const int lane = threadIdx.x & 31, kv = static_cast<int>(kr % s.Hkv);
-  const int64_t tok = kr / s.Hkv;
-  const int j = static_cast<int>(tok % s.N), b = static_cast<int>(tok / s.N);
-  const int L = a.len ? max(0, min(a.len[b], s.N)) : s.N;
-  float dk[E] = {}, dv[E] = {};
-  if (j < L) {
-    float k[E], v[E];
-    for (int e = 0; e < E; ++e) {
-      k[e] = __bfloat162float(a.K[tok * s.ks + kv * D + lane * E + e]);
-      v[e] = __bfloat162float(a.V[tok * s.vs + kv * D + lane * E + e]);
-    }
-    const int64_t hi = j < s.sinks ? L : min(static_cast<int64_t>(L), static_cast<int64_t>(j) + s.window);
-    for (int p = max(j, s.off); p < hi; ++p)
-      for (int h = kv * s.G; h < (kv + 1) * s.G; ++h) {
-        const int64_t qt = static_cast<int64_t>(b) * s.Nq + p - s.off, row = qt * s.Hq + h;
-        float q[E], g[E], x = 0.f, y = 0.f;
-        for (int e = 0; e < E; ++e) {
-          q[e] = __bfloat162float(a.Q[qt * s.qs + h * D + lane * E + e]);
-          g[e] = __bfloat162float(a.dO[row * D + lane * E + e]);
-          x += q[e] * k[e];
-          y += g[e] * v[e];
-        }
-        const float w = __expf(s.scale * warp_sum(x) - a.lse[(static_cast<int64_t>(b) * s.Hq + h) * s.Nq + p - s.off]);
-        const float ds = w * (warp_sum(y) - a.delta[row]) * s.scale;
-        for (int e = 0; e < E; ++e) {
-          dk[e] += ds * q[e];
-          dv[e] += w * g[e];
-        }
-      }
+int bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqSmem<D>::bytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvSmem<D>::bytes);
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope ps(st, "window_dq");
+    window_dq_kernel<D><<<std::min(a.n_items, sm_count()), kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[6]);
   }
-  for (int e = 0; e < E; ++e) {
-    a.dK[kr * D + lane * E + e] = __float2bfloat16_rn(dk[e]);
-    a.dV[kr * D + lane * E + e] = __float2bfloat16_rn(dv[e]);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope ps(st, "window_dkv");
+    const int items = a.n_reg + a.n_st * a.n_bh * std::max(0, a.ncs - a.nck);
+    window_dkv_kernel<D><<<items, kThreads, DkvSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[7], m[8]);
   }
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int first = a.ncs > 1 ? 0 : a.n_st, end = a.nck > 1 ? a.n_kt : a.n_st;
+  if (first < end) {
+    ProfScope ps(st, "window_dkv_sum");
+    window_dkv_sum_kernel<D><<<dim3((end - first) * a.n_bh, D / 4), 256, 0, st>>>(a, first);
+    e = cudaGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
 
 WinBwdWs window_bwd_ws(const WinDims& s) {
+  BwdArgs a{};
+  a.s = s;
+  plan(a);
+  const size_t rows = align256(static_cast<size_t>(s.B) * s.Hq * a.Nqp * 4 + 512);   // a tile's read may pass the end
   WinBwdWs w{};
   w.status = 0;
-  w.delta = 256;
-  w.total = w.delta + align256(static_cast<size_t>(s.B) * s.Nq * s.Hq * 4);
+  w.nlse = 256;
+  w.delta = w.nlse + rows;
+  w.part = w.delta + rows;
+  w.total = w.part + static_cast<size_t>(part_slots(a)) * 2 * 128 * s.d * 4;
   return w;
 }
 
 int launch_window_bwd(const WinDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse,
                       const void* dO, const int32_t* len, void* dQ, void* dK, void* dV, char* ws, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const WinBwdWs w = window_bwd_ws(s);
+  BwdArgs a{};
+  a.s = s;
+  plan(a);
+  a.len = len;
+  a.O = static_cast<const bf16*>(O);
+  a.lse = lse;
+  a.nlse = reinterpret_cast<float*>(ws + w.nlse);
+  a.delta = reinterpret_cast<float*>(ws + w.delta);
+  a.dQ = static_cast<bf16*>(dQ);
+  a.dK = static_cast<bf16*>(dK);
+  a.dV = static_cast<bf16*>(dV);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.wait_ns = wait_limit_ns();
+  a.stall = test_stall();
+  const int64_t hd = static_cast<int64_t>(s.Hq) * s.d, kd = static_cast<int64_t>(s.Hkv) * s.d;
+  CUtensorMap m[9];
+  if (int e = win::token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
+  if (int e = win::token_map(&m[1], dO, s.B, s.Nq, s.Hq, s.d, hd, a.P, a.tok)) return e;
+  if (int e = win::token_map(&m[2], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
+  if (int e = win::token_map(&m[3], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 128)) return e;
+  if (int e = win::token_map(&m[4], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
+  if (int e = win::token_map(&m[5], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
+  if (int e = win::token_map(&m[6], dQ, s.B, s.Nq, s.Hq, s.d, hd, a.P, 32 / a.P)) return e;
+  if (int e = win::token_map(&m[7], dK, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
+  if (int e = win::token_map(&m[8], dV, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
   if (e != cudaSuccess) return e;
-  auto c = [](const void* p) { return static_cast<const bf16*>(p); };
-  auto m = [](void* p) { return static_cast<bf16*>(p); };
-  const WinBwdArgs a{s, c(Q), c(K), c(V), c(O), c(dO), lse, len,
-                     reinterpret_cast<float*>(ws + window_bwd_ws(s).delta), m(dQ), m(dK), m(dV)};
-  const int64_t rows = static_cast<int64_t>(s.B) * s.Nq * s.Hq, keys = static_cast<int64_t>(s.B) * s.N * s.Hkv;
-  {
-    ProfScope ps(st, "window_dq");
-    (s.d == 128 ? window_dq_kernel<128> : window_dq_kernel<64>)
-        <<<static_cast<unsigned>((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a);
-  }
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  ProfScope ps(st, "window_dkv");
-  (s.d == 128 ? window_dkv_kernel<128> : window_dkv_kernel<64>)
-      <<<static_cast<unsigned>((keys + kWarps - 1) / kWarps), 32 * kWarps, 0, st>>>(a);
-  return cudaGetLastError();
+  return s.d == 128 ? bwd_launch<128>(a, m, st) : bwd_launch<64>(a, m, st);
 }
 
 }  // namespace pisa

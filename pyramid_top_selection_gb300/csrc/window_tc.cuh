@@ -3,6 +3,7 @@
 #pragma once
 
 #include "tc.cuh"
+#include "tmap.h"
 #include "window.h"
 
 namespace pisa {
@@ -45,6 +46,13 @@ __device__ __forceinline__ void tma_store4(const CUtensorMap* map, int c0, int c
                : "memory");
 }
 
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(tc::su32(bar))
+               : "memory");
+}
+
 // Heads of a group that share a 128-row tile: the largest power of two dividing G, at most 16. A
 // tile's rows are (token, head), heads fastest, so it covers 128 / P tokens and keys are read
 // once for its P heads; fewer tokens a tile also means fewer masked keys at a window's edges.
@@ -52,6 +60,17 @@ inline int packed_heads(int G) {
   int p = 1;
   while (p < 16 && G % (2 * p) == 0) p *= 2;
   return p;
+}
+
+// Tensor map of [B, N, H, d] bf16 with `stride` elements between tokens: boxes of 64 elements x
+// `heads` x `tokens`.
+inline int token_map(CUtensorMap* m, const void* p, int B, int N, int H, int d, int64_t stride, int heads, int tokens) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(H), static_cast<uint64_t>(N),
+                            static_cast<uint64_t>(B)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2,
+                               static_cast<uint64_t>(stride) * 2 * N};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(heads), static_cast<uint32_t>(tokens), 1};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box);
 }
 
 // Bits a .. b (inclusive, any integers) of a 32-bit mask.
