@@ -65,6 +65,9 @@ CASES = {  # B, Nq, N, Hq, Hkv, d, window, sinks, lens, fused
     "projection slices, padded": (2, 333, 333, 4, 4, 64, 100, 7, [12, 333], True),
     "window of one tile": (1, 1025, 1025, 4, 1, 128, 128, 4, None, False),
     "wide window": (1, 1500, 1500, 4, 2, 64, 1024, 4, None, False),
+    "padded, many tiles": (3, 1300, 1300, 4, 2, 64, 900, 4, [1300, 777, 1157], False),
+    "padded, many tiles, wide heads": (2, 1100, 1100, 4, 4, 128, 2000, 0, [1001, 1099], False),
+    "padded chunk with far sinks": (2, 400, 1500, 16, 2, 128, 128, 70, [1500, 1205], False),
     "long chunk": (1, 129, 2000, 8, 2, 128, 700, 16, None, False),
 }
 
