@@ -313,7 +313,8 @@ int pisa_window_workspace_size(const pisa_window_shape_t* shape, int op, size_t*
 
 /* O = softmax over the visible keys of (s q.k) times V, lse = log sum exp(s q.k). len: device
  * [B] int32, may be NULL. A bounded wait that gives up poisons the rows it leaves unfinished
- * (O = NaN, lse = NaN) and sets PISA_STATUS_TIMEOUT. Workspace: PISA_WINDOW_FWD. */
+ * (O = NaN, lse = NaN) and sets PISA_STATUS_TIMEOUT. Workspace: PISA_WINDOW_FWD, the status block
+ * only; NULL (with ws_bytes 0) leaves it out, and the poisoned outputs alone tell. */
 int pisa_window_attn_fwd(const pisa_window_shape_t* shape, const void* Q, const void* K, const void* V,
                          const int32_t* len, void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
 

@@ -340,11 +340,14 @@ def decode_step(shape: DecodeShape, pos, Kcache, Vcache, pyr, q, k_new, v_new, o
 
 def _on(dev, fn, *args) -> None:
     """Call fn(*args, stream) on dev's current stream, with dev the current device."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without its objects
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            rc = fn(*args, stream)
+    if rc != PISA_OK:
+        _check(rc)
 
 
 def _need_shaped(t, dtype, size, dev, name: str) -> None:
@@ -413,7 +416,8 @@ def _need_window(Q, K, V, shape, lens) -> None:
 def window_attn_fwd(Q, K, V, shape: WindowShape, lens=None, ws=None, out=None, lse=None):
     """Causal sliding-window attention with sinks: O [B,Nq,Hq,d] bf16, lse [B,Hq,Nq] fp32.
 
-    lens: valid tokens of each sequence, [B] int32 (None: all); rows past them get O = 0, lse = -inf."""
+    lens: valid tokens of each sequence, [B] int32 (None: all); rows past them get O = 0, lse = -inf.
+    ws: a workspace whose status word the call writes (None: a timeout shows in the outputs only)."""
     _need_window(Q, K, V, shape, lens)
     dev = Q.device
     size = (shape.B, shape.Nq, shape.Hq, shape.d)
@@ -425,10 +429,8 @@ def window_attn_fwd(Q, K, V, shape: WindowShape, lens=None, ws=None, out=None, l
         lse = torch.empty((shape.B, shape.Hq, shape.Nq), dtype=torch.float32, device=dev)
     else:
         _need_shaped(lse, torch.float32, (shape.B, shape.Hq, shape.Nq), dev, "lse")
-    if ws is None:
-        ws = window_workspace(shape, WINDOW_FWD, dev)
     _on(dev, lib().pisa_window_attn_fwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(lens),
-        out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+        out.data_ptr(), lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
 
 

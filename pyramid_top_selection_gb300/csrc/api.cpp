@@ -483,7 +483,7 @@ int pisa_window_attn_fwd(const pisa_window_shape_t* shape, const void* Q, const 
   PISA_CHECK(check_ptr(len, "len", true));
   PISA_CHECK(check_ptr(O, "O"));
   PISA_CHECK(check_ptr(lse, "lse"));
-  PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_FWD), ws, ws_bytes));
+  if (ws || ws_bytes) PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_FWD), ws, ws_bytes));
   return cuda_rc(pisa::launch_window_fwd(d, Q, K, V, len, O, lse, static_cast<char*>(ws), stream),
                  "pisa_window_attn_fwd");
 }

@@ -2,10 +2,43 @@
 // rotation (api.cpp checks the arguments and calls these).
 #pragma once
 
+#include <cuda_runtime.h>
+
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 namespace pisa {
+
+namespace win {
+
+// A kernel's dynamic shared memory, raised once per device (the attribute stays with the device's
+// context, and the call costs as much as a launch); `regs` registers a thread must have been compiled.
+class Ready {
+ public:
+  template <class F>
+  int operator()(F* kernel, int bytes, int regs = 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done_.load(std::memory_order_acquire) & bit) return 0;
+    if (regs > 0) {
+      cudaFuncAttributes f;
+      e = cudaFuncGetAttributes(&f, kernel);
+      if (e != cudaSuccess) return e;
+      if (f.numRegs < regs) return static_cast<int>(cudaErrorInvalidKernelImage);
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<uint64_t> done_{0};
+};
+
+}  // namespace win
 
 // Plain-old-data view of a window shape, passed to kernels by value. Strides in elements
 // between tokens; off = N - Nq is the first query's position.

@@ -10,7 +10,7 @@
 // and the window's edges mask few columns. Items with the most keys come first. Roles:
 //   * loader (warp 9, one thread): Q tiles, then the item's key and value tiles of 128 columns
 //     (KeyList: sinks and window as one list) by TMA into a ring of stages;
-//   * MMA (warp 8, one thread): per key tile and row tile, O += P V (P from tensor memory, V
+//   * MMA (warp 8, one lane issuing): per key tile and row tile, O += P V (P from tensor memory, V
 //     as stored, MN-major), then the next S = Q K^T into the columns P has left. A tile's P V and
 //     the next S alternate between the two row tiles, so one tile's softmax runs under the other's
 //     products;
@@ -169,76 +169,80 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           if (n_q[t]) tc::bar_wait(&q_full[t], (n_q[t] - 1) & 1, kDrainNs);
       }
     } else if (warp == 8) {
-      // ---------------------------------------------------------------- MMA
-      if (lane == 0) {
-        constexpr uint32_t idS = tc::idesc_bf16(128, 128);
-        constexpr uint32_t idO = tc::idesc_bf16_major(128, D, false, true);
-        int n_kv = 0;
-        int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, first P Vs so far
-        bool issued = false, ok = true;
-        for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
-          const FwdItem it(a, w);
-          const int L = win::valid_len(a.len, it.b, s.N);
-          const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
-          const int n = (kl.n_cols + 127) / 128;
-          if (n == 0) continue;
-          if (a.stall && !wait(&never, 0)) { ok = false; break; }
-          bool q_ready[2] = {false, false}, first[2] = {true, true};
-          auto active = [&](int t, int j) { return win::tile_active(s, kl, L, tile_p0(it, t), tile_p1(it, t), 128 * j); };
-          // stage of key tile j of this item: n_kv + 2 j, of its values one more
-          auto issue_s = [&](int t, int j) -> bool {
-            if (!q_ready[t]) {
-              if (!wait(&q_full[t], n_q[t] & 1)) return false;
-              ++n_q[t];
-              q_ready[t] = true;
-            }
-            const int k = n_kv + 2 * j, st = k % M::NST;
-            if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
-            if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
-            tc::after_sync();
-            issued = true;
-#pragma unroll
-            for (int k2 = 0; k2 < D / 16; ++k2) {
-              const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
-              tc::mma(tm + 128 * t, tc::desc(aQ + t * M::TILE + o), tc::desc(aKV + st * M::TILE + o), idS, k2 > 0);
-            }
-            tc::commit(&s_full[t]);
-            if (j == win::last_tile(kl, L, tile_p0(it, t), tile_p1(it, t))) tc::commit(&q_empty[t]);
-            return true;
-          };
-          auto issue_pv = [&](int t, int j) -> bool {
-            const int k = n_kv + 2 * j + 1, st = k % M::NST;
-            if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
-            if (first[t] && !wait(&o_empty[t], (n_o[t] & 1) ^ 1)) return false;
-            if (!wait(&p_full[t], n_p[t] & 1)) return false;
-            tc::after_sync();
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc::mma_ts(tm + 256 + D * t, tm + 128 * t + 8 * kk, tc::desc_mn(aKV + st * M::TILE + kk * 2048, 128 * 128), idO,
-                         !first[t] || kk > 0);
-            tc::commit(&pv_done[t]);
-            if (first[t]) ++n_o[t];
-            first[t] = false;
-            ++n_p[t];
-            return true;
-          };
-          for (int t = 0; ok && t < 2; ++t)
-            if (active(t, 0)) ok = issue_s(t, 0);
-          if (ok) tc::commit(&kv_empty[n_kv % M::NST]);
-          for (int j = 0; ok && j < n && !aborted(); ++j) {
-            for (int t = 0; ok && t < 2; ++t) {
-              if (active(t, j)) ok = issue_pv(t, j);
-              if (ok && t == 1) tc::commit(&kv_empty[(n_kv + 2 * j + 1) % M::NST]);
-              if (ok && j + 1 < n && active(t, j + 1)) ok = issue_s(t, j + 1);
-            }
-            if (ok && j + 1 < n) tc::commit(&kv_empty[(n_kv + 2 * j + 2) % M::NST]);
+      // ---------------------------------------------------------------- MMA (the warp together, one
+      // lane issuing: operands stay in uniform registers)
+      const bool leader = win::elect();
+      int n_kv = 0;
+      int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, first P Vs so far
+      bool issued = false, ok = true;
+      for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
+        const FwdItem it(a, w);
+        const int L = win::valid_len(a.len, it.b, s.N);
+        const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
+        const int n = (kl.n_cols + 127) / 128;
+        if (n == 0) continue;
+        if (a.stall && !wait(&never, 0)) { ok = false; break; }
+        const win::TileRange tr[2] = {{s, kl, L, tile_p0(it, 0), tile_p1(it, 0)}, {s, kl, L, tile_p0(it, 1), tile_p1(it, 1)}};
+        bool first[2] = {true, true}, q_ready[2] = {false, false};
+        // key tile j of this item is load n_kv + 2 j of the ring, its values are the one after
+        auto issue_s = [&](int t, int j) -> bool {
+          const int k = n_kv + 2 * j, st = k % M::NST;
+          if (!q_ready[t]) {
+            if (!wait(&q_full[t], n_q[t] & 1)) return false;
+            ++n_q[t];
+            q_ready[t] = true;
           }
-          n_kv += 2 * n;
+          if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
+          if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
+          tc::after_sync();
+          issued = true;
+          if (leader) {
+            win::product_ss<D>(tm + 128 * t, win::desc_lo(aQ + t * M::TILE), win::desc_lo(aKV + st * M::TILE));
+            tc::commit(&s_full[t]);
+            if (j == tr[t].last) tc::commit(&q_empty[t]);
+          }
+          __syncwarp();
+          return true;
+        };
+        auto issue_pv = [&](int t, int j) -> bool {
+          const int k = n_kv + 2 * j + 1, st = k % M::NST;
+          if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
+          if (first[t] && !wait(&o_empty[t], (n_o[t] & 1) ^ 1)) return false;
+          if (!wait(&p_full[t], n_p[t] & 1)) return false;
+          tc::after_sync();
+          if (leader) {
+            win::product_ts<D>(tm + 256 + D * t, tm + 128 * t, 32, win::desc_mn_lo(aKV + st * M::TILE, 128 * 128), !first[t]);
+            tc::commit(&pv_done[t]);
+          }
+          __syncwarp();
+          if (first[t]) ++n_o[t];
+          first[t] = false;
+          ++n_p[t];
+          return true;
+        };
+        auto release = [&](int k) {
+          if (leader) tc::commit(&kv_empty[k % M::NST]);
+          __syncwarp();
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && tr[t].has(0)) ok = issue_s(t, 0);
+        if (ok) release(n_kv);
+        for (int j = 0; ok && j < n && !aborted(); ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (ok && tr[t].has(j)) ok = issue_pv(t, j);
+            if (ok && t == 1) release(n_kv + 2 * j + 1);
+            if (ok && j + 1 < n && tr[t].has(j + 1)) ok = issue_s(t, j + 1);
+          }
+          if (ok && j + 1 < n) release(n_kv + 2 * j + 2);
         }
-        if (issued) {
-          tc::commit(&drain);
-          tc::bar_wait(&drain, 0, kDrainNs);
-        }
+        n_kv += 2 * n;
+      }
+      if (issued) {
+        if (leader) tc::commit(&drain);
+        __syncwarp();
+        tc::bar_wait(&drain, 0, kDrainNs);
       }
     }
   } else {
@@ -256,6 +260,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
       const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
       n = (kl.n_cols + 127) / 128;
+      const win::TileRange tr(s, kl, L, p0, p1), tr0(s, kl, L, tile_p0(it, 0), tile_p1(it, 0));
       const int p = p0 + r / a.P, h = it.h0 + r % a.P;
       const bool row = p < p1 && p < L;
       float m = neg_inf(), l = 0.f;
@@ -263,7 +268,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       bool ok = true;
       for (int j = 0; j < n; ++j) {
         const int v0 = 128 * j;
-        if (!win::tile_active(s, kl, L, p0, p1, v0)) continue;
+        if (!tr.has(j)) continue;
         ok = wait(&s_full[t], n_s & 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::after_sync();
@@ -342,7 +347,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         // padding's values (only the last tile can reach past the sequence) become zero; of two row
         // tiles that use the tile, the first, whose product the MMA thread issues first, does it
         if (L < s.N && kl.key(v0 + 127) >= L &&
-            (t == 0 || !win::tile_active(s, kl, L, tile_p0(it, 0), tile_p1(it, 0), v0))) {
+            (t == 0 || !tr0.has(j))) {
           const int k = n_kv + 2 * j + 1, st = k % M::NST;
           ok = wait(&kv_full[st], (k / M::NST) & 1);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -420,28 +425,18 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   }
   tc::before_sync();
   __syncthreads();
-  if (tid == 0 && s_abort) atomicOr(a.status, PISA_STATUS_TIMEOUT);
+  if (tid == 0 && s_abort && a.status) atomicOr(a.status, PISA_STATUS_TIMEOUT);
   if (warp == 0) {
     tc::after_sync();
     tc::tmem_free(tm, 512);
   }
 }
 
-// The softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread.
-template <int D>
-bool registers_fit() {
-  static const bool fit = [] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, window_fwd_kernel<D>) == cudaSuccess && f.numRegs >= 168;
-  }();
-  return fit;
-}
-
 template <int D>
 int fwd_launch(const FwdArgs& a, const CUtensorMap* m, int grid, cudaStream_t st) {
-  if (!registers_fit<D>()) return static_cast<int>(cudaErrorInvalidKernelImage);
-  cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FwdSmem<D>::bytes);
-  if (e != cudaSuccess) return e;
+  static win::Ready ready;
+  // the softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread
+  if (int e = ready(window_fwd_kernel<D>, FwdSmem<D>::bytes, 168)) return e;
   ProfScope ps(st, "window_fwd");
   window_fwd_kernel<D><<<grid, kThreads, FwdSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
   return cudaGetLastError();
@@ -473,8 +468,10 @@ int launch_window_fwd(const WinDims& s, const void* Q, const void* K, const void
   if (int e = win::token_map(&m[3], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
   if (int e = win::token_map(&m[4], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
   if (int e = win::token_map(&m[5], O, s.B, s.Nq, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
-  if (e != cudaSuccess) return e;
+  if (ws) {
+    cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+    if (e != cudaSuccess) return e;
+  }
   const int grid = static_cast<int>(std::min<int64_t>(items, sm_count()));
   return s.d == 128 ? fwd_launch<128>(a, m, grid, st) : fwd_launch<64>(a, m, grid, st);
 }

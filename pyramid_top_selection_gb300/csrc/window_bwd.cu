@@ -173,72 +173,68 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       if (n_q) tc::bar_wait(&q_full, (n_q - 1) & 1, kDrainNs);
     }
   } else if (warp == 8) {
-    // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idS = tc::idesc_bf16(128, 128);
-      constexpr uint32_t idQ = tc::idesc_bf16_major(128, D, false, true);
-      int n_q = 0, n_k = 0;
-      bool issued = false, ok = true;
-      for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
-        const DqItem it(a, w);
-        const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
-        const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
-        const int n = (kl.n_cols + 127) / 128;
-        if (n == 0) continue;
-        if (a.stall && !wait(&never, 0)) { ok = false; break; }
-        // g: key tiles so far. The dS that was in S's place has been read: that of two tiles ago, or,
-        // at an item's start, where all earlier products may be done, the last one's
-        auto issue_s = [&](int g, int before) -> bool {
-          const int st = g % M::NK;
-          if (!wait(&k_full[st], (g / M::NK) & 1)) return false;
-          if (before >= 0 && !wait(&dq_done, before & 1)) return false;
-          tc::after_sync();
-          issued = true;
-#pragma unroll
-          for (int k2 = 0; k2 < D / 16; ++k2) {
-            const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
-            tc::mma(tm + 128 * (g & 1), tc::desc(aQ + o), tc::desc(aK + st * M::TILE + o), idS, k2 > 0);
-          }
+    // ------------------------------------------------------------------ MMA (the warp together, one
+    // lane issuing: operands stay in uniform registers)
+    const bool leader = win::elect();
+    int n_q = 0, n_k = 0;
+    bool issued = false, ok = true;
+    for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
+      const DqItem it(a, w);
+      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
+      const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
+      const int n = (kl.n_cols + 127) / 128;
+      if (n == 0) continue;
+      if (a.stall && !wait(&never, 0)) { ok = false; break; }
+      // g: key tiles so far. The dS that was in S's place has been read: that of two tiles ago, or,
+      // at an item's start, where all earlier products may be done, the last one's
+      auto issue_s = [&](int g, int before) -> bool {
+        const int st = g % M::NK;
+        if (!wait(&k_full[st], (g / M::NK) & 1)) return false;
+        if (before >= 0 && !wait(&dq_done, before & 1)) return false;
+        tc::after_sync();
+        issued = true;
+        if (leader) {
+          win::product_ss<D>(tm + 128 * (g & 1), win::desc_lo(aQ), win::desc_lo(aK + st * M::TILE));
           tc::commit(&s_full[g & 1]);
-          return true;
-        };
-        auto issue_dp = [&](int g) -> bool {
-          const int st = g % M::NV;
-          if (!wait(&v_full[st], (g / M::NV) & 1)) return false;
-          tc::after_sync();
-#pragma unroll
-          for (int k2 = 0; k2 < D / 16; ++k2) {
-            const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
-            tc::mma(tm + 256, tc::desc(aO + o), tc::desc(aV + st * M::TILE + o), idS, k2 > 0);
-          }
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_dp = [&](int g) -> bool {
+        const int st = g % M::NV;
+        if (!wait(&v_full[st], (g / M::NV) & 1)) return false;
+        tc::after_sync();
+        if (leader) {
+          win::product_ss<D>(tm + 256, win::desc_lo(aO), win::desc_lo(aV + st * M::TILE));
           tc::commit(&dp_full);
           tc::commit(&v_empty[st]);
-          return true;
-        };
-        ok = wait(&q_full, n_q & 1) && issue_s(n_k, n_k - 1) && issue_dp(n_k);
-        for (int j = 0; ok && j < n && !aborted(); ++j) {
-          const int g = n_k + j;
-          if (j + 1 < n && !issue_s(g + 1, g - 1)) { ok = false; break; }
-          if (!wait(&ds_full, g & 1)) { ok = false; break; }
-          if (j + 1 < n && !issue_dp(g + 1)) { ok = false; break; }
-          if (j == 0 && !wait(&dq_empty, (n_q & 1) ^ 1)) { ok = false; break; }
-          tc::after_sync();
-          const int st = g % M::NK;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_ts(tm + 384, tm + 128 * (g & 1) + 64 * (kk >> 2) + 8 * (kk & 3),
-                       tc::desc_mn(aK + st * M::TILE + kk * 2048, 128 * 128), idQ, j > 0 || kk > 0);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = wait(&q_full, n_q & 1) && issue_s(n_k, n_k - 1) && issue_dp(n_k);
+      for (int j = 0; ok && j < n && !aborted(); ++j) {
+        const int g = n_k + j, st = g % M::NK;
+        if (j + 1 < n && !issue_s(g + 1, g - 1)) { ok = false; break; }
+        if (!wait(&ds_full, g & 1)) { ok = false; break; }
+        if (j + 1 < n && !issue_dp(g + 1)) { ok = false; break; }
+        if (j == 0 && !wait(&dq_empty, (n_q & 1) ^ 1)) { ok = false; break; }
+        tc::after_sync();
+        if (leader) {
+          win::product_ts<D>(tm + 384, tm + 128 * (g & 1), 64, win::desc_mn_lo(aK + st * M::TILE, 128 * 128), j > 0);
           tc::commit(&dq_done);
           tc::commit(&k_empty[st]);
           if (j + 1 == n) tc::commit(&dq_last);   // (dq_done may be two phases behind the softmax warps)
         }
-        ++n_q;
-        n_k += n;
+        __syncwarp();
       }
-      if (issued) {
-        tc::commit(&drain);
-        tc::bar_wait(&drain, 0, kDrainNs);
-      }
+      ++n_q;
+      n_k += n;
+    }
+    if (issued) {
+      if (leader) tc::commit(&drain);
+      __syncwarp();
+      tc::bar_wait(&drain, 0, kDrainNs);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax: row r, columns 64 g ..
@@ -565,63 +561,66 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       for (int x = max(0, n_st - 2); x < n_st; ++x) tc::bar_wait(&st_full[x & 1], (x >> 1) & 1, kDrainNs);
     }
   } else if (warp == 8) {
-    // ------------------------------------------------------------------ MMA
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t idS = tc::idesc_bf16(128, 128);
-      constexpr uint32_t idA = tc::idesc_bf16_major(128, D, false, true);
+    // ------------------------------------------------------------------ MMA (the warp together, one
+    // lane issuing)
+    if (n > 0) {
+      const bool leader = win::elect();
       bool ok = wait(&kv_full, 0);
       if (ok && a.stall) ok = wait(&never, 0);
       const bool issued = ok;
-      auto issue_s = [&](int k) -> bool {                    // S^T of row tile k
-        const int sq = k % M::NQ;
-        if (!wait(&q_full[sq], (k / M::NQ) & 1)) return false;
+      int sq = 0, so = 0, pq = 0, po = 0;                    // stages of row tile k and their parities
+      auto issue_s = [&](int k, int st, int par) -> bool {   // S^T of row tile k
+        if (!wait(&q_full[st], par)) return false;
         if (k > 0 && !wait(&dv_done, (k - 1) & 1)) return false;        // P^T has been read
         tc::after_sync();
-#pragma unroll
-        for (int k2 = 0; k2 < D / 16; ++k2) {
-          const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
-          tc::mma(tm, tc::desc(aK + o), tc::desc(aQ + sq * M::TILE + o), idS, k2 > 0);
+        if (leader) {
+          win::product_ss<D>(tm, win::desc_lo(aK), win::desc_lo(aQ + st * M::TILE));
+          tc::commit(&s_full);
         }
-        tc::commit(&s_full);
+        __syncwarp();
         return true;
       };
-      auto issue_dp = [&](int k) -> bool {
-        const int so = k % M::NO;
-        if (!wait(&o_full[so], (k / M::NO) & 1)) return false;
+      auto issue_dp = [&](int k, int st, int par) -> bool {
+        if (!wait(&o_full[st], par)) return false;
         if (k > 0 && !wait(&dk_done, (k - 1) & 1)) return false;        // dS^T has been read
         tc::after_sync();
-#pragma unroll
-        for (int k2 = 0; k2 < D / 16; ++k2) {
-          const uint32_t o = (k2 >> 2) * (128 * 128) + (k2 & 3) * 32;
-          tc::mma(tm + 128, tc::desc(aV + o), tc::desc(aO + so * M::TILE + o), idS, k2 > 0);
+        if (leader) {
+          win::product_ss<D>(tm + 128, win::desc_lo(aV), win::desc_lo(aO + st * M::TILE));
+          tc::commit(&dp_full);
         }
-        tc::commit(&dp_full);
+        __syncwarp();
         return true;
       };
-      ok = ok && issue_s(0) && issue_dp(0);
+      ok = ok && issue_s(0, 0, 0) && issue_dp(0, 0, 0);
       for (int k = 0; ok && k < n && !aborted(); ++k) {
-        const int sq = k % M::NQ, so = k % M::NO;
+        const int sq1 = sq + 1 == M::NQ ? 0 : sq + 1, pq1 = pq ^ (sq1 == 0);   // row tile k + 1's
+        const int so1 = so + 1 == M::NO ? 0 : so + 1, po1 = po ^ (so1 == 0);
         if (!wait(&p_full, k & 1)) { ok = false; break; }
         tc::after_sync();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ts(tm + 256, tm + 64 * (kk >> 2) + 8 * (kk & 3), tc::desc_mn(aO + so * M::TILE + kk * 2048, 128 * 128), idA,
-                     k > 0 || kk > 0);
-        tc::commit(&dv_done);
-        tc::commit(&o_empty[so]);
-        if (k + 1 < n && !issue_s(k + 1)) { ok = false; break; }
+        if (leader) {
+          win::product_ts<D>(tm + 256, tm, 64, win::desc_mn_lo(aO + so * M::TILE, 128 * 128), k > 0);
+          tc::commit(&dv_done);
+          tc::commit(&o_empty[so]);
+        }
+        __syncwarp();
+        if (k + 1 < n && !issue_s(k + 1, sq1, pq1)) { ok = false; break; }
         if (!wait(&ds_full, k & 1)) { ok = false; break; }
         tc::after_sync();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ts(tm + 256 + D, tm + 128 + 64 * (kk >> 2) + 8 * (kk & 3),
-                     tc::desc_mn(aQ + sq * M::TILE + kk * 2048, 128 * 128), idA, k > 0 || kk > 0);
-        tc::commit(&dk_done);
-        tc::commit(&q_empty[sq]);
-        if (k + 1 < n && !issue_dp(k + 1)) { ok = false; break; }
+        if (leader) {
+          win::product_ts<D>(tm + 256 + D, tm + 128, 64, win::desc_mn_lo(aQ + sq * M::TILE, 128 * 128), k > 0);
+          tc::commit(&dk_done);
+          tc::commit(&q_empty[sq]);
+        }
+        __syncwarp();
+        if (k + 1 < n && !issue_dp(k + 1, so1, po1)) { ok = false; break; }
+        sq = sq1;
+        pq = pq1;
+        so = so1;
+        po = po1;
       }
       if (issued) {
-        tc::commit(&drain);
+        if (leader) tc::commit(&drain);
+        __syncwarp();
         tc::bar_wait(&drain, 0, kDrainNs);
       }
     }
@@ -839,15 +838,14 @@ int64_t part_slots(const BwdArgs& a) {
 
 template <int D>
 int bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DqSmem<D>::bytes);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvSmem<D>::bytes);
-  if (e != cudaSuccess) return e;
+  static win::Ready dq_ready, dkv_ready;
+  if (int e = dq_ready(window_dq_kernel<D>, DqSmem<D>::bytes)) return e;
+  if (int e = dkv_ready(window_dkv_kernel<D>, DkvSmem<D>::bytes)) return e;
   {
     ProfScope ps(st, "window_dq");
     window_dq_kernel<D><<<std::min(a.n_items, sm_count()), kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[6]);
   }
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(st, "window_dkv");

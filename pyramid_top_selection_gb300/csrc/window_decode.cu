@@ -276,13 +276,16 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
 template <int D>
 int decode_launch(const WinDecodeArgs& a, cudaStream_t st) {
   const WinDecodeDims& s = a.s;
-  // CTAs of a cluster: enough to fill the GPU, with at least a chunk of keys for every warp
+  // CTAs of a cluster: as many as run at one time (two an SM, by their shared memory) with at least a
+  // chunk of keys for every warp. At 32 sequences x 8 KV heads and 4100 keys, 1 / 2 / 4 / 8 CTAs a
+  // unit took 84 / 92 / 103 / 125 us: a second wave, and the start and join of each CTA, cost more
+  // than an uneven first wave. A single sequence is latency, and wants all 8.
   const int64_t units = static_cast<int64_t>(s.B) * s.Hkv * a.sets;
   const int64_t keys = std::min<int64_t>(s.Ncap, static_cast<int64_t>(s.window) + s.sinks);
   int splits = 1;
-  while (splits < 8 && units * splits < 152 * 8 && keys > splits * kWarps * kChunk) splits *= 2;
-  cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeSmem<D>::bytes);
-  if (e != cudaSuccess) return e;
+  while (splits < 8 && units * splits * 2 <= 152 * 2 && keys > splits * kWarps * kChunk) splits *= 2;
+  static win::Ready ready;
+  if (int e = ready(window_decode_kernel<D>, DecodeSmem<D>::bytes)) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(s.Hkv * a.sets), static_cast<unsigned>(s.B));
   cfg.blockDim = dim3(32 * kWarps);

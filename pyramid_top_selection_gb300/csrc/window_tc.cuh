@@ -101,18 +101,63 @@ struct KeyList {
   __device__ __forceinline__ int key(int v) const { return v < SP ? v : lo + v - SP; }
 };
 
-// The last 128-column tile with keys that a position in [p0, p1) sees (-1: none).
-__device__ __forceinline__ int last_tile(const KeyList& kl, int L, int p0, int p1) {
-  const int last = min(p1, L) - 1;
-  return last < p0 ? -1 : (kl.SP + last - kl.lo) >> 7;
+// The 128-column tiles j of a key list that hold a key some position in [p0, p1) sees: those of the
+// sinks and of the window.
+struct TileRange {
+  int first, last, sink;
+  __device__ __forceinline__ TileRange(const WinDims& s, const KeyList& kl, int L, int p0, int p1) {
+    const int end = min(p1, L) - 1;
+    last = end < p0 ? -1 : (kl.SP + end - kl.lo) >> 7;
+    first = (kl.SP + max(kl.lo, p0 - s.window + 1) - kl.lo) >> 7;
+    sink = (s.sinks + 127) >> 7;
+  }
+  __device__ __forceinline__ bool has(int j) const { return j <= last && (j >= first || j < sink); }
+};
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
-// Whether the 128 columns at v0 hold a key that some position in [p0, p1) sees.
-__device__ __forceinline__ bool tile_active(const WinDims& s, const KeyList& kl, int L, int p0, int p1, int v0) {
-  const int last = min(p1, L) - 1;
-  if (last < p0) return false;
-  const int vend = kl.SP + last - kl.lo + 1, vbeg = kl.SP + max(kl.lo, p0 - s.window + 1) - kl.lo;
-  return v0 < vend && (v0 + 128 > vbeg || v0 < s.sinks);
+// Shared-memory matrix descriptors by their low word (address, MN stride), the part that changes: an
+// MMA's operands then cost one addition each to form (tc.cuh has the fields).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn_lo(uint32_t saddr, uint32_t mn_stride) { return (saddr >> 4) | ((mn_stride >> 4) << 16); }
+
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh));
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 b;\nsetp.ne.b32 p, %4, 0;\nmov.b64 b, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh));
+}
+
+// D (128 x 128) = A (128 x DIM) B (128 x DIM)^T, both K-major SW128 tiles (blocks of 64 columns).
+template <int DIM>
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo) {
+  constexpr uint32_t id = tc::idesc_bf16(128, 128);
+#pragma unroll
+  for (int k = 0; k < DIM / 16; ++k) {
+    const uint32_t o = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+    mma(d, a_lo + o, b_lo + o, id, k > 0);
+  }
+}
+
+// D (128 x DIM) (+)= A (128 x 128, bf16 in tensor memory, its second 64 columns `split` 32-bit columns
+// after the first) B (128 x DIM), B's rows as stored (MN-major).
+template <int DIM>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, int split, uint32_t b_lo, bool accumulate) {
+  constexpr uint32_t id = tc::idesc_bf16_major(128, DIM, false, true);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mma_ts(d, a_tmem + split * (k >> 2) + 8 * (k & 3), b_lo + k * (2048 >> 4), id, accumulate || k > 0);
 }
 
 }  // namespace win

@@ -82,6 +82,7 @@ def test_window_pointers_and_workspaces_refused():
         assert need >= 256
         _refused(fn, _pisa.PISA_EWORKSPACE, "workspace", ctypes.byref(s), *[A] * n, A, need - 1, None)
         _refused(fn, _pisa.PISA_EWORKSPACE, "NULL", ctypes.byref(s), *[A] * n, None, need, None)
+        _refused(fn, _pisa.PISA_EINVAL, "aligned", ctypes.byref(s), *[A] * n, A + 8, need, None)
         _refused(fn, _pisa.PISA_EINVAL, "shape is NULL", None, *[A] * n, A, need, None)
     _refused(L.pisa_window_workspace_size, _pisa.PISA_EINVAL, "op", ctypes.byref(s), 2, ctypes.byref(ctypes.c_size_t()))
 
