@@ -13,7 +13,8 @@
 //   * MMA (warp 8, one lane issuing): per key tile and row tile, O += P V (P from tensor memory, V
 //     as stored, MN-major), then the next S = Q K^T into the columns P has left. A tile's P V and
 //     the next S alternate between the two row tiles, so one tile's softmax runs under the other's
-//     products;
+//     products. (Two MMA warps, one a row tile, were slower, 1.76 against 1.59 ms at the 64K prefill:
+//     their MMAs interleave one by one, and both products of a pair finish late.);
 //   * softmax (warps 0-3 and 4-7, one row tile each, one row a thread): S row from tensor
 //     memory into registers, masks where the tile touches an edge, maximum, exponentials, sum, P
 //     as bf16 over the first half of S's columns; at the item's end O / l to bf16 through a
@@ -173,7 +174,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       // lane issuing: operands stay in uniform registers)
       const bool leader = win::elect();
       int n_kv = 0;
-      int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, first P Vs so far
+      int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, items of a row tile
       bool issued = false, ok = true;
       for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
         const FwdItem it(a, w);
@@ -183,59 +184,56 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (n == 0) continue;
         if (a.stall && !wait(&never, 0)) { ok = false; break; }
         const win::TileRange tr[2] = {{s, kl, L, tile_p0(it, 0), tile_p1(it, 0)}, {s, kl, L, tile_p0(it, 1), tile_p1(it, 1)}};
-        bool first[2] = {true, true}, q_ready[2] = {false, false};
-        // key tile j of this item is load n_kv + 2 j of the ring, its values are the one after
-        auto issue_s = [&](int t, int j) -> bool {
-          const int k = n_kv + 2 * j, st = k % M::NST;
-          if (!q_ready[t]) {
-            if (!wait(&q_full[t], n_q[t] & 1)) return false;
-            ++n_q[t];
-            q_ready[t] = true;
-          }
-          if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
+        // key tile j is load n_kv + 2 j of the ring, its values are the one after
+        auto landed = [&](int k) { return wait(&kv_full[k % M::NST], (k / M::NST) & 1); };
+        // S of row tile t from the key tile of load k; `last` of the row tile's, `free` the load's last use.
+        // What S needs is waited for while the product before it still runs.
+        auto issue_s = [&](int t, int k, bool last, bool free) -> bool {
           if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
           tc::after_sync();
-          issued = true;
           if (leader) {
-            win::product_ss<D>(tm + 128 * t, win::desc_lo(aQ + t * M::TILE), win::desc_lo(aKV + st * M::TILE));
+            win::product_ss<D>(tm + 128 * t, win::desc_lo(aQ + t * M::TILE), win::desc_lo(aKV + k % M::NST * M::TILE));
             tc::commit(&s_full[t]);
-            if (j == tr[t].last) tc::commit(&q_empty[t]);
+            if (free) tc::commit(&kv_empty[k % M::NST]);
+            if (last) tc::commit(&q_empty[t]);
           }
           __syncwarp();
           return true;
         };
-        auto issue_pv = [&](int t, int j) -> bool {
-          const int k = n_kv + 2 * j + 1, st = k % M::NST;
-          if (!wait(&kv_full[st], (k / M::NST) & 1)) return false;
-          if (first[t] && !wait(&o_empty[t], (n_o[t] & 1) ^ 1)) return false;
+        auto issue_pv = [&](int t, int k, bool accumulate, bool free) -> bool {
+          if (!accumulate && !wait(&o_empty[t], (n_o[t]++ & 1) ^ 1)) return false;   // the last item's O is out
           if (!wait(&p_full[t], n_p[t] & 1)) return false;
           tc::after_sync();
           if (leader) {
-            win::product_ts<D>(tm + 256 + D * t, tm + 128 * t, 32, win::desc_mn_lo(aKV + st * M::TILE, 128 * 128), !first[t]);
+            win::product_ts<D>(tm + 256 + D * t, tm + 128 * t, 32, win::desc_mn_lo(aKV + k % M::NST * M::TILE, 128 * 128),
+                               accumulate);
             tc::commit(&pv_done[t]);
+            if (free) tc::commit(&kv_empty[k % M::NST]);
           }
           __syncwarp();
-          if (first[t]) ++n_o[t];
-          first[t] = false;
           ++n_p[t];
           return true;
         };
-        auto release = [&](int k) {
-          if (leader) tc::commit(&kv_empty[k % M::NST]);
-          __syncwarp();
-        };
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok && tr[t].has(0)) ok = issue_s(t, 0);
-        if (ok) release(n_kv);
-        for (int j = 0; ok && j < n && !aborted(); ++j) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (ok && tr[t].has(j)) ok = issue_pv(t, j);
-            if (ok && t == 1) release(n_kv + 2 * j + 1);
-            if (ok && j + 1 < n && tr[t].has(j + 1)) ok = issue_s(t, j + 1);
-          }
-          if (ok && j + 1 < n) release(n_kv + 2 * j + 2);
+        bool has0 = tr[0].has(0), has1 = tr[1].has(0), acc0 = false, acc1 = false;
+        issued = true;
+        ok = landed(n_kv) && (tr[0].last < 0 || wait(&q_full[0], n_q[0]++ & 1));
+        if (ok && has0) ok = issue_s(0, n_kv, tr[0].last == 0, !has1);
+        ok = ok && (tr[1].last < 0 || wait(&q_full[1], n_q[1]++ & 1));
+        if (ok && has1) ok = issue_s(1, n_kv, tr[1].last == 0, true);
+        ok = ok && landed(n_kv + 1);
+        for (int j = 0; ok && j < n; ++j) {
+          const int k = n_kv + 2 * j + 1;
+          const bool next0 = tr[0].has(j + 1), next1 = tr[1].has(j + 1);
+          if (has0 && !issue_pv(0, k, acc0, !has1)) { ok = false; break; }
+          if (j + 1 < n && !landed(k + 1)) { ok = false; break; }
+          if (next0 && !issue_s(0, k + 1, tr[0].last == j + 1, !next1)) { ok = false; break; }
+          if (has1 && !issue_pv(1, k, acc1, true)) { ok = false; break; }
+          if (j + 1 < n && !landed(k + 2)) { ok = false; break; }
+          if (next1 && !issue_s(1, k + 1, tr[1].last == j + 1, true)) { ok = false; break; }
+          acc0 |= has0;
+          acc1 |= has1;
+          has0 = next0;
+          has1 = next1;
         }
         n_kv += 2 * n;
       }
@@ -260,7 +258,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
       const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
       n = (kl.n_cols + 127) / 128;
-      const win::TileRange tr(s, kl, L, p0, p1), tr0(s, kl, L, tile_p0(it, 0), tile_p1(it, 0));
+      const win::TileRange tr(s, kl, L, p0, p1);
       const int p = p0 + r / a.P, h = it.h0 + r % a.P;
       const bool row = p < p1 && p < L;
       float m = neg_inf(), l = 0.f;
@@ -292,62 +290,77 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
             for (int c = 0; c < 32; ++c) x[32 * q + c] = (see >> c) & 1 ? x[32 * q + c] : neg_inf();
           }
         }
-        float mx[4];
+        // P = 2^(c1 x - mm) over S's first half, its sum, the row's maximum
+        uint64_t sum[2];
+        const uint64_t cc = tc::pack2(c1, c1);
+        auto exps = [&](float mm) {
+          const uint64_t nm = tc::pack2(-mm, -mm);
+          sum[0] = sum[1] = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(x[q], x[4 + q]);
+          for (int q = 0; q < 8; ++q) {
+            uint32_t u[8];
 #pragma unroll
-        for (int c = 8; c < 128; c += 8)
+            for (int c = 0; c < 8; ++c) {
+              float y0, y1;
+              tc::unpack2(tc::fma2(tc::pack2(x[16 * q + 2 * c], x[16 * q + 2 * c + 1]), cc, nm), y0, y1);
+              y0 = tc::ex2(y0);
+              y1 = tc::ex2(y1);
+              sum[c & 1] = tc::add2(sum[c & 1], tc::pack2(y0, y1));
+              u[c] = pack_bf16(y0, y1);
+            }
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tS + 8 * q), "r"(u[0]),
+                         "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                         : "memory");
+          }
+        };
+        auto row_max = [&]() {
+          float mx[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = tc::max3(mx[q], x[c + q], x[c + 4 + q]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
-        const bool grow = top > m + kSlack;                  // also from m = -inf
-        const bool fix = grow && m > neg_inf();              // something has been accumulated
-        float f = 1.f;
-        if (grow) {
-          f = fix ? tc::ex2(m - top) : 1.f;
-          m = top;
-          l *= f;
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(x[q], x[4 + q]);
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx[q] = tc::max3(mx[q], x[c + q], x[c + 4 + q]);
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+        };
+        // After an item's first tile the exponentials do not wait for the tile's maximum: they are taken
+        // against the maximum so far, and once more in the rare tile whose maximum outgrows it.
+        float top;
+        bool grow;
+        if (done) {
+          exps(m > neg_inf() ? m : 0.f);
+          top = row_max();
+          grow = top > m + kSlack;                           // also from m = -inf
+        } else {
+          top = row_max();
+          grow = true;
         }
-        if (__any_sync(0xffffffffu, fix)) {                  // O waits for the product before, then follows
-          ok = wait(&pv_done[t], (n_s - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          tc::after_sync();
+        if (__any_sync(0xffffffffu, grow)) {
+          const bool fix = grow && m > neg_inf();            // something has been accumulated
+          float f = 1.f;
+          if (grow) {
+            f = fix ? tc::ex2(m - top) : 1.f;
+            m = top;
+            l *= f;
+          }
+          if (__any_sync(0xffffffffu, fix)) {                // O waits for the product before, then follows
+            ok = wait(&pv_done[t], (n_s - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc::after_sync();
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            float y[32];
-            tc::tmem_ld32(tO + 32 * q, y);
-            uint32_t u[16];
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t u[16];
+              win::tmem_ld16(tO + 16 * q, u);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(y[16 * hh + c] * f);
-              tc::tmem_st16(tO + 32 * q + 16 * hh, u);
+              for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * f);
+              tc::tmem_st16(tO + 16 * q, u);
             }
           }
+          exps(m > neg_inf() ? m : 0.f);
         }
-        const float mm = m > neg_inf() ? m : 0.f;
-        const uint64_t cc = tc::pack2(c1, c1), nm = tc::pack2(-mm, -mm);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          uint32_t u[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float y0, y1;
-            tc::unpack2(tc::fma2(tc::pack2(x[16 * q + 2 * c], x[16 * q + 2 * c + 1]), cc, nm), y0, y1);
-            y0 = tc::ex2(y0);
-            y1 = tc::ex2(y1);
-            sum[c & 1] = tc::add2(sum[c & 1], tc::pack2(y0, y1));
-            u[c] = pack_bf16(y0, y1);
-          }
-          asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(tS + 8 * q), "r"(u[0]),
-                       "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                       : "memory");
-        }
-        // padding's values (only the last tile can reach past the sequence) become zero; of two row
-        // tiles that use the tile, the first, whose product the MMA thread issues first, does it
-        if (L < s.N && kl.key(v0 + 127) >= L &&
-            (t == 0 || !tr0.has(j))) {
+        // padding's values (only the last tile can reach past the sequence) become zero before this row
+        // tile's product; the other row tile writes the same zeros before its own
+        if (L < s.N && kl.key(v0 + 127) >= L) {
           const int k = n_kv + 2 * j + 1, st = k % M::NST;
           ok = wait(&kv_full[st], (k / M::NST) & 1);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }

@@ -28,7 +28,7 @@ size_t align256(size_t x);
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kThreads = 320;                  // warps 0-7 softmax and output, 8 MMA, 9 loader
+constexpr int kThreads = 352;                  // warps 0-7 softmax and output, 8 and 10 MMA, 9 loader
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
 constexpr uint32_t kNaN2 = 0x7fc07fc0u;        // two bf16 NaNs
@@ -72,9 +72,10 @@ struct DqItem {
   }
 };
 
-// TMEM: S (and dS in its place) of key tile n at 128 (n & 1), dP at 256, dQ at 384. Per key tile the
-// MMA thread issues the next S, then (dS ready) the next dP, then dQ += dS K, so that the tensor
-// cores work on two products while the softmax warps turn S and dP into dS.
+// TMEM: S (and dS in its place) of key tile n at 128 (n & 1), dP at 256, dQ at 384. One MMA warp
+// issues dP(n) and the next tile's S, the other dQ += dS K as soon as dS is there, so that the
+// tensor cores have a product at hand while the softmax warps turn S and dP into dS. (The barriers of
+// dS and of dQ are two each, by the tile's parity: their waiters may be a tile apart.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
@@ -84,7 +85,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   using M = DqSmem<D>;
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
-      s_full[2], dp_full, ds_full, dq_done, dq_last, dq_empty, exch, drain, never;
+      s_full[2], dp_full, ds_full[2], dq_done[2], dq_last, dq_empty, exch, drain[2], never;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   __shared__ float s_dot[2][128];
@@ -107,12 +108,15 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     tc::bar_init(&s_full[0], 1);
     tc::bar_init(&s_full[1], 1);
     tc::bar_init(&dp_full, 1);
-    tc::bar_init(&ds_full, 256);
-    tc::bar_init(&dq_done, 1);
+    tc::bar_init(&ds_full[0], 256);
+    tc::bar_init(&ds_full[1], 256);
+    tc::bar_init(&dq_done[0], 1);
+    tc::bar_init(&dq_done[1], 1);
     tc::bar_init(&dq_last, 1);
     tc::bar_init(&dq_empty, 256);
     tc::bar_init(&exch, 256);
-    tc::bar_init(&drain, 1);
+    tc::bar_init(&drain[0], 1);
+    tc::bar_init(&drain[1], 1);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
     s_abort = 0;
@@ -173,10 +177,10 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       if (n_q) tc::bar_wait(&q_full, (n_q - 1) & 1, kDrainNs);
     }
   } else if (warp == 8) {
-    // ------------------------------------------------------------------ MMA (the warp together, one
-    // lane issuing: operands stay in uniform registers)
+    // ------------------------------------------------------------------ MMA, S and dP (the warp
+    // together, one lane issuing: operands stay in uniform registers)
     const bool leader = win::elect();
-    int n_q = 0, n_k = 0;
+    int n_q = 0, g = 0;                        // items, key tiles so far
     bool issued = false, ok = true;
     for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
       const DqItem it(a, w);
@@ -185,14 +189,14 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       const int n = (kl.n_cols + 127) / 128;
       if (n == 0) continue;
       if (a.stall && !wait(&never, 0)) { ok = false; break; }
-      // g: key tiles so far. The dS that was in S's place has been read: that of two tiles ago, or,
-      // at an item's start, where all earlier products may be done, the last one's
-      auto issue_s = [&](int g, int before) -> bool {
+      ok = wait(&q_full, n_q & 1);
+      ++n_q;
+      issued = true;
+      auto issue_s = [&](int g) -> bool {      // where dS of two tiles ago has been read
         const int st = g % M::NK;
         if (!wait(&k_full[st], (g / M::NK) & 1)) return false;
-        if (before >= 0 && !wait(&dq_done, before & 1)) return false;
+        if (g >= 2 && !wait(&dq_done[g & 1], ((g >> 1) - 1) & 1)) return false;
         tc::after_sync();
-        issued = true;
         if (leader) {
           win::product_ss<D>(tm + 128 * (g & 1), win::desc_lo(aQ), win::desc_lo(aK + st * M::TILE));
           tc::commit(&s_full[g & 1]);
@@ -200,9 +204,11 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         __syncwarp();
         return true;
       };
-      auto issue_dp = [&](int g) -> bool {
+      ok = ok && issue_s(g);
+      for (int j = 0; ok && j < n; ++j, ++g) {
         const int st = g % M::NV;
-        if (!wait(&v_full[st], (g / M::NV) & 1)) return false;
+        ok = wait(&v_full[st], (g / M::NV) & 1) && (g == 0 || wait(&ds_full[(g - 1) & 1], ((g - 1) >> 1) & 1));   // dP has been read
+        if (!ok) break;
         tc::after_sync();
         if (leader) {
           win::product_ss<D>(tm + 256, win::desc_lo(aO), win::desc_lo(aV + st * M::TILE));
@@ -210,31 +216,45 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           tc::commit(&v_empty[st]);
         }
         __syncwarp();
-        return true;
-      };
-      ok = wait(&q_full, n_q & 1) && issue_s(n_k, n_k - 1) && issue_dp(n_k);
-      for (int j = 0; ok && j < n && !aborted(); ++j) {
-        const int g = n_k + j, st = g % M::NK;
-        if (j + 1 < n && !issue_s(g + 1, g - 1)) { ok = false; break; }
-        if (!wait(&ds_full, g & 1)) { ok = false; break; }
-        if (j + 1 < n && !issue_dp(g + 1)) { ok = false; break; }
-        if (j == 0 && !wait(&dq_empty, (n_q & 1) ^ 1)) { ok = false; break; }
+        if (j + 1 < n) ok = issue_s(g + 1);
+      }
+    }
+    if (issued) {
+      if (leader) tc::commit(&drain[0]);
+      __syncwarp();
+      tc::bar_wait(&drain[0], 0, kDrainNs);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ MMA, dQ
+    const bool leader = win::elect();
+    int n_q = 0, g = 0;
+    bool issued = false, ok = true;
+    for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
+      const DqItem it(a, w);
+      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
+      const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
+      const int n = (kl.n_cols + 127) / 128;
+      if (n == 0) continue;
+      for (int j = 0; ok && j < n; ++j, ++g) {
+        const int st = g % M::NK;
+        ok = (j > 0 || wait(&dq_empty, (n_q & 1) ^ 1)) && wait(&ds_full[g & 1], (g >> 1) & 1);
+        if (!ok) break;
         tc::after_sync();
+        issued = true;
         if (leader) {
           win::product_ts<D>(tm + 384, tm + 128 * (g & 1), 64, win::desc_mn_lo(aK + st * M::TILE, 128 * 128), j > 0);
-          tc::commit(&dq_done);
+          tc::commit(&dq_done[g & 1]);
           tc::commit(&k_empty[st]);
-          if (j + 1 == n) tc::commit(&dq_last);   // (dq_done may be two phases behind the softmax warps)
+          if (j + 1 == n) tc::commit(&dq_last);
         }
         __syncwarp();
       }
       ++n_q;
-      n_k += n;
     }
     if (issued) {
-      if (leader) tc::commit(&drain);
+      if (leader) tc::commit(&drain[1]);
       __syncwarp();
-      tc::bar_wait(&drain, 0, kDrainNs);
+      tc::bar_wait(&drain[1], 0, kDrainNs);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax: row r, columns 64 g ..
@@ -343,7 +363,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         }
         tc::tmem_wait_st();
         tc::before_sync();
-        tc::bar_arrive(&ds_full);
+        tc::bar_arrive(&ds_full[n_k & 1]);
       }
       if (!ok) break;
       // dQ of the item, scaled, through Q's shared memory (nothing reads that any more)
@@ -460,7 +480,7 @@ struct DkvItem {
 
 // One CTA per item: a tile of 128 keys of one KV head and a run of the row tiles that see it. TMEM:
 // S^T (keys x rows; P^T in its place) at 0, dP^T (dS^T) at 128, dV at 256, dK at 256 + d. Per row
-// tile n the MMA thread issues dV(n), S^T(n + 1), dK(n), dP^T(n + 1): the exponentials of one tile
+// tile n the MMA warp issues dV(n), S^T(n + 1), dK(n), dP^T(n + 1): the exponentials of one tile
 // run under the dK and dP^T products, its dS under the next tile's dV and S^T.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -471,7 +491,8 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   extern __shared__ __align__(1024) unsigned char sm[];      // the only shared memory: SW128 tiles first
   DkvBars& bar = *reinterpret_cast<DkvBars*>(sm + M::oBar);
   auto &kv_full = bar.kv_full, &s_full = bar.s_full, &dp_full = bar.dp_full, &p_full = bar.p_full, &ds_full = bar.ds_full,
-       &dv_done = bar.dv_done, &dk_done = bar.dk_done, &drain = bar.drain, &never = bar.never;
+       &dv_done = bar.dv_done, &dk_done = bar.dk_done, &drain = bar.drain,
+       &never = bar.never;
   auto &q_full = bar.q_full, &q_empty = bar.q_empty;
   auto &o_full = bar.o_full, &o_empty = bar.o_empty, &st_full = bar.st_full, &st_empty = bar.st_empty;
   uint32_t& tmem_base = bar.tmem_base;
@@ -562,40 +583,40 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA (the warp together, one
-    // lane issuing)
+    // lane issuing). What a product needs is waited for while the one before it still runs.
     if (n > 0) {
       const bool leader = win::elect();
       bool ok = wait(&kv_full, 0);
       if (ok && a.stall) ok = wait(&never, 0);
       const bool issued = ok;
-      int sq = 0, so = 0, pq = 0, po = 0;                    // stages of row tile k and their parities
-      auto issue_s = [&](int k, int st, int par) -> bool {   // S^T of row tile k
-        if (!wait(&q_full[st], par)) return false;
+      int sq = 0, pq = 0;                                    // Q's stage of the next row tile and its parity
+      auto issue_s = [&](int k) -> bool {                    // S^T of row tile k
+        if (!wait(&q_full[sq], pq)) return false;
         if (k > 0 && !wait(&dv_done, (k - 1) & 1)) return false;        // P^T has been read
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm, win::desc_lo(aK), win::desc_lo(aQ + st * M::TILE));
+          win::product_ss<D>(tm, win::desc_lo(aK), win::desc_lo(aQ + sq * M::TILE));
           tc::commit(&s_full);
         }
         __syncwarp();
         return true;
       };
-      auto issue_dp = [&](int k, int st, int par) -> bool {
-        if (!wait(&o_full[st], par)) return false;
+      auto issue_dp = [&](int k) -> bool {
+        const int so = k % M::NO;
+        if (!wait(&o_full[so], (k / M::NO) & 1)) return false;
         if (k > 0 && !wait(&dk_done, (k - 1) & 1)) return false;        // dS^T has been read
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm + 128, win::desc_lo(aV), win::desc_lo(aO + st * M::TILE));
+          win::product_ss<D>(tm + 128, win::desc_lo(aV), win::desc_lo(aO + so * M::TILE));
           tc::commit(&dp_full);
         }
         __syncwarp();
         return true;
       };
-      ok = ok && issue_s(0, 0, 0) && issue_dp(0, 0, 0);
-      for (int k = 0; ok && k < n && !aborted(); ++k) {
-        const int sq1 = sq + 1 == M::NQ ? 0 : sq + 1, pq1 = pq ^ (sq1 == 0);   // row tile k + 1's
-        const int so1 = so + 1 == M::NO ? 0 : so + 1, po1 = po ^ (so1 == 0);
-        if (!wait(&p_full, k & 1)) { ok = false; break; }
+      ok = ok && issue_s(0) && issue_dp(0);
+      for (int k = 0; ok && k < n; ++k) {
+        const int so = k % M::NO, qk = sq;
+        if (!wait(&p_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
           win::product_ts<D>(tm + 256, tm, 64, win::desc_mn_lo(aO + so * M::TILE, 128 * 128), k > 0);
@@ -603,20 +624,20 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           tc::commit(&o_empty[so]);
         }
         __syncwarp();
-        if (k + 1 < n && !issue_s(k + 1, sq1, pq1)) { ok = false; break; }
-        if (!wait(&ds_full, k & 1)) { ok = false; break; }
+        if (++sq == M::NQ) {
+          sq = 0;
+          pq ^= 1;
+        }
+        if (k + 1 < n && !issue_s(k + 1)) break;
+        if (!wait(&ds_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D>(tm + 256 + D, tm + 128, 64, win::desc_mn_lo(aQ + sq * M::TILE, 128 * 128), k > 0);
+          win::product_ts<D>(tm + 256 + D, tm + 128, 64, win::desc_mn_lo(aQ + qk * M::TILE, 128 * 128), k > 0);
           tc::commit(&dk_done);
-          tc::commit(&q_empty[sq]);
+          tc::commit(&q_empty[qk]);
         }
         __syncwarp();
-        if (k + 1 < n && !issue_dp(k + 1, so1, po1)) { ok = false; break; }
-        sq = sq1;
-        pq = pq1;
-        so = so1;
-        po = po1;
+        if (k + 1 < n && !issue_dp(k + 1)) break;
       }
       if (issued) {
         if (leader) tc::commit(&drain);
