@@ -18,6 +18,7 @@
 
 #include "device.cuh"
 #include "profile.h"
+#include "tc.cuh"
 #include "window.h"
 
 namespace pisa {
@@ -25,7 +26,9 @@ namespace pisa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kInFlight = 4;     // rows of a lane group loaded before the first is used
+constexpr int kFwdBlocks = 3, kBwdBlocks = 2;     // blocks an SM holds, by registers
+constexpr int kRound = 4;        // row rounds (512 bytes a warp) of a step
+constexpr int kAhead = 3;        // steps in a warp's ring: two in flight, one in use
 
 struct RopeArgs {
   RopeDims s;
@@ -67,17 +70,10 @@ __device__ __forceinline__ void turn(uint64_t inc, int pos, float m, float& c, f
   s *= m;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t r[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(r[k] << 16);
-    v[2 * k + 1] = __uint_as_float(r[k] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 // Sum over the D / 8 lanes of a row.
@@ -88,207 +84,332 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// This lane's 8 elements of a row, with where they turn: IL (interleaved) pairs lie inside the
-// lane; otherwise the partner elements are those of lane `partner`.
+// A lane's 8 elements of a row: two runs of four, `at` elements [0] and [1] from the row's start, whose
+// k-th elements are a pair (first, second). Half-split: the runs lie rot / 2 apart. Interleaved
+// (IL), and elements that do not turn: eight in a row (interleaved, the pairs are its even and odd ones).
+// The warp forms a token's rot / 2 cosines and sines once, each lane two of them at most, in its
+// table in shared memory.
 template <int D, bool IL>
 struct Lane {
-  int c, partner;
-  bool turns, second;
-  uint64_t inc[IL ? 4 : 8];
+  int at[2], f0, half;
+  bool turns;
+  uint64_t inc[D / 64];
+  float2* tab;
 
-  __device__ __forceinline__ Lane(int lane, int rot, const float* inv_freq) {
-    c = lane % (D / 8);
+  __device__ __forceinline__ Lane(int lane, int rot, const float* inv_freq, float2* table) {
+    const int c = lane % (D / 8);
+    half = rot / 2;
     turns = 8 * c < rot;
-    second = !IL && 16 * c >= rot;
-    partner = IL || !turns ? lane : second ? lane - rot / 16 : lane + rot / 16;
-    const int f0 = IL ? 4 * c : 8 * c - (second ? rot / 2 : 0);
+    at[0] = turns && !IL ? 4 * c : 8 * c;
+    at[1] = turns && !IL ? half + 4 * c : 8 * c + 4;
+    f0 = turns ? 4 * c : 0;
+    tab = table;
 #pragma unroll
-    for (int k = 0; k < (IL ? 4 : 8); ++k) inc[k] = turns ? turns64(inv_freq[f0 + k]) : 0;
+    for (int k = 0; k < D / 64; ++k) inc[k] = lane + 32 * k < half ? turns64(inv_freq[lane + 32 * k]) : 0;
   }
-  // The partner's raw bits (zero where nothing turns, so that an infinity there stays itself).
-  __device__ __forceinline__ uint4 other(const uint4& u) const {
-    if (IL) return u;
-    uint4 p;
-    p.x = __shfl_sync(0xffffffffu, u.x, partner);
-    p.y = __shfl_sync(0xffffffffu, u.y, partner);
-    p.z = __shfl_sync(0xffffffffu, u.z, partner);
-    p.w = __shfl_sync(0xffffffffu, u.w, partner);
-    return turns ? p : make_uint4(0, 0, 0, 0);
-  }
-  // Per element: cos and the partner's factor (+-sin), times rot_scale; 1 and 0 where nothing turns.
-  __device__ __forceinline__ void factors(int pos, float scale, bool back, float (&a)[8], float (&b)[8]) const {
+  // Element k's place in the row (k < 4: first of pair k, else second of pair k - 4).
+  __device__ __forceinline__ int element(int k) const { return IL ? at[0] + 2 * (k & 3) + (k >> 2) : at[k >> 2] + (k & 3); }
+  // The table of one position, times rot_scale.
+  __device__ __forceinline__ void form(int lane, int pos, float scale) const {
+    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < (IL ? 4 : 8); ++k) {
-      float cs, sn;
-      turn(inc[k], pos, scale, cs, sn);
-      if (back) sn = -sn;
-      if (!turns) { cs = 1.f; sn = 0.f; }
-      if (IL) {
-        a[2 * k] = a[2 * k + 1] = cs;
-        b[2 * k] = -sn;
-        b[2 * k + 1] = sn;
-      } else {
-        a[k] = cs;
-        b[k] = second ? sn : -sn;
+    for (int k = 0; k < D / 64; ++k)
+      if (lane + 32 * k < half) {
+        float cs, sn;
+        turn(inc[k], pos, scale, cs, sn);
+        tab[lane + 32 * k] = make_float2(cs, sn);
       }
+    __syncwarp();
+  }
+  // Cosines and sines of the lane's four pairs; 1 and 0 where nothing turns.
+  __device__ __forceinline__ void factors(float (&c)[4], float (&s)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const float4 t = *reinterpret_cast<const float4*>(tab + f0 + k);
+      c[k] = turns ? t.x : 1.f;
+      s[k] = turns ? t.y : 0.f;
+      c[k + 1] = turns ? t.z : 1.f;
+      s[k + 1] = turns ? t.w : 0.f;
     }
+  }
+  // The lane's pairs of a row, and back: v[0], v[1] the firsts (two pairs each), v[2], v[3] the seconds.
+  __device__ __forceinline__ void load(const unsigned char* row, uint64_t (&v)[4]) const {
+    const uint2 a = *reinterpret_cast<const uint2*>(row + 2 * at[0]), b = *reinterpret_cast<const uint2*>(row + 2 * at[1]);
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+    float lo[4], hi[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo[k] = __uint_as_float(w[k] << 16);
+      hi[k] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      v[k] = IL ? tc::pack2(lo[2 * k], lo[2 * k + 1]) : tc::pack2(lo[k], hi[k]);
+      v[2 + k] = IL ? tc::pack2(hi[2 * k], hi[2 * k + 1]) : tc::pack2(lo[2 + k], hi[2 + k]);
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* row, const uint64_t (&v)[4]) const {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tc::unpack2(v[k], x[2 * k], x[2 * k + 1]);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = IL ? pack_bf16(x[k], x[4 + k]) : pack_bf16(x[2 * k], x[2 * k + 1]);
+    *reinterpret_cast<uint2*>(row + at[0]) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + at[1]) = make_uint2(w[2], w[3]);
   }
 };
 
-template <bool IL>
-__device__ __forceinline__ float partner_of(const float (&v)[8], const float (&p)[8], int e) {
-  return IL ? v[e ^ 1] : p[e];
-}
+// A warp's rows in order: its tokens' heads, Q's then K's, as steps of up to ROWS rows (a step does not
+// cross from Q to K). Rows are loaded a step or more before their arithmetic, by cp.async into a ring of
+// the warp's in shared memory.
+struct Cursor {
+  int64_t wk;        // unit of work: token * chunks + chunk of heads
+  int part, h, end;  // Q or K, the step's first head, one past the part's last
+};
 
-// The turned values: v a + partner b. (Interleaved elements that do not turn have b = 0, and their
-// partner is left out so that an infinity there stays itself.)
-template <bool IL>
-__device__ __forceinline__ float turned(const float (&v)[8], const float (&p)[8], const float (&a)[8],
-                                        const float (&b)[8], int e, bool turns) {
-  if (IL) return turns ? v[e] * a[e] + v[e ^ 1] * b[e] : v[e] * a[e];
-  return v[e] * a[e] + p[e] * b[e];
-}
-
-template <int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(32 * kWarps, 2) rope_kernel(const RopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const RopeDims& s = a.s;
-  const int lane = threadIdx.x & 31, g = lane / LPR;
-  const Lane<D, IL> L(lane, s.rot, a.inv_freq);
-  const int H = s.Hq + s.Hkv, hpw = a.heads_per_warp, chunks = (H + hpw - 1) / hpw;
-  const int64_t work = a.tokens * chunks;
-  for (int64_t wk = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); wk < work;
-       wk += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t t = wk / chunks;
-    const int h_beg = static_cast<int>(wk % chunks) * hpw, h_end = min(H, h_beg + hpw);
-    const int pos = a.pos ? a.pos[t] : static_cast<int>(t % s.N);
-    float ca[8], cb[8];
-    L.factors(pos, s.rot_scale, false, ca, cb);
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {                 // Q's heads, then K's
-      const int Hx = part ? s.Hkv : s.Hq, off = part ? s.Hq : 0;
-      const int lo = max(h_beg - off, 0), hi = min(h_end - off, Hx);
-      if (lo >= hi) continue;
-      float wa[8], wb[8];                                  // weight times factor, own and partner's
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wa[e] = NORM && a.w[part] ? a.w[part][8 * L.c + e] : 1.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float wp = IL ? wa[e ^ 1] : __shfl_sync(0xffffffffu, wa[e], L.partner);
-        wb[e] = cb[e] * wp;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wa[e] *= ca[e];
-      const __nv_bfloat16* x = a.x[part] + t * (part ? s.ks : s.qs) + 8 * L.c;
-      __nv_bfloat16* y = a.y[part] + t * Hx * D + 8 * L.c;
-      for (int h0 = lo; h0 < hi; h0 += RPW * kInFlight) {
-        uint4 u[kInFlight];
-#pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-          const int h = h0 + k * RPW + g;
-          u[k] = h < hi ? *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(h) * D) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-          const int h = h0 + k * RPW + g;
-          if (h0 + k * RPW >= hi) break;                   // the same for the whole warp
-          float v[8], p[8], o[8];
-          unpack8(u[k], v);
-          unpack8(L.other(u[k]), p);
-          float r = 1.f;
-          if (NORM) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-            r = rsqrtf(row_sum<D>(ss) * (1.f / D) + s.eps);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float z = turned<IL>(v, p, wa, wb, e, L.turns);
-            o[e] = NORM ? z * r : z;
-          }
-          if (h < hi) *reinterpret_cast<uint4*>(y + static_cast<int64_t>(h) * D) = pack8(o);
-        }
+template <int ROWS>
+struct Walk {
+  const RopeArgs& a;
+  int hpw, chunks;
+  int64_t work, step;
+  __device__ __forceinline__ Walk(const RopeArgs& args)
+      : a(args), hpw(args.heads_per_warp), chunks((args.s.Hq + args.s.Hkv + args.heads_per_warp - 1) / args.heads_per_warp),
+        work(args.tokens * chunks), step(static_cast<int64_t>(gridDim.x) * kWarps) {}
+  __device__ __forceinline__ int64_t token(const Cursor& c) const { return chunks == 1 ? c.wk : c.wk / chunks; }
+  __device__ __forceinline__ int first_head(const Cursor& c) const { return chunks == 1 ? 0 : static_cast<int>(c.wk % chunks) * hpw; }
+  __device__ __forceinline__ void open(Cursor& c) const {          // the first step of unit c.wk
+    const int beg = first_head(c);
+    c.part = beg >= a.s.Hq;
+    c.h = beg - (c.part ? a.s.Hq : 0);
+    c.end = c.part ? min(a.s.Hkv, c.h + hpw) : min(a.s.Hq, beg + hpw);
+  }
+  __device__ __forceinline__ void next(Cursor& c) const {
+    c.h += ROWS;
+    if (c.h < c.end) return;
+    if (c.part == 0) {
+      const int beg = first_head(c);
+      if (beg + hpw > a.s.Hq) {
+        c.part = 1;
+        c.h = 0;
+        c.end = min(a.s.Hkv, beg + hpw - a.s.Hq);
+        return;
       }
     }
+    c.wk += step;
+    open(c);
+  }
+};
+
+// Copies the step's rows (those below c.end) of a tensor into `dst`, D elements each.
+template <int D>
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const __nv_bfloat16* x, const Cursor& c, int lane) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int g = lane / LPR, e = 8 * (lane % LPR);
+#pragma unroll
+  for (int k = 0; k < kRound; ++k) {
+    const int r = k * RPW + g;
+    if (c.h + r < c.end) tc::cp_async16(dst + (r * D + e) * 2, x + static_cast<int64_t>(c.h + r) * D + e, true);
   }
 }
 
 template <int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const RopeArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  __shared__ float red[NORM ? kWarps : 1][2][D];
+__global__ void __launch_bounds__(32 * kWarps, kFwdBlocks) rope_kernel(const RopeArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kRound * 512;
+  extern __shared__ __align__(16) unsigned char ring_all[];
+  __shared__ __align__(16) float2 table[kWarps][D / 2];
   const RopeDims& s = a.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPR;
-  const Lane<D, IL> L(lane, s.rot, a.inv_freq);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-  float dw[2][8];
+  unsigned char* ring = ring_all + warp * kAhead * STEP;
+  const Lane<D, IL> L(lane, s.rot, a.inv_freq, table[warp]);
+  const Walk<RPW * kRound> walk(a);
+  Cursor c{static_cast<int64_t>(blockIdx.x) * kWarps + warp, 0, 0, 0};
+  walk.open(c);
+  Cursor f = c;
+  auto fetch = [&](int slot) {
+    if (f.wk < walk.work) {
+      fetch_rows<D>(tc::su32(ring + slot * STEP), a.x[f.part] + walk.token(f) * (f.part ? s.ks : s.qs), f, lane);
+      walk.next(f);
+    }
+    tc::cp_async_commit();
+  };
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.tokens;
-       t += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int pos = a.pos ? a.pos[t] : static_cast<int>(t % s.N);
-    float ca[8], cb[8];
-    L.factors(pos, s.rot_scale, true, ca, cb);
+  for (int k = 0; k < kAhead - 1; ++k) fetch(k);
+  int64_t now = -1;                                        // the unit and part that the factors are for
+  int now_part = 0;
+  uint64_t aa[2], ab[2], ba[2], bb[2];                     // first = aa first + ab second, second = ba first + bb second
+  for (int slot = 0; c.wk < walk.work; slot = slot + 1 == kAhead ? 0 : slot + 1) {
+    const int64_t t = walk.token(c);
+    if (c.wk != now || c.part != now_part) {
+      if (c.wk != now) L.form(lane, a.pos ? a.pos[t] : static_cast<int>(t % s.N), s.rot_scale);
+      now = c.wk;
+      now_part = c.part;
+      float cs[4], sn[4], w[8];
+      L.factors(cs, sn);
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int Hx = part ? s.Hkv : s.Hq;
-      float w[8];
+      for (int k = 0; k < 8; ++k) w[k] = NORM && a.w[c.part] ? a.w[c.part][L.element(k)] : 1.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = NORM && a.w[part] ? a.w[part][8 * L.c + e] : 1.f;
-      const __nv_bfloat16* x = a.x[part] + t * (part ? s.ks : s.qs) + 8 * L.c;
-      const __nv_bfloat16* dy = a.dy[part] + t * Hx * D + 8 * L.c;
-      __nv_bfloat16* y = a.y[part] + t * Hx * D + 8 * L.c;
-      constexpr int F = kInFlight / 2;                     // two tensors are read
-      for (int h0 = 0; h0 < Hx; h0 += RPW * F) {
-        uint4 u[F], ux[F];
-#pragma unroll
-        for (int k = 0; k < F; ++k) {
-          const int h = h0 + k * RPW + g;
-          const bool ok = h < Hx;
-          u[k] = ok ? *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(h) * D) : make_uint4(0, 0, 0, 0);
-          ux[k] = NORM && ok ? *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(h) * D) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < F; ++k) {
-          const int h = h0 + k * RPW + g;
-          if (h0 + k * RPW >= Hx) break;
-          float v[8], p[8], gr[8], xv[8];
-          unpack8(u[k], v);
-          unpack8(L.other(u[k]), p);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) gr[e] = turned<IL>(v, p, ca, cb, e, L.turns);
-          if (NORM) {
-            unpack8(ux[k], xv);
-            float ss = 0.f, dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              ss += xv[e] * xv[e];
-              dot += gr[e] * w[e] * xv[e];
-            }
-            const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + s.eps);
-            const float m = row_sum<D>(dot) * (1.f / D) * r * r * r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              dw[part][e] += gr[e] * xv[e] * r;
-              gr[e] = r * gr[e] * w[e] - xv[e] * m;
-            }
-          }
-          if (h < Hx) *reinterpret_cast<uint4*>(y + static_cast<int64_t>(h) * D) = pack8(gr);
-        }
+      for (int k = 0; k < 2; ++k) {
+        aa[k] = tc::pack2(w[2 * k] * cs[2 * k], w[2 * k + 1] * cs[2 * k + 1]);
+        ab[k] = tc::pack2(-w[4 + 2 * k] * sn[2 * k], -w[5 + 2 * k] * sn[2 * k + 1]);
+        ba[k] = tc::pack2(w[2 * k] * sn[2 * k], w[2 * k + 1] * sn[2 * k + 1]);
+        bb[k] = tc::pack2(w[4 + 2 * k] * cs[2 * k], w[5 + 2 * k] * cs[2 * k + 1]);
       }
     }
-  }
-  if (NORM && a.partial) {       // the block's sums: lane groups by shuffles, then warps in order
+    tc::cp_async_wait<kAhead - 2>();
+    __syncwarp();                                          // also: every lane has read the slot fetched next
+    fetch(slot == 0 ? kAhead - 1 : slot - 1);
+    const unsigned char* rows = ring + slot * STEP;
+    __nv_bfloat16* y = a.y[c.part] + (t * (c.part ? s.Hkv : s.Hq) + c.h + g) * D;
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
+    for (int k = 0; k < kRound; ++k) {
+      if (c.h + k * RPW >= c.end) break;                   // the same for the whole warp
+      uint64_t v[4], o[4];
+      L.load(rows + (k * RPW + g) * D * 2, v);
+      uint64_t r2 = 0;
+      if (NORM) {
+        const uint64_t q = tc::fma2(v[3], v[3], tc::fma2(v[2], v[2], tc::fma2(v[1], v[1], mul2(v[0], v[0]))));
+        float q0, q1;
+        tc::unpack2(q, q0, q1);
+        const float r = rsqrtf(row_sum<D>(q0 + q1) * (1.f / D) + s.eps);
+        r2 = tc::pack2(r, r);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // what does not turn does not meet its partner, so that an infinity there stays itself
+        o[e] = L.turns ? tc::fma2(v[2 + e], ab[e], mul2(v[e], aa[e])) : mul2(v[e], aa[e]);
+        o[2 + e] = L.turns ? tc::fma2(v[e], ba[e], mul2(v[2 + e], bb[e])) : mul2(v[2 + e], bb[e]);
+      }
+      if (NORM) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = mul2(o[e], r2);
+      }
+      if (c.h + k * RPW + g < c.end) L.store(y + k * RPW * D, o);
+    }
+    walk.next(c);
+  }
+  tc::cp_async_wait<0>();
+}
+
+template <int D, bool IL, bool NORM>
+__global__ void __launch_bounds__(32 * kWarps, kBwdBlocks) rope_bwd_kernel(const RopeArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, STEP = kRound * 512;
+  extern __shared__ __align__(16) unsigned char ring_all[];
+  __shared__ __align__(16) float2 table[kWarps][D / 2];
+  const RopeDims& s = a.s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPR;
+  unsigned char* ring = ring_all + warp * kAhead * (NORM ? 2 : 1) * STEP;      // per slot: dy, then x
+  const Lane<D, IL> L(lane, s.rot, a.inv_freq, table[warp]);
+  const Walk<RPW * kRound> walk(a);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+  Cursor c{static_cast<int64_t>(blockIdx.x) * kWarps + warp, 0, 0, 0};
+  walk.open(c);
+  Cursor f = c;
+  auto fetch = [&](int slot) {
+    if (f.wk < walk.work) {
+      const int64_t t = walk.token(f);
+      const uint32_t dst = tc::su32(ring + slot * (NORM ? 2 : 1) * STEP);
+      fetch_rows<D>(dst, a.dy[f.part] + t * (f.part ? s.Hkv : s.Hq) * D, f, lane);
+      if (NORM) fetch_rows<D>(dst + STEP, a.x[f.part] + t * (f.part ? s.ks : s.qs), f, lane);
+      walk.next(f);
+    }
+    tc::cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) fetch(k);
+  uint64_t dw[2][4];                                       // Q's and K's weight gradients of the lane's elements
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dw[0][e] = dw[1][e] = 0;
+  int64_t now = -1;                                        // the unit and part that the factors are for
+  int now_part = 0;
+  uint64_t cs2[2], sn2[2], w2[4];
+  for (int slot = 0; c.wk < walk.work; slot = slot + 1 == kAhead ? 0 : slot + 1) {
+    const int64_t t = walk.token(c);
+    if (c.wk != now || c.part != now_part) {
+      if (c.wk != now) {
+        L.form(lane, a.pos ? a.pos[t] : static_cast<int>(t % s.N), s.rot_scale);
+        float cs[4], sn[4];
+        L.factors(cs, sn);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          cs2[k] = tc::pack2(cs[2 * k], cs[2 * k + 1]);
+          sn2[k] = tc::pack2(sn[2 * k], sn[2 * k + 1]);
+        }
+      }
+      now = c.wk;
+      now_part = c.part;
+      if (NORM) {
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = a.w[c.part] ? a.w[c.part][L.element(k)] : 1.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w2[k] = tc::pack2(w[2 * k], w[2 * k + 1]);
+      }
+    }
+    tc::cp_async_wait<kAhead - 2>();
+    __syncwarp();                                          // also: every lane has read the slot fetched next
+    fetch(slot == 0 ? kAhead - 1 : slot - 1);
+    const unsigned char* rows = ring + slot * (NORM ? 2 : 1) * STEP;
+    __nv_bfloat16* y = a.y[c.part] + (t * (c.part ? s.Hkv : s.Hq) + c.h + g) * D;
+    uint64_t sum[4] = {0, 0, 0, 0};                        // of the step's g h
+#pragma unroll
+    for (int k = 0; k < kRound; ++k) {
+      if (c.h + k * RPW >= c.end) break;                   // the same for the whole warp
+      const bool row = c.h + k * RPW + g < c.end;
+      uint64_t v[4], gr[4];
+      L.load(rows + (k * RPW + g) * D * 2, v);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {                        // turned back: first = c first + s second, second = c second - s first
+        const uint64_t ms = mul2(sn2[e], tc::pack2(-1.f, -1.f));
+        gr[e] = L.turns ? tc::fma2(v[2 + e], sn2[e], mul2(v[e], cs2[e])) : v[e];
+        gr[2 + e] = L.turns ? tc::fma2(v[e], ms, mul2(v[2 + e], cs2[e])) : v[2 + e];
+      }
+      if (NORM) {
+        uint64_t x[4], gw[4];
+        L.load(rows + STEP + (k * RPW + g) * D * 2, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gw[e] = mul2(gr[e], w2[e]);
+        const uint64_t q = tc::fma2(x[3], x[3], tc::fma2(x[2], x[2], tc::fma2(x[1], x[1], mul2(x[0], x[0]))));
+        const uint64_t d = tc::fma2(x[3], gw[3], tc::fma2(x[2], gw[2], tc::fma2(x[1], gw[1], mul2(x[0], gw[0]))));
+        float q0, q1, d0, d1;
+        tc::unpack2(q, q0, q1);
+        tc::unpack2(d, d0, d1);
+        const float r = rsqrtf(row_sum<D>(q0 + q1) * (1.f / D) + s.eps);
+        const float m = row_sum<D>(d0 + d1) * (-1.f / D) * r * r * r;
+        const uint64_t r2 = tc::pack2(r, r), m2 = tc::pack2(m, m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (row) sum[e] = tc::fma2(mul2(gr[e], x[e]), r2, sum[e]);
+          gr[e] = tc::fma2(x[e], m2, mul2(gw[e], r2));
+        }
+      }
+      if (row) L.store(y + k * RPW * D, gr);
+    }
+    if (NORM) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (c.part) dw[1][e] = tc::add2(dw[1][e], sum[e]);
+        else dw[0][e] = tc::add2(dw[0][e], sum[e]);
+      }
+    }
+    walk.next(c);
+  }
+  tc::cp_async_wait<0>();
+  if (NORM && a.partial) {       // the block's sums: lane groups by shuffles, then warps in order
+    __syncthreads();             // the ring's last reads are done
+    float(*red)[2][D] = reinterpret_cast<float(*)[2][D]>(ring_all);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tc::unpack2(dw[part][e], v[2 * e], v[2 * e + 1]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float v = dw[part][e];
 #pragma unroll
-        for (int o = 16; o >= LPR; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane < LPR) red[warp][part][8 * L.c + e] = v;
+        for (int o = 16; o >= LPR; o >>= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+        if (lane < LPR) red[warp][part][L.element(e)] = v[e];
       }
+    }
     __syncthreads();
     for (int k = threadIdx.x; k < 2 * D; k += 32 * kWarps) {
       float v = 0.f;
@@ -298,27 +419,29 @@ __global__ void __launch_bounds__(32 * kWarps, 2) rope_bwd_kernel(const RopeArgs
   }
 }
 
-// dw[part][e] = sum over the blocks' partials, in a fixed order: 8 interleaved runs, then those.
+// dw[part][e] = sum over the blocks' partials, in a fixed order: 32 interleaved runs, then those.
+// grid: (part, 32 elements).
 template <int D>
-__global__ void __launch_bounds__(8 * D) rope_dw_kernel(const float* partial, int blocks, float* dwq, float* dwk) {
-  __shared__ float red[8][D];
-  const int part = blockIdx.x, e = threadIdx.x % D, run = threadIdx.x / D;
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int blocks, float* dwq, float* dwk) {
+  __shared__ float red[32][33];
+  const int part = blockIdx.x, lane = threadIdx.x & 31, run = threadIdx.x >> 5, e = blockIdx.y * 32 + lane;
   float v = 0.f;
-  for (int k = run; k < blocks; k += 8) v += partial[(static_cast<int64_t>(k) * 2 + part) * D + e];
-  red[run][e] = v;
+#pragma unroll 8
+  for (int k = run; k < blocks; k += 32) v += partial[(static_cast<int64_t>(k) * 2 + part) * D + e];
+  red[run][lane] = v;
   __syncthreads();
   float* out = part ? dwk : dwq;
   if (run == 0 && out) {
-    for (int k = 1; k < 8; ++k) v += red[k][e];
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v += red[k][lane];
     out[e] = v;
   }
 }
 
-constexpr int kBlocksPerSm = 2;
-
 int bwd_blocks(const RopeDims& s) {
   const int64_t need = (static_cast<int64_t>(s.B) * s.N + kWarps - 1) / kWarps;
-  return static_cast<int>(std::min<int64_t>(need, 152 * kBlocksPerSm));
+  return static_cast<int>(std::min<int64_t>(need, 152 * kBwdBlocks));
 }
 
 template <template <int, bool, bool> class Launch, class... A>
@@ -334,8 +457,11 @@ int by_kind(const RopeDims& s, A... args) {
 template <int D, bool IL, bool NORM>
 struct FwdLaunch {
   static int run(const RopeArgs& a, int blocks, cudaStream_t st) {
+    static win::Ready ready;
+    constexpr int smem = kWarps * kAhead * kRound * 512;
+    if (int e = ready(rope_kernel<D, IL, NORM>, smem)) return e;
     ProfScope ps(st, "qk_norm_rope");
-    rope_kernel<D, IL, NORM><<<blocks, 32 * kWarps, 0, st>>>(a);
+    rope_kernel<D, IL, NORM><<<blocks, 32 * kWarps, smem, st>>>(a);
     return cudaGetLastError();
   }
 };
@@ -343,14 +469,17 @@ struct FwdLaunch {
 template <int D, bool IL, bool NORM>
 struct BwdLaunch {
   static int run(const RopeArgs& a, int blocks, float* dwq, float* dwk, cudaStream_t st) {
+    static win::Ready ready;
+    constexpr int smem = kWarps * kAhead * kRound * 512 * (NORM ? 2 : 1);
+    if (int e = ready(rope_bwd_kernel<D, IL, NORM>, smem)) return e;
     {
       ProfScope ps(st, "qk_norm_rope_bwd");
-      rope_bwd_kernel<D, IL, NORM><<<blocks, 32 * kWarps, 0, st>>>(a);
+      rope_bwd_kernel<D, IL, NORM><<<blocks, 32 * kWarps, smem, st>>>(a);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
     ProfScope ps(st, "qk_norm_rope_dw");
-    rope_dw_kernel<D><<<2, 8 * D, 0, st>>>(a.partial, blocks, dwq, dwk);
+    rope_dw_kernel<D><<<dim3(2, D / 32), 1024, 0, st>>>(a.partial, blocks, dwq, dwk);
     return cudaGetLastError();
   }
 };
@@ -359,6 +488,7 @@ RopeArgs make_args(const RopeDims& s, const void* Q, const void* K, const float*
                    const float* wk, const int32_t* pos) {
   RopeArgs a{};
   a.s = s;
+  a.heads_per_warp = s.Hq + s.Hkv;
   a.x[0] = static_cast<const __nv_bfloat16*>(Q);
   a.x[1] = static_cast<const __nv_bfloat16*>(K);
   a.w[0] = wq;
@@ -383,10 +513,10 @@ int launch_rope(const RopeDims& s, const void* Q, const void* K, const float* in
   const int H = s.Hq + s.Hkv, rpw = 256 / s.d;
   // all heads of a token to one warp where the tokens alone fill the GPU's warps; else a warp
   // takes one round of rows
-  const int64_t slots = 152 * kBlocksPerSm * kWarps;
+  const int64_t slots = 152 * kFwdBlocks * kWarps;
   a.heads_per_warp = a.tokens >= slots ? H : rpw;
   const int64_t work = a.tokens * ((H + a.heads_per_warp - 1) / a.heads_per_warp);
-  const int blocks = static_cast<int>(std::min<int64_t>((work + kWarps - 1) / kWarps, 152 * kBlocksPerSm));
+  const int blocks = static_cast<int>(std::min<int64_t>((work + kWarps - 1) / kWarps, 152 * kFwdBlocks));
   return by_kind<FwdLaunch>(s, a, blocks, static_cast<cudaStream_t>(stream));
 }
 
