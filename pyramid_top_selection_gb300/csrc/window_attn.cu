@@ -59,7 +59,7 @@ struct FwdArgs {
   int32_t* status;
   uint64_t wait_ns;
   int stall;
-  int P, tok;              // heads of a tile, tokens of a tile (128 / P)
+  int P, lp, tok;          // heads of a tile (P = 2^lp), tokens of a tile (128 / P)
   int n_tiles, n_heads, n_items;   // token tile pairs, (b, kv, head set) combinations
 };
 
@@ -259,7 +259,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
       n = (kl.n_cols + 127) / 128;
       const win::TileRange tr(s, kl, L, p0, p1);
-      const int p = p0 + r / a.P, h = it.h0 + r % a.P;
+      const int p = p0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
       const bool row = p < p1 && p < L;
       float m = neg_inf(), l = 0.f;
       int done = 0;
@@ -390,7 +390,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + p - s.off] = l == 0.f ? neg_inf() : (m + log2f(l)) * kLn2;
       const float inv = 1.f / l;                             // l = 0: an empty row, whose output is 0
       unsigned char* stg = sm + M::oStage + warp * M::STG;
-      const int tk = it.t0 + t * a.tok + (warp & 3) * 32 / a.P;   // the warp's first token
+      const int tk = it.t0 + t * a.tok + ((warp & 3) * 32 >> a.lp);   // the warp's first token
 #pragma unroll 1
       for (int kb = 0; kb < M::KB; ++kb) {
         uint32_t u[32];
@@ -428,7 +428,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     if (aborted()) {                                         // the rows of the item at hand and of those left
       for (; w < a.n_items; w += gridDim.x) {
         const FwdItem it(a, w);
-        const int i = it.t0 + t * a.tok + r / a.P, h = it.h0 + r % a.P;
+        const int i = it.t0 + t * a.tok + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
         if (i >= s.Nq) continue;
         a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + i] = __int_as_float(0x7fc00000);
         uint4* o = reinterpret_cast<uint4*>(a.O + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
@@ -469,6 +469,7 @@ int launch_window_fwd(const WinDims& s, const void* Q, const void* K, const void
   a.wait_ns = wait_limit_ns();
   a.stall = test_stall();
   a.P = win::packed_heads(s.G);
+  a.lp = win::log2_of(a.P);
   a.tok = 128 / a.P;
   a.n_tiles = (s.Nq + 2 * a.tok - 1) / (2 * a.tok);
   a.n_heads = s.B * s.Hkv * (s.G / a.P);

@@ -28,7 +28,7 @@ size_t align256(size_t x);
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kThreads = 352;                  // warps 0-7 softmax and output, 8 and 10 MMA, 9 loader
+constexpr int kThreads = 384;                  // warps 0-7 softmax and output, 8 (and 10) MMA, 9 loader, 11 row statistics
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
 constexpr uint32_t kNaN2 = 0x7fc07fc0u;        // two bf16 NaNs
@@ -36,7 +36,7 @@ constexpr uint32_t kNaN2 = 0x7fc07fc0u;        // two bf16 NaNs
 struct BwdArgs {
   WinDims s;
   const int32_t* len;
-  const bf16* O;
+  const bf16 *O, *dO;
   const float* lse;
   float *nlse, *delta;     // [B][Hkv][sets][Nqp][P]: -lse log2 e and D
   bf16 *dQ, *dK, *dV;
@@ -44,7 +44,7 @@ struct BwdArgs {
   int32_t* status;
   uint64_t wait_ns;
   int stall;
-  int P, tok, sets, Nqp;   // heads and tokens of a row tile, head sets of a group, padded Nq
+  int P, lp, tok, sets, Nqp;   // heads (2^lp) and tokens of a row tile, head sets of a group, padded Nq
   int n_tiles, n_heads, n_items;           // dQ: token tiles, (b, kv, set), items
   // dK, dV: key tiles, (b, kv), key tiles with sinks, token tiles of a chunk, chunks of a band and
   // of a sink tile, items of the bands
@@ -80,15 +80,14 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                 const __grid_constant__ CUtensorMap kmap32, const __grid_constant__ CUtensorMap vmap32,
-                 const __grid_constant__ CUtensorMap dqmap) {
+                 const __grid_constant__ CUtensorMap kmap32, const __grid_constant__ CUtensorMap vmap32) {
   using M = DqSmem<D>;
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
-      s_full[2], dp_full, ds_full[2], dq_done[2], dq_last, dq_empty, exch, drain[2], never;
+      s_full[2], dp_full, ds_full[2], dq_done[2], dq_last, dq_empty, st_full[2], st_empty[2], drain[2], never;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  __shared__ float s_dot[2][128];
+  __shared__ float s_stat[2][2][128];        // per item (two at a time): -lse log2 e, D
 
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -96,7 +95,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
 
   if (tid == 0) {
     tc::bar_init(&q_full, 1);
-    tc::bar_init(&q_empty, 8);
+    tc::bar_init(&q_empty, 1);
     for (int k = 0; k < M::NK; ++k) {
       tc::bar_init(&k_full[k], 1);
       tc::bar_init(&k_empty[k], 1);
@@ -114,7 +113,10 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     tc::bar_init(&dq_done[1], 1);
     tc::bar_init(&dq_last, 1);
     tc::bar_init(&dq_empty, 256);
-    tc::bar_init(&exch, 256);
+    for (int k = 0; k < 2; ++k) {
+      tc::bar_init(&st_full[k], 1);
+      tc::bar_init(&st_empty[k], 8);
+    }
     tc::bar_init(&drain[0], 1);
     tc::bar_init(&drain[1], 1);
     tc::bar_init(&never, 1);
@@ -214,6 +216,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           win::product_ss<D>(tm + 256, win::desc_lo(aO), win::desc_lo(aV + st * M::TILE));
           tc::commit(&dp_full);
           tc::commit(&v_empty[st]);
+          if (j + 1 == n) tc::commit(&q_empty);
         }
         __syncwarp();
         if (j + 1 < n) ok = issue_s(g + 1);
@@ -256,6 +259,68 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       __syncwarp();
       tc::bar_wait(&drain[1], 0, kDrainNs);
     }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------------ D = dO . O and -lse log2 e of
+    // the rows, an item ahead: D / 8 lanes a row, several rounds of rows in flight. One warp's loads do not
+    // cover the latency of memory, so the rows of the item after are asked into L2 meanwhile.
+    constexpr int LPR = D / 8, RPW = 32 / LPR, R = 6;
+    int n_q = 0;
+    for (int w = blockIdx.x; w < a.n_items && !aborted(); w += gridDim.x) {
+      const DqItem it(a, w);
+      if (w + static_cast<int>(gridDim.x) < a.n_items) {
+        const DqItem nx(a, w + gridDim.x);
+        const int64_t f = (static_cast<int64_t>(nx.b) * s.Nq + nx.t0) * s.Hq + nx.kv * s.G + nx.set * a.P;
+        for (int r = lane; r < min(128, (s.Nq - nx.t0) * a.P); r += 32)
+#pragma unroll
+          for (int c = 0; c < D; c += 64) {
+            const int64_t at = (f + static_cast<int64_t>((r >> a.lp)) * s.Hq + (r & (a.P - 1))) * D + c;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.O + at));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dO + at));
+          }
+      }
+      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
+      if (win::KeyList(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok)).n_cols == 0) continue;
+      const int sl = n_q & 1, rows = min(128, (min(s.Nq, L - s.off) - it.t0) * a.P), h0 = it.kv * s.G + it.set * a.P;
+      if (!__all_sync(0xffffffffu, wait(&st_empty[sl], ((n_q >> 1) & 1) ^ 1))) break;
+      const int64_t first = (static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + h0;    // row r: + r / P * Hq + r % P
+      for (int r0 = 0; r0 < rows; r0 += RPW * R) {
+        uint4 o[R], g[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const int r = r0 + k * RPW + lane / LPR;
+          const int64_t at = (first + static_cast<int64_t>((r >> a.lp)) * s.Hq + (r & (a.P - 1))) * D + 8 * (lane % LPR);
+          o[k] = r < rows ? ldg_u4(a.O + at) : make_uint4(0, 0, 0, 0);
+          g[k] = r < rows ? ldg_u4(a.dO + at) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const uint32_t u[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, v[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+          float d = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            d = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), d);
+            d = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), d);
+          }
+#pragma unroll
+          for (int x = LPR / 2; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+          if (lane % LPR == 0 && r0 + k * RPW + lane / LPR < 128) s_stat[sl][1][r0 + k * RPW + lane / LPR] = d;
+        }
+      }
+      __syncwarp();
+      const int64_t at0 = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + it.set) * a.Nqp + it.t0) * a.P;
+#pragma unroll
+      for (int r = lane; r < 128; r += 32) {
+        const float nl = r < rows ? -a.lse[(static_cast<int64_t>(it.b) * s.Hq + h0 + (r & (a.P - 1))) * s.Nq + it.t0 + (r >> a.lp)] * kLog2e : 0.f;
+        s_stat[sl][0][r] = nl;
+        if (r < rows) {
+          a.nlse[at0 + r] = nl;
+          a.delta[at0 + r] = s_stat[sl][1][r];
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&st_full[sl]);
+      ++n_q;
+    }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax: row r, columns 64 g ..
     const int g = warp >> 2, r = tid & 127;
@@ -267,7 +332,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0, p1 = s.off + min(s.Nq, it.t0 + a.tok);
       const win::KeyList kl(s, L, p0, p1);
       const int n = (kl.n_cols + 127) / 128;
-      const int hp = r % a.P, i = it.t0 + r / a.P, p = s.off + i, h = it.kv * s.G + it.set * a.P + hp;
+      const int hp = (r & (a.P - 1)), i = it.t0 + (r >> a.lp), p = s.off + i, h = it.kv * s.G + it.set * a.P + hp;
       const bool row = p < p1 && p < L;
       if (n == 0) {                                          // no row sees anything: dQ = 0
         if (g == 0 && i < s.Nq) {
@@ -276,35 +341,11 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         }
         continue;
       }
-      // D = dO . O, half a row each; the halves meet in shared memory
-      bool ok = wait(&q_full, n_q & 1);
-      float nl = 0.f, dl = 0.f;
-      if (row) {
-        const bf16* o = a.O + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D + g * (D / 2);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 u = ldg_u4(o + 8 * c);
-          const int col = g * (D / 2) + 8 * c;
-          const uint4 v = *reinterpret_cast<const uint4*>(sm + M::oO + (col >> 6) * (128 * 128) + tc::sw128(r, col & 63));
-          const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            dl = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(vv[k] << 16), dl);
-            dl = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(vv[k] & 0xffff0000u), dl);
-          }
-        }
-        nl = -a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + i] * kLog2e;
-      }
-      s_dot[g][r] = dl;
-      tc::bar_arrive(&exch);
-      ok = ok && wait(&exch, n_q & 1);
+      bool ok = wait(&st_full[n_q & 1], (n_q >> 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
-      dl = s_dot[0][r] + s_dot[1][r];
-      if (g == 0 && i < s.Nq) {
-        const int64_t at = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + it.set) * a.Nqp + i) * a.P + hp;
-        a.nlse[at] = nl;
-        a.delta[at] = dl;
-      }
+      const float nl = s_stat[n_q & 1][0][r], dl = s_stat[n_q & 1][1][r];
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&st_empty[n_q & 1]);
       for (int j = 0; j < n; ++j, ++n_k) {
         const int v0 = 128 * j + 64 * g;
         ok = wait(&s_full[n_k & 1], (n_k >> 1) & 1);
@@ -335,12 +376,8 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         tc::after_sync();
         tc::tmem_ld64(tm + 256 + 64 * g + lane_off, y);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float e0, e1;
-          tc::unpack2(tc::add2(tc::pack2(y[c], y[c + 1]), dd), e0, e1);
-          x[c] *= e0;
-          x[c + 1] *= e1;
-        }
+        for (int c = 0; c < 64; c += 2)
+          tc::unpack2(win::mul2(tc::pack2(x[c], x[c + 1]), tc::add2(tc::pack2(y[c], y[c + 1]), dd)), x[c], x[c + 1]);
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
@@ -366,42 +403,34 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         tc::bar_arrive(&ds_full[n_k & 1]);
       }
       if (!ok) break;
-      // dQ of the item, scaled, through Q's shared memory (nothing reads that any more)
+      // dQ of the item, scaled: row r's columns 64 g .. (shared memory is full, and Q's and dO's tiles
+      // already take the next item's, so the rows go out from registers)
       ok = wait(&dq_last, n_q & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::after_sync();
       ++n_q;
+      uint4* out = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D + 64 * g);
       if (g < M::KB) {
-        float x[64];
-        tc::tmem_ld64(tm + 384 + 64 * g + lane_off, x);
-        unsigned char* stg = sm + M::oQ + g * (128 * 128);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t u[4];
+        for (int q = 0; q < 2; ++q) {
+          float y[32];
+          tc::tmem_ld32(tm + 384 + 64 * g + 32 * q + lane_off, y);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) u[k] = pack_bf16(s.scale * x[8 * c + 2 * k], s.scale * x[8 * c + 2 * k + 1]);
-          *reinterpret_cast<uint4*>(stg + tc::sw128(r, 8 * c)) = make_uint4(u[0], u[1], u[2], u[3]);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = pack_bf16(s.scale * y[8 * c + 2 * k], s.scale * y[8 * c + 2 * k + 1]);
+            if (i < s.Nq) out[4 * q + c] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
         }
-        tc::fence_async_smem();
-        __syncwarp();
-        const int tk = it.t0 + (warp & 3) * 32 / a.P;
-        if (lane == 0) {
-          if (tk < s.Nq)
-            win::tma_store4(&dqmap, 64 * g, it.kv * s.G + it.set * a.P, tk, it.b, aQ + g * (128 * 128) + (warp & 3) * (32 * 128));
-          tc::bulk_commit();
-          tc::bulk_wait_read<0>();
-        }
-        __syncwarp();
       }
       tc::before_sync();
       tc::bar_arrive(&dq_empty);
-      if (lane == 0) tc::bar_arrive(&q_empty);
     }
-    if (lane == 0) tc::bulk_wait<0>();
     if (aborted() && g == 0) {                               // the rows of the item at hand and of those left
       for (; w < a.n_items; w += gridDim.x) {
         const DqItem it(a, w);
-        const int i = it.t0 + r / a.P, h = it.kv * s.G + it.set * a.P + r % a.P;
+        const int i = it.t0 + (r >> a.lp), h = it.kv * s.G + it.set * a.P + (r & (a.P - 1));
         if (i >= s.Nq) continue;
         uint4* o = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
         for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(kNaN2, kNaN2, kNaN2, kNaN2);
@@ -701,7 +730,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         ok = wait(&dp_full, k & 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         const int base = g ? M::oO + k % M::NO * M::TILE : M::oQ + sq * M::TILE;
-        if (pt0 + r / a.P >= L)
+        if (pt0 + (r >> a.lp) >= L)
           for (int c = 0; c < M::KB * 8; ++c)
             *reinterpret_cast<uint4*>(sm + base + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
         tc::fence_async_smem();
@@ -720,10 +749,9 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           const float4 d4 = dl[8 * q + c / 4];
-          x[32 * q + c] *= y[c] - d4.x;
-          x[32 * q + c + 1] *= y[c + 1] - d4.y;
-          x[32 * q + c + 2] *= y[c + 2] - d4.z;
-          x[32 * q + c + 3] *= y[c + 3] - d4.w;
+          float* p = x + 32 * q + c;
+          tc::unpack2(win::mul2(tc::pack2(p[0], p[1]), win::sub2(tc::pack2(y[c], y[c + 1]), tc::pack2(d4.x, d4.y))), p[0], p[1]);
+          tc::unpack2(win::mul2(tc::pack2(p[2], p[3]), win::sub2(tc::pack2(y[c + 2], y[c + 3]), tc::pack2(d4.z, d4.w))), p[2], p[3]);
         }
         if (masked) {                                        // what is not visible may be NaN in dP or D
 #pragma unroll
@@ -832,6 +860,7 @@ __global__ void __launch_bounds__(256) window_dkv_sum_kernel(const BwdArgs a, in
 void plan(BwdArgs& a) {
   const WinDims& s = a.s;
   a.P = win::packed_heads(s.G);
+  a.lp = win::log2_of(a.P);
   a.tok = 128 / a.P;
   a.sets = s.G / a.P;
   a.Nqp = (s.Nq + 3) & ~3;
@@ -864,14 +893,14 @@ int bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   if (int e = dkv_ready(window_dkv_kernel<D>, DkvSmem<D>::bytes)) return e;
   {
     ProfScope ps(st, "window_dq");
-    window_dq_kernel<D><<<std::min(a.n_items, sm_count()), kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[6]);
+    window_dq_kernel<D><<<std::min(a.n_items, sm_count()), kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(st, "window_dkv");
     const int items = a.n_reg + a.n_st * a.n_bh * std::max(0, a.ncs - a.nck);
-    window_dkv_kernel<D><<<items, kThreads, DkvSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[7], m[8]);
+    window_dkv_kernel<D><<<items, kThreads, DkvSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[6], m[7]);
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -909,6 +938,7 @@ int launch_window_bwd(const WinDims& s, const void* Q, const void* K, const void
   plan(a);
   a.len = len;
   a.O = static_cast<const bf16*>(O);
+  a.dO = static_cast<const bf16*>(dO);
   a.lse = lse;
   a.nlse = reinterpret_cast<float*>(ws + w.nlse);
   a.delta = reinterpret_cast<float*>(ws + w.delta);
@@ -920,16 +950,15 @@ int launch_window_bwd(const WinDims& s, const void* Q, const void* K, const void
   a.wait_ns = wait_limit_ns();
   a.stall = test_stall();
   const int64_t hd = static_cast<int64_t>(s.Hq) * s.d, kd = static_cast<int64_t>(s.Hkv) * s.d;
-  CUtensorMap m[9];
+  CUtensorMap m[8];
   if (int e = win::token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
   if (int e = win::token_map(&m[1], dO, s.B, s.Nq, s.Hq, s.d, hd, a.P, a.tok)) return e;
   if (int e = win::token_map(&m[2], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
   if (int e = win::token_map(&m[3], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 128)) return e;
   if (int e = win::token_map(&m[4], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
   if (int e = win::token_map(&m[5], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
-  if (int e = win::token_map(&m[6], dQ, s.B, s.Nq, s.Hq, s.d, hd, a.P, 32 / a.P)) return e;
-  if (int e = win::token_map(&m[7], dK, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
-  if (int e = win::token_map(&m[8], dV, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
+  if (int e = win::token_map(&m[6], dK, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
+  if (int e = win::token_map(&m[7], dV, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
   if (e != cudaSuccess) return e;
   return s.d == 128 ? bwd_launch<128>(a, m, st) : bwd_launch<64>(a, m, st);

@@ -33,6 +33,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort_
   return false;
 }
 
+// Packed pairs of fp32 (tc.cuh).
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  return tc::fma2(b, tc::pack2(-1.f, -1.f), a);
+}
+
 template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -71,6 +81,12 @@ inline int packed_heads(int G) {
   int p = 1;
   while (p < 16 && G % (2 * p) == 0) p *= 2;
   return p;
+}
+
+inline int log2_of(int p) {
+  int l = 0;
+  while (1 << l < p) ++l;
+  return l;
 }
 
 // Tensor map of [B, N, H, d] bf16 with `stride` elements between tokens: boxes of 64 elements x
