@@ -8,7 +8,8 @@
 // Persistent, one CTA per SM; a work item is 256 rows of one KV head: two 128-row tiles of (token,
 // head) rows, P heads of the group together (window_tc.cuh), so the keys are read once for two tiles
 // and the window's edges mask few columns. Items with the most keys come first. Roles:
-//   * loader (warp 9, one thread): Q tiles, then the item's key and value tiles of 128 columns
+//   * items (warp 10, one thread): decodes the CTA's items a few ahead, for all other roles;
+//   * loader (warp 9, one lane issuing): Q tiles, then the item's key and value tiles of 128 columns
 //     (KeyList: sinks and window as one list) by TMA into a ring of stages;
 //   * MMA (warp 8, one lane issuing): per key tile and row tile, O += P V (P from tensor memory, V
 //     as stored, MN-major), then the next S = Q K^T into the columns P has left. A tile's P V and
@@ -40,6 +41,7 @@ constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;                  // log2 growth of the maximum that O is rescaled for
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
+constexpr uint64_t kPatient = 1ull << 40;      // the item warp outwaits the others, whose giving up it sees
 
 template <int D>
 struct FwdSmem {
@@ -63,16 +65,28 @@ struct FwdArgs {
   int n_tiles, n_heads, n_items;   // token tile pairs, (b, kv, head set) combinations
 };
 
-struct FwdItem {
-  int b, kv, h0, t0;       // batch, KV head, first query head, first token
-  __device__ __forceinline__ FwdItem(const FwdArgs& a, int w) {
-    const int tile = a.n_tiles - 1 - w / a.n_heads, hh = w % a.n_heads, sets = a.s.G / a.P;
-    b = hh / (a.s.Hkv * sets);
-    kv = hh / sets % a.s.Hkv;
-    h0 = kv * a.s.G + hh % sets * a.P;
-    t0 = tile * 2 * a.tok;
-  }
-};
+// Work item w: 2 x tok tokens of P heads.
+__device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
+  const WinDims& s = a.s;
+  const int tile = a.n_tiles - 1 - w / a.n_heads, hh = w % a.n_heads, sets = s.G / a.P;
+  win::Item it;
+  it.b = hh / (s.Hkv * sets);
+  it.kv = hh / sets % s.Hkv;
+  it.h0 = it.kv * s.G + hh % sets * a.P;
+  it.t0 = tile * 2 * a.tok;
+  it.L = win::valid_len(a.len, it.b, s.N);
+  const int p0 = s.off + it.t0, p1 = s.off + min(s.Nq, it.t0 + a.tok), p2 = s.off + min(s.Nq, it.t0 + 2 * a.tok);
+  const win::KeyList kl(s, it.L, p0, p2);
+  it.lo = kl.lo;
+  it.SP = kl.SP;
+  it.n = (kl.n_cols + 127) >> 7;
+  const win::TileRange r0(s, kl, it.L, p0, p1), r1(s, kl, it.L, p0 + a.tok, p2);
+  it.first[0] = r0.first;
+  it.first[1] = r1.first;
+  it.last[0] = r0.last;
+  it.last[1] = r1.last;
+  return it;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -83,11 +97,12 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], kv_full[M::NST], kv_empty[M::NST], s_full[2], p_full[2],
       pv_done[2], o_empty[2], drain, never;
+  __shared__ win::ItemRing s_items;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
 
   const WinDims& s = a.s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
   const uint32_t aQ = tc::su32(sm + M::oQ), aKV = tc::su32(sm + M::oKV), aStage = tc::su32(sm + M::oStage);
 
   if (tid == 0) {
@@ -103,6 +118,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       tc::bar_init(&kv_full[k], 1);
       tc::bar_init(&kv_empty[k], 1);
     }
+    win::ring_init(s_items, 10);
     tc::bar_init(&drain, 1);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
@@ -116,33 +132,40 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   // positions of row tile t of an item: [p0, p1)
-  auto tile_p0 = [&](const FwdItem& it, int t) { return s.off + it.t0 + t * a.tok; };
-  auto tile_p1 = [&](const FwdItem& it, int t) { return s.off + min(s.Nq, it.t0 + (t + 1) * a.tok); };
+  auto tile_p0 = [&](const win::Item& it, int t) { return s.off + it.t0 + t * a.tok; };
+  auto tile_p1 = [&](const win::Item& it, int t) { return s.off + min(s.Nq, it.t0 + (t + 1) * a.tok); };
+  auto get = [&](int k) { return win::ring_get(s_items, k, &s_abort, a.wait_ns); };
+  const int sink_tiles = (s.sinks + 127) >> 7;
+  auto uses = [&](const win::Item& it, int t, int j) { return j <= it.last[t] && (j >= it.first[t] || j < sink_tiles); };
 
   if (warp >= 8) {
     win::regs_dec<88>();
     if (warp == 9) {
       // ---------------------------------------------------------------- loader
-      if (lane == 0) {
-        int n_kv = 0, n_q[2] = {0, 0};         // loads issued
-        for (int w = blockIdx.x; w < a.n_items && !aborted(); w += gridDim.x) {
-          const FwdItem it(a, w);
-          const int L = win::valid_len(a.len, it.b, s.N);
-          const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
-          auto load_q = [&](int t) -> bool {
-            if (min(tile_p1(it, t), L) <= tile_p0(it, t)) return true;
-            if (!wait(&q_empty[t], (n_q[t] & 1) ^ 1)) return false;
-            ++n_q[t];
+      int n_kv = 0, n_q[2] = {0, 0};           // loads issued
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const win::Item it = get(i);
+        if (it.n < 0) break;
+        const win::KeyList kl(it.lo, it.SP);
+        auto load_q = [&](int t) -> bool {
+          if (it.last[t] < 0) return true;
+          if (!wait(&q_empty[t], (n_q[t] & 1) ^ 1)) return false;
+          ++n_q[t];
+          if (lane == 0) {
             tc::bar_expect_tx(&q_full[t], M::TILE);
 #pragma unroll
             for (int kb = 0; kb < M::KB; ++kb)
               tc::tma_load4(aQ + t * M::TILE + kb * (128 * 128), &qmap, kb * 64, it.h0, it.t0 + t * a.tok, it.b, &q_full[t]);
-            return true;
-          };
-          auto load_kv = [&](int v0, const CUtensorMap* big, const CUtensorMap* small) -> bool {
-            const int st = n_kv % M::NST;
-            if (!wait(&kv_empty[st], ((n_kv / M::NST) & 1) ^ 1)) return false;
-            ++n_kv;
+          }
+          __syncwarp();
+          return true;
+        };
+        auto load_kv = [&](int v0, const CUtensorMap* big, const CUtensorMap* small) -> bool {
+          const int st = n_kv % M::NST;
+          if (!wait(&kv_empty[st], ((n_kv / M::NST) & 1) ^ 1)) return false;
+          ++n_kv;
+          if (lane == 0) {
             tc::bar_expect_tx(&kv_full[st], M::TILE);
             const uint32_t dst = aKV + st * M::TILE;
             if (v0 >= kl.SP) {
@@ -156,18 +179,29 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
                   tc::tma_load4(dst + kb * (128 * 128) + r * (32 * 128), small, kb * 64, it.kv, kl.key(v0 + 32 * r), it.b,
                                 &kv_full[st]);
             }
-            return true;
-          };
-          if (kl.n_cols == 0) continue;
-          bool ok = load_q(0) && load_kv(0, &kmap, &kmap32) && load_q(1) && load_kv(0, &vmap, &vmap32);
-          for (int v0 = 128; ok && v0 < kl.n_cols; v0 += 128)
-            ok = load_kv(v0, &kmap, &kmap32) && load_kv(v0, &vmap, &vmap32);
-          if (!ok) break;
+          }
+          __syncwarp();
+          return true;
+        };
+        if (it.n == 0) continue;
+        ok = load_q(0) && load_kv(0, &kmap, &kmap32) && load_q(1) && load_kv(0, &vmap, &vmap32);
+        for (int j = 1; ok && j < it.n; ++j) ok = load_kv(128 * j, &kmap, &kmap32) && load_kv(128 * j, &vmap, &vmap32);
+      }
+      // whatever is still in flight lands before the CTA leaves
+      for (int k = max(0, n_kv - M::NST); k < n_kv; ++k) tc::bar_wait(&kv_full[k % M::NST], (k / M::NST) & 1, kDrainNs);
+      for (int t = 0; t < 2; ++t)
+        if (n_q[t]) tc::bar_wait(&q_full[t], (n_q[t] - 1) & 1, kDrainNs);
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- items, decoded ahead of the other roles
+      if (lane == 0) {
+        const int rounds = win::rounds_of(a.n_items);
+        for (int k = 0; k <= rounds; ++k) {
+          const int64_t w = k < rounds ? win::item_of(k, a.n_items) : -1;
+          win::Item it{};
+          if (w >= 0) it = fwd_item(a, static_cast<int>(w));
+          else it.n = -1;                                    // only the last round can miss a CTA
+          if (!win::ring_put(s_items, k, it, &s_abort, kPatient) || w < 0) break;
         }
-        // whatever is still in flight lands before the CTA leaves
-        for (int k = max(0, n_kv - M::NST); k < n_kv; ++k) tc::bar_wait(&kv_full[k % M::NST], (k / M::NST) & 1, kDrainNs);
-        for (int t = 0; t < 2; ++t)
-          if (n_q[t]) tc::bar_wait(&q_full[t], (n_q[t] - 1) & 1, kDrainNs);
       }
     } else if (warp == 8) {
       // ---------------------------------------------------------------- MMA (the warp together, one
@@ -176,14 +210,12 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       int n_kv = 0;
       int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, items of a row tile
       bool issued = false, ok = true;
-      for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
-        const FwdItem it(a, w);
-        const int L = win::valid_len(a.len, it.b, s.N);
-        const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
-        const int n = (kl.n_cols + 127) / 128;
+      for (int i = 0; ok; ++i) {
+        const win::Item it = get(i);
+        const int n = it.n;
+        if (n < 0) break;
         if (n == 0) continue;
         if (a.stall && !wait(&never, 0)) { ok = false; break; }
-        const win::TileRange tr[2] = {{s, kl, L, tile_p0(it, 0), tile_p1(it, 0)}, {s, kl, L, tile_p0(it, 1), tile_p1(it, 1)}};
         // key tile j is load n_kv + 2 j of the ring, its values are the one after
         auto landed = [&](int k) { return wait(&kv_full[k % M::NST], (k / M::NST) & 1); };
         // S of row tile t from the key tile of load k; `last` of the row tile's, `free` the load's last use.
@@ -214,22 +246,22 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           ++n_p[t];
           return true;
         };
-        bool has0 = tr[0].has(0), has1 = tr[1].has(0), acc0 = false, acc1 = false;
+        bool has0 = uses(it, 0, 0), has1 = uses(it, 1, 0), acc0 = false, acc1 = false;
         issued = true;
-        ok = landed(n_kv) && (tr[0].last < 0 || wait(&q_full[0], n_q[0]++ & 1));
-        if (ok && has0) ok = issue_s(0, n_kv, tr[0].last == 0, !has1);
-        ok = ok && (tr[1].last < 0 || wait(&q_full[1], n_q[1]++ & 1));
-        if (ok && has1) ok = issue_s(1, n_kv, tr[1].last == 0, true);
+        ok = landed(n_kv) && (it.last[0] < 0 || wait(&q_full[0], n_q[0]++ & 1));
+        if (ok && has0) ok = issue_s(0, n_kv, it.last[0] == 0, !has1);
+        ok = ok && (it.last[1] < 0 || wait(&q_full[1], n_q[1]++ & 1));
+        if (ok && has1) ok = issue_s(1, n_kv, it.last[1] == 0, true);
         ok = ok && landed(n_kv + 1);
         for (int j = 0; ok && j < n; ++j) {
           const int k = n_kv + 2 * j + 1;
-          const bool next0 = tr[0].has(j + 1), next1 = tr[1].has(j + 1);
+          const bool next0 = uses(it, 0, j + 1), next1 = uses(it, 1, j + 1);
           if (has0 && !issue_pv(0, k, acc0, !has1)) { ok = false; break; }
           if (j + 1 < n && !landed(k + 1)) { ok = false; break; }
-          if (next0 && !issue_s(0, k + 1, tr[0].last == j + 1, !next1)) { ok = false; break; }
+          if (next0 && !issue_s(0, k + 1, it.last[0] == j + 1, !next1)) { ok = false; break; }
           if (has1 && !issue_pv(1, k, acc1, true)) { ok = false; break; }
           if (j + 1 < n && !landed(k + 2)) { ok = false; break; }
-          if (next1 && !issue_s(1, k + 1, tr[1].last == j + 1, true)) { ok = false; break; }
+          if (next1 && !issue_s(1, k + 1, it.last[1] == j + 1, true)) { ok = false; break; }
           acc0 |= has0;
           acc1 |= has1;
           has0 = next0;
@@ -251,14 +283,15 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const uint32_t tS = tm + 128 * t + lane_off, tO = tm + 256 + D * t + lane_off;
     const float c1 = s.scale * kLog2e;
     int n_s = 0, n_kv = 0;                     // key tiles done by this row tile; stages used by earlier items
-    int w = blockIdx.x;
-    for (int n = 0; w < a.n_items && !aborted(); w += gridDim.x, n_kv += 2 * n) {
-      const FwdItem it(a, w);
-      const int L = win::valid_len(a.len, it.b, s.N);
-      const win::KeyList kl(s, L, tile_p0(it, 0), tile_p1(it, 1));
+    int i = 0;
+    for (int n = 0;; ++i, n_kv += 2 * n) {
+      const win::Item it = get(i);
+      n = it.n;
+      if (n < 0) break;
+      const int L = it.L;
+      const win::KeyList kl(it.lo, it.SP);
       const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
-      n = (kl.n_cols + 127) / 128;
-      const win::TileRange tr(s, kl, L, p0, p1);
+      const int j_first = t ? it.first[1] : it.first[0], j_last = t ? it.last[1] : it.last[0];
       const int p = p0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
       const bool row = p < p1 && p < L;
       float m = neg_inf(), l = 0.f;
@@ -266,7 +299,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       bool ok = true;
       for (int j = 0; j < n; ++j) {
         const int v0 = 128 * j;
-        if (!tr.has(j)) continue;
+        if (j > j_last || (j < j_first && j >= sink_tiles)) continue;
         ok = wait(&s_full[t], n_s & 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::after_sync();
@@ -426,12 +459,14 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     }
     if (lane == 0) tc::bulk_wait<0>();
     if (aborted()) {                                         // the rows of the item at hand and of those left
-      for (; w < a.n_items; w += gridDim.x) {
-        const FwdItem it(a, w);
-        const int i = it.t0 + t * a.tok + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
-        if (i >= s.Nq) continue;
-        a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + i] = __int_as_float(0x7fc00000);
-        uint4* o = reinterpret_cast<uint4*>(a.O + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
+      for (; i < win::rounds_of(a.n_items); ++i) {
+        const int64_t w = win::item_of(i, a.n_items);
+        if (w < 0) break;
+        const win::Item it = fwd_item(a, static_cast<int>(w));
+        const int row = it.t0 + t * a.tok + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
+        if (row >= s.Nq) continue;
+        a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + row] = __int_as_float(0x7fc00000);
+        uint4* o = reinterpret_cast<uint4*>(a.O + ((static_cast<int64_t>(it.b) * s.Nq + row) * s.Hq + h) * D);
         for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
       }
     }

@@ -31,6 +31,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kThreads = 384;                  // warps 0-7 softmax and output, 8 (and 10) MMA, 9 loader, 11 row statistics
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
+constexpr uint64_t kPatient = 1ull << 40;      // the item warp outwaits the others, whose giving up it sees
 constexpr uint32_t kNaN2 = 0x7fc07fc0u;        // two bf16 NaNs
 
 struct BwdArgs {
@@ -61,16 +62,24 @@ struct DqSmem {
   static constexpr int bytes = oV + NV * TILE;
 };
 
-struct DqItem {
-  int b, kv, set, t0;
-  __device__ __forceinline__ DqItem(const BwdArgs& a, int w) {
-    const int tile = a.n_tiles - 1 - w / a.n_heads, hh = w % a.n_heads;
-    b = hh / (a.s.Hkv * a.sets);
-    kv = hh / a.sets % a.s.Hkv;
-    set = hh % a.sets;
-    t0 = tile * a.tok;
-  }
-};
+// Work item w: a row tile. first[0]: its heads' place in the statistics' order.
+__device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
+  const WinDims& s = a.s;
+  const int tile = a.n_tiles - 1 - w / a.n_heads, hh = w % a.n_heads, set = hh % a.sets;
+  win::Item it;
+  it.b = hh / (s.Hkv * a.sets);
+  it.kv = hh / a.sets % s.Hkv;
+  it.h0 = it.kv * s.G + set * a.P;
+  it.t0 = tile * a.tok;
+  it.L = win::valid_len(a.len, it.b, s.N);
+  const win::KeyList kl(s, it.L, s.off + it.t0, s.off + min(s.Nq, it.t0 + a.tok));
+  it.lo = kl.lo;
+  it.SP = kl.SP;
+  it.n = (kl.n_cols + 127) >> 7;
+  it.first[0] = (it.b * s.Hkv + it.kv) * a.sets + set;
+  it.first[1] = it.last[0] = it.last[1] = 0;
+  return it;
+}
 
 // TMEM: S (and dS in its place) of key tile n at 128 (n & 1), dP at 256, dQ at 384. One MMA warp
 // issues dP(n) and the next tile's S, the other dQ += dS K as soon as dS is there, so that the
@@ -85,12 +94,13 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
       s_full[2], dp_full, ds_full[2], dq_done[2], dq_last, dq_empty, st_full[2], st_empty[2], drain[2], never;
+  __shared__ win::ItemRing s_items;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   __shared__ float s_stat[2][2][128];        // per item (two at a time): -lse log2 e, D
 
   const WinDims& s = a.s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
   const uint32_t aQ = tc::su32(sm + M::oQ), aO = tc::su32(sm + M::oO), aK = tc::su32(sm + M::oK), aV = tc::su32(sm + M::oV);
 
   if (tid == 0) {
@@ -119,6 +129,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     }
     tc::bar_init(&drain[0], 1);
     tc::bar_init(&drain[1], 1);
+    win::ring_init(s_items, 11);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
     s_abort = 0;
@@ -129,22 +140,24 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   tc::after_sync();
   const uint32_t tm = tmem_base;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
+  auto get = [&](int k) { return win::ring_get(s_items, k, &s_abort, a.wait_ns); };
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
 
   if (warp == 9) {
     // ------------------------------------------------------------------ loader
-    if (lane == 0) {
-      int n_k = 0, n_v = 0, n_q = 0;           // loads issued
-      for (int w = blockIdx.x; w < a.n_items && !aborted(); w += gridDim.x) {
-        const DqItem it(a, w);
-        const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
-        const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
-        if (kl.n_cols == 0) continue;
-        auto load = [&](int& k, uint64_t* full, uint64_t* empty, int ns, uint32_t base, int v0, const CUtensorMap* big,
-                        const CUtensorMap* small) -> bool {
-          const int st = k % ns;
-          if (!wait(&empty[st], ((k / ns) & 1) ^ 1)) return false;
-          ++k;
+    int n_k = 0, n_v = 0, n_q = 0;             // loads issued
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const win::Item it = get(i);
+      if (it.n < 0) break;
+      if (it.n == 0) continue;
+      const win::KeyList kl(it.lo, it.SP);
+      auto load = [&](int& k, uint64_t* full, uint64_t* empty, int ns, uint32_t base, int v0, const CUtensorMap* big,
+                      const CUtensorMap* small) -> bool {
+        const int st = k % ns;
+        if (!wait(&empty[st], ((k / ns) & 1) ^ 1)) return false;
+        ++k;
+        if (lane == 0) {
           tc::bar_expect_tx(&full[st], M::TILE);
           const uint32_t dst = base + st * M::TILE;
           if (v0 >= kl.SP) {
@@ -157,38 +170,38 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
               for (int kb = 0; kb < M::KB; ++kb)
                 tc::tma_load4(dst + kb * (128 * 128) + r * (32 * 128), small, kb * 64, it.kv, kl.key(v0 + 32 * r), it.b, &full[st]);
           }
-          return true;
-        };
-        if (!wait(&q_empty, (n_q & 1) ^ 1)) break;
-        ++n_q;
+        }
+        __syncwarp();
+        return true;
+      };
+      if (!wait(&q_empty, (n_q & 1) ^ 1)) break;
+      ++n_q;
+      if (lane == 0) {
         tc::bar_expect_tx(&q_full, 2 * M::TILE);
 #pragma unroll
         for (int kb = 0; kb < M::KB; ++kb) {
-          tc::tma_load4(aQ + kb * (128 * 128), &qmap, kb * 64, it.kv * s.G + it.set * a.P, it.t0, it.b, &q_full);
-          tc::tma_load4(aO + kb * (128 * 128), &domap, kb * 64, it.kv * s.G + it.set * a.P, it.t0, it.b, &q_full);
+          tc::tma_load4(aQ + kb * (128 * 128), &qmap, kb * 64, it.h0, it.t0, it.b, &q_full);
+          tc::tma_load4(aO + kb * (128 * 128), &domap, kb * 64, it.h0, it.t0, it.b, &q_full);
         }
-        bool ok = true;
-        for (int v0 = 0; ok && v0 < kl.n_cols; v0 += 128)
-          ok = load(n_k, k_full, k_empty, M::NK, aK, v0, &kmap, &kmap32) &&
-               load(n_v, v_full, v_empty, M::NV, aV, v0, &vmap, &vmap32);
-        if (!ok) break;
       }
-      // whatever is still in flight lands before the CTA leaves
-      for (int k = max(0, n_k - M::NK); k < n_k; ++k) tc::bar_wait(&k_full[k % M::NK], (k / M::NK) & 1, kDrainNs);
-      for (int k = max(0, n_v - M::NV); k < n_v; ++k) tc::bar_wait(&v_full[k % M::NV], (k / M::NV) & 1, kDrainNs);
-      if (n_q) tc::bar_wait(&q_full, (n_q - 1) & 1, kDrainNs);
+      __syncwarp();
+      for (int j = 0; ok && j < it.n; ++j)
+        ok = load(n_k, k_full, k_empty, M::NK, aK, 128 * j, &kmap, &kmap32) &&
+             load(n_v, v_full, v_empty, M::NV, aV, 128 * j, &vmap, &vmap32);
     }
+    // whatever is still in flight lands before the CTA leaves
+    for (int k = max(0, n_k - M::NK); k < n_k; ++k) tc::bar_wait(&k_full[k % M::NK], (k / M::NK) & 1, kDrainNs);
+    for (int k = max(0, n_v - M::NV); k < n_v; ++k) tc::bar_wait(&v_full[k % M::NV], (k / M::NV) & 1, kDrainNs);
+    if (n_q) tc::bar_wait(&q_full, (n_q - 1) & 1, kDrainNs);
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA, S and dP (the warp
     // together, one lane issuing: operands stay in uniform registers)
     const bool leader = win::elect();
     int n_q = 0, g = 0;                        // items, key tiles so far
     bool issued = false, ok = true;
-    for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
-      const DqItem it(a, w);
-      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
-      const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
-      const int n = (kl.n_cols + 127) / 128;
+    for (int i = 0; ok; ++i) {
+      const int n = get(i).n;
+      if (n < 0) break;
       if (n == 0) continue;
       if (a.stall && !wait(&never, 0)) { ok = false; break; }
       ok = wait(&q_full, n_q & 1);
@@ -232,11 +245,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     const bool leader = win::elect();
     int n_q = 0, g = 0;
     bool issued = false, ok = true;
-    for (int w = blockIdx.x; ok && w < a.n_items && !aborted(); w += gridDim.x) {
-      const DqItem it(a, w);
-      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
-      const win::KeyList kl(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok));
-      const int n = (kl.n_cols + 127) / 128;
+    for (int i = 0; ok; ++i) {
+      const int n = get(i).n;
+      if (n < 0) break;
       if (n == 0) continue;
       for (int j = 0; ok && j < n; ++j, ++g) {
         const int st = g % M::NK;
@@ -263,25 +274,34 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     // ------------------------------------------------------------------ D = dO . O and -lse log2 e of
     // the rows, an item ahead: D / 8 lanes a row, several rounds of rows in flight. One warp's loads do not
     // cover the latency of memory, so the rows of the item after are asked into L2 meanwhile.
+    // It also decodes the items for the other roles.
     constexpr int LPR = D / 8, RPW = 32 / LPR, R = 6;
+    const int rounds = win::rounds_of(a.n_items);
     int n_q = 0;
-    for (int w = blockIdx.x; w < a.n_items && !aborted(); w += gridDim.x) {
-      const DqItem it(a, w);
-      if (w + static_cast<int>(gridDim.x) < a.n_items) {
-        const DqItem nx(a, w + gridDim.x);
-        const int64_t f = (static_cast<int64_t>(nx.b) * s.Nq + nx.t0) * s.Hq + nx.kv * s.G + nx.set * a.P;
+    for (int k = 0; k <= rounds; ++k) {
+      const int64_t w = k < rounds ? win::item_of(k, a.n_items) : -1;
+      win::Item it{};
+      if (w >= 0) it = dq_item(a, static_cast<int>(w));
+      else it.n = -1;                                        // only the last round can miss a CTA
+      bool ok = lane != 0 || win::ring_put(s_items, k, it, &s_abort, kPatient);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || w < 0) break;
+      const int64_t w1 = k + 1 < rounds ? win::item_of(k + 1, a.n_items) : -1;
+      if (w1 >= 0) {
+        const win::Item nx = dq_item(a, static_cast<int>(w1));
+        const int64_t f = (static_cast<int64_t>(nx.b) * s.Nq + nx.t0) * s.Hq + nx.h0;
         for (int r = lane; r < min(128, (s.Nq - nx.t0) * a.P); r += 32)
 #pragma unroll
           for (int c = 0; c < D; c += 64) {
-            const int64_t at = (f + static_cast<int64_t>((r >> a.lp)) * s.Hq + (r & (a.P - 1))) * D + c;
+            const int64_t at = (f + static_cast<int64_t>(r >> a.lp) * s.Hq + (r & (a.P - 1))) * D + c;
             asm volatile("prefetch.global.L2 [%0];" ::"l"(a.O + at));
             asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dO + at));
           }
       }
-      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0;
-      if (win::KeyList(s, L, p0, s.off + min(s.Nq, it.t0 + a.tok)).n_cols == 0) continue;
-      const int sl = n_q & 1, rows = min(128, (min(s.Nq, L - s.off) - it.t0) * a.P), h0 = it.kv * s.G + it.set * a.P;
-      if (!__all_sync(0xffffffffu, wait(&st_empty[sl], ((n_q >> 1) & 1) ^ 1))) break;
+      if (it.n == 0) continue;
+      const int sl = n_q & 1, rows = min(128, (min(s.Nq, it.L - s.off) - it.t0) * a.P), h0 = it.h0;
+      ok = __all_sync(0xffffffffu, win::wait(&st_empty[sl], ((n_q >> 1) & 1) ^ 1, &s_abort, kPatient));
+      if (!ok) break;
       const int64_t first = (static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + h0;    // row r: + r / P * Hq + r % P
       for (int r0 = 0; r0 < rows; r0 += RPW * R) {
         uint4 o[R], g[R];
@@ -307,7 +327,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         }
       }
       __syncwarp();
-      const int64_t at0 = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + it.set) * a.Nqp + it.t0) * a.P;
+      const int64_t at0 = (static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P;
 #pragma unroll
       for (int r = lane; r < 128; r += 32) {
         const float nl = r < rows ? -a.lse[(static_cast<int64_t>(it.b) * s.Hq + h0 + (r & (a.P - 1))) * s.Nq + it.t0 + (r >> a.lp)] * kLog2e : 0.f;
@@ -326,14 +346,14 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c1 = s.scale * kLog2e;
-    int n_k = 0, n_q = 0, w = blockIdx.x;
-    for (; w < a.n_items && !aborted(); w += gridDim.x) {
-      const DqItem it(a, w);
-      const int L = win::valid_len(a.len, it.b, s.N), p0 = s.off + it.t0, p1 = s.off + min(s.Nq, it.t0 + a.tok);
-      const win::KeyList kl(s, L, p0, p1);
-      const int n = (kl.n_cols + 127) / 128;
-      const int hp = (r & (a.P - 1)), i = it.t0 + (r >> a.lp), p = s.off + i, h = it.kv * s.G + it.set * a.P + hp;
-      const bool row = p < p1 && p < L;
+    int n_k = 0, n_q = 0, k_item = 0;
+    for (;; ++k_item) {
+      const win::Item it = get(k_item);
+      const int n = it.n, L = it.L;
+      if (n < 0) break;
+      const win::KeyList kl(it.lo, it.SP);
+      const int i = it.t0 + (r >> a.lp), p = s.off + i, h = it.h0 + (r & (a.P - 1));
+      const bool row = i < s.Nq && p < L;
       if (n == 0) {                                          // no row sees anything: dQ = 0
         if (g == 0 && i < s.Nq) {
           uint4* o = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
@@ -409,18 +429,24 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::after_sync();
       ++n_q;
-      uint4* out = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D + 64 * g);
       if (g < M::KB) {
+        const int64_t row0 = ((static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + it.h0) * D + 64 * g + 8 * (lane & 3);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           float y[32];
           tc::tmem_ld32(tm + 384 + 64 * g + 32 * q + lane_off, y);
+          uint32_t u[4][4];                                  // four 16-byte pieces of row r
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[c][k] = pack_bf16(s.scale * y[8 * c + 2 * k], s.scale * y[8 * c + 2 * k + 1]);
+          win::transpose4(u, lane);                          // piece lane & 3 of four rows: 64 bytes of a row a store
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t u[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) u[k] = pack_bf16(s.scale * y[8 * c + 2 * k], s.scale * y[8 * c + 2 * k + 1]);
-            if (i < s.Nq) out[4 * q + c] = make_uint4(u[0], u[1], u[2], u[3]);
+            const int rr = (r & ~3) + c;
+            if (it.t0 + (rr >> a.lp) < s.Nq)
+              *reinterpret_cast<uint4*>(a.dQ + row0 + (static_cast<int64_t>(rr >> a.lp) * s.Hq + (rr & (a.P - 1))) * D + 32 * q) =
+                  make_uint4(u[c][0], u[c][1], u[c][2], u[c][3]);
           }
         }
       }
@@ -428,9 +454,11 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       tc::bar_arrive(&dq_empty);
     }
     if (aborted() && g == 0) {                               // the rows of the item at hand and of those left
-      for (; w < a.n_items; w += gridDim.x) {
-        const DqItem it(a, w);
-        const int i = it.t0 + (r >> a.lp), h = it.kv * s.G + it.set * a.P + (r & (a.P - 1));
+      for (; k_item < win::rounds_of(a.n_items); ++k_item) {
+        const int64_t w = win::item_of(k_item, a.n_items);
+        if (w < 0) break;
+        const win::Item it = dq_item(a, static_cast<int>(w));
+        const int i = it.t0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
         if (i >= s.Nq) continue;
         uint4* o = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
         for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(kNaN2, kNaN2, kNaN2, kNaN2);
@@ -528,14 +556,14 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   int& s_abort = bar.abort;
 
   const WinDims& s = a.s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
   const uint32_t aK = tc::su32(sm + M::oK), aV = tc::su32(sm + M::oV), aQ = tc::su32(sm + M::oQ), aO = tc::su32(sm + M::oO);
 
   const DkvItem it(a, blockIdx.x);
   const int kb = 128 * it.kt, L = win::valid_len(a.len, it.b, s.N);
   const TokenRange tr(s, a.tok, L, it.kt);
   // this chunk's row tiles: token tile n / sets, head set n % sets
-  const int tile0 = it.c * a.ct, n = max(0, min(a.ct, tr.n - tile0)) * a.sets;
+  const int tile0 = it.c * a.ct, n = win::uniform(max(0, min(a.ct, tr.n - tile0)) * a.sets);
   if (n == 0 && it.slot >= 0) return;                        // the reduction knows which chunks are empty
   auto tile_tok = [&](int k) { return tr.i0 + (tile0 + k / a.sets) * a.tok; };
   auto tile_end = [&](int k) { return s.off + tile_tok(k) + a.tok; };    // one past its last position

@@ -43,6 +43,11 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
   return tc::fma2(b, tc::pack2(-1.f, -1.f), a);
 }
 
+// A value that is the same in the whole warp, in a form that the compiler knows to be: what an MMA
+// warp's operands and branches come from then stays in uniform registers (the forward at the 64K prefill
+// took 1.60 ms without and 1.44 ms with them).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -89,6 +94,23 @@ inline int log2_of(int p) {
   return l;
 }
 
+// Among four neighbouring lanes: lane l's piece c becomes lane c's piece l (16-byte pieces).
+__device__ __forceinline__ void transpose4(uint32_t (&u)[4][4], int lane) {
+#pragma unroll
+  for (int m = 1; m < 4; m *= 2) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & m) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? u[c][k] : u[c | m][k], m);
+        if (up) u[c][k] = t; else u[c | m][k] = t;
+      }
+    }
+  }
+}
+
 // Tensor map of [B, N, H, d] bf16 with `stride` elements between tokens: boxes of 64 elements x
 // `heads` x `tokens`.
 inline int token_map(CUtensorMap* m, const void* p, int B, int N, int H, int d, int64_t stride, int heads, int tokens) {
@@ -118,6 +140,7 @@ __device__ __forceinline__ int valid_len(const int32_t* len, int b, int N) {
 // starts at key 0. So every padding column holds a key below lo, one of the sequence's.
 struct KeyList {
   int lo, SP, n_cols;
+  __device__ __forceinline__ KeyList(int lo_, int SP_) : lo(lo_), SP(SP_), n_cols(0) {}
   __device__ __forceinline__ KeyList(const WinDims& s, int L, int p0, int p1) {
     const int last = min(p1, L) - 1;
     lo = max(0, p0 - s.window + 1);
@@ -140,6 +163,61 @@ struct TileRange {
   }
   __device__ __forceinline__ bool has(int j) const { return j <= last && (j >= first || j < sink); }
 };
+
+// A work item as its CTA's roles take it: decoded by one warp, ahead of the others (the divisions would
+// sit at every item's start otherwise), and handed over through a ring in shared memory. n: key tiles of
+// 128 columns, -1 past the last item. first / last: the key tiles of the item's row tiles (TileRange).
+struct __align__(16) Item {
+  int b, kv, h0, t0;
+  int L, lo, SP, n;
+  int first[2], last[2];
+};
+
+constexpr int kItems = 4;
+
+// The CTA's k-th item of n, or -1: rounds of one item a CTA, every second one backwards. Items come
+// with the longest first, and a round's first CTA would otherwise always have the longest.
+__device__ __forceinline__ int64_t item_of(int k, int n) {
+  const int64_t w = static_cast<int64_t>(k) * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  return w < n ? w : -1;
+}
+__device__ __forceinline__ int rounds_of(int n) { return static_cast<int>((n + static_cast<int64_t>(gridDim.x) - 1) / gridDim.x); }
+
+struct ItemRing {
+  Item item[kItems];
+  uint64_t full[kItems], empty[kItems];
+};
+
+__device__ __forceinline__ void ring_init(ItemRing& q, int consumer_warps) {
+  for (int k = 0; k < kItems; ++k) {
+    tc::bar_init(&q.full[k], 1);
+    tc::bar_init(&q.empty[k], consumer_warps);
+  }
+}
+
+// Publisher (one lane): item k of the CTA.
+__device__ __forceinline__ bool ring_put(ItemRing& q, int k, const Item& it, int* abort_flag, uint64_t limit_ns) {
+  if (!wait(&q.empty[k % kItems], ((k / kItems) & 1) ^ 1, abort_flag, limit_ns)) return false;
+  q.item[k % kItems] = it;
+  tc::bar_arrive(&q.full[k % kItems]);
+  return true;
+}
+
+// Consumer warp: item k; n = -1 past the last one, or when the CTA gives up.
+__device__ __forceinline__ Item ring_get(ItemRing& q, int k, int* abort_flag, uint64_t limit_ns) {
+  const bool ok = __all_sync(0xffffffffu, wait(&q.full[k % kItems], (k / kItems) & 1, abort_flag, limit_ns));
+  Item it = q.item[k % kItems];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::bar_arrive(&q.empty[k % kItems]);
+  if (!ok) it.n = -1;
+  it.n = uniform(it.n);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.first[t] = uniform(it.first[t]);
+    it.last[t] = uniform(it.last[t]);
+  }
+  return it;
+}
 
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect() {

@@ -187,6 +187,40 @@ def test_two_streams_at_once():
             assert torch.equal(t, w[n]), n
 
 
+@pytest.fixture
+def stalled():
+    pisa.set_wait_limit(2_000_000)          # 2 ms
+    pisa.set_test_stall(True)
+    try:
+        yield
+    finally:
+        pisa.set_test_stall(False)
+        pisa.set_wait_limit(0)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,d,window,sinks", [(700, 8, 2, 128, 150, 5), (20000, 4, 1, 64, 300, 0), (3000, 2, 2, 128, 3000, 0)])
+def test_wait_that_runs_out_is_reported_and_poisons_outputs(stalled, N, Hq, Hkv, d, window, sinks):
+    Q, K, V, dO = _inputs(1, N, N, Hq, Hkv, d, seed=6)
+    s = pisa.window_shape_of(Q, K, V, window, sinks)
+    wf, wb = (pisa.window_workspace(s, op, Q.device) for op in (pisa.WINDOW_FWD, pisa.WINDOW_BWD))
+    O, lse = pisa.window_attn_fwd(Q, K, V, s, ws=wf)
+    assert pisa.workspace_status(wf) & pisa.STATUS_TIMEOUT
+    assert bool(O.isnan().all()) and bool(lse.isnan().all())
+    with pytest.raises(pisa.PisaError):
+        pisa.check_status(wf)
+    assert bool(pisa.window_attn_fwd(Q, K, V, s)[0].isnan().all())       # without a workspace the outputs tell
+    z = torch.zeros_like(O)
+    grads = pisa.window_attn_bwd(Q, K, V, z, torch.zeros_like(lse), dO, s, ws=wb)
+    assert pisa.workspace_status(wb) & pisa.STATUS_TIMEOUT
+    for t in grads:
+        assert bool(t.isnan().all())
+    pisa.set_test_stall(False)                                           # and the next calls are sound again
+    pisa.set_wait_limit(0)
+    got = _run(Q, K, V, dO, window, sinks)
+    for t in got.values():
+        assert bool(t.isfinite().all())
+
+
 # --------------------------------------------------------------------------------------- decode
 def _slot(j, sinks, cap):
     return j if j < sinks else sinks + (j - sinks) % (cap - sinks)
