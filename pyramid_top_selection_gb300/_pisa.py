@@ -352,7 +352,7 @@ def _on(dev, fn, *args) -> None:
 
 def _need_shaped(t, dtype, size, dev, name: str) -> None:
     """A contiguous tensor of this type and size on `dev`."""
-    if t.dtype != dtype or t.device != dev or not t.is_cuda or t.shape != size or not t.is_contiguous():
+    if t.device != dev or dev.type != "cuda" or t.dtype != dtype or t.shape != size or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(size)} on {dev} "
                          f"(got {t.dtype}, {tuple(t.shape)}, {t.device}, contiguous={t.is_contiguous()})")
 

@@ -237,7 +237,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           if (!wait(&p_full[t], n_p[t] & 1)) return false;
           tc::after_sync();
           if (leader) {
-            win::product_ts<D>(tm + 256 + D * t, tm + 128 * t, 32, win::desc_mn_lo(aKV + k % M::NST * M::TILE, 128 * 128),
+            win::product_ts<D, 128>(tm + 256 + D * t, tm + 128 * t, win::desc_mn_lo(aKV + k % M::NST * M::TILE, 128 * 128),
                                accumulate);
             tc::commit(&pv_done[t]);
             if (free) tc::commit(&kv_empty[k % M::NST]);
@@ -514,8 +514,12 @@ int launch_window_fwd(const WinDims& s, const void* Q, const void* K, const void
   if (int e = win::token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
   if (int e = win::token_map(&m[1], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
   if (int e = win::token_map(&m[2], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 128)) return e;
-  if (int e = win::token_map(&m[3], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
-  if (int e = win::token_map(&m[4], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
+  m[3] = m[1];                     // the sinks' boxes, where there are any
+  m[4] = m[2];
+  if (s.sinks > 0) {
+    if (int e = win::token_map(&m[3], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 32)) return e;
+    if (int e = win::token_map(&m[4], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
+  }
   if (int e = win::token_map(&m[5], O, s.B, s.Nq, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
   if (ws) {
     cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);

@@ -256,7 +256,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         tc::after_sync();
         issued = true;
         if (leader) {
-          win::product_ts<D>(tm + 384, tm + 128 * (g & 1), 64, win::desc_mn_lo(aK + st * M::TILE, 128 * 128), j > 0);
+          win::product_ts<D, 64>(tm + 384, tm + 128 * (g & 1), win::desc_mn_lo(aK + st * M::TILE, 128 * 128), j > 0);
           tc::commit(&dq_done[g & 1]);
           tc::commit(&k_empty[st]);
           if (j + 1 == n) tc::commit(&dq_last);
@@ -676,7 +676,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!wait(&p_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D>(tm + 256, tm, 64, win::desc_mn_lo(aO + so * M::TILE, 128 * 128), k > 0);
+          win::product_ts<D, 64>(tm + 256, tm, win::desc_mn_lo(aO + so * M::TILE, 128 * 128), k > 0);
           tc::commit(&dv_done);
           tc::commit(&o_empty[so]);
         }
@@ -689,7 +689,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!wait(&ds_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D>(tm + 256 + D, tm + 128, 64, win::desc_mn_lo(aQ + qk * M::TILE, 128 * 128), k > 0);
+          win::product_ts<D, 64>(tm + 256 + D, tm + 128, win::desc_mn_lo(aQ + qk * M::TILE, 128 * 128), k > 0);
           tc::commit(&dk_done);
           tc::commit(&q_empty[qk]);
         }

@@ -256,13 +256,15 @@ __device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_lo, uint32_t b
   }
 }
 
-// D (128 x DIM) (+)= A (128 x 128, bf16 in tensor memory, its second 64 columns `split` 32-bit columns
-// after the first) B (128 x DIM), B's rows as stored (MN-major).
-template <int DIM>
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, int split, uint32_t b_lo, bool accumulate) {
+// D (128 x DIM) (+)= A (128 x 128, bf16 in tensor memory) B (128 x DIM), B's rows as stored (MN-major).
+// A's columns lie in groups of RUN, each packed in the first half of the RUN 32-bit columns that held the
+// fp32 values it was made from.
+template <int DIM, int RUN>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, bool accumulate) {
   constexpr uint32_t id = tc::idesc_bf16_major(128, DIM, false, true);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) mma_ts(d, a_tmem + split * (k >> 2) + 8 * (k & 3), b_lo + k * (2048 >> 4), id, accumulate || k > 0);
+  for (int k = 0; k < 8; ++k)
+    mma_ts(d, a_tmem + 16 * k / RUN * RUN + 16 * k % RUN / 2, b_lo + k * (2048 >> 4), id, accumulate || k > 0);
 }
 
 }  // namespace win
