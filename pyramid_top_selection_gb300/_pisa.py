@@ -340,6 +340,8 @@ def decode_step(shape: DecodeShape, pos, Kcache, Vcache, pyr, q, k_new, v_new, o
 
 def _on(dev, fn, *args) -> None:
     """Call fn(*args, stream) on dev's current stream, with dev the current device."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be CUDA tensors (got {dev})")
     stream = torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without its objects
     if dev.index == torch.cuda.current_device():
         rc = fn(*args, stream)
@@ -351,18 +353,18 @@ def _on(dev, fn, *args) -> None:
 
 
 def _need_shaped(t, dtype, size, dev, name: str) -> None:
-    """A contiguous tensor of this type and size on `dev`."""
-    if t.device != dev or dev.type != "cuda" or t.dtype != dtype or t.shape != size or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(size)} on {dev} "
+    """A contiguous tensor of this type and size on `dev` (the other tensors' device)."""
+    if t.dtype is not dtype or t.shape != size or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(size)} on {dev} "
                          f"(got {t.dtype}, {tuple(t.shape)}, {t.device}, contiguous={t.is_contiguous()})")
 
 
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements between consecutive tokens of [B, N, H, d] (0: contiguous), d and the heads contiguous."""
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [B, N, H, d] (got {tuple(t.shape)})")
     if t.is_contiguous():
         return 0
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, N, H, d] (got {tuple(t.shape)})")
     B, N, H, d = t.shape
     sb, sn, sh, sd = t.stride()
     step = sn if N > 1 else sb
@@ -372,10 +374,10 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
 
 
 def _need_tokens(t, size, stride: int, dev, name: str) -> None:
-    if t.dtype != torch.bfloat16 or t.device != dev or not t.is_cuda or t.shape != size:
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor {tuple(size)} on {dev} "
+    if t.dtype is not torch.bfloat16 or t.shape != size or t.device != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor {tuple(size)} on {dev} "
                          f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
-    if not t.is_contiguous() or stride not in (0, size[2] * size[3]):
+    if stride or not t.is_contiguous():
         if size[0] * size[1] > 1 and (_token_stride(t, name) or size[2] * size[3]) != (stride or size[2] * size[3]):
             raise ValueError(f"{name} has strides {tuple(t.stride())}, the shape says {stride} elements a token")
 

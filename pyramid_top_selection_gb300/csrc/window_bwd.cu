@@ -900,8 +900,11 @@ void plan(BwdArgs& a) {
   a.n_st = std::min(a.n_kt, (s.sinks + 127) / 128);
   const int64_t all = (s.Nq + 3 + a.tok - 1) / a.tok;                       // token tiles of every row
   const int64_t band = std::min(all, (int64_t(s.window) + 130 + a.tok - 1) / a.tok);
-  const int64_t total = band * a.sets * a.n_kt * a.n_bh;
-  const int64_t want = std::max<int64_t>(16, total / (152 * 6));            // row tiles of an item
+  const int64_t tiles = static_cast<int64_t>(a.n_kt) * a.n_bh, total = band * a.sets * tiles;
+  // row tiles of an item: a sixth of a CTA's share, at least 16; a small problem (under 32 a CTA) whose
+  // key tiles leave CTAs idle is cut into as many equal runs as there are CTAs for
+  int64_t want = std::max<int64_t>(16, total / (152 * 6));
+  if (total < 152 * 32 && tiles < 152) want = (band * a.sets + 152 / tiles - 1) / (152 / tiles);
   a.ct = static_cast<int>(std::min(band, (want + a.sets - 1) / a.sets));
   a.nck = static_cast<int>((band + a.ct - 1) / a.ct);
   a.ncs = a.n_st ? static_cast<int>((all + a.ct - 1) / a.ct) : a.nck;

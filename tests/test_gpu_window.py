@@ -68,6 +68,8 @@ CASES = {  # B, Nq, N, Hq, Hkv, d, window, sinks, lens, fused
     "padded, many tiles": (3, 1300, 1300, 4, 2, 64, 900, 4, [1300, 777, 1157], False),
     "padded, many tiles, wide heads": (2, 1100, 1100, 4, 4, 128, 2000, 0, [1001, 1099], False),
     "padded chunk with far sinks": (2, 400, 1500, 16, 2, 128, 128, 70, [1500, 1205], False),
+    "many heads, whole key tiles": (3, 900, 900, 8, 8, 64, 100, 3, None, False),
+    "many heads, whole key tiles, padded": (2, 1300, 1300, 16, 8, 128, 90, 0, [1300, 1001], True),
     "long chunk": (1, 129, 2000, 8, 2, 128, 700, 16, None, False),
 }
 

@@ -148,6 +148,17 @@ def test_binding_refuses_tensors_that_do_not_fit():
         pisa.window_attn_fwd(z, z, z, s)
     with pytest.raises(ValueError, match="CUDA"):
         pisa.qk_norm_rope(z, z, torch.zeros(32), pisa.rope_shape_of(z, z, 64))
+    for bad in (z.float(), z[:, :7], z.transpose(1, 2).contiguous().transpose(1, 2)):
+        with pytest.raises(ValueError, match="V "):
+            pisa.window_attn_fwd(z, z, bad, s)
+    with pytest.raises(ValueError, match="lens"):
+        pisa.window_attn_fwd(z, z, z, s, lens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="out"):
+        pisa.window_attn_fwd(z, z, z, s, out=z[:1])
+    with pytest.raises(ValueError, match="dO"):
+        pisa.window_attn_bwd(z, z, z, z, torch.zeros(2, 4, 8), z[:, :, :2], s)
+    with pytest.raises(ValueError, match="inv_freq"):
+        pisa.qk_norm_rope(z, z, torch.zeros(16), pisa.rope_shape_of(z, z, 64))
     with pytest.raises(ValueError, match="pos"):
         pisa.window_decode_step(pisa.make_window_decode_shape(2, 8, 4, 4, 64, 4), torch.zeros(2), z, z, z[:, 0],
                                 z[:, 0], z[:, 0])
