@@ -272,10 +272,14 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     }
   } else if (warp == 11) {
     // ------------------------------------------------------------------ D = dO . O and -lse log2 e of
-    // the rows, an item ahead: D / 8 lanes a row, several rounds of rows in flight. One warp's loads do not
-    // cover the latency of memory, so the rows of the item after are asked into L2 meanwhile.
-    // It also decodes the items for the other roles.
-    constexpr int LPR = D / 8, RPW = 32 / LPR, R = 6;
+    // the rows, an item ahead. The dot products of 8 rows are the diagonal of an 8 x 8 product on
+    // m16n8k16 MMAs (half of A's rows zero; k taken in an order that makes a lane's operands 16 bytes of
+    // a row): one warp then keeps up with the item's other work, where sums by lanes and shuffles kept
+    // the softmax warps waiting 8400 of 31000 cycles an item at a window of 1024. One warp's loads do not
+    // cover the latency of memory, so the rows of the item after are asked into L2 meanwhile. It also
+    // decodes the items for the other roles.
+    constexpr int PC = D / 32, RG = 256 / D;                 // 16-byte pieces of a row a lane takes; groups of 8 rows in flight
+    const int g8 = lane >> 2, p4 = lane & 3;
     const int rounds = win::rounds_of(a.n_items);
     int n_q = 0;
     for (int k = 0; k <= rounds; ++k) {
@@ -303,27 +307,28 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       ok = __all_sync(0xffffffffu, win::wait(&st_empty[sl], ((n_q >> 1) & 1) ^ 1, &s_abort, kPatient));
       if (!ok) break;
       const int64_t first = (static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + h0;    // row r: + r / P * Hq + r % P
-      for (int r0 = 0; r0 < rows; r0 += RPW * R) {
-        uint4 o[R], g[R];
+      for (int r0 = 0; r0 < rows; r0 += 8 * RG) {
+        uint4 o[RG][PC], g[RG][PC];
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-          const int r = r0 + k * RPW + lane / LPR;
-          const int64_t at = (first + static_cast<int64_t>((r >> a.lp)) * s.Hq + (r & (a.P - 1))) * D + 8 * (lane % LPR);
-          o[k] = r < rows ? ldg_u4(a.O + at) : make_uint4(0, 0, 0, 0);
-          g[k] = r < rows ? ldg_u4(a.dO + at) : make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < RG; ++x) {
+          const int r = r0 + 8 * x + g8;
+          const int64_t at = (first + static_cast<int64_t>(r >> a.lp) * s.Hq + (r & (a.P - 1))) * D + 8 * p4;
+#pragma unroll
+          for (int c = 0; c < PC; ++c) {
+            o[x][c] = r < rows ? ldg_u4(a.O + at + 32 * c) : make_uint4(0, 0, 0, 0);
+            g[x][c] = r < rows ? ldg_u4(a.dO + at + 32 * c) : make_uint4(0, 0, 0, 0);
+          }
         }
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-          const uint32_t u[4] = {o[k].x, o[k].y, o[k].z, o[k].w}, v[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
-          float d = 0.f;
+        for (int x = 0; x < RG; ++x) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            d = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), d);
-            d = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), d);
+          for (int c = 0; c < PC; ++c) {
+            const uint32_t a0[4] = {g[x][c].x, 0u, g[x][c].y, 0u}, a1[4] = {g[x][c].z, 0u, g[x][c].w, 0u};
+            mma_bf16(d, a0, o[x][c].x, o[x][c].y);
+            mma_bf16(d, a1, o[x][c].z, o[x][c].w);
           }
-#pragma unroll
-          for (int x = LPR / 2; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-          if (lane % LPR == 0 && r0 + k * RPW + lane / LPR < 128) s_stat[sl][1][r0 + k * RPW + lane / LPR] = d;
+          if (p4 == g8 >> 1) s_stat[sl][1][r0 + 8 * x + g8] = g8 & 1 ? d[1] : d[0];
         }
       }
       __syncwarp();
