@@ -573,7 +573,30 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   auto tile_tok = [&](int k) { return tr.i0 + (tile0 + k / a.sets) * a.tok; };
   auto tile_end = [&](int k) { return s.off + tile_tok(k) + a.tok; };    // one past its last position
 
-  if (tid == 0) {
+  // the loads of row tile k (one lane; the stages it waits for are `wait`'s business)
+  auto load_q = [&](int k) {
+    const int sq = k % M::NQ;
+    tc::bar_expect_tx(&q_full[sq], M::TILE);
+#pragma unroll
+    for (int x = 0; x < M::KB; ++x)
+      tc::tma_load4(aQ + sq * M::TILE + x * (128 * 128), &qmap, x * 64, it.kv * s.G + k % a.sets * a.P, tile_tok(k), it.b, &q_full[sq]);
+  };
+  auto load_o = [&](int k) {
+    const int so = k % M::NO;
+    tc::bar_expect_tx(&o_full[so], M::TILE);
+#pragma unroll
+    for (int x = 0; x < M::KB; ++x)
+      tc::tma_load4(aO + so * M::TILE + x * (128 * 128), &domap, x * 64, it.kv * s.G + k % a.sets * a.P, tile_tok(k), it.b, &o_full[so]);
+  };
+  auto load_stat = [&](int k) {
+    const int ss = k & 1;
+    const int64_t at = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + k % a.sets) * a.Nqp + tile_tok(k)) * a.P;
+    const uint32_t stat = tc::su32(sm + M::oStat) + ss * 1024;
+    tc::bar_expect_tx(&st_full[ss], 1024);
+    win::bulk_load(stat, a.nlse + at, 512, &st_full[ss]);
+    win::bulk_load(stat + 512, a.delta + at, 512, &st_full[ss]);
+  };
+  if (warp == 9 && lane == 0) {        // the first loads run under the rest of the CTA's start
     tc::bar_init(&kv_full, 1);
     for (int k = 0; k < M::NQ; ++k) {
       tc::bar_init(&q_full[k], 1);
@@ -595,6 +618,16 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
     s_abort = 0;
+    if (n > 0) {
+      tc::bar_expect_tx(&kv_full, 2 * M::TILE);
+#pragma unroll
+      for (int x = 0; x < M::KB; ++x) tc::tma_load4(aK + x * (128 * 128), &kmap, x * 64, it.kv, kb, it.b, &kv_full);
+      load_q(0);
+#pragma unroll
+      for (int x = 0; x < M::KB; ++x) tc::tma_load4(aV + x * (128 * 128), &vmap, x * 64, it.kv, kb, it.b, &kv_full);
+      load_o(0);
+      load_stat(0);
+    }
   }
   if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
   tc::before_sync();
@@ -607,35 +640,17 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   if (warp == 9) {
     // ------------------------------------------------------------------ loader
     if (lane == 0 && n > 0) {
-      tc::bar_expect_tx(&kv_full, 2 * M::TILE);
-#pragma unroll
-      for (int x = 0; x < M::KB; ++x) {
-        tc::tma_load4(aK + x * (128 * 128), &kmap, x * 64, it.kv, kb, it.b, &kv_full);
-        tc::tma_load4(aV + x * (128 * 128), &vmap, x * 64, it.kv, kb, it.b, &kv_full);
-      }
-      int n_q = 0, n_o = 0, n_st = 0;          // loads issued
-      for (int k = 0; k < n && !aborted(); ++k) {
-        const int i0 = tile_tok(k), set = k % a.sets, h0 = it.kv * s.G + set * a.P;
-        const int sq = k % M::NQ, so = k % M::NO, ss = k & 1;
-        if (!wait(&q_empty[sq], ((k / M::NQ) & 1) ^ 1)) break;
+      int n_q = 1, n_o = 1, n_st = 1;          // loads issued
+      for (int k = 1; k < n && !aborted(); ++k) {
+        if (!wait(&q_empty[k % M::NQ], ((k / M::NQ) & 1) ^ 1)) break;
         ++n_q;
-        tc::bar_expect_tx(&q_full[sq], M::TILE);
-#pragma unroll
-        for (int x = 0; x < M::KB; ++x)
-          tc::tma_load4(aQ + sq * M::TILE + x * (128 * 128), &qmap, x * 64, h0, i0, it.b, &q_full[sq]);
-        if (!wait(&o_empty[so], ((k / M::NO) & 1) ^ 1)) break;
+        load_q(k);
+        if (!wait(&o_empty[k % M::NO], ((k / M::NO) & 1) ^ 1)) break;
         ++n_o;
-        tc::bar_expect_tx(&o_full[so], M::TILE);
-#pragma unroll
-        for (int x = 0; x < M::KB; ++x)
-          tc::tma_load4(aO + so * M::TILE + x * (128 * 128), &domap, x * 64, h0, i0, it.b, &o_full[so]);
-        if (!wait(&st_empty[ss], ((k >> 1) & 1) ^ 1)) break;
+        load_o(k);
+        if (!wait(&st_empty[k & 1], ((k >> 1) & 1) ^ 1)) break;
         ++n_st;
-        const int64_t at = ((static_cast<int64_t>(it.b * s.Hkv + it.kv) * a.sets + set) * a.Nqp + i0) * a.P;
-        const uint32_t stat = tc::su32(sm + M::oStat) + ss * 1024;
-        tc::bar_expect_tx(&st_full[ss], 1024);
-        win::bulk_load(stat, a.nlse + at, 512, &st_full[ss]);
-        win::bulk_load(stat + 512, a.delta + at, 512, &st_full[ss]);
+        load_stat(k);
       }
       // whatever is still in flight lands before the CTA leaves
       tc::bar_wait(&kv_full, 0, kDrainNs);
@@ -811,15 +826,23 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const uint32_t tA = tm + 256 + D * g + lane_off;
     const float nan = __int_as_float(0x7fc00000);
     if (it.slot >= 0) {
-      float4* o = reinterpret_cast<float4*>(a.part + ((it.slot * 2 + g) * 128 + r) * D);
+      float* o = a.part + ((it.slot * 2 + g) * 128 + (r & ~3)) * D + 4 * (lane & 3);
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float x[32];
         if (ok) tc::tmem_ld32(tA + 32 * q, x);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          o[8 * q + c] = ok ? make_float4(f * x[4 * c], f * x[4 * c + 1], f * x[4 * c + 2], f * x[4 * c + 3])
-                            : make_float4(nan, nan, nan, nan);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t u[4][4];                                  // four 16-byte pieces of row r, then one of four rows
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[c][k] = __float_as_uint(ok ? f * x[16 * h + 4 * c + k] : nan);
+          win::transpose4(u, lane);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(o + c * D + 32 * q + 16 * h) = make_uint4(u[c][0], u[c][1], u[c][2], u[c][3]);
+        }
       }
     } else if (!ok || n == 0) {
       const uint32_t v = ok ? 0u : kNaN2;
