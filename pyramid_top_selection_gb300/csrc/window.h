@@ -14,10 +14,11 @@ namespace win {
 
 // A kernel's dynamic shared memory, raised once per device (the attribute stays with the device's
 // context, and the call costs as much as a launch); `regs` registers a thread must have been compiled.
+// `wide_cluster`: clusters of more than 8 CTAs are launched.
 class Ready {
  public:
   template <class F>
-  int operator()(F* kernel, int bytes, int regs = 0) {
+  int operator()(F* kernel, int bytes, int regs = 0, bool wide_cluster = false) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -30,6 +31,7 @@ class Ready {
       if (f.numRegs < regs) return static_cast<int>(cudaErrorInvalidKernelImage);
     }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && wide_cluster) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
     return e;
   }

@@ -23,9 +23,16 @@
 //     value rows at tokens >= len, so that padding's values (NaN, say) do not meet P = 0.
 // TMEM: S (and P) of row tile t at 128 t, O at 256 + d t: all 512 columns at d = 128.
 // P is rounded to bf16 for the product (2^-8 relative at most); the sum l takes it unrounded.
+// With few rows (a short chunk against a long context) the items are fewer than the SMs. An item's key
+// tiles are then cut into 2, 4, 8 or 16 runs, one CTA each, the CTAs a cluster: each lays its O, maxima
+// and sums into its shared memory, and takes a share of the rows, which it reads from all of them and
+// adds up in their order (no workspace, no second launch). The join takes some 3.5 us, as long as three key tiles.
+// One token, 16 heads over 2 KV heads, 65536 keys: 68 us with 16 CTAs an item, 878 with one; 256 tokens
+// of 8 heads and 4096 keys 20.0 (8 CTAs) and 57; 5 key tiles 12.4 (8), 14.2 (4), 14.6 (1).
 // Every wait is bounded; one that gives up sets the CTA's abort flag, every role leaves, copies and
 // MMAs in flight are drained, and the rows of the items left are poisoned.
 #include <algorithm>
+#include <atomic>
 
 #include "device.cuh"
 #include "internal.h"
@@ -42,6 +49,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;                  // log2 growth of the maximum that O is rescaled for
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
 constexpr uint64_t kPatient = 1ull << 40;      // the item warp outwaits the others, whose giving up it sees
+
+constexpr int kJoinTiles = 3;                  // the join of a split item in key tiles
 
 template <int D>
 struct FwdSmem {
@@ -63,6 +72,7 @@ struct FwdArgs {
   int stall;
   int P, lp, tok;          // heads of a tile (P = 2^lp), tokens of a tile (128 / P)
   int n_tiles, n_heads, n_items;   // token tile pairs, (b, kv, head set) combinations
+  int splits;              // CTAs of an item (SPLIT)
 };
 
 // Work item w: 2 x tok tokens of P heads.
@@ -88,7 +98,8 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
   return it;
 }
 
-template <int D>
+// SPLIT: one item per cluster of a.splits CTAs; otherwise a.splits is 1 and the CTAs are persistent.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kmap32,
@@ -129,6 +140,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   __syncthreads();
   tc::after_sync();
   const uint32_t tm = tmem_base;
+  const uint32_t dQ = win::desc_lo(aQ), dK = win::desc_lo(aKV), dV = win::desc_mn_lo(aKV, 128 * 128);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
   // positions of row tile t of an item: [p0, p1)
@@ -137,6 +149,12 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   auto get = [&](int k) { return win::ring_get(s_items, k, &s_abort, a.wait_ns); };
   const int sink_tiles = (s.sinks + 127) >> 7;
   auto uses = [&](const win::Item& it, int t, int j) { return j <= it.last[t] && (j >= it.first[t] || j < sink_tiles); };
+  // the CTA's key tiles [j0, j1) of an item
+  const int rank = SPLIT ? static_cast<int>(win::cluster_rank()) : 0;
+  auto run_begin = [&](const win::Item& it) { return SPLIT ? it.n * rank / a.splits : 0; };
+  auto run_end = [&](const win::Item& it) { return SPLIT ? it.n * (rank + 1) / a.splits : it.n; };
+  float m = neg_inf(), l = 0.f;                              // softmax threads: their row's maximum and sum
+  int done = 0;                                              // key tiles that went into them
 
   if (warp >= 8) {
     win::regs_dec<88>();
@@ -183,9 +201,10 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           __syncwarp();
           return true;
         };
-        if (it.n == 0) continue;
-        ok = load_q(0) && load_kv(0, &kmap, &kmap32) && load_q(1) && load_kv(0, &vmap, &vmap32);
-        for (int j = 1; ok && j < it.n; ++j) ok = load_kv(128 * j, &kmap, &kmap32) && load_kv(128 * j, &vmap, &vmap32);
+        const int j0 = run_begin(it), j1 = run_end(it);
+        if (j0 == j1) continue;
+        ok = load_q(0) && load_kv(128 * j0, &kmap, &kmap32) && load_q(1) && load_kv(128 * j0, &vmap, &vmap32);
+        for (int j = j0 + 1; ok && j < j1; ++j) ok = load_kv(128 * j, &kmap, &kmap32) && load_kv(128 * j, &vmap, &vmap32);
       }
       // whatever is still in flight lands before the CTA leaves
       for (int k = max(0, n_kv - M::NST); k < n_kv; ++k) tc::bar_wait(&kv_full[k % M::NST], (k / M::NST) & 1, kDrainNs);
@@ -194,9 +213,9 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     } else if (warp == 10) {
       // ---------------------------------------------------------------- items, decoded ahead of the other roles
       if (lane == 0) {
-        const int rounds = win::rounds_of(a.n_items);
+        const int rounds = SPLIT ? 1 : win::rounds_of(a.n_items);
         for (int k = 0; k <= rounds; ++k) {
-          const int64_t w = k < rounds ? win::item_of(k, a.n_items) : -1;
+          const int64_t w = k == rounds ? -1 : SPLIT ? blockIdx.x / a.splits : win::item_of(k, a.n_items);
           win::Item it{};
           if (w >= 0) it = fwd_item(a, static_cast<int>(w));
           else it.n = -1;                                    // only the last round can miss a CTA
@@ -212,11 +231,11 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       bool issued = false, ok = true;
       for (int i = 0; ok; ++i) {
         const win::Item it = get(i);
-        const int n = it.n;
-        if (n < 0) break;
-        if (n == 0) continue;
+        if (it.n < 0) break;
+        const int j0 = run_begin(it), j1 = run_end(it);
+        if (j0 == j1) continue;
         if (a.stall && !wait(&never, 0)) { ok = false; break; }
-        // key tile j is load n_kv + 2 j of the ring, its values are the one after
+        // key tile j is load n_kv + 2 (j - j0) of the ring, its values are the one after
         auto landed = [&](int k) { return wait(&kv_full[k % M::NST], (k / M::NST) & 1); };
         // S of row tile t from the key tile of load k; `last` of the row tile's, `free` the load's last use.
         // What S needs is waited for while the product before it still runs.
@@ -224,7 +243,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
           tc::after_sync();
           if (leader) {
-            win::product_ss<D>(tm + 128 * t, win::desc_lo(aQ + t * M::TILE), win::desc_lo(aKV + k % M::NST * M::TILE));
+            win::product_ss<D>(tm + 128 * t, dQ + t * (M::TILE >> 4), dK + k % M::NST * (M::TILE >> 4));
             tc::commit(&s_full[t]);
             if (free) tc::commit(&kv_empty[k % M::NST]);
             if (last) tc::commit(&q_empty[t]);
@@ -237,8 +256,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           if (!wait(&p_full[t], n_p[t] & 1)) return false;
           tc::after_sync();
           if (leader) {
-            win::product_ts<D, 128>(tm + 256 + D * t, tm + 128 * t, win::desc_mn_lo(aKV + k % M::NST * M::TILE, 128 * 128),
-                               accumulate);
+            win::product_ts<D, 128>(tm + 256 + D * t, tm + 128 * t, dV + k % M::NST * (M::TILE >> 4), accumulate);
             tc::commit(&pv_done[t]);
             if (free) tc::commit(&kv_empty[k % M::NST]);
           }
@@ -246,28 +264,29 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           ++n_p[t];
           return true;
         };
-        bool has0 = uses(it, 0, 0), has1 = uses(it, 1, 0), acc0 = false, acc1 = false;
+        bool has0 = uses(it, 0, j0), has1 = uses(it, 1, j0), acc0 = false, acc1 = false;
         issued = true;
         ok = landed(n_kv) && (it.last[0] < 0 || wait(&q_full[0], n_q[0]++ & 1));
-        if (ok && has0) ok = issue_s(0, n_kv, it.last[0] == 0, !has1);
+        if (ok && has0) ok = issue_s(0, n_kv, it.last[0] == j0, !has1);
         ok = ok && (it.last[1] < 0 || wait(&q_full[1], n_q[1]++ & 1));
-        if (ok && has1) ok = issue_s(1, n_kv, it.last[1] == 0, true);
+        if (ok && has1) ok = issue_s(1, n_kv, it.last[1] == j0, true);
         ok = ok && landed(n_kv + 1);
-        for (int j = 0; ok && j < n; ++j) {
-          const int k = n_kv + 2 * j + 1;
-          const bool next0 = uses(it, 0, j + 1), next1 = uses(it, 1, j + 1);
+        for (int j = j0; ok && j < j1; ++j) {
+          const int k = n_kv + 2 * (j - j0) + 1;
+          const bool more = !SPLIT || j + 1 < j1;            // (an item's last tile has no next one anyway)
+          const bool next0 = more && uses(it, 0, j + 1), next1 = more && uses(it, 1, j + 1);
           if (has0 && !issue_pv(0, k, acc0, !has1)) { ok = false; break; }
-          if (j + 1 < n && !landed(k + 1)) { ok = false; break; }
+          if (j + 1 < j1 && !landed(k + 1)) { ok = false; break; }
           if (next0 && !issue_s(0, k + 1, it.last[0] == j + 1, !next1)) { ok = false; break; }
           if (has1 && !issue_pv(1, k, acc1, true)) { ok = false; break; }
-          if (j + 1 < n && !landed(k + 2)) { ok = false; break; }
+          if (j + 1 < j1 && !landed(k + 2)) { ok = false; break; }
           if (next1 && !issue_s(1, k + 1, it.last[1] == j + 1, true)) { ok = false; break; }
           acc0 |= has0;
           acc1 |= has1;
           has0 = next0;
           has1 = next1;
         }
-        n_kv += 2 * n;
+        n_kv += 2 * (j1 - j0);
       }
       if (issued) {
         if (leader) tc::commit(&drain);
@@ -286,18 +305,22 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     int i = 0;
     for (int n = 0;; ++i, n_kv += 2 * n) {
       const win::Item it = get(i);
-      n = it.n;
-      if (n < 0) break;
+      if (it.n < 0) break;
+      const int j0 = run_begin(it), j1 = run_end(it);
+      n = j1 - j0;
       const int L = it.L;
       const win::KeyList kl(it.lo, it.SP);
       const int p0 = tile_p0(it, t), p1 = tile_p1(it, t);
       const int j_first = t ? it.first[1] : it.first[0], j_last = t ? it.last[1] : it.last[0];
       const int p = p0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
       const bool row = p < p1 && p < L;
-      float m = neg_inf(), l = 0.f;
-      int done = 0;
+      if (!SPLIT) {
+        m = neg_inf();
+        l = 0.f;
+        done = 0;
+      }
       bool ok = true;
-      for (int j = 0; j < n; ++j) {
+      for (int j = j0; j < j1; ++j) {
         const int v0 = 128 * j;
         if (j > j_last || (j < j_first && j >= sink_tiles)) continue;
         ok = wait(&s_full[t], n_s & 1);
@@ -394,7 +417,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         // padding's values (only the last tile can reach past the sequence) become zero before this row
         // tile's product; the other row tile writes the same zeros before its own
         if (L < s.N && kl.key(v0 + 127) >= L) {
-          const int k = n_kv + 2 * j + 1, st = k % M::NST;
+          const int k = n_kv + 2 * (j - j0) + 1, st = k % M::NST;
           ok = wait(&kv_full[st], (k / M::NST) & 1);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           if (v0 + r >= kl.SP && kl.key(v0 + r) >= L)
@@ -419,6 +442,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!__all_sync(0xffffffffu, ok)) break;
         tc::after_sync();
       }
+      if (SPLIT) continue;                                   // the cluster's results are joined below
       if (p < p1)
         a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + p - s.off] = l == 0.f ? neg_inf() : (m + log2f(l)) * kLn2;
       const float inv = 1.f / l;                             // l = 0: an empty row, whose output is 0
@@ -458,7 +482,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       }
     }
     if (lane == 0) tc::bulk_wait<0>();
-    if (aborted()) {                                         // the rows of the item at hand and of those left
+    if (!SPLIT && aborted()) {                               // the rows of the item at hand and of those left
       for (; i < win::rounds_of(a.n_items); ++i) {
         const int64_t w = win::item_of(i, a.n_items);
         if (w < 0) break;
@@ -471,6 +495,84 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       }
     }
   }
+  if (SPLIT) {
+    // ------------------------------------------------------------------ join: every CTA lays its O and (m, l)
+    // into shared memory, over the key tiles that nothing reads any more, and takes 1 / splits of the rows
+    tc::before_sync();
+    __syncthreads();
+    tc::after_sync();
+    const win::Item it = fwd_item(a, blockIdx.x / a.splits);
+    float* part = reinterpret_cast<float*>(sm + M::oKV);     // [256][D], a row's 16-byte pieces permuted by its number
+    float2* stat = reinterpret_cast<float2*>(sm + M::oStage);   // [256] (m, l)
+    constexpr int PC = D / 4;
+    if (warp < 8) {
+      stat[tid] = make_float2(m, l);
+      if (done)
+#pragma unroll 1
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t u[16];
+          win::tmem_ld16(tm + 256 + D * (warp >> 2) + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 16 * q, u);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            reinterpret_cast<uint4*>(part)[tid * PC + ((4 * q + c) ^ (tid & (PC - 1)))] =
+                make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+        }
+    }
+    __syncwarp();
+    win::cluster_sync();
+    if (warp < 8) {
+      // a warp's 32 / splits rows x splits CTAs are 32 pairs: one a lane for the statistics, then all of
+      // them (half of them, at d = 64) in turn for a lane's four columns, eight reads under way at a time
+      const int n = a.splits, ln = __ffs(n) - 1, x0 = (rank * 8 + warp) * (32 >> ln);
+      const float2 ml = win::ld_cluster_f2(stat + x0 + (lane >> ln), lane & (n - 1));
+      const bool bad = __any_sync(0xffffffffu, win::ld_cluster_u32(&s_abort, lane & (n - 1)) != 0);
+      float top = ml.x;
+      for (int d = n >> 1; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      float f = ml.y == 0.f ? 0.f : tc::ex2(ml.x - top);     // (a row's NaN goes on)
+      float sum = f * ml.y;
+      for (int d = n >> 1; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      int64_t row = -1;                                      // (token, head) of the lane's pair
+      {
+        const int x = x0 + (lane >> ln), t = x >> 7, r = x & 127, p = tile_p0(it, t) + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
+        if (p < tile_p1(it, t)) {
+          row = (it.b * static_cast<int64_t>(s.Nq) + p - s.off) * s.Hq + h;
+          if ((lane & (n - 1)) == 0)
+            a.lse[(static_cast<int64_t>(it.b) * s.Hq + h) * s.Nq + p - s.off] =
+                bad ? __int_as_float(0x7fc00000) : sum == 0.f ? neg_inf() : (top + log2f(sum)) * kLn2;
+        }
+      }
+      f *= bad ? __int_as_float(0x7fc00000) : sum == 0.f ? 0.f : 1.f / sum;
+      constexpr int HALF = 32 / PC;                          // rows at a time
+      const int pc = lane % PC, e0 = lane / PC * (32 / HALF);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int e = e0; e < e0 + 32 / HALF; e += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int x = x0 + ((e + k) >> ln);
+          const float fc = __shfl_sync(0xffffffffu, f, e + k);
+          v[k] = make_float4(fc, fc, fc, fc);                // zeros: nothing seen there, perhaps nothing written
+          if (fc != 0.f && !bad) v[k] = win::ld_cluster_f4(part + x * D + ((pc ^ (x & (PC - 1))) << 2), (e + k) & (n - 1));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float fc = __shfl_sync(0xffffffffu, f, e + k);
+          const int64_t to = __shfl_sync(0xffffffffu, row, e + k);
+          o.x += fc * v[k].x;
+          o.y += fc * v[k].y;
+          o.z += fc * v[k].z;
+          o.w += fc * v[k].w;
+          if (((e + k + 1) & (n - 1)) == 0) {                // the row's last CTA
+            if (to >= 0) *reinterpret_cast<uint2*>(a.O + to * D + 4 * pc) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    win::cluster_sync();                                     // nobody leaves while its results are read
+  }
   tc::before_sync();
   __syncthreads();
   if (tid == 0 && s_abort && a.status) atomicOr(a.status, PISA_STATUS_TIMEOUT);
@@ -480,13 +582,69 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   }
 }
 
-template <int D>
-int fwd_launch(const FwdArgs& a, const CUtensorMap* m, int grid, cudaStream_t st) {
+// The cluster launch of `splits` CTAs an item.
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  ClusterLaunch(int grid, int splits, int smem, cudaStream_t st) {
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(splits);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  ClusterLaunch(const ClusterLaunch&) = delete;
+};
+
+// The softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread.
+template <int D, bool SPLIT>
+int fwd_ready() {
   static win::Ready ready;
-  // the softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread
-  if (int e = ready(window_fwd_kernel<D>, FwdSmem<D>::bytes, 168)) return e;
+  return ready(window_fwd_kernel<D, SPLIT>, FwdSmem<D>::bytes, 168, SPLIT);
+}
+
+// CTAs of an item, one of 1, 2, 4, 8, 16: the number with the fewest key tiles for the longest run,
+// the join counted as kJoinTiles of them, among those whose clusters all run at one time.
+template <int D>
+int fwd_splits(int64_t items, int64_t tiles) {
+  static std::atomic<int> known[64][5];                      // clusters of 2^k CTAs at one time + 1, per device
+  int best = 1, dev = 0;
+  if (items * 2 > sm_count() || tiles < kJoinTiles + 2) return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64 || fwd_ready<D, true>()) return 1;
+  for (int k = 1; k <= 4; ++k) {
+    const int n = 1 << k;
+    if (items * n > sm_count()) break;
+    const int64_t cost = (tiles + n - 1) / n + kJoinTiles, now = (tiles + best - 1) / best + (best > 1 ? kJoinTiles : 0);
+    if (cost >= now) continue;
+    int at_once = known[dev][k].load(std::memory_order_relaxed) - 1;
+    if (at_once < 0) {
+      ClusterLaunch c(n, n, FwdSmem<D>::bytes, nullptr);
+      if (cudaOccupancyMaxActiveClusters(&at_once, window_fwd_kernel<D, true>, &c.cfg) != cudaSuccess) {
+        cudaGetLastError();
+        at_once = 0;
+      }
+      known[dev][k].store(at_once + 1, std::memory_order_relaxed);
+    }
+    if (items <= at_once) best = n;
+  }
+  return best;
+}
+
+template <int D>
+int fwd_launch(FwdArgs& a, int64_t tiles, const CUtensorMap* m, cudaStream_t st) {
+  a.splits = fwd_splits<D>(a.n_items, tiles);
   ProfScope ps(st, "window_fwd");
-  window_fwd_kernel<D><<<grid, kThreads, FwdSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
+  if (a.splits > 1) {
+    ClusterLaunch c(a.n_items * a.splits, a.splits, FwdSmem<D>::bytes, st);
+    return cudaLaunchKernelEx(&c.cfg, window_fwd_kernel<D, true>, a, m[0], m[1], m[2], m[3], m[4], m[5]);
+  }
+  if (int e = fwd_ready<D, false>()) return e;
+  window_fwd_kernel<D, false><<<std::min(a.n_items, sm_count()), kThreads, FwdSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3],
+                                                                                                     m[4], m[5]);
   return cudaGetLastError();
 }
 
@@ -525,8 +683,10 @@ int launch_window_fwd(const WinDims& s, const void* Q, const void* K, const void
     cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
     if (e != cudaSuccess) return e;
   }
-  const int grid = static_cast<int>(std::min<int64_t>(items, sm_count()));
-  return s.d == 128 ? fwd_launch<128>(a, m, grid, st) : fwd_launch<64>(a, m, grid, st);
+  // key tiles of the longest item
+  const int64_t cols = std::min<int64_t>(s.N, s.window + 2ll * a.tok - 1) + (s.sinks + 31) / 32 * 32;
+  const int64_t tiles = (cols + 127) / 128;
+  return s.d == 128 ? fwd_launch<128>(a, tiles, m, st) : fwd_launch<64>(a, tiles, m, st);
 }
 
 }  // namespace pisa

@@ -219,6 +219,40 @@ __device__ __forceinline__ Item ring_get(ItemRing& q, int k, int* abort_flag, ui
   return it;
 }
 
+// Clusters: this CTA's number, a barrier over all threads of all its CTAs, and reads of a shared
+// variable as CTA `rank` has it.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::su32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(const void* p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(const void* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect() {
   uint32_t p;
@@ -227,10 +261,11 @@ __device__ __forceinline__ bool elect() {
 }
 
 // Shared-memory matrix descriptors by their low word (address, MN stride), the part that changes: an
-// MMA's operands then cost one addition each to form (tc.cuh has the fields).
+// MMA's operands then cost one addition each to form (tc.cuh has the fields). In a cluster an address
+// carries the CTA's number above its 18 bits of offset.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
-__device__ __forceinline__ uint32_t desc_mn_lo(uint32_t saddr, uint32_t mn_stride) { return (saddr >> 4) | ((mn_stride >> 4) << 16); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr & 0x3ffff) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn_lo(uint32_t saddr, uint32_t mn_stride) { return ((saddr & 0x3ffff) >> 4) | ((mn_stride >> 4) << 16); }
 
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(

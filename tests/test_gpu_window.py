@@ -142,6 +142,55 @@ def test_long_sequences_on_sampled_rows(Hq, Hkv, d, window, sinks):
             check("dV", got["dV"][0, j0:j1, kv], dv, dvt + H * dv.abs())
 
 
+@pytest.mark.parametrize("B,Nq,N,Hq,Hkv,d,window,sinks,lens", [
+    (1, 1, 9000, 16, 2, 128, 9000, 0, None),               # two items: sixteen CTAs each
+    (1, 3, 5001, 5, 1, 64, 4000, 40, None),
+    (3, 40, 4100, 4, 1, 128, 2500, 4, [4100, 0, 4071]),    # rows, and a whole sequence, that see nothing
+    (2, 300, 2200, 8, 2, 64, 1500, 300, [2200, 2050]),     # sinks of several key tiles
+    (1, 65, 700, 4, 2, 128, 640, 0, [650]),
+    (1, 513, 1800, 8, 4, 64, 900, 1, None),
+    (2, 1, 1300, 4, 4, 128, 1024, 200, [1300, 1299]),      # the only query of the second sequence is padding
+])
+def test_few_rows_against_many_keys(B, Nq, N, Hq, Hkv, d, window, sinks, lens):
+    # an item's keys are cut among a cluster's CTAs, whose sums are joined
+    Q, K, V, _ = _inputs(B, Nq, N, Hq, Hkv, d, lens=lens, seed=N)
+    K[:, N // 2] *= 3                                      # the runs' maxima differ
+    got = _run(Q, K, V, None, window, sinks, lens)
+    again = _run(Q, K, V, None, window, sinks, lens)
+    want, tol = attention(Q, K, V, window, sinks, lens)
+    for n in got:
+        check(n, got[n], want[n], tol[n])
+        assert torch.equal(got[n], again[n])
+
+
+def test_split_item_keeps_nan_and_reports_waits(request):
+    Q, K, V, _ = _inputs(1, 70, 4000, 2, 1, 128, seed=2)
+    Q[0, 33, 1] = math.nan                                 # one row's own NaN, in every CTA's part
+    got = _run(Q, K, V, None, 3500, 0)
+    bad = got["O"].isnan().any(-1)[0]
+    assert bool(bad[33, 1]) and int(bad.sum()) == 1 and bool(got["lse"][0, 1, 33].isnan())
+    request.getfixturevalue("stalled")
+    s = pisa.window_shape_of(Q, K, V, 3500, 0)
+    ws = pisa.window_workspace(s, pisa.WINDOW_FWD, Q.device)
+    O, lse = pisa.window_attn_fwd(Q, K, V, s, ws=ws)
+    assert pisa.workspace_status(ws) & pisa.STATUS_TIMEOUT
+    assert bool(O.isnan().all()) and bool(lse.isnan().all())
+
+
+def test_split_item_captured():
+    Q, K, V, _ = _inputs(1, 16, 6000, 8, 1, 64, seed=8)
+    s = pisa.window_shape_of(Q, K, V, 6000, 0)
+    want = [x.clone() for x in pisa.window_attn_fwd(Q, K, V, s)]
+    O, lse = torch.empty_like(Q), torch.empty(1, 8, 16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pisa.window_attn_fwd(Q, K, V, s, out=O, lse=lse)
+    for _ in range(3):
+        O.zero_()
+        g.replay()
+        assert torch.equal(O, want[0]) and torch.equal(lse, want[1])
+
+
 def test_same_call_gives_same_bits():
     Q, K, V, dO = _inputs(2, 900, 900, 8, 2, 128, seed=1)
     a, b = _run(Q, K, V, dO, 250, 40), _run(Q, K, V, dO, 250, 40)
