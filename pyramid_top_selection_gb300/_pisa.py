@@ -367,8 +367,8 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
         raise ValueError(f"{name} must be [B, N, H, d] (got {tuple(t.shape)})")
     B, N, H, d = t.shape
     sb, sn, sh, sd = t.stride()
-    step = sn if N > 1 else sb
-    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (N > 1 and B > 1 and sb != N * sn):
+    step = sn if N > 1 else sb if B > 1 else H * d
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (N > 1 and B > 1 and sb != N * sn) or not H * d <= step < 1 << 31:
         raise ValueError(f"{name} must have contiguous heads and evenly spaced tokens (strides {tuple(t.stride())})")
     return step if B * N > 1 else 0
 
@@ -378,8 +378,14 @@ def _need_tokens(t, size, stride: int, dev, name: str) -> None:
         raise ValueError(f"{name} must be a bfloat16 tensor {tuple(size)} on {dev} "
                          f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
     if stride or not t.is_contiguous():
-        if size[0] * size[1] > 1 and (_token_stride(t, name) or size[2] * size[3]) != (stride or size[2] * size[3]):
+        step, row = _token_stride(t, name), size[2] * size[3]
+        if size[0] * size[1] > 1 and (step or row) != (stride or row):
             raise ValueError(f"{name} has strides {tuple(t.stride())}, the shape says {stride} elements a token")
+
+
+def _need_ws(ws, dev) -> None:
+    if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev} (got {ws.dtype}, {ws.device})")
 
 
 def make_window_shape(B, Nq, N, Hq, Hkv, d, window, sinks=0, scale=0.0, q_stride=0, k_stride=0,
@@ -431,6 +437,8 @@ def window_attn_fwd(Q, K, V, shape: WindowShape, lens=None, ws=None, out=None, l
         lse = torch.empty((shape.B, shape.Hq, shape.Nq), dtype=torch.float32, device=dev)
     else:
         _need_shaped(lse, torch.float32, (shape.B, shape.Hq, shape.Nq), dev, "lse")
+    if ws is not None:
+        _need_ws(ws, dev)
     _on(dev, lib().pisa_window_attn_fwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(lens),
         out.data_ptr(), lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
@@ -449,6 +457,7 @@ def window_attn_bwd(Q, K, V, O, lse, dO, shape: WindowShape, lens=None, ws=None)
     dV = torch.empty_like(dK)
     if ws is None:
         ws = window_workspace(shape, WINDOW_BWD, dev)
+    _need_ws(ws, dev)
     _on(dev, lib().pisa_window_attn_bwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
         lse.data_ptr(), dO.data_ptr(), _ptr(lens), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(),
         ws.numel())
@@ -486,6 +495,8 @@ def window_decode_step(shape: WindowDecodeShape, pos, Kcache, Vcache, q, k_new, 
         _need_shaped(lse, torch.float32, (B, shape.Hq), dev, "lse")
     if status is None:
         status = torch.zeros(4, dtype=torch.int32, device=dev)
+    elif status.dtype is not torch.int32 or status.device != dev or status.numel() < 1:
+        raise ValueError(f"status must be an int32 tensor on {dev} (got {status.dtype}, {status.device})")
     _on(dev, lib().pisa_window_decode_step, ctypes.byref(shape), pos.data_ptr(), Kcache.data_ptr(), Vcache.data_ptr(),
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), o.data_ptr(), lse.data_ptr(), status.data_ptr())
     return o, lse, status
@@ -612,6 +623,7 @@ def qk_norm_rope_bwd(Q, K, dQr, dKr, inv_freq, shape: RopeShape, q_weight=None, 
         dwk = torch.empty(shape.d, dtype=torch.float32, device=dev)
     if ws is None:
         ws = qk_norm_rope_workspace(shape, dev)
+    _need_ws(ws, dev)
     _on(dev, lib().pisa_qk_norm_rope_bwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), dQr.data_ptr(),
         dKr.data_ptr(), _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(pos), dQ.data_ptr(), dK.data_ptr(),
         _ptr(dwq), _ptr(dwk), ws.data_ptr(), ws.numel())

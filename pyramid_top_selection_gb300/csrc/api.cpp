@@ -173,6 +173,26 @@ int check_stride(int32_t stride, int H, int d, const char* name, int64_t* out) {
   return PISA_OK;
 }
 
+// A buffer's bytes; `tokens` rows of `row` elements, `stride` elements apart.
+struct Span {
+  const char* name;
+  uintptr_t begin, end;
+  Span(const char* n, const void* p, int64_t tokens, int64_t stride, int64_t row, int bytes = 2)
+      : name(n), begin(reinterpret_cast<uintptr_t>(p)),
+        end(p ? begin + static_cast<uintptr_t>(((tokens - 1) * stride + row) * bytes) : begin) {}
+};
+
+// No output may share bytes with an input; with `in_place`, the k-th output may be the k-th input.
+template <int NIN, int NOUT>
+int check_apart(const Span (&in)[NIN], const Span (&out)[NOUT], bool in_place = false) {
+  for (int o = 0; o < NOUT; ++o)
+    for (int i = 0; i < NIN; ++i) {
+      if (in_place && i == o && in[i].begin == out[o].begin) continue;
+      if (out[o].begin < in[i].end && in[i].begin < out[o].end) return fail(PISA_EINVAL, "%s overlaps %s", out[o].name, in[i].name);
+    }
+  return PISA_OK;
+}
+
 float scale_or_default(float scale, int d) { return scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d)); }
 
 int window_dims(const pisa_window_shape_t* s, pisa::WinDims* o) {
@@ -484,6 +504,11 @@ int pisa_window_attn_fwd(const pisa_window_shape_t* shape, const void* Q, const 
   PISA_CHECK(check_ptr(O, "O"));
   PISA_CHECK(check_ptr(lse, "lse"));
   if (ws || ws_bytes) PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_FWD), ws, ws_bytes));
+  const int64_t tq = static_cast<int64_t>(d.B) * d.Nq, tk = static_cast<int64_t>(d.B) * d.N;
+  const int64_t q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
+  const Span in[] = {{"Q", Q, tq, d.qs, q}, {"K", K, tk, d.ks, kv}, {"V", V, tk, d.vs, kv}};
+  const Span out[] = {{"O", O, tq, q, q}, {"lse", lse, tq, d.Hq, d.Hq, 4}};
+  PISA_CHECK(check_apart(in, out));
   return cuda_rc(pisa::launch_window_fwd(d, Q, K, V, len, O, lse, static_cast<char*>(ws), stream),
                  "pisa_window_attn_fwd");
 }
@@ -498,6 +523,13 @@ int pisa_window_attn_bwd(const pisa_window_shape_t* shape, const void* Q, const 
   for (int k = 0; k < 9; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
   PISA_CHECK(check_ptr(len, "len", true));
   PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_BWD), ws, ws_bytes));
+  const int64_t tq = static_cast<int64_t>(d.B) * d.Nq, tk = static_cast<int64_t>(d.B) * d.N;
+  const int64_t q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
+  const Span spans[] = {{"Q", Q, tq, d.qs, q}, {"K", K, tk, d.ks, kv}, {"V", V, tk, d.vs, kv}, {"O", O, tq, q, q},
+                        {"dO", dO, tq, q, q}, {"lse", lse, tq, d.Hq, d.Hq, 4}};
+  const Span out[] = {{"dQ", dQ, tq, q, q}, {"dK", dK, tk, kv, kv}, {"dV", dV, tk, kv, kv},
+                      {"workspace", ws, 1, 0, static_cast<int64_t>(window_ws_bytes(d, PISA_WINDOW_BWD)), 1}};
+  PISA_CHECK(check_apart(spans, out));
   return cuda_rc(pisa::launch_window_bwd(d, Q, K, V, O, lse, dO, len, dQ, dK, dV, static_cast<char*>(ws), stream),
                  "pisa_window_attn_bwd");
 }
@@ -530,6 +562,10 @@ int pisa_qk_norm_rope(const pisa_rope_shape_t* shape, const void* Q, const void*
   PISA_CHECK(check_ptr(Kr, "Kr"));
   if ((Qr == Q && d.qs != static_cast<int64_t>(d.Hq) * d.d) || (Kr == K && d.ks != static_cast<int64_t>(d.Hkv) * d.d))
     return fail(PISA_EINVAL, "in place needs a contiguous Q and K");
+  const int64_t t = static_cast<int64_t>(d.B) * d.N, q = static_cast<int64_t>(d.Hq) * d.d, k = static_cast<int64_t>(d.Hkv) * d.d;
+  const Span in[] = {{"Q", Q, t, d.qs, q}, {"K", K, t, d.ks, k}};
+  const Span out[] = {{"Qr", Qr, t, q, q}, {"Kr", Kr, t, k, k}};
+  PISA_CHECK(check_apart(in, out, true));
   return cuda_rc(pisa::launch_rope(d, Q, K, inv_freq, q_weight, k_weight, pos, Qr, Kr, stream), "pisa_qk_norm_rope");
 }
 
@@ -557,6 +593,10 @@ int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const v
   if (!d.norm && (dq_weight || dk_weight)) return fail(PISA_EINVAL, "norm=0 has no weight gradients");
   if (dQ == Q || dK == K) return fail(PISA_EINVAL, "dQ and dK must not be Q and K");
   PISA_CHECK(check_ws_bytes(pisa::rope_bwd_ws(d), ws, ws_bytes));
+  const int64_t t = static_cast<int64_t>(d.B) * d.N, q = static_cast<int64_t>(d.Hq) * d.d, k = static_cast<int64_t>(d.Hkv) * d.d;
+  const Span grads[] = {{"dQr", dQr, t, q, q}, {"dKr", dKr, t, k, k}, {"Q", Q, t, d.qs, q}, {"K", K, t, d.ks, k}};
+  const Span out[] = {{"dQ", dQ, t, q, q}, {"dK", dK, t, k, k}};
+  PISA_CHECK(check_apart(grads, out, true));
   return cuda_rc(pisa::launch_rope_bwd(d, Q, K, dQr, dKr, inv_freq, q_weight, k_weight, pos, dQ, dK, dq_weight,
                                        dk_weight, static_cast<char*>(ws), stream),
                  "pisa_qk_norm_rope_bwd");

@@ -140,6 +140,66 @@ def test_rope_arguments_refused():
              A, b.value - 1, None)
 
 
+def test_overlapping_buffers_refused():
+    # 100 tokens of 2 x 64 and 1 x 64 bf16: 25600 and 12800 bytes; a fused projection interleaves its slices
+    L = pisa.lib()
+    q, k = 25600, 12800
+    s = ctypes.byref(pisa.make_window_shape(1, 100, 100, 2, 1, 64, 10))
+    far = [A + n * (1 << 20) for n in range(12)]
+    for out in (far[0], far[0] + q - 16, far[1] + k - 16, far[2] - q + 16):
+        _refused(L.pisa_window_attn_fwd, _pisa.PISA_EINVAL, "O overlaps", s, *far[:3], None, out, far[5], None, 0, None)
+    _refused(L.pisa_window_attn_fwd, _pisa.PISA_EINVAL, "lse overlaps K", s, *far[:3], None, far[4], far[1], None, 0, None)
+    for j, n in enumerate(["dQ", "dK", "dV", "workspace"]):
+        out = far[6:10]
+        for i, m in enumerate(["Q", "K", "V", "O", "lse", "dO"]):
+            _refused(L.pisa_window_attn_bwd, _pisa.PISA_EINVAL, f"{n} overlaps {m}", s, *far[:6], None,
+                     *out[:j], far[i], *out[j + 1:], 1 << 19, None)
+    fused = ctypes.byref(pisa.make_window_shape(1, 100, 100, 2, 1, 64, 10, q_stride=256, k_stride=256, v_stride=256))
+    _refused(L.pisa_window_attn_fwd, _pisa.PISA_EINVAL, "O overlaps", fused, A, A + 256, A + 384, None, A + 99 * 512, far[5],
+             None, 0, None)
+    r = ctypes.byref(pisa.make_rope_shape(1, 100, 2, 1, 64, 64))
+    _refused(L.pisa_qk_norm_rope, _pisa.PISA_EINVAL, "Kr overlaps Q", r, far[0], far[1], far[2], None, None, None, far[3],
+             far[0], None)
+    _refused(L.pisa_qk_norm_rope, _pisa.PISA_EINVAL, "Qr overlaps Q", r, far[0], far[1], far[2], None, None, None, far[0] + 16,
+             far[4], None)
+    _refused(L.pisa_qk_norm_rope_bwd, _pisa.PISA_EINVAL, "dK overlaps dQr", r, *far[:5], None, None, None, far[6], far[2],
+             None, None, far[8], 1 << 19, None)
+
+
+def test_binding_refuses_expanded_and_far_apart_tokens():
+    # tokens that share memory, or lie 2^31 elements apart, have no stride the shape can hold
+    z = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16)
+    s = pisa.window_shape_of(z, z, z, 4, 1)
+    for bad in (z[:, :1].expand(2, 8, 4, 64), z[:1].expand(2, 8, 4, 64), z[:, :, :1].expand(2, 8, 4, 64),
+                z[:1, :1].expand(2, 1, 4, 64), z.as_strided((2, 8, 4, 64), (8 * 128, 128, 64, 1)),
+                z[:, :, :, :1].expand(2, 8, 4, 64),
+                torch.empty(1 << 33, dtype=torch.bfloat16, device="meta").as_strided((2, 1, 4, 64), (1 << 32, 256, 64, 1))):
+        with pytest.raises(ValueError, match="evenly spaced"):
+            pisa.window_shape_of(z, bad, z, 4)
+    with pytest.raises(ValueError, match="evenly spaced"):
+        pisa.window_attn_fwd(z, z[:, :1].expand(2, 8, 4, 64), z, s)
+    one = torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16)[..., :64]          # a single token with gaps between its heads
+    with pytest.raises(ValueError, match="evenly spaced"):
+        pisa.window_attn_fwd(one, one, one, pisa.make_window_shape(1, 1, 1, 4, 4, 64, 1))
+
+
+def test_binding_refuses_workspaces_and_status_words_elsewhere():
+    z = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16)
+    s = pisa.window_shape_of(z, z, z, 4, 1)
+    lse = torch.zeros(2, 4, 8)
+    for ws in (torch.zeros(1 << 16, dtype=torch.float32), torch.zeros(1 << 16, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="ws must"):
+            pisa.window_attn_fwd(z, z, z, s, ws=ws)
+        with pytest.raises(ValueError, match="ws must"):
+            pisa.window_attn_bwd(z, z, z, z, lse, z, s, ws=ws)
+        with pytest.raises(ValueError, match="ws must"):
+            pisa.qk_norm_rope_bwd(z, z, z, z, torch.zeros(32), pisa.rope_shape_of(z, z, 64), ws=ws)
+    with pytest.raises(ValueError, match="status must"):
+        pisa.window_decode_step(pisa.make_window_decode_shape(2, 8, 4, 4, 64, 4), torch.zeros(2, dtype=torch.int32), z, z,
+                                z[:, 0].contiguous(), z[:, 0].contiguous(), z[:, 0].contiguous(),
+                                status=torch.zeros(4))
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     z = torch.zeros(2, 8, 4, 64, dtype=torch.bfloat16)
     s = pisa.window_shape_of(z, z, z, 4, 1)
