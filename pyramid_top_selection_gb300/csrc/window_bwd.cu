@@ -102,6 +102,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
   const uint32_t aQ = tc::su32(sm + M::oQ), aO = tc::su32(sm + M::oO), aK = tc::su32(sm + M::oK), aV = tc::su32(sm + M::oV);
+  constexpr uint32_t kStage = M::TILE >> 4;                  // from one stage's descriptor to the next
 
   if (tid == 0) {
     tc::bar_init(&q_full, 1);
@@ -197,6 +198,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     // ------------------------------------------------------------------ MMA, S and dP (the warp
     // together, one lane issuing: operands stay in uniform registers)
     const bool leader = win::elect();
+    const uint32_t dQ = win::desc_lo(aQ), dO = win::desc_lo(aO), dK = win::desc_lo(aK), dV = win::desc_lo(aV);
     int n_q = 0, g = 0;                        // items, key tiles so far
     bool issued = false, ok = true;
     for (int i = 0; ok; ++i) {
@@ -213,7 +215,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         if (g >= 2 && !wait(&dq_done[g & 1], ((g >> 1) - 1) & 1)) return false;
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm + 128 * (g & 1), win::desc_lo(aQ), win::desc_lo(aK + st * M::TILE));
+          win::product_ss<D>(tm + 128 * (g & 1), dQ, dK + st * kStage);
           tc::commit(&s_full[g & 1]);
         }
         __syncwarp();
@@ -226,7 +228,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         if (!ok) break;
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm + 256, win::desc_lo(aO), win::desc_lo(aV + st * M::TILE));
+          win::product_ss<D>(tm + 256, dO, dV + st * kStage);
           tc::commit(&dp_full);
           tc::commit(&v_empty[st]);
           if (j + 1 == n) tc::commit(&q_empty);
@@ -243,6 +245,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   } else if (warp == 10) {
     // ------------------------------------------------------------------ MMA, dQ
     const bool leader = win::elect();
+    const uint32_t dK = win::desc_mn_lo(aK, 128 * 128);
     int n_q = 0, g = 0;
     bool issued = false, ok = true;
     for (int i = 0; ok; ++i) {
@@ -256,7 +259,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         tc::after_sync();
         issued = true;
         if (leader) {
-          win::product_ts<D, 64>(tm + 384, tm + 128 * (g & 1), win::desc_mn_lo(aK + st * M::TILE, 128 * 128), j > 0);
+          win::product_ts<D, 64>(tm + 384, tm + 128 * (g & 1), dK + st * kStage, j > 0);
           tc::commit(&dq_done[g & 1]);
           tc::commit(&k_empty[st]);
           if (j + 1 == n) tc::commit(&dq_last);
@@ -663,6 +666,9 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     // lane issuing). What a product needs is waited for while the one before it still runs.
     if (n > 0) {
       const bool leader = win::elect();
+      constexpr uint32_t kStage = M::TILE >> 4;              // from one stage's descriptor to the next
+      const uint32_t dK = win::desc_lo(aK), dV = win::desc_lo(aV), dQ = win::desc_lo(aQ), dO = win::desc_lo(aO),
+                     dQt = win::desc_mn_lo(aQ, 128 * 128), dOt = win::desc_mn_lo(aO, 128 * 128);   // as stored
       bool ok = wait(&kv_full, 0);
       if (ok && a.stall) ok = wait(&never, 0);
       const bool issued = ok;
@@ -672,7 +678,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (k > 0 && !wait(&dv_done, (k - 1) & 1)) return false;        // P^T has been read
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm, win::desc_lo(aK), win::desc_lo(aQ + sq * M::TILE));
+          win::product_ss<D>(tm, dK, dQ + sq * kStage);
           tc::commit(&s_full);
         }
         __syncwarp();
@@ -684,7 +690,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (k > 0 && !wait(&dk_done, (k - 1) & 1)) return false;        // dS^T has been read
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm + 128, win::desc_lo(aV), win::desc_lo(aO + so * M::TILE));
+          win::product_ss<D>(tm + 128, dV, dO + so * kStage);
           tc::commit(&dp_full);
         }
         __syncwarp();
@@ -696,7 +702,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!wait(&p_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D, 64>(tm + 256, tm, win::desc_mn_lo(aO + so * M::TILE, 128 * 128), k > 0);
+          win::product_ts<D, 64>(tm + 256, tm, dOt + so * kStage, k > 0);
           tc::commit(&dv_done);
           tc::commit(&o_empty[so]);
         }
@@ -709,7 +715,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!wait(&ds_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D, 64>(tm + 256 + D, tm + 128, win::desc_mn_lo(aQ + qk * M::TILE, 128 * 128), k > 0);
+          win::product_ts<D, 64>(tm + 256 + D, tm + 128, dQt + qk * kStage, k > 0);
           tc::commit(&dk_done);
           tc::commit(&q_empty[qk]);
         }

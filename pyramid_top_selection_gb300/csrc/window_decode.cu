@@ -16,8 +16,7 @@
 
 #include "device.cuh"
 #include "profile.h"
-#include "tc.cuh"
-#include "window.h"
+#include "window_tc.cuh"
 
 namespace pisa {
 
@@ -56,23 +55,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The same shared-memory variable in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::su32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-
 template <int D>
 struct DecodeSmem {
   static constexpr int ROW = D * 2;                              // bytes of a key
@@ -97,7 +79,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
   __shared__ Joined<D> s_join;
   const WinDecodeDims& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, p2 = lane & 3;
-  const int rank = static_cast<int>(cluster_rank());
+  const int rank = static_cast<int>(win::cluster_rank());
   const int kv = blockIdx.y / a.sets, set = blockIdx.y % a.sets, b = blockIdx.z;
   const int heads = min(kHeads, s.G - set * kHeads), h0 = kv * s.G + set * kHeads;
   const int p = a.pos[b];
@@ -257,20 +239,20 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
       s_join.l[h] = ll;
     }
   }
-  cluster_sync();
+  win::cluster_sync();
   for (int x = rank * 32 * kWarps + threadIdx.x; x < heads * D; x += splits * 32 * kWarps) {
     const int h = x / D;
     float mm = neg_inf(), ll = 0.f, oo = 0.f;
-    for (int c = 0; c < splits; ++c) mm = fmaxf(mm, ld_cluster(&s_join.m[h], c));
+    for (int c = 0; c < splits; ++c) mm = fmaxf(mm, win::ld_cluster_f(&s_join.m[h], c));
     for (int c = 0; c < splits; ++c) {
-      const float f = tc::ex2(ld_cluster(&s_join.m[h], c) - mm);
-      oo += f * ld_cluster(&s_join.o[h][x % D], c);
-      ll += f * ld_cluster(&s_join.l[h], c);
+      const float f = tc::ex2(win::ld_cluster_f(&s_join.m[h], c) - mm);
+      oo += f * win::ld_cluster_f(&s_join.o[h][x % D], c);
+      ll += f * win::ld_cluster_f(&s_join.l[h], c);
     }
     a.o[(static_cast<int64_t>(b) * s.Hq + h0 + h) * D + x % D] = __float2bfloat16_rn(oo / ll);
     if (x % D == 0 && a.lse) a.lse[static_cast<int64_t>(b) * s.Hq + h0 + h] = (mm + log2f(ll)) * kLn2;
   }
-  cluster_sync();                                                // nobody leaves while its results are read
+  win::cluster_sync();                                                // nobody leaves while its results are read
 }
 
 template <int D>

@@ -1,5 +1,5 @@
-// What the tensor-core kernels of the window attention share: bounded waits that sleep, register
-// moves between warpgroups, and the walk over a query tile's keys.
+// What the window attention's kernels share: bounded waits that sleep, register moves between warpgroups,
+// the walk over a query tile's keys, clusters, and tensor-core products from descriptors.
 #pragma once
 
 #include "tc.cuh"
@@ -238,6 +238,9 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank)
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
   return v;
+}
+__device__ __forceinline__ float ld_cluster_f(const float* p, uint32_t rank) {
+  return __uint_as_float(ld_cluster_u32(p, rank));
 }
 __device__ __forceinline__ float2 ld_cluster_f2(const void* p, uint32_t rank) {
   float2 v;
