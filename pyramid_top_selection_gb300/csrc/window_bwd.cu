@@ -84,7 +84,12 @@ __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
 // TMEM: S (and dS in its place) of key tile n at 128 (n & 1), dP at 256, dQ at 384. One MMA warp
 // issues dP(n) and the next tile's S, the other dQ += dS K as soon as dS is there, so that the
 // tensor cores have a product at hand while the softmax warps turn S and dP into dS. (The barriers of
-// dS and of dQ are two each, by the tile's parity: their waiters may be a tile apart.)
+// dP, dS and dQ are two each, by the tile's parity: their waiters may be a tile apart.)
+//
+// D is dO . O from the forward's O, whose rounding to bf16 a row with few keys feels (windows under
+// some 60 keys: dQ and dK 1.5 to 2 times as far from the exact ones as their own rounding to bf16 puts
+// them). An item of one or two key tiles, and so every short row, has all its dP in tensor memory at one
+// time, the second tile's where dQ will be: there D is the fp32 sum of P dP itself, and O is not read.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
@@ -93,11 +98,12 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   using M = DqSmem<D>;
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
-      s_full[2], dp_full, ds_full[2], dq_done[2], dq_last, dq_empty, st_full[2], st_empty[2], drain[2], never;
+      s_full[2], dp_full[2], d_full, ds_full[2], dq_done[2], dq_last, dq_empty, st_full[2], st_empty[2], drain[2], never;
   __shared__ win::ItemRing s_items;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   __shared__ float s_stat[2][2][128];        // per item (two at a time): -lse log2 e, D
+  __shared__ float s_sum[128];               // sums of P dP, columns 0 .. 63 (the others' take D's place)
 
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
@@ -117,7 +123,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     }
     tc::bar_init(&s_full[0], 1);
     tc::bar_init(&s_full[1], 1);
-    tc::bar_init(&dp_full, 1);
+    tc::bar_init(&dp_full[0], 1);
+    tc::bar_init(&dp_full[1], 1);
+    tc::bar_init(&d_full, 256);
     tc::bar_init(&ds_full[0], 256);
     tc::bar_init(&ds_full[1], 256);
     tc::bar_init(&dq_done[0], 1);
@@ -224,12 +232,14 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       ok = ok && issue_s(g);
       for (int j = 0; ok && j < n; ++j, ++g) {
         const int st = g % M::NV;
-        ok = wait(&v_full[st], (g / M::NV) & 1) && (g == 0 || wait(&ds_full[(g - 1) & 1], ((g - 1) >> 1) & 1));   // dP has been read
+        const bool aside = n == 2 && j == 1;   // dP(1) where dQ was, once the item before's has been read
+        ok = wait(&v_full[st], (g / M::NV) & 1) &&
+             (aside ? wait(&dq_empty, n_q & 1) : g == 0 || wait(&ds_full[(g - 1) & 1], ((g - 1) >> 1) & 1));   // dP has been read
         if (!ok) break;
         tc::after_sync();
         if (leader) {
-          win::product_ss<D>(tm + 256, dO, dV + st * kStage);
-          tc::commit(&dp_full);
+          win::product_ss<D>(tm + (aside ? 384 : 256), dO, dV + st * kStage);
+          tc::commit(&dp_full[g & 1]);
           tc::commit(&v_empty[st]);
           if (j + 1 == n) tc::commit(&q_empty);
         }
@@ -254,7 +264,8 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       if (n == 0) continue;
       for (int j = 0; ok && j < n; ++j, ++g) {
         const int st = g % M::NK;
-        ok = (j > 0 || wait(&dq_empty, (n_q & 1) ^ 1)) && wait(&ds_full[g & 1], (g >> 1) & 1);
+        ok = (j > 0 || wait(&dq_empty, (n_q & 1) ^ 1)) && wait(&ds_full[g & 1], (g >> 1) & 1) &&
+             (j > 0 || n != 2 || wait(&ds_full[(g + 1) & 1], ((g + 1) >> 1) & 1));   // dP(1) has been read, too
         if (!ok) break;
         tc::after_sync();
         issued = true;
@@ -297,7 +308,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       if (w1 >= 0) {
         const win::Item nx = dq_item(a, static_cast<int>(w1));
         const int64_t f = (static_cast<int64_t>(nx.b) * s.Nq + nx.t0) * s.Hq + nx.h0;
-        for (int r = lane; r < min(128, (s.Nq - nx.t0) * a.P); r += 32)
+        for (int r = lane; r < (nx.n > 2 ? min(128, (s.Nq - nx.t0) * a.P) : 0); r += 32)
 #pragma unroll
           for (int c = 0; c < D; c += 64) {
             const int64_t at = (f + static_cast<int64_t>(r >> a.lp) * s.Hq + (r & (a.P - 1))) * D + c;
@@ -310,7 +321,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       ok = __all_sync(0xffffffffu, win::wait(&st_empty[sl], ((n_q >> 1) & 1) ^ 1, &s_abort, kPatient));
       if (!ok) break;
       const int64_t first = (static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + h0;    // row r: + r / P * Hq + r % P
-      for (int r0 = 0; r0 < rows; r0 += 8 * RG) {
+      for (int r0 = 0; r0 < rows && it.n > 2; r0 += 8 * RG) {
         uint4 o[RG][PC], g[RG][PC];
 #pragma unroll
         for (int x = 0; x < RG; ++x) {
@@ -342,7 +353,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         s_stat[sl][0][r] = nl;
         if (r < rows) {
           a.nlse[at0 + r] = nl;
-          a.delta[at0 + r] = s_stat[sl][1][r];
+          if (it.n > 2) a.delta[at0 + r] = s_stat[sl][1][r];
         }
       }
       __syncwarp();
@@ -354,7 +365,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c1 = s.scale * kLog2e;
-    int n_k = 0, n_q = 0, k_item = 0;
+    int n_k = 0, n_q = 0, n_d = 0, k_item = 0;
     for (;; ++k_item) {
       const win::Item it = get(k_item);
       const int n = it.n, L = it.L;
@@ -371,27 +382,25 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       }
       bool ok = wait(&st_full[n_q & 1], (n_q >> 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const float nl = s_stat[n_q & 1][0][r], dl = s_stat[n_q & 1][1][r];
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&st_empty[n_q & 1]);
-      for (int j = 0; j < n; ++j, ++n_k) {
-        const int v0 = 128 * j + 64 * g;
-        ok = wait(&s_full[n_k & 1], (n_k >> 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      const float nl = s_stat[n_q & 1][0][r];
+      float dl = s_stat[n_q & 1][1][r];
+      // x = P, y = dP of key tile j; see: the visible columns, where some are not
+      auto load = [&](int j, float (&x)[64], float (&y)[64], uint32_t (&see)[2], bool& masked) -> bool {
+        const int k = n_k + j, v0 = 128 * j + 64 * g;
+        bool ok = wait(&s_full[k & 1], (k >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
         tc::after_sync();
-        float x[64], y[64];
-        const uint32_t tS = tm + 128 * (n_k & 1) + 64 * g + lane_off;
-        tc::tmem_ld64(tS, x);
+        tc::tmem_ld64(tm + 128 * (k & 1) + 64 * g + lane_off, x);
         const int kb = kl.lo + v0 - kl.SP;
         const int hi = row ? p - kb : -1, lo = max(p - s.window + 1, kl.lo) - kb, sk = s.sinks - v0;
-        uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-        const bool masked = !__all_sync(0xffffffffu, hi >= 63 && (lo <= 0 || sk >= 64));
+        see[0] = see[1] = 0xffffffffu;
+        masked = !__all_sync(0xffffffffu, hi >= 63 && (lo <= 0 || sk >= 64));
         if (masked) {
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             see[q] = win::bit_range(0, hi - 32 * q) & (win::bit_range(lo - 32 * q, 31) | win::bit_range(0, sk - 1 - 32 * q));
         }
-        const uint64_t cc = tc::pack2(c1, c1), ll = tc::pack2(nl, nl), dd = tc::pack2(-dl, -dl);
+        const uint64_t cc = tc::pack2(c1, c1), ll = tc::pack2(nl, nl);
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {
           float y0, y1;
@@ -399,10 +408,40 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           x[c] = tc::ex2(y0);
           x[c + 1] = tc::ex2(y1);
         }
-        ok = wait(&dp_full, n_k & 1);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        ok = wait(&dp_full[k & 1], (k >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return false;
         tc::after_sync();
-        tc::tmem_ld64(tm + 256 + 64 * g + lane_off, y);
+        tc::tmem_ld64(tm + (n == 2 && j == 1 ? 384 : 256) + 64 * g + lane_off, y);
+        return true;
+      };
+      float x[64], y[64];
+      uint32_t see[2];
+      bool masked;
+      if (n <= 2) {                                          // D = sum of P dP
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; ok && j < n; ++j) {
+          ok = load(j, x, y, see, masked);
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!masked || (see[c >> 5] >> (c & 31)) & 1) sum[c & 3] = fmaf(x[c], y[c], sum[c & 3]);
+        }
+        if (!ok) break;
+        (g ? s_stat[n_q & 1][1] : s_sum)[r] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::bar_arrive(&d_full);
+        ok = wait(&d_full, n_d++ & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        dl = s_sum[r] + s_stat[n_q & 1][1][r];
+        if (g == 0 && row) a.delta[(static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P + r] = dl;
+      }
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&st_empty[n_q & 1]);
+      for (int j = 0; j < n; ++j) {
+        ok = load(j, x, y, see, masked);
+        if (!ok) break;
+        const int k = n_k + j;
+        const uint32_t tS = tm + 128 * (k & 1) + 64 * g + lane_off;
+        const uint64_t dd = tc::pack2(-dl, -dl);
 #pragma unroll
         for (int c = 0; c < 64; c += 2)
           tc::unpack2(win::mul2(tc::pack2(x[c], x[c + 1]), tc::add2(tc::pack2(y[c], y[c + 1]), dd)), x[c], x[c + 1]);
@@ -422,15 +461,16 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         if (g == 0 && L < s.N && kl.key(128 * j + 127) >= L) {
           if (128 * j + r >= kl.SP && kl.key(128 * j + r) >= L)
             for (int c = 0; c < M::KB * 8; ++c)
-              *reinterpret_cast<uint4*>(sm + M::oK + (n_k % M::NK) * M::TILE + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
+              *reinterpret_cast<uint4*>(sm + M::oK + (k % M::NK) * M::TILE + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
           tc::fence_async_smem();
         }
         tc::tmem_wait_st();
         tc::before_sync();
-        tc::bar_arrive(&ds_full[n_k & 1]);
+        tc::bar_arrive(&ds_full[k & 1]);
       }
       if (!ok) break;
+      n_k += n;
       // dQ of the item, scaled: row r's columns 64 g .. (shared memory is full, and Q's and dO's tiles
       // already take the next item's, so the rows go out from registers)
       ok = wait(&dq_last, n_q & 1);
@@ -475,7 +515,16 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   }
   tc::before_sync();
   __syncthreads();
-  if (tid == 0 && s_abort) atomicOr(a.status, PISA_STATUS_TIMEOUT);
+  if (s_abort) {                                             // the next kernel's gradients of these rows' keys are NaN
+    if (tid == 0) atomicOr(a.status, PISA_STATUS_TIMEOUT);
+    for (int k = 0; k < win::rounds_of(a.n_items); ++k) {
+      const int64_t w = win::item_of(k, a.n_items);
+      if (w < 0) break;
+      const win::Item it = dq_item(a, static_cast<int>(w));
+      if (tid < 128 && it.t0 + (tid >> a.lp) < s.Nq)
+        a.nlse[(static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P + tid] = __int_as_float(0x7fc00000);
+    }
+  }
   if (warp == 0) {
     tc::after_sync();
     tc::tmem_free(tm, 512);

@@ -191,6 +191,22 @@ def test_split_item_captured():
         assert torch.equal(O, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,d,window,sinks,lens", [
+    (1, 400, 8, 2, 64, 2, 1, None), (2, 600, 4, 2, 128, 4, 0, [600, 391]), (1, 2000, 3, 1, 128, 17, 4, None),
+    (1, 97, 5, 1, 128, 97, 0, None), (2, 300, 2, 2, 64, 60, 33, None),
+])
+def test_gradients_of_rows_with_few_keys_keep_their_precision(B, N, Hq, Hkv, d, window, sinks, lens):
+    # dQ and dK carry two roundings to bf16 of the same size, dS's and their own: sqrt 2 of one's error (rms),
+    # and 6 % for the sample. O's rounding, which D = dO . O would feel most here, is not to add to it.
+    Q, K, V, dO = _inputs(B, N, N, Hq, Hkv, d, lens=lens, seed=N)
+    got = _run(Q, K, V, dO, window, sinks, lens)
+    want, _ = attention(Q, K, V, window, sinks, lens, dO=dO)
+    for n in ("dQ", "dK", "dV"):
+        w = want[n].double()
+        one = (w.to(bf16).double() - w).norm()
+        assert float((got[n].double() - w).norm() / one) < 1.5, n
+
+
 def test_same_call_gives_same_bits():
     Q, K, V, dO = _inputs(2, 900, 900, 8, 2, 128, seed=1)
     a, b = _run(Q, K, V, dO, 250, 40), _run(Q, K, V, dO, 250, 40)
