@@ -292,7 +292,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     // the softmax warps waiting 8400 of 31000 cycles an item at a window of 1024. One warp's loads do not
     // cover the latency of memory, so the rows of the item after are asked into L2 meanwhile. It also
     // decodes the items for the other roles.
-    constexpr int PC = D / 32, RG = 256 / D;                 // 16-byte pieces of a row a lane takes; groups of 8 rows in flight
+    constexpr int PC = D / 32, RG = 512 / D;                 // 16-byte pieces of a row a lane takes; groups of 8 rows in flight
     const int g8 = lane >> 2, p4 = lane & 3;
     const int rounds = win::rounds_of(a.n_items);
     int n_q = 0;
@@ -335,14 +335,21 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         }
 #pragma unroll
         for (int x = 0; x < RG; ++x) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t acc = 0;
 #pragma unroll
           for (int c = 0; c < PC; ++c) {
-            const uint32_t a0[4] = {g[x][c].x, 0u, g[x][c].y, 0u}, a1[4] = {g[x][c].z, 0u, g[x][c].w, 0u};
-            mma_bf16(d, a0, o[x][c].x, o[x][c].y);
-            mma_bf16(d, a1, o[x][c].z, o[x][c].w);
+            const uint32_t ow[4] = {o[x][c].x, o[x][c].y, o[x][c].z, o[x][c].w}, gw[4] = {g[x][c].x, g[x][c].y, g[x][c].z, g[x][c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc = tc::fma2(tc::pack2(__uint_as_float(ow[e] << 16), __uint_as_float(ow[e] & 0xffff0000u)),
+                             tc::pack2(__uint_as_float(gw[e] << 16), __uint_as_float(gw[e] & 0xffff0000u)), acc);
           }
-          if (p4 == g8 >> 1) s_stat[sl][1][r0 + 8 * x + g8] = g8 & 1 ? d[1] : d[0];
+          float d0, d1;
+          tc::unpack2(acc, d0, d1);
+          d0 += d1;
+          d0 += __shfl_xor_sync(0xffffffffu, d0, 1);
+          d0 += __shfl_xor_sync(0xffffffffu, d0, 2);
+          if (p4 == 0) s_stat[sl][1][r0 + 8 * x + g8] = d0;
         }
       }
       __syncwarp();
