@@ -28,7 +28,7 @@ size_t align256(size_t x);
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kThreads = 384;                  // warps 0-7 softmax and output, 8 (and 10) MMA, 9 loader, 11 row statistics
+constexpr int kThreads = 384;                  // warps 0-7 softmax and output, 8 (and 10) MMA, 9 loader, 11 items (dQ)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
 constexpr uint64_t kPatient = 1ull << 40;      // the item warp outwaits the others, whose giving up it sees
@@ -37,7 +37,6 @@ constexpr uint32_t kNaN2 = 0x7fc07fc0u;        // two bf16 NaNs
 struct BwdArgs {
   WinDims s;
   const int32_t* len;
-  const bf16 *O, *dO;
   const float* lse;
   float *nlse, *delta;     // [B][Hkv][sets][Nqp][P]: -lse log2 e and D
   bf16 *dQ, *dK, *dV;
@@ -86,24 +85,31 @@ __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
 // tensor cores have a product at hand while the softmax warps turn S and dP into dS. (The barriers of
 // dP, dS and dQ are two each, by the tile's parity: their waiters may be a tile apart.)
 //
-// D is dO . O from the forward's O, whose rounding to bf16 a row with few keys feels (windows under
-// some 60 keys: dQ and dK 1.5 to 2 times as far from the exact ones as their own rounding to bf16 puts
-// them). An item of one or two key tiles, and so every short row, has all its dP in tensor memory at one
-// time, the second tile's where dQ will be: there D is the fp32 sum of P dP itself, and O is not read.
+// D is dO . O from the forward's O: O's rows come by TMA as one more tile through the keys' ring, dO's
+// are in shared memory for dP anyway, and the softmax threads form half a row's product each (a warp
+// that formed D an item ahead from global memory bounded the kernel below windows of 1000 keys: 424 against
+// 493 us at 512, 326 against 467 at 256, 4 x 16384 rows of 16 heads). But O's rounding to bf16 is felt by
+// rows with few keys (windows under some 60: dQ and dK 1.5 to 2 times as far from the exact ones as
+// their own rounding puts them, 1.42 times without it). An item of one or two key tiles, and so every
+// short row, has all its dP in tensor memory at one time, the second tile's where dQ will be: there D
+// is the fp32 sum of P dP itself.
+//
+// 4 x 16384 rows of 16 heads over 4 KV heads, d = 128: 639 us at a window of 1024 and 4 sinks (1.26
+// PFLOP/s of its three products), 256 us for 8192 rows of 16 heads over 2, all causal (1.61).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                 const __grid_constant__ CUtensorMap kmap32, const __grid_constant__ CUtensorMap vmap32) {
+                 const __grid_constant__ CUtensorMap kmap32, const __grid_constant__ CUtensorMap vmap32,
+                 const __grid_constant__ CUtensorMap omap) {
   using M = DqSmem<D>;
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
-      s_full[2], dp_full[2], d_full, ds_full[2], dq_done[2], dq_last, dq_empty, st_full[2], st_empty[2], drain[2], never;
+      s_full[2], dp_full[2], d_full, ds_full[2], dq_done[2], dq_last, dq_empty, drain[2], never;
   __shared__ win::ItemRing s_items;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  __shared__ float s_stat[2][2][128];        // per item (two at a time): -lse log2 e, D
-  __shared__ float s_sum[128];               // sums of P dP, columns 0 .. 63 (the others' take D's place)
+  __shared__ float s_sum[2][128];            // D of the rows, as two sums
 
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
@@ -132,10 +138,6 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     tc::bar_init(&dq_done[1], 1);
     tc::bar_init(&dq_last, 1);
     tc::bar_init(&dq_empty, 256);
-    for (int k = 0; k < 2; ++k) {
-      tc::bar_init(&st_full[k], 1);
-      tc::bar_init(&st_empty[k], 8);
-    }
     tc::bar_init(&drain[0], 1);
     tc::bar_init(&drain[1], 1);
     win::ring_init(s_items, 11);
@@ -194,6 +196,18 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         }
       }
       __syncwarp();
+      if (it.n > 2) {                          // O's rows take a key tile's place, before the first one
+        const int st = n_k % M::NK;
+        if (!wait(&k_empty[st], ((n_k / M::NK) & 1) ^ 1)) break;
+        ++n_k;
+        if (lane == 0) {
+          tc::bar_expect_tx(&k_full[st], M::TILE);
+#pragma unroll
+          for (int kb = 0; kb < M::KB; ++kb)
+            tc::tma_load4(aK + st * M::TILE + kb * (128 * 128), &omap, kb * 64, it.h0, it.t0, it.b, &k_full[st]);
+        }
+        __syncwarp();
+      }
       for (int j = 0; ok && j < it.n; ++j)
         ok = load(n_k, k_full, k_empty, M::NK, aK, 128 * j, &kmap, &kmap32) &&
              load(n_v, v_full, v_empty, M::NV, aV, 128 * j, &vmap, &vmap32);
@@ -207,7 +221,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     // together, one lane issuing: operands stay in uniform registers)
     const bool leader = win::elect();
     const uint32_t dQ = win::desc_lo(aQ), dO = win::desc_lo(aO), dK = win::desc_lo(aK), dV = win::desc_lo(aV);
-    int n_q = 0, g = 0;                        // items, key tiles so far
+    int n_q = 0, g = 0, kk = 0;                // items, key tiles, tiles through K's ring so far
     bool issued = false, ok = true;
     for (int i = 0; ok; ++i) {
       const int n = get(i).n;
@@ -217,9 +231,11 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       ok = wait(&q_full, n_q & 1);
       ++n_q;
       issued = true;
+      kk += n > 2;
       auto issue_s = [&](int g) -> bool {      // where dS of two tiles ago has been read
-        const int st = g % M::NK;
-        if (!wait(&k_full[st], (g / M::NK) & 1)) return false;
+        const int st = kk % M::NK;
+        if (!wait(&k_full[st], (kk / M::NK) & 1)) return false;
+        ++kk;
         if (g >= 2 && !wait(&dq_done[g & 1], ((g >> 1) - 1) & 1)) return false;
         tc::after_sync();
         if (leader) {
@@ -256,14 +272,15 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     // ------------------------------------------------------------------ MMA, dQ
     const bool leader = win::elect();
     const uint32_t dK = win::desc_mn_lo(aK, 128 * 128);
-    int n_q = 0, g = 0;
+    int n_q = 0, g = 0, kk = 0;
     bool issued = false, ok = true;
     for (int i = 0; ok; ++i) {
       const int n = get(i).n;
       if (n < 0) break;
       if (n == 0) continue;
-      for (int j = 0; ok && j < n; ++j, ++g) {
-        const int st = g % M::NK;
+      kk += n > 2;
+      for (int j = 0; ok && j < n; ++j, ++g, ++kk) {
+        const int st = kk % M::NK;
         ok = (j > 0 || wait(&dq_empty, (n_q & 1) ^ 1)) && wait(&ds_full[g & 1], (g >> 1) & 1) &&
              (j > 0 || n != 2 || wait(&ds_full[(g + 1) & 1], ((g + 1) >> 1) & 1));   // dP(1) has been read, too
         if (!ok) break;
@@ -285,17 +302,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       tc::bar_wait(&drain[1], 0, kDrainNs);
     }
   } else if (warp == 11) {
-    // ------------------------------------------------------------------ D = dO . O and -lse log2 e of
-    // the rows, an item ahead. The dot products of 8 rows are the diagonal of an 8 x 8 product on
-    // m16n8k16 MMAs (half of A's rows zero; k taken in an order that makes a lane's operands 16 bytes of
-    // a row): one warp then keeps up with the item's other work, where sums by lanes and shuffles kept
-    // the softmax warps waiting 8400 of 31000 cycles an item at a window of 1024. One warp's loads do not
-    // cover the latency of memory, so the rows of the item after are asked into L2 meanwhile. It also
-    // decodes the items for the other roles.
-    constexpr int PC = D / 32, RG = 512 / D;                 // 16-byte pieces of a row a lane takes; groups of 8 rows in flight
-    const int g8 = lane >> 2, p4 = lane & 3;
+    // ------------------------------------------------------------------ items, decoded ahead of the other
+    // roles; their rows' lse is asked into L2 meanwhile
     const int rounds = win::rounds_of(a.n_items);
-    int n_q = 0;
     for (int k = 0; k <= rounds; ++k) {
       const int64_t w = k < rounds ? win::item_of(k, a.n_items) : -1;
       win::Item it{};
@@ -304,77 +313,27 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       bool ok = lane != 0 || win::ring_put(s_items, k, it, &s_abort, kPatient);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok || w < 0) break;
-      const int64_t w1 = k + 1 < rounds ? win::item_of(k + 1, a.n_items) : -1;
-      if (w1 >= 0) {
-        const win::Item nx = dq_item(a, static_cast<int>(w1));
-        const int64_t f = (static_cast<int64_t>(nx.b) * s.Nq + nx.t0) * s.Hq + nx.h0;
-        for (int r = lane; r < (nx.n > 2 ? min(128, (s.Nq - nx.t0) * a.P) : 0); r += 32)
-#pragma unroll
-          for (int c = 0; c < D; c += 64) {
-            const int64_t at = (f + static_cast<int64_t>(r >> a.lp) * s.Hq + (r & (a.P - 1))) * D + c;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.O + at));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.dO + at));
-          }
-      }
       if (it.n == 0) continue;
-      const int sl = n_q & 1, rows = min(128, (min(s.Nq, it.L - s.off) - it.t0) * a.P), h0 = it.h0;
-      ok = __all_sync(0xffffffffu, win::wait(&st_empty[sl], ((n_q >> 1) & 1) ^ 1, &s_abort, kPatient));
-      if (!ok) break;
-      const int64_t first = (static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + h0;    // row r: + r / P * Hq + r % P
-      for (int r0 = 0; r0 < rows && it.n > 2; r0 += 8 * RG) {
-        uint4 o[RG][PC], g[RG][PC];
-#pragma unroll
-        for (int x = 0; x < RG; ++x) {
-          const int r = r0 + 8 * x + g8;
-          const int64_t at = (first + static_cast<int64_t>(r >> a.lp) * s.Hq + (r & (a.P - 1))) * D + 8 * p4;
-#pragma unroll
-          for (int c = 0; c < PC; ++c) {
-            o[x][c] = r < rows ? ldg_u4(a.O + at + 32 * c) : make_uint4(0, 0, 0, 0);
-            g[x][c] = r < rows ? ldg_u4(a.dO + at + 32 * c) : make_uint4(0, 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < RG; ++x) {
-          uint64_t acc = 0;
-#pragma unroll
-          for (int c = 0; c < PC; ++c) {
-            const uint32_t ow[4] = {o[x][c].x, o[x][c].y, o[x][c].z, o[x][c].w}, gw[4] = {g[x][c].x, g[x][c].y, g[x][c].z, g[x][c].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc = tc::fma2(tc::pack2(__uint_as_float(ow[e] << 16), __uint_as_float(ow[e] & 0xffff0000u)),
-                             tc::pack2(__uint_as_float(gw[e] << 16), __uint_as_float(gw[e] & 0xffff0000u)), acc);
-          }
-          float d0, d1;
-          tc::unpack2(acc, d0, d1);
-          d0 += d1;
-          d0 += __shfl_xor_sync(0xffffffffu, d0, 1);
-          d0 += __shfl_xor_sync(0xffffffffu, d0, 2);
-          if (p4 == 0) s_stat[sl][1][r0 + 8 * x + g8] = d0;
-        }
+      if (lane < 2 * a.P) {                                  // the first and the last token's lse of each head
+        const int t = lane & 1 ? min(s.Nq, it.t0 + a.tok) - 1 : it.t0;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.lse + (static_cast<int64_t>(it.b) * s.Hq + it.h0 + (lane >> 1)) * s.Nq + t));
       }
-      __syncwarp();
-      const int64_t at0 = (static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P;
-#pragma unroll
-      for (int r = lane; r < 128; r += 32) {
-        const float nl = r < rows ? -a.lse[(static_cast<int64_t>(it.b) * s.Hq + h0 + (r & (a.P - 1))) * s.Nq + it.t0 + (r >> a.lp)] * kLog2e : 0.f;
-        s_stat[sl][0][r] = nl;
-        if (r < rows) {
-          a.nlse[at0 + r] = nl;
-          if (it.n > 2) a.delta[at0 + r] = s_stat[sl][1][r];
-        }
-      }
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&st_full[sl]);
-      ++n_q;
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax: row r, columns 64 g ..
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c1 = s.scale * kLog2e;
-    int n_k = 0, n_q = 0, n_d = 0, k_item = 0;
+    int n_k = 0, n_q = 0, kk = 0, k_item = 0;
+    auto lse_of = [&](const win::Item& x) -> float {
+      const int rows = x.n > 0 ? min(128, (min(s.Nq, x.L - s.off) - x.t0) * a.P) : 0;
+      return r < rows ? a.lse[(static_cast<int64_t>(x.b) * s.Hq + x.h0 + (r & (a.P - 1))) * s.Nq + x.t0 + (r >> a.lp)] : 0.f;
+    };
+    win::Item next = get(0);
+    float lse_next = lse_of(next);
     for (;; ++k_item) {
-      const win::Item it = get(k_item);
+      const win::Item it = next;
+      const float nl = -kLog2e * lse_next;
       const int n = it.n, L = it.L;
       if (n < 0) break;
       const win::KeyList kl(it.lo, it.SP);
@@ -385,12 +344,11 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           uint4* o = reinterpret_cast<uint4*>(a.dQ + ((static_cast<int64_t>(it.b) * s.Nq + i) * s.Hq + h) * D);
           for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
         }
+        next = get(k_item + 1);
+        lse_next = lse_of(next);
         continue;
       }
-      bool ok = wait(&st_full[n_q & 1], (n_q >> 1) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const float nl = s_stat[n_q & 1][0][r];
-      float dl = s_stat[n_q & 1][1][r];
+      bool ok = true;
       // x = P, y = dP of key tile j; see: the visible columns, where some are not
       auto load = [&](int j, float (&x)[64], float (&y)[64], uint32_t (&see)[2], bool& masked) -> bool {
         const int k = n_k + j, v0 = 128 * j + 64 * g;
@@ -424,8 +382,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       float x[64], y[64];
       uint32_t see[2];
       bool masked;
-      if (n <= 2) {                                          // D = sum of P dP
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      // D: the sum of P dP, or dO . O of the tiles in shared memory
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      if (n <= 2) {
         for (int j = 0; ok && j < n; ++j) {
           ok = load(j, x, y, see, masked);
           if (!ok) break;
@@ -434,15 +393,38 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
             if (!masked || (see[c >> 5] >> (c & 31)) & 1) sum[c & 3] = fmaf(x[c], y[c], sum[c & 3]);
         }
         if (!ok) break;
-        (g ? s_stat[n_q & 1][1] : s_sum)[r] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tc::bar_arrive(&d_full);
-        ok = wait(&d_full, n_d++ & 1);
+      } else {
+        ok = wait(&q_full, n_q & 1) && wait(&k_full[kk % M::NK], (kk / M::NK) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
-        dl = s_sum[r] + s_stat[n_q & 1][1][r];
-        if (g == 0 && row) a.delta[(static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P + r] = dl;
+        uint64_t acc[2] = {0, 0};
+        const unsigned char* po = sm + M::oK + kk % M::NK * M::TILE + r * 128;
+        const unsigned char* pd = sm + M::oO + r * 128;
+        constexpr int HC = D / 16;                           // 16-byte pieces of half a row
+#pragma unroll
+        for (int c = 0; c < HC; ++c) {
+          const int pc = g * HC + c, at = (pc >> 3) * (128 * 128) + (((pc & 7) ^ (r & 7)) << 4);
+          const uint4 o = *reinterpret_cast<const uint4*>(po + at), d = *reinterpret_cast<const uint4*>(pd + at);
+          const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[e & 1] = tc::fma2(tc::pack2(__uint_as_float(ow[e] << 16), __uint_as_float(ow[e] & 0xffff0000u)),
+                                  tc::pack2(__uint_as_float(dw[e] << 16), __uint_as_float(dw[e] & 0xffff0000u)), acc[e & 1]);
+        }
+        tc::unpack2(acc[0], sum[0], sum[1]);
+        tc::unpack2(acc[1], sum[2], sum[3]);
       }
-      __syncwarp();
-      if (lane == 0) tc::bar_arrive(&st_empty[n_q & 1]);
+      s_sum[g][r] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc::bar_arrive(&d_full);
+      ok = wait(&d_full, n_q & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const float dl = s_sum[0][r] + s_sum[1][r];
+      if (n > 2 && tid == 0) tc::bar_arrive(&k_empty[kk % M::NK]);
+      kk += n > 2;
+      if (g == 0 && row) {
+        const int64_t at = (static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P + r;
+        a.nlse[at] = nl;
+        a.delta[at] = dl;
+      }
       for (int j = 0; j < n; ++j) {
         ok = load(j, x, y, see, masked);
         if (!ok) break;
@@ -468,7 +450,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         if (g == 0 && L < s.N && kl.key(128 * j + 127) >= L) {
           if (128 * j + r >= kl.SP && kl.key(128 * j + r) >= L)
             for (int c = 0; c < M::KB * 8; ++c)
-              *reinterpret_cast<uint4*>(sm + M::oK + (k % M::NK) * M::TILE + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
+              *reinterpret_cast<uint4*>(sm + M::oK + ((kk + j) % M::NK) * M::TILE + (c >> 3) * (128 * 128) + r * 128 + (c & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
           tc::fence_async_smem();
         }
@@ -478,6 +460,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       }
       if (!ok) break;
       n_k += n;
+      kk += n;
+      next = get(k_item + 1);
+      lse_next = lse_of(next);
       // dQ of the item, scaled: row r's columns 64 g .. (shared memory is full, and Q's and dO's tiles
       // already take the next item's, so the rows go out from registers)
       ok = wait(&dq_last, n_q & 1);
@@ -1014,7 +999,7 @@ int bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   if (int e = dkv_ready(window_dkv_kernel<D>, DkvSmem<D>::bytes)) return e;
   {
     ProfScope ps(st, "window_dq");
-    window_dq_kernel<D><<<std::min(a.n_items, sm_count()), kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
+    window_dq_kernel<D><<<std::min(a.n_items, sm_count()), kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[8]);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1058,8 +1043,6 @@ int launch_window_bwd(const WinDims& s, const void* Q, const void* K, const void
   a.s = s;
   plan(a);
   a.len = len;
-  a.O = static_cast<const bf16*>(O);
-  a.dO = static_cast<const bf16*>(dO);
   a.lse = lse;
   a.nlse = reinterpret_cast<float*>(ws + w.nlse);
   a.delta = reinterpret_cast<float*>(ws + w.delta);
@@ -1071,7 +1054,7 @@ int launch_window_bwd(const WinDims& s, const void* Q, const void* K, const void
   a.wait_ns = wait_limit_ns();
   a.stall = test_stall();
   const int64_t hd = static_cast<int64_t>(s.Hq) * s.d, kd = static_cast<int64_t>(s.Hkv) * s.d;
-  CUtensorMap m[8];
+  CUtensorMap m[9];
   if (int e = win::token_map(&m[0], Q, s.B, s.Nq, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
   if (int e = win::token_map(&m[1], dO, s.B, s.Nq, s.Hq, s.d, hd, a.P, a.tok)) return e;
   if (int e = win::token_map(&m[2], K, s.B, s.N, s.Hkv, s.d, s.ks, 1, 128)) return e;
@@ -1080,6 +1063,7 @@ int launch_window_bwd(const WinDims& s, const void* Q, const void* K, const void
   if (int e = win::token_map(&m[5], V, s.B, s.N, s.Hkv, s.d, s.vs, 1, 32)) return e;
   if (int e = win::token_map(&m[6], dK, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
   if (int e = win::token_map(&m[7], dV, s.B, s.N, s.Hkv, s.d, kd, 1, 32)) return e;
+  if (int e = win::token_map(&m[8], O, s.B, s.Nq, s.Hq, s.d, hd, a.P, a.tok)) return e;
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
   if (e != cudaSuccess) return e;
   return s.d == 128 ? bwd_launch<128>(a, m, st) : bwd_launch<64>(a, m, st);
