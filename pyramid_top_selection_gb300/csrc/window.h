@@ -51,7 +51,7 @@ struct WinDims {
 };
 
 struct WinBwdWs {
-  size_t status, nlse, delta, part, total;
+  size_t status, gave_up, nlse, delta, part, total;
 };
 WinBwdWs window_bwd_ws(const WinDims& s);
 

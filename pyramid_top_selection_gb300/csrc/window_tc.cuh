@@ -256,6 +256,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(const void* p, uint32_t rank) {
   return v;
 }
 
+// Programmatic launches: lets the kernel behind this one start once all CTAs have come here (its CTAs
+// take the SMs as they fall free); waits for the kernel before to be complete and its writes visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect() {
   uint32_t p;
