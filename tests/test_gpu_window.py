@@ -150,6 +150,13 @@ def test_long_sequences_on_sampled_rows(Hq, Hkv, d, window, sinks):
     (1, 65, 700, 4, 2, 128, 640, 0, [650]),
     (1, 513, 1800, 8, 4, 64, 900, 1, None),
     (2, 1, 1300, 4, 4, 128, 1024, 200, [1300, 1299]),      # the only query of the second sequence is padding
+    # padded batches: items with nothing to see among the split ones
+    (3, 777, 5003, 12, 4, 128, 1500, 5, [5003, 3752, 0]),
+    (4, 130, 3000, 8, 2, 64, 1200, 3, [3000, 2990, 2871, 100]),
+    (5, 64, 2600, 4, 1, 128, 2600, 0, [2600, 2599, 2537, 2536, 0]),
+    (2, 500, 2200, 8, 2, 128, 2000, 0, [2200, 2200]),
+    (3, 300, 1500, 8, 4, 64, 1000, 40, [0, 0, 1201]),
+    (2, 600, 2000, 12, 4, 128, 900, 1, [0, 1399]),         # no row at all
 ])
 def test_few_rows_against_many_keys(B, Nq, N, Hq, Hkv, d, window, sinks, lens):
     # an item's keys are cut among a cluster's CTAs, whose sums are joined
@@ -175,6 +182,17 @@ def test_split_item_keeps_nan_and_reports_waits(request):
     O, lse = pisa.window_attn_fwd(Q, K, V, s, ws=ws)
     assert pisa.workspace_status(ws) & pisa.STATUS_TIMEOUT
     assert bool(O.isnan().all()) and bool(lse.isnan().all())
+
+
+def test_split_items_of_a_padded_batch_report_waits(stalled):
+    Q, K, V, _ = _inputs(3, 200, 3000, 8, 2, 64, lens=[3000, 2900, 50], seed=4)
+    s = pisa.window_shape_of(Q, K, V, 2000, 4)
+    ws = pisa.window_workspace(s, pisa.WINDOW_FWD, Q.device)
+    ln = torch.tensor([3000, 2900, 50], dtype=torch.int32, device="cuda")
+    O, lse = pisa.window_attn_fwd(Q, K, V, s, lens=ln, ws=ws)
+    assert pisa.workspace_status(ws) & pisa.STATUS_TIMEOUT
+    assert bool(O[0].isnan().all()) and bool(O[1, :100].isnan().all()) and bool(lse[0].isnan().all())
+    assert float(O[2].abs().max()) == 0.0 and bool((lse[2] == -math.inf).all())
 
 
 def test_split_item_captured():
