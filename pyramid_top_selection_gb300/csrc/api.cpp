@@ -219,8 +219,13 @@ int window_dims(const pisa_window_shape_t* s, pisa::WinDims* o) {
   d.B = s->B; d.Nq = s->Nq; d.N = s->N; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d;
   d.G = s->Hq / s->Hkv;
   d.off = s->N - s->Nq;
-  d.window = s->window < s->N ? s->window : s->N;     // the same keys, and no sum of positions overflows
+  // the same keys, and no sum of positions overflows
+  d.window = s->window < s->N ? s->window : s->N;
   d.sinks = s->sinks < s->N ? s->sinks : s->N;
+  if (d.window + d.sinks >= s->N) {                   // no key lies between sinks and window: full causal attention
+    d.window = s->N;
+    d.sinks = 0;
+  }
   d.scale = scale_or_default(s->scale, s->d);
   *o = d;
   return PISA_OK;

@@ -51,9 +51,9 @@ struct BwdArgs {
   int stall;
   int P, lp, tok, sets, Nqp;   // heads (2^lp) and tokens of a row tile, head sets of a group, padded Nq
   int n_tiles, n_heads, n_items;           // dQ: token tiles, (b, kv, set), items
-  // dK, dV: key tiles, (b, kv), key tiles with sinks, token tiles of a chunk, chunks of a band and
-  // of a sink tile, items of the bands
-  int n_kt, n_bh, n_st, ct, nck, ncs, n_reg;
+  // dK, dV: key tiles, (b, kv), key tiles with sinks; token tiles of a chunk and chunks of a key tile, of
+  // those without sinks (ct, nck) and with them (cts, ncs); items of the tiles with sinks, which come first
+  int n_kt, n_bh, n_st, ct, nck, cts, ncs, n_snk;
 };
 
 // ------------------------------------------------------------------------------------------ dQ
@@ -564,30 +564,24 @@ struct TokenRange {
 };
 
 struct DkvItem {
-  int b, kv, kt, c, chunks;        // chunk c of the key tile's `chunks`
+  int b, kv, kt, c, ct;            // chunk c, of ct token tiles, of the key tile's
   int64_t slot;                    // partial sums' slot, -1: the only chunk, written as it is
   __host__ __device__ DkvItem(const BwdArgs& a, int w) {
-    int bh;
-    if (w < a.n_reg) {
-      c = w / (a.n_kt * a.n_bh);
-      const int x = w % (a.n_kt * a.n_bh);
-      kt = x / a.n_bh;
-      bh = x % a.n_bh;
-    } else {
-      const int x = w - a.n_reg;
-      c = a.nck + x / (a.n_st * a.n_bh);
-      kt = x / a.n_bh % a.n_st;
-      bh = x % a.n_bh;
-    }
+    const bool sink = w < a.n_snk;
+    const int x = sink ? w : w - a.n_snk, tiles = sink ? a.n_st : a.n_kt - a.n_st;
+    const int bh = x % a.n_bh;
+    kt = x / a.n_bh % tiles + (sink ? 0 : a.n_st);
+    c = x / a.n_bh / tiles;
     b = bh / a.s.Hkv;
     kv = bh % a.s.Hkv;
-    chunks = kt < a.n_st ? a.ncs : a.nck;
-    slot = chunks == 1 ? -1 : slot_of(a, kt, bh, c);
+    ct = run_of(a, kt);
+    slot = (sink ? a.ncs : a.nck) == 1 ? -1 : slot_of(a, kt, bh, c);
   }
-  // slots: sink tiles first ([kt][bh][ncs]), then the others ([kt][bh][nck])
+  static __host__ __device__ int run_of(const BwdArgs& a, int kt) { return kt < a.n_st ? a.cts : a.ct; }
+  // slots: sink tiles first ([kt][bh][ncs], where these are cut), then the others ([kt][bh][nck])
   static __host__ __device__ int64_t slot_of(const BwdArgs& a, int kt, int bh, int c) {
     if (kt < a.n_st) return (static_cast<int64_t>(kt) * a.n_bh + bh) * a.ncs + c;
-    return static_cast<int64_t>(a.n_st) * a.n_bh * a.ncs + (static_cast<int64_t>(kt - a.n_st) * a.n_bh + bh) * a.nck + c;
+    return (a.ncs > 1 ? a.n_snk : 0) + (static_cast<int64_t>(kt - a.n_st) * a.n_bh + bh) * a.nck + c;
   }
 };
 
@@ -622,7 +616,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   const int kb = 128 * it.kt, L = win::valid_len(a.len, it.b, s.N);
   const TokenRange tr(s, a.tok, L, it.kt);
   // this chunk's row tiles: token tile n / sets, head set n % sets
-  const int tile0 = it.c * a.ct, n = win::uniform(max(0, min(a.ct, tr.n - tile0)) * a.sets);
+  const int tile0 = it.c * it.ct, n = win::uniform(max(0, min(it.ct, tr.n - tile0)) * a.sets);
   // This kernel starts while dQ's ends: what that wrote (statistics, status) is read after grid_wait only,
   // and one warp here waits for it in any case.
   if (warp == 11) {
@@ -965,7 +959,7 @@ __global__ void __launch_bounds__(256) window_dkv_sum_kernel(const BwdArgs a, in
   const int kt = first_kt + blockIdx.x / a.n_bh, bh = blockIdx.x % a.n_bh, b = bh / s.Hkv, kv = bh % s.Hkv;
   const int L = win::valid_len(a.len, b, s.N);
   const TokenRange tr(s, a.tok, L, kt);
-  const int chunks = (tr.n + a.ct - 1) / a.ct;
+  const int ct = DkvItem::run_of(a, kt), chunks = (tr.n + ct - 1) / ct;
   const int e = (blockIdx.y * 256 + threadIdx.x) * 4, which = e / (128 * D), r = e / D % 128, col = e % D;
   const int key = 128 * kt + r;
   if (key >= s.N) return;
@@ -984,8 +978,11 @@ __global__ void __launch_bounds__(256) window_dkv_sum_kernel(const BwdArgs a, in
 }
 
 // The sizes that follow from a shape. Chunks: a key tile's rows are one item where the key tiles
-// alone fill the GPU six times over; else (few heads, wide windows) and for the rows that only
-// sinks see, runs of `ct` token tiles, whose partial sums a last kernel adds.
+// alone fill the GPU six times over; else (few heads, wide windows) runs of `ct` token tiles, whose
+// partial sums a last kernel adds. Key tiles with sinks are seen by all rows behind them and have a run
+// length of their own, `cts`. A tile that is cut has more rows than one run, so that there are less than
+// twice as many runs as equal shares: under 2 x 17/16 x 912 of the tiles without sinks and as many of
+// those with them, whatever the shape.
 void plan(BwdArgs& a) {
   const WinDims& s = a.s;
   a.P = win::packed_heads(s.G);
@@ -1005,15 +1002,25 @@ void plan(BwdArgs& a) {
   // row tiles of an item: a sixth of a CTA's share, at least 16; a small problem (under 32 a CTA) whose
   // key tiles leave CTAs idle is cut into as many equal runs as there are CTAs for
   int64_t want = std::max<int64_t>(16, total / (152 * 6));
-  if (total < 152 * 32 && tiles < 152) want = (band * a.sets + 152 / tiles - 1) / (152 / tiles);
+  const bool small = total < 152 * 32 && tiles < 152;
+  if (small) want = (band * a.sets + 152 / tiles - 1) / (152 / tiles);
   a.ct = static_cast<int>(std::min(band, (want + a.sets - 1) / a.sets));
   a.nck = static_cast<int>((band + a.ct - 1) / a.ct);
-  a.ncs = a.n_st ? static_cast<int>((all + a.ct - 1) / a.ct) : a.nck;
-  a.n_reg = a.n_kt * a.n_bh * a.nck;
+  a.cts = a.ct;
+  a.ncs = a.nck;
+  a.n_snk = 0;
+  if (a.n_st > 0) {              // the same shares, of all the work; in a small problem half a CTA's, if not the others' run
+    const int64_t sink_tiles = static_cast<int64_t>(a.n_st) * a.n_bh;
+    const int64_t work = (band * (tiles - sink_tiles) + all * sink_tiles) * a.sets;
+    const int64_t run = small ? std::max(want, work / (152 * 2)) : std::max<int64_t>(16, work / (152 * 6));
+    a.cts = static_cast<int>(std::min(all, (run + a.sets - 1) / a.sets));
+    a.ncs = static_cast<int>((all + a.cts - 1) / a.cts);
+    a.n_snk = a.n_st * a.n_bh * a.ncs;
+  }
 }
 
 int64_t part_slots(const BwdArgs& a) {
-  const int64_t sink = a.ncs > 1 ? static_cast<int64_t>(a.n_st) * a.n_bh * a.ncs : 0;
+  const int64_t sink = a.ncs > 1 ? a.n_snk : 0;
   const int64_t rest = a.nck > 1 ? static_cast<int64_t>(a.n_kt - a.n_st) * a.n_bh * a.nck : 0;
   return sink + rest;
 }
@@ -1049,7 +1056,7 @@ int bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(st, "window_dkv");
-    const int items = a.n_reg + a.n_st * a.n_bh * std::max(0, a.ncs - a.nck);
+    const int items = a.n_snk + (a.n_kt - a.n_st) * a.n_bh * a.nck;
     const Behind b(dim3(items), kThreads, DkvSmem<D>::bytes, st);
     e = cudaLaunchKernelEx(&b.cfg, window_dkv_kernel<D>, a, m[0], m[1], m[2], m[3], m[6], m[7], dq_ctas);
   }

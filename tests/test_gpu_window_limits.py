@@ -1,0 +1,59 @@
+"""Window attention at its limits on the GPU, against the 64-bit definition (_window_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import pyramid_top_selection_gb300 as pisa
+from _window_ref import attention, check
+
+pytestmark = pytest.mark.gpu
+bf16 = torch.bfloat16
+
+
+def _inputs(B, Nq, N, Hq, Hkv, d, lens=None, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    Q, K, V, dO = (torch.randn(B, n, h, d, generator=g, device="cuda").to(bf16)
+                   for n, h in ((Nq, Hq), (N, Hkv), (N, Hkv), (Nq, Hq)))
+    for b, L in enumerate(lens or []):     # what lies past a sequence's tokens is never used
+        K[b, L:], V[b, L:] = math.nan, math.inf
+        r = max(0, L - (N - Nq))
+        Q[b, r:], dO[b, r:] = math.nan, -math.inf
+    return Q, K, V, dO
+
+
+def _run(Q, K, V, dO, window, sinks, lens=None):
+    s = pisa.window_shape_of(Q, K, V, window, sinks)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    O, lse = pisa.window_attn_fwd(Q, K, V, s, lens=ln)
+    ws = pisa.window_workspace(s, pisa.WINDOW_BWD, Q.device).fill_(0xAB)
+    grads = pisa.window_attn_bwd(Q, K, V, O, lse, dO, s, lens=ln, ws=ws)
+    assert pisa.workspace_status(ws) == 0
+    return dict(zip(("O", "lse", "dQ", "dK", "dV"), (O, lse, *grads)))
+
+
+@pytest.mark.parametrize("B,Nq,N,Hq,Hkv,d,window,sinks,lens", [
+    (1, 3000, 3000, 8, 2, 64, 16, 600, None),
+    (2, 2500, 2500, 4, 4, 128, 5, 40, [2500, 1201]),
+    (1, 700, 2600, 16, 1, 128, 1, 2000, None),
+    (3, 900, 900, 24, 8, 64, 130, 300, [900, 17, 0]),
+    (1, 2000, 2000, 6, 2, 128, 3, 1990, [1999]),
+    (2, 4000, 4000, 2, 1, 64, 1, 129, None),
+    (4, 2300, 2300, 8, 8, 64, 20, 1, None),
+])
+def test_many_sinks_and_short_windows(B, Nq, N, Hq, Hkv, d, window, sinks, lens):
+    # the rows of a key tile with sinks are cut into runs of their own length
+    Q, K, V, dO = _inputs(B, Nq, N, Hq, Hkv, d, lens, seed=N)
+    got, again = (_run(Q, K, V, dO, window, sinks, lens) for _ in range(2))
+    want, tol = attention(Q, K, V, window, sinks, lens, dO=dO)
+    for n in want:
+        check(n, got[n], want[n], tol[n])
+        assert torch.equal(got[n], again[n]), n
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 700), (300, 400), (650, 50), (1, 5000)])
+def test_sinks_that_meet_the_window_are_full_causal_attention(window, sinks):
+    Q, K, V, dO = _inputs(2, 700, 700, 8, 2, 64, [700, 431], seed=3)
+    a, b = _run(Q, K, V, dO, window, sinks, [700, 431]), _run(Q, K, V, dO, 700, 0, [700, 431])
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
