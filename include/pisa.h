@@ -295,7 +295,7 @@ int pisa_decode_step(const pisa_decode_shape_t* shape, const int32_t* pos, void*
  * projection need no copy. O, dO, dQ [B,Nq,Hq,d], dK, dV [B,N,Hkv,d] bf16 and lse [B,Hq,Nq]
  * fp32 are contiguous. Any group size G = Hq / Hkv <= 64; d in {64, 128}; 1 <= Nq <= N <= 2^24;
  * B*N*Hq < 2^31. scale as in pisa_shape_t.
- * No output (or workspace) may overlap an input.
+ * Nothing written (outputs, the workspace) may overlap anything that is read, nor one another.
  * Values at tokens j >= L (an uninitialised cache, padding) are never used, whatever they
  * are. Non-finite values at tokens j < L can reach the rows of any query near them, masked
  * or not. */
@@ -345,6 +345,7 @@ typedef struct {
  *   o [B,Hq,d] bf16, lse [B,Hq] fp32 (may be NULL) (written).
  *   status: device int32 word; PISA_STATUS_POS_RANGE is ORed in when some pos[b] is negative,
  *   or at or past Ncap with Ncap < sinks + window; that sequence is then left untouched.
+ * Nothing written (the caches, o, lse, status) may overlap anything else; o may be q itself.
  * G <= 64, d in {64, 128}, Ncap <= 2^24. Keys at slots that p does not see are never used,
  * whatever their values. */
 int pisa_window_decode_step(const pisa_window_decode_shape_t* shape, const int32_t* pos, void* Kcache,
@@ -375,7 +376,7 @@ typedef struct {
  * position (finite; may be NULL with rot = 0); q_weight, k_weight device [d] fp32 (NULL: ones;
  * ignored with norm = 0); pos device [B,N] int32 (NULL: token i of every sequence at i).
  * Qr [B,N,Hq,d], Kr [B,N,Hkv,d] bf16 contiguous (written); Qr may be Q itself and Kr K where
- * those are contiguous; no other overlap. */
+ * those are contiguous; no other overlap with anything read, nor of the two. */
 int pisa_qk_norm_rope(const pisa_rope_shape_t* shape, const void* Q, const void* K, const float* inv_freq,
                       const float* q_weight, const float* k_weight, const int32_t* pos, void* Qr, void* Kr,
                       void* stream);
@@ -386,8 +387,9 @@ int pisa_qk_norm_rope_workspace_size(const pisa_rope_shape_t* shape, size_t* byt
 /* Its backward: with g the gradient turned back (times rot_scale), dw = sum over rows of g h,
  * dx = r (g w - h mean(g w h)), r = 1 / sqrt(mean(x^2) + eps) (dx = g with norm = 0).
  * Q, K the forward's inputs; dQr, dKr contiguous bf16 (read); dQ [B,N,Hq,d], dK [B,N,Hkv,d]
- * bf16 contiguous (written; may be dQr and dKr themselves, no other overlap); dq_weight, dk_weight [d] fp32
- * (written; NULL: not wanted; with norm = 0 they must be NULL). The sums' order is fixed. */
+ * bf16 contiguous (written; may be dQr and dKr themselves); dq_weight, dk_weight [d] fp32
+ * (written; NULL: not wanted; with norm = 0 they must be NULL). Nothing else that is written (the workspace
+ * included) may overlap anything read, nor one another. The sums' order is fixed. */
 int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const void* K, const void* dQr,
                           const void* dKr, const float* inv_freq, const float* q_weight,
                           const float* k_weight, const int32_t* pos, void* dQ, void* dK, float* dq_weight,

@@ -182,14 +182,22 @@ struct Span {
         end(p ? begin + static_cast<uintptr_t>(((tokens - 1) * stride + row) * bytes) : begin) {}
 };
 
-// No output may share bytes with an input; with `in_place`, the k-th output may be the k-th input.
+// One value, or `n` of `bytes` bytes in a row.
+Span flat(const char* name, const void* p, int64_t n, int bytes) { return Span(name, p, 1, 0, n, bytes); }
+
+// What is written shares no bytes with what is read, nor with anything else that is written; of the first
+// `in_place` buffers, the k-th written may be the k-th read.
 template <int NIN, int NOUT>
-int check_apart(const Span (&in)[NIN], const Span (&out)[NOUT], bool in_place = false) {
-  for (int o = 0; o < NOUT; ++o)
+int check_apart(const Span (&in)[NIN], const Span (&out)[NOUT], int in_place = 0) {
+  auto meet = [](const Span& a, const Span& b) { return a.begin < b.end && b.begin < a.end; };
+  for (int o = 0; o < NOUT; ++o) {
     for (int i = 0; i < NIN; ++i) {
-      if (in_place && i == o && in[i].begin == out[o].begin) continue;
-      if (out[o].begin < in[i].end && in[i].begin < out[o].end) return fail(PISA_EINVAL, "%s overlaps %s", out[o].name, in[i].name);
+      if (i == o && i < in_place && in[i].begin == out[o].begin) continue;
+      if (meet(out[o], in[i])) return fail(PISA_EINVAL, "%s overlaps %s", out[o].name, in[i].name);
     }
+    for (int k = 0; k < o; ++k)
+      if (meet(out[o], out[k])) return fail(PISA_EINVAL, "%s overlaps %s", out[o].name, out[k].name);
+  }
   return PISA_OK;
 }
 
@@ -511,8 +519,9 @@ int pisa_window_attn_fwd(const pisa_window_shape_t* shape, const void* Q, const 
   if (ws || ws_bytes) PISA_CHECK(check_ws_bytes(window_ws_bytes(d, PISA_WINDOW_FWD), ws, ws_bytes));
   const int64_t tq = static_cast<int64_t>(d.B) * d.Nq, tk = static_cast<int64_t>(d.B) * d.N;
   const int64_t q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
-  const Span in[] = {{"Q", Q, tq, d.qs, q}, {"K", K, tk, d.ks, kv}, {"V", V, tk, d.vs, kv}};
-  const Span out[] = {{"O", O, tq, q, q}, {"lse", lse, tq, d.Hq, d.Hq, 4}};
+  const Span in[] = {{"Q", Q, tq, d.qs, q}, {"K", K, tk, d.ks, kv}, {"V", V, tk, d.vs, kv}, flat("len", len, d.B, 4)};
+  const Span out[] = {{"O", O, tq, q, q}, {"lse", lse, tq, d.Hq, d.Hq, 4},
+                      flat("workspace", ws, static_cast<int64_t>(window_ws_bytes(d, PISA_WINDOW_FWD)), 1)};
   PISA_CHECK(check_apart(in, out));
   return cuda_rc(pisa::launch_window_fwd(d, Q, K, V, len, O, lse, static_cast<char*>(ws), stream),
                  "pisa_window_attn_fwd");
@@ -531,9 +540,9 @@ int pisa_window_attn_bwd(const pisa_window_shape_t* shape, const void* Q, const 
   const int64_t tq = static_cast<int64_t>(d.B) * d.Nq, tk = static_cast<int64_t>(d.B) * d.N;
   const int64_t q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
   const Span spans[] = {{"Q", Q, tq, d.qs, q}, {"K", K, tk, d.ks, kv}, {"V", V, tk, d.vs, kv}, {"O", O, tq, q, q},
-                        {"dO", dO, tq, q, q}, {"lse", lse, tq, d.Hq, d.Hq, 4}};
+                        {"dO", dO, tq, q, q}, {"lse", lse, tq, d.Hq, d.Hq, 4}, flat("len", len, d.B, 4)};
   const Span out[] = {{"dQ", dQ, tq, q, q}, {"dK", dK, tk, kv, kv}, {"dV", dV, tk, kv, kv},
-                      {"workspace", ws, 1, 0, static_cast<int64_t>(window_ws_bytes(d, PISA_WINDOW_BWD)), 1}};
+                      flat("workspace", ws, static_cast<int64_t>(window_ws_bytes(d, PISA_WINDOW_BWD)), 1)};
   PISA_CHECK(check_apart(spans, out));
   return cuda_rc(pisa::launch_window_bwd(d, Q, K, V, O, lse, dO, len, dQ, dK, dV, static_cast<char*>(ws), stream),
                  "pisa_window_attn_bwd");
@@ -548,6 +557,11 @@ int pisa_window_decode_step(const pisa_window_decode_shape_t* shape, const int32
   const char* names[] = {"pos", "Kcache", "Vcache", "q", "k_new", "v_new", "o", "status"};
   for (int k = 0; k < 8; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
   PISA_CHECK(check_ptr(lse, "lse", true));
+  const int64_t qn = static_cast<int64_t>(d.B) * d.Hq, kn = static_cast<int64_t>(d.B) * d.Hkv * d.d;
+  const Span read[] = {flat("q", q, qn * d.d, 2), flat("k_new", k_new, kn, 2), flat("v_new", v_new, kn, 2), flat("pos", pos, d.B, 4)};
+  const Span out[] = {flat("o", o, qn * d.d, 2), flat("lse", lse, qn, 4), flat("status", status, 1, 4),
+                      flat("Kcache", Kcache, kn * d.Ncap, 2), flat("Vcache", Vcache, kn * d.Ncap, 2)};
+  PISA_CHECK(check_apart(read, out, 1));
   return cuda_rc(pisa::launch_window_decode(d, pos, Kcache, Vcache, q, k_new, v_new, o, lse, status, stream),
                  "pisa_window_decode_step");
 }
@@ -568,9 +582,10 @@ int pisa_qk_norm_rope(const pisa_rope_shape_t* shape, const void* Q, const void*
   if ((Qr == Q && d.qs != static_cast<int64_t>(d.Hq) * d.d) || (Kr == K && d.ks != static_cast<int64_t>(d.Hkv) * d.d))
     return fail(PISA_EINVAL, "in place needs a contiguous Q and K");
   const int64_t t = static_cast<int64_t>(d.B) * d.N, q = static_cast<int64_t>(d.Hq) * d.d, k = static_cast<int64_t>(d.Hkv) * d.d;
-  const Span in[] = {{"Q", Q, t, d.qs, q}, {"K", K, t, d.ks, k}};
+  const Span in[] = {{"Q", Q, t, d.qs, q}, {"K", K, t, d.ks, k}, flat("inv_freq", inv_freq, d.rot / 2, 4),
+                     flat("q_weight", q_weight, d.d, 4), flat("k_weight", k_weight, d.d, 4), flat("pos", pos, t, 4)};
   const Span out[] = {{"Qr", Qr, t, q, q}, {"Kr", Kr, t, k, k}};
-  PISA_CHECK(check_apart(in, out, true));
+  PISA_CHECK(check_apart(in, out, 2));
   return cuda_rc(pisa::launch_rope(d, Q, K, inv_freq, q_weight, k_weight, pos, Qr, Kr, stream), "pisa_qk_norm_rope");
 }
 
@@ -599,9 +614,12 @@ int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const v
   if (dQ == Q || dK == K) return fail(PISA_EINVAL, "dQ and dK must not be Q and K");
   PISA_CHECK(check_ws_bytes(pisa::rope_bwd_ws(d), ws, ws_bytes));
   const int64_t t = static_cast<int64_t>(d.B) * d.N, q = static_cast<int64_t>(d.Hq) * d.d, k = static_cast<int64_t>(d.Hkv) * d.d;
-  const Span grads[] = {{"dQr", dQr, t, q, q}, {"dKr", dKr, t, k, k}, {"Q", Q, t, d.qs, q}, {"K", K, t, d.ks, k}};
-  const Span out[] = {{"dQ", dQ, t, q, q}, {"dK", dK, t, k, k}};
-  PISA_CHECK(check_apart(grads, out, true));
+  const Span read[] = {{"dQr", dQr, t, q, q}, {"dKr", dKr, t, k, k}, {"Q", Q, t, d.qs, q}, {"K", K, t, d.ks, k},
+                       flat("inv_freq", inv_freq, d.rot / 2, 4), flat("q_weight", q_weight, d.d, 4),
+                       flat("k_weight", k_weight, d.d, 4), flat("pos", pos, t, 4)};
+  const Span out[] = {{"dQ", dQ, t, q, q}, {"dK", dK, t, k, k}, flat("dq_weight", dq_weight, d.d, 4),
+                      flat("dk_weight", dk_weight, d.d, 4), flat("workspace", ws, static_cast<int64_t>(pisa::rope_bwd_ws(d)), 1)};
+  PISA_CHECK(check_apart(read, out, 2));
   return cuda_rc(pisa::launch_rope_bwd(d, Q, K, dQr, dKr, inv_freq, q_weight, k_weight, pos, dQ, dK, dq_weight,
                                        dk_weight, static_cast<char*>(ws), stream),
                  "pisa_qk_norm_rope_bwd");

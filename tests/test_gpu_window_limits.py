@@ -57,3 +57,17 @@ def test_sinks_that_meet_the_window_are_full_causal_attention(window, sinks):
     a, b = _run(Q, K, V, dO, window, sinks, [700, 431]), _run(Q, K, V, dO, 700, 0, [700, 431])
     for n in a:
         assert torch.equal(a[n], b[n]), n
+
+
+def test_decode_output_in_place_of_the_query():
+    B, Ncap, Hq, Hkv, d = 3, 400, 32, 2, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(bf16)       # noqa: E731
+    Kc, Vc, q, k, v = rnd(B, Ncap, Hkv, d), rnd(B, Ncap, Hkv, d), rnd(B, Hq, d), rnd(B, Hkv, d), rnd(B, Hkv, d)
+    shape = pisa.make_window_decode_shape(B, Ncap, Hq, Hkv, d, 300, 4)
+    pos = torch.tensor([399, 20, 5000], dtype=torch.int32, device="cuda")
+    want = pisa.window_decode_step(shape, pos, Kc.clone(), Vc.clone(), q, k, v)
+    got = pisa.window_decode_step(shape, pos, Kc, Vc, q, k, v, o=q)
+    assert got[0] is q and torch.equal(q, want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(pisa.PisaError, match="Kcache overlaps lse"):
+        pisa.window_decode_step(shape, pos, Kc, Vc, q, k, v, lse=Kc.view(torch.float32).reshape(-1)[:B * Hq].reshape(B, Hq))

@@ -1,10 +1,12 @@
 """Limits of the window attention and of the query/key norm without a GPU: sizes of workspaces,
 refusals of calls that would read or write the wrong memory."""
+import ctypes
 import random
 
 import pytest
 
 import pyramid_top_selection_gb300 as pisa
+from pyramid_top_selection_gb300 import _pisa
 
 # ------------------------------------------------------------------------ workspace of the backward
 # Partial sums: a key tile is cut into runs of at least a 912th of all the row tiles, and at least 16 of them,
@@ -47,3 +49,50 @@ def test_backward_workspace_is_bounded():
 def test_sinks_that_meet_the_window_are_full_causal_attention():
     for N, window, sinks in ((32768, 128, 32768), (32768, 128, 32640), (5000, 4999, 1), (5000, 1, 4999), (1, 1, 1)):
         assert _backward_bytes(2, N, N, 8, 2, 128, window, sinks) == _backward_bytes(2, N, N, 8, 2, 128, N, 0)
+
+
+# ------------------------------------------------------------------------------- overlapping buffers
+A = 1 << 24        # fake, 16-byte aligned addresses: never dereferenced
+
+
+def _overlaps(fn, shape, names, sizes, written, may_be, tail=(None,)):
+    """Every buffer in `written` laid over every other one, at its first and its last 16 bytes, is refused by
+    name; `may_be`: pairs (written, read) that may be the same buffer (or are refused in other words), but not lie askew."""
+    far = {n: A + (k << 20) for k, n in enumerate(names)}
+    for w in written:
+        for r in names:
+            if r == w:
+                continue
+            for at in (0, max(16, -(-sizes[r] // 16) * 16) - 16):
+                if ((w, r) in may_be or (r, w) in may_be) and at == 0:
+                    continue
+                args = [far[r] + at if n == w else far[n] for n in names]
+                rc = fn(ctypes.byref(shape), *args, *tail)
+                msg = pisa.lib().pisa_last_error().decode()
+                assert rc == _pisa.PISA_EINVAL and (f"{w} overlaps {r}" in msg or f"{r} overlaps {w}" in msg), (w, r, rc, msg)
+
+
+def test_every_overlap_is_refused():
+    # 100 tokens, 4 query heads over 4 KV heads of 64: 51200 bytes a tensor
+    L, t = pisa.lib(), 100 * 4 * 64 * 2
+    s = pisa.make_window_shape(1, 100, 100, 4, 4, 64, 10)
+    need = pisa.window_workspace_size(s, pisa.WINDOW_BWD)
+    fwd = ["Q", "K", "V", "len", "O", "lse", "workspace"]
+    size = dict(Q=t, K=t, V=t, O=t, dO=t, dQ=t, dK=t, dV=t, len=4, lse=1600)
+    _overlaps(L.pisa_window_attn_fwd, s, fwd, size | dict(workspace=256), ["O", "lse", "workspace"], [], (256, None))
+    bwd = ["Q", "K", "V", "O", "lse", "dO", "len", "dQ", "dK", "dV", "workspace"]
+    _overlaps(L.pisa_window_attn_bwd, s, bwd, size | dict(workspace=need), bwd[7:], [], (need, None))
+    dec = ["pos", "Kcache", "Vcache", "q", "k_new", "v_new", "o", "lse", "status"]
+    size = dict(pos=8, Kcache=2 * t, Vcache=2 * t, q=1024, k_new=1024, v_new=1024, o=1024, lse=32, status=4)
+    _overlaps(L.pisa_window_decode_step, pisa.make_window_decode_shape(2, 100, 4, 4, 64, 10), dec, size,
+              ["Kcache", "Vcache", "o", "lse", "status"], [("o", "q")])
+    r = pisa.make_rope_shape(1, 100, 4, 4, 64, 64)
+    size = dict(Q=t, K=t, Qr=t, Kr=t, dQr=t, dKr=t, dQ=t, dK=t, inv_freq=128, q_weight=256, k_weight=256, pos=400,
+                dq_weight=256, dk_weight=256)
+    _overlaps(L.pisa_qk_norm_rope, r, ["Q", "K", "inv_freq", "q_weight", "k_weight", "pos", "Qr", "Kr"], size,
+              ["Qr", "Kr"], [("Qr", "Q"), ("Kr", "K")])
+    b = ctypes.c_size_t()
+    assert L.pisa_qk_norm_rope_workspace_size(ctypes.byref(r), ctypes.byref(b)) == 0
+    bwd = ["Q", "K", "dQr", "dKr", "inv_freq", "q_weight", "k_weight", "pos", "dQ", "dK", "dq_weight", "dk_weight", "workspace"]
+    _overlaps(L.pisa_qk_norm_rope_bwd, r, bwd, size | dict(workspace=b.value), bwd[8:], [("dQ", "dQr"), ("dK", "dKr"), ("dQ", "Q"), ("dK", "K")],
+              (b.value, None))
