@@ -321,11 +321,14 @@ def decode_step(shape: DecodeShape, pos, Kcache, Vcache, pyr, q, k_new, v_new, o
                 score=None, status=None, rope: Rope | None = None):
     """One fused decode step (append + ancestor update + select + attend) for all sequences.
 
-    With `rope`, q and k_new are raw projections: they are normed and rotated at `pos` first
-    (qk_norm_rope, one more launch)."""
+    With `rope`, q and k_new are raw projections (slices of a fused one, if need be): they are normed and
+    rotated at `pos` first (qk_norm_rope, one more launch). What the step itself reads is contiguous."""
     dev = q.device
+    _need(v_new, torch.bfloat16, "v_new")
     if rope is not None:
         q, k_new = _ready_token(rope, q, k_new, pos)
+    _need(q, torch.bfloat16, "q")
+    _need(k_new, torch.bfloat16, "k_new")
     o = o if o is not None else torch.empty_like(q)
     idx = idx if idx is not None else torch.empty(shape.B, shape.Hkv, shape.K, dtype=torch.int32, device=dev)
     status = status if status is not None else torch.zeros(4, dtype=torch.int32, device=dev)
@@ -472,8 +475,9 @@ def window_decode_step(shape: WindowDecodeShape, pos, Kcache, Vcache, q, k_new, 
                        status=None, rope: Rope | None = None):
     """One decode step of the window attention: append at the slot of pos, attend. Returns o, lse, status.
 
-    The cache rolls once positions reach its capacity (see pisa.h). With `rope`, q and k_new are
-    raw projections: they are normed and rotated at `pos` first (qk_norm_rope, one more launch)."""
+    The cache rolls once positions reach its capacity (see pisa.h). With `rope`, q and k_new are raw
+    projections (slices of a fused one, if need be): they are normed and rotated at `pos` first
+    (qk_norm_rope, one more launch). What the step itself reads is contiguous."""
     dev = q.device
     B, H = shape.B, (shape.B, shape.Hkv, shape.d)
     cache = (B, shape.Ncap, shape.Hkv, shape.d)

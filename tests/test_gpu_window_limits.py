@@ -71,3 +71,31 @@ def test_decode_output_in_place_of_the_query():
     assert got[0] is q and torch.equal(q, want[0]) and torch.equal(got[1], want[1])
     with pytest.raises(pisa.PisaError, match="Kcache overlaps lse"):
         pisa.window_decode_step(shape, pos, Kc, Vc, q, k, v, lse=Kc.view(torch.float32).reshape(-1)[:B * Hq].reshape(B, Hq))
+
+
+def test_decode_steps_from_slices_of_a_projection():
+    # with `rope`, q and k_new may be slices; a v_new that is one is refused by both steps, not misread
+    B, Ncap, Hq, Hkv, d, L = 2, 512, 8, 2, 128, 200
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(bf16)       # noqa: E731
+    Kc, Vc, x = rnd(B, Ncap, Hkv, d), rnd(B, Ncap, Hkv, d), rnd(B, Hq + 2 * Hkv, d)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    rope = pisa.Rope(pisa.rope_frequencies(d)[0].cuda(), d)
+    pos = torch.tensor([L, L - 60], dtype=torch.int32, device="cuda")
+    dshape, wshape = pisa.make_decode_shape(B, Ncap, Hq, Hkv, d, 64, 4), pisa.make_window_decode_shape(B, Ncap, Hq, Hkv, d, 64, 4)
+
+    def selected(q, k, v):
+        K, V = Kc.clone(), Vc.clone()
+        return (*pisa.decode_step(dshape, pos, K, V, pisa.decode_build_pyramid(K, pos, dshape), q, k, v, rope=rope)[:2], K, V)
+
+    def window(q, k, v):
+        K, V = Kc.clone(), Vc.clone()
+        return (*pisa.window_decode_step(wshape, pos, K, V, q, k, v, rope=rope)[:2], K, V)
+
+    for step in (selected, window):
+        for a, b in zip(step(q, k, v.contiguous()), step(q.contiguous(), k.contiguous(), v.contiguous())):
+            assert torch.equal(a, b)
+        with pytest.raises(ValueError, match="v_new must be"):
+            step(q, k, v)
+    with pytest.raises(ValueError, match="q must be"):
+        pisa.decode_step(dshape, pos, Kc, Vc, pisa.decode_build_pyramid(Kc, pos, dshape), q, k.contiguous(), v.contiguous())

@@ -4,6 +4,7 @@ import ctypes
 import random
 
 import pytest
+import torch
 
 import pyramid_top_selection_gb300 as pisa
 from pyramid_top_selection_gb300 import _pisa
@@ -96,3 +97,18 @@ def test_every_overlap_is_refused():
     bwd = ["Q", "K", "dQr", "dKr", "inv_freq", "q_weight", "k_weight", "pos", "dQ", "dK", "dq_weight", "dk_weight", "workspace"]
     _overlaps(L.pisa_qk_norm_rope_bwd, r, bwd, size | dict(workspace=b.value), bwd[8:], [("dQ", "dQr"), ("dK", "dKr"), ("dQ", "Q"), ("dK", "K")],
               (b.value, None))
+
+
+# --------------------------------------------------------------------------------- token inputs of a step
+def test_decode_step_refuses_token_slices():
+    # a token's values as a slice of a fused projection lie H d apart, and the step reads them in a row: with
+    # `rope`, q and k_new may be such slices (they pass through the norm), v_new may not
+    B, Hq, Hkv, d = 2, 4, 2, 64
+    x = torch.zeros(B, Hq + 2 * Hkv, d, dtype=torch.bfloat16)
+    q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    cache, pos = torch.zeros(B, 64, Hkv, d, dtype=torch.bfloat16), torch.zeros(B, dtype=torch.int32)
+    shape = pisa.make_decode_shape(B, 64, Hq, Hkv, d, 64, 1)
+    pyr = torch.zeros(B, Hkv, 1, d)
+    for rope in (None, pisa.Rope(torch.zeros(32), d)):
+        with pytest.raises(ValueError, match="v_new must be"):
+            pisa.decode_step(shape, pos, cache, cache, pyr, q, k, v, rope=rope)
