@@ -66,6 +66,10 @@ struct DecodeSmem {
   static_assert(WARP >= OUT, "the warp's results fit its stages");
 };
 
+// What a running maximum stands for in an exponent: as long as every score was -inf, nothing is to be
+// subtracted, and 2^-inf is 0 as it should be.
+__device__ __forceinline__ float base_of(float m) { return m > neg_inf() ? m : 0.f; }
+
 // One CTA's results, read by the others of its cluster.
 template <int D>
 struct Joined {
@@ -173,8 +177,8 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
       float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(m[e], top[e]);                    // finite: every chunk has a visible key
-        f[e] = tc::ex2(m[e] - mn);
+        const float mn = fmaxf(m[e], top[e]);
+        f[e] = tc::ex2(m[e] - base_of(mn));
         m[e] = mn;
         l[e] *= f[e];
       }
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = tc::ex2(x[e] - m[e & 1]);
+    for (int e = 0; e < 4; ++e) x[e] = tc::ex2(x[e] - base_of(m[e & 1]));
     l[0] += x[0] + x[2];
     l[1] += x[1] + x[3];
     const uint32_t b0 = transpose8(pack_bf16(x[0], x[1])), b1 = transpose8(pack_bf16(x[2], x[3]));
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float* r = reinterpret_cast<const float*>(sm + w * M::WARP);
-      const float f = mm > neg_inf() ? tc::ex2(r[kHeads * D + h] - mm) : 0.f;
+      const float f = tc::ex2(r[kHeads * D + h] - base_of(mm));
       oo += f * r[x];
       ll += f * r[kHeads * D + kHeads + h];
     }
@@ -246,11 +250,12 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const WinDec
     float mm = neg_inf(), ll = 0.f, oo = 0.f;
     for (int c = 0; c < splits; ++c) mm = fmaxf(mm, win::ld_cluster_f(&s_join.m[h], c));
     for (int c = 0; c < splits; ++c) {
-      const float f = tc::ex2(win::ld_cluster_f(&s_join.m[h], c) - mm);
+      const float f = tc::ex2(win::ld_cluster_f(&s_join.m[h], c) - base_of(mm));
       oo += f * win::ld_cluster_f(&s_join.o[h][x % D], c);
       ll += f * win::ld_cluster_f(&s_join.l[h], c);
     }
-    a.o[(static_cast<int64_t>(b) * s.Hq + h0 + h) * D + x % D] = __float2bfloat16_rn(oo / ll);
+    const float out = ll == 0.f ? 0.f : oo / ll;                 // 0: all scores were -inf
+    a.o[(static_cast<int64_t>(b) * s.Hq + h0 + h) * D + x % D] = __float2bfloat16_rn(out);
     if (x % D == 0 && a.lse) a.lse[static_cast<int64_t>(b) * s.Hq + h0 + h] = (mm + log2f(ll)) * kLn2;
   }
   win::cluster_sync();                                                // nobody leaves while its results are read

@@ -99,3 +99,29 @@ def test_decode_steps_from_slices_of_a_projection():
             step(q, k, v)
     with pytest.raises(ValueError, match="q must be"):
         pisa.decode_step(dshape, pos, Kc, Vc, pisa.decode_build_pyramid(Kc, pos, dshape), q, k.contiguous(), v.contiguous())
+
+
+@pytest.mark.parametrize("first,end", [(0, 64), (16, 32), (0, 299), (100, 300), (0, 300)])
+@pytest.mark.parametrize("Hq,d", [(6, 64), (32, 128)])
+def test_logits_of_minus_infinity(first, end, Hq, d):
+    # keys with scores of -inf weigh nothing, though they be all that one warp of the decode step, or one key tile
+    # of the forward, has: as if these keys were not there; a row of nothing else is an empty one
+    N, Hkv = 300, 2
+    Q, K, V, _ = _inputs(1, N, N, Hq, Hkv, d, seed=12)
+    Q[..., 0] = 1.0
+    K[:, first:end, :, 0] = -math.inf
+    O, lse = pisa.window_attn_fwd(Q, K, V, pisa.window_shape_of(Q, K, V, N))
+    shape = pisa.make_window_decode_shape(1, N, Hq, Hkv, d, N)
+    k, v = K[:, -1].clone(), V[:, -1].clone()
+    o, l, _ = pisa.window_decode_step(shape, torch.tensor([N - 1], dtype=torch.int32, device="cuda"), K.clone(), V.clone(),
+                                      Q[:, -1].contiguous(), k, v)
+    seen = [j for j in range(N) if not first <= j < end]
+    if not seen:
+        want = {"O": torch.zeros(1, 1, Hq, d, device="cuda"), "lse": torch.full((1, Hq, 1), -math.inf, device="cuda")}
+        tol = {n: torch.zeros_like(x) for n, x in want.items()}
+    else:
+        want, tol = attention(Q[:, -1:], K[:, seen], V[:, seen], len(seen), 0)
+    check("O", O[:, -1:], want["O"], tol["O"])
+    check("lse", lse[..., -1:], want["lse"], tol["lse"])
+    check("o", o, want["O"][:, 0], tol["O"][:, 0])
+    check("l", l, want["lse"][..., 0], tol["lse"][..., 0])
