@@ -361,8 +361,9 @@ int pisa_window_decode_step(const pisa_window_decode_shape_t* shape, const int32
  * (c, c + rot/2) with interleaved = 0, turns by the angle pos * inv_freq[c] and is multiplied
  * by rot_scale:
  *     (a, b) -> rot_scale (a cos - b sin, a sin + b cos);
- * elements rot .. d-1 pass unturned. pos * inv_freq is formed exactly (fixed point, modulo a
- * turn) for every int32 position, so far positions lose nothing.
+ * elements rot .. d-1 pass unturned. pos * inv_freq is formed in fixed point
+ * modulo a turn, to within 2^-31 turns for every int32 position and finite inv_freq, so far positions
+ * lose nothing.
  * d in {64, 128}; rot a multiple of 16 in [0, d]; B*N*(Hq+Hkv) < 2^31. q_stride, k_stride: the
  * distance between consecutive tokens in elements, as in pisa_window_shape_t. rot_scale 0
  * selects 1. */

@@ -17,7 +17,8 @@
 //
 // Angles: pos * inv_freq / (2 pi) is needed modulo 1, and a float product would lose the fraction
 // of far positions (at position 10^6 by 0.03 turns). inv_freq / (2 pi) is held as a 64-bit binary
-// fraction of a turn; its product with the position modulo 2^64 is exact integer arithmetic.
+// fraction of a turn, of which its product with the position keeps 32 bits exactly (2^-63 of a turn off times
+// 2^31: within 2^-31 of a turn for every position and frequency, cut to 32 bits included).
 #include <algorithm>
 
 #include "device.cuh"
@@ -47,17 +48,23 @@ struct RopeArgs {
   int64_t tokens;
 };
 
-// x / (2 pi) as a 64-bit fraction of a turn (modulo 1): x = m 2^e with a 24-bit m, times the
-// first 64 binary digits of 1 / (2 pi).
+// x / (2 pi) as a 64-bit fraction of a turn (modulo 1), for any finite x, to within 2^-63: x = m 2^-sh with a
+// 24-bit m, times 128 of the first 256 binary digits of 1 / (2 pi). Where x is a multiple of 2^up, the first `up`
+// digits make whole turns and are passed over. (The digits are immediates: read from constant memory they
+// delayed the kernel's start by 1 us.)
 __device__ __forceinline__ uint64_t turns64(float x) {
   const uint32_t bits = __float_as_uint(x);
   const int ex = (bits >> 23) & 255;
   const uint64_t m = ex ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
-  const uint64_t inv2pi = 0x28BE60DB9391054Aull;
-  const uint64_t lo = m * inv2pi, hi = __umul64hi(m, inv2pi);
-  const int sh = 150 - (ex ? ex : 1);            // x = m 2^-sh
+  const int sh = 150 - (ex ? ex : 1), up = max(0, -sh);
+  const bool far = up >= 64;
+  const uint64_t d0 = far ? 0x7F09D5F47D4D3770ull : 0x28BE60DB9391054Aull, d1 = far ? 0x36D8A5664F10E410ull : 0x7F09D5F47D4D3770ull,
+                 d2 = far ? 0x7F9458EAF7AEF158ull : 0x36D8A5664F10E410ull;
+  auto digits = [&](uint64_t a, uint64_t b) { return up & 63 ? a << (up & 63) | b >> (64 - (up & 63)) : a; };
+  const uint64_t first = digits(d0, d1), carry = __umul64hi(m, digits(d1, d2)), lo = m * first + carry,
+                 hi = __umul64hi(m, first) + (lo < carry);
   uint64_t t;
-  if (sh <= 0) t = sh > -64 ? lo << -sh : 0;
+  if (sh <= 0) t = lo;
   else if (sh < 64) t = (hi << (64 - sh)) | (lo >> sh);
   else t = sh < 128 ? hi >> (sh - 64) : 0;
   return bits >> 31 ? 0 - t : t;

@@ -125,3 +125,47 @@ def test_logits_of_minus_infinity(first, end, Hq, d):
     check("lse", lse[..., -1:], want["lse"], tol["lse"])
     check("o", o, want["O"][:, 0], tol["O"][:, 0])
     check("l", l, want["lse"][..., 0], tol["lse"][..., 0])
+
+
+def _inv_2pi(bits):
+    """1 / (2 pi) as an integer over 2^bits, by Machin's formula."""
+    one = 1 << (bits + 64)
+
+    def arctan_of_one_over(x):
+        t = s = one // x
+        n = 1
+        while t:
+            t //= -x * x
+            n += 2
+            s += t // n
+        return s
+
+    pi = 4 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239))
+    return (one << bits) // (2 * pi)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_of_any_frequency_and_position(interleaved):
+    # pairs (1, 0) turned by pos * inv_freq, against integer arithmetic with 512 digits of 1 / (2 pi)
+    f = torch.tensor([1.0, 0.1, 3.7e-5, 2.0 ** -40, 1e-38, 0.0, -0.75, 1000.5, 65536.25, -12345.678, 1e7, 2.0 ** 24 + 2, 1.7e12,
+                      -3.1e19, 2.5e30, 3.4e38])
+    pos = [0, 1, -1, 12345, 10**6 + 3, 2**24 + 1, 2**31 - 1, -2**31, -2**31 + 7, 1999999999]
+    x = torch.zeros(1, len(pos), 1, 64, dtype=bf16, device="cuda")
+    x[..., 0:32:2 if interleaved else 1] = 1.0
+    if not interleaved:
+        x[..., 16:32] = 0.0
+    p = torch.tensor([pos], dtype=torch.int32, device="cuda")
+    y, z = pisa.qk_norm_rope(x, x, f.cuda(), pisa.rope_shape_of(x, x, 32, interleaved, norm=False), pos=p)
+    assert torch.equal(y, z)
+    y = y[0, :, 0, :32].double().cpu()
+    c, s = (y[:, 0::2], y[:, 1::2]) if interleaved else (y[:, :16], y[:, 16:])
+    inv = _inv_2pi(512)
+    want = torch.zeros(2, len(pos), 16, dtype=torch.float64)
+    for i, q in enumerate(pos):
+        for k, v in enumerate(f.tolist()):
+            num, den = v.as_integer_ratio()
+            turns = (q * num * inv // den) % (1 << 512) / (1 << 512)
+            want[:, i, k] = torch.tensor([math.cos(2 * math.pi * turns), math.sin(2 * math.pi * turns)])
+    # bf16's half step, and 2^-18 for the angle in fp32 (2^-24 of pi) and its cosine and sine (2^-21)
+    for got, w in ((c, want[0]), (s, want[1])):
+        assert float(((got - w).abs() - 2.0 ** -8 * w.abs()).max()) <= 2.0 ** -18
