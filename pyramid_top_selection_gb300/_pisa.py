@@ -391,8 +391,18 @@ def _need_ws(ws, dev) -> None:
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev} (got {ws.dtype}, {ws.device})")
 
 
+def _need_int32(**sizes) -> None:
+    """Sizes have to fit the C struct's int32 (ctypes would keep their low 32 bits)."""
+    bad = [f"{n}={v}" for n, v in sizes.items() if not -0x80000000 <= v <= 0x7fffffff]
+    if bad:
+        raise ValueError(f"sizes must fit 32 bits (got {', '.join(bad)})")
+
+
 def make_window_shape(B, Nq, N, Hq, Hkv, d, window, sinks=0, scale=0.0, q_stride=0, k_stride=0,
                       v_stride=0) -> WindowShape:
+    if not 0 <= B | Nq | N | Hq | Hkv | d | window | sinks | q_stride | k_stride | v_stride <= 0x7fffffff:
+        _need_int32(B=B, Nq=Nq, N=N, Hq=Hq, Hkv=Hkv, d=d, window=window, sinks=sinks, q_stride=q_stride, k_stride=k_stride,
+                    v_stride=v_stride)
     return WindowShape(B, Nq, N, Hq, Hkv, d, window, sinks, float(scale), q_stride, k_stride, v_stride)
 
 
@@ -468,6 +478,8 @@ def window_attn_bwd(Q, K, V, O, lse, dO, shape: WindowShape, lens=None, ws=None)
 
 
 def make_window_decode_shape(B, Ncap, Hq, Hkv, d, window, sinks=0, scale=0.0) -> WindowDecodeShape:
+    if not 0 <= B | Ncap | Hq | Hkv | d | window | sinks <= 0x7fffffff:
+        _need_int32(B=B, Ncap=Ncap, Hq=Hq, Hkv=Hkv, d=d, window=window, sinks=sinks)
     return WindowDecodeShape(B, Ncap, Hq, Hkv, d, window, sinks, float(scale))
 
 
@@ -508,6 +520,8 @@ def window_decode_step(shape: WindowDecodeShape, pos, Kcache, Vcache, q, k_new, 
 
 def make_rope_shape(B, N, Hq, Hkv, d, rot, interleaved=False, norm=True, eps=1e-6, rot_scale=1.0, q_stride=0,
                     k_stride=0) -> RopeShape:
+    if not 0 <= B | N | Hq | Hkv | d | rot | q_stride | k_stride <= 0x7fffffff:
+        _need_int32(B=B, N=N, Hq=Hq, Hkv=Hkv, d=d, rot=rot, q_stride=q_stride, k_stride=k_stride)
     return RopeShape(B, N, Hq, Hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, float(eps), float(rot_scale),
                      q_stride, k_stride)
 

@@ -112,3 +112,20 @@ def test_decode_step_refuses_token_slices():
     for rope in (None, pisa.Rope(torch.zeros(32), d)):
         with pytest.raises(ValueError, match="v_new must be"):
             pisa.decode_step(shape, pos, cache, cache, pyr, q, k, v, rope=rope)
+
+
+# ---------------------------------------------------------------------------------------------- sizes
+@pytest.mark.parametrize("make,kw", [
+    (pisa.make_window_shape, dict(B=1, Nq=8, N=8, Hq=2, Hkv=1, d=64, window=4, sinks=0, q_stride=0, k_stride=0, v_stride=0)),
+    (pisa.make_window_decode_shape, dict(B=1, Ncap=8, Hq=2, Hkv=1, d=64, window=4, sinks=0)),
+    (pisa.make_rope_shape, dict(B=1, N=8, Hq=2, Hkv=1, d=64, rot=64, q_stride=0, k_stride=0)),
+])
+def test_sizes_past_32_bits_are_refused(make, kw):
+    # ctypes would keep the low 32 bits: a window of 2^32 + 4 "for no limit" would be one of 4 keys
+    make(**kw)
+    for n in kw:
+        for bad in (2 ** 32 + kw[n], -2 ** 32 + kw[n], 2 ** 31):
+            with pytest.raises(ValueError, match=n):
+                make(**{**kw, n: bad})
+    if "window" in kw:
+        assert make(**{**kw, "window": 2 ** 31 - 1}).window == 2 ** 31 - 1
