@@ -151,17 +151,15 @@ struct KeyList {
   __device__ __forceinline__ int key(int v) const { return v < SP ? v : lo + v - SP; }
 };
 
-// The 128-column tiles j of a key list that hold a key some position in [p0, p1) sees: those of the
-// sinks and of the window.
+// The 128-column tiles of a key list that hold a key some position in [p0, p1) sees are those from `first` to
+// `last`, and those of the sinks before them.
 struct TileRange {
-  int first, last, sink;
+  int first, last;
   __device__ __forceinline__ TileRange(const WinDims& s, const KeyList& kl, int L, int p0, int p1) {
     const int end = min(p1, L) - 1;
     last = end < p0 ? -1 : (kl.SP + end - kl.lo) >> 7;
     first = (kl.SP + max(kl.lo, p0 - s.window + 1) - kl.lo) >> 7;
-    sink = (s.sinks + 127) >> 7;
   }
-  __device__ __forceinline__ bool has(int j) const { return j <= last && (j >= first || j < sink); }
 };
 
 // A work item as its CTA's roles take it: decoded by one warp, ahead of the others (the divisions would
