@@ -22,6 +22,7 @@
 #include <algorithm>
 
 #include "device.cuh"
+#include "internal.h"
 #include "profile.h"
 #include "window_tc.cuh"
 
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int
 
 int bwd_blocks(const RopeDims& s) {
   const int64_t need = (static_cast<int64_t>(s.B) * s.N + kWarps - 1) / kWarps;
-  return static_cast<int>(std::min<int64_t>(need, 152 * kBwdBlocks));
+  return static_cast<int>(std::min<int64_t>(need, win::kPlanSms * kBwdBlocks));
 }
 
 template <template <int, bool, bool> class Launch, class... A>
@@ -519,10 +520,10 @@ int launch_rope(const RopeDims& s, const void* Q, const void* K, const float* in
   const int H = s.Hq + s.Hkv, rpw = 256 / s.d;
   // all heads of a token to one warp where the tokens alone fill the GPU's warps; else a warp
   // takes one round of rows
-  const int64_t slots = 152 * kFwdBlocks * kWarps;
+  const int64_t room = sm_count() * kFwdBlocks, slots = room * kWarps;
   a.heads_per_warp = a.tokens >= slots ? H : rpw;
   const int64_t work = a.tokens * ((H + a.heads_per_warp - 1) / a.heads_per_warp);
-  const int blocks = static_cast<int>(std::min<int64_t>((work + kWarps - 1) / kWarps, 152 * kFwdBlocks));
+  const int blocks = static_cast<int>(std::min<int64_t>((work + kWarps - 1) / kWarps, room));
   return by_kind<FwdLaunch>(s, a, blocks, static_cast<cudaStream_t>(stream));
 }
 

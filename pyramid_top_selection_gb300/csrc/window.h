@@ -12,6 +12,10 @@ namespace pisa {
 
 namespace win {
 
+// The SM count that plans with a host-only size query go by, which have to give the same sizes without a GPU
+// (launches ask sm_count()).
+constexpr int kPlanSms = 152;
+
 // A kernel's dynamic shared memory, raised once per device (the attribute stays with the device's
 // context, and the call costs as much as a launch); `regs` registers a thread must have been compiled.
 // `wide_cluster`: clusters of more than 8 CTAs are launched.

@@ -999,11 +999,12 @@ void plan(BwdArgs& a) {
   const int64_t all = (s.Nq + 3 + a.tok - 1) / a.tok;                       // token tiles of every row
   const int64_t band = std::min(all, (int64_t(s.window) + 130 + a.tok - 1) / a.tok);
   const int64_t tiles = static_cast<int64_t>(a.n_kt) * a.n_bh, total = band * a.sets * tiles;
+  constexpr int kSms = win::kPlanSms;
   // row tiles of an item: a sixth of a CTA's share, at least 16; a small problem (under 32 a CTA) whose
   // key tiles leave CTAs idle is cut into as many equal runs as there are CTAs for
-  int64_t want = std::max<int64_t>(16, total / (152 * 6));
-  const bool small = total < 152 * 32 && tiles < 152;
-  if (small) want = (band * a.sets + 152 / tiles - 1) / (152 / tiles);
+  int64_t want = std::max<int64_t>(16, total / (kSms * 6));
+  const bool small = total < kSms * 32 && tiles < kSms;
+  if (small) want = (band * a.sets + kSms / tiles - 1) / (kSms / tiles);
   a.ct = static_cast<int>(std::min(band, (want + a.sets - 1) / a.sets));
   a.nck = static_cast<int>((band + a.ct - 1) / a.ct);
   a.cts = a.ct;
@@ -1012,7 +1013,7 @@ void plan(BwdArgs& a) {
   if (a.n_st > 0) {              // the same shares, of all the work; in a small problem half a CTA's, if not the others' run
     const int64_t sink_tiles = static_cast<int64_t>(a.n_st) * a.n_bh;
     const int64_t work = (band * (tiles - sink_tiles) + all * sink_tiles) * a.sets;
-    const int64_t run = small ? std::max(want, work / (152 * 2)) : std::max<int64_t>(16, work / (152 * 6));
+    const int64_t run = small ? std::max(want, work / (kSms * 2)) : std::max<int64_t>(16, work / (kSms * 6));
     a.cts = static_cast<int>(std::min(all, (run + a.sets - 1) / a.sets));
     a.ncs = static_cast<int>((all + a.cts - 1) / a.cts);
     a.n_snk = a.n_st * a.n_bh * a.ncs;

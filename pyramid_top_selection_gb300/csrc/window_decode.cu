@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "device.cuh"
+#include "internal.h"
 #include "profile.h"
 #include "window_tc.cuh"
 
@@ -271,7 +272,7 @@ int decode_launch(const WinDecodeArgs& a, cudaStream_t st) {
   const int64_t units = static_cast<int64_t>(s.B) * s.Hkv * a.sets;
   const int64_t keys = std::min<int64_t>(s.Ncap, static_cast<int64_t>(s.window) + s.sinks);
   int splits = 1;
-  while (splits < 8 && units * splits * 2 <= 152 * 2 && keys > splits * kWarps * kChunk) splits *= 2;
+  while (splits < 8 && units * splits * 2 <= sm_count() * 2 && keys > splits * kWarps * kChunk) splits *= 2;
   static win::Ready ready;
   if (int e = ready(window_decode_kernel<D>, DecodeSmem<D>::bytes)) return e;
   cudaLaunchConfig_t cfg{};
