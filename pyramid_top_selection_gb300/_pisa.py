@@ -543,8 +543,10 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", fac
       "ntk"     the base raised by factor ** (rot / (rot - 2)): the lowest frequency is divided by
                 factor, the highest stays
       "yarn"    by parts (YaRN): pairs that turn more than `fast` times within trained_len stay, those
-                under `slow` turns are divided by factor, a linear ramp in the turns between; and
-                rot_scale = 0.1 ln(factor) + 1
+                under `slow` turns are divided by factor, a linear ramp in the turns between, as the method's
+                paper states it; and rot_scale = 0.1 ln(factor) + 1. (A model trained with a ramp over
+                the pairs' index between rounded bounds has other frequencies in between: pass its own as
+                inv_freq.)
     """
     if rot < 2 or rot % 2 or factor < 1 or base <= 0:
         raise ValueError(f"rot={rot} must be even and positive, factor={factor} at least 1, base={base} positive")

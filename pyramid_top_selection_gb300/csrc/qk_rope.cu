@@ -5,7 +5,7 @@
 // dw += g x r, dx = r (g w) - x (r^3 / d) sum(g w x).
 //
 // Bound: memory (read and write once, 2 bytes an element each way); the 64K prefill's 16 + 2 heads of
-// 128 take 102 us, 5.9 TB/s, the 16K training batch's 16 + 4 heads 110 us forward and 171 us backward.
+// 128 take 98 us, 6.2 TB/s, the 16K training batch's 16 + 4 heads 111 us forward and 169 us backward.
 // One warp takes one token and runs over its heads, Q's then K's, so that the cosines and sines, and
 // their products with the weights, are formed once per token. A row is held by d / 8 lanes, each with
 // both elements of its four pairs (in the half-split layout two runs of 8 bytes that lie rot / 2 apart),

@@ -25,7 +25,8 @@
 // P is rounded to bf16 for the product (2^-8 relative at most); the sum l takes it unrounded.
 // Bound: the MMA warp, whose four groups of products a step are issued in some 2000 cycles and then
 // waited for; the softmax is not (the time stays without any exponential). 65536 rows of 16 heads over 2, d =
-// 128, a window of 4096: 1.43 ms, 1.48 PFLOP/s, 77 % of a large library product's rate. S in two halves,
+// 128, a window of 4096: 1.48-1.52 ms a call in rows of calls, which run into the power limit (1.40-1.44 PFLOP/s,
+// 73-75 % of a large library product's burst rate), 1.43 ms in a short burst (1.49 PFLOP/s). S in two halves,
 // the upper one ahead of P's reading: 1.61 ms (64 columns cost 48 cycles a step of 16, 128 columns 64).
 // With few rows (a short chunk against a long context) the items are fewer than the SMs. An item's key
 // tiles are then cut into 2, 4, 8 or 16 runs, one CTA each, the CTAs a cluster: each lays its O, maxima

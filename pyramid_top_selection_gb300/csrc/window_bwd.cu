@@ -99,8 +99,9 @@ __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
 // short row, has all its dP in tensor memory at one time, the second tile's where dQ will be: there D
 // is the fp32 sum of P dP itself.
 //
-// 4 x 16384 rows of 16 heads over 4 KV heads, d = 128: 639 us at a window of 1024 and 4 sinks (1.26
-// PFLOP/s of its three products), 256 us for 8192 rows of 16 heads over 2, all causal (1.61).
+// 4 x 16384 rows of 16 heads over 4 KV heads, d = 128: 690 us at a window of 1024 and 4 sinks (1.16
+// PFLOP/s of its three products), 268 us for 8192 rows of 16 heads over 2, all causal (1.54); 640 and 256 us
+// in short bursts.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
@@ -591,7 +592,7 @@ struct DkvItem {
 // run under the dK and dP^T products, its dS under the next tile's dV and S^T. Each wait for a product
 // that the next one overwrites the operand of is seen some 300 cycles after its issue; dK and dP^T a
 // tile later would close these gaps, but hold two tiles' P in registers and spill (twice the time).
-// 4 x 16384 rows of 16 heads over 4, a window of 1024: 810 us, 1.32 PFLOP/s of its four products.
+// 4 x 16384 rows of 16 heads over 4, a window of 1024, 4 sinks: 829 us, 1.29 PFLOP/s of its four products.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
@@ -980,7 +981,9 @@ __global__ void __launch_bounds__(256) window_dkv_sum_kernel(const BwdArgs a, in
 // The sizes that follow from a shape. Chunks: a key tile's rows are one item where the key tiles
 // alone fill the GPU six times over; else (few heads, wide windows) runs of `ct` token tiles, whose
 // partial sums a last kernel adds. Key tiles with sinks are seen by all rows behind them and have a run
-// length of their own, `cts`. A tile that is cut has more rows than one run, so that there are less than
+// length of their own, `cts` (as long as the others', which a short window keeps short, they took 153 us of
+// partial sums and 1054 us of dK/dV at 32768 tokens, 32 heads over 8, a window of 128 and 1024 sinks, now 24
+// and 846). A tile that is cut has more rows than one run, so that there are less than
 // twice as many runs as equal shares: under 2 x 17/16 x 912 of the tiles without sinks and as many of
 // those with them, whatever the shape.
 void plan(BwdArgs& a) {
