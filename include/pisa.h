@@ -28,7 +28,7 @@
  *    PISA_EWORKSPACE and enqueues nothing. A launch failure returns PISA_ECUDA. The text
  *    of the last error of the calling thread is returned by pisa_last_error().
  *  - Supported by the selection, the selected blocks' attention and its decode step (the window
- *    attention and the query/key norm state their own): d in {64,128}, C = 64, g in {2,4} (4 for the entry points
+ *    attention, the query/key norm, the documents' attention and the paged cache state their own): d in {64,128}, C = 64, g in {2,4} (4 for the entry points
  *    named under pisa_shape_t), 1 <= K <= 32 with gK <= 64, G in {1,2,4,8},
  *    1 <= N <= 2^24, B*U*N*gK < 2^31 (U = Hkv, or Hq for a per-head selection) and
  *    B*N*Hq < 2^31. Anything else returns PISA_EUNSUPPORTED.
@@ -43,7 +43,7 @@
 extern "C" {
 #endif
 
-#define PISA_VERSION 5
+#define PISA_VERSION 6
 #define PISA_MAX_LEVELS 32
 
 enum {
@@ -395,6 +395,111 @@ int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const v
                           const void* dKr, const float* inv_freq, const float* q_weight,
                           const float* k_weight, const int32_t* pos, void* dQ, void* dK, float* dq_weight,
                           float* dk_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Attention over packed documents: the full attention of a model's global layers in training and
+ * over prompts (no counterpart on the pages; windows and selected blocks stand beside it). T tokens
+ * hold n_docs documents one behind another: document m is the tokens [starts[m], starts[m + 1]),
+ * clamped to [0, T]. Row t sees key j of its own document [s, e) iff
+ *     j <= t  or  j < s + prefix[m]
+ * (a prefix of the document sees itself whole; prefix NULL: none). Documents of no tokens and tokens before
+ * starts[0] or from starts[n_docs] on (padding) are allowed: padding's rows see nothing (O = 0, lse = -inf,
+ * dQ = dK = dV = 0) and its values are never used, whatever they are. Scores, per query head h:
+ *     x = scale q.k,   y = cap tanh(x / cap)  (cap 0: y = x),   z = y - slopes[h] |t - j|
+ * (slopes NULL: z = y), O = softmax over the visible keys of z times V, lse = log sum exp z.
+ *
+ * Q [T,Hq,d], K, V [T,Hkv,d] bf16, d and the heads contiguous, *_stride as in pisa_window_shape_t;
+ * O, dO, dQ [T,Hq,d], dK, dV [T,Hkv,d] bf16 and lse [Hq,T] fp32 contiguous; starts device
+ * [n_docs + 1] int32, not descending (else results are undefined, but nothing outside the
+ * buffers is touched); prefix device [n_docs] int32; slopes device [Hq] fp32, finite. d in {64, 128}, G = Hq / Hkv
+ * <= 64, T <= 2^24, T*Hq < 2^31, n_docs <= 2^24, cap 0 or in [2^-10, 2^20]. max_len: the longest document, as far as the caller
+ * knows (0: T); how work is cut follows it, results do not depend on it beyond the order of the sums.
+ * Nothing written (outputs, the workspace) may overlap anything that is read, nor one another.
+ * Non-finite values at one document's tokens can reach rows of another that lie within 256 tokens of it. */
+typedef struct {
+  int32_t T, Hq, Hkv, d, n_docs, max_len;
+  float scale, cap;
+  int32_t q_stride, k_stride, v_stride;
+} pisa_doc_shape_t;
+
+/* pisa_doc_workspace_size's `op`. */
+enum { PISA_DOC_FWD = 0, PISA_DOC_BWD = 1 };
+
+/* Bytes of workspace of the documents' attention (host-only). The first 256 bytes are the status
+ * block. */
+int pisa_doc_workspace_size(const pisa_doc_shape_t* shape, int op, size_t* bytes);
+
+/* O and lse. A bounded wait that gives up poisons the rows it leaves unfinished (O = NaN, lse = NaN) and sets
+ * PISA_STATUS_TIMEOUT. Workspace: PISA_DOC_FWD. */
+int pisa_doc_attn_fwd(const pisa_doc_shape_t* shape, const void* Q, const void* K, const void* V,
+                      const int32_t* starts, const int32_t* prefix, const float* slopes, void* O, float* lse,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* With P = exp(z - lse), D = dO.O and dx = P (dO.v - D) (1 - (y / cap)^2) on the visible pairs (the last
+ * factor 1 without a cap): dQ = scale dx K, dK = scale dx^T Q, dV = P^T dO; dK and dV sum over the group's
+ * heads. O and lse from the forward of the same inputs. The slopes are constants: no gradient. The sums'
+ * order is fixed. A bounded wait that gives up poisons the gradients it leaves unfinished (NaN).
+ * Workspace: PISA_DOC_BWD. */
+int pisa_doc_attn_bwd(const pisa_doc_shape_t* shape, const void* Q, const void* K, const void* V, const void* O,
+                      const float* lse, const void* dO, const int32_t* starts, const int32_t* prefix,
+                      const float* slopes, void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * A paged key/value cache: sequences of any lengths share one pool of pages, in 16 or in 4 bits (no counterpart
+ * on the pages). A page holds `page` tokens of every KV head, head by head, so that a head's tokens are one
+ * run of memory. Token p of sequence b lies in slot p % page of page table[b][p / page].
+ *   bits = 16: k, v [n_pages,Hkv,page,d] bf16.
+ *   bits = 4:  k, v [n_pages,Hkv,page,d/2] bytes of two codes, the even channel's in the low four bits;
+ *              k_scale, v_scale [n_pages,Hkv,page,d/16] e4m3, one for 16 channels; k_amp, v_amp
+ *              [Hkv] fp32, positive (NULL: ones). A code (sign, then 0, .5, 1, 1.5, 2, 3, 4 or 6; e2m1)
+ *              stands for code * scale * amp.
+ * table device [B,max_pages] int32; entries behind a sequence's last page are never read. page a power of two in
+ * [16, 1024], max_pages*page <= 2^24, d in {64, 128}, G = Hq / Hkv <= 64, 1 <= nq <= 16,
+ * B*nq*Hq < 2^31, B*Hkv < 2^24, n_pages*page*Hkv < 2^39 / d. scale as in pisa_shape_t, cap as in pisa_doc_shape_t. */
+typedef struct {
+  int32_t B, Hq, Hkv, d, n_pages, page, max_pages, bits, nq;
+  float scale, cap;
+} pisa_paged_shape_t;
+
+typedef struct {
+  void *k, *v, *k_scale, *v_scale;
+  const float *k_amp, *v_amp;
+} pisa_paged_cache_t;
+
+/* Appends T = tokens->B * tokens->N tokens, each to its sequence and position: keys normed and rotated as by
+ * pisa_qk_norm_rope at those positions (tokens' norm and rot; norm = 0, rot = 0 stores them as they are),
+ * rounded to bf16, values as they are, both then put into their slots; queries normed and rotated
+ * into Qr. In 4 bits a group of 16 channels x (over amp) gets scale = e4m3(max |x| / 6), at most 448,
+ * and every channel the code nearest to x / scale, ties to the even one; a group with a NaN
+ * or an infinity gets the scale NaN, and stands for 16 NaNs.
+ *   tokens: pisa_qk_norm_rope's shape; its Hq, Hkv and d those of `shape`. Q [T,Hq,d], Qr [T,Hq,d] (both NULL: keys
+ *   and values only), K [T,Hkv,d] with tokens' strides, V [T,Hkv,d] with v_stride (0: contiguous), inv_freq, q_weight,
+ *   k_weight as there; seq device [T] int32 (NULL: token t belongs to sequence t / tokens->N, tokens->B being
+ *   shape->B); pos device [T] int32. Each (seq, pos) at most once a call: a slot given twice holds some bytes of each.
+ *   A token with seq < 0 is padding: nothing is stored and its row of Qr stays as it is. So does that of a token whose seq
+ *   is not below B, whose pos is outside [0, max_pages*page) or whose page is outside [0, n_pages), and the status
+ *   word then gets PISA_STATUS_POS_RANGE ORed in.
+ * Nothing written (cache, Qr, status) may overlap anything else; Qr may be a contiguous Q itself.
+ * shape->nq is not looked at. */
+int pisa_paged_append(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const pisa_rope_shape_t* tokens,
+                      const void* Q, const void* K, const void* V, int32_t v_stride, const float* inv_freq,
+                      const float* q_weight, const float* k_weight, const int32_t* table, const int32_t* seq,
+                      const int32_t* pos, void* Qr, int32_t* status, void* stream);
+
+/* Bytes of workspace of pisa_paged_attn (host-only). The first 256 bytes are the status block. */
+int pisa_paged_workspace_size(const pisa_paged_shape_t* shape, size_t* bytes);
+
+/* Attention of the last nq tokens of every sequence over its pages: with n = len[b], query i sits at p = n - nq + i and
+ * sees keys j <= p, scores as pisa_doc_attn_fwd has them. A query at p < 0 sees nothing: o = 0, lse = -inf.
+ *   len device [B] int32: tokens in the cache, the new ones included; clamped to [0, max_pages*page], with
+ *   PISA_STATUS_POS_RANGE where that changes it. A page outside [0, n_pages) sets the same bit and its keys are not
+ *   seen. q [B,nq,Hq,d] bf16, slopes [Hq] fp32 or NULL (read); o [B,nq,Hq,d] bf16, lse [B,nq,Hq] fp32 (may be
+ *   NULL) (written). What lies in slots behind a sequence's end is never used, whatever it is.
+ * The order of the sums follows the lengths and the GPU's SM count only.
+ * Nothing written (o, lse, the workspace) may overlap anything that is read, nor one another. */
+int pisa_paged_attn(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const int32_t* table,
+                    const int32_t* len, const void* q, const float* slopes, void* o, float* lse, void* ws,
+                    size_t ws_bytes, void* stream);
 
 /* Per-kernel timing (no counterpart on the pages: a measurement aid). After
  * pisa_profile_start(), every kernel that the library launches is bracketed by two CUDA

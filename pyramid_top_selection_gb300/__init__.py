@@ -11,5 +11,7 @@ from ._pisa import (  # noqa: F401
     Rope, RopeShape, WindowDecodeShape, WindowShape, make_rope_shape, make_window_decode_shape, make_window_shape,
     qk_norm_rope, qk_norm_rope_bwd, qk_norm_rope_workspace, rope_frequencies, rope_shape_of, window_attn_bwd,
     window_attn_fwd, window_decode_step, window_shape_of, window_workspace, window_workspace_size,
+    DOC_BWD, DOC_FWD, DocShape, PagedCache, PagedShape, doc_attn_bwd, doc_attn_fwd, doc_shape_of, doc_workspace,
+    doc_workspace_size, make_doc_shape, make_paged_shape, paged_append, paged_attn, paged_cache, paged_shape_of, paged_workspace,
     STATUS_POS_RANGE, STATUS_TIMEOUT, WINDOW_BWD, WINDOW_FWD, check_status, set_test_stall, set_wait_limit, workspace_status,
 )

@@ -19,10 +19,11 @@ LIB_PATH = os.path.join(_HERE, "libpisa.so")
 
 PISA_OK, PISA_EINVAL, PISA_EUNSUPPORTED, PISA_EWORKSPACE, PISA_ECUDA, PISA_ETIMEOUT = range(6)
 WINDOW_FWD, WINDOW_BWD = range(2)
+DOC_FWD, DOC_BWD = range(2)
 OP_SELECT, OP_SELECT_FLAT, OP_ATTN_FWD, OP_ATTN_BWD, OP_SELECT_MEAN, OP_SELECT_MEANVAR = range(6)
 STATUS_POS_RANGE, STATUS_TIMEOUT = 1, 2
 MAX_LEVELS = 32
-ABI_VERSION = 5          # PISA_VERSION of the header these argument lists follow
+ABI_VERSION = 6          # PISA_VERSION of the header these argument lists follow
 
 EXPORTS = (
     "pisa_version", "pisa_last_error", "pisa_pyramid_layout", "pisa_workspace_size",
@@ -32,6 +33,8 @@ EXPORTS = (
     "pisa_select_noalloc", "pisa_select_mean", "pisa_set_wait_limit", "pisa_test_stall",
     "pisa_select_meanvar", "pisa_window_workspace_size", "pisa_window_attn_fwd", "pisa_window_attn_bwd",
     "pisa_window_decode_step", "pisa_qk_norm_rope", "pisa_qk_norm_rope_workspace_size", "pisa_qk_norm_rope_bwd",
+    "pisa_doc_workspace_size", "pisa_doc_attn_fwd", "pisa_doc_attn_bwd", "pisa_paged_append",
+    "pisa_paged_workspace_size", "pisa_paged_attn",
 )
 
 
@@ -72,6 +75,21 @@ class RopeShape(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("q_stride", "k_stride")]
 
 
+class DocShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "Hq", "Hkv", "d", "n_docs", "max_len")] + \
+               [("scale", ctypes.c_float), ("cap", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("q_stride", "k_stride", "v_stride")]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "d", "n_pages", "page", "max_pages", "bits", "nq")] + \
+               [("scale", ctypes.c_float), ("cap", ctypes.c_float)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "k_amp", "v_amp")]
+
+
 _lib = None
 
 
@@ -108,6 +126,12 @@ def lib() -> ctypes.CDLL:
         L.pisa_qk_norm_rope.argtypes = [P(RopeShape)] + [vp] * 9
         L.pisa_qk_norm_rope_workspace_size.argtypes = [P(RopeShape), P(sz)]
         L.pisa_qk_norm_rope_bwd.argtypes = [P(RopeShape)] + [vp] * 13 + [sz, vp]
+        L.pisa_doc_workspace_size.argtypes = [P(DocShape), ctypes.c_int, P(sz)]
+        L.pisa_doc_attn_fwd.argtypes = [P(DocShape)] + [vp] * 9 + [sz, vp]
+        L.pisa_doc_attn_bwd.argtypes = [P(DocShape)] + [vp] * 13 + [sz, vp]
+        L.pisa_paged_append.argtypes = [P(PagedShape), P(_PagedCache), P(RopeShape)] + [vp] * 3 + [i32] + [vp] * 9
+        L.pisa_paged_workspace_size.argtypes = [P(PagedShape), P(sz)]
+        L.pisa_paged_attn.argtypes = [P(PagedShape), P(_PagedCache)] + [vp] * 7 + [sz, vp]
         L.pisa_profile_start.argtypes = []
         L.pisa_profile_stop.argtypes = []
         L.pisa_profile_read.argtypes = [P(ProfileEntry), i32, P(i32)]
@@ -648,6 +672,261 @@ def qk_norm_rope_bwd(Q, K, dQr, dKr, inv_freq, shape: RopeShape, q_weight=None, 
         dKr.data_ptr(), _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), _ptr(pos), dQ.data_ptr(), dK.data_ptr(),
         _ptr(dwq), _ptr(dwk), ws.data_ptr(), ws.numel())
     return dQ, dK, dwq, dwk
+
+
+# ---------------------------------------------------------------------------------------
+# Attention over packed documents; the paged key/value cache
+
+def make_doc_shape(T, Hq, Hkv, d, n_docs, max_len=0, scale=0.0, cap=0.0, q_stride=0, k_stride=0, v_stride=0) -> DocShape:
+    if not 0 <= T | Hq | Hkv | d | n_docs | max_len | q_stride | k_stride | v_stride <= 0x7fffffff:
+        _need_int32(T=T, Hq=Hq, Hkv=Hkv, d=d, n_docs=n_docs, max_len=max_len, q_stride=q_stride, k_stride=k_stride,
+                    v_stride=v_stride)
+    return DocShape(T, Hq, Hkv, d, n_docs, max_len, float(scale), float(cap), q_stride, k_stride, v_stride)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between consecutive tokens of [T, H, d] (0: contiguous)."""
+    if t.is_contiguous():
+        return 0
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, H, d] (got {tuple(t.shape)})")
+    return _token_stride(t[None], name)
+
+
+def doc_shape_of(Q, K, V, starts, max_len=0, scale=0.0, cap=0.0) -> DocShape:
+    """The shape of Q [T,Hq,d], K, V [T,Hkv,d] (slices of a fused projection, if need be) and starts [n_docs + 1].
+
+    max_len: the longest document's tokens, where the caller knows them (0: not)."""
+    T, Hq, d = Q.shape
+    return make_doc_shape(T, Hq, K.shape[1], d, starts.numel() - 1, max_len, scale, cap, _row_stride(Q, "Q"),
+                          _row_stride(K, "K"), _row_stride(V, "V"))
+
+
+def doc_workspace_size(shape: DocShape, op: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().pisa_doc_workspace_size(ctypes.byref(shape), op, ctypes.byref(b)))
+    return b.value
+
+
+def doc_workspace(shape: DocShape, op: int, device) -> torch.Tensor:
+    """A device workspace of the size `op` (DOC_FWD, DOC_BWD) needs (uint8 tensor)."""
+    return torch.empty(doc_workspace_size(shape, op), dtype=torch.uint8, device=device)
+
+
+def _need_rows(t, size, stride: int, dev, name: str) -> None:
+    if t.dtype is not torch.bfloat16 or t.shape != size or t.device != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor {tuple(size)} on {dev} "
+                         f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
+    if stride or not t.is_contiguous():
+        step, row = _row_stride(t, name), size[1] * size[2]
+        if size[0] > 1 and (step or row) != (stride or row):
+            raise ValueError(f"{name} has strides {tuple(t.stride())}, the shape says {stride} elements a token")
+
+
+def _need_docs(Q, K, V, starts, shape, prefix, slopes) -> None:
+    dev = Q.device
+    kv = (shape.T, shape.Hkv, shape.d)
+    _need_rows(Q, (shape.T, shape.Hq, shape.d), shape.q_stride, dev, "Q")
+    _need_rows(K, kv, shape.k_stride, dev, "K")
+    _need_rows(V, kv, shape.v_stride, dev, "V")
+    _need_shaped(starts, torch.int32, (shape.n_docs + 1,), dev, "starts")
+    if prefix is not None:
+        _need_shaped(prefix, torch.int32, (shape.n_docs,), dev, "prefix")
+    if slopes is not None:
+        _need_shaped(slopes, torch.float32, (shape.Hq,), dev, "slopes")
+
+
+def doc_attn_fwd(Q, K, V, starts, shape: DocShape, prefix=None, slopes=None, ws=None, out=None, lse=None):
+    """Attention over packed documents: O [T,Hq,d] bf16, lse [Hq,T] fp32.
+
+    starts: the documents' first tokens and one past the last, [n_docs + 1] int32. prefix: leading tokens of each document
+    that see one another, [n_docs] int32 (None: none). slopes: [Hq] fp32, what a score loses per token of
+    distance (None: nothing). Rows outside every document get O = 0, lse = -inf."""
+    _need_docs(Q, K, V, starts, shape, prefix, slopes)
+    dev = Q.device
+    size = (shape.T, shape.Hq, shape.d)
+    if out is None:
+        out = torch.empty(size, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shaped(out, torch.bfloat16, size, dev, "out")
+    if lse is None:
+        lse = torch.empty((shape.Hq, shape.T), dtype=torch.float32, device=dev)
+    else:
+        _need_shaped(lse, torch.float32, (shape.Hq, shape.T), dev, "lse")
+    if ws is None:
+        ws = doc_workspace(shape, DOC_FWD, dev)
+    _need_ws(ws, dev)
+    _on(dev, lib().pisa_doc_attn_fwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), starts.data_ptr(),
+        _ptr(prefix), _ptr(slopes), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return out, lse
+
+
+def doc_attn_bwd(Q, K, V, O, lse, dO, starts, shape: DocShape, prefix=None, slopes=None, ws=None):
+    """Gradients of doc_attn_fwd: dQ, dK, dV (bf16), from its O and lse."""
+    _need_docs(Q, K, V, starts, shape, prefix, slopes)
+    dev = Q.device
+    size = (shape.T, shape.Hq, shape.d)
+    _need_shaped(O, torch.bfloat16, size, dev, "O")
+    _need_shaped(dO, torch.bfloat16, size, dev, "dO")
+    _need_shaped(lse, torch.float32, (shape.Hq, shape.T), dev, "lse")
+    dQ = torch.empty(size, dtype=torch.bfloat16, device=dev)
+    dK = torch.empty((shape.T, shape.Hkv, shape.d), dtype=torch.bfloat16, device=dev)
+    dV = torch.empty_like(dK)
+    if ws is None:
+        ws = doc_workspace(shape, DOC_BWD, dev)
+    _need_ws(ws, dev)
+    _on(dev, lib().pisa_doc_attn_bwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+        lse.data_ptr(), dO.data_ptr(), starts.data_ptr(), _ptr(prefix), _ptr(slopes), dQ.data_ptr(), dK.data_ptr(),
+        dV.data_ptr(), ws.data_ptr(), ws.numel())
+    return dQ, dK, dV
+
+
+class PagedCache(NamedTuple):
+    """A paged key/value cache's tensors: k, v [n_pages,Hkv,page,d] bf16, or uint8 [n_pages,Hkv,page,d/2] (two e2m1 codes a
+    byte) with k_scale, v_scale [n_pages,Hkv,page,d/16] float8_e4m3fn and k_amp, v_amp [Hkv] fp32 (None: ones)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+    k_amp: torch.Tensor | None = None
+    v_amp: torch.Tensor | None = None
+
+
+def make_paged_shape(B, Hq, Hkv, d, n_pages, page, max_pages, bits=16, nq=1, scale=0.0, cap=0.0) -> PagedShape:
+    if not 0 <= B | Hq | Hkv | d | n_pages | page | max_pages | bits | nq <= 0x7fffffff:
+        _need_int32(B=B, Hq=Hq, Hkv=Hkv, d=d, n_pages=n_pages, page=page, max_pages=max_pages, bits=bits, nq=nq)
+    return PagedShape(B, Hq, Hkv, d, n_pages, page, max_pages, bits, nq, float(scale), float(cap))
+
+
+def paged_shape_of(cache: PagedCache, table, Hq, nq=1, scale=0.0, cap=0.0) -> PagedShape:
+    """The shape of a cache and its page table [B, max_pages]."""
+    n_pages, Hkv, page, row = cache.k.shape
+    four = cache.k.dtype is torch.uint8
+    return make_paged_shape(table.shape[0], Hq, Hkv, 2 * row if four else row, n_pages, page, table.shape[1],
+                            4 if four else 16, nq, scale, cap)
+
+
+def paged_cache(shape: PagedShape, device, k_amp=None, v_amp=None) -> PagedCache:
+    """An empty cache of this shape (zeros)."""
+    size = (shape.n_pages, shape.Hkv, shape.page)
+    if shape.bits == 16:
+        return PagedCache(*(torch.zeros(*size, shape.d, dtype=torch.bfloat16, device=device) for _ in range(2)))
+    codes = (torch.zeros(*size, shape.d // 2, dtype=torch.uint8, device=device) for _ in range(2))
+    scales = (torch.zeros(*size, shape.d // 16, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+    return PagedCache(*codes, *scales, k_amp, v_amp)
+
+
+def _need_paged(shape, cache, table, dev):
+    """The cache's C struct, its tensors checked."""
+    size = (shape.n_pages, shape.Hkv, shape.page)
+    four = shape.bits == 4
+    kind, row = (torch.uint8, shape.d // 2) if four else (torch.bfloat16, shape.d)
+    _need_shaped(cache.k, kind, size + (row,), dev, "k")
+    _need_shaped(cache.v, kind, size + (row,), dev, "v")
+    if four:
+        if cache.k_scale is None or cache.v_scale is None:
+            raise ValueError("a cache in 4 bits needs k_scale and v_scale")
+        _need_shaped(cache.k_scale, torch.float8_e4m3fn, size + (shape.d // 16,), dev, "k_scale")
+        _need_shaped(cache.v_scale, torch.float8_e4m3fn, size + (shape.d // 16,), dev, "v_scale")
+        for t, n in ((cache.k_amp, "k_amp"), (cache.v_amp, "v_amp")):
+            if t is not None:
+                _need_shaped(t, torch.float32, (shape.Hkv,), dev, n)
+    elif any(t is not None for t in cache[2:]):
+        raise ValueError("a cache in 16 bits has no scales")
+    _need_shaped(table, torch.int32, (shape.B, shape.max_pages), dev, "table")
+    return _PagedCache(*(_ptr(t) for t in cache))
+
+
+def _need_status(status, dev):
+    if status is None:
+        return torch.zeros(4, dtype=torch.int32, device=dev)
+    if status.dtype is not torch.int32 or status.device != dev or status.numel() < 1:
+        raise ValueError(f"status must be an int32 tensor on {dev} (got {status.dtype}, {status.device})")
+    return status
+
+
+def paged_append(shape: PagedShape, cache: PagedCache, table, pos, K, V, Q=None, seq=None, rope: Rope | None = None,
+                 q_out=None, status=None):
+    """Appends tokens to a paged cache, keys normed and rotated on the way. Returns Qr (None without Q) and status.
+
+    K, V [T,Hkv,d] bf16 and Q [T,Hq,d] (slices of a fused projection, if need be). pos [T] int32: each token's position in its
+    sequence; seq [T] int32: its sequence, below 0 for padding (None: T / B tokens of each sequence, in order).
+    rope (None: K as it is, and no Q): the norm and the rotation at pos, of K and of Q into q_out, which may be Q itself."""
+    dev = K.device
+    T = K.shape[0]
+    if T < 1:
+        raise ValueError("no tokens to append")
+    B, N = (1, T) if seq is not None else (shape.B, T // shape.B)
+    if B * N != T:
+        raise ValueError(f"without seq the {T} tokens must be as many for each of {shape.B} sequences")
+    if rope is None:
+        if Q is not None:
+            raise ValueError("Q is normed and rotated: it needs rope")
+        rope = Rope(None, 0, norm=False)
+    c = _need_paged(shape, cache, table, dev)
+    ks, vs = _row_stride(K, "K"), _row_stride(V, "V")
+    qs = 0 if Q is None else _row_stride(Q, "Q")
+    kv, q = (T, shape.Hkv, shape.d), (T, shape.Hq, shape.d)
+    _need_rows(K, kv, ks, dev, "K")
+    _need_rows(V, kv, vs, dev, "V")
+    _need_shaped(pos, torch.int32, (T,), dev, "pos")
+    if seq is not None:
+        _need_shaped(seq, torch.int32, (T,), dev, "seq")
+    if rope.inv_freq is not None:
+        _need_shaped(rope.inv_freq, torch.float32, (rope.rot // 2,), dev, "inv_freq")
+    for t, n in ((rope.q_weight, "q_weight"), (rope.k_weight, "k_weight")):
+        if t is not None:
+            _need_shaped(t, torch.float32, (shape.d,), dev, n)
+    if Q is not None:
+        _need_rows(Q, q, qs, dev, "Q")
+        if q_out is None:
+            q_out = torch.empty(q, dtype=torch.bfloat16, device=dev)
+        else:
+            _need_shaped(q_out, torch.bfloat16, q, dev, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without Q")
+    status = _need_status(status, dev)
+    tokens = make_rope_shape(B, N, shape.Hq, shape.Hkv, shape.d, rope.rot, rope.interleaved, rope.norm, rope.eps,
+                             rope.rot_scale, qs, ks)
+    _on(dev, lib().pisa_paged_append, ctypes.byref(shape), ctypes.byref(c), ctypes.byref(tokens), _ptr(Q), K.data_ptr(),
+        V.data_ptr(), vs, _ptr(rope.inv_freq), _ptr(rope.q_weight), _ptr(rope.k_weight), table.data_ptr(), _ptr(seq),
+        pos.data_ptr(), _ptr(q_out), status.data_ptr())
+    return q_out, status
+
+
+def paged_workspace(shape: PagedShape, device) -> torch.Tensor:
+    """A device workspace for paged_attn (uint8 tensor)."""
+    b = ctypes.c_size_t()
+    _check(lib().pisa_paged_workspace_size(ctypes.byref(shape), ctypes.byref(b)))
+    return torch.empty(b.value, dtype=torch.uint8, device=device)
+
+
+def paged_attn(shape: PagedShape, cache: PagedCache, table, lens, q, slopes=None, ws=None, o=None, lse=None):
+    """The last nq tokens of every sequence against its pages: o [B,nq,Hq,d] bf16, lse [B,nq,Hq] fp32.
+
+    lens: tokens of each sequence in the cache, the new ones included, [B] int32. slopes as in doc_attn_fwd. A query before its
+    sequence's first token gets o = 0, lse = -inf. The workspace's status word tells of lengths and pages out of range."""
+    dev = q.device
+    c = _need_paged(shape, cache, table, dev)
+    size = (shape.B, shape.nq, shape.Hq, shape.d)
+    _need_shaped(lens, torch.int32, (shape.B,), dev, "lens")
+    _need_shaped(q, torch.bfloat16, size, dev, "q")
+    if slopes is not None:
+        _need_shaped(slopes, torch.float32, (shape.Hq,), dev, "slopes")
+    if o is None:
+        o = torch.empty(size, dtype=torch.bfloat16, device=dev)
+    else:
+        _need_shaped(o, torch.bfloat16, size, dev, "o")
+    if lse is None:
+        lse = torch.empty(size[:3], dtype=torch.float32, device=dev)
+    else:
+        _need_shaped(lse, torch.float32, size[:3], dev, "lse")
+    if ws is None:
+        ws = paged_workspace(shape, dev)
+    _need_ws(ws, dev)
+    _on(dev, lib().pisa_paged_attn, ctypes.byref(shape), ctypes.byref(c), table.data_ptr(), lens.data_ptr(), q.data_ptr(),
+        _ptr(slopes), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return o, lse
 
 
 def workspace_status(ws: torch.Tensor) -> int:

@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "internal.h"
+#include "paged.h"
 #include "window.h"
 
 namespace {
@@ -290,6 +291,100 @@ int rope_dims(const pisa_rope_shape_t* s, pisa::RopeDims* o) {
   *o = d;
   return PISA_OK;
 }
+
+// ---- packed documents, paged cache
+
+int check_cap(float cap) {
+  if (cap == 0.f || (cap >= 0x1p-10f && cap <= 0x1p20f)) return PISA_OK;
+  return fail(PISA_EINVAL, "cap=%g must be 0 or in [2^-10, 2^20]", static_cast<double>(cap));
+}
+
+int check_group(int Hq, int Hkv, int d) {
+  PISA_CHECK(check_heads(Hq, Hkv, d));
+  if (Hq / Hkv > 64) return fail(PISA_EUNSUPPORTED, "GQA group G=%d (supported: at most 64)", Hq / Hkv);
+  return PISA_OK;
+}
+
+int doc_dims(const pisa_doc_shape_t* s, pisa::DocDims* o) {
+  if (!s) return fail(PISA_EINVAL, "shape is NULL");
+  if (s->T < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1 || s->n_docs < 1)
+    return fail(PISA_EINVAL, "sizes must be positive (T=%d Hq=%d Hkv=%d d=%d n_docs=%d)", s->T, s->Hq, s->Hkv, s->d, s->n_docs);
+  if (s->max_len < 0) return fail(PISA_EINVAL, "max_len=%d is negative", s->max_len);
+  PISA_CHECK(check_group(s->Hq, s->Hkv, s->d));
+  if (s->T > (1 << 24) || s->n_docs > (1 << 24)) return fail(PISA_EUNSUPPORTED, "T=%d or n_docs=%d exceeds 2^24", s->T, s->n_docs);
+  if (static_cast<int64_t>(s->T) * s->Hq >= (int64_t(1) << 31))
+    return fail(PISA_EUNSUPPORTED, "T*Hq=%lld exceeds 2^31", static_cast<long long>(s->T) * s->Hq);
+  PISA_CHECK(check_scale(s->scale, "scale"));
+  PISA_CHECK(check_cap(s->cap));
+  pisa::DocDims d{};
+  PISA_CHECK(check_stride(s->q_stride, s->Hq, s->d, "q_stride", &d.qs));
+  PISA_CHECK(check_stride(s->k_stride, s->Hkv, s->d, "k_stride", &d.ks));
+  PISA_CHECK(check_stride(s->v_stride, s->Hkv, s->d, "v_stride", &d.vs));
+  const int64_t strides[] = {d.qs, d.ks, d.vs};
+  for (const int64_t st : strides)
+    if (st * s->T >= (int64_t(1) << 39)) return fail(PISA_EUNSUPPORTED, "token stride %lld at T=%d", static_cast<long long>(st), s->T);
+  d.T = s->T; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d; d.n_docs = s->n_docs;
+  d.G = s->Hq / s->Hkv;
+  d.max_len = s->max_len > 0 && s->max_len < s->T ? s->max_len : s->T;
+  d.scale = scale_or_default(s->scale, s->d);
+  d.cap = s->cap;
+  *o = d;
+  return PISA_OK;
+}
+
+size_t doc_ws_bytes(const pisa::DocDims& d, int op) { return op == PISA_DOC_FWD ? pisa::doc_fwd_ws(d) : pisa::doc_bwd_ws(d); }
+
+int paged_dims(const pisa_paged_shape_t* s, pisa::PagedDims* o) {
+  if (!s) return fail(PISA_EINVAL, "shape is NULL");
+  if (s->B < 1 || s->Hq < 1 || s->Hkv < 1 || s->d < 1 || s->n_pages < 1 || s->page < 1 || s->max_pages < 1)
+    return fail(PISA_EINVAL, "sizes must be positive (B=%d Hq=%d Hkv=%d d=%d n_pages=%d page=%d max_pages=%d)", s->B, s->Hq,
+                s->Hkv, s->d, s->n_pages, s->page, s->max_pages);
+  PISA_CHECK(check_group(s->Hq, s->Hkv, s->d));
+  if (s->bits != 16 && s->bits != 4) return fail(PISA_EUNSUPPORTED, "bits=%d (supported: 16, 4)", s->bits);
+  if (s->page < 16 || s->page > 1024 || (s->page & (s->page - 1)))
+    return fail(PISA_EUNSUPPORTED, "page=%d (supported: powers of two from 16 to 1024)", s->page);
+  if (static_cast<int64_t>(s->max_pages) * s->page > (1 << 24))
+    return fail(PISA_EUNSUPPORTED, "max_pages*page=%lld exceeds 2^24", static_cast<long long>(s->max_pages) * s->page);
+  if (s->nq < 1 || s->nq > 16) return fail(PISA_EUNSUPPORTED, "nq=%d (supported: 1..16)", s->nq);
+  if (static_cast<int64_t>(s->B) * s->Hkv >= (1 << 24)) return fail(PISA_EUNSUPPORTED, "B*Hkv=%lld exceeds 2^24", static_cast<long long>(s->B) * s->Hkv);
+  if (static_cast<int64_t>(s->B) * s->Hq >= (int64_t(1) << 31) / s->nq) return fail(PISA_EUNSUPPORTED, "B*nq*Hq exceeds 2^31");
+  if (static_cast<int64_t>(s->n_pages) * s->page >= (int64_t(1) << 39) / s->d / s->Hkv)
+    return fail(PISA_EUNSUPPORTED, "n_pages*page*Hkv*d exceeds 2^39");
+  PISA_CHECK(check_scale(s->scale, "scale"));
+  PISA_CHECK(check_cap(s->cap));
+  pisa::PagedDims d{};
+  d.B = s->B; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d; d.n_pages = s->n_pages; d.page = s->page;
+  d.max_pages = s->max_pages; d.bits = s->bits; d.nq = s->nq;
+  d.G = s->Hq / s->Hkv;
+  while ((1 << d.log_page) < s->page) ++d.log_page;
+  d.scale = scale_or_default(s->scale, s->d);
+  d.cap = s->cap;
+  *o = d;
+  return PISA_OK;
+}
+
+int paged_cache(const pisa::PagedDims& d, const pisa_paged_cache_t* c, pisa::PagedCache* o) {
+  if (!c) return fail(PISA_EINVAL, "cache is NULL");
+  PISA_CHECK(check_ptr(c->k, "k"));
+  PISA_CHECK(check_ptr(c->v, "v"));
+  if (d.bits == 4) {
+    PISA_CHECK(check_ptr(c->k_scale, "k_scale"));
+    PISA_CHECK(check_ptr(c->v_scale, "v_scale"));
+    PISA_CHECK(check_ptr(c->k_amp, "k_amp", true));
+    PISA_CHECK(check_ptr(c->v_amp, "v_amp", true));
+  } else if (c->k_scale || c->v_scale || c->k_amp || c->v_amp) {
+    return fail(PISA_EINVAL, "bits=16 has no scales");
+  }
+  *o = {static_cast<unsigned char*>(c->k), static_cast<unsigned char*>(c->v), static_cast<unsigned char*>(c->k_scale),
+        static_cast<unsigned char*>(c->v_scale), c->k_amp, c->v_amp};
+  return PISA_OK;
+}
+
+// Bytes of one of the cache's tensors, and of its scales.
+int64_t page_bytes(const pisa::PagedDims& d) {
+  return static_cast<int64_t>(d.n_pages) * d.Hkv * d.page * (d.bits == 16 ? 2 * d.d : d.d / 2);
+}
+int64_t scale_bytes(const pisa::PagedDims& d) { return d.bits == 16 ? 0 : static_cast<int64_t>(d.n_pages) * d.Hkv * d.page * (d.d / 16); }
 
 }  // namespace
 
@@ -623,6 +718,128 @@ int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const v
   return cuda_rc(pisa::launch_rope_bwd(d, Q, K, dQr, dKr, inv_freq, q_weight, k_weight, pos, dQ, dK, dq_weight,
                                        dk_weight, static_cast<char*>(ws), stream),
                  "pisa_qk_norm_rope_bwd");
+}
+
+int pisa_doc_workspace_size(const pisa_doc_shape_t* shape, int op, size_t* bytes) {
+  pisa::DocDims d;
+  PISA_CHECK(doc_dims(shape, &d));
+  if (!bytes) return fail(PISA_EINVAL, "bytes is NULL");
+  if (op != PISA_DOC_FWD && op != PISA_DOC_BWD) return fail(PISA_EINVAL, "unknown op %d", op);
+  *bytes = doc_ws_bytes(d, op);
+  return PISA_OK;
+}
+
+int pisa_doc_attn_fwd(const pisa_doc_shape_t* shape, const void* Q, const void* K, const void* V,
+                      const int32_t* starts, const int32_t* prefix, const float* slopes, void* O, float* lse,
+                      void* ws, size_t ws_bytes, void* stream) {
+  pisa::DocDims d;
+  PISA_CHECK(doc_dims(shape, &d));
+  const void* in[] = {Q, K, V, starts, O, lse};
+  const char* names[] = {"Q", "K", "V", "starts", "O", "lse"};
+  for (int k = 0; k < 6; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(prefix, "prefix", true));
+  PISA_CHECK(check_ptr(slopes, "slopes", true));
+  const size_t need = doc_ws_bytes(d, PISA_DOC_FWD);
+  PISA_CHECK(check_ws_bytes(need, ws, ws_bytes));
+  const int64_t q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
+  const Span read[] = {{"Q", Q, d.T, d.qs, q}, {"K", K, d.T, d.ks, kv}, {"V", V, d.T, d.vs, kv}, flat("starts", starts, d.n_docs + 1, 4),
+                       flat("prefix", prefix, d.n_docs, 4), flat("slopes", slopes, d.Hq, 4)};
+  const Span out[] = {{"O", O, d.T, q, q}, {"lse", lse, d.T, d.Hq, d.Hq, 4}, flat("workspace", ws, static_cast<int64_t>(need), 1)};
+  PISA_CHECK(check_apart(read, out));
+  return cuda_rc(pisa::launch_doc_fwd(d, Q, K, V, {starts, prefix, slopes}, O, lse, static_cast<char*>(ws), stream),
+                 "pisa_doc_attn_fwd");
+}
+
+int pisa_doc_attn_bwd(const pisa_doc_shape_t* shape, const void* Q, const void* K, const void* V, const void* O,
+                      const float* lse, const void* dO, const int32_t* starts, const int32_t* prefix,
+                      const float* slopes, void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes, void* stream) {
+  pisa::DocDims d;
+  PISA_CHECK(doc_dims(shape, &d));
+  const void* in[] = {Q, K, V, O, lse, dO, starts, dQ, dK, dV};
+  const char* names[] = {"Q", "K", "V", "O", "lse", "dO", "starts", "dQ", "dK", "dV"};
+  for (int k = 0; k < 10; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(prefix, "prefix", true));
+  PISA_CHECK(check_ptr(slopes, "slopes", true));
+  const size_t need = doc_ws_bytes(d, PISA_DOC_BWD);
+  PISA_CHECK(check_ws_bytes(need, ws, ws_bytes));
+  const int64_t q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
+  const Span read[] = {{"Q", Q, d.T, d.qs, q}, {"K", K, d.T, d.ks, kv}, {"V", V, d.T, d.vs, kv}, {"O", O, d.T, q, q},
+                       {"dO", dO, d.T, q, q}, {"lse", lse, d.T, d.Hq, d.Hq, 4}, flat("starts", starts, d.n_docs + 1, 4),
+                       flat("prefix", prefix, d.n_docs, 4), flat("slopes", slopes, d.Hq, 4)};
+  const Span out[] = {{"dQ", dQ, d.T, q, q}, {"dK", dK, d.T, kv, kv}, {"dV", dV, d.T, kv, kv},
+                      flat("workspace", ws, static_cast<int64_t>(need), 1)};
+  PISA_CHECK(check_apart(read, out));
+  return cuda_rc(pisa::launch_doc_bwd(d, Q, K, V, O, lse, dO, {starts, prefix, slopes}, dQ, dK, dV, static_cast<char*>(ws), stream),
+                 "pisa_doc_attn_bwd");
+}
+
+int pisa_paged_append(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const pisa_rope_shape_t* tokens,
+                      const void* Q, const void* K, const void* V, int32_t v_stride, const float* inv_freq,
+                      const float* q_weight, const float* k_weight, const int32_t* table, const int32_t* seq,
+                      const int32_t* pos, void* Qr, int32_t* status, void* stream) {
+  pisa::PagedDims d;
+  pisa::PagedCache c;
+  pisa::RopeDims t;
+  int64_t vs = 0;
+  PISA_CHECK(paged_dims(shape, &d));
+  PISA_CHECK(paged_cache(d, cache, &c));
+  PISA_CHECK(rope_dims(tokens, &t));
+  if (t.Hq != d.Hq || t.Hkv != d.Hkv || t.d != d.d)
+    return fail(PISA_EINVAL, "tokens have Hq=%d Hkv=%d d=%d, the cache Hq=%d Hkv=%d d=%d", t.Hq, t.Hkv, t.d, d.Hq, d.Hkv, d.d);
+  if (!seq && t.B != d.B) return fail(PISA_EINVAL, "without seq the tokens' B=%d must be the cache's B=%d", t.B, d.B);
+  PISA_CHECK(check_stride(v_stride, d.Hkv, d.d, "v_stride", &vs));
+  const int64_t n = static_cast<int64_t>(t.B) * t.N, q = static_cast<int64_t>(d.Hq) * d.d, kv = static_cast<int64_t>(d.Hkv) * d.d;
+  if (n * (d.Hq + 2 * static_cast<int64_t>(d.Hkv)) >= (int64_t(1) << 31)) return fail(PISA_EUNSUPPORTED, "T*(Hq+2Hkv) exceeds 2^31");
+  if (!Q != !Qr) return fail(PISA_EINVAL, "Q and Qr must both be given or both be NULL");
+  const void* in[] = {K, V, table, pos, status};
+  const char* names[] = {"K", "V", "table", "pos", "status"};
+  for (int k = 0; k < 5; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(inv_freq, "inv_freq", t.rot == 0));
+  const void* opt[] = {Q, Qr, q_weight, k_weight, seq};
+  const char* opt_names[] = {"Q", "Qr", "q_weight", "k_weight", "seq"};
+  for (int k = 0; k < 5; ++k) PISA_CHECK(check_ptr(opt[k], opt_names[k], true));
+  if (Q && Qr == Q && t.qs != q) return fail(PISA_EINVAL, "in place needs a contiguous Q");
+  const Span read[] = {{"Q", Q, n, t.qs, q}, {"K", K, n, t.ks, kv}, {"V", V, n, vs, kv}, flat("inv_freq", inv_freq, t.rot / 2, 4),
+                       flat("q_weight", q_weight, d.d, 4), flat("k_weight", k_weight, d.d, 4), flat("seq", seq, n, 4),
+                       flat("pos", pos, n, 4), flat("table", table, static_cast<int64_t>(d.B) * d.max_pages, 4),
+                       flat("k_amp", c.k_amp, d.Hkv, 4), flat("v_amp", c.v_amp, d.Hkv, 4)};
+  const Span out[] = {{"Qr", Qr, n, q, q}, flat("k", c.k, page_bytes(d), 1), flat("v", c.v, page_bytes(d), 1),
+                      flat("k_scale", c.ks, scale_bytes(d), 1), flat("v_scale", c.vs, scale_bytes(d), 1), flat("status", status, 1, 4)};
+  PISA_CHECK(check_apart(read, out, 1));
+  return cuda_rc(pisa::launch_paged_append(d, c, t, Q, K, V, vs, inv_freq, q_weight, k_weight, table, seq, pos, Qr, status, stream),
+                 "pisa_paged_append");
+}
+
+int pisa_paged_workspace_size(const pisa_paged_shape_t* shape, size_t* bytes) {
+  pisa::PagedDims d;
+  PISA_CHECK(paged_dims(shape, &d));
+  if (!bytes) return fail(PISA_EINVAL, "bytes is NULL");
+  *bytes = pisa::paged_attn_ws(d);
+  return PISA_OK;
+}
+
+int pisa_paged_attn(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const int32_t* table,
+                    const int32_t* len, const void* q, const float* slopes, void* o, float* lse, void* ws,
+                    size_t ws_bytes, void* stream) {
+  pisa::PagedDims d;
+  pisa::PagedCache c;
+  PISA_CHECK(paged_dims(shape, &d));
+  PISA_CHECK(paged_cache(d, cache, &c));
+  const void* in[] = {table, len, q, o};
+  const char* names[] = {"table", "len", "q", "o"};
+  for (int k = 0; k < 4; ++k) PISA_CHECK(check_ptr(in[k], names[k]));
+  PISA_CHECK(check_ptr(slopes, "slopes", true));
+  PISA_CHECK(check_ptr(lse, "lse", true));
+  const size_t need = pisa::paged_attn_ws(d);
+  PISA_CHECK(check_ws_bytes(need, ws, ws_bytes));
+  const int64_t rows = static_cast<int64_t>(d.B) * d.nq * d.Hq;
+  const Span read[] = {flat("q", q, rows * d.d, 2), flat("k", c.k, page_bytes(d), 1), flat("v", c.v, page_bytes(d), 1),
+                       flat("k_scale", c.ks, scale_bytes(d), 1), flat("v_scale", c.vs, scale_bytes(d), 1),
+                       flat("k_amp", c.k_amp, d.Hkv, 4), flat("v_amp", c.v_amp, d.Hkv, 4), flat("slopes", slopes, d.Hq, 4),
+                       flat("len", len, d.B, 4), flat("table", table, static_cast<int64_t>(d.B) * d.max_pages, 4)};
+  const Span out[] = {flat("o", o, rows * d.d, 2), flat("lse", lse, rows, 4), flat("workspace", ws, static_cast<int64_t>(need), 1)};
+  PISA_CHECK(check_apart(read, out));
+  return cuda_rc(pisa::launch_paged_attn(d, c, table, len, q, slopes, o, lse, static_cast<char*>(ws), stream), "pisa_paged_attn");
 }
 
 }  // extern "C"

@@ -1,0 +1,220 @@
+"""Attention over packed documents on the GPU against its 64-bit definition: forward and backward, causal and prefix
+masks, capped and distance-biased scores, with bounds that count the kernels' roundings (_docs_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import pyramid_top_selection_gb300 as pisa
+from _docs_ref import doc_attention
+from _window_ref import check
+
+pytestmark = pytest.mark.gpu
+bf16 = torch.bfloat16
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _inputs(T, Hq, Hkv, d, fused=False, seed=0, spread=1.0, padding=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if fused:
+        x = (torch.randn(T, Hq + 2 * Hkv, d, generator=g, device="cuda") * spread).to(bf16)
+        Q, K, V = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    else:
+        Q = (torch.randn(T, Hq, d, generator=g, device="cuda") * spread).to(bf16)
+        K = (torch.randn(T, Hkv, d, generator=g, device="cuda") * spread).to(bf16)
+        V = torch.randn(T, Hkv, d, generator=g, device="cuda").to(bf16)
+    dO = torch.randn(T, Hq, d, generator=g, device="cuda").to(bf16)
+    if padding is not None:                # what belongs to no document is never used
+        Q[padding], K[padding], V[padding], dO[padding] = math.nan, math.nan, math.inf, -math.inf
+    return Q, K, V, dO
+
+
+def _run(Q, K, V, dO, starts, prefix=None, slopes=None, cap=0.0, scale=0.0, max_len=0):
+    T, Hq, d = Q.shape
+    s = pisa.doc_shape_of(Q, K, V, starts, max_len, scale, cap)
+    out = torch.full((T, Hq, d), 7.0, dtype=bf16, device="cuda")       # every element is written
+    lse = torch.full((Hq, T), 7.0, device="cuda")
+    ws = pisa.doc_workspace(s, pisa.DOC_FWD, Q.device)
+    ws.fill_(0xAB)
+    O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s, prefix, slopes, ws=ws, out=out, lse=lse)
+    assert pisa.workspace_status(ws) == 0
+    got = {"O": O, "lse": lse}
+    if dO is not None:
+        ws = pisa.doc_workspace(s, pisa.DOC_BWD, Q.device)
+        ws.fill_(0xAB)
+        got["dQ"], got["dK"], got["dV"] = pisa.doc_attn_bwd(Q, K, V, O, lse, dO, starts, s, prefix, slopes, ws=ws)
+        assert pisa.workspace_status(ws) == 0
+    return got
+
+
+def _slopes(H):
+    return torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], device="cuda")
+
+
+CASES = {  # T, Hq, Hkv, d, starts, prefix, cap, slopes, fused
+    "one token": (1, 1, 1, 64, [0, 1], None, 0.0, False, False),
+    "one document": (257, 8, 1, 128, [0, 257], None, 0.0, False, False),
+    "one key each": (40, 4, 2, 128, list(range(41)), None, 0.0, False, False),
+    "no document at all": (70, 4, 2, 64, [0, 0, 0], None, 0.0, False, False),
+    "documents and padding": (700, 4, 2, 128, [0, 130, 131, 131, 400, 650], None, 0.0, False, False),
+    "tokens before the first document": (300, 6, 2, 64, [37, 200, 290], None, 0.0, False, True),
+    "starts past the tokens": (200, 2, 2, 64, [0, 150, 400, 500], None, 0.0, False, False),
+    "prefixes": (600, 8, 2, 128, [0, 300, 310, 555, 600], [100, 10, 0, 1], 0.0, False, False),
+    "prefixes of whole documents": (500, 4, 4, 64, [0, 260, 500], [260, 900], 0.0, False, True),
+    "prefix longer than a tile": (900, 4, 1, 128, [5, 900], [500], 0.0, False, False),
+    "capped": (513, 8, 2, 128, [0, 513], None, 3.0, False, False),
+    "capped, several": (777, 5, 5, 64, [0, 400, 500, 777], None, 20.0, False, True),
+    "distance": (600, 8, 2, 128, [0, 411, 600], None, 0.0, True, False),
+    "distance, three heads, prefixes": (650, 6, 2, 64, [0, 300, 610], [77, 300], 0.0, True, False),
+    "capped and distance": (500, 4, 1, 128, [0, 490], None, 5.0, True, False),
+    "all of it": (900, 12, 4, 64, [3, 100, 101, 600, 850], [50, 1, 200, 30], 10.0, True, True),
+    "group of 64": (90, 64, 1, 64, [0, 50, 90], [7, 0], 15.0, True, False),
+    "group of 16": (300, 16, 1, 128, [0, 299], None, 0.0, True, False),
+    "many documents": (1500, 4, 2, 128, list(range(0, 1501, 23)), None, 0.0, False, False),
+    "many short documents, capped": (1000, 16, 2, 64, list(range(0, 1000, 7)), None, 4.0, False, False),
+    "long documents": (2300, 4, 4, 128, [0, 1100, 2300], None, 0.0, False, False),
+    "long documents, capped": (2300, 4, 2, 64, [0, 1300, 2299], None, 8.0, False, False),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_against_definition(name):
+    T, Hq, Hkv, d, starts, prefix, cap, biased, fused = CASES[name]
+    pad = torch.ones(T, dtype=torch.bool, device="cuda")
+    pad[starts[0]:starts[-1]] = False
+    Q, K, V, dO = _inputs(T, Hq, Hkv, d, fused, len(name), padding=pad)
+    slopes = _slopes(Hq) if biased else None
+    got = _run(Q, K, V, dO, _ints(starts), None if prefix is None else _ints(prefix), slopes, cap)
+    want, tol = doc_attention(Q, K, V, starts, prefix, slopes, cap, dO=dO)
+    for n in want:
+        check(n, got[n], want[n], tol[n])
+
+
+@pytest.mark.parametrize("cap", [0.0, 1.0, 30.0])
+@pytest.mark.parametrize("biased", [False, True])
+def test_peaked_scores(cap, biased):
+    # products up to several hundred: the cap's tanh from its linear part to 1, the running maximum moves
+    Q, K, V, dO = _inputs(520, 4, 2, 128, seed=3, spread=6.0)
+    K[100::90] *= 4
+    Q[200:210] = 0
+    starts, slopes = [0, 40, 500], _slopes(4) * 3 if biased else None
+    Q[500:], K[500:], V[500:] = 0, 0, 0
+    got = _run(Q, K, V, dO, _ints(starts), None, slopes, cap)
+    want, tol = doc_attention(Q, K, V, starts, None, slopes, cap, dO=dO)
+    for n in want:
+        check(n, got[n], want[n], tol[n])
+
+
+def test_scores_that_grow_with_distance():
+    # negative slopes: the farthest key wins, row by row
+    Q, K, V, dO = _inputs(400, 2, 1, 64, seed=4)
+    slopes = torch.tensor([-0.25, -1.0], device="cuda")
+    got = _run(Q, K, V, dO, _ints([0, 180, 400]), None, slopes)
+    want, tol = doc_attention(Q, K, V, [0, 180, 400], None, slopes, dO=dO)
+    for n in want:
+        check(n, got[n], want[n], tol[n])
+
+
+def test_one_document_is_the_window_attention_of_all_keys():
+    Q, K, V, dO = _inputs(1000, 8, 2, 128, seed=5)
+    got = _run(Q, K, V, dO, _ints([0, 1000]))
+    s = pisa.window_shape_of(Q[None], K[None], V[None], 1000)
+    O, lse = pisa.window_attn_fwd(Q[None], K[None], V[None], s)
+    want, tol = doc_attention(Q, K, V, [0, 1000])
+    check("O", O[0], want["O"], tol["O"])
+    check("O", got["O"], want["O"], tol["O"])
+    check("lse", got["lse"], lse[0].double(), 2 * tol["lse"])
+
+
+@pytest.mark.parametrize("max_len", [1, 100, 450, 1000])
+def test_what_the_caller_says_of_the_longest_document_does_not_matter(max_len):
+    Q, K, V, dO = _inputs(1000, 4, 1, 128, seed=6)
+    starts = [0, 450, 900]
+    got = _run(Q, K, V, dO, _ints(starts), max_len=max_len)
+    Q[900:], K[900:], V[900:], dO[900:] = 0, 0, 0, 0
+    want, tol = doc_attention(Q, K, V, starts, dO=dO)
+    for n in want:
+        check(n, got[n], want[n], tol[n])
+
+
+@pytest.mark.parametrize("cap,biased,prefix", [(0.0, False, None), (6.0, False, None), (6.0, True, [90, 20])])
+def test_gradients_against_differences(cap, biased, prefix):
+    # the kernel's gradients along random directions against differences of the 64-bit loss sum(O dO)
+    Q, K, V, dO = _inputs(220, 4, 2, 64, seed=7, spread=1.5)
+    starts, slopes = [0, 120, 220], _slopes(4) if biased else None
+    got = _run(Q, K, V, dO, _ints(starts), None if prefix is None else _ints(prefix), slopes, cap)
+    _, tol = doc_attention(Q, K, V, starts, prefix, slopes, cap, dO=dO)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = {"dQ": Q.double(), "dK": K.double(), "dV": V.double()}
+
+    def loss(y):
+        out, _ = doc_attention(y["dQ"], y["dK"], y["dV"], starts, prefix, slopes, cap)
+        return float((out["O"] * dO.double()).sum())
+
+    for n in x:
+        u = torch.randn(x[n].shape, generator=g, device="cuda", dtype=torch.float64)
+        h = 1e-4                           # the differences' own error: h^2 times third derivatives, and 2^-53 / h of the loss
+        diff = (loss(x | {n: x[n] + h * u}) - loss(x | {n: x[n] - h * u})) / (2 * h)
+        got_n = float((got[n].double() * u).sum())
+        bound = float((tol[n] * u.abs()).sum())
+        assert abs(got_n - diff) <= bound + 1e-3 * abs(diff), (n, got_n, diff, bound)
+
+
+def test_the_same_call_gives_the_same_bits():
+    Q, K, V, dO = _inputs(3000, 8, 2, 128, seed=8)
+    starts, slopes = _ints([0, 10, 900, 2500, 2990]), _slopes(8)
+    one, two = (_run(Q, K, V, dO, starts, None, slopes, 10.0) for _ in range(2))
+    for n in one:
+        assert torch.equal(one[n][torch.isfinite(one[n])], two[n][torch.isfinite(two[n])]), n
+
+
+def test_captured_and_replayed_on_other_documents():
+    # starts are read by the kernels: one graph serves every packing of the same size
+    T, Hq, Hkv, d = 1200, 8, 2, 128
+    Q, K, V, dO = _inputs(T, Hq, Hkv, d, seed=9)
+    starts, pre, slopes = _ints([0, 600, 1200, 1200]), _ints([0, 50, 0]), _slopes(Hq)
+    s = pisa.doc_shape_of(Q, K, V, starts, cap=12.0)
+    ws, wb = (pisa.doc_workspace(s, op, Q.device) for op in (pisa.DOC_FWD, pisa.DOC_BWD))
+
+    def step():
+        O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s, pre, slopes, ws=ws)
+        return O, lse, *pisa.doc_attn_bwd(Q, K, V, O, lse, dO, starts, s, pre, slopes, ws=wb)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for new_starts, new_pre in (([0, 600, 1200, 1200], [0, 50, 0]), ([0, 1, 777, 1190], [1, 300, 0])):
+        starts.copy_(_ints(new_starts))
+        pre.copy_(_ints(new_pre))
+        graph.replay()
+        eager = step()
+        torch.cuda.synchronize()
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
+        assert pisa.workspace_status(ws) == 0 and pisa.workspace_status(wb) == 0
+
+
+def test_two_streams_at_once():
+    Q, K, V, dO = _inputs(2000, 4, 2, 64, seed=10)
+    starts = _ints([0, 1500, 2000])
+    want = _run(Q, K, V, dO, starts)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    s = pisa.doc_shape_of(Q, K, V, starts)
+    got = []
+    for st in streams:
+        with torch.cuda.stream(st):
+            O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s)
+            got.append((O, lse, *pisa.doc_attn_bwd(Q, K, V, O, lse, dO, starts, s)))
+    torch.cuda.synchronize()
+    for g in got:
+        for a, n in zip(g, ("O", "lse", "dQ", "dK", "dV")):
+            assert torch.equal(a, want[n]), n
