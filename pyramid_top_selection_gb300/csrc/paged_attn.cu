@@ -1,10 +1,29 @@
-// Attention of the last tokens of every sequence over a paged cache in 16 or 4 bits: one warp per (sequence, query, head),
-// a key at a time.
-#include <cmath>
+// Attention of the last tokens of every sequence over a paged cache in 16 or 4 bits.
+//
+// o = softmax over the visible keys of the scores times V, per query head; bound by HBM: every cached key and value
+// is read once (4 d bytes per KV head and token, 1.125 d in 4 bits) for the group's heads and drafted tokens.
+//
+// All chunks of all (sequence, KV head, set of rows) units form one list, which is cut into equal runs, one a warp: lengths
+// may differ as they like, the work is the same everywhere. The list follows from the lengths, which only the device
+// knows, so every warp finds its own run. A warp walks its run with its own running maximum, sum and output. Units that lie
+// wholly in a run are written at once; a run's first and last ones may be parts, which the CTA's warps join through shared
+// memory, and a second, small kernel joins what crosses CTAs. All sums are in the list's order.
+//
+// S^T = K Q^T and O^T += V^T P^T on m16n8k16 MMAs with tokens (then channels) as the 16 rows and the rows of the unit (heads
+// x drafted tokens) as the 8 columns; tcgen05's 128-row tiles would be 94 % padding. Keys and values come by cp.async
+// into each warp's ring.
+//   16 bits: chunks of 16 tokens, fragments by ldmatrix.
+//   4 bits: chunks of 32 tokens; codes become halves in registers (a code times its scale is exact in fp16: 2 and 4
+//   significant bits), with q brought into fp16's range by a power of two per row, and P held 2^7 larger
+//   (down to 2^-31 of the largest). A lane of S's fragments takes 32 channels of its token in a row (16 bytes), which channel goes to
+//   which slot of the contraction being free; V's fragments want two tokens of one channel in a register, so the nibbles of
+//   two tokens are interleaved before they are converted.
+#include <algorithm>
 
 #include "internal.h"
 #include "paged.cuh"
 #include "profile.h"
+#include "scores.cuh"
 #include "window_tc.cuh"
 
 namespace pisa {
@@ -12,6 +31,11 @@ namespace pisa {
 namespace {
 
 using bf16 = __nv_bfloat16;
+constexpr int kWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;                  // log2 growth of the maximum that O is rescaled for
+constexpr int kMinChunks = 2;                  // chunks of a run at least, where the list has as many
+constexpr int kMaxCtas = 3;                    // CTAs an SM holds at most
 
 struct PagedArgs {
   PagedDims s;
@@ -22,65 +46,753 @@ struct PagedArgs {
   bf16* o;
   float* lse;
   int32_t* status;
+  int32_t* flags;          // per CTA: PISA_STATUS_POS_RANGE if it met a length or page out of range
+  float* part;             // parts of units, [rows][D] O, then m and l: two a CTA for the join, then one a warp for the CTA's own
+  int32_t sets, rows;      // sets of rows of a KV head; its rows (group heads x nq)
+  int32_t units;           // of a sequence: Hkv * sets
 };
 
-template <int D>
-__device__ __forceinline__ float element(const PagedDims& s, const unsigned char* p, const unsigned char* sc, int64_t row, int e) {
-  if (s.bits == 16) return __bfloat162float(reinterpret_cast<const bf16*>(p)[row * D + e]);
-  uint32_t h[4];
-  paged::from_e2m1x8(p[row * (D / 2) + e / 2], h);
-  const __half2 v = *reinterpret_cast<__half2*>(&h[0]);
-  return __half2float(e & 1 ? __high2half(v) : __low2half(v)) * __low2float(paged::from_e4m3x2(sc[row * (D / 16) + e / 16]));
+template <int D, bool FOUR, int NT>
+struct Plan {
+  static constexpr int CH = FOUR ? 32 : 16;                        // tokens of a chunk
+  static constexpr int ROW = FOUR ? D / 2 : D * 2;                 // bytes of a token
+  static constexpr int SROW = FOUR ? D / 16 : 0;                   // of its scales
+  static constexpr int HALF = CH * (ROW + SROW);                   // keys with their scales; values follow
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int ST = 3;
+  static constexpr int RING = ST * STAGE;
+  static constexpr int COLS = 8 * NT;                              // rows of a unit
+  static constexpr int PARTF = COLS * (D + 2), PART = PARTF * 4;   // a part: O [COLS][D], m, l
+  static constexpr int RINGP = RING > PART ? RING : PART;          // the run's last part is laid over the ring
+  static constexpr int bytes = kWarps * RINGP;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// Transposes an 8x8 matrix of 16-bit values held by a warp (lane 4 g + p: row g, columns 2 p, 2 p + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t scales_of(uint32_t two) {      // two e4m3 bytes as halves
+  const __half2 v = paged::from_e4m3x2(static_cast<uint16_t>(two));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int D>
-__global__ void paged_attn_kernel(const PagedArgs a) {
+// What a running maximum stands for in an exponent: as long as every score was -inf, nothing is to be subtracted.
+__device__ __forceinline__ float base_of(float m) { return m > neg_inf() ? m : 0.f; }
+
+// The list of chunks: sequence b's units (KV heads x sets) one after another, n_chunks(b) each.
+template <int CH>
+struct List {
+  const PagedArgs& a;
+  int most;
+  __device__ __forceinline__ explicit List(const PagedArgs& args) : a(args), most(args.s.max_pages << args.s.log_page) {}
+  __device__ __forceinline__ int tokens(int b) const { return max(0, min(a.len[b], most)); }
+  static __device__ __forceinline__ int chunks(int n) { return max(1, (n + CH - 1) / CH); }    // an empty sequence has rows to write, too
+  // whole warp: the list's length
+  __device__ __forceinline__ int64_t total() const {
+    int64_t t = 0;
+    for (int b = threadIdx.x & 31; b < a.s.B; b += 32) t += chunks(tokens(b));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t * a.units;
+  }
+  // whole warp: the sequence that place t of the list belongs to, and where its first unit begins
+  __device__ __forceinline__ void find(int64_t t, int& b, int64_t& begin) const {
+    const int lane = threadIdx.x & 31;
+    begin = 0;
+    for (int b0 = 0; b0 < a.s.B; b0 += 32) {
+      const int64_t mine = b0 + lane < a.s.B ? static_cast<int64_t>(chunks(tokens(b0 + lane))) * a.units : 0;
+      int64_t sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, begin + sum > t);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        b = b0 + k;
+        begin += __shfl_sync(0xffffffffu, sum - mine, k);
+        return;
+      }
+      begin += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    b = a.s.B - 1;               // t is below the total
+  }
+};
+
+// Runs: `n` of them over `total` places, run w the places [begin(w), begin(w + 1)).
+struct Runs {
+  int64_t total;
+  int n;
+  __device__ __forceinline__ Runs(int64_t total_, int most)
+      : total(total_), n(static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(most), total_ / kMinChunks)))) {}
+  __device__ __forceinline__ int64_t begin(int w) const { return w >= n ? total : total * w / n; }
+};
+
+// A place in the list.
+template <int CH>
+struct Place {
+  int b, u, c, n, chunks;        // sequence, unit of it, chunk; the sequence's tokens and chunks of a unit
+  __device__ __forceinline__ void next(const List<CH>& l) {
+    if (++c < chunks) return;
+    c = 0;
+    if (++u < l.a.units) return;
+    u = 0;
+    if (++b < l.a.s.B) {
+      n = l.tokens(b);
+      chunks = l.chunks(n);
+    }
+  }
+};
+
+// A part of a unit, or none (unit -1): whether it has the unit's first and last chunk, and the CTA's first.
+struct Part {
+  int unit, head, tail, first;
+};
+
+template <int D, bool FOUR, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kernel(const PagedArgs a) {
+  using M = Plan<D, FOUR, NT>;
+  constexpr int CH = M::CH, SUB = CH / 16, KS = D / 16;
+  constexpr float kLift = FOUR ? 7.f : 0.f;                        // P is held 2^kLift larger
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ Part s_part[kWarps][2];
+  __shared__ int s_bad[kWarps][M::ST], s_flag;
   const PagedDims& s = a.s;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= static_cast<int64_t>(s.B) * s.nq * s.Hq) return;
-  const int h = static_cast<int>(w % s.Hq), i = static_cast<int>(w / s.Hq % s.nq), b = static_cast<int>(w / s.Hq / s.nq), kv = h / s.G;
-  const int most = s.max_pages << s.log_page, n0 = a.len[b], n = max(0, min(n0, most)), p = n - s.nq + i;
-  if (n != n0 && lane == 0) atomicOr(a.status, PISA_STATUS_POS_RANGE);
-  float q[D / 32], o[D / 32] = {}, m = neg_inf(), l = 0.f;
-  for (int k = 0; k < D / 32; ++k) q[k] = __bfloat162float(a.q[w * D + lane + 32 * k]);
-  const float ka = a.c.k_amp ? a.c.k_amp[kv] : 1.f, va = a.c.v_amp ? a.c.v_amp[kv] : 1.f, slope = a.slopes ? a.slopes[h] : 0.f;
-  for (int j = 0; j <= p; ++j) {
-    const int page = a.table[static_cast<int64_t>(b) * s.max_pages + (j >> s.log_page)];
-    if (page < 0 || page >= s.n_pages) {
-      if (lane == 0) atomicOr(a.status, PISA_STATUS_POS_RANGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, p2 = lane & 3;
+  const List<CH> list(a);
+  const Runs runs(list.total(), static_cast<int>(gridDim.x) * kWarps);
+  if (blockIdx.x * kWarps >= runs.n) {
+    if (threadIdx.x == 0) a.flags[blockIdx.x] = 0;
+    win::launch_dependents();
+    return;
+  }
+  if (threadIdx.x == 0) s_flag = 0;
+  if (threadIdx.x < 2 * kWarps) s_part[threadIdx.x >> 1][threadIdx.x & 1] = Part{-1, 0, 0, 0};
+  __syncthreads();
+  unsigned char* ring = sm + warp * M::RINGP;
+  auto first_part = [&](int k) { return a.part + (2 * static_cast<int64_t>(gridDim.x) + blockIdx.x * kWarps + k) * M::PARTF; };
+  const uint32_t ring_at = tc::su32(ring);
+  const int w = static_cast<int>(blockIdx.x) * kWarps + warp;
+  const int64_t t0 = runs.begin(w);
+  const int mine = static_cast<int>(runs.begin(w + 1) - t0);      // 0 past the last run
+
+  if (mine > 0) {
+    Place<CH> con;
+    {
+      int64_t begin;
+      list.find(t0, con.b, begin);
+      con.n = list.tokens(con.b);
+      con.chunks = list.chunks(con.n);
+      con.u = static_cast<int>((t0 - begin) / con.chunks);
+      con.c = static_cast<int>((t0 - begin) % con.chunks);
+    }
+    Place<CH> fet = con;
+    int ids = 0, ids_b = -1, ids_base = 0, fetched = 0;            // page of token ids_base + 16 lane of sequence ids_b
+    // byte offset of 16-byte piece c of a token's row
+    auto piece = [&](int r, int c) {
+      if (FOUR) return r * M::ROW + (D == 128 ? c ^ ((r >> 1) & 2) : c) * 16;
+      return r * M::ROW + (((c & ~7) | ((c ^ r) & 7)) << 4);
+    };
+    auto fetch = [&]() {
+      if (fetched < mine) {
+        const int stage = fetched % M::ST, v0 = fet.c * CH, kv = fet.u / a.sets;
+        if (fet.b != ids_b || v0 < ids_base || v0 >= ids_base + 512) {
+          ids_b = fet.b;
+          ids_base = v0 & ~511;
+          const int tok = ids_base + 16 * lane;
+          ids = tok < fet.n ? __ldg(a.table + static_cast<int64_t>(fet.b) * s.max_pages + (tok >> s.log_page)) : 0;
+        }
+        const uint32_t at = ring_at + stage * M::STAGE;
+        int bad = 0;
+#pragma unroll
+        for (int k = 0; k < SUB; ++k) {
+          const int tok = v0 + 16 * k, left = fet.n - tok;
+          const int page = __shfl_sync(0xffffffffu, ids, (tok - ids_base) >> 4);
+          const bool ok = left > 0 && page >= 0 && page < s.n_pages;
+          bad |= (left > 0 && !ok) << k;
+          const int64_t row = ok ? (static_cast<int64_t>(page) * s.Hkv + kv) * s.page + (tok & (s.page - 1)) : 0;
+          constexpr int P = M::ROW / 16, N = 16 * P;               // pieces of a token, of 16
+#pragma unroll
+          for (int x = 0; x < N / 32; ++x) {
+            const int r = (x * 32 + lane) / P, c = (x * 32 + lane) % P;
+            const bool in = ok && r < left;
+            const int64_t from = in ? (row + r) * M::ROW + 16 * c : 0;
+            const uint32_t to = at + k * 16 * M::ROW + piece(r, c);
+            tc::cp_async16(to, a.c.k + from, in);
+            tc::cp_async16(to + M::HALF, a.c.v + from, in);
+          }
+          if constexpr (FOUR) {
+            constexpr int SN = M::SROW;                            // 16-byte pieces of 16 tokens' scales
+            if (lane < 2 * SN) {
+              const int c = lane % SN;
+              const bool in = ok && c * 16 < left * M::SROW;
+              tc::cp_async16(at + (lane >= SN ? M::HALF : 0) + CH * M::ROW + k * 16 * M::SROW + 16 * c,
+                             (lane >= SN ? a.c.vs : a.c.ks) + (in ? row * M::SROW + 16 * c : 0), in);
+            }
+          }
+        }
+        if (lane == 0) {
+          s_bad[warp][stage] = bad;
+          const int len = a.len[fet.b];
+          if (bad || len < 0 || len > list.most) s_flag = 1;
+        }
+        ++fetched;
+        fet.next(list);
+      }
+      tc::cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < M::ST - 1; ++i) fetch();
+
+    uint32_t qf[NT][KS][2];                                        // Q^T: rows of the unit as columns
+    float c1[NT][2], slope[NT][2];                                 // of columns 2 p2, 2 p2 + 1: what a product is multiplied by; slope log2 e
+    int pos[NT][2];
+    float m[NT][2], l[NT][2], o[NT][KS][4];
+    int begun = 0;                                                 // the part's first chunk
+    auto unit_rows = [&](int u) { return min(M::COLS, a.rows - u % a.sets * M::COLS); };
+    // row x of unit u: the offset of its q and o in rows of D, its place in slopes, its position
+    auto row_at = [&](const Place<CH>& p, int x) {
+      const int r = p.u % a.sets * M::COLS + x, i = r / s.G, h = p.u / a.sets * s.G + r % s.G;
+      return (static_cast<int64_t>(p.b) * s.nq + i) * s.Hq + h;
+    };
+    auto open = [&]() {
+      begun = con.c;
+      const int rows = unit_rows(con.u), kv = con.u / a.sets;
+      const float scale = s.scale * (FOUR && a.c.k_amp ? __ldg(a.c.k_amp + kv) : 1.f) * (s.cap > 0.f ? 1.f / s.cap : kLog2e);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int x = 8 * t + g;
+        const bool in = x < rows;
+        float up = 1.f;
+        if (FOUR) {
+          // channels D / 4 p2 ..: a lane's quarter of the row
+          const bf16* qp = a.q + (in ? row_at(con, x) : 0) * D + D / 4 * p2;
+          uint32_t raw[D / 8];
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const uint4 v = in ? ldg_u4(qp + 8 * k) : make_uint4(0, 0, 0, 0);
+            raw[4 * k] = v.x;
+            raw[4 * k + 1] = v.y;
+            raw[4 * k + 2] = v.z;
+            raw[4 * k + 3] = v.w;
+          }
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) top = max(top, max(raw[k] & 0x7fffu, (raw[k] >> 16) & 0x7fffu));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // the largest magnitude between 2^7 and 2^8, by a power of two; its reciprocal goes into the scale
+          const int e = min(max(static_cast<int>(top >> 7), 14), 254) - 127 - 7;
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t v = raw[2 * k + y];
+              qf[t][k][y] = pack_f16(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
+            }
+          }
+        } else {
+          const bf16* qp = a.q + (in ? row_at(con, x) : 0) * D + 2 * p2;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            qf[t][k][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * k)) : 0u;
+            qf[t][k][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * k + 8)) : 0u;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = 8 * t + 2 * p2 + e, r = con.u % a.sets * M::COLS + col;
+          const bool there = col < rows;
+          c1[t][e] = scale * __shfl_sync(0xffffffffu, up, 8 * p2 + 4 * e);
+          slope[t][e] = there && a.slopes ? __ldg(a.slopes + kv * s.G + r % s.G) * kLog2e : 0.f;
+          pos[t][e] = there ? con.n - s.nq + r / s.G : -1;
+          m[t][e] = neg_inf();
+          l[t][e] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) o[t][k][0] = o[t][k][1] = o[t][k][2] = o[t][k][3] = 0.f;
+      }
+    };
+    // channel of o[..][k][e]
+    auto channel = [&](int k, int e) { return FOUR ? D / 8 * g + 2 * k + (e >> 1) : 16 * k + g + 8 * (e >> 1); };
+    // the part at hand is over: the unit's output if it is all of it, else a part
+    auto close = [&](bool tail) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
+      const bool head = begun == 0;
+      if (head && tail) {
+        const int rows = unit_rows(con.u);
+        const float amp = FOUR && a.c.v_amp ? __ldg(a.c.v_amp + con.u / a.sets) : 1.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int x = 8 * t + 2 * p2 + e;
+            if (x >= rows) continue;
+            const int64_t at = row_at(con, x);
+            const float inv = l[t][e] == 0.f ? 0.f : amp / l[t][e];
+            if (FOUR) {
+              uint32_t v[KS];
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+                v[k] = l[t][e] == 0.f ? 0u : pack_bf16(o[t][k][e] * inv, o[t][k][e + 2] * inv);
+#pragma unroll
+              for (int k = 0; k < KS; k += 4)
+                *reinterpret_cast<uint4*>(a.o + at * D + D / 8 * g + 2 * k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  a.o[at * D + channel(k, 2 * y)] = __float2bfloat16_rn(l[t][e] == 0.f ? 0.f : o[t][k][e + 2 * y] * inv);
+            }
+            if (g == 0 && a.lse) a.lse[at] = l[t][e] == 0.f ? neg_inf() : (m[t][e] - kLift + log2f(l[t][e])) * kLn2;
+          }
+        return;
+      }
+      if (head) {                                                  // the run's last part: over the ring, which nothing fills any more
+        tc::cp_async_wait<0>();
+        __syncwarp();
+      }
+      float* to = head ? reinterpret_cast<float*>(ring) : first_part(warp);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[(8 * t + 2 * p2 + (e & 1)) * D + channel(k, e)] = o[t][k][e];
+        if (g == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            to[M::COLS * D + 8 * t + 2 * p2 + e] = m[t][e];
+            to[M::COLS * D + M::COLS + 8 * t + 2 * p2 + e] = l[t][e];
+          }
+        }
+      }
+      if (lane == 0) s_part[warp][head] = Part{con.b * a.units + con.u, head, tail, 0};
+    };
+
+    const float cap2 = s.cap * kLog2e;
+    const int tok_g = FOUR ? (D == 128 ? g ^ ((g >> 1) & 1) : g ^ ((g >> 2) & 1)) : g;   // the token of S's row g
+    for (int i = 0; i < mine; ++i) {
+      if (i == 0 || con.c == 0) open();
+      tc::cp_async_wait<M::ST - 2>();
+      __syncwarp();
+      const int stage = i % M::ST, v0 = con.c * CH, bad = s_bad[warp][stage];
+      const uint32_t at = ring_at + stage * M::STAGE;
+      const unsigned char* st = ring + stage * M::STAGE;
+      float x[NT][SUB][4];
+#pragma unroll
+      for (int k = 0; k < SUB; ++k) {
+        float sc[NT][2][4] = {};
+        if constexpr (FOUR) {
+          uint32_t w0[D / 32], w1[D / 32], s2[2];                  // the lane's codes of tokens tok_g and tok_g + 8
+          const int r0 = 16 * k + tok_g, r1 = r0 + 8;
+          if constexpr (D == 128) {
+            const uint4 u0 = *reinterpret_cast<const uint4*>(st + piece(r0, p2)), u1 = *reinterpret_cast<const uint4*>(st + piece(r1, p2));
+            w0[0] = u0.x, w0[1] = u0.y, w0[2] = u0.z, w0[3] = u0.w;
+            w1[0] = u1.x, w1[1] = u1.y, w1[2] = u1.z, w1[3] = u1.w;
+            s2[0] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r0 * M::SROW + 2 * p2));
+            s2[1] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r1 * M::SROW + 2 * p2));
+          } else {
+            const uint2 u0 = *reinterpret_cast<const uint2*>(st + r0 * M::ROW + 8 * p2), u1 = *reinterpret_cast<const uint2*>(st + r1 * M::ROW + 8 * p2);
+            w0[0] = u0.x, w0[1] = u0.y;
+            w1[0] = u1.x, w1[1] = u1.y;
+            s2[0] = scales_of(st[CH * M::ROW + r0 * M::SROW + p2]);
+            s2[1] = scales_of(st[CH * M::ROW + r1 * M::SROW + p2]);
+          }
+#pragma unroll
+          for (int wd = 0; wd < D / 32; ++wd) {
+            uint32_t h0[4], h1[4];
+            paged::from_e2m1x8(w0[wd], h0);
+            paged::from_e2m1x8(w1[wd], h1);
+            const uint32_t sel = wd & 2 ? 0x3232u : 0x1010u;       // a group is two words
+            const uint32_t f0 = __byte_perm(s2[0], 0, sel), f1 = __byte_perm(s2[1], 0, sel);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t kf[4] = {mul_h2(h0[2 * y], f0), mul_h2(h1[2 * y], f1), mul_h2(h0[2 * y + 1], f0), mul_h2(h1[2 * y + 1], f1)};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma_f16(sc[t][y], kf, qf[t][2 * wd + y][0], qf[t][2 * wd + y][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {
+            uint32_t kf[4];
+            ldsm4(kf, at + piece(lane & 15, 2 * y + (lane >> 4)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_bf16(sc[t][y & 1], kf, qf[t][y][0], qf[t][y][1]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][k][e] = sc[t][0][e] + sc[t][1][e];
+      }
+      // scores in powers of two; what is not seen
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < SUB; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = v0 + 16 * k + tok_g + 8 * (e >> 1), q = e & 1;
+            float z = x[t][k][e] * c1[t][q];
+            if (s.cap > 0.f) z = cap2 * tanh_of(z);
+            z -= slope[t][q] * static_cast<float>(pos[t][q] - j);
+            x[t][k][e] = j <= pos[t][q] && !((bad >> k) & 1) ? z : neg_inf();
+          }
+      float top[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(x[t][0][e], x[t][0][e + 2]);
+#pragma unroll
+          for (int k = 1; k < SUB; ++k) v = fmaxf(v, fmaxf(x[t][k][e], x[t][k][e + 2]));
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+          top[t][e] = v;
+          grow |= v > m[t][e] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[t][e], top[t][e]);
+            f[e] = tc::ex2(m[t][e] - base_of(mn));
+            m[t][e] = mn;
+            l[t][e] *= f[e];
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            o[t][k][0] *= f[0];
+            o[t][k][1] *= f[1];
+            o[t][k][2] *= f[0];
+            o[t][k][3] *= f[1];
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < SUB; ++k) {
+        uint32_t pb[NT][2];                                        // P^T: tokens x rows
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[t][k][e] = tc::ex2(x[t][k][e] - (base_of(m[t][e & 1]) - kLift));
+          l[t][0] += x[t][k][0] + x[t][k][2];
+          l[t][1] += x[t][k][1] + x[t][k][3];
+          if (FOUR) {
+            pb[t][0] = transpose8(pack_f16(x[t][k][0], x[t][k][1]));
+            pb[t][1] = transpose8(pack_f16(x[t][k][2], x[t][k][3]));
+          } else {
+            pb[t][0] = transpose8(pack_bf16(x[t][k][0], x[t][k][1]));
+            pb[t][1] = transpose8(pack_bf16(x[t][k][2], x[t][k][3]));
+          }
+        }
+        if constexpr (FOUR) {
+          // tokens of the contraction's slots 2 p2, 2 p2 + 1 (pair 0) and those + 8 (pair 1)
+          auto tok = [&](int slot) { return 16 * k + (D == 128 ? slot ^ ((slot >> 1) & 1) : slot ^ ((slot >> 2) & 1)); };
+          const int ra = tok(2 * p2), rb = tok(2 * p2 + 1);
+          const unsigned char* vt = st + M::HALF;
+          uint32_t va[2][D / 64], vb[2][D / 64], f[2];             // the lane's codes, D / 8 channels from D / 8 g on
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int a8 = ra + 8 * h, b8 = rb + 8 * h;
+            if constexpr (D == 128) {
+              const uint2 ua = *reinterpret_cast<const uint2*>(vt + piece(a8, g >> 1) + 8 * (g & 1)),
+                          ub = *reinterpret_cast<const uint2*>(vt + piece(b8, g >> 1) + 8 * (g & 1));
+              va[h][0] = ua.x, va[h][1] = ua.y;
+              vb[h][0] = ub.x, vb[h][1] = ub.y;
+            } else {
+              va[h][0] = *reinterpret_cast<const uint32_t*>(vt + a8 * M::ROW + 4 * g);
+              vb[h][0] = *reinterpret_cast<const uint32_t*>(vt + b8 * M::ROW + 4 * g);
+            }
+            const int grp = D == 128 ? g : g >> 1;
+            uint32_t sa = vt[CH * M::ROW + a8 * M::SROW + grp], sb = vt[CH * M::ROW + b8 * M::SROW + grp];
+            if (v0 + a8 >= con.n) sa = 0;                          // behind the end the codes are 0, the scales whatever they are
+            if (v0 + b8 >= con.n) sb = 0;
+            f[h] = scales_of(sa | sb << 8);
+          }
+#pragma unroll
+          for (int wd = 0; wd < D / 64; ++wd) {
+            uint32_t lo[2][4], hi[2][4];                           // even and odd channels, both tokens of a pair
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t ua = va[h][wd], ub = vb[h][wd];
+              paged::from_e2m1x8((ua & 0x0f0f0f0fu) | ((ub & 0x0f0f0f0fu) << 4), lo[h]);
+              paged::from_e2m1x8(((ua >> 4) & 0x0f0f0f0fu) | (ub & 0xf0f0f0f0u), hi[h]);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t vf[4] = {mul_h2(lo[0][y], f[0]), mul_h2(hi[0][y], f[0]), mul_h2(lo[1][y], f[1]), mul_h2(hi[1][y], f[1])};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * wd + y], vf, pb[t][0], pb[t][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < KS; ++y) {
+            uint32_t vf[4];
+            ldsm4_trans(vf, at + M::HALF + piece((lane & 7) + ((lane >> 4) << 3), 2 * y + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_bf16(o[t][y], vf, pb[t][0], pb[t][1]);
+          }
+        }
+      }
+      __syncwarp();                                                // every lane has read the stage that fetch() refills next
+      fetch();
+      const bool tail = con.c + 1 == con.chunks;
+      if (tail || i + 1 == mine) {
+        const bool first = warp == 0 && i - (con.c - begun) == 0;  // the part has the run's first chunk, and the run is the CTA's first
+        close(tail);
+        __syncwarp();
+        if (lane == 0 && first && !(begun == 0 && tail)) s_part[warp][begun == 0].first = 1;
+      }
+      con.next(list);
+    }
+    tc::cp_async_wait<0>();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) a.flags[blockIdx.x] = s_flag ? PISA_STATUS_POS_RANGE : 0;
+  // ---- join the warps' parts: at most two a warp, in the list's order, those of one unit next to one another
+  int at = 0;
+  while (at < 2 * kWarps) {
+    const Part p = s_part[at >> 1][at & 1];
+    if (p.unit < 0) {
+      ++at;
       continue;
     }
-    const int64_t row = (static_cast<int64_t>(page) * s.Hkv + kv) * s.page + (j & (s.page - 1));
-    float x = 0.f;
-    for (int k = 0; k < D / 32; ++k) x += q[k] * element<D>(s, a.c.k, a.c.ks, row, lane + 32 * k);
-    x = warp_sum(x) * s.scale * ka;
-    if (s.cap > 0.f) x = s.cap * tanhf(x / s.cap);
-    x -= slope * static_cast<float>(p - j);
-    const float mn = fmaxf(m, x), f = mn == neg_inf() ? 1.f : expf(m - mn), e = mn == neg_inf() ? 0.f : expf(x - mn);
-    m = mn;
-    l = l * f + e;
-    for (int k = 0; k < D / 32; ++k) o[k] = o[k] * f + e * element<D>(s, a.c.v, a.c.vs, row, lane + 32 * k);
+    int end = at + 1;
+    bool tail = p.tail;
+    for (; end < 2 * kWarps; ++end) {
+      const Part x = s_part[end >> 1][end & 1];
+      if (x.unit >= 0 && x.unit != p.unit) break;
+      if (x.unit == p.unit) tail |= x.tail;
+    }
+    const int b = p.unit / a.units, u = p.unit % a.units, rows = min(M::COLS, a.rows - u % a.sets * M::COLS);
+    auto part = [&](int k) {
+      return k & 1 ? reinterpret_cast<const float*>(sm + (k >> 1) * M::RINGP) : first_part(k >> 1);
+    };
+    const bool whole = p.head && tail;
+    float* to = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (p.first ? 0 : 1)) * M::PARTF;
+    const float amp = FOUR && a.c.v_amp ? __ldg(a.c.v_amp + u / a.sets) : 1.f;
+    for (int y = threadIdx.x; y < rows * D; y += 32 * kWarps) {
+      const int x = y / D;
+      float mm = neg_inf(), ll = 0.f, oo = 0.f;
+      for (int k = at; k < end; ++k)
+        if (s_part[k >> 1][k & 1].unit >= 0) mm = fmaxf(mm, part(k)[M::COLS * D + x]);
+      for (int k = at; k < end; ++k)
+        if (s_part[k >> 1][k & 1].unit >= 0) {
+          const float f = tc::ex2(part(k)[M::COLS * D + x] - base_of(mm));
+          oo += f * part(k)[y];
+          ll += f * part(k)[M::COLS * D + M::COLS + x];
+        }
+      if (whole) {
+        const int r = u % a.sets * M::COLS + x, i = r / s.G, h = u / a.sets * s.G + r % s.G;
+        const int64_t row = (static_cast<int64_t>(b) * s.nq + i) * s.Hq + h;
+        a.o[row * D + y % D] = __float2bfloat16_rn(ll == 0.f ? 0.f : oo * amp / ll);
+        if (y % D == 0 && a.lse) a.lse[row] = ll == 0.f ? neg_inf() : (mm - kLift + log2f(ll)) * kLn2;
+      } else {
+        to[y] = oo;
+        if (y % D == 0) {
+          to[M::COLS * D + x] = mm;
+          to[M::COLS * D + M::COLS + x] = ll;
+        }
+      }
+    }
+    at = end;
   }
-  for (int k = 0; k < D / 32; ++k) a.o[w * D + lane + 32 * k] = __float2bfloat16_rn(l == 0.f ? 0.f : o[k] * va / l);
-  if (lane == 0 && a.lse) a.lse[w] = l == 0.f ? neg_inf() : m + logf(l);
+  win::launch_dependents();
 }
+
+// Units that cross CTAs: block (c, x) joins row x of the unit that crosses into CTA c + 1, if c + 1 is the first CTA that it crosses
+// into. Also the status word, from the CTAs' flags.
+template <int D, bool FOUR, int NT>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int ctas) {
+  using M = Plan<D, FOUR, NT>;
+  constexpr int LPR = D / 4, GR = 128 / LPR;                       // lanes of a row, parts at a time
+  constexpr float kLift = FOUR ? 7.f : 0.f;
+  __shared__ float s_m[GR], s_l[GR];
+  __shared__ float4 s_o[GR][LPR];
+  const PagedDims& s = a.s;
+  const List<M::CH> list(a);
+  const Runs runs(list.total(), ctas * kWarps);
+  const int c = static_cast<int>(blockIdx.x) + 1, x = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t t = runs.begin(c * kWarps);
+  int b = 0;
+  int64_t begin = 0;
+  bool mine = c < ctas && t < runs.total;
+  int u = 0, last = c;
+  if (mine) {
+    list.find(t, b, begin);
+    const int chunks = list.chunks(list.tokens(b));
+    u = static_cast<int>((t - begin) / chunks);
+    begin += static_cast<int64_t>(u) * chunks;
+    mine = t > begin && runs.begin((c - 1) * kWarps) <= begin && x < min(M::COLS, a.rows - u % a.sets * M::COLS);
+    while (last + 1 < ctas && runs.begin((last + 1) * kWarps) < begin + chunks) ++last;
+  }
+  win::grid_wait();
+  if (blockIdx.x == 0 && x == 0 && threadIdx.x < 32) {
+    int any = 0;
+    for (int k = lane; k < ctas; k += 32) any |= a.flags[k];
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) *a.status = any ? PISA_STATUS_POS_RANGE : 0;
+  }
+  if (!mine) return;
+  const int gr = threadIdx.x / LPR, e = threadIdx.x % LPR;
+  auto part = [&](int k) {
+    return a.part + (2 * static_cast<int64_t>(k) + (runs.begin(k * kWarps) >= begin ? 0 : 1)) * M::PARTF;
+  };
+  float mm = neg_inf(), ll = 0.f;
+  float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = c - 1 + gr; k <= last; k += GR) mm = fmaxf(mm, part(k)[M::COLS * D + x]);
+#pragma unroll 4
+  for (int k = c - 1 + gr; k <= last; k += GR) {
+    const float* p = part(k);
+    const float f = tc::ex2(p[M::COLS * D + x] - base_of(mm));
+    const float4 v = *reinterpret_cast<const float4*>(p + x * D + 4 * e);
+    oo.x += f * v.x;
+    oo.y += f * v.y;
+    oo.z += f * v.z;
+    oo.w += f * v.w;
+    ll += f * p[M::COLS * D + M::COLS + x];
+  }
+  s_o[gr][e] = oo;
+  if (e == 0) {
+    s_m[gr] = mm;
+    s_l[gr] = ll;
+  }
+  __syncthreads();
+  if (gr > 0) return;
+#pragma unroll
+  for (int k = 1; k < GR; ++k) mm = fmaxf(mm, s_m[k]);
+  ll = 0.f;
+  oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < GR; ++k) {
+    const float f = tc::ex2(s_m[k] - base_of(mm));
+    const float4 v = s_o[k][e];
+    oo.x += f * v.x;
+    oo.y += f * v.y;
+    oo.z += f * v.z;
+    oo.w += f * v.w;
+    ll += f * s_l[k];
+  }
+  const int r = u % a.sets * M::COLS + x, i = r / s.G, h = u / a.sets * s.G + r % s.G;
+  const int64_t row = (static_cast<int64_t>(b) * s.nq + i) * s.Hq + h;
+  const float inv = ll == 0.f ? 0.f : (FOUR && a.c.v_amp ? __ldg(a.c.v_amp + u / a.sets) : 1.f) / ll;
+  const uint2 out = ll == 0.f ? make_uint2(0, 0) : make_uint2(pack_bf16(oo.x * inv, oo.y * inv), pack_bf16(oo.z * inv, oo.w * inv));
+  *reinterpret_cast<uint2*>(a.o + row * D + 4 * e) = out;
+  if (e == 0 && a.lse) a.lse[row] = ll == 0.f ? neg_inf() : (mm - kLift + log2f(ll)) * kLn2;
+}
+
+int cols_of(const PagedDims& s) { return s.G * s.nq <= 8 ? 8 : 16; }
+
+template <int D, bool FOUR, int NT>
+int attn_launch(PagedArgs& a, cudaStream_t st) {
+  using M = Plan<D, FOUR, NT>;
+  static win::Ready ready;
+  static std::atomic<int> known[64];                               // CTAs an SM holds + 1, per device
+  int dev = 0;
+  if (int e = ready(paged_attn_kernel<D, FOUR, NT>, M::bytes)) return e;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  int held = dev < 64 ? known[dev].load(std::memory_order_relaxed) - 1 : -1;
+  if (held < 0) {
+    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, paged_attn_kernel<D, FOUR, NT>, 32 * kWarps, M::bytes)) return e;
+    if (held < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 64) known[dev].store(held + 1, std::memory_order_relaxed);
+  }
+  const int ctas = std::min(sm_count() * std::min(held, kMaxCtas), win::kPlanSms * kMaxCtas);
+  a.sets = (a.rows + M::COLS - 1) / M::COLS;
+  a.units = a.s.Hkv * a.sets;
+  {
+    ProfScope ps(st, "paged_attn");
+    paged_attn_kernel<D, FOUR, NT><<<ctas, 32 * kWarps, M::bytes, st>>>(a);
+  }
+  if (cudaError_t e = cudaGetLastError()) return e;
+  ProfScope ps(st, "paged_join");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1, ctas - 1)), M::COLS);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT>, static_cast<const PagedArgs&>(a), ctas);
+}
+
+template <int D, bool FOUR>
+int by_rows(PagedArgs& a, cudaStream_t st) {
+  return cols_of(a.s) == 8 ? attn_launch<D, FOUR, 1>(a, st) : attn_launch<D, FOUR, 2>(a, st);
+}
+
+constexpr size_t kFlags = 256, kParts = kFlags + (win::kPlanSms * kMaxCtas * 4 + 255) / 256 * 256;
 
 }  // namespace
 
-size_t paged_attn_ws(const PagedDims&) { return 256; }
+size_t paged_attn_ws(const PagedDims& s) {
+  return kParts + static_cast<size_t>((2 + kWarps) * win::kPlanSms * kMaxCtas) * cols_of(s) * (s.d + 2) * 4;
+}
 
 int launch_paged_attn(const PagedDims& s, const PagedCache& c, const int32_t* table, const int32_t* len, const void* q,
                       const float* slopes, void* o, float* lse, char* ws, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const PagedArgs a{s, c, table, len, static_cast<const bf16*>(q), slopes, static_cast<bf16*>(o), lse, reinterpret_cast<int32_t*>(ws)};
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
-  if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(s.B) * s.nq * s.Hq + 3) / 4);
-  ProfScope ps(st, "paged_attn");
-  if (s.d == 128) paged_attn_kernel<128><<<blocks, 128, 0, st>>>(a);
-  else paged_attn_kernel<64><<<blocks, 128, 0, st>>>(a);
-  return cudaGetLastError();
+  PagedArgs a{};
+  a.s = s;
+  a.c = c;
+  a.table = table;
+  a.len = len;
+  a.q = static_cast<const bf16*>(q);
+  a.slopes = slopes;
+  a.o = static_cast<bf16*>(o);
+  a.lse = lse;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.flags = reinterpret_cast<int32_t*>(ws + kFlags);
+  a.part = reinterpret_cast<float*>(ws + kParts);
+  a.rows = s.G * s.nq;
+  if (s.d == 128) return s.bits == 4 ? by_rows<128, true>(a, st) : by_rows<128, false>(a, st);
+  return s.bits == 4 ? by_rows<64, true>(a, st) : by_rows<64, false>(a, st);
 }
 
 }  // namespace pisa
