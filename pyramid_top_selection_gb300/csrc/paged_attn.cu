@@ -35,7 +35,7 @@ constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;                  // log2 growth of the maximum that O is rescaled for
 constexpr int kMinChunks = 2;                  // chunks of a run at least, where the list has as many
-constexpr int kMaxCtas = 3;                    // CTAs an SM holds at most
+constexpr int kMaxCtas = 4;                    // CTAs an SM holds at most
 
 struct PagedArgs {
   PagedDims s;
@@ -63,7 +63,8 @@ struct Plan {
   static constexpr int RING = ST * STAGE;
   static constexpr int COLS = 8 * NT;                              // rows of a unit
   static constexpr int PARTF = COLS * (D + 2), PART = PARTF * 4;   // a part: O [COLS][D], m, l
-  static constexpr int RINGP = RING > PART ? RING : PART;          // the run's last part is laid over the ring
+  static constexpr int TAIL = PART + 2 * kWarps * COLS * 4;        // the run's last part is laid over the ring, the join's factors behind it
+  static constexpr int RINGP = RING > TAIL ? RING : TAIL;
   static constexpr int bytes = kWarps * RINGP;
 };
 
@@ -155,6 +156,7 @@ struct Runs {
   __device__ __forceinline__ Runs(int64_t total_, int most)
       : total(total_), n(static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(most), total_ / kMinChunks)))) {}
   __device__ __forceinline__ int64_t begin(int w) const { return w >= n ? total : total * w / n; }
+  __device__ __forceinline__ int of(int64_t t) const { return static_cast<int>(((t + 1) * n - 1) / total); }   // the run that has place t
 };
 
 // A place in the list.
@@ -179,7 +181,7 @@ struct Part {
 };
 
 template <int D, bool FOUR, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged_attn_kernel(const PagedArgs a) {
   using M = Plan<D, FOUR, NT>;
   constexpr int CH = M::CH, SUB = CH / 16, KS = D / 16;
   constexpr float kLift = FOUR ? 7.f : 0.f;                        // P is held 2^kLift larger
@@ -222,14 +224,18 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
       if (FOUR) return r * M::ROW + (D == 128 ? c ^ ((r >> 1) & 2) : c) * 16;
       return r * M::ROW + (((c & ~7) | ((c ^ r) & 7)) << 4);
     };
+    // 16-byte pieces of 16 tokens: a lane's are those at lane + 32 x; rows of a piece's run of 32 lanes
+    constexpr int P = M::ROW / 16, NP = P / 2, RPX = 32 / P;
+    const int lane_from = lane * 16, lane_to = piece(lane / P, lane % P);
     auto fetch = [&]() {
       if (fetched < mine) {
         const int stage = fetched % M::ST, v0 = fet.c * CH, kv = fet.u / a.sets;
         if (fet.b != ids_b || v0 < ids_base || v0 >= ids_base + 512) {
           ids_b = fet.b;
           ids_base = v0 & ~511;
-          const int tok = ids_base + 16 * lane;
+          const int tok = ids_base + 16 * lane, len = a.len[fet.b];
           ids = tok < fet.n ? __ldg(a.table + static_cast<int64_t>(fet.b) * s.max_pages + (tok >> s.log_page)) : 0;
+          if (len < 0 || len > list.most) s_flag = 1;
         }
         const uint32_t at = ring_at + stage * M::STAGE;
         int bad = 0;
@@ -237,33 +243,43 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
         for (int k = 0; k < SUB; ++k) {
           const int tok = v0 + 16 * k, left = fet.n - tok;
           const int page = __shfl_sync(0xffffffffu, ids, (tok - ids_base) >> 4);
-          const bool ok = left > 0 && page >= 0 && page < s.n_pages;
+          const bool ok = left > 0 && static_cast<uint32_t>(page) < static_cast<uint32_t>(s.n_pages);
           bad |= (left > 0 && !ok) << k;
-          const int64_t row = ok ? (static_cast<int64_t>(page) * s.Hkv + kv) * s.page + (tok & (s.page - 1)) : 0;
-          constexpr int P = M::ROW / 16, N = 16 * P;               // pieces of a token, of 16
-#pragma unroll
-          for (int x = 0; x < N / 32; ++x) {
-            const int r = (x * 32 + lane) / P, c = (x * 32 + lane) % P;
-            const bool in = ok && r < left;
-            const int64_t from = in ? (row + r) * M::ROW + 16 * c : 0;
-            const uint32_t to = at + k * 16 * M::ROW + piece(r, c);
-            tc::cp_async16(to, a.c.k + from, in);
-            tc::cp_async16(to + M::HALF, a.c.v + from, in);
-          }
+          const int64_t row = (static_cast<int64_t>(ok ? page : 0) * s.Hkv + kv) * s.page + (tok & (s.page - 1));
+          const unsigned char* kp = a.c.k + row * M::ROW + lane_from;
+          const unsigned char* vp = a.c.v + row * M::ROW + lane_from;
+          const uint32_t to = at + k * 16 * M::ROW + lane_to;
           if constexpr (FOUR) {
-            constexpr int SN = M::SROW;                            // 16-byte pieces of 16 tokens' scales
-            if (lane < 2 * SN) {
-              const int c = lane % SN;
-              const bool in = ok && c * 16 < left * M::SROW;
-              tc::cp_async16(at + (lane >= SN ? M::HALF : 0) + CH * M::ROW + k * 16 * M::SROW + 16 * c,
-                             (lane >= SN ? a.c.vs : a.c.ks) + (in ? row * M::SROW + 16 * c : 0), in);
+            // slots behind the end come along: whatever they hold, their scores are hidden and their scales set to 0
+            if (ok) {
+#pragma unroll
+              for (int x = 0; x < NP; ++x) {
+                // (the piece's permutation goes by bit 2 of the row: the same for rows 8 apart)
+                static_assert(NP == 1 || RPX == 8, "a lane's pieces lie 8 rows apart");
+                tc::cp_async16(to + x * 512, kp + x * 512, true);
+                tc::cp_async16(to + x * 512 + M::HALF, vp + x * 512, true);
+              }
+              constexpr int SN = M::SROW;                          // 16-byte pieces of 16 tokens' scales
+              if (lane < 2 * SN) {
+                const int c = lane % SN;
+                tc::cp_async16(at + (lane >= SN ? M::HALF : 0) + CH * M::ROW + k * 16 * M::SROW + 16 * c,
+                               (lane >= SN ? a.c.vs : a.c.ks) + row * M::SROW + 16 * c, true);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+              const int r = x * RPX + lane / P;
+              const bool in = ok && r < left;
+              const uint32_t dst = at + piece(r, lane % P);
+              tc::cp_async16(dst, kp + x * 512, in);
+              tc::cp_async16(dst + M::HALF, vp + x * 512, in);
             }
           }
         }
         if (lane == 0) {
           s_bad[warp][stage] = bad;
-          const int len = a.len[fet.b];
-          if (bad || len < 0 || len > list.most) s_flag = 1;
+          if (bad) s_flag = 1;
         }
         ++fetched;
         fet.next(list);
@@ -465,18 +481,39 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
           for (int e = 0; e < 4; ++e) x[t][k][e] = sc[t][0][e] + sc[t][1][e];
       }
       // scores in powers of two; what is not seen
+      const bool full = bad == 0 && v0 + CH <= con.n - s.nq + 1;   // every row sees the whole chunk
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int k = 0; k < SUB; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = v0 + 16 * k + tok_g + 8 * (e >> 1), q = e & 1;
-            float z = x[t][k][e] * c1[t][q];
-            if (s.cap > 0.f) z = cap2 * tanh_of(z);
-            z -= slope[t][q] * static_cast<float>(pos[t][q] - j);
-            x[t][k][e] = j <= pos[t][q] && !((bad >> k) & 1) ? z : neg_inf();
-          }
+          for (int e = 0; e < 4; ++e) x[t][k][e] *= c1[t][e & 1];
+      if (s.cap > 0.f) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < SUB; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][k][e] = cap2 * tanh_of(x[t][k][e]);
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < SUB; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[t][k][e] -= slope[t][e & 1] * static_cast<float>(pos[t][e & 1] - (v0 + 16 * k + tok_g + 8 * (e >> 1)));
+      }
+      if (!full) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < SUB; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (v0 + 16 * k + tok_g + 8 * (e >> 1) > pos[t][e & 1] || (bad >> k) & 1) x[t][k][e] = neg_inf();
+      }
       float top[NT][2];
       bool grow = false;
 #pragma unroll
@@ -548,8 +585,10 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
             }
             const int grp = D == 128 ? g : g >> 1;
             uint32_t sa = vt[CH * M::ROW + a8 * M::SROW + grp], sb = vt[CH * M::ROW + b8 * M::SROW + grp];
-            if (v0 + a8 >= con.n) sa = 0;                          // behind the end the codes are 0, the scales whatever they are
-            if (v0 + b8 >= con.n) sb = 0;
+            if (!full) {                                           // what is behind the end, or was not copied
+              if (v0 + a8 >= con.n || (bad >> k) & 1) sa = 0;
+              if (v0 + b8 >= con.n || (bad >> k) & 1) sb = 0;
+            }
             f[h] = scales_of(sa | sb << 8);
           }
 #pragma unroll
@@ -558,8 +597,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t ua = va[h][wd], ub = vb[h][wd];
-              paged::from_e2m1x8((ua & 0x0f0f0f0fu) | ((ub & 0x0f0f0f0fu) << 4), lo[h]);
-              paged::from_e2m1x8(((ua >> 4) & 0x0f0f0f0fu) | (ub & 0xf0f0f0f0u), hi[h]);
+              constexpr uint32_t kLow = 0x0f0f0f0fu;
+              paged::from_e2m1x8((ua & kLow) | ((ub << 4) & ~kLow), lo[h]);
+              paged::from_e2m1x8(((ua >> 4) & kLow) | (ub & ~kLow), hi[h]);
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -594,6 +634,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
   __syncthreads();
   if (threadIdx.x == 0) a.flags[blockIdx.x] = s_flag ? PISA_STATUS_POS_RANGE : 0;
   // ---- join the warps' parts: at most two a warp, in the list's order, those of one unit next to one another
+  float* f_of = reinterpret_cast<float*>(sm) + M::PARTF;           // [2 kWarps][COLS]: behind the first warp's part, in its ring
   int at = 0;
   while (at < 2 * kWarps) {
     const Part p = s_part[at >> 1][at & 1];
@@ -603,42 +644,70 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) paged_attn_kerne
     }
     int end = at + 1;
     bool tail = p.tail;
+    uint32_t in = 1u << at;
     for (; end < 2 * kWarps; ++end) {
       const Part x = s_part[end >> 1][end & 1];
       if (x.unit >= 0 && x.unit != p.unit) break;
-      if (x.unit == p.unit) tail |= x.tail;
+      if (x.unit == p.unit) {
+        tail |= x.tail;
+        in |= 1u << end;
+      }
     }
     const int b = p.unit / a.units, u = p.unit % a.units, rows = min(M::COLS, a.rows - u % a.sets * M::COLS);
-    auto part = [&](int k) {
+    auto part = [&](int k) -> const float* {
       return k & 1 ? reinterpret_cast<const float*>(sm + (k >> 1) * M::RINGP) : first_part(k >> 1);
     };
     const bool whole = p.head && tail;
     float* to = a.part + (2 * static_cast<int64_t>(blockIdx.x) + (p.first ? 0 : 1)) * M::PARTF;
     const float amp = FOUR && a.c.v_amp ? __ldg(a.c.v_amp + u / a.sets) : 1.f;
-    for (int y = threadIdx.x; y < rows * D; y += 32 * kWarps) {
-      const int x = y / D;
-      float mm = neg_inf(), ll = 0.f, oo = 0.f;
-      for (int k = at; k < end; ++k)
-        if (s_part[k >> 1][k & 1].unit >= 0) mm = fmaxf(mm, part(k)[M::COLS * D + x]);
-      for (int k = at; k < end; ++k)
-        if (s_part[k >> 1][k & 1].unit >= 0) {
-          const float f = tc::ex2(part(k)[M::COLS * D + x] - base_of(mm));
-          oo += f * part(k)[y];
-          ll += f * part(k)[M::COLS * D + M::COLS + x];
-        }
-      if (whole) {
-        const int r = u % a.sets * M::COLS + x, i = r / s.G, h = u / a.sets * s.G + r % s.G;
-        const int64_t row = (static_cast<int64_t>(b) * s.nq + i) * s.Hq + h;
-        a.o[row * D + y % D] = __float2bfloat16_rn(ll == 0.f ? 0.f : oo * amp / ll);
-        if (y % D == 0 && a.lse) a.lse[row] = ll == 0.f ? neg_inf() : (mm - kLift + log2f(ll)) * kLn2;
-      } else {
-        to[y] = oo;
-        if (y % D == 0) {
-          to[M::COLS * D + x] = mm;
-          to[M::COLS * D + M::COLS + x] = ll;
-        }
+    auto row_of = [&](int x) {
+      const int r = u % a.sets * M::COLS + x, i = r / s.G, h = u / a.sets * s.G + r % s.G;
+      return (static_cast<int64_t>(b) * s.nq + i) * s.Hq + h;
+    };
+    if (threadIdx.x < rows) {                                      // a row's factor of every part, and its sum
+      const int x = threadIdx.x;
+      float pm[2 * kWarps], mm = neg_inf(), ll = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k) {
+        pm[k] = (in >> k) & 1 ? part(k)[M::COLS * D + x] : neg_inf();
+        mm = fmaxf(mm, pm[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k) {
+        pm[k] = tc::ex2(pm[k] - base_of(mm));
+        if ((in >> k) & 1) ll += pm[k] * part(k)[M::COLS * D + M::COLS + x];
+      }
+      const float inv = !whole ? 1.f : ll == 0.f ? 0.f : amp / ll;
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k) f_of[k * M::COLS + x] = pm[k] * inv;
+      if (!whole) {
+        to[M::COLS * D + x] = mm;
+        to[M::COLS * D + M::COLS + x] = ll;
+      } else if (a.lse) {
+        a.lse[row_of(x)] = ll == 0.f ? neg_inf() : (mm - kLift + log2f(ll)) * kLn2;
       }
     }
+    __syncthreads();
+    for (int y = threadIdx.x; y < rows * (D / 4); y += 32 * kWarps) {
+      const int x = y / (D / 4), e = 4 * (y % (D / 4));
+      float4 v[2 * kWarps], oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k)
+        v[k] = (in >> k) & 1 ? *reinterpret_cast<const float4*>(part(k) + x * D + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 2 * kWarps; ++k) {
+        const float f = f_of[k * M::COLS + x];
+        if ((in >> k) & 1) {
+          oo.x += f * v[k].x;
+          oo.y += f * v[k].y;
+          oo.z += f * v[k].z;
+          oo.w += f * v[k].w;
+        }
+      }
+      if (whole) *reinterpret_cast<uint2*>(a.o + row_of(x) * D + e) = make_uint2(pack_bf16(oo.x, oo.y), pack_bf16(oo.z, oo.w));
+      else *reinterpret_cast<float4*>(to + x * D + e) = oo;
+    }
+    __syncthreads();                                               // before the next unit's factors
     at = end;
   }
   win::launch_dependents();
@@ -668,7 +737,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int 
     u = static_cast<int>((t - begin) / chunks);
     begin += static_cast<int64_t>(u) * chunks;
     mine = t > begin && runs.begin((c - 1) * kWarps) <= begin && x < min(M::COLS, a.rows - u % a.sets * M::COLS);
-    while (last + 1 < ctas && runs.begin((last + 1) * kWarps) < begin + chunks) ++last;
+    last = runs.of(begin + chunks - 1) / kWarps;
   }
   win::grid_wait();
   if (blockIdx.x == 0 && x == 0 && threadIdx.x < 32) {
@@ -679,13 +748,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int 
   }
   if (!mine) return;
   const int gr = threadIdx.x / LPR, e = threadIdx.x % LPR;
-  auto part = [&](int k) {
-    return a.part + (2 * static_cast<int64_t>(k) + (runs.begin(k * kWarps) >= begin ? 0 : 1)) * M::PARTF;
-  };
+  // only the first of its CTAs can have begun before the unit
+  const int late = mine && runs.begin((c - 1) * kWarps) < begin ? c - 1 : -1;
+  auto part = [&](int k) { return a.part + (2 * static_cast<int64_t>(k) + (k == late)) * M::PARTF; };
   float mm = neg_inf(), ll = 0.f;
   float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
   for (int k = c - 1 + gr; k <= last; k += GR) mm = fmaxf(mm, part(k)[M::COLS * D + x]);
-#pragma unroll 4
+#pragma unroll 8
   for (int k = c - 1 + gr; k <= last; k += GR) {
     const float* p = part(k);
     const float f = tc::ex2(p[M::COLS * D + x] - base_of(mm));
