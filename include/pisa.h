@@ -455,7 +455,7 @@ int pisa_doc_attn_bwd(const pisa_doc_shape_t* shape, const void* Q, const void* 
  *              stands for code * scale * amp.
  * table device [B,max_pages] int32; entries behind a sequence's last page are never read. page a power of two in
  * [16, 1024], max_pages*page <= 2^24, d in {64, 128}, G = Hq / Hkv <= 64, 1 <= nq <= 16,
- * B*nq*Hq < 2^31, B*nq*Hq*max_pages*page < 2^44, B*Hkv < 2^24, n_pages*page*Hkv < 2^39 / d. scale as in pisa_shape_t, cap as in pisa_doc_shape_t. */
+ * B*nq*Hq < 2^31, B*nq*Hq*max_pages*page < 2^44, B*Hkv < 2^24, page*Hkv*d < 2^30, n_pages*page*Hkv < 2^39 / d. scale as in pisa_shape_t, cap as in pisa_doc_shape_t. */
 typedef struct {
   int32_t B, Hq, Hkv, d, n_pages, page, max_pages, bits, nq;
   float scale, cap;

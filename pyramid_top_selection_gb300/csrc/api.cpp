@@ -348,6 +348,7 @@ int paged_dims(const pisa_paged_shape_t* s, pisa::PagedDims* o) {
   if (s->nq < 1 || s->nq > 16) return fail(PISA_EUNSUPPORTED, "nq=%d (supported: 1..16)", s->nq);
   if (static_cast<int64_t>(s->B) * s->Hkv >= (1 << 24)) return fail(PISA_EUNSUPPORTED, "B*Hkv=%lld exceeds 2^24", static_cast<long long>(s->B) * s->Hkv);
   if (static_cast<int64_t>(s->B) * s->Hq >= (int64_t(1) << 31) / s->nq) return fail(PISA_EUNSUPPORTED, "B*nq*Hq exceeds 2^31");
+  if (static_cast<int64_t>(s->page) * s->Hkv * s->d >= (1 << 30)) return fail(PISA_EUNSUPPORTED, "page*Hkv*d=%lld exceeds 2^30", static_cast<long long>(s->page) * s->Hkv * s->d);
   if (static_cast<int64_t>(s->B) * s->Hq * s->nq >= (int64_t(1) << 44) / (static_cast<int64_t>(s->max_pages) * s->page))
     return fail(PISA_EUNSUPPORTED, "B*nq*Hq*max_pages*page exceeds 2^44");
   if (static_cast<int64_t>(s->n_pages) * s->page >= (int64_t(1) << 39) / s->d / s->Hkv)

@@ -227,27 +227,30 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
     // 16-byte pieces of 16 tokens: a lane's are those at lane + 32 x; rows of a piece's run of 32 lanes
     constexpr int P = M::ROW / 16, NP = P / 2, RPX = 32 / P;
     const int lane_from = lane * 16, lane_to = piece(lane / P, lane % P);
+    // a KV head's page in bytes of the cache, the pages' distance, the place of 16 tokens in their page
+    const uint32_t head_bytes = static_cast<uint32_t>(s.page) * M::ROW, page_bytes = head_bytes * s.Hkv;
+    int slot_f = 0;                                                // the stage that is filled next
     auto fetch = [&]() {
       if (fetched < mine) {
-        const int stage = fetched % M::ST, v0 = fet.c * CH, kv = fet.u / a.sets;
-        if (fet.b != ids_b || v0 < ids_base || v0 >= ids_base + 512) {
+        const int v0 = fet.c * CH;
+        if (fet.b != ids_b || static_cast<uint32_t>(v0 - ids_base) >= 512u) {
           ids_b = fet.b;
           ids_base = v0 & ~511;
           const int tok = ids_base + 16 * lane, len = a.len[fet.b];
           ids = tok < fet.n ? __ldg(a.table + static_cast<int64_t>(fet.b) * s.max_pages + (tok >> s.log_page)) : 0;
           if (len < 0 || len > list.most) s_flag = 1;
         }
-        const uint32_t at = ring_at + stage * M::STAGE;
+        const uint32_t at = ring_at + slot_f * M::STAGE, head = (fet.u / a.sets) * head_bytes + lane_from;
         int bad = 0;
 #pragma unroll
         for (int k = 0; k < SUB; ++k) {
           const int tok = v0 + 16 * k, left = fet.n - tok;
-          const int page = __shfl_sync(0xffffffffu, ids, (tok - ids_base) >> 4);
-          const bool ok = left > 0 && static_cast<uint32_t>(page) < static_cast<uint32_t>(s.n_pages);
-          bad |= (left > 0 && !ok) << k;
-          const int64_t row = (static_cast<int64_t>(ok ? page : 0) * s.Hkv + kv) * s.page + (tok & (s.page - 1));
-          const unsigned char* kp = a.c.k + row * M::ROW + lane_from;
-          const unsigned char* vp = a.c.v + row * M::ROW + lane_from;
+          const int page = __shfl_sync(0xffffffffu, ids, (tok >> 4) & 31);
+          const bool known = static_cast<uint32_t>(page) < static_cast<uint32_t>(s.n_pages), ok = left > 0 && known;
+          if (left > 0 && !known) bad |= 1 << k;
+          const int64_t off = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_bytes) + head + (tok & (s.page - 1)) * M::ROW;
+          const unsigned char* kp = a.c.k + off;
+          const unsigned char* vp = a.c.v + off;
           const uint32_t to = at + k * 16 * M::ROW + lane_to;
           if constexpr (FOUR) {
             // slots behind the end come along: whatever they hold, their scores are hidden and their scales set to 0
@@ -259,11 +262,11 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
                 tc::cp_async16(to + x * 512, kp + x * 512, true);
                 tc::cp_async16(to + x * 512 + M::HALF, vp + x * 512, true);
               }
-              constexpr int SN = M::SROW;                          // 16-byte pieces of 16 tokens' scales
+              constexpr int SN = M::SROW;                          // 16-byte pieces of 16 tokens' scales; a token has an eighth of its codes' bytes
               if (lane < 2 * SN) {
                 const int c = lane % SN;
                 tc::cp_async16(at + (lane >= SN ? M::HALF : 0) + CH * M::ROW + k * 16 * M::SROW + 16 * c,
-                               (lane >= SN ? a.c.vs : a.c.ks) + row * M::SROW + 16 * c, true);
+                               (lane >= SN ? a.c.vs : a.c.ks) + ((off - lane_from) >> 3) + 16 * c, true);
               }
             }
           } else {
@@ -278,10 +281,11 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
           }
         }
         if (lane == 0) {
-          s_bad[warp][stage] = bad;
+          s_bad[warp][slot_f] = bad;
           if (bad) s_flag = 1;
         }
         ++fetched;
+        slot_f = slot_f + 1 == M::ST ? 0 : slot_f + 1;
         fet.next(list);
       }
       tc::cp_async_commit();
@@ -425,208 +429,216 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
 
     const float cap2 = s.cap * kLog2e;
     const int tok_g = FOUR ? (D == 128 ? g ^ ((g >> 1) & 1) : g ^ ((g >> 2) & 1)) : g;   // the token of S's row g
-    for (int i = 0; i < mine; ++i) {
-      if (i == 0 || con.c == 0) open();
-      tc::cp_async_wait<M::ST - 2>();
-      __syncwarp();
-      const int stage = i % M::ST, v0 = con.c * CH, bad = s_bad[warp][stage];
-      const uint32_t at = ring_at + stage * M::STAGE;
-      const unsigned char* st = ring + stage * M::STAGE;
-      float x[NT][SUB][4];
+    int stage = 0;
+    for (int done = 0; done < mine;) {         // the run's chunks of one unit
+      open();
+      const int count = min(con.chunks - con.c, mine - done);
+      int v0 = con.c * CH;
+      for (int i = 0; i < count; ++i, v0 += CH) {
+        tc::cp_async_wait<M::ST - 2>();
+        __syncwarp();
+        const int bad = s_bad[warp][stage];
+        const uint32_t at = ring_at + stage * M::STAGE;
+        const unsigned char* st = ring + stage * M::STAGE;
+        float x[NT][SUB][4];
 #pragma unroll
-      for (int k = 0; k < SUB; ++k) {
-        float sc[NT][2][4] = {};
-        if constexpr (FOUR) {
-          uint32_t w0[D / 32], w1[D / 32], s2[2];                  // the lane's codes of tokens tok_g and tok_g + 8
-          const int r0 = 16 * k + tok_g, r1 = r0 + 8;
-          if constexpr (D == 128) {
-            const uint4 u0 = *reinterpret_cast<const uint4*>(st + piece(r0, p2)), u1 = *reinterpret_cast<const uint4*>(st + piece(r1, p2));
-            w0[0] = u0.x, w0[1] = u0.y, w0[2] = u0.z, w0[3] = u0.w;
-            w1[0] = u1.x, w1[1] = u1.y, w1[2] = u1.z, w1[3] = u1.w;
-            s2[0] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r0 * M::SROW + 2 * p2));
-            s2[1] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r1 * M::SROW + 2 * p2));
+        for (int k = 0; k < SUB; ++k) {
+          float sc[NT][2][4] = {};
+          if constexpr (FOUR) {
+            uint32_t w0[D / 32], w1[D / 32], s2[2];                  // the lane's codes of tokens tok_g and tok_g + 8
+            const int r0 = 16 * k + tok_g, r1 = r0 + 8;
+            if constexpr (D == 128) {
+              const uint4 u0 = *reinterpret_cast<const uint4*>(st + piece(r0, p2)), u1 = *reinterpret_cast<const uint4*>(st + piece(r1, p2));
+              w0[0] = u0.x, w0[1] = u0.y, w0[2] = u0.z, w0[3] = u0.w;
+              w1[0] = u1.x, w1[1] = u1.y, w1[2] = u1.z, w1[3] = u1.w;
+              s2[0] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r0 * M::SROW + 2 * p2));
+              s2[1] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r1 * M::SROW + 2 * p2));
+            } else {
+              const uint2 u0 = *reinterpret_cast<const uint2*>(st + r0 * M::ROW + 8 * p2), u1 = *reinterpret_cast<const uint2*>(st + r1 * M::ROW + 8 * p2);
+              w0[0] = u0.x, w0[1] = u0.y;
+              w1[0] = u1.x, w1[1] = u1.y;
+              s2[0] = scales_of(st[CH * M::ROW + r0 * M::SROW + p2]);
+              s2[1] = scales_of(st[CH * M::ROW + r1 * M::SROW + p2]);
+            }
+#pragma unroll
+            for (int wd = 0; wd < D / 32; ++wd) {
+              uint32_t h0[4], h1[4];
+              paged::from_e2m1x8(w0[wd], h0);
+              paged::from_e2m1x8(w1[wd], h1);
+              const uint32_t sel = wd & 2 ? 0x3232u : 0x1010u;       // a group is two words
+              const uint32_t f0 = __byte_perm(s2[0], 0, sel), f1 = __byte_perm(s2[1], 0, sel);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t kf[4] = {mul_h2(h0[2 * y], f0), mul_h2(h1[2 * y], f1), mul_h2(h0[2 * y + 1], f0), mul_h2(h1[2 * y + 1], f1)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_f16(sc[t][y], kf, qf[t][2 * wd + y][0], qf[t][2 * wd + y][1]);
+              }
+            }
           } else {
-            const uint2 u0 = *reinterpret_cast<const uint2*>(st + r0 * M::ROW + 8 * p2), u1 = *reinterpret_cast<const uint2*>(st + r1 * M::ROW + 8 * p2);
-            w0[0] = u0.x, w0[1] = u0.y;
-            w1[0] = u1.x, w1[1] = u1.y;
-            s2[0] = scales_of(st[CH * M::ROW + r0 * M::SROW + p2]);
-            s2[1] = scales_of(st[CH * M::ROW + r1 * M::SROW + p2]);
-          }
 #pragma unroll
-          for (int wd = 0; wd < D / 32; ++wd) {
-            uint32_t h0[4], h1[4];
-            paged::from_e2m1x8(w0[wd], h0);
-            paged::from_e2m1x8(w1[wd], h1);
-            const uint32_t sel = wd & 2 ? 0x3232u : 0x1010u;       // a group is two words
-            const uint32_t f0 = __byte_perm(s2[0], 0, sel), f1 = __byte_perm(s2[1], 0, sel);
+            for (int y = 0; y < KS; ++y) {
+              uint32_t kf[4];
+              ldsm4(kf, at + piece(lane & 15, 2 * y + (lane >> 4)));
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t kf[4] = {mul_h2(h0[2 * y], f0), mul_h2(h1[2 * y], f1), mul_h2(h0[2 * y + 1], f0), mul_h2(h1[2 * y + 1], f1)};
-#pragma unroll
-              for (int t = 0; t < NT; ++t) mma_f16(sc[t][y], kf, qf[t][2 * wd + y][0], qf[t][2 * wd + y][1]);
+              for (int t = 0; t < NT; ++t) mma_bf16(sc[t][y & 1], kf, qf[t][y][0], qf[t][y][1]);
             }
           }
-        } else {
 #pragma unroll
-          for (int y = 0; y < KS; ++y) {
-            uint32_t kf[4];
-            ldsm4(kf, at + piece(lane & 15, 2 * y + (lane >> 4)));
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_bf16(sc[t][y & 1], kf, qf[t][y][0], qf[t][y][1]);
-          }
+            for (int e = 0; e < 4; ++e) x[t][k][e] = sc[t][0][e] + sc[t][1][e];
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[t][k][e] = sc[t][0][e] + sc[t][1][e];
-      }
-      // scores in powers of two; what is not seen
-      const bool full = bad == 0 && v0 + CH <= con.n - s.nq + 1;   // every row sees the whole chunk
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int k = 0; k < SUB; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[t][k][e] *= c1[t][e & 1];
-      if (s.cap > 0.f) {
+        // scores in powers of two; what is not seen
+        const bool full = bad == 0 && v0 + CH <= con.n - s.nq + 1;   // every row sees the whole chunk
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < SUB; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][k][e] = cap2 * tanh_of(x[t][k][e]);
-      }
-      if (a.slopes) {
+            for (int e = 0; e < 4; ++e) x[t][k][e] *= c1[t][e & 1];
+        if (s.cap > 0.f) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int k = 0; k < SUB; ++k)
+            for (int k = 0; k < SUB; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[t][k][e] -= slope[t][e & 1] * static_cast<float>(pos[t][e & 1] - (v0 + 16 * k + tok_g + 8 * (e >> 1)));
-      }
-      if (!full) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < SUB; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (v0 + 16 * k + tok_g + 8 * (e >> 1) > pos[t][e & 1] || (bad >> k) & 1) x[t][k][e] = neg_inf();
-      }
-      float top[NT][2];
-      bool grow = false;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(x[t][0][e], x[t][0][e + 2]);
-#pragma unroll
-          for (int k = 1; k < SUB; ++k) v = fmaxf(v, fmaxf(x[t][k][e], x[t][k][e + 2]));
-#pragma unroll
-          for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-          top[t][e] = v;
-          grow |= v > m[t][e] + kSlack;
+              for (int e = 0; e < 4; ++e) x[t][k][e] = cap2 * tanh_of(x[t][k][e]);
         }
-      if (__any_sync(0xffffffffu, grow)) {
+        if (a.slopes) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float f[2];
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < SUB; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[t][k][e] -= slope[t][e & 1] * static_cast<float>(pos[t][e & 1] - (v0 + 16 * k + tok_g + 8 * (e >> 1)));
+        }
+        if (!full) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < SUB; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (v0 + 16 * k + tok_g + 8 * (e >> 1) > pos[t][e & 1] || (bad >> k) & 1) x[t][k][e] = neg_inf();
+        }
+        // the running maximum follows only when a lane's scores outgrow it: then, and no sooner, by the chunk's maximum
+        float top[NT][2];
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m[t][e], top[t][e]);
-            f[e] = tc::ex2(m[t][e] - base_of(mn));
-            m[t][e] = mn;
-            l[t][e] *= f[e];
+            float v = fmaxf(x[t][0][e], x[t][0][e + 2]);
+#pragma unroll
+            for (int k = 1; k < SUB; ++k) v = tc::max3(v, x[t][k][e], x[t][k][e + 2]);
+            top[t][e] = v;
+            grow |= v > m[t][e] + kSlack;
           }
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            o[t][k][0] *= f[0];
-            o[t][k][1] *= f[1];
-            o[t][k][2] *= f[0];
-            o[t][k][3] *= f[1];
-          }
-        }
-      }
+          for (int t = 0; t < NT; ++t) {
+            float f[2];
 #pragma unroll
-      for (int k = 0; k < SUB; ++k) {
-        uint32_t pb[NT][2];                                        // P^T: tokens x rows
+            for (int e = 0; e < 2; ++e) {
+              float v = top[t][e];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+              for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+              const float mn = fmaxf(m[t][e], v);
+              f[e] = tc::ex2(m[t][e] - base_of(mn));
+              m[t][e] = mn;
+              l[t][e] *= f[e];
+            }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[t][k][e] = tc::ex2(x[t][k][e] - (base_of(m[t][e & 1]) - kLift));
-          l[t][0] += x[t][k][0] + x[t][k][2];
-          l[t][1] += x[t][k][1] + x[t][k][3];
-          if (FOUR) {
-            pb[t][0] = transpose8(pack_f16(x[t][k][0], x[t][k][1]));
-            pb[t][1] = transpose8(pack_f16(x[t][k][2], x[t][k][3]));
-          } else {
-            pb[t][0] = transpose8(pack_bf16(x[t][k][0], x[t][k][1]));
-            pb[t][1] = transpose8(pack_bf16(x[t][k][2], x[t][k][3]));
+            for (int k = 0; k < KS; ++k) {
+              o[t][k][0] *= f[0];
+              o[t][k][1] *= f[1];
+              o[t][k][2] *= f[0];
+              o[t][k][3] *= f[1];
+            }
           }
         }
-        if constexpr (FOUR) {
-          // tokens of the contraction's slots 2 p2, 2 p2 + 1 (pair 0) and those + 8 (pair 1)
-          auto tok = [&](int slot) { return 16 * k + (D == 128 ? slot ^ ((slot >> 1) & 1) : slot ^ ((slot >> 2) & 1)); };
-          const int ra = tok(2 * p2), rb = tok(2 * p2 + 1);
-          const unsigned char* vt = st + M::HALF;
-          uint32_t va[2][D / 64], vb[2][D / 64], f[2];             // the lane's codes, D / 8 channels from D / 8 g on
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int a8 = ra + 8 * h, b8 = rb + 8 * h;
-            if constexpr (D == 128) {
-              const uint2 ua = *reinterpret_cast<const uint2*>(vt + piece(a8, g >> 1) + 8 * (g & 1)),
-                          ub = *reinterpret_cast<const uint2*>(vt + piece(b8, g >> 1) + 8 * (g & 1));
-              va[h][0] = ua.x, va[h][1] = ua.y;
-              vb[h][0] = ub.x, vb[h][1] = ub.y;
+        for (int k = 0; k < SUB; ++k) {
+          uint32_t pb[NT][2];                                        // P^T: tokens x rows
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][k][e] = tc::ex2(x[t][k][e] - (base_of(m[t][e & 1]) - kLift));
+            l[t][0] += x[t][k][0] + x[t][k][2];
+            l[t][1] += x[t][k][1] + x[t][k][3];
+            if (FOUR) {
+              pb[t][0] = transpose8(pack_f16(x[t][k][0], x[t][k][1]));
+              pb[t][1] = transpose8(pack_f16(x[t][k][2], x[t][k][3]));
             } else {
-              va[h][0] = *reinterpret_cast<const uint32_t*>(vt + a8 * M::ROW + 4 * g);
-              vb[h][0] = *reinterpret_cast<const uint32_t*>(vt + b8 * M::ROW + 4 * g);
+              pb[t][0] = transpose8(pack_bf16(x[t][k][0], x[t][k][1]));
+              pb[t][1] = transpose8(pack_bf16(x[t][k][2], x[t][k][3]));
             }
-            const int grp = D == 128 ? g : g >> 1;
-            uint32_t sa = vt[CH * M::ROW + a8 * M::SROW + grp], sb = vt[CH * M::ROW + b8 * M::SROW + grp];
-            if (!full) {                                           // what is behind the end, or was not copied
-              if (v0 + a8 >= con.n || (bad >> k) & 1) sa = 0;
-              if (v0 + b8 >= con.n || (bad >> k) & 1) sb = 0;
-            }
-            f[h] = scales_of(sa | sb << 8);
           }
-#pragma unroll
-          for (int wd = 0; wd < D / 64; ++wd) {
-            uint32_t lo[2][4], hi[2][4];                           // even and odd channels, both tokens of a pair
+          if constexpr (FOUR) {
+            // tokens of the contraction's slots 2 p2, 2 p2 + 1 (pair 0) and those + 8 (pair 1)
+            auto tok = [&](int slot) { return 16 * k + (D == 128 ? slot ^ ((slot >> 1) & 1) : slot ^ ((slot >> 2) & 1)); };
+            const int ra = tok(2 * p2), rb = tok(2 * p2 + 1);
+            const unsigned char* vt = st + M::HALF;
+            uint32_t va[2][D / 64], vb[2][D / 64], f[2];             // the lane's codes, D / 8 channels from D / 8 g on
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t ua = va[h][wd], ub = vb[h][wd];
-              constexpr uint32_t kLow = 0x0f0f0f0fu;
-              paged::from_e2m1x8((ua & kLow) | ((ub << 4) & ~kLow), lo[h]);
-              paged::from_e2m1x8(((ua >> 4) & kLow) | (ub & ~kLow), hi[h]);
+              const int a8 = ra + 8 * h, b8 = rb + 8 * h;
+              if constexpr (D == 128) {
+                const uint2 ua = *reinterpret_cast<const uint2*>(vt + piece(a8, g >> 1) + 8 * (g & 1)),
+                            ub = *reinterpret_cast<const uint2*>(vt + piece(b8, g >> 1) + 8 * (g & 1));
+                va[h][0] = ua.x, va[h][1] = ua.y;
+                vb[h][0] = ub.x, vb[h][1] = ub.y;
+              } else {
+                va[h][0] = *reinterpret_cast<const uint32_t*>(vt + a8 * M::ROW + 4 * g);
+                vb[h][0] = *reinterpret_cast<const uint32_t*>(vt + b8 * M::ROW + 4 * g);
+              }
+              const int grp = D == 128 ? g : g >> 1;
+              uint32_t sa = vt[CH * M::ROW + a8 * M::SROW + grp], sb = vt[CH * M::ROW + b8 * M::SROW + grp];
+              if (!full) {                                           // what is behind the end, or was not copied
+                if (v0 + a8 >= con.n || (bad >> k) & 1) sa = 0;
+                if (v0 + b8 >= con.n || (bad >> k) & 1) sb = 0;
+              }
+              f[h] = scales_of(sa | sb << 8);
             }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t vf[4] = {mul_h2(lo[0][y], f[0]), mul_h2(hi[0][y], f[0]), mul_h2(lo[1][y], f[1]), mul_h2(hi[1][y], f[1])};
+            for (int wd = 0; wd < D / 64; ++wd) {
+              uint32_t lo[2][4], hi[2][4];                           // even and odd channels, both tokens of a pair
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * wd + y], vf, pb[t][0], pb[t][1]);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t ua = va[h][wd], ub = vb[h][wd];
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                paged::from_e2m1x8((ua & kLow) | ((ub << 4) & ~kLow), lo[h]);
+                paged::from_e2m1x8(((ua >> 4) & kLow) | (ub & ~kLow), hi[h]);
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const uint32_t vf[4] = {mul_h2(lo[0][y], f[0]), mul_h2(hi[0][y], f[0]), mul_h2(lo[1][y], f[1]), mul_h2(hi[1][y], f[1])};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * wd + y], vf, pb[t][0], pb[t][1]);
+              }
             }
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int y = 0; y < KS; ++y) {
-            uint32_t vf[4];
-            ldsm4_trans(vf, at + M::HALF + piece((lane & 7) + ((lane >> 4) << 3), 2 * y + ((lane >> 3) & 1)));
+            for (int y = 0; y < KS; ++y) {
+              uint32_t vf[4];
+              ldsm4_trans(vf, at + M::HALF + piece((lane & 7) + ((lane >> 4) << 3), 2 * y + ((lane >> 3) & 1)));
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma_bf16(o[t][y], vf, pb[t][0], pb[t][1]);
+              for (int t = 0; t < NT; ++t) mma_bf16(o[t][y], vf, pb[t][0], pb[t][1]);
+            }
           }
         }
+        __syncwarp();                                                // every lane has read the stage that fetch() refills next
+        fetch();
+        stage = stage + 1 == M::ST ? 0 : stage + 1;
       }
-      __syncwarp();                                                // every lane has read the stage that fetch() refills next
-      fetch();
+      const bool first = warp == 0 && done == 0;                   // the part has the CTA's first chunk
+      done += count;
+      con.c += count - 1;
       const bool tail = con.c + 1 == con.chunks;
-      if (tail || i + 1 == mine) {
-        const bool first = warp == 0 && i - (con.c - begun) == 0;  // the part has the run's first chunk, and the run is the CTA's first
-        close(tail);
-        __syncwarp();
-        if (lane == 0 && first && !(begun == 0 && tail)) s_part[warp][begun == 0].first = 1;
-      }
+      close(tail);
+      __syncwarp();
+      if (lane == 0 && first && !(begun == 0 && tail)) s_part[warp][begun == 0].first = 1;
       con.next(list);
     }
     tc::cp_async_wait<0>();
@@ -713,32 +725,49 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
   win::launch_dependents();
 }
 
-// Units that cross CTAs: block (c, x) joins row x of the unit that crosses into CTA c + 1, if c + 1 is the first CTA that it crosses
-// into. Also the status word, from the CTAs' flags.
-template <int D, bool FOUR, int NT>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int ctas) {
+// Units that cross CTAs: a block joins one row (blockIdx.y) of one of them. Block x of BY_UNIT takes unit x of all; else, where
+// there are more units than CTAs, the unit that crosses into CTA x + 1, if that is the first CTA that it crosses into. Also
+// the status word, from the CTAs' flags.
+template <int D, bool FOUR, int NT, int THREADS, bool BY_UNIT>
+__global__ void __launch_bounds__(THREADS) paged_join_kernel(const PagedArgs a, int ctas) {
   using M = Plan<D, FOUR, NT>;
-  constexpr int LPR = D / 4, GR = 128 / LPR;                       // lanes of a row, parts at a time
+  constexpr int LPR = D / 4, GR = THREADS / LPR;                   // lanes of a row, parts at a time
   constexpr float kLift = FOUR ? 7.f : 0.f;
   __shared__ float s_m[GR], s_l[GR];
   __shared__ float4 s_o[GR][LPR];
   const PagedDims& s = a.s;
   const List<M::CH> list(a);
   const Runs runs(list.total(), ctas * kWarps);
-  const int c = static_cast<int>(blockIdx.x) + 1, x = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t t = runs.begin(c * kWarps);
-  int b = 0;
+  const int x = blockIdx.y, lane = threadIdx.x & 31;
+  int b = 0, u = 0, c = 0, last = 0;                               // the unit, and the first and last of its CTAs
   int64_t begin = 0;
-  bool mine = c < ctas && t < runs.total;
-  int u = 0, last = c;
-  if (mine) {
-    list.find(t, b, begin);
-    const int chunks = list.chunks(list.tokens(b));
-    u = static_cast<int>((t - begin) / chunks);
-    begin += static_cast<int64_t>(u) * chunks;
-    mine = t > begin && runs.begin((c - 1) * kWarps) <= begin && x < min(M::COLS, a.rows - u % a.sets * M::COLS);
-    last = runs.of(begin + chunks - 1) / kWarps;
+  bool mine = true;
+  if (BY_UNIT) {
+    b = static_cast<int>(blockIdx.x) / a.units;
+    u = static_cast<int>(blockIdx.x) % a.units;
+    for (int k = lane; k < b; k += 32) begin += list.chunks(list.tokens(k));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) begin += __shfl_xor_sync(0xffffffffu, begin, o);
+    begin *= a.units;
+  } else {
+    c = static_cast<int>(blockIdx.x);
+    const int64_t t = runs.begin((c + 1) * kWarps);
+    mine = t < runs.total;
+    if (mine) {
+      list.find(t, b, begin);
+      u = static_cast<int>((t - begin) / list.chunks(list.tokens(b)));
+    }
   }
+  if (mine) {
+    const int chunks = list.chunks(list.tokens(b));
+    begin += static_cast<int64_t>(u) * chunks;
+    const int first = runs.of(begin) / kWarps;
+    last = runs.of(begin + chunks - 1) / kWarps;
+    mine = first < last && (BY_UNIT || first == c) && x < min(M::COLS, a.rows - u % a.sets * M::COLS);
+    c = first;
+  }
+  // only the first of its CTAs can have begun before the unit
+  const int late = mine && runs.begin(c * kWarps) < begin ? c : -1;
   win::grid_wait();
   if (blockIdx.x == 0 && x == 0 && threadIdx.x < 32) {
     int any = 0;
@@ -748,23 +777,39 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a, int 
   }
   if (!mine) return;
   const int gr = threadIdx.x / LPR, e = threadIdx.x % LPR;
-  // only the first of its CTAs can have begun before the unit
-  const int late = mine && runs.begin((c - 1) * kWarps) < begin ? c - 1 : -1;
   auto part = [&](int k) { return a.part + (2 * static_cast<int64_t>(k) + (k == late)) * M::PARTF; };
+  // eight parts at a time, against their maximum so far
   float mm = neg_inf(), ll = 0.f;
   float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int k = c - 1 + gr; k <= last; k += GR) mm = fmaxf(mm, part(k)[M::COLS * D + x]);
-#pragma unroll 8
-  for (int k = c - 1 + gr; k <= last; k += GR) {
-    const float* p = part(k);
-    const float f = tc::ex2(p[M::COLS * D + x] - base_of(mm));
-    const float4 v = *reinterpret_cast<const float4*>(p + x * D + 4 * e);
-    oo.x += f * v.x;
-    oo.y += f * v.y;
-    oo.z += f * v.z;
-    oo.w += f * v.w;
-    ll += f * p[M::COLS * D + M::COLS + x];
+  for (int k0 = c + gr; k0 <= last; k0 += 8 * GR) {
+    float pm[8], pl[8], top = mm;
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = k0 + k * GR <= last;
+      const float* p = part(in ? k0 + k * GR : c);
+      pm[k] = in ? p[M::COLS * D + x] : neg_inf();
+      pl[k] = p[M::COLS * D + M::COLS + x];
+      v[k] = *reinterpret_cast<const float4*>(p + x * D + 4 * e);
+      top = fmaxf(top, pm[k]);
+    }
+    const float f0 = tc::ex2(mm - base_of(top));
+    mm = top;
+    ll *= f0;
+    oo.x *= f0;
+    oo.y *= f0;
+    oo.z *= f0;
+    oo.w *= f0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = tc::ex2(pm[k] - base_of(top));
+      if (f == 0.f) continue;                                      // also what is no part, whatever was read for it
+      oo.x += f * v[k].x;
+      oo.y += f * v[k].y;
+      oo.z += f * v[k].z;
+      oo.w += f * v[k].w;
+      ll += f * pl[k];
+    }
   }
   s_o[gr][e] = oo;
   if (e == 0) {
@@ -820,16 +865,22 @@ int attn_launch(PagedArgs& a, cudaStream_t st) {
   }
   if (cudaError_t e = cudaGetLastError()) return e;
   ProfScope ps(st, "paged_join");
+  // a unit a block where they are fewer than the CTAs, with more threads where they have many parts each
+  const int64_t units = static_cast<int64_t>(a.s.B) * a.units;
+  const bool by_unit = units < ctas, many = units * 16 < ctas;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1, ctas - 1)), M::COLS);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(by_unit ? units : std::max(1, ctas - 1)), static_cast<unsigned>(std::min(M::COLS, a.rows)));
+  cfg.blockDim = dim3(many ? 512 : 128);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT>, static_cast<const PagedArgs&>(a), ctas);
+  const PagedArgs& ca = a;
+  if (many) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT, 512, true>, ca, ctas);
+  if (by_unit) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT, 128, true>, ca, ctas);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT, 128, false>, ca, ctas);
 }
 
 template <int D, bool FOUR>

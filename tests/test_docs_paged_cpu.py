@@ -45,7 +45,8 @@ def test_document_shapes_are_checked(change, code, text):
     (dict(Hkv=3), EINVAL, "multiple"), (dict(d=32), EUNSUP, "head dim"), (dict(Hq=130), EUNSUP, "GQA group"),
     (dict(bits=8), EUNSUP, "bits"), (dict(page=8), EUNSUP, "page"), (dict(page=48), EUNSUP, "page"), (dict(page=2048), EUNSUP, "page"),
     (dict(max_pages=(1 << 20) + 1), EUNSUP, "2^24"), (dict(nq=0), EUNSUP, "nq"), (dict(nq=17), EUNSUP, "nq"),
-    (dict(B=1 << 23), EUNSUP, "2^24"), (dict(n_pages=(1 << 31) - 1, page=1024), EUNSUP, "2^39"), (dict(cap=2e6), EINVAL, "cap"),
+    (dict(B=1 << 23), EUNSUP, "2^24"), (dict(n_pages=(1 << 31) - 1, page=1024), EUNSUP, "2^39"), (dict(Hq=1 << 16, Hkv=1 << 16, page=1024), EUNSUP, "2^30"),
+    (dict(B=1 << 12, Hq=1 << 10, Hkv=1 << 8, max_pages=1 << 20), EUNSUP, "2^44"), (dict(cap=2e6), EINVAL, "cap"),
     (dict(scale=math.nan), EINVAL, "scale"),
 ])
 def test_paged_shapes_are_checked(change, code, text):
