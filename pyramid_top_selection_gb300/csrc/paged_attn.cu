@@ -19,6 +19,7 @@
 //   which slot of the contraction being free; V's fragments want two tokens of one channel in a register, so the nibbles of
 //   two tokens are interleaved before they are converted.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -91,6 +92,40 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Shared memory by address.
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -155,7 +190,11 @@ struct Runs {
   int n;
   __device__ __forceinline__ Runs(int64_t total_, int most)
       : total(total_), n(static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(most), total_ / kMinChunks)))) {}
-  __device__ __forceinline__ int64_t begin(int w) const { return w >= n ? total : total * w / n; }
+  __device__ __forceinline__ int64_t begin(int w) const {
+    if (w >= n) return total;
+    if (total < (int64_t(1) << 32) / n) return static_cast<uint32_t>(total) * static_cast<uint32_t>(w) / static_cast<uint32_t>(n);
+    return total * w / n;
+  }
   __device__ __forceinline__ int of(int64_t t) const { return static_cast<int>(((t + 1) * n - 1) / total); }   // the run that has place t
 };
 
@@ -181,7 +220,7 @@ struct Part {
 };
 
 template <int D, bool FOUR, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged_attn_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kernel(const PagedArgs a) {
   using M = Plan<D, FOUR, NT>;
   constexpr int CH = M::CH, SUB = CH / 16, KS = D / 16;
   constexpr float kLift = FOUR ? 7.f : 0.f;                        // P is held 2^kLift larger
@@ -214,8 +253,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
       list.find(t0, con.b, begin);
       con.n = list.tokens(con.b);
       con.chunks = list.chunks(con.n);
-      con.u = static_cast<int>((t0 - begin) / con.chunks);
-      con.c = static_cast<int>((t0 - begin) % con.chunks);
+      const int64_t in = t0 - begin;
+      con.u = in < (int64_t(1) << 31) ? static_cast<int>(in) / con.chunks : static_cast<int>(in / con.chunks);
+      con.c = static_cast<int>(in - static_cast<int64_t>(con.u) * con.chunks);
     }
     Place<CH> fet = con;
     int ids = 0, ids_b = -1, ids_base = 0, fetched = 0;            // page of token ids_base + 16 lane of sequence ids_b
@@ -227,9 +267,20 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
     // 16-byte pieces of 16 tokens: a lane's are those at lane + 32 x; rows of a piece's run of 32 lanes
     constexpr int P = M::ROW / 16, NP = P / 2, RPX = 32 / P;
     const int lane_from = lane * 16, lane_to = piece(lane / P, lane % P);
-    // a KV head's page in bytes of the cache, the pages' distance, the place of 16 tokens in their page
+    // a KV head's page in bytes, the pages' distance; where the lane's pieces of page 0 of fet's KV head lie: keys, values and
+    // (4 bits) the scales of keys or values
     const uint32_t head_bytes = static_cast<uint32_t>(s.page) * M::ROW, page_bytes = head_bytes * s.Hkv;
-    int slot_f = 0;                                                // the stage that is filled next
+    const unsigned char *kp0 = nullptr, *vp0 = nullptr, *sp0 = nullptr;
+    const uint32_t lane_scale = CH * M::ROW + (lane >= 16 ? M::HALF : 0) + 16 * (lane & 15);
+    uint32_t at_f = ring_at;                                       // the stage that is filled next, and its flag
+    int* bad_f = s_bad[warp];
+    auto unit_f = [&]() {
+      const int64_t head = static_cast<int64_t>(fet.u / a.sets) * head_bytes;
+      kp0 = a.c.k + head + lane_from;
+      vp0 = a.c.v + head + lane_from;
+      if (FOUR) sp0 = (lane >= 16 ? a.c.vs : a.c.ks) + (head >> 3) + 16 * (lane & 15);   // a token's scales: an eighth of its codes
+    };
+    unit_f();
     auto fetch = [&]() {
       if (fetched < mine) {
         const int v0 = fet.c * CH;
@@ -240,53 +291,66 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
           ids = tok < fet.n ? __ldg(a.table + static_cast<int64_t>(fet.b) * s.max_pages + (tok >> s.log_page)) : 0;
           if (len < 0 || len > list.most) s_flag = 1;
         }
-        const uint32_t at = ring_at + slot_f * M::STAGE, head = (fet.u / a.sets) * head_bytes + lane_from;
         int bad = 0;
-#pragma unroll
-        for (int k = 0; k < SUB; ++k) {
+        // `N` 16-token blocks from block k of the chunk on, which lie in one page
+        auto blocks = [&](auto first, auto number) {
+          constexpr int k = decltype(first)::value, N = decltype(number)::value;
           const int tok = v0 + 16 * k, left = fet.n - tok;
-          const int page = __shfl_sync(0xffffffffu, ids, (tok >> 4) & 31);
-          const bool known = static_cast<uint32_t>(page) < static_cast<uint32_t>(s.n_pages), ok = left > 0 && known;
-          if (left > 0 && !known) bad |= 1 << k;
-          const int64_t off = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(ok ? page : 0)) * page_bytes) + head + (tok & (s.page - 1)) * M::ROW;
-          const unsigned char* kp = a.c.k + off;
-          const unsigned char* vp = a.c.v + off;
-          const uint32_t to = at + k * 16 * M::ROW + lane_to;
+          uint32_t page = __shfl_sync(0xffffffffu, ids, tok >> 4);         // (the lane's number modulo 32)
+          const bool known = page < static_cast<uint32_t>(s.n_pages), ok = left > 0 && known;
+          if (left > 0 && !known) bad |= ((1 << N) - 1) << k;
+          const uint32_t in_page = static_cast<uint32_t>(tok & (s.page - 1)) * M::ROW;
           if constexpr (FOUR) {
             // slots behind the end come along: whatever they hold, their scores are hidden and their scales set to 0
             if (ok) {
+              const unsigned char* kp = kp0 + static_cast<uint64_t>(page) * page_bytes + in_page;
+              const unsigned char* vp = vp0 + static_cast<uint64_t>(page) * page_bytes + in_page;
+              const uint32_t to = at_f + k * 16 * M::ROW + lane_to;
 #pragma unroll
-              for (int x = 0; x < NP; ++x) {
+              for (int x = 0; x < N * NP; ++x) {
                 // (the piece's permutation goes by bit 2 of the row: the same for rows 8 apart)
-                static_assert(NP == 1 || RPX == 8, "a lane's pieces lie 8 rows apart");
+                static_assert(D == 64 || RPX == 8, "a lane's pieces lie 8 rows apart");
                 tc::cp_async16(to + x * 512, kp + x * 512, true);
                 tc::cp_async16(to + x * 512 + M::HALF, vp + x * 512, true);
               }
-              constexpr int SN = M::SROW;                          // 16-byte pieces of 16 tokens' scales; a token has an eighth of its codes' bytes
-              if (lane < 2 * SN) {
-                const int c = lane % SN;
-                tc::cp_async16(at + (lane >= SN ? M::HALF : 0) + CH * M::ROW + k * 16 * M::SROW + 16 * c,
-                               (lane >= SN ? a.c.vs : a.c.ks) + ((off - lane_from) >> 3) + 16 * c, true);
-              }
+              if ((lane & 15) < N * M::SROW)       // lanes 0 .. take the keys' scales, 16 .. the values'
+                tc::cp_async16(at_f + lane_scale + k * 16 * M::SROW, sp0 + static_cast<uint64_t>(page) * (page_bytes >> 3) + (in_page >> 3), true);
             }
           } else {
+            if (!ok) page = 0;
+            const unsigned char* kp = kp0 + static_cast<uint64_t>(page) * page_bytes + in_page;
+            const unsigned char* vp = vp0 + static_cast<uint64_t>(page) * page_bytes + in_page;
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
               const int r = x * RPX + lane / P;
               const bool in = ok && r < left;
-              const uint32_t dst = at + piece(r, lane % P);
+              const uint32_t dst = at_f + piece(r, lane % P);
               tc::cp_async16(dst, kp + x * 512, in);
               tc::cp_async16(dst + M::HALF, vp + x * 512, in);
             }
           }
+        };
+        using C0 = std::integral_constant<int, 0>;
+        using C1 = std::integral_constant<int, 1>;
+        if (SUB == 1) {
+          blocks(C0{}, C1{});
+        } else if (s.page >= CH) {
+          blocks(C0{}, std::integral_constant<int, SUB>{});
+        } else {
+          blocks(C0{}, C1{});
+          blocks(C1{}, C1{});
         }
-        if (lane == 0) {
-          s_bad[warp][slot_f] = bad;
-          if (bad) s_flag = 1;
-        }
+        if (lane == 0) *bad_f = bad;
+        if (bad) s_flag = 1;
         ++fetched;
-        slot_f = slot_f + 1 == M::ST ? 0 : slot_f + 1;
+        at_f += M::STAGE;
+        ++bad_f;
+        if (at_f == ring_at + M::RING) {
+          at_f = ring_at;
+          bad_f = s_bad[warp];
+        }
         fet.next(list);
+        if (fet.c == 0) unit_f();
       }
       tc::cp_async_commit();
     };
@@ -294,7 +358,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
     for (int i = 0; i < M::ST - 1; ++i) fetch();
 
     uint32_t qf[NT][KS][2];                                        // Q^T: rows of the unit as columns
-    float c1[NT][2], slope[NT][2];                                 // of columns 2 p2, 2 p2 + 1: what a product is multiplied by; slope log2 e
+    // of columns 2 p2, 2 p2 + 1: what a product is multiplied by, at once (c1) or in the exponent (cz); slope log2 e
+    float c1[NT][2], cz[NT][2], slope[NT][2];
     int pos[NT][2];
     float m[NT][2], l[NT][2], o[NT][KS][4];
     int begun = 0;                                                 // the part's first chunk
@@ -355,6 +420,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
           const int col = 8 * t + 2 * p2 + e, r = con.u % a.sets * M::COLS + col;
           const bool there = col < rows;
           c1[t][e] = scale * __shfl_sync(0xffffffffu, up, 8 * p2 + 4 * e);
+          cz[t][e] = s.cap > 0.f || a.slopes ? 1.f : c1[t][e];
           slope[t][e] = there && a.slopes ? __ldg(a.slopes + kv * s.G + r % s.G) * kLog2e : 0.f;
           pos[t][e] = there ? con.n - s.nq + r / s.G : -1;
           m[t][e] = neg_inf();
@@ -429,6 +495,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
 
     const float cap2 = s.cap * kLog2e;
     const int tok_g = FOUR ? (D == 128 ? g ^ ((g >> 1) & 1) : g ^ ((g >> 2) & 1)) : g;   // the token of S's row g
+    // 4 bits: a lane's places in a stage, from the tokens' first 8 rows: K's codes of token tok_g, V's of the tokens of slots
+    // 2 p2 and 2 p2 + 1, the scales of both
+    const int tok_a = D == 128 ? 2 * p2 ^ (p2 & 1) : 2 * p2 ^ (p2 >> 1), tok_b = tok_a ^ 1, v_grp = D == 128 ? g : g >> 1;
+    const uint32_t k_codes = D == 128 ? piece(tok_g, p2) : tok_g * M::ROW + 8 * p2,
+                   k_scales = CH * M::ROW + tok_g * M::SROW + (D == 128 ? 2 * p2 : p2),
+                   va_codes = D == 128 ? piece(tok_a, g >> 1) + 8 * (g & 1) : tok_a * M::ROW + 4 * g,
+                   vb_codes = D == 128 ? piece(tok_b, g >> 1) + 8 * (g & 1) : tok_b * M::ROW + 4 * g,
+                   va_scales = CH * M::ROW + tok_a * M::SROW + v_grp, vb_scales = CH * M::ROW + tok_b * M::SROW + v_grp;
     int stage = 0;
     for (int done = 0; done < mine;) {         // the run's chunks of one unit
       open();
@@ -439,42 +513,51 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
         __syncwarp();
         const int bad = s_bad[warp][stage];
         const uint32_t at = ring_at + stage * M::STAGE;
-        const unsigned char* st = ring + stage * M::STAGE;
         float x[NT][SUB][4];
 #pragma unroll
         for (int k = 0; k < SUB; ++k) {
-          float sc[NT][2][4] = {};
+          float sc[NT][2][4];
           if constexpr (FOUR) {
-            uint32_t w0[D / 32], w1[D / 32], s2[2];                  // the lane's codes of tokens tok_g and tok_g + 8
-            const int r0 = 16 * k + tok_g, r1 = r0 + 8;
-            if constexpr (D == 128) {
-              const uint4 u0 = *reinterpret_cast<const uint4*>(st + piece(r0, p2)), u1 = *reinterpret_cast<const uint4*>(st + piece(r1, p2));
-              w0[0] = u0.x, w0[1] = u0.y, w0[2] = u0.z, w0[3] = u0.w;
-              w1[0] = u1.x, w1[1] = u1.y, w1[2] = u1.z, w1[3] = u1.w;
-              s2[0] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r0 * M::SROW + 2 * p2));
-              s2[1] = scales_of(*reinterpret_cast<const uint16_t*>(st + CH * M::ROW + r1 * M::SROW + 2 * p2));
-            } else {
-              const uint2 u0 = *reinterpret_cast<const uint2*>(st + r0 * M::ROW + 8 * p2), u1 = *reinterpret_cast<const uint2*>(st + r1 * M::ROW + 8 * p2);
-              w0[0] = u0.x, w0[1] = u0.y;
-              w1[0] = u1.x, w1[1] = u1.y;
-              s2[0] = scales_of(st[CH * M::ROW + r0 * M::SROW + p2]);
-              s2[1] = scales_of(st[CH * M::ROW + r1 * M::SROW + p2]);
+            // the lane's codes of tokens tok_g (0) and tok_g + 8 (1), and their scales
+            uint32_t wd[2][D / 32], s2[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t row = at + (16 * k + 8 * r) * M::ROW + k_codes, srow = at + (16 * k + 8 * r) * M::SROW + k_scales;
+              if constexpr (D == 128) {
+                const uint4 u = lds128(row);
+                wd[r][0] = u.x, wd[r][1] = u.y, wd[r][2] = u.z, wd[r][3] = u.w;
+                s2[r] = scales_of(lds16(srow));
+              } else {
+                const uint2 u = lds64(row);
+                wd[r][0] = u.x, wd[r][1] = u.y;
+                s2[r] = scales_of(lds8(srow));
+              }
             }
 #pragma unroll
-            for (int wd = 0; wd < D / 32; ++wd) {
-              uint32_t h0[4], h1[4];
-              paged::from_e2m1x8(w0[wd], h0);
-              paged::from_e2m1x8(w1[wd], h1);
-              const uint32_t sel = wd & 2 ? 0x3232u : 0x1010u;       // a group is two words
-              const uint32_t f0 = __byte_perm(s2[0], 0, sel), f1 = __byte_perm(s2[1], 0, sel);
+            for (int grp = 0; grp < D / 64; ++grp) {               // 16 channels: two words of a token's
+              const uint32_t f0 = __byte_perm(s2[0], 0, grp ? 0x3232u : 0x1010u), f1 = __byte_perm(s2[1], 0, grp ? 0x3232u : 0x1010u);
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t kf[4] = {mul_h2(h0[2 * y], f0), mul_h2(h1[2 * y], f1), mul_h2(h0[2 * y + 1], f0), mul_h2(h1[2 * y + 1], f1)};
+              for (int h = 0; h < 2; ++h) {
+                uint32_t h0[4], h1[4];
+                paged::from_e2m1x8(wd[0][2 * grp + h], h0);
+                paged::from_e2m1x8(wd[1][2 * grp + h], h1);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma_f16(sc[t][y], kf, qf[t][2 * wd + y][0], qf[t][2 * wd + y][1]);
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t kf[4] = {mul_h2(h0[2 * y], f0), mul_h2(h1[2 * y], f1), mul_h2(h0[2 * y + 1], f0), mul_h2(h1[2 * y + 1], f1)};
+                  const int step = 2 * (2 * grp + h) + y;
+#pragma unroll
+                  for (int t = 0; t < NT; ++t) {
+                    if (step < 2) mma_f16_first(sc[t][y], kf, qf[t][step][0], qf[t][step][1]);
+                    else mma_f16(sc[t][y], kf, qf[t][step][0], qf[t][step][1]);
+                  }
+                }
               }
             }
           } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[t][0][e] = sc[t][1][e] = 0.f;
 #pragma unroll
             for (int y = 0; y < KS; ++y) {
               uint32_t kf[4];
@@ -490,19 +573,13 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
         }
         // scores in powers of two; what is not seen
         const bool full = bad == 0 && v0 + CH <= con.n - s.nq + 1;   // every row sees the whole chunk
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < SUB; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][k][e] *= c1[t][e & 1];
         if (s.cap > 0.f) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int k = 0; k < SUB; ++k)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[t][k][e] = cap2 * tanh_of(x[t][k][e]);
+              for (int e = 0; e < 4; ++e) x[t][k][e] = cap2 * tanh_of(x[t][k][e] * c1[t][e & 1]);
         }
         if (a.slopes) {
 #pragma unroll
@@ -511,7 +588,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
             for (int k = 0; k < SUB; ++k)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                x[t][k][e] -= slope[t][e & 1] * static_cast<float>(pos[t][e & 1] - (v0 + 16 * k + tok_g + 8 * (e >> 1)));
+                x[t][k][e] = x[t][k][e] * (s.cap > 0.f ? 1.f : c1[t][e & 1]) - slope[t][e & 1] * static_cast<float>(pos[t][e & 1] - (v0 + 16 * k + tok_g + 8 * (e >> 1)));
         }
         if (!full) {
 #pragma unroll
@@ -532,8 +609,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
             float v = fmaxf(x[t][0][e], x[t][0][e + 2]);
 #pragma unroll
             for (int k = 1; k < SUB; ++k) v = tc::max3(v, x[t][k][e], x[t][k][e + 2]);
-            top[t][e] = v;
-            grow |= v > m[t][e] + kSlack;
+            top[t][e] = v * cz[t][e];
+            grow |= top[t][e] > m[t][e] + kSlack;
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -564,7 +641,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][k][e] = tc::ex2(x[t][k][e] - (base_of(m[t][e & 1]) - kLift));
+            for (int e = 0; e < 4; ++e) x[t][k][e] = tc::ex2(fmaf(x[t][k][e], cz[t][e & 1], kLift - base_of(m[t][e & 1])));
             l[t][0] += x[t][k][0] + x[t][k][2];
             l[t][1] += x[t][k][1] + x[t][k][3];
             if (FOUR) {
@@ -576,28 +653,23 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : FOUR ? 4 : 3) paged
             }
           }
           if constexpr (FOUR) {
-            // tokens of the contraction's slots 2 p2, 2 p2 + 1 (pair 0) and those + 8 (pair 1)
-            auto tok = [&](int slot) { return 16 * k + (D == 128 ? slot ^ ((slot >> 1) & 1) : slot ^ ((slot >> 2) & 1)); };
-            const int ra = tok(2 * p2), rb = tok(2 * p2 + 1);
-            const unsigned char* vt = st + M::HALF;
-            uint32_t va[2][D / 64], vb[2][D / 64], f[2];             // the lane's codes, D / 8 channels from D / 8 g on
+            // the lane's codes of the tokens of slots 2 p2 (a) and 2 p2 + 1 (b), and of those 8 slots on
+            uint32_t va[2][D / 64], vb[2][D / 64], f[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int a8 = ra + 8 * h, b8 = rb + 8 * h;
+              const uint32_t rows = at + M::HALF + (16 * k + 8 * h) * M::ROW, srows = at + M::HALF + (16 * k + 8 * h) * M::SROW;
               if constexpr (D == 128) {
-                const uint2 ua = *reinterpret_cast<const uint2*>(vt + piece(a8, g >> 1) + 8 * (g & 1)),
-                            ub = *reinterpret_cast<const uint2*>(vt + piece(b8, g >> 1) + 8 * (g & 1));
+                const uint2 ua = lds64(rows + va_codes), ub = lds64(rows + vb_codes);
                 va[h][0] = ua.x, va[h][1] = ua.y;
                 vb[h][0] = ub.x, vb[h][1] = ub.y;
               } else {
-                va[h][0] = *reinterpret_cast<const uint32_t*>(vt + a8 * M::ROW + 4 * g);
-                vb[h][0] = *reinterpret_cast<const uint32_t*>(vt + b8 * M::ROW + 4 * g);
+                va[h][0] = lds32(rows + va_codes);
+                vb[h][0] = lds32(rows + vb_codes);
               }
-              const int grp = D == 128 ? g : g >> 1;
-              uint32_t sa = vt[CH * M::ROW + a8 * M::SROW + grp], sb = vt[CH * M::ROW + b8 * M::SROW + grp];
-              if (!full) {                                           // what is behind the end, or was not copied
-                if (v0 + a8 >= con.n || (bad >> k) & 1) sa = 0;
-                if (v0 + b8 >= con.n || (bad >> k) & 1) sb = 0;
+              uint32_t sa = lds8(srows + va_scales), sb = lds8(srows + vb_scales);
+              if (!full) {                                         // what is behind the end, or was not copied
+                if (v0 + 16 * k + 8 * h + tok_a >= con.n || (bad >> k) & 1) sa = 0;
+                if (v0 + 16 * k + 8 * h + tok_b >= con.n || (bad >> k) & 1) sb = 0;
               }
               f[h] = scales_of(sa | sb << 8);
             }

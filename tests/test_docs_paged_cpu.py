@@ -71,7 +71,7 @@ def test_sizes_that_do_not_fit_32_bits_are_refused():
 # -------------------------------------------------------------------------------------- buffers
 def _overlaps(call, names, sizes, written, may_be=()):
     """Every buffer in `written` laid over every other one, at its first and its last 16 bytes, is refused by name."""
-    far = {n: A + (k << 20) for k, n in enumerate(names)}
+    far = {n: A + (k << 28) for k, n in enumerate(names)}
     for w in written:
         for r in names:
             if r == w:
@@ -104,7 +104,7 @@ def test_overlaps_of_the_documents_calls_are_refused():
 def test_missing_and_misaligned_buffers_of_the_documents_calls_are_refused():
     fwd, call_f, nf, bwd, call_b, nb = _doc_calls()
     for names, call, need in ((fwd, call_f, nf), (bwd, call_b, nb)):
-        far = {n: A + (k << 20) for k, n in enumerate(names)}
+        far = {n: A + (k << 28) for k, n in enumerate(names)}
         for n in names:
             if n not in ("prefix", "slopes"):
                 _said(call(far | {n: None}), EWS if n == "workspace" else EINVAL, f"{n} is NULL")
@@ -152,21 +152,21 @@ def test_missing_and_misaligned_buffers_of_the_paged_calls_are_refused(bits):
     tensors, rest, att, append, attn, _, need = _paged_calls(bits)
     for names, call, may in ((tensors + rest, append, ("q_weight", "k_weight", "seq", "k_amp", "v_amp")),
                              (tensors + att, attn, ("slopes", "lse", "k_amp", "v_amp"))):
-        far = {n: A + (k << 20) for k, n in enumerate(names)}
+        far = {n: A + (k << 28) for k, n in enumerate(names)}
         for n in names:
             if n not in may:
                 text = "both" if n in ("Q", "Qr") else f"{n} is NULL"
                 _said(call(far | {n: None}), EWS if n == "workspace" else EINVAL, text)
             _said(call(far | {n: far[n] + 8}), EINVAL, f"{n} is not 16-byte aligned")
-    far = {n: A + (k << 20) for k, n in enumerate(tensors + att)}
+    far = {n: A + (k << 28) for k, n in enumerate(tensors + att)}
     _said(attn(far, need - 1), EWS, "workspace")
     if bits == 16:
-        _said(attn(far | dict(k_scale=A)), EINVAL, "no scales")
+        _said(attn(far | dict(k_scale=A >> 1)), EINVAL, "no scales")
 
 
 def test_append_checks_its_tokens_against_the_cache():
     tensors, rest, _, append, _, _, _ = _paged_calls(16)
-    far = {n: A + (k << 20) for k, n in enumerate(tensors + rest)}
+    far = {n: A + (k << 28) for k, n in enumerate(tensors + rest)}
     _said(append(far, pisa.make_rope_shape(2, 50, 4, 2, 64, 64)), EINVAL, "the cache")
     _said(append(far, pisa.make_rope_shape(2, 50, 4, 4, 128, 64)), EINVAL, "the cache")
     _said(append(far | dict(seq=None), pisa.make_rope_shape(1, 100, 4, 4, 64, 64)), EINVAL, "without seq")
