@@ -1,0 +1,79 @@
+// Attention over packed documents, backward: sizes and launches of window_bwd.cuh's kernels behind the documents' rows
+// (doc_attn.cu).
+#include <algorithm>
+
+#include "doc_rows.cuh"
+#include "profile.h"
+#include "tmap.h"
+#include "window_bwd.cuh"
+
+namespace pisa {
+
+namespace {
+
+template <int D, int MASK>
+int doc_bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  static win::Ready dq_ready, dkv_ready;
+  if (int e = dq_ready(window_dq_kernel<D, MASK>, DqSmem<D>::bytes)) return e;
+  if (int e = dkv_ready(window_dkv_kernel<D, MASK>, DkvSmem<D>::bytes)) return e;
+  const int dq_ctas = std::min({a.n_items, sm_count(), kDqCtas});
+  cudaError_t e;
+  {
+    ProfScope ps(st, "doc_dq");
+    const win::Behind b(dim3(dq_ctas), kThreads, DqSmem<D>::bytes, st);
+    e = cudaLaunchKernelEx(&b.cfg, window_dq_kernel<D, MASK>, a, m[0], m[1], m[2], m[3], m[2], m[3], m[6]);
+  }
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope ps(st, "doc_dkv");
+    const win::Behind b(dim3(a.n_kt * a.n_bh * a.nck), kThreads, DkvSmem<D>::bytes, st);
+    e = cudaLaunchKernelEx(&b.cfg, window_dkv_kernel<D, MASK>, a, m[0], m[1], m[2], m[3], m[4], m[5], dq_ctas);
+  }
+  if (e != cudaSuccess || a.nck == 1) return e;
+  ProfScope ps(st, "doc_dkv_sum");
+  const win::Behind b(dim3(a.n_kt * a.n_bh, D / 4), 256, 0, st);
+  return cudaLaunchKernelEx(&b.cfg, window_dkv_sum_kernel<D, MASK>, a, 0);
+}
+
+// The window's backward workspace, then the documents' rows with tiles of `tok` tokens.
+size_t rows_at(const DocDims& s) { return (window_bwd_ws(doc_as_window(s)).total + 255) / 256 * 256; }
+int row_tile(const DocDims& s) { return 128 / win::packed_heads(s.G); }
+
+}  // namespace
+
+size_t doc_bwd_ws(const DocDims& s) { return rows_at(s) + doc_rows_bytes(s, row_tile(s)); }
+
+int launch_doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                   const void* dO, const DocMask& m, void* dQ, void* dK, void* dV, char* ws, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  BwdArgs a{};
+  a.s = doc_as_window(s);
+  const WinBwdWs w = window_bwd_ws(a.s);
+  plan(a);
+  a.lse = lse;
+  a.nlse = reinterpret_cast<float*>(ws + w.nlse);
+  a.delta = reinterpret_cast<float*>(ws + w.delta);
+  a.dQ = static_cast<bf16*>(dQ);
+  a.dK = static_cast<bf16*>(dK);
+  a.dV = static_cast<bf16*>(dV);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.gave_up = reinterpret_cast<int32_t*>(ws + w.gave_up);
+  a.wait_ns = wait_limit_ns();
+  a.stall = test_stall();
+  const int64_t hd = static_cast<int64_t>(s.Hq) * s.d, kd = static_cast<int64_t>(s.Hkv) * s.d;
+  CUtensorMap map[7];
+  if (int e = win::token_map(&map[0], Q, 1, s.T, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
+  if (int e = win::token_map(&map[1], dO, 1, s.T, s.Hq, s.d, hd, a.P, a.tok)) return e;
+  if (int e = win::token_map(&map[2], K, 1, s.T, s.Hkv, s.d, s.ks, 1, 128)) return e;
+  if (int e = win::token_map(&map[3], V, 1, s.T, s.Hkv, s.d, s.vs, 1, 128)) return e;
+  if (int e = win::token_map(&map[4], dK, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
+  if (int e = win::token_map(&map[5], dV, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
+  if (int e = win::token_map(&map[6], O, 1, s.T, s.Hq, s.d, hd, a.P, a.tok)) return e;
+  if (int e = launch_doc_rows(s, m, a.tok, ws + rows_at(s), a.status, &a.docs, st)) return e;
+  if (s.cap > 0.f || m.slopes)
+    return s.d == 128 ? doc_bwd_launch<128, win::kScored>(a, map, st) : doc_bwd_launch<64, win::kScored>(a, map, st);
+  return s.d == 128 ? doc_bwd_launch<128, win::kDocs>(a, map, st) : doc_bwd_launch<64, win::kDocs>(a, map, st);
+}
+
+}  // namespace pisa

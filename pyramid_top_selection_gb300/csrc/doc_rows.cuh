@@ -1,0 +1,132 @@
+// The documents' rows on the device: every token's document and the order of the token tiles (masks.cuh), as the forward
+// and backward kernels take them.
+#pragma once
+
+#include "device.cuh"
+#include "internal.h"
+#include "masks.cuh"
+#include "paged.h"
+#include "profile.h"
+
+namespace pisa {
+
+namespace {
+
+constexpr int kRowThreads = 512, kStarts = 4096, kBuckets = 256;
+
+struct DocRowsArgs {
+  int32_t T, n_docs, tile, n_tiles, shift;     // tile: tokens of one; shift: key tiles of a bucket of the order, as a power of two
+  const int32_t *starts, *prefix;
+  int4* bounds;
+  int32_t *order, *status;
+};
+
+// Block 0 sorts the tiles, the others look tokens up. The starts are held in shared memory where they fit.
+__global__ void __launch_bounds__(kRowThreads) doc_rows_kernel(const DocRowsArgs a) {
+  __shared__ int32_t s_starts[kStarts];
+  __shared__ int32_t s_count[kBuckets];
+  win::launch_dependents();
+  const bool held = a.n_docs < kStarts;
+  if (held)
+    for (int k = threadIdx.x; k <= a.n_docs; k += kRowThreads) s_starts[k] = a.starts[k];
+  if (blockIdx.x == 0) {
+    for (int k = threadIdx.x; k < kBuckets; k += kRowThreads) s_count[k] = 0;
+    if (threadIdx.x == 0) *a.status = 0;
+  }
+  __syncthreads();
+  auto start_of = [&](int m) { return held ? s_starts[m] : a.starts[m]; };
+  auto clamped = [&](int v) { return max(0, min(v, a.T)); };
+  auto bounds_of = [&](int t) {
+    int lo = 0, hi = a.n_docs + 1;                     // starts below lo are <= t, those from hi on are > t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (start_of(mid) <= t) lo = mid + 1; else hi = mid;
+    }
+    int4 b;
+    if (lo == 0 || lo > a.n_docs) {
+      b.x = b.y = b.z = clamped(start_of(lo == 0 ? 0 : a.n_docs));
+    } else {
+      b.x = clamped(start_of(lo - 1));
+      b.y = clamped(start_of(lo));
+      b.z = a.prefix ? b.x + max(0, min(a.prefix[lo - 1], b.y - b.x)) : b.x;
+    }
+    b.w = 0;
+    return b;
+  };
+  if (blockIdx.x > 0) {
+    const int t = static_cast<int>((blockIdx.x - 1) * kRowThreads + threadIdx.x);
+    if (t < a.T) a.bounds[t] = bounds_of(t);
+    if (t == a.T) a.bounds[t] = make_int4(clamped(start_of(0)), clamped(start_of(a.n_docs)), 0, 0);
+    return;
+  }
+  auto bucket_of = [&](int k) {                        // key tiles of token tile k
+    const int t1 = min(a.T, (k + 1) * a.tile) - 1;
+    const int4 p = bounds_of(k * a.tile), q = bounds_of(t1);
+    const int last = t1 < q.y ? max(t1, q.z - 1) : q.y - 1;
+    return kBuckets - 1 - min(kBuckets - 1, max(0, (last - p.x + 128) >> 7) >> a.shift);
+  };
+  for (int k = threadIdx.x; k < a.n_tiles; k += kRowThreads) atomicAdd(&s_count[bucket_of(k)], 1);
+  __syncthreads();
+  if (threadIdx.x < 32) {                              // counts to places
+    int before = 0;
+    for (int k = threadIdx.x; k < kBuckets; k += 32) {
+      const int n = s_count[k];
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (static_cast<int>(threadIdx.x) >= o) sum += x;
+      }
+      s_count[k] = before + sum - n;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < a.n_tiles; k += kRowThreads) a.order[atomicAdd(&s_count[bucket_of(k)], 1)] = k;
+}
+
+inline size_t doc_bounds_bytes(const DocDims& s) { return (static_cast<size_t>(s.T + 1) * 16 + 255) / 256 * 256; }
+
+// Bytes of the rows with token tiles of `tile` tokens.
+inline size_t doc_rows_bytes(const DocDims& s, int tile) {
+  return doc_bounds_bytes(s) + static_cast<size_t>((s.T + tile - 1) / tile) * 4;
+}
+
+inline int launch_doc_rows(const DocDims& s, const DocMask& m, int tile, char* ws, int32_t* status, win::DocRows* out,
+                           cudaStream_t st) {
+  DocRowsArgs a{};
+  a.T = s.T;
+  a.n_docs = s.n_docs;
+  a.tile = tile;
+  a.n_tiles = (s.T + tile - 1) / tile;
+  while ((s.max_len / 128 + 3) >> a.shift >= kBuckets) ++a.shift;
+  a.starts = m.starts;
+  a.prefix = m.prefix;
+  a.bounds = reinterpret_cast<int4*>(ws);
+  a.order = reinterpret_cast<int32_t*>(ws + doc_bounds_bytes(s));
+  a.status = status;
+  *out = {a.bounds, a.order, m.slopes, s.cap};
+  ProfScope ps(st, "doc_rows");
+  doc_rows_kernel<<<2 + s.T / kRowThreads, kRowThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+// The documents' shape as the window's kernels take it: one sequence, no sinks, a window of the longest document.
+inline WinDims doc_as_window(const DocDims& s) {
+  WinDims d{};
+  d.B = 1;
+  d.Nq = d.N = s.T;
+  d.Hq = s.Hq;
+  d.Hkv = s.Hkv;
+  d.d = s.d;
+  d.G = s.G;
+  d.window = s.max_len;
+  d.scale = s.scale;
+  d.qs = s.qs;
+  d.ks = s.ks;
+  d.vs = s.vs;
+  return d;
+}
+
+}  // namespace
+}  // namespace pisa

@@ -44,6 +44,23 @@ class Ready {
   std::atomic<uint64_t> done_{0};
 };
 
+// A launch that starts while the kernel before it ends (which it waits for itself, with grid_wait).
+struct Behind {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  Behind(dim3 grid, int threads, int smem, cudaStream_t st) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  Behind(const Behind&) = delete;
+};
+
 }  // namespace win
 
 // Plain-old-data view of a window shape, passed to kernels by value. Strides in elements
