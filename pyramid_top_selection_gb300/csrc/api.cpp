@@ -772,7 +772,8 @@ int pisa_doc_attn_bwd(const pisa_doc_shape_t* shape, const void* Q, const void* 
   const Span out[] = {{"dQ", dQ, d.T, q, q}, {"dK", dK, d.T, kv, kv}, {"dV", dV, d.T, kv, kv},
                       flat("workspace", ws, static_cast<int64_t>(need), 1)};
   PISA_CHECK(check_apart(read, out));
-  return cuda_rc(pisa::launch_doc_bwd(d, Q, K, V, O, lse, dO, {starts, prefix, slopes}, dQ, dK, dV, static_cast<char*>(ws), stream),
+  const auto launch = d.d == 128 ? pisa::launch_doc_bwd_d128 : pisa::launch_doc_bwd_d64;
+  return cuda_rc(launch(d, Q, K, V, O, lse, dO, {starts, prefix, slopes}, dQ, dK, dV, static_cast<char*>(ws), stream),
                  "pisa_doc_attn_bwd");
 }
 

@@ -26,6 +26,13 @@ int doc_fwd_launch(const FwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   return cudaLaunchKernelEx(&b.cfg, window_fwd_kernel<D, false, MASK>, a, m[0], m[1], m[2], m[1], m[2], m[3]);
 }
 
+template <int D>
+int doc_fwd_by_scores(const FwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  constexpr int C = win::kDocs | win::kCap, B = win::kDocs | win::kBias;
+  if (a.docs.cap > 0.f) return a.docs.slopes ? doc_fwd_launch<D, C | B>(a, m, st) : doc_fwd_launch<D, C>(a, m, st);
+  return a.docs.slopes ? doc_fwd_launch<D, B>(a, m, st) : doc_fwd_launch<D, win::kDocs>(a, m, st);
+}
+
 // Tokens of a forward item: two row tiles.
 int fwd_tile(const DocDims& s) { return 2 * 128 / win::packed_heads(s.G); }
 
@@ -56,9 +63,7 @@ int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V
   if (int e = win::token_map(&map[2], V, 1, s.T, s.Hkv, s.d, s.vs, 1, 128)) return e;
   if (int e = win::token_map(&map[3], O, 1, s.T, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
   if (int e = launch_doc_rows(s, m, 2 * a.tok, ws + 256, a.status, &a.docs, st)) return e;
-  if (s.cap > 0.f || m.slopes)
-    return s.d == 128 ? doc_fwd_launch<128, win::kScored>(a, map, st) : doc_fwd_launch<64, win::kScored>(a, map, st);
-  return s.d == 128 ? doc_fwd_launch<128, win::kDocs>(a, map, st) : doc_fwd_launch<64, win::kDocs>(a, map, st);
+  return s.d == 128 ? doc_fwd_by_scores<128>(a, map, st) : doc_fwd_by_scores<64>(a, map, st);
 }
 
 }  // namespace pisa

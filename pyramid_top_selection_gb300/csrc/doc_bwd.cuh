@@ -1,10 +1,10 @@
-// Attention over packed documents, backward: sizes and launches of window_bwd.cuh's kernels behind the documents' rows
-// (doc_attn.cu).
+// Launches of the documents' backward kernels at one head size (doc_bwd_d64.cu, doc_bwd_d128.cu; a file a size, which compile side by side).
+#pragma once
+
 #include <algorithm>
 
 #include "doc_rows.cuh"
 #include "profile.h"
-#include "tmap.h"
 #include "window_bwd.cuh"
 
 namespace pisa {
@@ -35,17 +35,20 @@ int doc_bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   return cudaLaunchKernelEx(&b.cfg, window_dkv_sum_kernel<D, MASK>, a, 0);
 }
 
+template <int D>
+int doc_bwd_by_scores(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  constexpr int C = win::kDocs | win::kCap, B = win::kDocs | win::kBias;
+  if (a.docs.cap > 0.f) return a.docs.slopes ? doc_bwd_launch<D, C | B>(a, m, st) : doc_bwd_launch<D, C>(a, m, st);
+  return a.docs.slopes ? doc_bwd_launch<D, B>(a, m, st) : doc_bwd_launch<D, win::kDocs>(a, m, st);
+}
+
 // The window's backward workspace, then the documents' rows with tiles of `tok` tokens.
 size_t rows_at(const DocDims& s) { return (window_bwd_ws(doc_as_window(s)).total + 255) / 256 * 256; }
 int row_tile(const DocDims& s) { return 128 / win::packed_heads(s.G); }
 
-}  // namespace
-
-size_t doc_bwd_ws(const DocDims& s) { return rows_at(s) + doc_rows_bytes(s, row_tile(s)); }
-
-int launch_doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse,
-                   const void* dO, const DocMask& m, void* dQ, void* dK, void* dV, char* ws, void* stream) {
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+template <int D>
+int doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse, const void* dO,
+            const DocMask& m, void* dQ, void* dK, void* dV, char* ws, cudaStream_t st) {
   BwdArgs a{};
   a.s = doc_as_window(s);
   const WinBwdWs w = window_bwd_ws(a.s);
@@ -71,9 +74,8 @@ int launch_doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V
   if (int e = win::token_map(&map[5], dV, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
   if (int e = win::token_map(&map[6], O, 1, s.T, s.Hq, s.d, hd, a.P, a.tok)) return e;
   if (int e = launch_doc_rows(s, m, a.tok, ws + rows_at(s), a.status, &a.docs, st)) return e;
-  if (s.cap > 0.f || m.slopes)
-    return s.d == 128 ? doc_bwd_launch<128, win::kScored>(a, map, st) : doc_bwd_launch<64, win::kScored>(a, map, st);
-  return s.d == 128 ? doc_bwd_launch<128, win::kDocs>(a, map, st) : doc_bwd_launch<64, win::kDocs>(a, map, st);
+  return doc_bwd_by_scores<D>(a, map, st);
 }
 
+}  // namespace
 }  // namespace pisa

@@ -9,7 +9,8 @@
 namespace pisa {
 namespace win {
 
-constexpr int kWindow = 0, kDocs = 1, kScored = 2;
+// (flags: kDocs, with capped scores, with scores that lose a slope times the distance)
+constexpr int kWindow = 0, kDocs = 1, kCap = 2, kBias = 4;
 
 // Documents on the device, as the prologue (doc_attn.cu) lays them out.
 struct DocRows {
@@ -54,66 +55,105 @@ struct DocSeen {
   }
 };
 
-// Scores in powers of two of a thread's products x (a row's against columns, or a key's against rows).
-//   y = cap tanh(k x), k = scale / cap: within |k x| <= 1 by a polynomial of (k x)^2 on the FMA units (minimax on [0, 1]:
-//   tanh within 2.5e-7), as a warp that has no larger product takes it; else by tanh_of, three special-function operations.
+// Scores in powers of two from products x, two at a time, before the distance's share:
+//   y = scale log2 e x, or (CAP) cap log2 e tanh(k x), k = scale / cap: within |k x| <= 1 by a polynomial of (k x)^2 on
+//   the FMA units (minimax on [0, 1]: tanh within 2.5e-7), as a warp that has no larger product takes it; else by
+//   tanh_of, three special-function operations, in a loop of its own over tensor memory (cap_far).
 // The polynomial's coefficients are taken times k^2i and scale log2 e, so that y = x p(x^2).
+template <bool CAP>
 struct Scores {
-  float c1, k, cap2;       // scale log2 e, scale / cap, cap log2 e
-  float p[6];
-  __device__ __forceinline__ Scores(float scale, float cap) : c1(scale * kScoreLog2e), k(0.f), cap2(cap * kScoreLog2e) {
-    if (cap > 0.f) {
+  float k, cap2, back2;    // scale / cap, cap log2 e, -1 / (cap log2 e)^2
+  uint64_t p[CAP ? 6 : 1]; // coefficients in pairs (p[0] alone: scale log2 e)
+  uint64_t one;            // what a product is multiplied by where the polynomial does not apply: scale log2 e, or 1 after cap_far
+  bool near;
+  __device__ __forceinline__ Scores(float scale, float cap) : k(0.f), cap2(0.f), back2(0.f), near(false) {
+    const float c1 = scale * kScoreLog2e;
+    one = tc::pack2(c1, c1);
+    p[0] = one;
+    if (CAP) {
+      one = tc::pack2(1.f, 1.f);
       k = scale / cap;
-      const float k2 = k * k;
-      const float c[6] = {0.999996841f, -0.333240032f, 0.132535249f, -0.0509728603f, 0.016114179f, -0.00283946446f};
+      cap2 = cap * kScoreLog2e;
+      back2 = -1.f / (cap2 * cap2);
+      const float k2 = k * k, c[6] = {0.999996841f, -0.333240032f, 0.132535249f, -0.0509728603f, 0.016114179f, -0.00283946446f};
       float f = c1;
 #pragma unroll
-      for (int i = 0; i < 6; ++i, f *= k2) p[i] = c[i] * f;
+      for (int i = 0; i < 6; ++i, f *= k2) p[CAP ? i : 0] = tc::pack2(c[i] * f, c[i] * f);
     }
   }
-  // Whether a warp's products are within the polynomial's range.
+  // Looks at a warp's products: whether all are in the polynomial's range.
   template <int N>
-  __device__ __forceinline__ bool near(const float (&x)[N]) const {
-    float top[4] = {fabsf(x[0]), fabsf(x[1]), fabsf(x[2]), fabsf(x[3])};
+  __device__ __forceinline__ bool look(const float (&x)[N]) {
+    near = false;
+    if (CAP) {
+      float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 4; c < N; c += 4)
+      for (int c = 0; c < N; c += 8)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], fabsf(x[c + q]));
-    return __all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * k <= 1.f);   // (NaN: not)
-  }
-  // Two scores before the distance's share.
-  template <bool NEAR>
-  __device__ __forceinline__ void capped(float& a, float& b) const {
-    if (NEAR) {
-      const uint64_t x = tc::pack2(a, b), y = mul2(x, x);
-      uint64_t r = tc::pack2(p[5], p[5]);
-#pragma unroll
-      for (int i = 4; i >= 0; --i) r = tc::fma2(r, y, tc::pack2(p[i], p[i]));
-      tc::unpack2(mul2(x, r), a, b);
-    } else {
-      a = cap2 * tanh_of(a * k);
-      b = cap2 * tanh_of(b * k);
+        for (int q = 0; q < 4; ++q) asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(top[q]) : "f"(x[c + q]), "f"(x[c + 4 + q]));
+      near = __all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * k <= 1.f);
     }
+    return !CAP || near;
   }
-  // All of a thread's scores before the distance's share.
+  // The factor of a pair of products: y = x factor.
+  __device__ __forceinline__ uint64_t factor(uint64_t x) const {
+    uint64_t r = p[CAP ? 5 : 0];
+    if (CAP) {
+      const uint64_t y = mul2(x, x);
+#pragma unroll
+      for (int i = 4; i >= 0; --i) r = tc::fma2(r, y, p[CAP ? i : 0]);
+    }
+    return r;
+  }
+  // What a gradient takes through the cap, from capped scores: 1 - tanh^2.
+  __device__ __forceinline__ uint64_t back(uint64_t y) const { return tc::fma2(mul2(y, y), tc::pack2(back2, back2), tc::pack2(1.f, 1.f)); }
+  // N columns (a multiple of 32) of the thread's lane in tensor memory: products to capped scores, in place.
   template <int N>
-  __device__ __forceinline__ void cap_all(float (&x)[N]) const {
-    if (cap2 == 0.f) {
+  __device__ __forceinline__ void cap_far(uint32_t taddr) const {
+#pragma unroll 1
+    for (int q = 0; q < N; q += 16) {
+      uint32_t u[16];
+      tmem_ld16(taddr + q, u);
 #pragma unroll
-      for (int c = 0; c < N; ++c) x[c] *= c1;
-    } else if (near(x)) {
-#pragma unroll
-      for (int c = 0; c < N; c += 2) capped<true>(x[c], x[c + 1]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < N; c += 2) capped<false>(x[c], x[c + 1]);
+      for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(cap2 * tanh_of(__uint_as_float(u[c]) * k));
+      tc::tmem_st16(taddr + q, u);
     }
+    tc::tmem_wait_st();
   }
-  // What a gradient takes through the cap, from a capped score: 1 - tanh^2.
-  __device__ __forceinline__ float back(float y, float icap2) const {
-    const float t = y * icap2;
-    return fmaf(-t, t, 1.f);
+};
+
+// 128 consecutive fp32 columns of this thread's TMEM lane, in one load.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
+      "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+      "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,"
+      "%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int k = 0; k < 128; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+// The distance's share of a row's scores against columns 0 .. N - 1 of a tile, powers of two: -slope |d0 - c|, d0 the row's
+// position less the first column's key. Where a row sees no later key, -slope (d0 - c): linear in c, as a term of
+// each 16 columns, which costs nothing where it goes into another sum, and one of 16 that do not change.
+struct Distance {
+  float slope;
+  uint64_t part[8];        // slope c, c = 0 .. 15, in pairs
+  bool ahead;              // some row of the warp sees later keys
+  __device__ __forceinline__ void set(float slope_, bool sees_later) {
+    slope = slope_;
+    ahead = __any_sync(0xffffffffu, sees_later);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) part[c] = tc::pack2(slope * (2 * c), slope * (2 * c + 1));
   }
+  __device__ __forceinline__ float base(float d0, int c16) const { return -slope * (d0 - static_cast<float>(c16)); }
 };
 
 }  // namespace win

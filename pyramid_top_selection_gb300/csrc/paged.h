@@ -37,8 +37,10 @@ struct PagedCache {
 // Launchers: return 0 or a cudaError_t value.
 int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V, const DocMask& m, void* O, float* lse,
                    char* ws, void* stream);
-int launch_doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse,
-                   const void* dO, const DocMask& m, void* dQ, void* dK, void* dV, char* ws, void* stream);
+int launch_doc_bwd_d64(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                       const void* dO, const DocMask& m, void* dQ, void* dK, void* dV, char* ws, void* stream);
+int launch_doc_bwd_d128(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                        const void* dO, const DocMask& m, void* dQ, void* dK, void* dV, char* ws, void* stream);
 int launch_paged_append(const PagedDims& s, const PagedCache& c, const RopeDims& t, const void* Q, const void* K,
                         const void* V, int64_t vs, const float* inv_freq, const float* wq, const float* wk,
                         const int32_t* table, const int32_t* seq, const int32_t* pos, void* Qr, int32_t* status,

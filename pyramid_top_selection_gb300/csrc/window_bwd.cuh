@@ -1,5 +1,5 @@
 // Attention of rows over a run of keys each, backward, on the fifth-generation tensor cores: a sliding window with sinks
-// (window_bwd.cu), or documents (doc_bwd.cu).
+// (window_bwd.cu), or documents (doc_bwd.cuh).
 //
 // P = exp(s q.k - lse), D = dO . O, dS = P (dO . v - D):  dQ = s dS K,  dK = s dS^T Q,  dV = P^T dO.
 // Two kernels, each with its sums in tensor memory and no atomics, so the order of every sum is
@@ -347,8 +347,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c1 = s.scale * kLog2e;
-    const win::Scores scores(s.scale, MASK == win::kScored ? a.docs.cap : 0.f);
-    const float icap2 = MASK == win::kScored && a.docs.cap > 0.f ? 1.f / scores.cap2 : 0.f;
+    constexpr bool CAP = MASK & win::kCap, BIAS = MASK & win::kBias;
+    win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
+    win::Distance dist;
     int n_k = 0, n_q = 0, kk = 0, k_item = 0;
     auto lse_of = [&](const win::Item& x) -> float {
       const int rows = x.n > 0 ? min(128, (min(s.Nq, x.L - s.off) - x.t0) * a.P) : 0;
@@ -375,9 +376,9 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       }
       bool ok = true;
       win::DocSpan span;
-      float slope = 0.f;
       if (MASK != win::kWindow && i < s.Nq) span = win::DocSpan(a.docs, i);
-      if (MASK == win::kScored && a.docs.slopes) slope = __ldg(a.docs.slopes + h) * kLog2e;
+      if (BIAS) dist.set(__ldg(a.docs.slopes + h) * kLog2e, span.hi > p);
+      uint32_t far = 0;                                      // tiles of a short item whose S has been capped in place
       // x = P (through: times what a gradient takes through the cap), y = dP of key tile j; see: the visible columns,
       // where some are not
       auto load = [&](int j, float (&x)[64], float (&y)[64], uint32_t (&see)[2], bool& masked, bool through) -> bool {
@@ -400,13 +401,38 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           for (int q = 0; q < 2; ++q)
             see[q] = win::bit_range(0, hi - 32 * q) & (win::bit_range(lo - 32 * q, 31) | win::bit_range(0, sk - 1 - 32 * q));
         }
-        if constexpr (MASK == win::kScored) {
+        if constexpr (CAP || BIAS) {
+          if (CAP && (far >> j) & 1) {                       // taken a second time (n <= 2): capped already
+            scores.near = false;
+          } else if (!scores.look(x)) {
+            scores.template cap_far<64>(tm + 128 * (k & 1) + 64 * g + lane_off);
+            tc::tmem_ld64(tm + 128 * (k & 1) + 64 * g + lane_off, x);
+            far |= n <= 2 ? 1u << j : 0u;
+          }
           const float d0 = static_cast<float>(p - kb);
-          scores.cap_all(x);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const float f = through ? scores.back(x[c], icap2) : 1.f;
-            x[c] = tc::ex2(fmaf(-slope, fabsf(d0 - static_cast<float>(c)), x[c]) + nl) * f;
+          for (int q = 0; q < 4; ++q) {
+            const float b = nl + (BIAS && !dist.ahead ? dist.base(d0, 16 * q) : 0.f);
+            const uint64_t bb = tc::pack2(b, b);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              float& x0 = x[16 * q + 2 * c];
+              float& x1 = x[16 * q + 2 * c + 1];
+              const uint64_t v = tc::pack2(x0, x1), y = win::mul2(v, !CAP || scores.near ? scores.factor(v) : scores.one);
+              uint64_t z = tc::add2(y, bb);
+              if (BIAS) {
+                if (!dist.ahead) {
+                  z = tc::add2(z, dist.part[c]);
+                } else {
+                  const float e0 = fabsf(d0 - static_cast<float>(16 * q + 2 * c)), e1 = fabsf(d0 - static_cast<float>(16 * q + 2 * c + 1));
+                  z = tc::fma2(tc::pack2(e0, e1), tc::pack2(-dist.slope, -dist.slope), z);
+                }
+              }
+              tc::unpack2(z, x0, x1);
+              x0 = tc::ex2(x0);
+              x1 = tc::ex2(x1);
+              if (CAP && through) tc::unpack2(win::mul2(tc::pack2(x0, x1), scores.back(y)), x0, x1);
+            }
           }
         } else {
           const uint64_t cc = tc::pack2(c1, c1), ll = tc::pack2(nl, nl);
@@ -584,7 +610,7 @@ struct DkvBars {
       dv_done, dk_done, drain, never;
   uint32_t tmem_base;
   int abort;
-  float __align__(16) slope[64];   // the group's heads' slopes times log2 e (kScored)
+  float __align__(16) slope[64];   // the group's heads' slopes times -log2 e (kBias)
 };
 static_assert(sizeof(DkvBars) <= 512, "barrier block");
 
@@ -734,8 +760,8 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
     s_abort = 0;
-    if (MASK == win::kScored)
-      for (int h = 0; h < s.G; ++h) bar.slope[h] = a.docs.slopes ? __ldg(a.docs.slopes + it.kv * s.G + h) * kLog2e : 0.f;
+    if (MASK & win::kBias)
+      for (int h = 0; h < s.G; ++h) bar.slope[h] = -kLog2e * __ldg(a.docs.slopes + it.kv * s.G + h);
     if (n > 0) {
       tc::bar_expect_tx(&kv_full, 2 * M::TILE);
 #pragma unroll
@@ -857,8 +883,8 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       see_first = seen.first;
       see_end = seen.end;
     }
-    const win::Scores scores(s.scale, MASK == win::kScored ? a.docs.cap : 0.f);
-    const float icap2 = MASK == win::kScored && a.docs.cap > 0.f ? 1.f / scores.cap2 : 0.f;
+    constexpr bool CAP = MASK & win::kCap, BIAS = MASK & win::kBias;
+    win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
     bool ok = true;
     for (int k = 0; k < n; ++k) {
       const int sq = k % M::NQ, ss = k & 1, pt0 = s.off + tile_tok(k);
@@ -881,12 +907,21 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const float4* dl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 512 + 256 * g);
       // P as bf16 over S^T's first half
       auto put = [&](int q, const uint32_t (&u)[16]) { tc::tmem_st16(tS + 16 * q, u); };
-      if constexpr (MASK == win::kScored) {
+      if constexpr (CAP || BIAS) {
         // P goes out, and stays here times what a gradient takes through the cap
-        scores.cap_all(x);
-        const float* sl = bar.slope + k % a.sets * a.P;
-        const float4 sl_few = make_float4(sl[0], sl[1 & (a.P - 1)], sl[0], sl[1 & (a.P - 1)]);       // P < 4
-        const float step[4] = {0.f, static_cast<float>(1 >> a.lp), static_cast<float>(2 >> a.lp), static_cast<float>(3 >> a.lp)};
+        if (!scores.look(x)) {
+          scores.template cap_far<64>(tS);
+          tc::tmem_ld64(tS, x);
+        }
+        const float* sl = bar.slope + k % a.sets * a.P;      // column c of the tile: token c / P, head c % P
+        float few[4], step[4];                               // P < 4: four columns' slopes, and their tokens'
+        if (BIAS) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            few[y] = sl[y & (a.P - 1)];
+            step[y] = static_cast<float>(y >> a.lp);
+          }
+        }
         const int d0 = pt0 - key;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -895,18 +930,41 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           for (int c = 0; c < 32; c += 4) {
             float* e = x + 32 * q + c;
             const float4 l4 = nl[8 * q + c / 4];
-            const int col = 64 * g + 32 * q + c;             // of the tile: token col / P, head col % P
-            const float4 s4 = a.P >= 4 ? *reinterpret_cast<const float4*>(sl + (col & (a.P - 1))) : sl_few;
-            const float lse4[4] = {l4.x, l4.y, l4.z, l4.w}, slope4[4] = {s4.x, s4.y, s4.z, s4.w}, d = static_cast<float>(d0 + (col >> a.lp));
-            float P[4];
+            const uint64_t v[2] = {tc::pack2(e[0], e[1]), tc::pack2(e[2], e[3])};
+            uint64_t y[2], z[2];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              P[y] = tc::ex2(fmaf(-slope4[y], fabsf(d + step[y]), e[y]) + lse4[y]);
-              if (masked) P[y] = (see[q] >> (c + y)) & 1 ? P[y] : 0.f;
-              e[y] = P[y] * scores.back(e[y], icap2);
+            for (int w = 0; w < 2; ++w) {
+              y[w] = win::mul2(v[w], !CAP || scores.near ? scores.factor(v[w]) : scores.one);
+              z[w] = tc::add2(y[w], w ? tc::pack2(l4.z, l4.w) : tc::pack2(l4.x, l4.y));
             }
-            u[c / 2] = pack_bf16(P[0], P[1]);
-            u[c / 2 + 1] = pack_bf16(P[2], P[3]);
+            if (BIAS) {
+              const int col = 64 * g + 32 * q + c;
+              const float d = static_cast<float>(d0 + (col >> a.lp));
+              if (a.P >= 4) {
+                const float4 s4 = *reinterpret_cast<const float4*>(sl + (col & (a.P - 1)));
+                const uint64_t dd = tc::pack2(fabsf(d), fabsf(d));
+                z[0] = tc::fma2(tc::pack2(s4.x, s4.y), dd, z[0]);
+                z[1] = tc::fma2(tc::pack2(s4.z, s4.w), dd, z[1]);
+              } else {
+                z[0] = tc::fma2(tc::pack2(few[0], few[1]), tc::pack2(fabsf(d + step[0]), fabsf(d + step[1])), z[0]);
+                z[1] = tc::fma2(tc::pack2(few[2], few[3]), tc::pack2(fabsf(d + step[2]), fabsf(d + step[3])), z[1]);
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              float P0, P1;
+              tc::unpack2(z[w], P0, P1);
+              P0 = tc::ex2(P0);
+              P1 = tc::ex2(P1);
+              if (masked) {
+                P0 = (see[q] >> (c + 2 * w)) & 1 ? P0 : 0.f;
+                P1 = (see[q] >> (c + 2 * w + 1)) & 1 ? P1 : 0.f;
+              }
+              u[c / 2 + w] = pack_bf16(P0, P1);
+              if (CAP) tc::unpack2(win::mul2(tc::pack2(P0, P1), scores.back(y[w])), P0, P1);
+              e[2 * w] = P0;
+              e[2 * w + 1] = P1;
+            }
           }
           put(q, u);
         }

@@ -320,8 +320,10 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tm + 128 * t + lane_off, tO = tm + 256 + D * t + lane_off;
-    const float c1 = MASK == win::kScored ? 1.f : s.scale * kLog2e;    // (scored: powers of two already)
-    const win::Scores scores(s.scale, MASK == win::kScored ? a.docs.cap : 0.f);
+    constexpr bool CAP = MASK & win::kCap, BIAS = MASK & win::kBias;
+    const float c1 = CAP || BIAS ? 1.f : s.scale * kLog2e;   // (scores: powers of two already)
+    win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
+    win::Distance dist;
     int n_s = 0, n_kv = 0;                     // key tiles done by this row tile; stages used by earlier items
     int i = 0;
     for (int n = 0;; ++i, n_kv += 2 * n) {
@@ -336,9 +338,8 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const int p = p0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
       const bool row = p < p1 && p < L;
       win::DocSpan span;
-      float slope = 0.f;
       if (MASK != win::kWindow && p < p1) span = win::DocSpan(a.docs, p);
-      if (MASK == win::kScored && a.docs.slopes) slope = __ldg(a.docs.slopes + h) * kLog2e;
+      if (BIAS) dist.set(__ldg(a.docs.slopes + h) * kLog2e, span.hi > p);
       if (!SPLIT) {
         m = neg_inf();
         l = 0.f;
@@ -352,12 +353,16 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::after_sync();
         float x[128];
+        if constexpr (CAP || BIAS) {
+          win::tmem_ld128(tS, x);
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float y[32];
-          tc::tmem_ld32(tS + 32 * q, y);
+          for (int q = 0; q < 4; ++q) {
+            float y[32];
+            tc::tmem_ld32(tS + 32 * q, y);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[32 * q + c] = y[c];
+            for (int c = 0; c < 32; ++c) x[32 * q + c] = y[c];
+          }
         }
         // column c is key kb + c (or sink v0 + c): visible iff c <= hi and (c >= lo or c < sk)
         const int kb = kl.lo + v0 - kl.SP;
@@ -367,12 +372,36 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           lo = span.lo - kb;
           sk = 0;
         }
-        if constexpr (MASK == win::kScored) {
-          scores.cap_all(x);
-          if (a.docs.slopes) {
-            const float d0 = static_cast<float>(p - kb);
+        if constexpr (CAP || BIAS) {
+          if (!scores.look(x)) {
+            scores.template cap_far<128>(tS);
+            win::tmem_ld128(tS, x);
+          }
+          const float d0 = static_cast<float>(p - kb);
 #pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = fmaf(-slope, fabsf(d0 - static_cast<float>(c)), x[c]);
+          for (int q = 0; q < 8; ++q) {
+            const float b = BIAS && !dist.ahead ? dist.base(d0, 16 * q) : 0.f;
+            const uint64_t bb = tc::pack2(b, b);
+            if (!CAP || scores.near) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint64_t v = tc::pack2(x[16 * q + 2 * c], x[16 * q + 2 * c + 1]), f = scores.factor(v);
+                tc::unpack2(BIAS ? tc::fma2(v, f, bb) : win::mul2(v, f), x[16 * q + 2 * c], x[16 * q + 2 * c + 1]);
+              }
+            } else if (BIAS) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) x[16 * q + c] += b;
+            }
+          }
+          if (BIAS) {
+            if (!dist.ahead) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                tc::unpack2(tc::add2(tc::pack2(x[2 * c], x[2 * c + 1]), dist.part[c & 7]), x[2 * c], x[2 * c + 1]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) x[c] = fmaf(-dist.slope, fabsf(d0 - static_cast<float>(c)), x[c]);
+            }
           }
         }
         const bool all = hi >= 127 && (lo <= 0 || sk >= 128);

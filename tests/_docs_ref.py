@@ -45,7 +45,9 @@ def head(q, k, v, see, scale, cap=0.0, slope=0.0, dist=None, g=None):
         dS = P * (dP - D) * back
         De = (g.abs() * tol["O"]).sum(1, keepdim=True) + (g.abs() * o.abs()).sum(1, keepdim=True) * d * E
         dPe = (g.abs() @ v.abs().T) * d * E
-        dSe = dS.abs() * (H + pe) + P * back.abs() * (De + dPe) * (1 + H) + P * (dP - D).abs() * 2.0 ** -19 * bool(cap)
+        # P (x + ex) (b + eb) with x = dP - D, b = 1 - tanh^2 is off by P (|b| ex + |x| eb + ex eb), ex = De + dPe, eb = 2^-19
+        # (the last term is what remains where x and b are both 0)
+        dSe = dS.abs() * (H + pe) + P * back.abs() * (De + dPe) * (1 + H) + P * ((dP - D).abs() + De + dPe) * 2.0 ** -19 * bool(cap)
         out |= {"dQ": scale * dS @ k, "dK": scale * dS.T @ q, "dV": P.T @ g}
         tol |= {"dQ": scale * (dSe + acc * dS.abs()) @ k.abs() + H * out["dQ"].abs(),
                 "dK": scale * (dSe + acc * dS.abs()).T @ q.abs(), "dV": (P * (H + pe + acc)).T @ g.abs()}
