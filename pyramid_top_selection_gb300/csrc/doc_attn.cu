@@ -22,7 +22,7 @@ int doc_fwd_launch(const FwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   // (the softmax warps' larger register share is drawn from what the CTA was launched with: 168 a thread)
   if (int e = ready(window_fwd_kernel<D, false, MASK>, FwdSmem<D>::bytes, 168)) return e;
   ProfScope ps(st, "doc_fwd");
-  const win::Behind b(dim3(static_cast<unsigned>(std::min(a.n_items, sm_count()))), kThreads, FwdSmem<D>::bytes, st);
+  const win::Behind b(dim3(static_cast<unsigned>(std::min(a.n_items, sm_count()))), kFwdThreads, FwdSmem<D>::bytes, st);
   return cudaLaunchKernelEx(&b.cfg, window_fwd_kernel<D, false, MASK>, a, m[0], m[1], m[2], m[1], m[2], m[3]);
 }
 

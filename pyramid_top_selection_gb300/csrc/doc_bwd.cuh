@@ -13,21 +13,24 @@ namespace {
 
 template <int D, int MASK>
 int doc_bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
+  // capped scores in dQ's kernel: four threads a row (425 -> 346 us for 8192 rows of 16 heads over 2, all causal; no gain without
+  // a cap, nor in dK, dV's kernel, where 96 registers a thread are too few)
+  constexpr int NQ = MASK & win::kCap ? 4 : 2;
   static win::Ready dq_ready, dkv_ready;
-  if (int e = dq_ready(window_dq_kernel<D, MASK>, DqSmem<D>::bytes)) return e;
-  if (int e = dkv_ready(window_dkv_kernel<D, MASK>, DkvSmem<D>::bytes)) return e;
+  if (int e = dq_ready(window_dq_kernel<D, MASK, NQ>, DqSmem<D>::bytes)) return e;
+  if (int e = dkv_ready(window_dkv_kernel<D, MASK, 2>, DkvSmem<D>::bytes)) return e;
   const int dq_ctas = std::min({a.n_items, sm_count(), kDqCtas});
   cudaError_t e;
   {
     ProfScope ps(st, "doc_dq");
-    const win::Behind b(dim3(dq_ctas), kThreads, DqSmem<D>::bytes, st);
-    e = cudaLaunchKernelEx(&b.cfg, window_dq_kernel<D, MASK>, a, m[0], m[1], m[2], m[3], m[2], m[3], m[6]);
+    const win::Behind b(dim3(dq_ctas), bwd_threads(NQ), DqSmem<D>::bytes, st);
+    e = cudaLaunchKernelEx(&b.cfg, window_dq_kernel<D, MASK, NQ>, a, m[0], m[1], m[2], m[3], m[2], m[3], m[6]);
   }
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(st, "doc_dkv");
-    const win::Behind b(dim3(a.n_kt * a.n_bh * a.nck), kThreads, DkvSmem<D>::bytes, st);
-    e = cudaLaunchKernelEx(&b.cfg, window_dkv_kernel<D, MASK>, a, m[0], m[1], m[2], m[3], m[4], m[5], dq_ctas);
+    const win::Behind b(dim3(a.n_kt * a.n_bh * a.nck), bwd_threads(2), DkvSmem<D>::bytes, st);
+    e = cudaLaunchKernelEx(&b.cfg, window_dkv_kernel<D, MASK, 2>, a, m[0], m[1], m[2], m[3], m[4], m[5], dq_ctas);
   }
   if (e != cudaSuccess || a.nck == 1) return e;
   ProfScope ps(st, "doc_dkv_sum");

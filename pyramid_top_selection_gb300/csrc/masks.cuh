@@ -55,71 +55,88 @@ struct DocSeen {
   }
 };
 
-// Scores in powers of two from products x, two at a time, before the distance's share:
-//   y = scale log2 e x, or (CAP) cap log2 e tanh(k x), k = scale / cap: within |k x| <= 1 by a polynomial of (k x)^2 on
-//   the FMA units (minimax on [0, 1]: tanh within 2.5e-7), as a warp that has no larger product takes it; else by
-//   tanh_of, three special-function operations, in a loop of its own over tensor memory (cap_far).
-// The polynomial's coefficients are taken times k^2i and scale log2 e, so that y = x p(x^2).
+// Scores in powers of two from a thread's products x, before the distance's share:
+//   y = scale log2 e x, or (CAP) cap log2 e tanh(k x), k = scale / cap. Where a warp has no product beyond |k x| = 3/4, tanh
+//   is a polynomial of (k x)^2 on the FMA units (minimax, within 2.7e-7 in fp32), its coefficients taken times k^2i and
+//   scale log2 e: 6 operations; else 1 - 2 / (1 + e^(2 k x)) (within 2.5e-7): 3 of the FMA units and two special
+//   functions, of which the reciprocal alone takes as long as the 6 (16 a cycle and SM).
+// Not hidden by the products: the FMA units are these operations' bound, 128 a cycle and SM, packed or not.
 template <bool CAP>
 struct Scores {
   float k, cap2, back2;    // scale / cap, cap log2 e, -1 / (cap log2 e)^2
-  uint64_t p[CAP ? 6 : 1]; // coefficients in pairs (p[0] alone: scale log2 e)
-  uint64_t one;            // what a product is multiplied by where the polynomial does not apply: scale log2 e, or 1 after cap_far
-  bool near;
-  __device__ __forceinline__ Scores(float scale, float cap) : k(0.f), cap2(0.f), back2(0.f), near(false) {
+  uint64_t p[CAP ? 5 : 1]; // coefficients in pairs (p[0] alone: scale log2 e)
+  __device__ __forceinline__ Scores(float scale, float cap) : k(0.f), cap2(0.f), back2(0.f) {
     const float c1 = scale * kScoreLog2e;
-    one = tc::pack2(c1, c1);
-    p[0] = one;
+    p[0] = tc::pack2(c1, c1);
     if (CAP) {
-      one = tc::pack2(1.f, 1.f);
       k = scale / cap;
       cap2 = cap * kScoreLog2e;
       back2 = -1.f / (cap2 * cap2);
-      const float k2 = k * k, c[6] = {0.999996841f, -0.333240032f, 0.132535249f, -0.0509728603f, 0.016114179f, -0.00283946446f};
+      const float k2 = k * k, c[5] = {0.999997199f, -0.333230764f, 0.132260919f, -0.0492804497f, 0.0123188347f};
       float f = c1;
 #pragma unroll
-      for (int i = 0; i < 6; ++i, f *= k2) p[CAP ? i : 0] = tc::pack2(c[i] * f, c[i] * f);
+      for (int i = 0; i < 5; ++i, f *= k2) p[CAP ? i : 0] = tc::pack2(c[i] * f, c[i] * f);
     }
   }
-  // Looks at a warp's products: whether all are in the polynomial's range.
+  // N products to y, in place; the chains of four pairs side by side.
   template <int N>
-  __device__ __forceinline__ bool look(const float (&x)[N]) {
-    near = false;
-    if (CAP) {
+  __device__ __forceinline__ void apply(float (&x)[N]) const { apply_with<false>(x, [](int) { return 0.f; }); }
+  // The same plus add(q) for the q-th 16 of them.
+  template <int N, class A>
+  __device__ __forceinline__ void apply(float (&x)[N], A add) const { apply_with<true>(x, add); }
+
+ private:
+  template <bool ADD, int N, class A>
+  __device__ __forceinline__ void apply_with(float (&x)[N], A add) const {
+    auto plus = [&](uint64_t a, uint64_t b, int c) {           // a b, plus what is added at column c
+      if constexpr (!ADD) return mul2(a, b);
+      const float s = add(c >> 4);
+      return tc::fma2(a, b, tc::pack2(s, s));
+    };
+    if constexpr (!CAP) {
+#pragma unroll
+      for (int c = 0; c < N; c += 2) tc::unpack2(plus(tc::pack2(x[c], x[c + 1]), p[0], c), x[c], x[c + 1]);
+    } else {
       float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < N; c += 8)
 #pragma unroll
         for (int q = 0; q < 4; ++q) asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(top[q]) : "f"(x[c + q]), "f"(x[c + 4 + q]));
-      near = __all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * k <= 1.f);
-    }
-    return !CAP || near;
-  }
-  // The factor of a pair of products: y = x factor.
-  __device__ __forceinline__ uint64_t factor(uint64_t x) const {
-    uint64_t r = p[CAP ? 5 : 0];
-    if (CAP) {
-      const uint64_t y = mul2(x, x);
+      if (__all_sync(0xffffffffu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * k <= 0.75f)) {
 #pragma unroll
-      for (int i = 4; i >= 0; --i) r = tc::fma2(r, y, p[CAP ? i : 0]);
+        for (int c0 = 0; c0 < N; c0 += 8) {
+          uint64_t v[4], r[4], y[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            v[c] = tc::pack2(x[c0 + 2 * c], x[c0 + 2 * c + 1]);
+            y[c] = mul2(v[c], v[c]);
+            r[c] = p[4];
+          }
+#pragma unroll
+          for (int i = 3; i >= 0; --i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) r[c] = tc::fma2(r[c], y[c], p[i]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::unpack2(plus(v[c], r[c], c0 + 2 * c), x[c0 + 2 * c], x[c0 + 2 * c + 1]);
+        }
+      } else {
+        const float e2 = 2.f * kScoreLog2e * k;
+        const uint64_t ee = tc::pack2(e2, e2), one = tc::pack2(1.f, 1.f), m2 = tc::pack2(-2.f * cap2, -2.f * cap2);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+          float a, b;
+          tc::unpack2(mul2(tc::pack2(x[c], x[c + 1]), ee), a, b);
+          tc::unpack2(tc::add2(tc::pack2(tc::ex2(a), tc::ex2(b)), one), a, b);
+          const float top = cap2 + (ADD ? add(c >> 4) : 0.f);
+          tc::unpack2(tc::fma2(tc::pack2(rcp_approx(a), rcp_approx(b)), m2, tc::pack2(top, top)), x[c], x[c + 1]);
+        }
+      }
     }
-    return r;
   }
+
+ public:
   // What a gradient takes through the cap, from capped scores: 1 - tanh^2.
   __device__ __forceinline__ uint64_t back(uint64_t y) const { return tc::fma2(mul2(y, y), tc::pack2(back2, back2), tc::pack2(1.f, 1.f)); }
-  // N columns (a multiple of 32) of the thread's lane in tensor memory: products to capped scores, in place.
-  template <int N>
-  __device__ __forceinline__ void cap_far(uint32_t taddr) const {
-#pragma unroll 1
-    for (int q = 0; q < N; q += 16) {
-      uint32_t u[16];
-      tmem_ld16(taddr + q, u);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(cap2 * tanh_of(__uint_as_float(u[c]) * k));
-      tc::tmem_st16(taddr + q, u);
-    }
-    tc::tmem_wait_st();
-  }
 };
 
 // 128 consecutive fp32 columns of this thread's TMEM lane, in one load.

@@ -17,7 +17,7 @@ struct ClusterLaunch {
   cudaLaunchAttribute attr{};
   ClusterLaunch(int grid, int splits, int smem, cudaStream_t st) {
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kFwdThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -72,7 +72,7 @@ int fwd_launch(FwdArgs& a, int64_t tiles, const CUtensorMap* m, cudaStream_t st)
     return cudaLaunchKernelEx(&c.cfg, window_fwd_kernel<D, true, win::kWindow>, a, m[0], m[1], m[2], m[3], m[4], m[5]);
   }
   if (int e = fwd_ready<D, false>()) return e;
-  window_fwd_kernel<D, false, win::kWindow><<<std::min(a.n_items, sm_count()), kThreads, FwdSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3],
+  window_fwd_kernel<D, false, win::kWindow><<<std::min(a.n_items, sm_count()), kFwdThreads, FwdSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3],
                                                                                                      m[4], m[5]);
   return cudaGetLastError();
 }

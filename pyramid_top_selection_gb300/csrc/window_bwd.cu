@@ -15,20 +15,20 @@ namespace {
 template <int D>
 int bwd_launch(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   static win::Ready dq_ready, dkv_ready;
-  if (int e = dq_ready(window_dq_kernel<D, win::kWindow>, DqSmem<D>::bytes)) return e;
-  if (int e = dkv_ready(window_dkv_kernel<D, win::kWindow>, DkvSmem<D>::bytes)) return e;
+  if (int e = dq_ready(window_dq_kernel<D, win::kWindow, 2>, DqSmem<D>::bytes)) return e;
+  if (int e = dkv_ready(window_dkv_kernel<D, win::kWindow, 2>, DkvSmem<D>::bytes)) return e;
   const int dq_ctas = std::min({a.n_items, sm_count(), kDqCtas});
   {
     ProfScope ps(st, "window_dq");
-    window_dq_kernel<D, win::kWindow><<<dq_ctas, kThreads, DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[8]);
+    window_dq_kernel<D, win::kWindow, 2><<<dq_ctas, bwd_threads(2), DqSmem<D>::bytes, st>>>(a, m[0], m[1], m[2], m[3], m[4], m[5], m[8]);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(st, "window_dkv");
     const int items = a.n_snk + (a.n_kt - a.n_st) * a.n_bh * a.nck;
-    const win::Behind b(dim3(items), kThreads, DkvSmem<D>::bytes, st);
-    e = cudaLaunchKernelEx(&b.cfg, window_dkv_kernel<D, win::kWindow>, a, m[0], m[1], m[2], m[3], m[6], m[7], dq_ctas);
+    const win::Behind b(dim3(items), bwd_threads(2), DkvSmem<D>::bytes, st);
+    e = cudaLaunchKernelEx(&b.cfg, window_dkv_kernel<D, win::kWindow, 2>, a, m[0], m[1], m[2], m[3], m[6], m[7], dq_ctas);
   }
   if (e != cudaSuccess) return e;
   const int first = a.ncs > 1 ? 0 : a.n_st, end = a.nck > 1 ? a.n_kt : a.n_st;

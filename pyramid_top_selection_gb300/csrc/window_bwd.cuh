@@ -30,7 +30,9 @@ namespace pisa {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int kThreads = 384;                  // warps 0-7 softmax and output, 8 (and 10) MMA, 9 loader, 11 items (dQ)
+// Warps: 4 NG softmax and output (NG threads a row, 128 / NG columns each), then MMA, loader, MMA (dQ), items (dQ).
+// NG = 2 is the window's; scores that cost more than the products hide take NG = 4 (launches).
+constexpr int bwd_threads(int NG) { return 32 * (4 * NG + 4); }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
 constexpr uint64_t kPatient = 1ull << 40;      // the item warp outwaits the others, whose giving up it sees
@@ -61,6 +63,10 @@ template <int MASK>
 __device__ __forceinline__ int end_of(const BwdArgs& a, int b) {
   return MASK == win::kWindow ? win::valid_len(a.len, b, a.s.N) : a.docs.bounds[a.s.N].y;
 }
+
+// COLS consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&v)[64]) { tc::tmem_ld64(taddr, v); }
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&v)[32]) { tc::tmem_ld32(taddr, v); }
 
 // ------------------------------------------------------------------------------------------ dQ
 template <int D>
@@ -116,20 +122,21 @@ __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
 // 4 x 16384 rows of 16 heads over 4 KV heads, d = 128: 690 us at a window of 1024 and 4 sinks (1.16
 // PFLOP/s of its three products), 268 us for 8192 rows of 16 heads over 2, all causal (1.54); 640 and 256 us
 // in short bursts.
-template <int D, int MASK>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int MASK, int NG>
+__global__ void __launch_bounds__(bwd_threads(NG), 1)
 window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap kmap32, const __grid_constant__ CUtensorMap vmap32,
                  const __grid_constant__ CUtensorMap omap) {
   using M = DqSmem<D>;
+  constexpr int NS = 4 * NG, COLS = 128 / NG;
   extern __shared__ __align__(1024) unsigned char sm[];      // SW128 tiles first
   __shared__ __align__(8) uint64_t q_full, q_empty, k_full[M::NK], k_empty[M::NK], v_full[M::NV], v_empty[M::NV],
       s_full[2], dp_full[2], d_full, ds_full[2], dq_done[2], dq_last, dq_empty, drain[2], never;
   __shared__ win::ItemRing s_items;
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  __shared__ float s_sum[2][128];            // D of the rows, as two sums
+  __shared__ float s_sum[NG][128];           // D of the rows, a sum for each of their threads
 
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
@@ -151,16 +158,16 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     tc::bar_init(&s_full[1], 1);
     tc::bar_init(&dp_full[0], 1);
     tc::bar_init(&dp_full[1], 1);
-    tc::bar_init(&d_full, 256);
-    tc::bar_init(&ds_full[0], 256);
-    tc::bar_init(&ds_full[1], 256);
+    tc::bar_init(&d_full, 32 * NS);
+    tc::bar_init(&ds_full[0], 32 * NS);
+    tc::bar_init(&ds_full[1], 32 * NS);
     tc::bar_init(&dq_done[0], 1);
     tc::bar_init(&dq_done[1], 1);
     tc::bar_init(&dq_last, 1);
-    tc::bar_init(&dq_empty, 256);
+    tc::bar_init(&dq_empty, 32 * NS);
     tc::bar_init(&drain[0], 1);
     tc::bar_init(&drain[1], 1);
-    win::ring_init(s_items, 11);
+    win::ring_init(s_items, NS + 3);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
     s_abort = 0;
@@ -177,7 +184,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   auto get = [&](int k) { return win::ring_get(s_items, k, &s_abort, a.wait_ns); };
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
 
-  if (warp == 9) {
+  if (warp == NS + 1) {
     // ------------------------------------------------------------------ loader
     int n_k = 0, n_v = 0, n_q = 0;             // loads issued
     bool ok = true;
@@ -239,7 +246,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     for (int k = max(0, n_k - M::NK); k < n_k; ++k) tc::bar_wait(&k_full[k % M::NK], (k / M::NK) & 1, kDrainNs);
     for (int k = max(0, n_v - M::NV); k < n_v; ++k) tc::bar_wait(&v_full[k % M::NV], (k / M::NV) & 1, kDrainNs);
     if (n_q) tc::bar_wait(&q_full, (n_q - 1) & 1, kDrainNs);
-  } else if (warp == 8) {
+  } else if (warp == NS) {
     // ------------------------------------------------------------------ MMA, S and dP (the warp
     // together, one lane issuing: operands stay in uniform registers)
     const bool leader = win::elect();
@@ -291,7 +298,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       __syncwarp();
       tc::bar_wait(&drain[0], 0, kDrainNs);
     }
-  } else if (warp == 10) {
+  } else if (warp == NS + 2) {
     // ------------------------------------------------------------------ MMA, dQ
     const bool leader = win::elect();
     const uint32_t dK = win::desc_mn_lo(aK, 128 * 128);
@@ -310,7 +317,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         tc::after_sync();
         issued = true;
         if (leader) {
-          win::product_ts<D, 64>(tm + 384, tm + 128 * (g & 1), dK + st * kStage, j > 0);
+          win::product_ts<D, COLS>(tm + 384, tm + 128 * (g & 1), dK + st * kStage, j > 0);
           tc::commit(&dq_done[g & 1]);
           tc::commit(&k_empty[st]);
           if (j + 1 == n) tc::commit(&dq_last);
@@ -324,7 +331,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       __syncwarp();
       tc::bar_wait(&drain[1], 0, kDrainNs);
     }
-  } else if (warp == 11) {
+  } else if (warp == NS + 3) {
     // ------------------------------------------------------------------ items, decoded ahead of the other
     // roles; their rows' lse is asked into L2 meanwhile
     const int rounds = win::rounds_of(a.n_items);
@@ -342,13 +349,13 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.lse + (static_cast<int64_t>(it.b) * s.Hq + it.h0 + (lane >> 1)) * s.Nq + t));
       }
     }
-  } else if (warp < 8) {
-    // ------------------------------------------------------------------ softmax: row r, columns 64 g ..
+  } else {
+    // ------------------------------------------------------------------ softmax: row r, columns COLS g ..
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c1 = s.scale * kLog2e;
     constexpr bool CAP = MASK & win::kCap, BIAS = MASK & win::kBias;
-    win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
+    const win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
     win::Distance dist;
     int n_k = 0, n_q = 0, kk = 0, k_item = 0;
     auto lse_of = [&](const win::Item& x) -> float {
@@ -378,15 +385,14 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       win::DocSpan span;
       if (MASK != win::kWindow && i < s.Nq) span = win::DocSpan(a.docs, i);
       if (BIAS) dist.set(__ldg(a.docs.slopes + h) * kLog2e, span.hi > p);
-      uint32_t far = 0;                                      // tiles of a short item whose S has been capped in place
       // x = P (through: times what a gradient takes through the cap), y = dP of key tile j; see: the visible columns,
       // where some are not
-      auto load = [&](int j, float (&x)[64], float (&y)[64], uint32_t (&see)[2], bool& masked, bool through) -> bool {
-        const int k = n_k + j, v0 = 128 * j + 64 * g;
+      auto load = [&](int j, float (&x)[COLS], float (&y)[COLS], uint32_t (&see)[COLS / 32], bool& masked, bool through) -> bool {
+        const int k = n_k + j, v0 = 128 * j + COLS * g;
         bool ok = wait(&s_full[k & 1], (k >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc::after_sync();
-        tc::tmem_ld64(tm + 128 * (k & 1) + 64 * g + lane_off, x);
+        tmem_cols(tm + 128 * (k & 1) + COLS * g + lane_off, x);
         const int kb = kl.lo + v0 - kl.SP;
         int hi = row ? p - kb : -1, lo = max(p - s.window + 1, kl.lo) - kb, sk = s.sinks - v0;
         if constexpr (MASK != win::kWindow) {
@@ -394,31 +400,26 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           lo = span.lo - kb;
           sk = 0;
         }
-        see[0] = see[1] = 0xffffffffu;
-        masked = !__all_sync(0xffffffffu, hi >= 63 && (lo <= 0 || sk >= 64));
+#pragma unroll
+        for (int q = 0; q < COLS / 32; ++q) see[q] = 0xffffffffu;
+        masked = !__all_sync(0xffffffffu, hi >= COLS - 1 && (lo <= 0 || sk >= COLS));
         if (masked) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < COLS / 32; ++q)
             see[q] = win::bit_range(0, hi - 32 * q) & (win::bit_range(lo - 32 * q, 31) | win::bit_range(0, sk - 1 - 32 * q));
         }
         if constexpr (CAP || BIAS) {
-          if (CAP && (far >> j) & 1) {                       // taken a second time (n <= 2): capped already
-            scores.near = false;
-          } else if (!scores.look(x)) {
-            scores.template cap_far<64>(tm + 128 * (k & 1) + 64 * g + lane_off);
-            tc::tmem_ld64(tm + 128 * (k & 1) + 64 * g + lane_off, x);
-            far |= n <= 2 ? 1u << j : 0u;
-          }
+          scores.apply(x);
           const float d0 = static_cast<float>(p - kb);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < COLS / 16; ++q) {
             const float b = nl + (BIAS && !dist.ahead ? dist.base(d0, 16 * q) : 0.f);
             const uint64_t bb = tc::pack2(b, b);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               float& x0 = x[16 * q + 2 * c];
               float& x1 = x[16 * q + 2 * c + 1];
-              const uint64_t v = tc::pack2(x0, x1), y = win::mul2(v, !CAP || scores.near ? scores.factor(v) : scores.one);
+              const uint64_t y = tc::pack2(x0, x1);
               uint64_t z = tc::add2(y, bb);
               if (BIAS) {
                 if (!dist.ahead) {
@@ -437,7 +438,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         } else {
           const uint64_t cc = tc::pack2(c1, c1), ll = tc::pack2(nl, nl);
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
+          for (int c = 0; c < COLS; c += 2) {
             float y0, y1;
             tc::unpack2(tc::fma2(tc::pack2(x[c], x[c + 1]), cc, ll), y0, y1);
             x[c] = tc::ex2(y0);
@@ -447,11 +448,11 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         ok = wait(&dp_full[k & 1], (k >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc::after_sync();
-        tc::tmem_ld64(tm + (n == 2 && j == 1 ? 384 : 256) + 64 * g + lane_off, y);
+        tmem_cols(tm + (n == 2 && j == 1 ? 384 : 256) + COLS * g + lane_off, y);
         return true;
       };
-      float x[64], y[64];
-      uint32_t see[2];
+      float x[COLS], y[COLS];
+      uint32_t see[COLS / 32];
       bool masked;
       // D: the sum of P dP, or dO . O of the tiles in shared memory
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -460,7 +461,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
           ok = load(j, x, y, see, masked, false);
           if (!ok) break;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < COLS; ++c)
             if (!masked || (see[c >> 5] >> (c & 31)) & 1) sum[c & 3] = fmaf(x[c], y[c], sum[c & 3]);
         }
         if (!ok) break;
@@ -470,7 +471,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         uint64_t acc[2] = {0, 0};
         const unsigned char* po = sm + M::oK + kk % M::NK * M::TILE + r * 128;
         const unsigned char* pd = sm + M::oO + r * 128;
-        constexpr int HC = D / 16;                           // 16-byte pieces of half a row
+        constexpr int HC = D / 8 / NG;                       // 16-byte pieces of a thread's part of a row
 #pragma unroll
         for (int c = 0; c < HC; ++c) {
           const int pc = g * HC + c, at = (pc >> 3) * (128 * 128) + (((pc & 7) ^ (r & 7)) << 4);
@@ -488,7 +489,8 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       tc::bar_arrive(&d_full);
       ok = wait(&d_full, n_q & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const float dl = s_sum[0][r] + s_sum[1][r];
+      float dl = s_sum[0][r] + s_sum[1][r];
+      if (NG == 4) dl += s_sum[NG - 2][r] + s_sum[NG - 1][r];
       if (n > 2 && tid == 0) tc::bar_arrive(&k_empty[kk % M::NK]);
       kk += n > 2;
       if (g == 0 && row) {
@@ -500,17 +502,17 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         ok = load(j, x, y, see, masked, true);
         if (!ok) break;
         const int k = n_k + j;
-        const uint32_t tS = tm + 128 * (k & 1) + 64 * g + lane_off;
+        const uint32_t tS = tm + 128 * (k & 1) + COLS * g + lane_off;
         const uint64_t dd = tc::pack2(-dl, -dl);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2)
+        for (int c = 0; c < COLS; c += 2)
           tc::unpack2(win::mul2(tc::pack2(x[c], x[c + 1]), tc::add2(tc::pack2(y[c], y[c + 1]), dd)), x[c], x[c + 1]);
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
+          for (int c = 0; c < COLS; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < COLS / 32; ++q) {
           uint32_t u[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) u[c] = pack_bf16(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
@@ -534,31 +536,29 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       kk += n;
       next = get(k_item + 1);
       lse_next = lse_of(next);
-      // dQ of the item, scaled: row r's columns 64 g .. (shared memory is full, and Q's and dO's tiles
+      // dQ of the item, scaled: row r's 32 columns in turn for its threads (shared memory is full, and Q's and dO's tiles
       // already take the next item's, so the rows go out from registers)
       ok = wait(&dq_last, n_q & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::after_sync();
       ++n_q;
-      if (g < M::KB) {
-        const int64_t row0 = ((static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + it.h0) * D + 64 * g + 8 * (lane & 3);
+      const int64_t row0 = ((static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + it.h0) * D + 8 * (lane & 3);
+#pragma unroll 1
+      for (int q = g; q < D / 32; q += NG) {
+        float y[32];
+        tc::tmem_ld32(tm + 384 + 32 * q + lane_off, y);
+        uint32_t u[4][4];                                    // four 16-byte pieces of row r
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float y[32];
-          tc::tmem_ld32(tm + 384 + 64 * g + 32 * q + lane_off, y);
-          uint32_t u[4][4];                                  // four 16-byte pieces of row r
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int k = 0; k < 4; ++k) u[c][k] = pack_bf16(s.scale * y[8 * c + 2 * k], s.scale * y[8 * c + 2 * k + 1]);
+        win::transpose4(u, lane);                            // piece lane & 3 of four rows: 64 bytes of a row a store
 #pragma unroll
-            for (int k = 0; k < 4; ++k) u[c][k] = pack_bf16(s.scale * y[8 * c + 2 * k], s.scale * y[8 * c + 2 * k + 1]);
-          win::transpose4(u, lane);                          // piece lane & 3 of four rows: 64 bytes of a row a store
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int rr = (r & ~3) + c;
-            if (it.t0 + (rr >> a.lp) < s.Nq)
-              *reinterpret_cast<uint4*>(a.dQ + row0 + (static_cast<int64_t>(rr >> a.lp) * s.Hq + (rr & (a.P - 1))) * D + 32 * q) =
-                  make_uint4(u[c][0], u[c][1], u[c][2], u[c][3]);
-          }
+        for (int c = 0; c < 4; ++c) {
+          const int rr = (r & ~3) + c;
+          if (it.t0 + (rr >> a.lp) < s.Nq)
+            *reinterpret_cast<uint4*>(a.dQ + row0 + (static_cast<int64_t>(rr >> a.lp) * s.Hq + (rr & (a.P - 1))) * D + 32 * q) =
+                make_uint4(u[c][0], u[c][1], u[c][2], u[c][3]);
         }
       }
       tc::before_sync();
@@ -673,12 +673,13 @@ struct DkvItem {
 // that the next one overwrites the operand of is seen some 300 cycles after its issue; dK and dP^T a
 // tile later would close these gaps, but hold two tiles' P in registers and spill (twice the time).
 // 4 x 16384 rows of 16 heads over 4, a window of 1024, 4 sinks: 829 us, 1.29 PFLOP/s of its four products.
-template <int D, int MASK>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int MASK, int NG>
+__global__ void __launch_bounds__(bwd_threads(NG), 1)
 window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap domap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap dkmap, const __grid_constant__ CUtensorMap dvmap, int dq_ctas) {
   using M = DkvSmem<D>;
+  constexpr int NS = 4 * NG, COLS = 128 / NG;
   extern __shared__ __align__(1024) unsigned char sm[];      // the only shared memory: SW128 tiles first
   DkvBars& bar = *reinterpret_cast<DkvBars*>(sm + M::oBar);
   auto &kv_full = bar.kv_full, &s_full = bar.s_full, &dp_full = bar.dp_full, &p_full = bar.p_full, &ds_full = bar.ds_full,
@@ -702,7 +703,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   const int n = win::uniform(own * a.sets);
   // This kernel starts while dQ's ends: what that wrote (statistics, status) is read after grid_wait only,
   // and one warp here waits for it in any case.
-  if (warp == 11) {
+  if (warp == NS + 3) {
     if (lane == 0) win::launch_dependents();
     if (blockIdx.x == 0) {
       win::grid_wait();
@@ -738,7 +739,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     win::bulk_load(stat, a.nlse + at, 512, &st_full[ss]);
     win::bulk_load(stat + 512, a.delta + at, 512, &st_full[ss]);
   };
-  if (warp == 9 && lane == 0) {        // the first loads run under the rest of the CTA's start
+  if (warp == NS + 1 && lane == 0) {        // the first loads run under the rest of the CTA's start
     tc::bar_init(&kv_full, 1);
     for (int k = 0; k < M::NQ; ++k) {
       tc::bar_init(&q_full[k], 1);
@@ -748,12 +749,12 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       tc::bar_init(&o_full[k], 1);
       tc::bar_init(&o_empty[k], 1);
       tc::bar_init(&st_full[k], 1);
-      tc::bar_init(&st_empty[k], 8);
+      tc::bar_init(&st_empty[k], NS);
     }
     tc::bar_init(&s_full, 1);
     tc::bar_init(&dp_full, 1);
-    tc::bar_init(&p_full, 256);
-    tc::bar_init(&ds_full, 256);
+    tc::bar_init(&p_full, 32 * NS);
+    tc::bar_init(&ds_full, 32 * NS);
     tc::bar_init(&dv_done, 1);
     tc::bar_init(&dk_done, 1);
     tc::bar_init(&drain, 1);
@@ -782,7 +783,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
   auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&s_abort) != 0; };
 
-  if (warp == 9) {
+  if (warp == NS + 1) {
     // ------------------------------------------------------------------ loader
     if (lane == 0 && n > 0) {
       int n_q = 1, n_o = 1, n_st = 1;          // loads issued
@@ -803,7 +804,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       for (int x = max(0, n_o - M::NO); x < n_o; ++x) tc::bar_wait(&o_full[x % M::NO], (x / M::NO) & 1, kDrainNs);
       for (int x = max(0, n_st - 2); x < n_st; ++x) tc::bar_wait(&st_full[x & 1], (x >> 1) & 1, kDrainNs);
     }
-  } else if (warp == 8) {
+  } else if (warp == NS) {
     // ------------------------------------------------------------------ MMA (the warp together, one
     // lane issuing). What a product needs is waited for while the one before it still runs.
     if (n > 0) {
@@ -844,7 +845,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!wait(&p_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D, 64>(tm + 256, tm, dOt + so * kStage, k > 0);
+          win::product_ts<D, COLS>(tm + 256, tm, dOt + so * kStage, k > 0);
           tc::commit(&dv_done);
           tc::commit(&o_empty[so]);
         }
@@ -857,7 +858,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         if (!wait(&ds_full, k & 1)) break;
         tc::after_sync();
         if (leader) {
-          win::product_ts<D, 64>(tm + 256 + D, tm + 128, dQt + qk * kStage, k > 0);
+          win::product_ts<D, COLS>(tm + 256 + D, tm + 128, dQt + qk * kStage, k > 0);
           tc::commit(&dk_done);
           tc::commit(&q_empty[qk]);
         }
@@ -870,8 +871,8 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         tc::bar_wait(&drain, 0, kDrainNs);
       }
     }
-  } else if (warp < 8) {
-    // ------------------------------------------------------------------ softmax: key (lane) r, rows 64 g ..
+  } else if (warp < NS) {
+    // ------------------------------------------------------------------ softmax: key (lane) r, rows COLS g ..
     const int g = warp >> 2, r = tid & 127, key = kb + r;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float c1 = s.scale * kLog2e;
@@ -884,35 +885,30 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       see_end = seen.end;
     }
     constexpr bool CAP = MASK & win::kCap, BIAS = MASK & win::kBias;
-    win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
+    const win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
     bool ok = true;
     for (int k = 0; k < n; ++k) {
       const int sq = k % M::NQ, ss = k & 1, pt0 = s.off + tile_tok(k);
       ok = wait(&st_full[ss], (k >> 1) & 1) && wait(&s_full, k & 1);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc::after_sync();
-      float x[64];
-      const uint32_t tS = tm + 64 * g + lane_off;
-      tc::tmem_ld64(tS, x);
+      float x[COLS];
+      const uint32_t tS = tm + COLS * g + lane_off;
+      tmem_cols(tS, x);
       // column c is a row at position pt0 + c / P: visible iff lo <= c <= hi
-      const int lo = max(-1, min(128, see_first - pt0)) * a.P - 64 * g;
-      const int hi = static_cast<int>(max(int64_t(0), min(int64_t(128), see_end - pt0))) * a.P - 1 - 64 * g;
-      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-      const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 63);
-      if (masked) {
-        see[0] = win::bit_range(lo, hi);
-        see[1] = win::bit_range(lo - 32, hi - 32);
-      }
-      const float4* nl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 256 * g);
-      const float4* dl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 512 + 256 * g);
+      const int lo = max(-1, min(128, see_first - pt0)) * a.P - COLS * g;
+      const int hi = static_cast<int>(max(int64_t(0), min(int64_t(128), see_end - pt0))) * a.P - 1 - COLS * g;
+      uint32_t see[COLS / 32];
+      const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= COLS - 1);
+#pragma unroll
+      for (int q = 0; q < COLS / 32; ++q) see[q] = masked ? win::bit_range(lo - 32 * q, hi - 32 * q) : 0xffffffffu;
+      const float4* nl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 4 * COLS * g);
+      const float4* dl = reinterpret_cast<const float4*>(sm + M::oStat + ss * 1024 + 512 + 4 * COLS * g);
       // P as bf16 over S^T's first half
       auto put = [&](int q, const uint32_t (&u)[16]) { tc::tmem_st16(tS + 16 * q, u); };
       if constexpr (CAP || BIAS) {
         // P goes out, and stays here times what a gradient takes through the cap
-        if (!scores.look(x)) {
-          scores.template cap_far<64>(tS);
-          tc::tmem_ld64(tS, x);
-        }
+        scores.apply(x);
         const float* sl = bar.slope + k % a.sets * a.P;      // column c of the tile: token c / P, head c % P
         float few[4], step[4];                               // P < 4: four columns' slopes, and their tokens'
         if (BIAS) {
@@ -924,21 +920,18 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         }
         const int d0 = pt0 - key;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < COLS / 32; ++q) {
           uint32_t u[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
             float* e = x + 32 * q + c;
             const float4 l4 = nl[8 * q + c / 4];
-            const uint64_t v[2] = {tc::pack2(e[0], e[1]), tc::pack2(e[2], e[3])};
-            uint64_t y[2], z[2];
+            const uint64_t y[2] = {tc::pack2(e[0], e[1]), tc::pack2(e[2], e[3])};
+            uint64_t z[2];
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              y[w] = win::mul2(v[w], !CAP || scores.near ? scores.factor(v[w]) : scores.one);
-              z[w] = tc::add2(y[w], w ? tc::pack2(l4.z, l4.w) : tc::pack2(l4.x, l4.y));
-            }
+            for (int w = 0; w < 2; ++w) z[w] = tc::add2(y[w], w ? tc::pack2(l4.z, l4.w) : tc::pack2(l4.x, l4.y));
             if (BIAS) {
-              const int col = 64 * g + 32 * q + c;
+              const int col = COLS * g + 32 * q + c;
               const float d = static_cast<float>(d0 + (col >> a.lp));
               if (a.P >= 4) {
                 const float4 s4 = *reinterpret_cast<const float4*>(sl + (col & (a.P - 1)));
@@ -971,7 +964,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       } else {
         const uint64_t cc = tc::pack2(c1, c1);
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < COLS; c += 4) {
           const float4 l4 = nl[c / 4];
           float y0, y1;
           tc::unpack2(tc::fma2(tc::pack2(x[c], x[c + 1]), cc, tc::pack2(l4.x, l4.y)), y0, y1);
@@ -983,10 +976,10 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         }
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
+          for (int c = 0; c < COLS; ++c) x[c] = (see[c >> 5] >> (c & 31)) & 1 ? x[c] : 0.f;
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < COLS / 32; ++q) {
           uint32_t u[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) u[c] = pack_bf16(x[32 * q + 2 * c], x[32 * q + 2 * c + 1]);
@@ -995,7 +988,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       }
       // rows at positions >= len (documents: and those before the first one) become zero in both tiles once S^T and dP^T have read them: P and dS
       // are 0 there, and dV and dK must not meet what padding holds
-      if ((L < s.N && tile_end(k) > L) || (MASK != win::kWindow && pt0 < begin)) {
+      if (g < 2 && ((L < s.N && tile_end(k) > L) || (MASK != win::kWindow && pt0 < begin))) {
         ok = wait(&dp_full, k & 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         const int base = g ? M::oO + k % M::NO * M::TILE : M::oQ + sq * M::TILE;
@@ -1010,9 +1003,9 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       ok = wait(&dp_full, k & 1);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc::after_sync();
-      const uint32_t tD = tm + 128 + 64 * g + lane_off;
+      const uint32_t tD = tm + 128 + COLS * g + lane_off;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < COLS / 32; ++q) {
         float y[32];
         tc::tmem_ld32(tD + 32 * q, y);
 #pragma unroll
@@ -1042,14 +1035,16 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       tc::after_sync();
     }
     ok = !__any_sync(0xffffffffu, !ok || aborted());
-    // output: warps 0-3 dV, 4-7 dK (scaled), key r
-    const float f = g ? s.scale : 1.f;
-    const uint32_t tA = tm + 256 + D * g + lane_off;
+    // output of key r: the first half of the warps dV, the others dK (scaled); of NG / 2 threads each takes its columns
+    constexpr int NH = NG / 2;
+    const int which = g / NH, part = g % NH;
+    const float f = which ? s.scale : 1.f;
+    const uint32_t tA = tm + 256 + D * which + lane_off;
     const float nan = __int_as_float(0x7fc00000);
     if (it.slot >= 0) {
-      float* o = a.part + ((it.slot * 2 + g) * 128 + (r & ~3)) * D + 4 * (lane & 3);
+      float* o = a.part + ((it.slot * 2 + which) * 128 + (r & ~3)) * D + 4 * (lane & 3);
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = part; q < D / 32; q += NH) {
         float x[32];
         if (ok) tc::tmem_ld32(tA + 32 * q, x);
 #pragma unroll
@@ -1067,29 +1062,32 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       }
     } else if (!ok || n == 0) {
       const uint32_t v = ok ? 0u : kNaN2;
-      if (key < s.N) {
-        uint4* o = reinterpret_cast<uint4*>((g ? a.dK : a.dV) + ((static_cast<int64_t>(it.b) * s.N + key) * s.Hkv + it.kv) * D);
+      if (key < s.N && part == 0) {
+        uint4* o = reinterpret_cast<uint4*>((which ? a.dK : a.dV) + ((static_cast<int64_t>(it.b) * s.N + key) * s.Hkv + it.kv) * D);
         for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(v, v, v, v);
       }
     } else {                                                 // through V's and K's shared memory
-      const int base = g ? M::oK : M::oV;
+      const int base = which ? M::oK : M::oV;
 #pragma unroll 1
-      for (int x2 = 0; x2 < M::KB; ++x2) {
-        float x[64];
-        tc::tmem_ld64(tA + 64 * x2, x);
+      for (int x2 = part; x2 < M::KB; x2 += NH) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t u[4];
+        for (int h = 0; h < 2; ++h) {
+          float x[32];
+          tc::tmem_ld32(tA + 64 * x2 + 32 * h, x);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) u[k] = pack_bf16(f * x[8 * c + 2 * k], f * x[8 * c + 2 * k + 1]);
-          *reinterpret_cast<uint4*>(sm + base + x2 * (128 * 128) + tc::sw128(r, 8 * c)) = make_uint4(u[0], u[1], u[2], u[3]);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = pack_bf16(f * x[8 * c + 2 * k], f * x[8 * c + 2 * k + 1]);
+            *reinterpret_cast<uint4*>(sm + base + x2 * (128 * 128) + tc::sw128(r, 32 * h + 8 * c)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
         }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) {
           const int k0 = kb + 32 * (warp & 3);
           if (k0 < s.N)
-            win::tma_store4(g ? &dkmap : &dvmap, 64 * x2, it.kv, k0, it.b,
+            win::tma_store4(which ? &dkmap : &dvmap, 64 * x2, it.kv, k0, it.b,
                             tc::su32(sm + base) + x2 * (128 * 128) + (warp & 3) * (32 * 128));
           tc::bulk_commit();
         }

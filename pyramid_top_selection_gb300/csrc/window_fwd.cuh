@@ -47,7 +47,7 @@ namespace pisa {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kFwdThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;                  // log2 growth of the maximum that O is rescaled for
 constexpr uint64_t kDrainNs = 1000000000ull;   // bound of the drain waits (work already issued)
@@ -119,7 +119,7 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
 // SPLIT: one item per cluster of a.splits CTAs; otherwise a.splits is 1 and the CTAs are persistent.
 // MASK: win::kWindow, or documents (their rows come from a kernel that this one is launched behind).
 template <int D, bool SPLIT, int MASK>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
 window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kmap32,
                   const __grid_constant__ CUtensorMap vmap32, const __grid_constant__ CUtensorMap omap) {
@@ -176,6 +176,10 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   float m = neg_inf(), l = 0.f;                              // softmax threads: their row's maximum and sum
   int done = 0;                                              // key tiles that went into them
 
+  // the key tile that is taken k-th: by distance-biased scores the nearest first, which have the largest
+  constexpr bool BACK = MASK & win::kBias;
+  auto tile_at = [&](int j0, int j1, int k) { return BACK ? j1 - 1 - k : j0 + k; };
+
   if (warp >= 8) {
     win::regs_dec<88>();
     if (warp == 9) {
@@ -223,8 +227,12 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         };
         const int j0 = run_begin(it), j1 = run_end(it);
         if (j0 == j1) continue;
-        ok = load_q(0) && load_kv(128 * j0, &kmap, &kmap32) && load_q(1) && load_kv(128 * j0, &vmap, &vmap32);
-        for (int j = j0 + 1; ok && j < j1; ++j) ok = load_kv(128 * j, &kmap, &kmap32) && load_kv(128 * j, &vmap, &vmap32);
+        const int jf = tile_at(j0, j1, 0);
+        ok = load_q(0) && load_kv(128 * jf, &kmap, &kmap32) && load_q(1) && load_kv(128 * jf, &vmap, &vmap32);
+        for (int i = 1; ok && i < j1 - j0; ++i) {
+          const int j = tile_at(j0, j1, i);
+          ok = load_kv(128 * j, &kmap, &kmap32) && load_kv(128 * j, &vmap, &vmap32);
+        }
       }
       // whatever is still in flight lands before the CTA leaves
       for (int k = max(0, n_kv - M::NST); k < n_kv; ++k) tc::bar_wait(&kv_full[k % M::NST], (k / M::NST) & 1, kDrainNs);
@@ -284,23 +292,24 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           ++n_p[t];
           return true;
         };
-        bool has0 = uses(it, 0, j0), has1 = uses(it, 1, j0), acc0 = false, acc1 = false;
+        const int jf = tile_at(j0, j1, 0), end0 = BACK ? it.first[0] : it.last[0], end1 = BACK ? it.first[1] : it.last[1];   // Q's last tile
+        bool has0 = uses(it, 0, jf), has1 = uses(it, 1, jf), acc0 = false, acc1 = false;
         issued = true;
         ok = landed(n_kv) && (it.last[0] < 0 || wait(&q_full[0], n_q[0]++ & 1));
-        if (ok && has0) ok = issue_s(0, n_kv, it.last[0] == j0, !has1);
+        if (ok && has0) ok = issue_s(0, n_kv, end0 == jf, !has1);
         ok = ok && (it.last[1] < 0 || wait(&q_full[1], n_q[1]++ & 1));
-        if (ok && has1) ok = issue_s(1, n_kv, it.last[1] == j0, true);
+        if (ok && has1) ok = issue_s(1, n_kv, end1 == jf, true);
         ok = ok && landed(n_kv + 1);
         for (int j = j0; ok && j < j1; ++j) {
-          const int k = n_kv + 2 * (j - j0) + 1;
-          const bool more = !SPLIT || j + 1 < j1;            // (an item's last tile has no next one anyway)
-          const bool next0 = more && uses(it, 0, j + 1), next1 = more && uses(it, 1, j + 1);
+          const int k = n_kv + 2 * (j - j0) + 1, jn = tile_at(j0, j1, j - j0 + 1);
+          const bool more = (!SPLIT && !BACK) || j + 1 < j1; // (an item's last tile has no next one anyway)
+          const bool next0 = more && uses(it, 0, jn), next1 = more && uses(it, 1, jn);
           if (has0 && !issue_pv(0, k, acc0, !has1)) { ok = false; break; }
           if (j + 1 < j1 && !landed(k + 1)) { ok = false; break; }
-          if (next0 && !issue_s(0, k + 1, it.last[0] == j + 1, !next1)) { ok = false; break; }
+          if (next0 && !issue_s(0, k + 1, end0 == jn, !next1)) { ok = false; break; }
           if (has1 && !issue_pv(1, k, acc1, true)) { ok = false; break; }
           if (j + 1 < j1 && !landed(k + 2)) { ok = false; break; }
-          if (next1 && !issue_s(1, k + 1, it.last[1] == j + 1, true)) { ok = false; break; }
+          if (next1 && !issue_s(1, k + 1, end1 == jn, true)) { ok = false; break; }
           acc0 |= has0;
           acc1 |= has1;
           has0 = next0;
@@ -322,7 +331,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const uint32_t tS = tm + 128 * t + lane_off, tO = tm + 256 + D * t + lane_off;
     constexpr bool CAP = MASK & win::kCap, BIAS = MASK & win::kBias;
     const float c1 = CAP || BIAS ? 1.f : s.scale * kLog2e;   // (scores: powers of two already)
-    win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
+    const win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
     win::Distance dist;
     int n_s = 0, n_kv = 0;                     // key tiles done by this row tile; stages used by earlier items
     int i = 0;
@@ -346,8 +355,8 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         done = 0;
       }
       bool ok = true;
-      for (int j = j0; j < j1; ++j) {
-        const int v0 = 128 * j;
+      for (int i_k = 0; i_k < n; ++i_k) {
+        const int j = tile_at(j0, j1, i_k), v0 = 128 * j;
         if (j > j_last || (j < j_first && j >= sink_tiles)) continue;
         ok = wait(&s_full[t], n_s & 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -373,27 +382,11 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           sk = 0;
         }
         if constexpr (CAP || BIAS) {
-          if (!scores.look(x)) {
-            scores.template cap_far<128>(tS);
-            win::tmem_ld128(tS, x);
-          }
-          const float d0 = static_cast<float>(p - kb);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float b = BIAS && !dist.ahead ? dist.base(d0, 16 * q) : 0.f;
-            const uint64_t bb = tc::pack2(b, b);
-            if (!CAP || scores.near) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint64_t v = tc::pack2(x[16 * q + 2 * c], x[16 * q + 2 * c + 1]), f = scores.factor(v);
-                tc::unpack2(BIAS ? tc::fma2(v, f, bb) : win::mul2(v, f), x[16 * q + 2 * c], x[16 * q + 2 * c + 1]);
-              }
-            } else if (BIAS) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) x[16 * q + c] += b;
-            }
-          }
-          if (BIAS) {
+          if constexpr (!BIAS) {
+            scores.apply(x);
+          } else {
+            const float d0 = static_cast<float>(p - kb);
+            scores.apply(x, [&](int q) { return dist.ahead ? 0.f : dist.base(d0, 16 * q); });
             if (!dist.ahead) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
@@ -481,10 +474,13 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           }
           exps(m > neg_inf() ? m : 0.f);
         }
+        float s0, s1;
+        tc::unpack2(tc::add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         // padding's values (only the last tile can reach past the sequence) become zero before this row
         // tile's product; the other row tile writes the same zeros before its own
         if (L < s.N && kl.key(v0 + 127) >= L) {
-          const int k = n_kv + 2 * (j - j0) + 1, st = k % M::NST;
+          const int k = n_kv + 2 * i_k + 1, st = k % M::NST;
           ok = wait(&kv_full[st], (k / M::NST) & 1);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           if (v0 + r >= kl.SP && kl.key(v0 + r) >= L)
@@ -496,9 +492,6 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         tc::tmem_wait_st();
         tc::before_sync();
         tc::bar_arrive(&p_full[t]);
-        float s0, s1;
-        tc::unpack2(tc::add2(sum[0], sum[1]), s0, s1);
-        l += s0 + s1;
         ++n_s;
         ++done;
       }
@@ -506,7 +499,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       if (p0 >= s.off + s.Nq) continue;                      // a tile past the last query
       if (done) {
         ok = wait(&pv_done[t], (n_s - 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::after_sync();
       }
       if (SPLIT) continue;                                   // the cluster's results are joined below
