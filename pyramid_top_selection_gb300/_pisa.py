@@ -741,7 +741,8 @@ def doc_attn_fwd(Q, K, V, starts, shape: DocShape, prefix=None, slopes=None, ws=
 
     starts: the documents' first tokens and one past the last, [n_docs + 1] int32. prefix: leading tokens of each document
     that see one another, [n_docs] int32 (None: none). slopes: [Hq] fp32, what a score loses per token of
-    distance (None: nothing). Rows outside every document get O = 0, lse = -inf."""
+    distance (None: nothing). Rows outside every document get O = 0, lse = -inf.
+    ws: a workspace whose status word the call writes (None: a timeout shows in the outputs only)."""
     _need_docs(Q, K, V, starts, shape, prefix, slopes)
     dev = Q.device
     size = (shape.T, shape.Hq, shape.d)
@@ -753,11 +754,14 @@ def doc_attn_fwd(Q, K, V, starts, shape: DocShape, prefix=None, slopes=None, ws=
         lse = torch.empty((shape.Hq, shape.T), dtype=torch.float32, device=dev)
     else:
         _need_shaped(lse, torch.float32, (shape.Hq, shape.T), dev, "lse")
-    if ws is None:
-        ws = doc_workspace(shape, DOC_FWD, dev)
-    _need_ws(ws, dev)
+    if ws is not None:
+        _need_ws(ws, dev)
+    else:
+        n = doc_workspace_size(shape, DOC_FWD)
+        if n > 256:                      # more than the status block
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
     _on(dev, lib().pisa_doc_attn_fwd, ctypes.byref(shape), Q.data_ptr(), K.data_ptr(), V.data_ptr(), starts.data_ptr(),
-        _ptr(prefix), _ptr(slopes), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+        _ptr(prefix), _ptr(slopes), out.data_ptr(), lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
 
 

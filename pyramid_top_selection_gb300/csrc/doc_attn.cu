@@ -2,9 +2,9 @@
 //
 // A token sees one run of keys of its own document, [start, max(t, start + prefix - 1)], and spans neither begin nor end
 // before an earlier token's: so a tile of tokens sees one run as well, whether it lies in one document or over several, and the
-// window's kernels walk it with other ends (masks.cuh). A first, small kernel looks every token's document up (16 bytes a
-// token), sorts the token tiles by their keys, the most first, and clears the status word; the attention's kernel is
-// launched behind it while it runs.
+// window's kernels walk it with other ends (masks.cuh). Where there are many items, a first, small kernel looks every token's
+// document up (16 bytes a token), sorts the token tiles by their keys, the most first, and clears the status word; the
+// attention's kernel is launched behind it while it runs.
 #include <algorithm>
 
 #include "doc_rows.cuh"
@@ -33,12 +33,15 @@ int doc_fwd_by_scores(const FwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   return a.docs.slopes ? doc_fwd_launch<D, B>(a, m, st) : doc_fwd_launch<D, win::kDocs>(a, m, st);
 }
 
-// Tokens of a forward item: two row tiles.
+// Tokens of a forward item, two row tiles, and the items.
 int fwd_tile(const DocDims& s) { return 2 * 128 / win::packed_heads(s.G); }
+int64_t fwd_items(const DocDims& s) {                              // < T Hq
+  return static_cast<int64_t>((s.T + fwd_tile(s) - 1) / fwd_tile(s)) * s.Hkv * (s.G / win::packed_heads(s.G));
+}
 
 }  // namespace
 
-size_t doc_fwd_ws(const DocDims& s) { return 256 + doc_rows_bytes(s, fwd_tile(s)); }
+size_t doc_fwd_ws(const DocDims& s) { return 256 + doc_rows_bytes(s, fwd_tile(s), fwd_items(s)); }
 
 int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V, const DocMask& m, void* O, float* lse,
                    char* ws, void* stream) {
@@ -55,14 +58,18 @@ int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V
   a.tok = 128 / a.P;
   a.n_tiles = (s.T + 2 * a.tok - 1) / (2 * a.tok);
   a.n_heads = s.Hkv * (s.G / a.P);
-  a.n_items = a.n_tiles * a.n_heads;                               // < T Hq
+  a.n_items = static_cast<int>(fwd_items(s));
   a.splits = 1;
   CUtensorMap map[4];
   if (int e = win::token_map(&map[0], Q, 1, s.T, s.Hq, s.d, s.qs, a.P, a.tok)) return e;
   if (int e = win::token_map(&map[1], K, 1, s.T, s.Hkv, s.d, s.ks, 1, 128)) return e;
   if (int e = win::token_map(&map[2], V, 1, s.T, s.Hkv, s.d, s.vs, 1, 128)) return e;
   if (int e = win::token_map(&map[3], O, 1, s.T, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
-  if (int e = launch_doc_rows(s, m, 2 * a.tok, ws + 256, a.status, &a.docs, st)) return e;
+  if (int e = launch_doc_rows(s, m, 2 * a.tok, a.n_items, ws + 256, a.status, &a.docs, st)) return e;
+  if (ws && !a.docs.bounds) {
+    cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+    if (e != cudaSuccess) return e;
+  }
   return s.d == 128 ? doc_fwd_by_scores<128>(a, map, st) : doc_fwd_by_scores<64>(a, map, st);
 }
 

@@ -1,5 +1,5 @@
-// The documents' rows on the device: every token's document and the order of the token tiles (masks.cuh), as the forward
-// and backward kernels take them.
+// The documents' rows laid out on the device: every token's document and the order of the token tiles (masks.cuh), where the
+// forward and backward kernels want them.
 #pragma once
 
 #include "device.cuh"
@@ -15,10 +15,10 @@ namespace {
 constexpr int kRowThreads = 512, kStarts = 4096, kBuckets = 256;
 
 struct DocRowsArgs {
-  int32_t T, n_docs, tile, n_tiles, shift;     // tile: tokens of one; shift: key tiles of a bucket of the order, as a power of two
-  const int32_t *starts, *prefix;
+  win::DocRows d;
+  int32_t tile, n_tiles, shift;                // tokens of a tile; key tiles of a bucket of the order, as a power of two
   int4* bounds;
-  int32_t *order, *status;
+  int32_t *order, *status;                     // status: the workspace's word, cleared
 };
 
 // Block 0 sorts the tiles, the others look tokens up. The starts are held in shared memory where they fit.
@@ -26,41 +26,25 @@ __global__ void __launch_bounds__(kRowThreads) doc_rows_kernel(const DocRowsArgs
   __shared__ int32_t s_starts[kStarts];
   __shared__ int32_t s_count[kBuckets];
   win::launch_dependents();
-  const bool held = a.n_docs < kStarts;
+  const win::DocRows& d = a.d;
+  const bool held = d.n_docs < kStarts;
   if (held)
-    for (int k = threadIdx.x; k <= a.n_docs; k += kRowThreads) s_starts[k] = a.starts[k];
+    for (int k = threadIdx.x; k <= d.n_docs; k += kRowThreads) s_starts[k] = d.starts[k];
   if (blockIdx.x == 0) {
     for (int k = threadIdx.x; k < kBuckets; k += kRowThreads) s_count[k] = 0;
     if (threadIdx.x == 0) *a.status = 0;
   }
   __syncthreads();
-  auto start_of = [&](int m) { return held ? s_starts[m] : a.starts[m]; };
-  auto clamped = [&](int v) { return max(0, min(v, a.T)); };
-  auto bounds_of = [&](int t) {
-    int lo = 0, hi = a.n_docs + 1;                     // starts below lo are <= t, those from hi on are > t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (start_of(mid) <= t) lo = mid + 1; else hi = mid;
-    }
-    int4 b;
-    if (lo == 0 || lo > a.n_docs) {
-      b.x = b.y = b.z = clamped(start_of(lo == 0 ? 0 : a.n_docs));
-    } else {
-      b.x = clamped(start_of(lo - 1));
-      b.y = clamped(start_of(lo));
-      b.z = a.prefix ? b.x + max(0, min(a.prefix[lo - 1], b.y - b.x)) : b.x;
-    }
-    b.w = 0;
-    return b;
-  };
+  auto start_of = [&](int m) { return held ? s_starts[m] : d.starts[m]; };
+  auto bounds_of = [&](int t) { return d.search(t, start_of); };
   if (blockIdx.x > 0) {
     const int t = static_cast<int>((blockIdx.x - 1) * kRowThreads + threadIdx.x);
-    if (t < a.T) a.bounds[t] = bounds_of(t);
-    if (t == a.T) a.bounds[t] = make_int4(clamped(start_of(0)), clamped(start_of(a.n_docs)), 0, 0);
+    if (t < d.T) a.bounds[t] = bounds_of(t);
+    if (t == d.T) a.bounds[t] = make_int4(d.clamped(start_of(0)), d.clamped(start_of(d.n_docs)), 0, 0);
     return;
   }
   auto bucket_of = [&](int k) {                        // key tiles of token tile k
-    const int t1 = min(a.T, (k + 1) * a.tile) - 1;
+    const int t1 = min(d.T, (k + 1) * a.tile) - 1;
     const int4 p = bounds_of(k * a.tile), q = bounds_of(t1);
     const int last = t1 < q.y ? max(t1, q.z - 1) : q.y - 1;
     return kBuckets - 1 - min(kBuckets - 1, max(0, (last - p.x + 128) >> 7) >> a.shift);
@@ -87,25 +71,30 @@ __global__ void __launch_bounds__(kRowThreads) doc_rows_kernel(const DocRowsArgs
 
 inline size_t doc_bounds_bytes(const DocDims& s) { return (static_cast<size_t>(s.T + 1) * 16 + 255) / 256 * 256; }
 
+// Whether a kernel of `items` items wants the rows laid out: with one item a CTA, or one document (whose tiles are in
+// order as they are), the kernel before it would cost more than the searches (300 tokens of 4 heads: 12.2 us with, 8.8
+// without).
+inline bool doc_rows_wanted(const DocDims& s, int64_t items) { return s.n_docs > 1 && items > win::kPlanSms; }
+
 // Bytes of the rows with token tiles of `tile` tokens.
-inline size_t doc_rows_bytes(const DocDims& s, int tile) {
-  return doc_bounds_bytes(s) + static_cast<size_t>((s.T + tile - 1) / tile) * 4;
+inline size_t doc_rows_bytes(const DocDims& s, int tile, int64_t items) {
+  return doc_rows_wanted(s, items) ? doc_bounds_bytes(s) + static_cast<size_t>((s.T + tile - 1) / tile) * 4 : 0;
 }
 
-inline int launch_doc_rows(const DocDims& s, const DocMask& m, int tile, char* ws, int32_t* status, win::DocRows* out,
+inline int launch_doc_rows(const DocDims& s, const DocMask& m, int tile, int64_t items, char* ws, int32_t* status, win::DocRows* out,
                            cudaStream_t st) {
+  *out = win::DocRows{nullptr, nullptr, m.slopes, s.cap, s.T, s.n_docs, m.starts, m.prefix};
+  if (!doc_rows_wanted(s, items)) return 0;
   DocRowsArgs a{};
-  a.T = s.T;
-  a.n_docs = s.n_docs;
+  a.d = *out;
   a.tile = tile;
   a.n_tiles = (s.T + tile - 1) / tile;
   while ((s.max_len / 128 + 3) >> a.shift >= kBuckets) ++a.shift;
-  a.starts = m.starts;
-  a.prefix = m.prefix;
   a.bounds = reinterpret_cast<int4*>(ws);
   a.order = reinterpret_cast<int32_t*>(ws + doc_bounds_bytes(s));
   a.status = status;
-  *out = {a.bounds, a.order, m.slopes, s.cap};
+  out->bounds = a.bounds;
+  out->order = a.order;
   ProfScope ps(st, "doc_rows");
   doc_rows_kernel<<<2 + s.T / kRowThreads, kRowThreads, 0, st>>>(a);
   return cudaGetLastError();

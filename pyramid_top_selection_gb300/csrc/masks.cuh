@@ -12,13 +12,42 @@ namespace win {
 // (flags: kDocs, with capped scores, with scores that lose a slope times the distance)
 constexpr int kWindow = 0, kDocs = 1, kCap = 2, kBias = 4;
 
-// Documents on the device, as the prologue (doc_attn.cu) lays them out.
+// Documents on the device. Where a kernel's items are many, a kernel before it (doc_rows.cuh) lays their rows out; else every
+// look-up is a search among the starts.
 struct DocRows {
-  const int4* bounds;      // [T + 1]: of a token: its document's tokens [x, y), one past its prefix z (x = y = z past the token: none).
-                           // [T]: x the first document's first token, y one past the last one's
-  const int32_t* order;    // token tiles, those with the most keys first
+  const int4* bounds;      // [T + 1], of() of every token, or NULL
+  const int32_t* order;    // token tiles, those with the most keys first (NULL with bounds)
   const float* slopes;     // per query head, or NULL
   float cap;               // 0: none
+  int32_t T, n_docs;
+  const int32_t *starts, *prefix;
+
+  // What is known of token t: its document's tokens [x, y), one past its prefix z (x = y = z, at the first document's
+  // first token or one past the last one's: none). Of t = T: x the first document's first token, y one past the last one's.
+  __device__ __forceinline__ int4 of(int t) const {
+    if (bounds) return bounds[t];
+    if (t == T) return make_int4(clamped(starts[0]), clamped(starts[n_docs]), 0, 0);
+    return search(t, [&](int m) { return __ldg(starts + m); });
+  }
+  __device__ __forceinline__ int clamped(int v) const { return max(0, min(v, T)); }
+  template <class S>
+  __device__ __forceinline__ int4 search(int t, S start_of) const {
+    int lo = 0, hi = n_docs + 1;                       // starts below lo are <= t, those from hi on are > t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (start_of(mid) <= t) lo = mid + 1; else hi = mid;
+    }
+    int4 b;
+    if (lo == 0 || lo > n_docs) {
+      b.x = b.y = b.z = clamped(start_of(lo == 0 ? 0 : n_docs));
+    } else {
+      b.x = clamped(start_of(lo - 1));
+      b.y = clamped(start_of(lo));
+      b.z = prefix ? b.x + max(0, min(__ldg(prefix + lo - 1), b.y - b.x)) : b.x;
+    }
+    b.w = 0;
+    return b;
+  }
 };
 
 // The keys [lo, hi] that token t sees (hi < lo: none).
@@ -26,7 +55,7 @@ struct DocSpan {
   int lo, hi;
   __device__ __forceinline__ DocSpan() : lo(0), hi(-1) {}
   __device__ __forceinline__ DocSpan(const DocRows& d, int t) {
-    const int4 b = d.bounds[t];
+    const int4 b = d.of(t);
     lo = b.x;
     hi = t < b.y ? max(t, b.z - 1) : -1;
   }
@@ -37,7 +66,7 @@ struct DocRange {
   int lo, hi;
   __device__ __forceinline__ DocRange(const DocRows& d, int t0, int t1) : lo(0), hi(-1) {
     if (t0 >= t1) return;
-    const int4 a = d.bounds[t0], z = d.bounds[t1 - 1];
+    const int4 a = d.of(t0), z = d.of(t1 - 1);
     lo = a.x;
     hi = t1 - 1 < z.y ? max(t1 - 1, z.z - 1) : z.y - 1;
   }
@@ -48,7 +77,7 @@ struct DocSeen {
   int first, end;
   __device__ __forceinline__ DocSeen(const DocRows& d, int j, int T) : first(0), end(0) {
     if (j >= T) return;
-    const int4 b = d.bounds[j];
+    const int4 b = d.of(j);
     if (j >= b.y || j < b.x) return;
     first = j < b.z ? b.x : j;
     end = b.y;

@@ -83,7 +83,7 @@ struct FwdArgs {
 template <int MASK>
 __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
   const WinDims& s = a.s;
-  const int tile = MASK == win::kWindow ? a.n_tiles - 1 - w / a.n_heads : a.docs.order[w / a.n_heads], hh = w % a.n_heads, sets = s.G / a.P;
+  const int k = w / a.n_heads, tile = MASK != win::kWindow && a.docs.order ? a.docs.order[k] : a.n_tiles - 1 - k, hh = w % a.n_heads, sets = s.G / a.P;
   win::Item it;
   it.b = hh / (s.Hkv * sets);
   it.kv = hh / sets % s.Hkv;
@@ -92,7 +92,7 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
   if constexpr (MASK != win::kWindow) {
     const int t1 = min(s.Nq, it.t0 + a.tok), t2 = min(s.Nq, it.t0 + 2 * a.tok);
     const win::DocRange all(a.docs, it.t0, t2), r0(a.docs, it.t0, t1), r1(a.docs, t1, t2);
-    it.L = a.docs.bounds[s.N].y;
+    it.L = a.docs.of(s.N).y;
     it.lo = all.lo;
     it.SP = 0;
     it.n = all.hi < all.lo ? 0 : (all.hi - all.lo + 128) >> 7;

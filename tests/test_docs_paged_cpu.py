@@ -85,7 +85,8 @@ def _overlaps(call, names, sizes, written, may_be=()):
 
 
 def _doc_calls():
-    L, s = pisa.lib(), pisa.make_doc_shape(T=100, Hq=4, Hkv=4, d=64, n_docs=3)
+    # 4 heads of 12000 tokens: more items than the GPU has SMs, so that the forward has a workspace of its own
+    L, s = pisa.lib(), pisa.make_doc_shape(T=12000, Hq=4, Hkv=4, d=64, n_docs=300)
     nf, nb = (pisa.doc_workspace_size(s, op) for op in (pisa.DOC_FWD, pisa.DOC_BWD))
     fwd = ["Q", "K", "V", "starts", "prefix", "slopes", "O", "lse", "workspace"]
     bwd = ["Q", "K", "V", "O", "lse", "dO", "starts", "prefix", "slopes", "dQ", "dK", "dV", "workspace"]
@@ -95,8 +96,8 @@ def _doc_calls():
 
 def test_overlaps_of_the_documents_calls_are_refused():
     fwd, call_f, nf, bwd, call_b, nb = _doc_calls()
-    t = 100 * 4 * 64 * 2
-    size = dict(Q=t, K=t, V=t, O=t, dO=t, dQ=t, dK=t, dV=t, lse=1600, starts=16, prefix=12, slopes=16)
+    t = 12000 * 4 * 64 * 2
+    size = dict(Q=t, K=t, V=t, O=t, dO=t, dQ=t, dK=t, dV=t, lse=192000, starts=1204, prefix=1200, slopes=16)
     _overlaps(call_f, fwd, size | dict(workspace=nf), ["O", "lse", "workspace"])
     _overlaps(call_b, bwd, size | dict(workspace=nb), ["dQ", "dK", "dV", "workspace"])
 
