@@ -430,7 +430,7 @@ enum { PISA_DOC_FWD = 0, PISA_DOC_BWD = 1 };
 int pisa_doc_workspace_size(const pisa_doc_shape_t* shape, int op, size_t* bytes);
 
 /* O and lse. A bounded wait that gives up poisons the rows it leaves unfinished (O = NaN, lse = NaN) and sets
- * PISA_STATUS_TIMEOUT. Workspace: PISA_DOC_FWD; where that is the status block only (256 bytes: one document, or few rows),
+ * PISA_STATUS_TIMEOUT. Workspace: PISA_DOC_FWD; where that is the status block only (256 bytes: few rows),
  * NULL (with ws_bytes 0) leaves it out, and the poisoned outputs alone tell. */
 int pisa_doc_attn_fwd(const pisa_doc_shape_t* shape, const void* Q, const void* K, const void* V,
                       const int32_t* starts, const int32_t* prefix, const float* slopes, void* O, float* lse,

@@ -26,11 +26,11 @@ int doc_fwd_launch(const FwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
   return cudaLaunchKernelEx(&b.cfg, window_fwd_kernel<D, false, MASK>, a, m[0], m[1], m[2], m[1], m[2], m[3]);
 }
 
-template <int D>
+template <int D, int SEARCH>
 int doc_fwd_by_scores(const FwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
-  constexpr int C = win::kDocs | win::kCap, B = win::kDocs | win::kBias;
+  constexpr int N = win::kDocs | SEARCH, C = N | win::kCap, B = N | win::kBias;
   if (a.docs.cap > 0.f) return a.docs.slopes ? doc_fwd_launch<D, C | B>(a, m, st) : doc_fwd_launch<D, C>(a, m, st);
-  return a.docs.slopes ? doc_fwd_launch<D, B>(a, m, st) : doc_fwd_launch<D, win::kDocs>(a, m, st);
+  return a.docs.slopes ? doc_fwd_launch<D, B>(a, m, st) : doc_fwd_launch<D, N>(a, m, st);
 }
 
 // Tokens of a forward item, two row tiles, and the items.
@@ -39,9 +39,13 @@ int64_t fwd_items(const DocDims& s) {                              // < T Hq
   return static_cast<int64_t>((s.T + fwd_tile(s) - 1) / fwd_tile(s)) * s.Hkv * (s.G / win::packed_heads(s.G));
 }
 
+// With no more than an item a CTA the kernel that lays the rows out would cost more than their searches (300 tokens of 4
+// heads: 12.2 us with, 9 without, and 25.6 and 17.6 us a call).
+bool rows_laid_out(const DocDims& s) { return fwd_items(s) > win::kPlanSms; }
+
 }  // namespace
 
-size_t doc_fwd_ws(const DocDims& s) { return 256 + doc_rows_bytes(s, fwd_tile(s), fwd_items(s)); }
+size_t doc_fwd_ws(const DocDims& s) { return 256 + (rows_laid_out(s) ? doc_rows_bytes(s, fwd_tile(s)) : 0); }
 
 int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V, const DocMask& m, void* O, float* lse,
                    char* ws, void* stream) {
@@ -65,12 +69,16 @@ int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V
   if (int e = win::token_map(&map[1], K, 1, s.T, s.Hkv, s.d, s.ks, 1, 128)) return e;
   if (int e = win::token_map(&map[2], V, 1, s.T, s.Hkv, s.d, s.vs, 1, 128)) return e;
   if (int e = win::token_map(&map[3], O, 1, s.T, s.Hq, s.d, static_cast<int64_t>(s.Hq) * s.d, a.P, 32 / a.P)) return e;
-  if (int e = launch_doc_rows(s, m, 2 * a.tok, a.n_items, ws + 256, a.status, &a.docs, st)) return e;
-  if (ws && !a.docs.bounds) {
-    cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
-    if (e != cudaSuccess) return e;
+  if (!rows_laid_out(s)) {
+    a.docs = doc_rows_searched(s, m);
+    if (ws) {
+      cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
+      if (e != cudaSuccess) return e;
+    }
+    return s.d == 128 ? doc_fwd_by_scores<128, win::kSearch>(a, map, st) : doc_fwd_by_scores<64, win::kSearch>(a, map, st);
   }
-  return s.d == 128 ? doc_fwd_by_scores<128>(a, map, st) : doc_fwd_by_scores<64>(a, map, st);
+  if (int e = launch_doc_rows(s, m, 2 * a.tok, ws + 256, a.status, &a.docs, st)) return e;
+  return s.d == 128 ? doc_fwd_by_scores<128, 0>(a, map, st) : doc_fwd_by_scores<64, 0>(a, map, st);
 }
 
 }  // namespace pisa

@@ -47,12 +47,7 @@ int doc_bwd_by_scores(const BwdArgs& a, const CUtensorMap* m, cudaStream_t st) {
 
 // The window's backward workspace, then the documents' rows with tiles of `tok` tokens.
 size_t rows_at(const DocDims& s) { return (window_bwd_ws(doc_as_window(s)).total + 255) / 256 * 256; }
-size_t row_bytes(const DocDims& s) {
-  BwdArgs a{};
-  a.s = doc_as_window(s);
-  plan(a);
-  return doc_rows_bytes(s, a.tok, a.n_items);
-}
+int row_tile(const DocDims& s) { return 128 / win::packed_heads(s.G); }
 
 template <int D>
 int doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const void* O, const float* lse, const void* dO,
@@ -81,7 +76,7 @@ int doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const
   if (int e = win::token_map(&map[4], dK, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
   if (int e = win::token_map(&map[5], dV, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
   if (int e = win::token_map(&map[6], O, 1, s.T, s.Hq, s.d, hd, a.P, a.tok)) return e;
-  if (int e = launch_doc_rows(s, m, a.tok, a.n_items, ws + rows_at(s), a.status, &a.docs, st)) return e;
+  if (int e = launch_doc_rows(s, m, a.tok, ws + rows_at(s), a.status, &a.docs, st)) return e;
   return doc_bwd_by_scores<D>(a, map, st);
 }
 

@@ -71,28 +71,26 @@ __global__ void __launch_bounds__(kRowThreads) doc_rows_kernel(const DocRowsArgs
 
 inline size_t doc_bounds_bytes(const DocDims& s) { return (static_cast<size_t>(s.T + 1) * 16 + 255) / 256 * 256; }
 
-// Whether a kernel of `items` items wants the rows laid out: with one item a CTA, or one document (whose tiles are in
-// order as they are), the kernel before it would cost more than the searches (300 tokens of 4 heads: 12.2 us with, 8.8
-// without).
-inline bool doc_rows_wanted(const DocDims& s, int64_t items) { return s.n_docs > 1 && items > win::kPlanSms; }
-
 // Bytes of the rows with token tiles of `tile` tokens.
-inline size_t doc_rows_bytes(const DocDims& s, int tile, int64_t items) {
-  return doc_rows_wanted(s, items) ? doc_bounds_bytes(s) + static_cast<size_t>((s.T + tile - 1) / tile) * 4 : 0;
+inline size_t doc_rows_bytes(const DocDims& s, int tile) {
+  return doc_bounds_bytes(s) + static_cast<size_t>((s.T + tile - 1) / tile) * 4;
 }
 
-inline int launch_doc_rows(const DocDims& s, const DocMask& m, int tile, int64_t items, char* ws, int32_t* status, win::DocRows* out,
+inline win::DocRows doc_rows_searched(const DocDims& s, const DocMask& m) {
+  return {nullptr, nullptr, m.slopes, s.cap, s.T, s.n_docs, m.starts, m.prefix};
+}
+
+inline int launch_doc_rows(const DocDims& s, const DocMask& m, int tile, char* ws, int32_t* status, win::DocRows* out,
                            cudaStream_t st) {
-  *out = win::DocRows{nullptr, nullptr, m.slopes, s.cap, s.T, s.n_docs, m.starts, m.prefix};
-  if (!doc_rows_wanted(s, items)) return 0;
   DocRowsArgs a{};
-  a.d = *out;
+  a.d = doc_rows_searched(s, m);
   a.tile = tile;
   a.n_tiles = (s.T + tile - 1) / tile;
   while ((s.max_len / 128 + 3) >> a.shift >= kBuckets) ++a.shift;
   a.bounds = reinterpret_cast<int4*>(ws);
   a.order = reinterpret_cast<int32_t*>(ws + doc_bounds_bytes(s));
   a.status = status;
+  *out = a.d;
   out->bounds = a.bounds;
   out->order = a.order;
   ProfScope ps(st, "doc_rows");

@@ -11,12 +11,14 @@ namespace win {
 
 // (flags: kDocs, with capped scores, with scores that lose a slope times the distance)
 constexpr int kWindow = 0, kDocs = 1, kCap = 2, kBias = 4;
+// (and kSearch: documents looked up among the starts, not in a table. A flag, for the search in line cost the capped forward of
+// long documents 7 % of its time, whether it was run or not.)
+constexpr int kSearch = 8;
 
-// Documents on the device. Where a kernel's items are many, a kernel before it (doc_rows.cuh) lays their rows out; else every
-// look-up is a search among the starts.
+// Documents on the device. Where there are many tokens, a kernel laid their rows out before (doc_rows.cuh).
 struct DocRows {
-  const int4* bounds;      // [T + 1], of() of every token, or NULL
-  const int32_t* order;    // token tiles, those with the most keys first (NULL with bounds)
+  const int4* bounds;      // [T + 1], of() of every token; not with kSearch
+  const int32_t* order;    // token tiles, those with the most keys first; not with kSearch
   const float* slopes;     // per query head, or NULL
   float cap;               // 0: none
   int32_t T, n_docs;
@@ -24,10 +26,14 @@ struct DocRows {
 
   // What is known of token t: its document's tokens [x, y), one past its prefix z (x = y = z, at the first document's
   // first token or one past the last one's: none). Of t = T: x the first document's first token, y one past the last one's.
+  template <int MASK>
   __device__ __forceinline__ int4 of(int t) const {
-    if (bounds) return bounds[t];
-    if (t == T) return make_int4(clamped(starts[0]), clamped(starts[n_docs]), 0, 0);
-    return search(t, [&](int m) { return __ldg(starts + m); });
+    if constexpr (MASK & kSearch) {
+      if (t == T) return make_int4(clamped(starts[0]), clamped(starts[n_docs]), 0, 0);
+      return search(t, [&](int m) { return __ldg(starts + m); });
+    } else {
+      return bounds[t];
+    }
   }
   __device__ __forceinline__ int clamped(int v) const { return max(0, min(v, T)); }
   template <class S>
@@ -51,22 +57,24 @@ struct DocRows {
 };
 
 // The keys [lo, hi] that token t sees (hi < lo: none).
+template <int MASK>
 struct DocSpan {
   int lo, hi;
   __device__ __forceinline__ DocSpan() : lo(0), hi(-1) {}
   __device__ __forceinline__ DocSpan(const DocRows& d, int t) {
-    const int4 b = d.of(t);
+    const int4 b = d.of<MASK>(t);
     lo = b.x;
     hi = t < b.y ? max(t, b.z - 1) : -1;
   }
 };
 
 // The keys [lo, hi] that some token of [t0, t1) sees: spans neither begin nor end before an earlier token's.
+template <int MASK>
 struct DocRange {
   int lo, hi;
   __device__ __forceinline__ DocRange(const DocRows& d, int t0, int t1) : lo(0), hi(-1) {
     if (t0 >= t1) return;
-    const int4 a = d.of(t0), z = d.of(t1 - 1);
+    const int4 a = d.of<MASK>(t0), z = d.of<MASK>(t1 - 1);
     lo = a.x;
     hi = t1 - 1 < z.y ? max(t1 - 1, z.z - 1) : z.y - 1;
   }
@@ -77,7 +85,7 @@ struct DocSeen {
   int first, end;
   __device__ __forceinline__ DocSeen(const DocRows& d, int j, int T) : first(0), end(0) {
     if (j >= T) return;
-    const int4 b = d.of(j);
+    const int4 b = d.bounds[j];
     if (j >= b.y || j < b.x) return;
     first = j < b.z ? b.x : j;
     end = b.y;

@@ -61,7 +61,7 @@ struct BwdArgs {
 // One past the last valid token of sequence b, or of the documents.
 template <int MASK>
 __device__ __forceinline__ int end_of(const BwdArgs& a, int b) {
-  return MASK == win::kWindow ? win::valid_len(a.len, b, a.s.N) : a.docs.of(a.s.N).y;
+  return MASK == win::kWindow ? win::valid_len(a.len, b, a.s.N) : a.docs.bounds[a.s.N].y;
 }
 
 // COLS consecutive fp32 columns of this thread's TMEM lane.
@@ -82,7 +82,7 @@ struct DqSmem {
 template <int MASK>
 __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
   const WinDims& s = a.s;
-  const int k = w / a.n_heads, tile = MASK != win::kWindow && a.docs.order ? a.docs.order[k] : a.n_tiles - 1 - k, hh = w % a.n_heads, set = hh % a.sets;
+  const int tile = MASK == win::kWindow ? a.n_tiles - 1 - w / a.n_heads : a.docs.order[w / a.n_heads], hh = w % a.n_heads, set = hh % a.sets;
   win::Item it;
   it.b = hh / (s.Hkv * a.sets);
   it.kv = hh / a.sets % s.Hkv;
@@ -95,7 +95,7 @@ __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
     it.SP = kl.SP;
     it.n = (kl.n_cols + 127) >> 7;
   } else {
-    const win::DocRange r(a.docs, it.t0, min(s.Nq, it.t0 + a.tok));
+    const win::DocRange<MASK> r(a.docs, it.t0, min(s.Nq, it.t0 + a.tok));
     it.lo = r.lo;
     it.SP = 0;
     it.n = r.hi < r.lo ? 0 : (r.hi - r.lo + 128) >> 7;
@@ -177,10 +177,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
   tc::before_sync();
   __syncthreads();
   tc::after_sync();
-  if (MASK != win::kWindow) {
-    win::grid_wait();                                        // before the next kernel may start: it reads the documents' rows, too
-    if (tid == 0 && blockIdx.x == 0) *a.status = 0;
-  }
+  if (MASK != win::kWindow) win::grid_wait();                // before the next kernel may start: it reads the documents' rows, too
   if (tid == 0) win::launch_dependents();
   const uint32_t tm = tmem_base;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return win::wait(bar, parity, &s_abort, a.wait_ns); };
@@ -385,8 +382,8 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
         continue;
       }
       bool ok = true;
-      win::DocSpan span;
-      if (MASK != win::kWindow && i < s.Nq) span = win::DocSpan(a.docs, i);
+      win::DocSpan<MASK> span;
+      if (MASK != win::kWindow && i < s.Nq) span = win::DocSpan<MASK>(a.docs, i);
       if (BIAS) dist.set(__ldg(a.docs.slopes + h) * kLog2e, span.hi > p);
       // x = P (through: times what a gradient takes through the cap), y = dP of key tile j; see: the visible columns,
       // where some are not
@@ -632,7 +629,7 @@ struct TokenRange {
   // Documents: from the first token that sees the tile's first key to the last one of the last key's document.
   __device__ TokenRange(const win::DocRows& d, int T, int tok, int kt) {
     const int kb = 128 * kt;
-    const int4 a = d.of(kb), z = d.of(min(kb + 127, T - 1));
+    const int4 a = d.bounds[kb], z = d.bounds[min(kb + 127, T - 1)];
     const int first = kb >= a.x && kb < a.y && kb >= a.z ? kb : a.x, last = z.y;
     i0 = first & ~3;
     n = last > first ? (last - i0 + tok - 1) / tok : 0;
@@ -699,7 +696,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
 
   const DkvItem it(a, blockIdx.x);
   const int kb = 128 * it.kt, L = end_of<MASK>(a, it.b);
-  const int begin = MASK == win::kWindow ? 0 : a.docs.of(s.N).x;     // the first document's first token
+  const int begin = MASK == win::kWindow ? 0 : a.docs.bounds[s.N].x;     // the first document's first token
   const TokenRange tr = tokens_of<MASK>(a, L, it.kt);
   // this chunk's row tiles: token tile n / sets, head set n % sets
   const int tile0 = it.c * it.ct, own = MASK == win::kWindow ? max(0, min(it.ct, tr.n - tile0)) : chunk_tiles(tr.n, it.c, it.ct, a.nck);

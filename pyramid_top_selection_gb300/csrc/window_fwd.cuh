@@ -83,7 +83,7 @@ struct FwdArgs {
 template <int MASK>
 __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
   const WinDims& s = a.s;
-  const int k = w / a.n_heads, tile = MASK != win::kWindow && a.docs.order ? a.docs.order[k] : a.n_tiles - 1 - k, hh = w % a.n_heads, sets = s.G / a.P;
+  const int k = w / a.n_heads, tile = MASK == win::kWindow || (MASK & win::kSearch) ? a.n_tiles - 1 - k : a.docs.order[k], hh = w % a.n_heads, sets = s.G / a.P;
   win::Item it;
   it.b = hh / (s.Hkv * sets);
   it.kv = hh / sets % s.Hkv;
@@ -91,8 +91,8 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
   it.t0 = tile * 2 * a.tok;
   if constexpr (MASK != win::kWindow) {
     const int t1 = min(s.Nq, it.t0 + a.tok), t2 = min(s.Nq, it.t0 + 2 * a.tok);
-    const win::DocRange all(a.docs, it.t0, t2), r0(a.docs, it.t0, t1), r1(a.docs, t1, t2);
-    it.L = a.docs.of(s.N).y;
+    const win::DocRange<MASK> all(a.docs, it.t0, t2), r0(a.docs, it.t0, t1), r1(a.docs, t1, t2);
+    it.L = a.docs.of<MASK>(s.N).y;
     it.lo = all.lo;
     it.SP = 0;
     it.n = all.hi < all.lo ? 0 : (all.hi - all.lo + 128) >> 7;
@@ -346,8 +346,8 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const int j_first = t ? it.first[1] : it.first[0], j_last = t ? it.last[1] : it.last[0];
       const int p = p0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
       const bool row = p < p1 && p < L;
-      win::DocSpan span;
-      if (MASK != win::kWindow && p < p1) span = win::DocSpan(a.docs, p);
+      win::DocSpan<MASK> span;
+      if (MASK != win::kWindow && p < p1) span = win::DocSpan<MASK>(a.docs, p);
       if (BIAS) dist.set(__ldg(a.docs.slopes + h) * kLog2e, span.hi > p);
       if (!SPLIT) {
         m = neg_inf();
