@@ -6,15 +6,16 @@
 // e2m1 value nearest to v / s; that quotient is v times 1 / s, corrected by its remainder, so that ties come out as
 // ties.
 //
-// Bound: memory. One warp takes one token and runs over its heads (queries, keys, values) in steps of four rounds of 512
-// bytes that arrive by cp.async in the warp's ring, two steps ahead of the arithmetic; the slots of 32 tokens
-// of a warp are looked up at once, a lane each. With few tokens the heads are split over warps.
+// Bound: memory. One warp takes one token and runs over its queries, then its keys and values as one list of rows, in steps
+// of four rounds of 512 bytes that arrive by cp.async in the warp's ring, two steps ahead of the arithmetic; the slots
+// of 32 tokens of a warp are looked up at once, a lane each. With few tokens a warp takes a step.
 #include <algorithm>
 
 #include "internal.h"
 #include "paged.cuh"
 #include "profile.h"
 #include "rope.cuh"
+#include "scores.cuh"
 
 namespace pisa {
 
@@ -29,65 +30,45 @@ constexpr int kWarps = 8;
 constexpr int kBlocks = 3;       // blocks an SM holds, by registers
 constexpr int kRound = 4;        // row rounds (512 bytes a warp) of a step
 constexpr int kAhead = 3;        // steps in a warp's ring: two in flight, one in use
+constexpr int kStart = 2;        // a unit's start, in steps
+
+// v / by from r, nearly 1 / by: the quotient corrected by its remainder, right to the last bit but in the rarest cases, and
+// exact where v / by is (so are all ties). Pairs alike. With r = 0 (by = 0): 0.
+__device__ __forceinline__ float over(float v, float by, float r) {
+  const float q = v * r;
+  return fmaf(r, fmaf(-q, by, v), q);
+}
+__device__ __forceinline__ uint64_t over2(uint64_t v, float by, float r) {
+  const uint64_t rr = tc::pack2(r, r), q = mul2(v, rr);
+  return tc::fma2(rr, tc::fma2(q, tc::pack2(-by, -by), v), q);
+}
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 struct AppendArgs {
   PagedDims s;
   RopeDims t;
   PagedCache c;
-  const bf16* x[3];              // Q, K, V
-  int64_t stride[3];
-  int32_t heads[3];              // rows of a token: Hq (0 without queries), Hkv, Hkv
+  const bf16 *Q, *K, *V;
+  int64_t vs;
   const float* w[2];
   const float* inv_freq;
   const int32_t *table, *seq, *pos;
   bf16* Qr;
   int32_t* status;
-  int32_t heads_per_warp, chunks;
-  int64_t tokens;
+  int32_t q_steps, steps;        // a token's steps: its queries' (0 without), then its keys' and values'
+  int32_t per, parts;            // steps of a unit of work, units of a token
+  int64_t units;
 };
 
-// A warp's place: unit of work (token * chunks + chunk of heads), part (Q, K or V), the step's first head, one past
-// the last of the unit's heads in this part.
+// A step of a token: rows [h, end) of its queries (part 0), or of its keys and values (part 1: row r is key r, or value
+// r - Hkv).
 struct Place {
-  int64_t wk;
-  int part, h, end;
-};
-
-template <int ROWS>
-struct Steps {
-  const AppendArgs& a;
-  int64_t work, step;
-  __device__ __forceinline__ Steps(const AppendArgs& args)
-      : a(args), work(args.tokens * args.chunks), step(static_cast<int64_t>(gridDim.x) * kWarps) {}
-  __device__ __forceinline__ int64_t token(const Place& p) const { return a.chunks == 1 ? p.wk : p.wk / a.chunks; }
-  // the part from `part` on that has heads of the unit's, or the next unit
-  __device__ __forceinline__ void seek(Place& p) const {
-    const int beg = a.chunks == 1 ? 0 : static_cast<int>(p.wk % a.chunks) * a.heads_per_warp, end = beg + a.heads_per_warp;
-    int at = 0;
-    for (int k = 0; k < 3; ++k) {
-      const int lo = max(beg - at, 0), hi = min(end - at, a.heads[k]);
-      at += a.heads[k];
-      if (k >= p.part && lo < hi) {
-        p.part = k;
-        p.h = lo;
-        p.end = hi;
-        return;
-      }
-    }
-    p.wk += step;
-    p.part = -1;
-  }
-  __device__ __forceinline__ void open(Place& p) const {
-    p.part = 0;
-    seek(p);                     // a unit has heads
-  }
-  __device__ __forceinline__ void next(Place& p) const {
-    p.h += ROWS;
-    if (p.h < p.end) return;
-    ++p.part;
-    seek(p);
-    if (p.part < 0) open(p);
-  }
+  int64_t unit, token;
+  int step, end;                 // end: of the unit's steps
 };
 
 template <int D, bool IL, bool NORM, bool FOUR>
@@ -99,19 +80,38 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPR, e = 8 * (lane % LPR);
   unsigned char* ring = ring_all + warp * kAhead * STEP;
   const Lane<D, IL> L(lane, a.t.rot, a.inv_freq, table[warp]);
-  const Steps<ROWS> steps(a);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  auto open = [&](Place& p) {
+    p.token = a.parts == 1 ? p.unit : p.unit / a.parts;
+    p.step = static_cast<int>(p.unit - p.token * a.parts) * a.per;
+    p.end = min(a.steps, p.step + a.per);
+  };
+  auto next = [&](Place& p) {
+    if (++p.step < p.end) return;
+    p.unit += stride;
+    open(p);
+  };
   Place c{static_cast<int64_t>(blockIdx.x) * kWarps + warp, 0, 0, 0};
-  steps.open(c);
+  open(c);
   Place f = c;
   auto fetch = [&](int slot) {
-    if (f.wk < steps.work) {
-      const bf16* x = a.x[f.part] + steps.token(f) * a.stride[f.part];
+    if (f.unit < a.units) {
+      const uint32_t to = tc::su32(ring + slot * STEP) + lane * 16;
+      if (f.step < a.q_steps) {
+        const int h = f.step * ROWS + g;
+        const bf16* x = a.Q + f.token * a.t.qs + h * D + e;
 #pragma unroll
-      for (int k = 0; k < kRound; ++k) {
-        const int r = k * RPW + g;
-        if (f.h + r < f.end) tc::cp_async16(tc::su32(ring + slot * STEP) + (r * D + e) * 2, x + static_cast<int64_t>(f.h + r) * D + e, true);
+        for (int k = 0; k < kRound; ++k)
+          if (h + k * RPW < s.Hq) tc::cp_async16(to + k * 512, x + k * (RPW * D), true);
+      } else {
+        const int r = (f.step - a.q_steps) * ROWS + g;
+        const bf16* xk = a.K + f.token * a.t.ks + r * D + e;
+        const bf16* xv = a.V + f.token * a.vs + (r - s.Hkv) * D + e;
+#pragma unroll
+        for (int k = 0; k < kRound; ++k)
+          if (r + k * RPW < 2 * s.Hkv) tc::cp_async16(to + k * 512, (r + k * RPW < s.Hkv ? xk : xv) + k * (RPW * D), true);
       }
-      steps.next(f);
+      next(f);
     }
     tc::cp_async_commit();
   };
@@ -123,14 +123,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
   int64_t lane_row = -1;                   // the same of unit (unit & ~31) + lane
   int lane_pos = 0;
   uint64_t aa[2], ab[2], ba[2], bb[2];     // first = aa first + ab second, second = ba first + bb second
-  for (int slot = 0; c.wk < steps.work; slot = slot + 1 == kAhead ? 0 : slot + 1) {
-    const int64_t t = steps.token(c);
-    if (c.wk != now) {
+  for (int slot = 0; c.unit < a.units; slot = slot + 1 == kAhead ? 0 : slot + 1) {
+    const int part = c.step >= a.q_steps;
+    if (c.unit != now) {
       if ((++unit & 31) == 0) {            // the slots of this warp's next 32 units
-        const int64_t wk = c.wk + lane * steps.step;
+        const int64_t u = c.unit + lane * stride;
         lane_row = -1;
-        if (wk < steps.work) {
-          const int64_t tk = a.chunks == 1 ? wk : wk / a.chunks;
+        if (u < a.units) {
+          const int64_t tk = a.parts == 1 ? u : u / a.parts;
           const int seq = a.seq ? a.seq[tk] : static_cast<int>(tk / a.t.N);
           lane_pos = a.pos[tk];
           if (seq >= 0) {
@@ -147,12 +147,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
       row0 = __shfl_sync(0xffffffffu, lane_row, unit & 31);
       p0 = __shfl_sync(0xffffffffu, lane_pos, unit & 31);
     }
-    if (c.part < 2 && row0 >= 0 && (c.wk != now || c.part != now_part)) {
-      if (c.wk != now) L.form(lane, p0, a.t.rot_scale);
+    if (row0 >= 0 && (c.unit != now || part != now_part)) {
+      if (c.unit != now) L.form(lane, p0, a.t.rot_scale);
       float cs[4], sn[4], w[8];
       L.factors(cs, sn);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = NORM && a.w[c.part] ? a.w[c.part][L.element(k)] : 1.f;
+      for (int k = 0; k < 8; ++k) w[k] = NORM && a.w[part] ? a.w[part][L.element(k)] : 1.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         aa[k] = tc::pack2(w[2 * k] * cs[2 * k], w[2 * k + 1] * cs[2 * k + 1]);
@@ -161,90 +161,91 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
         bb[k] = tc::pack2(w[4 + 2 * k] * cs[2 * k], w[5 + 2 * k] * cs[2 * k + 1]);
       }
     }
-    now = c.wk;
-    now_part = c.part;
+    now = c.unit;
+    now_part = part;
     tc::cp_async_wait<kAhead - 2>();
     __syncwarp();                                          // also: every lane has read the slot fetched next
     fetch(slot == 0 ? kAhead - 1 : slot - 1);
     unsigned char* rows = ring + slot * STEP;
+    const int h0 = (part ? c.step - a.q_steps : c.step) * ROWS, end = part ? 2 * s.Hkv : s.Hq;
     if (row0 >= 0) {
-      if (c.part < 2) {
+      // where the lane group's first row goes, and from one round's rows to the next's
+      bf16* out = part ? reinterpret_cast<bf16*>(a.c.k) + (row0 + static_cast<int64_t>(h0 + g) * s.page) * D
+                       : a.Qr + (c.token * s.Hq + h0 + g) * D;
+      const int64_t out_step = static_cast<int64_t>(part ? s.page : 1) * (RPW * D);
 #pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-          if (c.h + k * RPW >= c.end) break;               // the same for the whole warp
-          unsigned char* row = rows + (k * RPW + g) * D * 2;
-          uint64_t v[4], o[4];
-          L.load(row, v);
-          uint64_t r2 = 0;
-          if (NORM) {
-            const uint64_t q = tc::fma2(v[3], v[3], tc::fma2(v[2], v[2], tc::fma2(v[1], v[1], mul2(v[0], v[0]))));
-            float q0, q1;
-            tc::unpack2(q, q0, q1);
-            const float r = rsqrtf(row_sum<D>(q0 + q1) * (1.f / D) + a.t.eps);
-            r2 = tc::pack2(r, r);
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            o[x] = L.turns ? tc::fma2(v[2 + x], ab[x], mul2(v[x], aa[x])) : mul2(v[x], aa[x]);
-            o[2 + x] = L.turns ? tc::fma2(v[x], ba[x], mul2(v[2 + x], bb[x])) : mul2(v[2 + x], bb[x]);
-          }
-          if (NORM) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] = mul2(o[x], r2);
-          }
-          const int h = c.h + k * RPW + g;
-          if (FOUR && c.part == 1) {
-            L.store(reinterpret_cast<bf16*>(row), o);      // in place: a lane reads and writes its own elements
-          } else if (h < c.end) {
-            bf16* to = c.part ? reinterpret_cast<bf16*>(a.c.k) + (row0 + static_cast<int64_t>(h) * s.page) * D
-                              : a.Qr + (t * s.Hq + h) * D;
-            L.store(to, o);
-          }
+      for (int k = 0; k < kRound; ++k) {
+        const int h = h0 + k * RPW;
+        if (h >= (part ? s.Hkv : end)) break;              // the same for the whole warp
+        unsigned char* row = rows + (k * RPW + g) * D * 2;
+        uint64_t v[4], o[4];
+        L.load(row, v);
+        uint64_t r2 = 0;
+        if (NORM) {
+          const uint64_t q = tc::fma2(v[3], v[3], tc::fma2(v[2], v[2], tc::fma2(v[1], v[1], mul2(v[0], v[0]))));
+          float q0, q1;
+          tc::unpack2(q, q0, q1);
+          const float r = rsqrtf(row_sum<D>(q0 + q1) * (1.f / D) + a.t.eps);
+          r2 = tc::pack2(r, r);
         }
-        if (FOUR && c.part == 1) __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[x] = L.turns ? tc::fma2(v[2 + x], ab[x], mul2(v[x], aa[x])) : mul2(v[x], aa[x]);
+          o[2 + x] = L.turns ? tc::fma2(v[x], ba[x], mul2(v[2 + x], bb[x])) : mul2(v[2 + x], bb[x]);
+        }
+        if (NORM) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[x] = mul2(o[x], r2);
+        }
+        if (h + g < (part ? s.Hkv : end)) {
+          // keys of 4-bit pages go back to the ring, in place: a lane reads and writes its own elements
+          L.store(FOUR && part ? reinterpret_cast<bf16*>(row) : out + k * out_step, o);
+        }
       }
-      if (c.part == 2 || (FOUR && c.part == 1)) {
-        const bool v_part = c.part == 2;
+      if (part && FOUR) __syncwarp();
+      if (part) {
 #pragma unroll
         for (int k = 0; k < kRound; ++k) {
-          if (c.h + k * RPW >= c.end) break;
-          const int h = c.h + k * RPW + g;
-          const bool row = h < c.end;
+          const int r = h0 + k * RPW + g;
+          if (h0 + k * RPW >= end) break;
+          if (!FOUR && h0 + (k + 1) * RPW <= s.Hkv) continue;
+          const bool value = r >= s.Hkv, in = r < end;
+          const int h = value ? r - s.Hkv : r;
           const uint4 u = *reinterpret_cast<const uint4*>(rows + ((k * RPW + g) * D + e) * 2);
           const int64_t to = row0 + static_cast<int64_t>(h) * s.page;
           if (!FOUR) {
-            if (row) *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.c.v) + to * D + e) = u;
+            if (in && value) *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.c.v) + to * D + e) = u;
             continue;
           }
           const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-          uint32_t top = 0;                                // the largest magnitude's bits: NaN above infinity above all
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top = max(top, max(uw[x] & 0x7fffu, (uw[x] >> 16) & 0x7fffu));
+          // the largest magnitude's bits: NaN above infinity above all
+          uint32_t top = max16x2(max16x2(uw[0] & 0x7fff7fffu, uw[1] & 0x7fff7fffu), max16x2(uw[2] & 0x7fff7fffu, uw[3] & 0x7fff7fffu));
+          top = max(top & 0xffffu, top >> 16);
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          const float* amps = v_part ? a.c.v_amp : a.c.k_amp;
-          const float amp = amps && row ? amps[h] : 1.f, ramp = amps ? 1.f / amp : 1.f;
-          // v / by, to the last bit but in the rarest cases
-          auto over = [](float v, float by, float r) { const float q = v * r; return fmaf(r, fmaf(-q, by, v), q); };
+          const float* amps = value ? a.c.v_amp : a.c.k_amp;
+          const float amp = amps && in ? amps[h] : 1.f, ramp = rcp_approx(amp);
           const float most = __uint_as_float(top << 16);
-          const uint32_t s8 = top >= 0x7f80u ? 0x7fu : paged::to_e4m3((amps ? over(most, amp, ramp) : most) / 6.f);
+          const uint32_t s8 = top >= 0x7f80u ? 0x7fu : paged::to_e4m3(over(amps ? over(most, amp, ramp) : most, 6.f, 1.f / 6.f));
           const float sc = __low2float(paged::from_e4m3x2(static_cast<uint16_t>(s8)));
-          const float rs = sc > 0.f ? 1.f / sc : 0.f;      // a scale of 0 or NaN: codes of 0
+          const float rs = sc > 0.f ? rcp_approx(sc) : 0.f;      // a scale of 0: codes of 0 (of NaN: whatever, they stand for NaN)
           float x[8];
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            x[y] = __uint_as_float(y & 1 ? uw[y >> 1] & 0xffff0000u : uw[y >> 1] << 16);
-            if (amps) x[y] = over(x[y], amp, ramp);
-            x[y] = sc > 0.f ? over(x[y], sc, rs) : copysignf(0.f, x[y]);
+          for (int y = 0; y < 4; ++y) {
+            uint64_t v = tc::pack2(__uint_as_float(uw[y] << 16), __uint_as_float(uw[y] & 0xffff0000u));
+            if (amps) v = over2(v, amp, ramp);
+            tc::unpack2(over2(v, sc, rs), x[2 * y], x[2 * y + 1]);
+            x[2 * y] = copysignf(x[2 * y], __uint_as_float(uw[y] << 16));          // (a zero's)
+            x[2 * y + 1] = copysignf(x[2 * y + 1], __uint_as_float(uw[y]));
           }
           const uint32_t codes = paged::to_e2m1x8(x);
-          if (row) {
-            *reinterpret_cast<uint32_t*>((v_part ? a.c.v : a.c.k) + to * (D / 2) + e / 2) = codes;
-            if ((lane & 1) == 0) (v_part ? a.c.vs : a.c.ks)[to * (D / 16) + e / 16] = static_cast<unsigned char>(s8);
+          if (in) {
+            *reinterpret_cast<uint32_t*>((value ? a.c.v : a.c.k) + to * (D / 2) + e / 2) = codes;
+            if ((lane & 1) == 0) (value ? a.c.vs : a.c.ks)[to * (D / 16) + e / 16] = static_cast<unsigned char>(s8);
           }
         }
       }
     }
-    steps.next(c);
+    next(c);
   }
   tc::cp_async_wait<0>();
 }
@@ -275,14 +276,10 @@ int launch_paged_append(const PagedDims& s, const PagedCache& c, const RopeDims&
   a.s = s;
   a.t = t;
   a.c = c;
-  a.x[0] = static_cast<const bf16*>(Q);
-  a.x[1] = static_cast<const bf16*>(K);
-  a.x[2] = static_cast<const bf16*>(V);
-  a.stride[0] = t.qs;
-  a.stride[1] = t.ks;
-  a.stride[2] = vs;
-  a.heads[0] = Q ? s.Hq : 0;
-  a.heads[1] = a.heads[2] = s.Hkv;
+  a.Q = static_cast<const bf16*>(Q);
+  a.K = static_cast<const bf16*>(K);
+  a.V = static_cast<const bf16*>(V);
+  a.vs = vs;
   a.w[0] = wq;
   a.w[1] = wk;
   a.inv_freq = inv_freq;
@@ -291,15 +288,25 @@ int launch_paged_append(const PagedDims& s, const PagedCache& c, const RopeDims&
   a.pos = pos;
   a.Qr = static_cast<bf16*>(Qr);
   a.status = status;
-  a.tokens = static_cast<int64_t>(t.B) * t.N;
-  // all heads of a token to one warp where the tokens alone fill the GPU's warps; else a warp takes
-  // one round of rows
-  const int H = a.heads[0] + 2 * s.Hkv;
-  const int64_t room = sm_count() * kBlocks;
-  a.heads_per_warp = a.tokens >= room * kWarps ? H : 256 / s.d;
-  a.chunks = (H + a.heads_per_warp - 1) / a.heads_per_warp;
-  const int64_t work = a.tokens * a.chunks;
-  const int blocks = static_cast<int>(std::min<int64_t>((work + kWarps - 1) / kWarps, room));
+  const int rows = 256 / s.d * kRound;
+  const int64_t room = sm_count() * kBlocks, tokens = static_cast<int64_t>(t.B) * t.N;
+  a.q_steps = Q ? (s.Hq + rows - 1) / rows : 0;
+  a.steps = a.q_steps + (2 * s.Hkv + rows - 1) / rows;
+  // A unit of work, which forms its token's angles and looks its slot up (kStart steps' time), is a token's steps or a
+  // part of them, whichever has the busiest warp done first (5127 tokens of 32 heads over 8, 6 steps each: 27 us with 3 steps
+  // a unit, 35 with 6, 44 with 1).
+  const int64_t slots = room * kWarps;
+  int64_t least = INT64_MAX;
+  for (int parts = 1; parts <= a.steps; ++parts) {
+    const int per = (a.steps + parts - 1) / parts;
+    const int64_t cost = ((tokens * parts + slots - 1) / slots) * (per + kStart);
+    if (cost >= least) continue;
+    least = cost;
+    a.per = per;
+    a.parts = (a.steps + per - 1) / per;
+  }
+  a.units = tokens * a.parts;
+  const int blocks = static_cast<int>(std::min<int64_t>((a.units + kWarps - 1) / kWarps, room));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.d == 128) return s.bits == 4 ? by_kind<128, true>(a, blocks, st) : by_kind<128, false>(a, blocks, st);
   return s.bits == 4 ? by_kind<64, true>(a, blocks, st) : by_kind<64, false>(a, blocks, st);
