@@ -61,13 +61,13 @@ struct AppendArgs {
   int32_t* status;
   int32_t q_steps, steps;        // a token's steps: its queries' (0 without), then its keys' and values'
   int32_t per, parts;            // steps of a unit of work, units of a token
-  int64_t units;
+  int32_t units;                 // < 2^31 - 32 (warps of the grid): see the launch
 };
 
 // A step of a token: rows [h, end) of its queries (part 0), or of its keys and values (part 1: row r is key r, or value
 // r - Hkv).
 struct Place {
-  int64_t unit, token;
+  int unit, token;
   int step, end;                 // end: of the unit's steps
 };
 
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPR, e = 8 * (lane % LPR);
   unsigned char* ring = ring_all + warp * kAhead * STEP;
   const Lane<D, IL> L(lane, a.t.rot, a.inv_freq, table[warp]);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int stride = static_cast<int>(gridDim.x) * kWarps;
   auto open = [&](Place& p) {
     p.token = a.parts == 1 ? p.unit : p.unit / a.parts;
     p.step = static_cast<int>(p.unit - p.token * a.parts) * a.per;
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
   };
   auto next = [&](Place& p) {
     if (++p.step < p.end) return;
-    p.unit += stride;
+    p.unit = p.unit < a.units - stride ? p.unit + stride : a.units;
     open(p);
   };
-  Place c{static_cast<int64_t>(blockIdx.x) * kWarps + warp, 0, 0, 0};
+  Place c{static_cast<int>(blockIdx.x) * kWarps + warp, 0, 0, 0};
   open(c);
   Place f = c;
   auto fetch = [&](int slot) {
@@ -99,14 +99,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
       const uint32_t to = tc::su32(ring + slot * STEP) + lane * 16;
       if (f.step < a.q_steps) {
         const int h = f.step * ROWS + g;
-        const bf16* x = a.Q + f.token * a.t.qs + h * D + e;
+        const bf16* x = a.Q + static_cast<int64_t>(f.token) * a.t.qs + h * D + e;
 #pragma unroll
         for (int k = 0; k < kRound; ++k)
           if (h + k * RPW < s.Hq) tc::cp_async16(to + k * 512, x + k * (RPW * D), true);
       } else {
         const int r = (f.step - a.q_steps) * ROWS + g;
-        const bf16* xk = a.K + f.token * a.t.ks + r * D + e;
-        const bf16* xv = a.V + f.token * a.vs + (r - s.Hkv) * D + e;
+        const bf16* xk = a.K + static_cast<int64_t>(f.token) * a.t.ks + r * D + e;
+        const bf16* xv = a.V + static_cast<int64_t>(f.token) * a.vs + (r - s.Hkv) * D + e;
 #pragma unroll
         for (int k = 0; k < kRound; ++k)
           if (r + k * RPW < 2 * s.Hkv) tc::cp_async16(to + k * 512, (r + k * RPW < s.Hkv ? xk : xv) + k * (RPW * D), true);
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
 #pragma unroll
   for (int k = 0; k < kAhead - 1; ++k) fetch(k);
 
-  int64_t now = -1, row0 = -1;             // the unit at hand, and its slot's row of KV head 0 (-1: nothing is stored)
-  int now_part = -1, unit = -1, p0 = 0;    // units so far; the position
+  int64_t row0 = -1;                       // the slot's row of KV head 0 (-1: nothing is stored)
+  int now = -1, now_part = -1, unit = -1, p0 = 0;    // the unit and part at hand, units so far, the position
   int64_t lane_row = -1;                   // the same of unit (unit & ~31) + lane
   int lane_pos = 0;
   uint64_t aa[2], ab[2], ba[2], bb[2];     // first = aa first + ab second, second = ba first + bb second
@@ -127,11 +127,11 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
     const int part = c.step >= a.q_steps;
     if (c.unit != now) {
       if ((++unit & 31) == 0) {            // the slots of this warp's next 32 units
-        const int64_t u = c.unit + lane * stride;
+        const int64_t u = c.unit + static_cast<int64_t>(lane) * stride;
         lane_row = -1;
         if (u < a.units) {
-          const int64_t tk = a.parts == 1 ? u : u / a.parts;
-          const int seq = a.seq ? a.seq[tk] : static_cast<int>(tk / a.t.N);
+          const int tk = a.parts == 1 ? static_cast<int>(u) : static_cast<int>(u) / a.parts;
+          const int seq = a.seq ? a.seq[tk] : tk / a.t.N;
           lane_pos = a.pos[tk];
           if (seq >= 0) {
             int page = -1;
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
     if (row0 >= 0) {
       // where the lane group's first row goes, and from one round's rows to the next's
       bf16* out = part ? reinterpret_cast<bf16*>(a.c.k) + (row0 + static_cast<int64_t>(h0 + g) * s.page) * D
-                       : a.Qr + (c.token * s.Hq + h0 + g) * D;
-      const int64_t out_step = static_cast<int64_t>(part ? s.page : 1) * (RPW * D);
+                       : a.Qr + (static_cast<int64_t>(c.token) * s.Hq + h0 + g) * D;
+      const int out_step = (part ? s.page : 1) * (RPW * D);
 #pragma unroll
       for (int k = 0; k < kRound; ++k) {
         const int h = h0 + k * RPW;
@@ -190,8 +190,15 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          o[x] = L.turns ? tc::fma2(v[2 + x], ab[x], mul2(v[x], aa[x])) : mul2(v[x], aa[x]);
-          o[2 + x] = L.turns ? tc::fma2(v[x], ba[x], mul2(v[2 + x], bb[x])) : mul2(v[2 + x], bb[x]);
+          o[x] = mul2(v[x], aa[x]);
+          o[2 + x] = mul2(v[2 + x], bb[x]);
+        }
+        if (L.turns) {                                     // what does not turn does not meet its partner: an infinity there stays itself
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            o[x] = tc::fma2(v[2 + x], ab[x], o[x]);
+            o[2 + x] = tc::fma2(v[x], ba[x], o[2 + x]);
+          }
         }
         if (NORM) {
 #pragma unroll
@@ -199,8 +206,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
         }
         if (h + g < (part ? s.Hkv : end)) {
           // keys of 4-bit pages go back to the ring, in place: a lane reads and writes its own elements
-          L.store(FOUR && part ? reinterpret_cast<bf16*>(row) : out + k * out_step, o);
+          L.store(FOUR && part ? reinterpret_cast<bf16*>(row) : out, o);
         }
+        out += out_step;
       }
       if (part && FOUR) __syncwarp();
       if (part) {
@@ -305,8 +313,8 @@ int launch_paged_append(const PagedDims& s, const PagedCache& c, const RopeDims&
     a.per = per;
     a.parts = (a.steps + per - 1) / per;
   }
-  a.units = tokens * a.parts;
-  const int blocks = static_cast<int>(std::min<int64_t>((a.units + kWarps - 1) / kWarps, room));
+  a.units = static_cast<int>(tokens * a.parts);          // parts: at most half of Hq + 2 Hkv, or 1; and T (Hq + 2 Hkv) < 2^31
+  const int blocks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(a.units) + kWarps - 1) / kWarps, room));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.d == 128) return s.bits == 4 ? by_kind<128, true>(a, blocks, st) : by_kind<128, false>(a, blocks, st);
   return s.bits == 4 ? by_kind<64, true>(a, blocks, st) : by_kind<64, false>(a, blocks, st);
