@@ -690,6 +690,10 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
         return 0
     if t.dim() != 3:
         raise ValueError(f"{name} must be [T, H, d] (got {tuple(t.shape)})")
+    T, H, d = t.shape
+    step, head, one = t.stride()
+    if T > 1 and head == d and one == 1 and H * d <= step < 1 << 31:
+        return step
     return _token_stride(t[None], name)
 
 
@@ -717,7 +721,7 @@ def _need_rows(t, size, stride: int, dev, name: str) -> None:
     if t.dtype is not torch.bfloat16 or t.shape != size or t.device != dev:
         raise ValueError(f"{name} must be a bfloat16 tensor {tuple(size)} on {dev} "
                          f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
-    if stride or not t.is_contiguous():
+    if t.stride() != (stride or size[1] * size[2], size[2], 1):     # else as the shape says; sizes of one have any stride
         step, row = _row_stride(t, name), size[1] * size[2]
         if size[0] > 1 and (step or row) != (stride or row):
             raise ValueError(f"{name} has strides {tuple(t.stride())}, the shape says {stride} elements a token")
@@ -822,23 +826,26 @@ def paged_cache(shape: PagedShape, device, k_amp=None, v_amp=None) -> PagedCache
 
 def _need_paged(shape, cache, table, dev):
     """The cache's C struct, its tensors checked."""
-    size = (shape.n_pages, shape.Hkv, shape.page)
-    four = shape.bits == 4
-    kind, row = (torch.uint8, shape.d // 2) if four else (torch.bfloat16, shape.d)
-    _need_shaped(cache.k, kind, size + (row,), dev, "k")
-    _need_shaped(cache.v, kind, size + (row,), dev, "v")
-    if four:
-        if cache.k_scale is None or cache.v_scale is None:
-            raise ValueError("a cache in 4 bits needs k_scale and v_scale")
-        _need_shaped(cache.k_scale, torch.float8_e4m3fn, size + (shape.d // 16,), dev, "k_scale")
-        _need_shaped(cache.v_scale, torch.float8_e4m3fn, size + (shape.d // 16,), dev, "v_scale")
-        for t, n in ((cache.k_amp, "k_amp"), (cache.v_amp, "v_amp")):
-            if t is not None:
-                _need_shaped(t, torch.float32, (shape.Hkv,), dev, n)
-    elif any(t is not None for t in cache[2:]):
-        raise ValueError("a cache in 16 bits has no scales")
+    k, v, k_scale, v_scale, k_amp, v_amp = cache
+    n_pages, Hkv, page, d = shape.n_pages, shape.Hkv, shape.page, shape.d
     _need_shaped(table, torch.int32, (shape.B, shape.max_pages), dev, "table")
-    return _PagedCache(*(_ptr(t) for t in cache))
+    if shape.bits != 4:
+        _need_shaped(k, torch.bfloat16, (n_pages, Hkv, page, d), dev, "k")
+        _need_shaped(v, torch.bfloat16, (n_pages, Hkv, page, d), dev, "v")
+        if not k_scale is v_scale is k_amp is v_amp is None:
+            raise ValueError("a cache in 16 bits has no scales")
+        return _PagedCache(k.data_ptr(), v.data_ptr(), None, None, None, None)
+    _need_shaped(k, torch.uint8, (n_pages, Hkv, page, d // 2), dev, "k")
+    _need_shaped(v, torch.uint8, (n_pages, Hkv, page, d // 2), dev, "v")
+    if k_scale is None or v_scale is None:
+        raise ValueError("a cache in 4 bits needs k_scale and v_scale")
+    _need_shaped(k_scale, torch.float8_e4m3fn, (n_pages, Hkv, page, d // 16), dev, "k_scale")
+    _need_shaped(v_scale, torch.float8_e4m3fn, (n_pages, Hkv, page, d // 16), dev, "v_scale")
+    if k_amp is not None:
+        _need_shaped(k_amp, torch.float32, (Hkv,), dev, "k_amp")
+    if v_amp is not None:
+        _need_shaped(v_amp, torch.float32, (Hkv,), dev, "v_amp")
+    return _PagedCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_amp), _ptr(v_amp))
 
 
 def _need_status(status, dev):
