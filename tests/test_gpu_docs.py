@@ -218,3 +218,106 @@ def test_two_streams_at_once():
     for g in got:
         for a, n in zip(g, ("O", "lse", "dQ", "dK", "dV")):
             assert torch.equal(a, want[n]), n
+
+
+@pytest.mark.parametrize("cap,biased", [(0.0, False), (9.0, True)])
+def test_small_calls_need_no_workspace(cap, biased):
+    # where nothing is laid out ahead the workspace is the status block alone, and may be left out
+    Q, K, V, _ = _inputs(300, 8, 2, 64, fused=True, seed=11)
+    starts, slopes = _ints([0, 120, 300]), _slopes(8) if biased else None
+    s = pisa.doc_shape_of(Q, K, V, starts, cap=cap)
+    assert pisa.doc_workspace_size(s, pisa.DOC_FWD) == 256
+    want = _run(Q, K, V, None, starts, None, slopes, cap)
+    O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s, slopes=slopes)
+    assert torch.equal(O, want["O"]) and torch.equal(lse, want["lse"])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (40, 8)])
+def test_more_documents_than_the_rows_kernel_holds(Hq, Hkv):
+    # 6000 documents of 0, 1 or 2 tokens: searched for in the starts themselves; with one head by the attention's kernel, with 40
+    # by the one before it. A token sees itself and, as its document's second, the first.
+    lens = [(0, 1, 2, 1)[m % 4] for m in range(6000)]
+    starts = [0]
+    for n in lens:
+        starts.append(starts[-1] + n)
+    T = starts[-1]
+    Q, K, V, dO = _inputs(T, Hq, Hkv, 64, seed=12)
+    got = _run(Q, K, V, dO, _ints(starts))
+    first = torch.tensor([starts[m] for m in range(6000) for _ in range(lens[m])], device="cuda")
+    second = torch.arange(T, device="cuda") > first
+    G = Hq // Hkv
+    q, k, v, g = Q.double(), K.double().repeat_interleave(G, 1), V.double().repeat_interleave(G, 1), dO.double()
+    x0, x1 = ((q * kk).sum(-1) / 8 for kk in (k[first], k))
+    p0 = torch.where(second[:, None], torch.sigmoid(x0 - x1), 0.0)[..., None]
+    want = p0 * v[first] + (1 - p0) * v
+    # P's error: the scores' (64 products, |q||k| up to 64 2^-24 of their sum) and the exponent's; its rounding; O's
+    size = p0 * v[first].abs() + (1 - p0) * v.abs()
+    xe = (q.abs() * torch.maximum(k.abs(), k[first].abs())).sum(-1)[..., None] / 8 * 72 * 2.0 ** -24 + 2.0 ** -19
+    tol = 2.0 ** -8 * (want.abs() + size) + (2 * xe + 2.0 ** -11) * size
+    check("O", got["O"], want, tol)
+    # gradients: dS of the first key is -dS of the token itself
+    dp0, dp1 = ((g * vv).sum(-1, keepdim=True) for vv in (v[first], v))
+    ds = p0 * (1 - p0) * (dp0 - dp1)
+    dq = ds * (k[first] - k) / 8
+    # |ds| off by its rounding, P's error, and D's (O's error times dO) for either key
+    De = (g.abs() * tol).sum(-1, keepdim=True) + (g.abs() * size).sum(-1, keepdim=True) * 64 * 2.0 ** -24
+    dse = ds.abs() * (2.0 ** -8 + 4 * xe + 2.0 ** -11) + torch.maximum(p0, 1 - p0) * De * 1.01
+    check("dQ", got["dQ"], dq, dse * (k[first].abs() + k.abs()) / 8 + 2.0 ** -8 * dq.abs())
+
+
+@pytest.fixture
+def stalled():
+    pisa.set_wait_limit(2_000_000)          # 2 ms
+    pisa.set_test_stall(True)
+    try:
+        yield
+    finally:
+        pisa.set_test_stall(False)
+        pisa.set_wait_limit(0)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,cap,biased", [(300, 4, 1, 64, 0.0, False), (700, 8, 2, 128, 10.0, False), (12000, 16, 2, 128, 0.0, True)])
+def test_wait_that_runs_out_is_reported_and_poisons_outputs(stalled, T, Hq, Hkv, d, cap, biased):
+    Q, K, V, dO = _inputs(T, Hq, Hkv, d, seed=13)
+    starts, slopes = _ints([0, T // 3, T]), _slopes(Hq) if biased else None
+    s = pisa.doc_shape_of(Q, K, V, starts, cap=cap)
+    wf, wb = (pisa.doc_workspace(s, op, Q.device) for op in (pisa.DOC_FWD, pisa.DOC_BWD))
+    O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s, slopes=slopes, ws=wf)
+    assert pisa.workspace_status(wf) & pisa.STATUS_TIMEOUT
+    with pytest.raises(pisa.PisaError):
+        pisa.check_status(wf)
+    assert bool(O.isnan().all()) and bool(lse.isnan().all())
+    assert bool(pisa.doc_attn_fwd(Q, K, V, starts, s, slopes=slopes)[0].isnan().all())    # without a workspace the outputs tell
+    grads = pisa.doc_attn_bwd(Q, K, V, torch.zeros_like(O), torch.zeros_like(lse), dO, starts, s, slopes=slopes, ws=wb)
+    assert pisa.workspace_status(wb) & pisa.STATUS_TIMEOUT
+    for t in grads:
+        assert bool(t.isnan().all())
+    pisa.set_test_stall(False)                                           # and the next calls are sound again
+    pisa.set_wait_limit(0)
+    for t in _run(Q, K, V, dO, starts, None, slopes, cap).values():
+        assert bool(t.isfinite().all())
+
+
+def test_two_graphs_share_workspaces():
+    # forwards and backwards of two packings, captured with the same workspaces, replayed in turn
+    Q, K, V, dO = _inputs(2500, 16, 4, 64, seed=14)
+    s = pisa.make_doc_shape(2500, 16, 4, 64, 2)
+    ws, wb = (pisa.doc_workspace(s, op, Q.device) for op in (pisa.DOC_FWD, pisa.DOC_BWD))
+    packs = [_ints([0, 2000, 2500]), _ints([0, 300, 2400])]
+
+    def step(starts):
+        O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s, ws=ws)
+        return O, lse, *pisa.doc_attn_bwd(Q, K, V, O, lse, dO, starts, s, ws=wb)
+
+    want = [[t.clone() for t in step(p)] for p in packs]
+    graphs, got = [torch.cuda.CUDAGraph() for _ in packs], []
+    for g, p in zip(graphs, packs):
+        with torch.cuda.graph(g):
+            got.append(step(p))
+    for k in (0, 1, 1, 0, 1):
+        for t in got[k]:
+            t.zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got[k], want[k]):
+            assert torch.equal(a, b)

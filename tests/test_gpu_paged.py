@@ -426,3 +426,76 @@ def test_4_bit_values_are_near_the_16_bit_ones():
         top = x.double().reshape(500, 4, 8, 16).abs().amax(-1, keepdim=True)
         off = (got - x.double()).reshape(500, 4, 8, 16).abs()
         assert bool((off <= top * (1 / 6) * (1 + 2.0 ** -4) + 2.0 ** -9).all())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_pages_past_32_bits(bits):
+    # pages whose bytes (and, in 16 bits, elements) lie past 2^32 (2^31): the same as in a small cache, to the bit
+    g = _gen(22)
+    Hq, Hkv, d, page = 8, 4, 128, 1024
+    row = d * 2 if bits == 16 else d // 2
+    pool = (9 << 29) // (Hkv * page * row)                               # 4.5 GiB of codes or values
+    lens = [3000, 1500]
+    small = pisa.make_paged_shape(2, Hq, Hkv, d, 5, page, 3, bits)
+    large = pisa.make_paged_shape(2, Hq, Hkv, d, pool, page, 3, bits)
+    few = _filled(g, small)
+    ids = torch.tensor([pool - 1, 0, pool - 2, pool // 2, pool - 5], device="cuda")
+    many = []
+    for x in few[:4]:
+        if x is None:
+            many.append(None)
+            continue
+        y = torch.empty(pool, *x.shape[1:], dtype=x.dtype, device="cuda")
+        y.view(torch.uint8)[ids] = x.view(torch.uint8)
+        many.append(y)
+    many = pisa.PagedCache(*many, *few[4:])
+    t0 = torch.tensor([[0, 1, 2], [3, 4, 0]], device="cuda")
+    t1 = ids[t0].to(torch.int32)
+    t0 = t0.to(torch.int32)
+    K, V, Q = _randn(g, 100, Hkv, d), _randn(g, 100, Hkv, d), _randn(g, 100, Hq, d)
+    seq = _ints([0] * 60 + [1] * 40)
+    pos = _ints(list(range(2940, 3000)) + list(range(1460, 1500)))
+    rope = pisa.Rope(pisa.rope_frequencies(d)[0].cuda(), d, norm=False)
+    q = _randn(g, 2, 1, Hq, d)
+    outs = []
+    for shape, cache, table in ((small, few, t0), (large, many, t1)):
+        Qr, status = pisa.paged_append(shape, cache, table, pos, K, V, Q=Q, seq=seq, rope=rope)
+        assert int(status[0]) == 0
+        outs.append((Qr, *pisa.paged_attn(shape, cache, table, _ints(lens), q)))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    for x, y in zip(few[:4], many[:4]):
+        assert x is None or torch.equal(y.view(torch.uint8)[ids], x.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_two_graphs_share_a_workspace(bits):
+    g = _gen(23)
+    page = 16
+    lens = [[700, 30, 0, 5], [1, 650, 64, 222]]
+    table, pool = _table(g, [700, 650, 64, 222], page)
+    shape = pisa.make_paged_shape(4, 16, 2, 128, pool, page, table.shape[1], bits, 2)
+    cache = _filled(g, shape)
+    q, ws = _randn(g, 4, 2, 16, 128), pisa.paged_workspace(shape, "cuda")
+    lens = [_ints(n) for n in lens]
+    want = [[t.clone() for t in pisa.paged_attn(shape, cache, table, n, q, ws=ws)] for n in lens]
+    graphs, got = [torch.cuda.CUDAGraph() for _ in lens], []
+    for graph, n in zip(graphs, lens):
+        with torch.cuda.graph(graph):
+            got.append(pisa.paged_attn(shape, cache, table, n, q, ws=ws))
+    for k in (0, 1, 1, 0, 1):
+        for t in got[k]:
+            t.zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got[k], want[k]):
+            assert torch.equal(a, b)
+    # and at once on streams of their own, with workspaces of their own
+    streams, out = [torch.cuda.Stream() for _ in lens], []
+    for st, n in zip(streams, lens):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            out.append(pisa.paged_attn(shape, cache, table, n, q))
+    torch.cuda.synchronize()
+    for x, y in zip(out, want):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
