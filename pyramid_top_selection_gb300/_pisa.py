@@ -370,7 +370,7 @@ def _on(dev, fn, *args) -> None:
     if dev.type != "cuda":
         raise ValueError(f"the tensors must be CUDA tensors (got {dev})")
     stream = torch._C._cuda_getCurrentRawStream(dev.index)   # current_stream(dev).cuda_stream without its objects
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():              # torch.cuda.current_device() of a context that exists
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -727,6 +727,17 @@ def _need_rows(t, size, stride: int, dev, name: str) -> None:
             raise ValueError(f"{name} has strides {tuple(t.stride())}, the shape says {stride} elements a token")
 
 
+def _rows_stride(t, size, dev, name: str) -> int:
+    """The stride of a tensor of this size, checked: elements between consecutive tokens (0: contiguous)."""
+    stride = t.stride()
+    if stride == (size[1] * size[2], size[2], 1):
+        _need_rows(t, size, 0, dev, name)
+        return 0
+    step = _row_stride(t, name)
+    _need_rows(t, size, step, dev, name)
+    return step
+
+
 def _need_docs(Q, K, V, starts, shape, prefix, slopes) -> None:
     dev = Q.device
     kv = (shape.T, shape.Hkv, shape.d)
@@ -875,11 +886,8 @@ def paged_append(shape: PagedShape, cache: PagedCache, table, pos, K, V, Q=None,
             raise ValueError("Q is normed and rotated: it needs rope")
         rope = Rope(None, 0, norm=False)
     c = _need_paged(shape, cache, table, dev)
-    ks, vs = _row_stride(K, "K"), _row_stride(V, "V")
-    qs = 0 if Q is None else _row_stride(Q, "Q")
-    kv, q = (T, shape.Hkv, shape.d), (T, shape.Hq, shape.d)
-    _need_rows(K, kv, ks, dev, "K")
-    _need_rows(V, kv, vs, dev, "V")
+    kv = (T, shape.Hkv, shape.d)
+    ks, vs, qs = _rows_stride(K, kv, dev, "K"), _rows_stride(V, kv, dev, "V"), 0
     _need_shaped(pos, torch.int32, (T,), dev, "pos")
     if seq is not None:
         _need_shaped(seq, torch.int32, (T,), dev, "seq")
@@ -889,7 +897,8 @@ def paged_append(shape: PagedShape, cache: PagedCache, table, pos, K, V, Q=None,
         if t is not None:
             _need_shaped(t, torch.float32, (shape.d,), dev, n)
     if Q is not None:
-        _need_rows(Q, q, qs, dev, "Q")
+        q = (T, shape.Hq, shape.d)
+        qs = _rows_stride(Q, q, dev, "Q")
         if q_out is None:
             q_out = torch.empty(q, dtype=torch.bfloat16, device=dev)
         else:

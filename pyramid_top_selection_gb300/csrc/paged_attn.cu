@@ -435,8 +435,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
     };
     // channel of o[..][k][e]
     auto channel = [&](int k, int e) { return FOUR ? D / 8 * g + 2 * k + (e >> 1) : 16 * k + g + 8 * (e >> 1); };
-    // the part at hand is over: the unit's output if it is all of it, else a part
-    auto close = [&](bool tail) {
+    // the part at hand is over: the unit's output if it is all of it, else a part; last: of the run
+    auto close = [&](bool tail, bool last) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -474,17 +474,26 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
           }
         return;
       }
-      if (head) {                                                  // the run's last part: over the ring, which nothing fills any more
+      if (last) {                                                  // the run's last part: over the ring, which nothing fills any more
         tc::cp_async_wait<0>();
         __syncwarp();
       }
-      float* to = head ? reinterpret_cast<float*>(ring) : first_part(warp);
+      float* to = last ? reinterpret_cast<float*>(ring) : first_part(warp);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
+        if (FOUR) {                                                // a lane's D / 8 channels lie in a row
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) to[(8 * t + 2 * p2 + (e & 1)) * D + channel(k, e)] = o[t][k][e];
+            for (int k = 0; k < KS; k += 2)
+              *reinterpret_cast<float4*>(to + (8 * t + 2 * p2 + e) * D + channel(k, e)) =
+                  make_float4(o[t][k][e], o[t][k][e + 2], o[t][k + 1][e], o[t][k + 1][e + 2]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[(8 * t + 2 * p2 + (e & 1)) * D + channel(k, e)] = o[t][k][e];
+        }
         if (g == 0) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -493,7 +502,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
           }
         }
       }
-      if (lane == 0) s_part[warp][head] = Part{con.b * a.units + con.u, head, tail, 0};
+      if (lane == 0) s_part[warp][last] = Part{con.b * a.units + con.u, head, tail, 0};
     };
 
     const float cap2 = s.cap * kLog2e;
@@ -711,9 +720,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
       done += count;
       con.c += count - 1;
       const bool tail = con.c + 1 == con.chunks;
-      close(tail);
+      close(tail, done == mine);
       __syncwarp();
-      if (lane == 0 && first && !(begun == 0 && tail)) s_part[warp][begun == 0].first = 1;
+      if (lane == 0 && first && !(begun == 0 && tail)) s_part[warp][done == mine].first = 1;
       con.next(list);
     }
     tc::cp_async_wait<0>();
