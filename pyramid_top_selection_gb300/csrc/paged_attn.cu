@@ -55,9 +55,6 @@ struct PagedArgs {
 template <int D, bool FOUR, int NT>
 struct Plan {
   static constexpr int CH = FOUR ? 32 : 16;                        // tokens of a chunk
-  // Chunks of a run, where the list has as many: 6 sequences of up to 3000 tokens in 16 bits take 13.7 us with 1 and 15.8 with 2; in
-  // 4 bits one of 64 tokens takes 14.4 with 1, 11.4 with 2 and 14.8 with 4, one of 8192 tokens 18.3, 16.9 and 18.0.
-  static constexpr int FEWEST = FOUR ? 2 : 1;
   static constexpr int ROW = FOUR ? D / 2 : D * 2;                 // bytes of a token
   static constexpr int SROW = FOUR ? D / 16 : 0;                   // of its scales
   static constexpr int HALF = CH * (ROW + SROW);                   // keys with their scales; values follow
@@ -186,13 +183,11 @@ struct List {
   }
 };
 
-// Runs: `n` of them over `total` places, run w the places [begin(w), begin(w + 1)), at least FEWEST of them where there are as many.
-template <int FEWEST>
+// Runs: `n` of them over `total` places, run w the places [begin(w), begin(w + 1)).
 struct Runs {
   int64_t total;
   int n;
-  __device__ __forceinline__ Runs(int64_t total_, int most)
-      : total(total_), n(static_cast<int>(max(int64_t(1), min(static_cast<int64_t>(most), total_ / FEWEST)))) {}
+  __device__ __forceinline__ Runs(int64_t total_, int most) : total(total_), n(static_cast<int>(min(static_cast<int64_t>(most), total_))) {}
   __device__ __forceinline__ int64_t begin(int w) const {
     if (w >= n) return total;
     if (total < (int64_t(1) << 32) / n) return static_cast<uint32_t>(total) * static_cast<uint32_t>(w) / static_cast<uint32_t>(n);
@@ -233,7 +228,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
   const PagedDims& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, p2 = lane & 3;
   const List<CH> list(a);
-  const Runs<M::FEWEST> runs(list.total(), static_cast<int>(gridDim.x) * kWarps);
+  const Runs runs(list.total(), static_cast<int>(gridDim.x) * kWarps);
   if (blockIdx.x * kWarps >= runs.n) {
     if (threadIdx.x == 0) a.flags[blockIdx.x] = 0;
     win::launch_dependents();
@@ -357,7 +352,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
       }
       tc::cp_async_commit();
     };
-#pragma unroll
+#pragma unroll 1                                                   // (code that short runs would wait for)
     for (int i = 0; i < M::ST - 1; ++i) fetch();
 
     uint32_t qf[NT][KS][2];                                        // Q^T: rows of the unit as columns
@@ -395,9 +390,10 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
             raw[4 * k + 3] = v.w;
           }
 #pragma unroll
-          for (int k = 0; k < D / 8; ++k) top = max(top, max(raw[k] & 0x7fffu, (raw[k] >> 16) & 0x7fffu));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          for (int k = 0; k < D / 8; ++k) top = __vmaxu2(top, raw[k] & 0x7fff7fffu);
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = max(top & 0xffffu, top >> 16);
           // the largest magnitude between 2^7 and 2^8, by a power of two; its reciprocal goes into the scale
           const int e = min(max(static_cast<int>(top >> 7), 14), 254) - 127 - 7;
           const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
@@ -821,7 +817,7 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(const PagedArgs a, 
   __shared__ float4 s_o[GR][LPR];
   const PagedDims& s = a.s;
   const List<M::CH> list(a);
-  const Runs<M::FEWEST> runs(list.total(), ctas * kWarps);
+  const Runs runs(list.total(), ctas * kWarps);
   const int x = blockIdx.y, lane = threadIdx.x & 31;
   int b = 0, u = 0, c = 0, last = 0;                               // the unit, and the first and last of its CTAs
   int64_t begin = 0;
