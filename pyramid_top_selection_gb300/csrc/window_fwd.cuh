@@ -26,8 +26,10 @@
 // P is rounded to bf16 for the product (2^-8 relative at most); the sum l takes it unrounded.
 // Bound: the MMA warp, whose four groups of products a step are issued in some 2000 cycles and then
 // waited for; the softmax is not (the time stays without any exponential). 65536 rows of 16 heads over 2, d =
-// 128, a window of 4096: 1.48-1.52 ms a call in rows of calls, which run into the power limit (1.40-1.44 PFLOP/s,
-// 73-75 % of a large library product's burst rate), 1.43 ms in a short burst (1.49 PFLOP/s). S in two halves,
+// 128, a window of 4096: 1.44-1.45 ms a call in rows of calls, which run into the power limit (1.47-1.48 PFLOP/s,
+// 78 % of a large library product's burst rate). An item's first S between the last products of the item before saves some
+// 2 us an item (1.50-1.52 ms with all of an item's products before the next one's); documents of 64 to 2048 tokens
+// lose 1 % by it, 6 prompts of up to 8192 gain 6 % (capped 3 %). S in two halves,
 // the upper one ahead of P's reading: 1.61 ms (64 columns cost 48 cycles a step of 16, 128 columns 64).
 // With few rows (a short chunk against a long context) the items are fewer than the SMs. An item's key
 // tiles are then cut into 2, 4, 8 or 16 runs, one CTA each, the CTAs a cluster: each lays its O, maxima
@@ -257,65 +259,93 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       int n_kv = 0;
       int n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};   // Q tiles, P V products, items of a row tile
       bool issued = false, ok = true;
-      for (int i = 0; ok; ++i) {
-        const win::Item it = get(i);
-        if (it.n < 0) break;
-        const int j0 = run_begin(it), j1 = run_end(it);
-        if (j0 == j1) continue;
-        if (a.stall && !wait(&never, 0)) { ok = false; break; }
-        // key tile j is load n_kv + 2 (j - j0) of the ring, its values are the one after
-        auto landed = [&](int k) { return wait(&kv_full[k % M::NST], (k / M::NST) & 1); };
-        // S of row tile t from the key tile of load k; `last` of the row tile's, `free` the load's last use.
-        // What S needs is waited for while the product before it still runs.
-        auto issue_s = [&](int t, int k, bool last, bool free) -> bool {
-          if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
-          tc::after_sync();
-          if (leader) {
-            win::product_ss<D>(tm + 128 * t, dQ + t * (M::TILE >> 4), dK + k % M::NST * (M::TILE >> 4));
-            tc::commit(&s_full[t]);
-            if (free) tc::commit(&kv_empty[k % M::NST]);
-            if (last) tc::commit(&q_empty[t]);
-          }
-          __syncwarp();
-          return true;
-        };
-        auto issue_pv = [&](int t, int k, bool accumulate, bool free) -> bool {
-          if (!accumulate && !wait(&o_empty[t], (n_o[t]++ & 1) ^ 1)) return false;   // the last item's O is out
-          if (!wait(&p_full[t], n_p[t] & 1)) return false;
-          tc::after_sync();
-          if (leader) {
-            win::product_ts<D, 128>(tm + 256 + D * t, tm + 128 * t, dV + k % M::NST * (M::TILE >> 4), accumulate);
-            tc::commit(&pv_done[t]);
-            if (free) tc::commit(&kv_empty[k % M::NST]);
-          }
-          __syncwarp();
-          ++n_p[t];
-          return true;
-        };
-        const int jf = tile_at(j0, j1, 0), end0 = BACK ? it.first[0] : it.last[0], end1 = BACK ? it.first[1] : it.last[1];   // Q's last tile
-        bool has0 = uses(it, 0, jf), has1 = uses(it, 1, jf), acc0 = false, acc1 = false;
+      // the next item with key tiles, if there is one, and its tiles [j0, j1)
+      win::Item it;
+      int i = 0, j0 = 0, j1 = 0;
+      auto open = [&]() {
+        for (;;) {
+          it = get(i++);
+          if (it.n < 0) return false;
+          j0 = run_begin(it);
+          j1 = run_end(it);
+          if (j0 < j1) return true;
+        }
+      };
+      auto landed = [&](int k) { return wait(&kv_full[k % M::NST], (k / M::NST) & 1); };
+      // S of row tile t from the key tile of load k; `last` of the row tile's, `free` the load's last use.
+      // What S needs is waited for while the product before it still runs.
+      auto issue_s = [&](int t, int k, bool last, bool free) -> bool {
+        if (n_p[t] > 0 && !wait(&pv_done[t], (n_p[t] - 1) & 1)) return false;   // P has been read
+        tc::after_sync();
+        if (leader) {
+          win::product_ss<D>(tm + 128 * t, dQ + t * (M::TILE >> 4), dK + k % M::NST * (M::TILE >> 4));
+          tc::commit(&s_full[t]);
+          if (free) tc::commit(&kv_empty[k % M::NST]);
+          if (last) tc::commit(&q_empty[t]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int t, int k, bool accumulate, bool free) -> bool {
+        if (!accumulate && !wait(&o_empty[t], (n_o[t]++ & 1) ^ 1)) return false;   // the last item's O is out
+        if (!wait(&p_full[t], n_p[t] & 1)) return false;
+        tc::after_sync();
+        if (leader) {
+          win::product_ts<D, 128>(tm + 256 + D * t, tm + 128 * t, dV + k % M::NST * (M::TILE >> 4), accumulate);
+          tc::commit(&pv_done[t]);
+          if (free) tc::commit(&kv_empty[k % M::NST]);
+        }
+        __syncwarp();
+        ++n_p[t];
+        return true;
+      };
+      // An item's first S is issued among the products of the last item's last tile.
+      bool has0 = false, has1 = false, acc0 = false, acc1 = false;
+      int jf = 0, end0 = 0, end1 = 0;          // the first tile, and Q's last
+      auto enter = [&](int t, int k) -> bool {
+        const bool has = t ? has1 : has0;
+        if (it.last[t] >= 0 && !wait(&q_full[t], n_q[t]++ & 1)) return false;
+        return !has || issue_s(t, k, (t ? end1 : end0) == jf, t ? true : !has1);
+      };
+      auto begin = [&]() {
+        jf = tile_at(j0, j1, 0);
+        end0 = BACK ? it.first[0] : it.last[0];
+        end1 = BACK ? it.first[1] : it.last[1];
+        has0 = uses(it, 0, jf);
+        has1 = uses(it, 1, jf);
         issued = true;
-        ok = landed(n_kv) && (it.last[0] < 0 || wait(&q_full[0], n_q[0]++ & 1));
-        if (ok && has0) ok = issue_s(0, n_kv, end0 == jf, !has1);
-        ok = ok && (it.last[1] < 0 || wait(&q_full[1], n_q[1]++ & 1));
-        if (ok && has1) ok = issue_s(1, n_kv, end1 == jf, true);
-        ok = ok && landed(n_kv + 1);
-        for (int j = j0; ok && j < j1; ++j) {
+      };
+      bool more = open();
+      if (more) {
+        if (a.stall) ok = wait(&never, 0);
+        begin();
+        ok = ok && landed(0) && enter(0, 0) && enter(1, 0) && landed(1);
+      }
+      while (ok && more) {
+        acc0 = acc1 = false;
+        for (int j = j0; j + 1 < j1; ++j) {
           const int k = n_kv + 2 * (j - j0) + 1, jn = tile_at(j0, j1, j - j0 + 1);
-          const bool more = (!SPLIT && !BACK) || j + 1 < j1; // (an item's last tile has no next one anyway)
-          const bool next0 = more && uses(it, 0, jn), next1 = more && uses(it, 1, jn);
+          const bool next0 = uses(it, 0, jn), next1 = uses(it, 1, jn);
           if (has0 && !issue_pv(0, k, acc0, !has1)) { ok = false; break; }
-          if (j + 1 < j1 && !landed(k + 1)) { ok = false; break; }
+          if (!landed(k + 1)) { ok = false; break; }
           if (next0 && !issue_s(0, k + 1, end0 == jn, !next1)) { ok = false; break; }
           if (has1 && !issue_pv(1, k, acc1, true)) { ok = false; break; }
-          if (j + 1 < j1 && !landed(k + 2)) { ok = false; break; }
+          if (!landed(k + 2)) { ok = false; break; }
           if (next1 && !issue_s(1, k + 1, end1 == jn, true)) { ok = false; break; }
           acc0 |= has0;
           acc1 |= has1;
           has0 = next0;
           has1 = next1;
         }
+        if (!ok) break;
         n_kv += 2 * (j1 - j0);
+        const bool pv0 = has0, pv1 = has1;
+        more = open();
+        if (more) begin();
+        if (pv0 && !issue_pv(0, n_kv - 1, acc0, !pv1)) { ok = false; break; }
+        if (more && !(landed(n_kv) && enter(0, n_kv))) { ok = false; break; }
+        if (pv1 && !issue_pv(1, n_kv - 1, acc1, true)) { ok = false; break; }
+        if (more) ok = enter(1, n_kv) && landed(n_kv + 1);
       }
       if (issued) {
         if (leader) tc::commit(&drain);
