@@ -119,7 +119,7 @@ const char* pisa_last_error(void);
 int pisa_set_wait_limit(uint64_t limit_ns);
 
 /* Test aid (no counterpart on the pages): with on != 0, the tensor-core kernels of the
- * following pisa_select and pisa_sparse_attn_fwd launches wait, after their first key tile is
+ * following launches (selection, selected blocks', window and documents' attention) wait, after their first key tile is
  * issued and before their first MMA, on a barrier that nothing signals, so that the wait
  * runs out after the wait limit and the give-up path runs (status PISA_STATUS_TIMEOUT,
  * poisoned outputs). Process-wide; 0 turns it off. Host-only, no CUDA call. */
@@ -412,10 +412,12 @@ int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const v
  * O, dO, dQ [T,Hq,d], dK, dV [T,Hkv,d] bf16 and lse [Hq,T] fp32 contiguous; starts device
  * [n_docs + 1] int32, not descending (else results are undefined, but nothing outside the
  * buffers is touched); prefix device [n_docs] int32; slopes device [Hq] fp32, finite. d in {64, 128}, G = Hq / Hkv
- * <= 64, T <= 2^24, T*Hq < 2^31, n_docs <= 2^24, cap 0 or in [2^-10, 2^20]. max_len: the longest document, as far as the caller
+ * <= 64, T <= 2^24, T*Hq < 2^31, n_docs <= 2^24, cap 0 or in [2^-10, 2^20] and at
+ * least scale / 1024. max_len: the longest document, as far as the caller
  * knows (0: T); how work is cut follows it, results do not depend on it beyond the order of the sums.
  * Nothing written (outputs, the workspace) may overlap anything that is read, nor one another.
- * Non-finite values at one document's tokens can reach rows of another that lie within 256 tokens of it. */
+ * Non-finite values of one document can reach results (rows, gradients) of other documents' tokens that lie within 256
+ * tokens of that document: tiles that hold both multiply them by weights of 0. */
 typedef struct {
   int32_t T, Hq, Hkv, d, n_docs, max_len;
   float scale, cap;
@@ -495,7 +497,8 @@ int pisa_paged_workspace_size(const pisa_paged_shape_t* shape, size_t* bytes);
  *   len device [B] int32: tokens in the cache, the new ones included; clamped to [0, max_pages*page], with
  *   PISA_STATUS_POS_RANGE where that changes it. A page outside [0, n_pages) sets the same bit and its keys are not
  *   seen. q [B,nq,Hq,d] bf16, slopes [Hq] fp32 or NULL (read); o [B,nq,Hq,d] bf16, lse [B,nq,Hq] fp32 (may be
- *   NULL) (written). What lies in slots behind a sequence's end is never used, whatever it is.
+ *   NULL) (written). What lies in slots behind a sequence's end is never used, whatever it is; values at the newest
+ *   nq - 1 keys have to be finite for the queries that do not see them.
  * The order of the sums follows the lengths and the GPU's SM count only.
  * Nothing written (o, lse, the workspace) may overlap anything that is read, nor one another. */
 int pisa_paged_attn(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const int32_t* table,

@@ -294,9 +294,12 @@ int rope_dims(const pisa_rope_shape_t* s, pisa::RopeDims* o) {
 
 // ---- packed documents, paged cache
 
-int check_cap(float cap) {
-  if (cap == 0.f || (cap >= 0x1p-10f && cap <= 0x1p20f)) return PISA_OK;
-  return fail(PISA_EINVAL, "cap=%g must be 0 or in [2^-10, 2^20]", static_cast<double>(cap));
+// (the kernels hold up to the eighth power of scale / cap in 32 bits)
+int check_cap(float cap, float scale) {
+  if (cap == 0.f) return PISA_OK;
+  if (!(cap >= 0x1p-10f && cap <= 0x1p20f)) return fail(PISA_EINVAL, "cap=%g must be 0 or in [2^-10, 2^20]", static_cast<double>(cap));
+  if (scale / cap > 1024.f) return fail(PISA_EUNSUPPORTED, "scale/cap=%g exceeds 1024", static_cast<double>(scale / cap));
+  return PISA_OK;
 }
 
 int check_group(int Hq, int Hkv, int d) {
@@ -315,7 +318,7 @@ int doc_dims(const pisa_doc_shape_t* s, pisa::DocDims* o) {
   if (static_cast<int64_t>(s->T) * s->Hq >= (int64_t(1) << 31))
     return fail(PISA_EUNSUPPORTED, "T*Hq=%lld exceeds 2^31", static_cast<long long>(s->T) * s->Hq);
   PISA_CHECK(check_scale(s->scale, "scale"));
-  PISA_CHECK(check_cap(s->cap));
+  PISA_CHECK(check_cap(s->cap, scale_or_default(s->scale, s->d)));
   pisa::DocDims d{};
   PISA_CHECK(check_stride(s->q_stride, s->Hq, s->d, "q_stride", &d.qs));
   PISA_CHECK(check_stride(s->k_stride, s->Hkv, s->d, "k_stride", &d.ks));
@@ -354,7 +357,7 @@ int paged_dims(const pisa_paged_shape_t* s, pisa::PagedDims* o) {
   if (static_cast<int64_t>(s->n_pages) * s->page >= (int64_t(1) << 39) / s->d / s->Hkv)
     return fail(PISA_EUNSUPPORTED, "n_pages*page*Hkv*d exceeds 2^39");
   PISA_CHECK(check_scale(s->scale, "scale"));
-  PISA_CHECK(check_cap(s->cap));
+  PISA_CHECK(check_cap(s->cap, scale_or_default(s->scale, s->d)));
   pisa::PagedDims d{};
   d.B = s->B; d.Hq = s->Hq; d.Hkv = s->Hkv; d.d = s->d; d.n_pages = s->n_pages; d.page = s->page;
   d.max_pages = s->max_pages; d.bits = s->bits; d.nq = s->nq;

@@ -29,7 +29,8 @@ PAGED = dict(B=2, Hq=4, Hkv=2, d=64, n_pages=8, page=16, max_pages=4)
     (dict(T=0), EINVAL, "positive"), (dict(n_docs=0), EINVAL, "positive"), (dict(Hq=5), EINVAL, "multiple"),
     (dict(d=96), EUNSUP, "head dim"), (dict(Hq=130), EUNSUP, "GQA group"), (dict(T=(1 << 24) + 1), EUNSUP, "2^24"),
     (dict(T=1 << 24, Hq=128, Hkv=128), EUNSUP, "2^31"), (dict(cap=-1.0), EINVAL, "cap"), (dict(cap=1e-9), EINVAL, "cap"),
-    (dict(cap=math.nan), EINVAL, "cap"), (dict(cap=math.inf), EINVAL, "cap"), (dict(scale=math.inf), EINVAL, "scale"),
+    (dict(cap=math.nan), EINVAL, "cap"), (dict(cap=math.inf), EINVAL, "cap"),
+    (dict(cap=2.0 ** -10, scale=1.5), EUNSUP, "1024"), (dict(scale=math.inf), EINVAL, "scale"),
     (dict(scale=-1.0), EINVAL, "scale"), (dict(q_stride=255), EINVAL, "q_stride"), (dict(k_stride=64), EINVAL, "k_stride"),
     (dict(v_stride=132), EINVAL, "v_stride"),
 ])
@@ -46,7 +47,7 @@ def test_document_shapes_are_checked(change, code, text):
     (dict(bits=8), EUNSUP, "bits"), (dict(page=8), EUNSUP, "page"), (dict(page=48), EUNSUP, "page"), (dict(page=2048), EUNSUP, "page"),
     (dict(max_pages=(1 << 20) + 1), EUNSUP, "2^24"), (dict(nq=0), EUNSUP, "nq"), (dict(nq=17), EUNSUP, "nq"),
     (dict(B=1 << 23), EUNSUP, "2^24"), (dict(n_pages=(1 << 31) - 1, page=1024), EUNSUP, "2^39"), (dict(Hq=1 << 16, Hkv=1 << 16, page=1024), EUNSUP, "2^30"),
-    (dict(B=1 << 12, Hq=1 << 10, Hkv=1 << 8, max_pages=1 << 20), EUNSUP, "2^44"), (dict(cap=2e6), EINVAL, "cap"),
+    (dict(B=1 << 12, Hq=1 << 10, Hkv=1 << 8, max_pages=1 << 20), EUNSUP, "2^44"), (dict(cap=2e6), EINVAL, "cap"), (dict(cap=0.5, scale=1e4), EUNSUP, "1024"),
     (dict(scale=math.nan), EINVAL, "scale"),
 ])
 def test_paged_shapes_are_checked(change, code, text):

@@ -108,6 +108,18 @@ def test_peaked_scores(cap, biased):
         check(n, got[n], want[n], tol[n])
 
 
+@pytest.mark.parametrize("biased", [False, True])
+def test_the_smallest_cap(biased):
+    # scale / cap at its limit: scores of 0 stay 0, all others are +-cap
+    Q, K, V, dO = _inputs(300, 4, 2, 64, seed=15)
+    Q[::3], K[::5] = 0, 0
+    starts, slopes, cap = [0, 170, 300], _slopes(4) if biased else None, 2.0 ** -10
+    got = _run(Q, K, V, dO, _ints(starts), None, slopes, cap, 1.0)
+    want, tol = doc_attention(Q, K, V, starts, None, slopes, cap, 1.0, dO=dO)
+    for n in want:
+        check(n, got[n], want[n], tol[n])
+
+
 def test_scores_that_grow_with_distance():
     # negative slopes: the farthest key wins, row by row
     Q, K, V, dO = _inputs(400, 2, 1, 64, seed=4)
