@@ -99,9 +99,10 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
     it.SP = 0;
     it.n = all.hi < all.lo ? 0 : (all.hi - all.lo + 128) >> 7;
     it.first[0] = (r0.lo - it.lo) >> 7;
-    it.last[0] = r0.hi < r0.lo ? -1 : (r0.hi - it.lo) >> 7;
+    // (no further than the item's, also where starts that descend say so)
+    it.last[0] = r0.hi < r0.lo ? -1 : (min(r0.hi, all.hi) - it.lo) >> 7;
     it.first[1] = (r1.lo - it.lo) >> 7;
-    it.last[1] = r1.hi < r1.lo ? -1 : (r1.hi - it.lo) >> 7;
+    it.last[1] = r1.hi < r1.lo ? -1 : (min(r1.hi, all.hi) - it.lo) >> 7;
     return it;
   }
   it.L = win::valid_len(a.len, it.b, s.N);

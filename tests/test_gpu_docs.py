@@ -333,3 +333,37 @@ def test_two_graphs_share_workspaces():
         torch.cuda.synchronize()
         for a, b in zip(got[k], want[k]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_tokens_past_32_bits(fused):
+    # elements beyond 2^31 (bytes beyond 2^32): the last documents of many, against their definition
+    T, Hq, Hkv, d, n = (1 << 18) + 300, 64, 1, 128, 300
+    few = _inputs(n, Hq, Hkv, d, seed=16)
+    if fused:
+        x = torch.zeros(T, Hq + 2 * Hkv, d, dtype=bf16, device="cuda")
+        Q, K, V = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+    else:
+        Q, K, V = (torch.zeros(T, h, d, dtype=bf16, device="cuda") for h in (Hq, Hkv, Hkv))
+    dO = torch.zeros(T, Hq, d, dtype=bf16, device="cuda")
+    for t, x in zip((Q, K, V, dO), few):
+        t[-n:] = x
+    starts = list(range(0, T - n, 1 << 12)) + [T - n, T - 120, T]
+    got = _run(Q, K, V, dO, _ints(starts), max_len=1 << 12)
+    want, tol = doc_attention(*few[:3], [0, 180, 300], dO=few[3])
+    for name in want:
+        check(name, got[name][:, -n:] if name == "lse" else got[name][-n:], want[name], tol[name])
+    assert not bool(got["O"][:-n].any()) and not bool(got["dQ"][:-n].any())
+
+
+@pytest.mark.parametrize("T,seed", [(500, 0), (500, 1), (6000, 2), (6000, 3)])
+def test_starts_in_no_order_are_survived(T, seed):
+    # what comes out is not defined, but the calls end, without a wait that gives up
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    Q, K, V, dO = _inputs(T, 16, 2, 64, seed=17)
+    starts = torch.randint(-T, 2 * T, (41,), generator=g, device="cuda").to(torch.int32)
+    prefix = torch.randint(-T, 2 * T, (40,), generator=g, device="cuda").to(torch.int32)
+    _run(Q, K, V, dO, starts, prefix, max_len=T // 8)
+    Q, K, V, dO = _inputs(T, 16, 2, 64, seed=18)
+    for t in _run(Q, K, V, dO, _ints([0, T]), None).values():
+        assert bool(t.isfinite().all())
