@@ -7,7 +7,7 @@
 // ties.
 //
 // Bound: memory in 16 bits (49K tokens of 16 heads over 2, d = 128: 82.5 us, 6.07 TB/s); in 4 bits the arithmetic
-// (5127 tokens of 32 heads over 8: 34 us, 3.2 TB/s, some 180 instructions for two rows, issued in 62 % of the cycles; with 1.4
+// (5127 tokens of 32 heads over 8: 33.4 us, 3.3 TB/s, some 180 instructions for two rows, issued in 62 % of the cycles; with 1.4
 // tokens a warp, the busiest warps' share is 1.3 times the mean). One warp takes one token and runs over its queries, then its keys and values as one list of rows, in steps
 // of four rounds of 512 bytes that arrive by cp.async in the warp's ring, two steps ahead of the arithmetic; the slots
 // of 32 tokens of a warp are looked up at once, a lane each. With few tokens a warp takes a step.
@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
   __shared__ __align__(16) float2 table[kWarps][D / 2];
   const PagedDims& s = a.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / LPR, e = 8 * (lane % LPR);
+  win::grid_wait();                                        // launched while the kernel before ends
+  win::launch_dependents();
   unsigned char* ring = ring_all + warp * kAhead * STEP;
   const Lane<D, IL> L(lane, a.t.rot, a.inv_freq, table[warp]);
   const int stride = static_cast<int>(gridDim.x) * kWarps;
@@ -266,8 +268,8 @@ int append_launch(const AppendArgs& a, int blocks, cudaStream_t st) {
   constexpr int smem = kWarps * kAhead * kRound * 512;
   if (int e = ready(append_kernel<D, IL, NORM, FOUR>, smem)) return e;
   ProfScope ps(st, "paged_append");
-  append_kernel<D, IL, NORM, FOUR><<<blocks, 32 * kWarps, smem, st>>>(a);
-  return cudaGetLastError();
+  const win::Behind b(dim3(blocks), 32 * kWarps, smem, st);
+  return cudaLaunchKernelEx(&b.cfg, append_kernel<D, IL, NORM, FOUR>, a);
 }
 
 template <int D, bool FOUR>

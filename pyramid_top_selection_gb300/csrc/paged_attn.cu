@@ -5,7 +5,7 @@
 // to 16384 tokens, 32 heads over 8, d = 128, pages of 64: 172 us in 16 bits (6.48 TB/s), 72 in 4 bits (4.35 TB/s: there each
 // of 12 warps an SM issues an instruction every five cycles, 620 for a chunk of 4.6 KB, of which 260 turn and
 // scale codes; with 128 registers and 16 warps 76 us, with a ring of four stages 72.6). One sequence of 131072 tokens in 4
-// bits, 16 heads over 2: 22.4 us, of 64 tokens 11: two kernels' start, three reads that wait for one another, and the joins.
+// bits, 16 heads over 2: 22.3 us, of 64 tokens 11: two kernels' start, three reads that wait for one another, and the joins.
 //
 // All chunks of all (sequence, KV head, set of rows) units form one list, which is cut into equal runs, one a warp: lengths
 // may differ as they like, the work is the same everywhere. The list follows from the lengths, which only the device
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
   __shared__ int s_bad[kWarps][M::ST], s_flag;
   const PagedDims& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, p2 = lane & 3;
+  win::grid_wait();                                                // launched while the kernel before ends
   const List<CH> list(a);
   const Runs runs(list.total(), static_cast<int>(gridDim.x) * kWarps);
   if (blockIdx.x * kWarps >= runs.n) {
@@ -821,6 +822,7 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(const PagedArgs a, 
   __shared__ float s_m[GR], s_l[GR];
   __shared__ float4 s_o[GR][LPR];
   const PagedDims& s = a.s;
+  win::launch_dependents();                                        // (what may start now waits for all of this kernel before it reads or writes)
   const List<M::CH> list(a);
   const Runs runs(list.total(), ctas * kWarps);
   const int x = blockIdx.y, lane = threadIdx.x & 31;
@@ -946,26 +948,20 @@ int attn_launch(PagedArgs& a, cudaStream_t st) {
   a.units = a.s.Hkv * a.sets;
   {
     ProfScope ps(st, "paged_attn");
-    paged_attn_kernel<D, FOUR, NT><<<ctas, 32 * kWarps, M::bytes, st>>>(a);
+    const win::Behind b(dim3(ctas), 32 * kWarps, M::bytes, st);
+    const PagedArgs& ca = a;
+    if (cudaError_t e = cudaLaunchKernelEx(&b.cfg, paged_attn_kernel<D, FOUR, NT>, ca)) return e;
   }
-  if (cudaError_t e = cudaGetLastError()) return e;
   ProfScope ps(st, "paged_join");
   // a unit a block where they are fewer than the CTAs, with more threads where they have many parts each
   const int64_t units = static_cast<int64_t>(a.s.B) * a.units;
   const bool by_unit = units < ctas, many = units * 16 < ctas;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(by_unit ? units : std::max(1, ctas - 1)), static_cast<unsigned>(std::min(M::COLS, a.rows)));
-  cfg.blockDim = dim3(many ? 512 : 128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  const win::Behind b(dim3(static_cast<unsigned>(by_unit ? units : std::max(1, ctas - 1)), static_cast<unsigned>(std::min(M::COLS, a.rows))),
+                      many ? 512 : 128, 0, st);
   const PagedArgs& ca = a;
-  if (many) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT, 512, true>, ca, ctas);
-  if (by_unit) return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT, 128, true>, ca, ctas);
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, FOUR, NT, 128, false>, ca, ctas);
+  if (many) return cudaLaunchKernelEx(&b.cfg, paged_join_kernel<D, FOUR, NT, 512, true>, ca, ctas);
+  if (by_unit) return cudaLaunchKernelEx(&b.cfg, paged_join_kernel<D, FOUR, NT, 128, true>, ca, ctas);
+  return cudaLaunchKernelEx(&b.cfg, paged_join_kernel<D, FOUR, NT, 128, false>, ca, ctas);
 }
 
 template <int D, bool FOUR>
