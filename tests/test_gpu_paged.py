@@ -499,3 +499,53 @@ def test_two_graphs_share_a_workspace(bits):
     torch.cuda.synchronize()
     for x, y in zip(out, want):
         assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_captured_behind_two_streams(bits):
+    # the calls' inputs come from two streams that meet right before them, in a graph and outside
+    g = _gen(24)
+    B, Hq, Hkv, d, page, n = 3, 8, 2, 128, 16, 90
+    table, pool = _table(g, [n + 1] * B, page)
+    shape = pisa.make_paged_shape(B, Hq, Hkv, d, pool, page, table.shape[1], bits)
+    cache = _filled(g, shape)
+    K, V, Q = (_randn(g, B, h, d) for h in (Hkv, Hkv, Hq))
+    pos, lens = _ints([n] * B), _ints([n + 1] * B)
+    rope = pisa.Rope(pisa.rope_frequencies(d)[0].cuda(), d, norm=False)
+    starts = _ints([0, 2, 3])
+    out = [torch.empty(B, Hq, d, dtype=bf16, device="cuda"), torch.empty(B, 1, Hq, d, dtype=bf16, device="cuda"),
+           torch.empty(B, Hq, d, dtype=bf16, device="cuda")]
+    status, ws = _ints([0, 0, 0, 0]), pisa.paged_workspace(shape, "cuda")
+    lse, dlse = torch.empty(B, 1, Hq, device="cuda"), torch.empty(Hq, B, device="cuda")
+    k, v, q = (torch.empty_like(x) for x in (K, V, Q))
+    other = torch.cuda.Stream()
+
+    def meet(work):
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            k.copy_(K * 1)
+            v.copy_(V * 1)
+        q.copy_(Q * 1)
+        here.wait_stream(other)
+        work()
+
+    def run():
+        meet(lambda: pisa.paged_append(shape, cache, table, pos, k, v, Q=q, rope=rope, q_out=out[0], status=status))
+        meet(lambda: pisa.paged_attn(shape, cache, table, lens, out[0][:, None], ws=ws, o=out[1], lse=lse))
+        meet(lambda: pisa.doc_attn_fwd(q, k, v, starts, pisa.doc_shape_of(q, k, v, starts), out=out[2], lse=dlse))
+
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (*out, lse, dlse)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        for t in (k, v, q, *out, lse, dlse):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*out, lse, dlse), want):
+            assert torch.equal(a, b)
+    assert int(status[0]) == 0 and pisa.workspace_status(ws) == 0
