@@ -50,7 +50,7 @@ bool rows_laid_out(const DocDims& s) { return fwd_items(s) > win::kPlanSms; }
 
 }  // namespace
 
-size_t doc_fwd_ws(const DocDims& s) { return 256 + (rows_laid_out(s) ? doc_rows_bytes(s, fwd_tile(s)) : 0); }
+size_t doc_fwd_ws(const DocDims& s) { return 256 + (rows_laid_out(s) ? doc_rows_bytes(s, fwd_tile(s), false) : 0); }
 
 int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V, const DocMask& m, void* O, float* lse,
                    char* ws, void* stream) {
@@ -82,7 +82,7 @@ int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V
     }
     return s.d == 128 ? doc_fwd_by_scores<128, win::kSearch>(a, map, st) : doc_fwd_by_scores<64, win::kSearch>(a, map, st);
   }
-  if (int e = launch_doc_rows(s, m, 2 * a.tok, ws + 256, a.status, &a.docs, st)) return e;
+  if (int e = launch_doc_rows(s, m, 2 * a.tok, false, ws + 256, a.status, &a.docs, st)) return e;
   return s.d == 128 ? doc_fwd_by_scores<128, 0>(a, map, st) : doc_fwd_by_scores<64, 0>(a, map, st);
 }
 

@@ -4,7 +4,8 @@
 // as bf16 has it where a row tile sees more than two key tiles: with peaked scores that rounding adds a tenth to the gradients'
 // error (0.0024 to 0.0026 of their size, rms), and would take a second pass over the keys to avoid.
 // 8192 tokens, 16 heads over 2, d = 128, one document: dQ 274 us, dK and dV 393, their partial sums 12; capped 299 and 537.
-// 35K tokens in 60 documents of 64 to 2048, 16 heads over 4: 254 and 288.
+// 35K tokens in 60 documents of 64 to 2048, 16 heads over 4: 256 and 271 (288 with key tiles in the order of their keys: those that
+// many tokens see come first).
 #pragma once
 
 #include <algorithm>
@@ -82,7 +83,7 @@ int doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const
   if (int e = win::token_map(&map[4], dK, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
   if (int e = win::token_map(&map[5], dV, 1, s.T, s.Hkv, s.d, kd, 1, 32)) return e;
   if (int e = win::token_map(&map[6], O, 1, s.T, s.Hq, s.d, hd, a.P, a.tok)) return e;
-  if (int e = launch_doc_rows(s, m, a.tok, ws + rows_at(s), a.status, &a.docs, st)) return e;
+  if (int e = launch_doc_rows(s, m, a.tok, true, ws + rows_at(s), a.status, &a.docs, st)) return e;
   return doc_bwd_by_scores<D>(a, map, st);
 }
 

@@ -19,6 +19,7 @@ constexpr int kSearch = 8;
 struct DocRows {
   const int4* bounds;      // [T + 1], of() of every token; not with kSearch
   const int32_t* order;    // token tiles, those with the most keys first; not with kSearch
+  const int32_t* key_order;   // tiles of 128 keys, those with the most tokens first; for the backward
   const float* slopes;     // per query head, or NULL
   float cap;               // 0: none
   int32_t T, n_docs;

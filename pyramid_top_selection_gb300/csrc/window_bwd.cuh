@@ -647,20 +647,22 @@ __device__ __forceinline__ int chunk_tiles(int n, int c, int ct, int nc) { retur
 struct DkvItem {
   int b, kv, kt, c, ct;            // chunk c, of ct token tiles, of the key tile's
   int64_t slot;                    // partial sums' slot, -1: the only chunk, written as it is
-  __host__ __device__ DkvItem(const BwdArgs& a, int w) {
+  // order: the key tiles' (NULL: as they come)
+  __device__ DkvItem(const BwdArgs& a, int w, const int32_t* order) {
     const bool sink = w < a.n_snk;
     const int x = sink ? w : w - a.n_snk, tiles = sink ? a.n_st : a.n_kt - a.n_st;
     const int bh = x % a.n_bh;
     kt = x / a.n_bh % tiles + (sink ? 0 : a.n_st);
+    if (order) kt = order[kt];
     c = x / a.n_bh / tiles;
     b = bh / a.s.Hkv;
     kv = bh % a.s.Hkv;
     ct = run_of(a, kt);
     slot = (sink ? a.ncs : a.nck) == 1 ? -1 : slot_of(a, kt, bh, c);
   }
-  static __host__ __device__ int run_of(const BwdArgs& a, int kt) { return kt < a.n_st ? a.cts : a.ct; }
+  static __device__ int run_of(const BwdArgs& a, int kt) { return kt < a.n_st ? a.cts : a.ct; }
   // slots: sink tiles first ([kt][bh][ncs], where these are cut), then the others ([kt][bh][nck])
-  static __host__ __device__ int64_t slot_of(const BwdArgs& a, int kt, int bh, int c) {
+  static __device__ int64_t slot_of(const BwdArgs& a, int kt, int bh, int c) {
     if (kt < a.n_st) return (static_cast<int64_t>(kt) * a.n_bh + bh) * a.ncs + c;
     return (a.ncs > 1 ? a.n_snk : 0) + (static_cast<int64_t>(kt - a.n_st) * a.n_bh + bh) * a.nck + c;
   }
@@ -694,7 +696,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
   const uint32_t aK = tc::su32(sm + M::oK), aV = tc::su32(sm + M::oV), aQ = tc::su32(sm + M::oQ), aO = tc::su32(sm + M::oO);
 
-  const DkvItem it(a, blockIdx.x);
+  const DkvItem it(a, blockIdx.x, MASK == win::kWindow ? nullptr : a.docs.key_order);
   const int kb = 128 * it.kt, L = end_of<MASK>(a, it.b);
   const int begin = MASK == win::kWindow ? 0 : a.docs.bounds[s.N].x;     // the first document's first token
   const TokenRange tr = tokens_of<MASK>(a, L, it.kt);
