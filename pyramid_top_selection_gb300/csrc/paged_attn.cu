@@ -889,8 +889,8 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(const PagedArgs a, 
     oo.w *= f0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+      if (k0 + k * GR > last) continue;                            // no part (a part's NaN goes on, whatever its factor)
       const float f = tc::ex2(pm[k] - base_of(top));
-      if (f == 0.f) continue;                                      // also what is no part, whatever was read for it
       oo.x += f * v[k].x;
       oo.y += f * v[k].y;
       oo.z += f * v[k].z;

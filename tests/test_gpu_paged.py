@@ -549,3 +549,85 @@ def test_captured_behind_two_streams(bits):
         for a, b in zip((*out, lse, dlse), want):
             assert torch.equal(a, b)
     assert int(status[0]) == 0 and pisa.workspace_status(ws) == 0
+
+
+# ------------------------------------------------------------------- visible values that are not finite
+SPREADS = {  # B, nq, Hq, Hkv, d, lens: a unit over all CTAs, units over several, more units than CTAs with one over several
+    "one sequence": (1, 1, 8, 1, 128, [9000]),
+    "a few": (6, 2, 8, 2, 64, [3000, 10, 0, 700, 1234, 5]),
+    "sixteen rows": (2, 4, 8, 2, 128, [4000, 900]),
+    "many": (130, 1, 8, 4, 64, [20000] + [(97 * b) % 500 for b in range(1, 130)]),
+    "within a CTA": (300, 1, 8, 4, 64, [60] * 300),
+}
+
+
+def _spread_case(name, bits, seed):
+    B, nq, Hq, Hkv, d, lens = SPREADS[name]
+    g, page = _gen(seed), 16
+    table, pool = _table(g, lens, page)
+    shape = pisa.make_paged_shape(B, Hq, Hkv, d, pool, page, table.shape[1], bits, nq)
+    return g, shape, _filled(g, shape), table, lens, _randn(g, B, nq, Hq, d)
+
+
+def _put(shape, cache, table, seq, pos, K, V):
+    """Tokens of sequence seq written over those at pos."""
+    _, status = pisa.paged_append(shape, cache, table, _ints(pos), K, V, seq=_ints([seq] * len(pos)))
+    assert int(status[0]) == 0
+
+
+def _same(a, b):
+    return torch.equal(a.nan_to_num(nan=9e9), b.nan_to_num(nan=9e9)) and torch.equal(a.isnan(), b.isnan())
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("name", SPREADS)
+def test_a_query_with_a_nan_gives_nan(name, bits):
+    g, shape, cache, table, lens, q = _spread_case(name, bits, 30)
+    o0, lse0 = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+    q[0, 0, 1, 5] = math.nan
+    o, lse = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+    o0[0, 0, 1], lse0[0, 0, 1] = math.nan, math.nan
+    assert _same(o, o0) and _same(lse, lse0)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("name", SPREADS)
+def test_keys_of_nan_give_nan(name, bits):
+    # a third of a sequence's keys, or two CTAs' part of a long one, in one KV head: parts of a unit see nothing else
+    g, shape, cache, table, lens, q = _spread_case(name, bits, 31)
+    o0, lse0 = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+    n = lens[0]
+    pos = list(range(n // 3, 2 * n // 3)) if n != 9000 else list(range(2560, 2688))
+    k, v = ([x[0][pos] for x in _keys(cache, table, lens[:1], shape.page)])
+    if bits == 16:
+        k[:, 0] = math.nan
+        _put(shape, cache, table, 0, pos, k.to(bf16), v.to(bf16))
+    else:                                                              # (the codes of the others stay as they are)
+        page, slot = _slots(table, [0] * len(pos), pos, shape.page)
+        cache.k_scale.view(torch.uint8)[page, 0, slot] = 0x7f
+    o, lse = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+    G = shape.Hq // shape.Hkv
+    o0[0, :, :G], lse0[0, :, :G] = math.nan, math.nan
+    assert _same(o, o0) and _same(lse, lse0)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("name", SPREADS)
+def test_a_value_of_nan_reaches_its_channels_however_small_its_weight(name, bits):
+    # the first key has all the weight: the others' parts are taken times factors that underflow
+    g, shape, cache, table, lens, q = _spread_case(name, bits, 32)
+    n, d = lens[0], shape.d
+    q[0] = q[0, :1, :1].clone()
+    V = _randn(g, 1, shape.Hkv, d)
+    _put(shape, cache, table, 0, [0], (40 * q[0, :1, :1]).expand(1, shape.Hkv, d).contiguous(), V)
+    low, bad = (-40 * q[0, :1, :1]).expand(1, shape.Hkv, d).contiguous(), V.clone()
+    bad[..., 16:32] = math.nan
+    for p in range(n // 9, n - n // 9, n // 9):
+        _put(shape, cache, table, 0, [p], low, V)
+        o0, lse0 = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+        assert bool(torch.isfinite(o0).all())
+        _put(shape, cache, table, 0, [p], low, bad)
+        o, lse = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+        o0[0, ..., 16:32] = math.nan
+        assert _same(o, o0) and _same(lse, lse0)
+        _put(shape, cache, table, 0, [p], low, V)
