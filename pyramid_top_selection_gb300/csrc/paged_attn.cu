@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
           const int col = 8 * t + 2 * p2 + e, r = con.u % a.sets * M::COLS + col;
           const bool there = col < rows;
           c1[t][e] = scale * __shfl_sync(0xffffffffu, up, 8 * p2 + 4 * e);
-          cz[t][e] = s.cap > 0.f || a.slopes ? 1.f : c1[t][e];
+          // (never 0, which hidden scores of -inf would turn into NaN: a row of zeros takes up = 2^-120, times a small amp)
+          cz[t][e] = s.cap > 0.f || a.slopes ? 1.f : c1[t][e] == 0.f ? 0x1p-126f : c1[t][e];
           slope[t][e] = there && a.slopes ? __ldg(a.slopes + kv * s.G + r % s.G) * kLog2e : 0.f;
           pos[t][e] = there ? con.n - s.nq + r / s.G : -1;
           m[t][e] = neg_inf();

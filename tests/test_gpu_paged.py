@@ -631,3 +631,24 @@ def test_a_value_of_nan_reaches_its_channels_however_small_its_weight(name, bits
         o0[0, ..., 16:32] = math.nan
         assert _same(o, o0) and _same(lse, lse0)
         _put(shape, cache, table, 0, [p], low, V)
+
+
+@pytest.mark.parametrize("cap,biased", [(0.0, False), (4.0, True)])
+@pytest.mark.parametrize("amp", [1e-8, 1e-19, 2.0 ** -64])
+def test_queries_of_zeros_with_small_factors(amp, cap, biased):
+    # what a score is multiplied by may leave 32 bits: a query of zeros, or of tiny values, has equal weights all the same
+    g = _gen(33)
+    lens, page = [33, 1, 70, 4001], 16
+    table, pool = _table(g, lens, page)
+    shape = pisa.make_paged_shape(4, 8, 2, 64, pool, page, table.shape[1], 4, cap=cap)
+    cache = _filled(g, shape)
+    cache = cache._replace(k_amp=torch.tensor([amp, 0.7], device="cuda"))
+    q = _randn(g, 4, 1, 8, 64)
+    q[:, :, ::2] = 0
+    q[:, :, 1] *= 2.0 ** -100
+    slopes = _slopes(8) if biased else None
+    o, lse = pisa.paged_attn(shape, cache, table, _ints(lens), q, slopes)
+    k, v = _keys(cache, table, lens, page)
+    want, tol = paged_attention(q, k, v, lens, slopes, cap)
+    check("o", o, want["O"], tol["O"])
+    check("lse", lse, want["lse"], tol["lse"])
