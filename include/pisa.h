@@ -454,7 +454,7 @@ int pisa_doc_attn_bwd(const pisa_doc_shape_t* shape, const void* Q, const void* 
  *   bits = 16: k, v [n_pages,Hkv,page,d] bf16.
  *   bits = 4:  k, v [n_pages,Hkv,page,d/2] bytes of two codes, the even channel's in the low four bits;
  *              k_scale, v_scale [n_pages,Hkv,page,d/16] e4m3, one for 16 channels; k_amp, v_amp
- *              [Hkv] fp32, positive (NULL: ones). A code (sign, then 0, .5, 1, 1.5, 2, 3, 4 or 6; e2m1)
+ *              [Hkv] fp32, in [2^-64, 2^64] (NULL: ones). A code (sign, then 0, .5, 1, 1.5, 2, 3, 4 or 6; e2m1)
  *              stands for code * scale * amp.
  * table device [B,max_pages] int32; entries behind a sequence's last page are never read. page a power of two in
  * [16, 1024], max_pages*page <= 2^24, d in {64, 128}, G = Hq / Hkv <= 64, 1 <= nq <= 16,

@@ -802,7 +802,8 @@ def doc_attn_bwd(Q, K, V, O, lse, dO, starts, shape: DocShape, prefix=None, slop
 
 class PagedCache(NamedTuple):
     """A paged key/value cache's tensors: k, v [n_pages,Hkv,page,d] bf16, or uint8 [n_pages,Hkv,page,d/2] (two e2m1 codes a
-    byte) with k_scale, v_scale [n_pages,Hkv,page,d/16] float8_e4m3fn and k_amp, v_amp [Hkv] fp32 (None: ones)."""
+    byte) with k_scale, v_scale [n_pages,Hkv,page,d/16] float8_e4m3fn and k_amp, v_amp [Hkv] fp32, 2^-64 to 2^64
+    (None: ones)."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor | None = None

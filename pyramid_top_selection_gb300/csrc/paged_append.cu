@@ -7,7 +7,7 @@
 // ties.
 //
 // Bound: memory in 16 bits (49K tokens of 16 heads over 2, d = 128: 82.5 us, 6.07 TB/s); in 4 bits the arithmetic
-// (5127 tokens of 32 heads over 8: 33.4 us, 3.3 TB/s, some 180 instructions for two rows, issued in 62 % of the cycles; with 1.4
+// (5127 tokens of 32 heads over 8: 34.4 us, 3.2 TB/s, some 180 instructions for two rows, issued in 62 % of the cycles; with 1.4
 // tokens a warp, the busiest warps' share is 1.3 times the mean). One warp takes one token and runs over its queries, then its keys and values as one list of rows, in steps
 // of four rounds of 512 bytes that arrive by cp.async in the warp's ring, two steps ahead of the arithmetic; the slots
 // of 32 tokens of a warp are looked up at once, a lane each. With few tokens a warp takes a step.
@@ -229,15 +229,24 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) append_kernel(const Appe
             if (in && value) *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.c.v) + to * D + e) = u;
             continue;
           }
-          const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+          uint32_t uw[4] = {u.x, u.y, u.z, u.w};
           // the largest magnitude's bits: NaN above infinity above all
           uint32_t top = max16x2(max16x2(uw[0] & 0x7fff7fffu, uw[1] & 0x7fff7fffu), max16x2(uw[2] & 0x7fff7fffu, uw[3] & 0x7fff7fffu));
           top = max(top & 0xffffu, top >> 16);
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           const float* amps = value ? a.c.v_amp : a.c.k_amp;
           const float amp = amps && in ? amps[h] : 1.f, ramp = rcp_approx(amp);
+          // quotients past 4096 all are the largest code (6) of the largest scale (448): they stop there, not at an infinity, which
+          // the remainder would turn into NaN
+          const uint32_t far = (__float_as_uint(amp) + (12u << 23)) >> 16;
+          const bool bad = top >= 0x7f80u;
+          if (top > far) {
+            top = far;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) uw[y] = (uw[y] & 0x80008000u) | __vminu2(uw[y] & 0x7fff7fffu, far * 0x10001u);
+          }
           const float most = __uint_as_float(top << 16);
-          const uint32_t s8 = top >= 0x7f80u ? 0x7fu : paged::to_e4m3(over(amps ? over(most, amp, ramp) : most, 6.f, 1.f / 6.f));
+          const uint32_t s8 = bad ? 0x7fu : paged::to_e4m3(over(amps ? over(most, amp, ramp) : most, 6.f, 1.f / 6.f));
           const float sc = __low2float(paged::from_e4m3x2(static_cast<uint16_t>(s8)));
           const float rs = sc > 0.f ? rcp_approx(sc) : 0.f;      // a scale of 0: codes of 0 (of NaN: whatever, they stand for NaN)
           float x[8];

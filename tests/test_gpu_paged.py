@@ -652,3 +652,25 @@ def test_queries_of_zeros_with_small_factors(amp, cap, biased):
     want, tol = paged_attention(q, k, v, lens, slopes, cap)
     check("o", o, want["O"], tol["O"])
     check("lse", lse, want["lse"], tol["lse"])
+
+
+@pytest.mark.parametrize("amp", [0.1, 1.0 / 3, 1e-3, 3e-12, 2.0 ** -64, 7e8, 2.0 ** 64])
+def test_codes_of_extremes_over_a_factor(amp):
+    # quotients past the largest code and scale, and past 32 bits: the scale stays 448, the codes 6, their signs what they were
+    rows = [[1e38] * 16, [-1e38, 1e38] * 8, [3.38e38, 1.0] * 8, [-3.38e38] + [0.0] * 15, [2688.0 * amp] * 16, [-5376.0 * amp, amp] * 8,
+            [4096.0 * amp, 4097.0 * amp] * 8, [amp, -2 * amp] * 8, [1e30, -1e-30] * 8, [1e-30] * 16, [-0.0, 0.0] * 8, [1e-40] * 16,
+            [math.inf, 1e38] * 8, [math.nan, 1e38] * 8, [6 * amp, 0.25 * amp] * 8, [1e38, -2.0 ** -100] * 8]
+    X = torch.tensor(rows, dtype=torch.float64, device="cuda").reshape(len(rows) // 4, 1, 64).to(bf16)
+    T = X.shape[0]
+    shape = pisa.make_paged_shape(1, 1, 1, 64, 1, 16, 1, bits=4)
+    factor = torch.tensor([amp], device="cuda")
+    cache = pisa.paged_cache(shape, "cuda", factor, factor)
+    pisa.paged_append(shape, cache, _ints([[0]]), _ints(list(range(T))), X, X)
+    x = X[:, 0].double() / factor.double()
+    near = x.float().double()                                          # the quotient in 32 bits, where it has a place there
+    codes, scales = quantise(torch.where(torch.isfinite(X[:, 0]) & torch.isinf(near), x, near))
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        got, got_s = codes_of(t[0, 0, :T]), s[0, 0, :T].double()
+        assert torch.equal(got_s.isnan(), scales.isnan()) and torch.equal(got_s.nan_to_num(), scales.nan_to_num())
+        fine = ~scales.isnan().repeat_interleave(16, -1)
+        assert torch.equal(got[fine], codes[fine])
