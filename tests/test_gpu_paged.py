@@ -674,3 +674,82 @@ def test_codes_of_extremes_over_a_factor(amp):
         assert torch.equal(got_s.isnan(), scales.isnan()) and torch.equal(got_s.nan_to_num(), scales.nan_to_num())
         fine = ~scales.isnan().repeat_interleave(16, -1)
         assert torch.equal(got[fine], codes[fine])
+
+
+# -------------------------------------------------------------------------------------- many of everything
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("name", ["many", "many, sixteen rows", "equal", "equal, sixteen rows", "a thousand", "rows in sets", "rows in sets, drafts"])
+def test_attention_of_many(name, bits):
+    # more units than CTAs (a unit that crosses into the next CTA is found by its place), units that end where a CTA's run does, more
+    # sequences than a few look-ups, and rows in several sets of 16
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    mixed = [30000] + [(b * b * 131) % 2001 for b in range(1, 129)] + [3000]
+    B, nq, Hq, Hkv, d, page, lens = {
+        "many": (130, 1, 8, 4, 64, 16, mixed), "many, sixteen rows": (130, 4, 12, 4, 128, 64, mixed),
+        "equal": (3 * sms // 2, 1, 4, 4, 128, 64, [320] * (3 * sms // 2)),
+        "equal, sixteen rows": (3 * sms // 2, 4, 12, 4, 64, 32, [160] * (3 * sms // 2)),
+        "a thousand": (1003, 1, 2, 1, 64, 16, [(b * b * 17) % 301 for b in range(1003)]),
+        "rows in sets": (3, 1, 48, 1, 128, 64, [5000, 2000, 17]), "rows in sets, drafts": (2, 16, 64, 1, 64, 16, [3000, 40]),
+    }[name]
+    g = _gen(40 + len(name))
+    table, pool = _table(g, lens, page)
+    shape = pisa.make_paged_shape(B, Hq, Hkv, d, pool, page, table.shape[1], bits, nq)
+    cache = _filled(g, shape)
+    q = _randn(g, B, nq, Hq, d)
+    ws = pisa.paged_workspace(shape, "cuda")
+    ws.fill_(0xAB)
+    o, lse = torch.full_like(q, 7.0), torch.full((B, nq, Hq), 7.0, device="cuda")
+    pisa.paged_attn(shape, cache, table, _ints(lens), q, ws=ws, o=o, lse=lse)
+    assert pisa.workspace_status(ws) == 0
+    k, v = _keys(cache, table, lens, page)
+    want, tol = paged_attention(q, k, v, lens)
+    check("o", o, want["O"], tol["O"])
+    check("lse", lse, want["lse"], tol["lse"])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_append_of_more_tokens_than_one_look_up(bits):
+    # every warp looks 32 units up at a time: some 117K tokens on 152 SMs, here more, and behind those padding, tokens out of
+    # range and pages that are none
+    g = _gen(41)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B, Hq, Hkv, d, page = 3, 1, 1, 64, 128
+    T = sms * 24 * 32 + 33333
+    n = T // B
+    lens = [n, n, T - 2 * n]
+    table, pool = _table(g, lens, page)
+    table[2, 30] = pool
+    shape = pisa.make_paged_shape(B, Hq, Hkv, d, pool, page, table.shape[1], bits)
+    cache = _filled(g, shape)
+    x = _randn(g, T, Hq + 2 * Hkv, d)
+    Q, K, V = x[:, :1], x[:, 1:2], x[:, 2:]
+    seq = torch.arange(B, device="cuda").repeat_interleave(torch.tensor(lens, device="cuda"))
+    pos = torch.cat([torch.arange(m, device="cuda") for m in lens])
+    late = torch.arange(T, device="cuda") > T - 20000
+    skip = late & (torch.randint(0, 4, (T,), generator=g, device="cuda") == 0)
+    off = late & ~skip & (torch.randint(0, 5, (T,), generator=g, device="cuda") == 0)
+    none = (seq == 2) & (pos // page == 30)
+    inv = pisa.rope_frequencies(d)[0].cuda()
+    rope = pisa.Rope(inv, d, q_weight=1 + 0.1 * torch.randn(d, generator=g, device="cuda"), k_weight=torch.ones(d, device="cuda"))
+    s = pisa.rope_shape_of(Q[None], K[None], d)
+    Qr, Kr = pisa.qk_norm_rope(Q[None], K[None], inv, s, rope.q_weight, rope.k_weight, pos.to(torch.int32)[None])
+    before = [None if t is None else t.clone() for t in cache[:4]]
+    given = torch.where(off, pos + (1 << 24), pos)
+    q_out = torch.full(Q.shape, 7.0, dtype=bf16, device="cuda")
+    got, status = pisa.paged_append(shape, cache, table, given.to(torch.int32), K, V, Q=Q, seq=torch.where(skip, -1, seq).to(torch.int32),
+                                    rope=rope, q_out=q_out)
+    assert int(status[0]) == pisa.STATUS_POS_RANGE
+    kept = ~(skip | off | none)
+    assert bool((got[~kept] == 7.0).all()) and torch.equal(got[kept], Qr[0][kept])
+    page_of, slot = table[seq[kept], pos[kept] // page].long(), pos[kept] % page
+    for t, sc, amp, src, old, old_s in ((cache.k, cache.k_scale, cache.k_amp, Kr[0], before[0], before[2]),
+                                        (cache.v, cache.v_scale, cache.v_amp, V, before[1], before[3])):
+        if bits == 16:
+            old[page_of, :, slot] = src[kept]
+            assert torch.equal(t, old)
+            continue
+        codes, scales = quantise((src[kept].float() / amp[:, None]).double())
+        c = codes.to(torch.uint8).reshape(*codes.shape[:2], -1, 2)
+        old[page_of, :, slot] = c[..., 0] | c[..., 1] << 4
+        old_s.view(torch.uint8)[page_of, :, slot] = scales.float().to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(t, old) and torch.equal(sc.view(torch.uint8), old_s.view(torch.uint8))
