@@ -98,11 +98,15 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
     it.lo = all.lo;
     it.SP = 0;
     it.n = all.hi < all.lo ? 0 : (all.hi - all.lo + 128) >> 7;
-    it.first[0] = (r0.lo - it.lo) >> 7;
-    // (no further than the item's, also where starts that descend say so)
-    it.last[0] = r0.hi < r0.lo ? -1 : (min(r0.hi, all.hi) - it.lo) >> 7;
-    it.first[1] = (r1.lo - it.lo) >> 7;
-    it.last[1] = r1.hi < r1.lo ? -1 : (min(r1.hi, all.hi) - it.lo) >> 7;
+    // (a row tile's key tiles are some of the item's, or none, also where starts that descend say otherwise: Q's place is given back
+    // at one of them)
+    auto ends = [&](const win::DocRange<MASK>& r, int& first, int& last) {
+      first = max(0, (r.lo - it.lo) >> 7);
+      last = r.hi < r.lo ? -1 : (min(r.hi, all.hi) - it.lo) >> 7;
+      if (last < first) last = -1;
+    };
+    ends(r0, it.first[0], it.last[0]);
+    ends(r1, it.first[1], it.last[1]);
     return it;
   }
   it.L = win::valid_len(a.len, it.b, s.N);

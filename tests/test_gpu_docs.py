@@ -1,6 +1,7 @@
 """Attention over packed documents on the GPU against its 64-bit definition: forward and backward, causal and prefix
 masks, capped and distance-biased scores, with bounds that count the kernels' roundings (_docs_ref.py)."""
 import math
+import random
 
 import pytest
 import torch
@@ -366,4 +367,17 @@ def test_starts_in_no_order_are_survived(T, seed):
     _run(Q, K, V, dO, starts, prefix, max_len=T // 8)
     Q, K, V, dO = _inputs(T, 16, 2, 64, seed=18)
     for t in _run(Q, K, V, dO, _ints([0, T]), None).values():
+        assert bool(t.isfinite().all())
+
+
+@pytest.mark.parametrize("cap", [0.0, 7.0])
+@pytest.mark.parametrize("seed", [11, 42, 44, 45])
+def test_starts_in_no_order_are_survived_with_biased_scores(seed, cap):
+    # starts with a row tile whose first key lies before its item's (tokens in 16s, two row tiles an item)
+    T, r = 6000, random.Random(seed)
+    starts = [r.randint(-T, 2 * T) for _ in range(41)]
+    prefix = [r.randint(-T, 2 * T) for _ in range(40)]
+    Q, K, V, dO = _inputs(T, 64, 8, 64, seed=19)
+    _run(Q, K, V, dO, _ints(starts), _ints(prefix), _slopes(64), cap, max_len=T // 8)
+    for t in _run(Q, K, V, dO, _ints([0, T]), None, _slopes(64), cap).values():
         assert bool(t.isfinite().all())
