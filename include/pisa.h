@@ -416,8 +416,9 @@ int pisa_qk_norm_rope_bwd(const pisa_rope_shape_t* shape, const void* Q, const v
  * least scale / 1024. max_len: the longest document, as far as the caller
  * knows (0: T); how work is cut follows it, results do not depend on it beyond the order of the sums.
  * Nothing written (outputs, the workspace) may overlap anything that is read, nor one another.
- * Non-finite values of one document can reach results (rows, gradients) of other documents' tokens that lie within 256
- * tokens of that document: tiles that hold both multiply them by weights of 0. */
+ * Non-finite values reach the rows that see them (and gradients through those rows) as sums over visible pairs have it, and
+ * nothing else; what they spoil of a tile beside that is formed once more, pair by pair, which takes longer (up to tenths of a
+ * second). */
 typedef struct {
   int32_t T, Hq, Hkv, d, n_docs, max_len;
   float scale, cap;

@@ -57,6 +57,9 @@ int launch_doc_fwd(const DocDims& s, const void* Q, const void* K, const void* V
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   FwdArgs a{};
   a.s = doc_as_window(s);
+  a.Q = static_cast<const __nv_bfloat16*>(Q);
+  a.K = static_cast<const __nv_bfloat16*>(K);
+  a.V = static_cast<const __nv_bfloat16*>(V);
   a.O = static_cast<__nv_bfloat16*>(O);
   a.lse = lse;
   a.status = reinterpret_cast<int32_t*>(ws);

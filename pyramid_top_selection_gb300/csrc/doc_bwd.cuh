@@ -63,6 +63,10 @@ int doc_bwd(const DocDims& s, const void* Q, const void* K, const void* V, const
   a.s = doc_as_window(s);
   const WinBwdWs w = window_bwd_ws(a.s);
   plan(a);
+  a.Q = static_cast<const bf16*>(Q);
+  a.K = static_cast<const bf16*>(K);
+  a.V = static_cast<const bf16*>(V);
+  a.dO = static_cast<const bf16*>(dO);
   a.lse = lse;
   a.nlse = reinterpret_cast<float*>(ws + w.nlse);
   a.delta = reinterpret_cast<float*>(ws + w.delta);

@@ -24,6 +24,7 @@
 #include "device.cuh"
 #include "internal.h"
 #include "masks.cuh"
+#include "pairs.cuh"
 
 namespace pisa {
 
@@ -55,7 +56,8 @@ struct BwdArgs {
   // dK, dV: key tiles, (b, kv), key tiles with sinks; token tiles of a chunk and chunks of a key tile, of
   // those without sinks (ct, nck) and with them (cts, ncs); items of the tiles with sinks, which come first
   int n_kt, n_bh, n_st, ct, nck, cts, ncs, n_snk;
-  win::DocRows docs;       // documents (MASK)
+  win::DocRows docs;       // documents (MASK), and what their gradients come from
+  const bf16 *Q, *K, *V, *dO;
 };
 
 // One past the last valid token of sequence b, or of the documents.
@@ -105,6 +107,47 @@ __device__ __forceinline__ win::Item dq_item(const BwdArgs& a, int w) {
   return it;
 }
 
+// Documents: the rows of an item once more, those that keys which they do not see have made NaN (whole CTA).
+template <int D, int MASK, int WARPS>
+__device__ __forceinline__ void restore_dq(const BwdArgs& a, const win::Item& it) {
+  const WinDims& s = a.s;
+  const int lane = threadIdx.x & 31;
+  const bf16 *K = a.K + it.kv * D, *V = a.V + it.kv * D;
+  const int end_key = min(it.lo + 128 * it.n, it.L);
+#pragma unroll 1
+  for (int r = threadIdx.x >> 5; r < 128; r += WARPS) {
+    const int i = it.t0 + (r >> a.lp), h = it.h0 + (r & (a.P - 1));
+    if (i >= s.Nq) return;
+    const int64_t row = static_cast<int64_t>(i) * s.Hq + h;
+    if (!win::RowSum<D>::bad(a.dQ + row * D)) continue;
+    const win::DocSpan<MASK> span(a.docs, i);
+    const float lse = a.lse[static_cast<int64_t>(h) * s.Nq + i];
+    float dl = 0.f;
+    if (span.hi >= span.lo) {                                // else a row of zeros
+      dl = a.delta[(static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P + r];
+      if (!isfinite(lse) || !isfinite(dl)) continue;         // it is what its own values make it
+      if (!win::rows_not_finite<D>(K, s.ks, it.lo, min(span.lo, end_key)) &&
+          !win::rows_not_finite<D>(K, s.ks, max(it.lo, span.hi + 1), end_key))
+        continue;
+    }
+    const bf16 *q = a.Q + i * s.qs + h * D, *g = a.dO + row * D;
+    const float slope = MASK & win::kBias ? __ldg(a.docs.slopes + h) * kLog2e : 0.f;
+    win::RowSum<D> o;
+#pragma unroll 1
+    for (int j0 = span.lo; j0 <= span.hi; j0 += 32) {
+      const int j = j0 + lane;
+      float w = 0.f;
+      if (j <= span.hi) {
+        float back;
+        const float y = win::pair_score<MASK>(win::row_product<D>(q, K + j * s.ks), s.scale, a.docs.cap, slope, i - j, back);
+        w = tc::ex2(y - lse * kLog2e) * back * (win::row_product<D>(g, V + j * s.vs) - dl);
+      }
+      o.add(w, K + j0 * s.ks, s.ks, min(32, span.hi + 1 - j0));
+    }
+    o.store(a.dQ + row * D, s.scale);
+  }
+}
+
 // TMEM: S (and dS in its place) of key tile n at 128 (n & 1), dP at 256, dQ at 384. One MMA warp
 // issues dP(n) and the next tile's S, the other dQ += dS K as soon as dS is there, so that the
 // tensor cores have a product at hand while the softmax warps turn S and dP into dS. (The barriers of
@@ -135,7 +178,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       s_full[2], dp_full[2], d_full, ds_full[2], dq_done[2], dq_last, dq_empty, drain[2], never;
   __shared__ win::ItemRing s_items;
   __shared__ uint32_t tmem_base;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_spoiled;         // s_spoiled: a row came out as it may not be (documents)
   __shared__ float s_sum[NG][128];           // D of the rows, a sum for each of their threads
 
   const WinDims& s = a.s;
@@ -170,7 +213,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
     win::ring_init(s_items, NS + 3);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
-    s_abort = 0;
+    s_abort = s_spoiled = 0;
     if (MASK == win::kWindow && blockIdx.x == 0) *a.status = 0;      // nothing else writes it before the next kernel
   }
   if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
@@ -543,10 +586,12 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       tc::after_sync();
       ++n_q;
       const int64_t row0 = ((static_cast<int64_t>(it.b) * s.Nq + it.t0) * s.Hq + it.h0) * D + 8 * (lane & 3);
+      win::Watch out;
 #pragma unroll 1
       for (int q = g; q < D / 32; q += NG) {
         float y[32];
         tc::tmem_ld32(tm + 384 + 32 * q + lane_off, y);
+        if (MASK != win::kWindow) out.add(y);
         uint32_t u[4][4];                                    // four 16-byte pieces of row r
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -563,6 +608,7 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       }
       tc::before_sync();
       tc::bar_arrive(&dq_empty);
+      if (MASK != win::kWindow && out.bad()) s_spoiled = 1;
     }
     if (aborted() && g == 0) {                               // the rows of the item at hand and of those left
       for (; k_item < win::rounds_of(a.n_items); ++k_item) {
@@ -587,6 +633,12 @@ window_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, cons
       if (tid < 128 && it.t0 + (tid >> a.lp) < s.Nq)
         a.nlse[(static_cast<int64_t>(it.first[0]) * a.Nqp + it.t0) * a.P + tid] = __int_as_float(0x7fc00000);
     }
+  } else if (MASK != win::kWindow && s_spoiled) {
+    for (int k = 0; k < win::rounds_of(a.n_items); ++k) {
+      const int64_t w = win::item_of(k, a.n_items);
+      if (w < 0) break;
+      restore_dq<D, MASK, NS + 4>(a, dq_item<MASK>(a, static_cast<int>(w)));
+    }
   }
   if (warp == 0) {
     tc::after_sync();
@@ -609,7 +661,7 @@ struct DkvBars {
   uint64_t kv_full, q_full[3], q_empty[3], o_full[2], o_empty[2], st_full[2], st_empty[2], s_full, dp_full, p_full, ds_full,
       dv_done, dk_done, drain, never;
   uint32_t tmem_base;
-  int abort;
+  int abort, spoiled;              // spoiled: a row came out as it may not be (documents)
   float __align__(16) slope[64];   // the group's heads' slopes times -log2 e (kBias)
 };
 static_assert(sizeof(DkvBars) <= 512, "barrier block");
@@ -668,6 +720,65 @@ struct DkvItem {
   }
 };
 
+// Documents: the keys of an item, whose rows are those of tokens [t0, t1), once more, those that rows which do not see them have
+// made NaN (whole CTA).
+template <int D, int MASK, int WARPS>
+__device__ __forceinline__ void restore_dkv(const BwdArgs& a, const DkvItem& it, int t0, int t1) {
+  const WinDims& s = a.s;
+  const int lane = threadIdx.x & 31, h0 = it.kv * s.G;
+  const int64_t gs = static_cast<int64_t>(s.Hq) * D;
+#pragma unroll 1
+  for (int r = threadIdx.x >> 5; r < 128; r += WARPS) {
+    const int j = 128 * it.kt + r;
+    if (j >= s.N) return;
+    const int64_t row = static_cast<int64_t>(j) * s.Hkv + it.kv;
+    float* part = a.part + (it.slot * 2 * 128 + r) * D;      // dV, then dK
+    const bool split = it.slot >= 0;
+    const bool bad = split ? win::RowSum<D>::bad(part) || win::RowSum<D>::bad(part + 128 * D)
+                           : win::RowSum<D>::bad(a.dV + row * D) || win::RowSum<D>::bad(a.dK + row * D);
+    if (!bad) continue;
+    const win::DocSeen seen(a.docs, j, s.N);
+    const int from = max(t0, seen.first), to = min(t1, seen.end);
+    auto other = [&](int x0, int x1) {                       // what does not see it is not finite
+#pragma unroll 1
+      for (int h = h0; h < h0 + s.G; ++h)
+        if (win::rows_not_finite<D>(a.Q + h * D, s.qs, x0, x1) || win::rows_not_finite<D>(a.dO + h * D, gs, x0, x1)) return true;
+      return false;
+    };
+    if (!other(t0, min(from, t1)) && !other(max(t0, to), t1)) continue;
+    const bf16 *k = a.K + j * s.ks + it.kv * D, *v = a.V + j * s.vs + it.kv * D;
+    win::RowSum<D> dk, dv;
+#pragma unroll 1
+    for (int h = h0; h < h0 + s.G; ++h) {
+      const float slope = MASK & win::kBias ? __ldg(a.docs.slopes + h) * kLog2e : 0.f;
+      const bf16 *Q = a.Q + h * D, *g = a.dO + h * D;
+      const int64_t at = (static_cast<int64_t>(it.kv) * a.sets + (h - h0) / a.P) * a.Nqp;
+#pragma unroll 1
+      for (int i0 = from; i0 < to; i0 += 32) {
+        const int i = i0 + lane;
+        float p = 0.f, ds = 0.f;
+        if (i < to) {
+          const int64_t x = (at + i) * a.P + (h - h0) % a.P;
+          float back;
+          const float y = win::pair_score<MASK>(win::row_product<D>(Q + i * s.qs, k), s.scale, a.docs.cap, slope, i - j, back);
+          p = tc::ex2(y + a.nlse[x]);
+          ds = p * back * (win::row_product<D>(g + i * gs, v) - a.delta[x]);
+        }
+        const int n = min(32, to - i0);
+        dv.add(p, g + i0 * gs, gs, n);
+        dk.add(ds, Q + i0 * s.qs, s.qs, n);
+      }
+    }
+    if (split) {
+      dv.store(part, 1.f);
+      dk.store(part + 128 * D, s.scale);
+    } else {
+      dv.store(a.dV + row * D, 1.f);
+      dk.store(a.dK + row * D, s.scale);
+    }
+  }
+}
+
 // One CTA per item: a tile of 128 keys of one KV head and a run of the row tiles that see it. TMEM:
 // S^T (keys x rows; P^T in its place) at 0, dP^T (dS^T) at 128, dV at 256, dK at 256 + d. Per row
 // tile n the MMA warp issues dV(n), S^T(n + 1), dK(n), dP^T(n + 1): the exponentials of one tile
@@ -690,7 +801,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
   auto &q_full = bar.q_full, &q_empty = bar.q_empty;
   auto &o_full = bar.o_full, &o_empty = bar.o_empty, &st_full = bar.st_full, &st_empty = bar.st_empty;
   uint32_t& tmem_base = bar.tmem_base;
-  int& s_abort = bar.abort;
+  int &s_abort = bar.abort, &s_spoiled = bar.spoiled;
 
   const WinDims& s = a.s;
   const int tid = threadIdx.x, warp = win::uniform(tid >> 5), lane = tid & 31;
@@ -762,7 +873,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     tc::bar_init(&drain, 1);
     tc::bar_init(&never, 1);
     tc::fence_bar_init();
-    s_abort = 0;
+    s_abort = s_spoiled = 0;
     if (MASK & win::kBias)
       for (int h = 0; h < s.G; ++h) bar.slope[h] = -kLog2e * __ldg(a.docs.slopes + it.kv * s.G + h);
     if (n > 0) {
@@ -1043,12 +1154,16 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const float f = which ? s.scale : 1.f;
     const uint32_t tA = tm + 256 + D * which + lane_off;
     const float nan = __int_as_float(0x7fc00000);
+    win::Watch out;
     if (it.slot >= 0) {
       float* o = a.part + ((it.slot * 2 + which) * 128 + (r & ~3)) * D + 4 * (lane & 3);
 #pragma unroll 1
       for (int q = part; q < D / 32; q += NH) {
         float x[32];
-        if (ok) tc::tmem_ld32(tA + 32 * q, x);
+        if (ok) {
+          tc::tmem_ld32(tA + 32 * q, x);
+          if (MASK != win::kWindow) out.add(x);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t u[4][4];                                  // four 16-byte pieces of row r, then one of four rows
@@ -1076,6 +1191,7 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
         for (int h = 0; h < 2; ++h) {
           float x[32];
           tc::tmem_ld32(tA + 64 * x2 + 32 * h, x);
+          if (MASK != win::kWindow) out.add(x);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t u[4];
@@ -1096,12 +1212,18 @@ window_dkv_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       }
       if (lane == 0) tc::bulk_wait<0>();
     }
+    if (MASK != win::kWindow && out.bad()) s_spoiled = 1;
   }
   tc::before_sync();
   __syncthreads();
   if (tid == 0 && s_abort) {
     win::grid_wait();
     atomicOr(a.status, PISA_STATUS_TIMEOUT);
+  }
+  if (MASK != win::kWindow && s_spoiled && !s_abort) {
+    win::fence_async_global();                               // dK and dV may have gone out by TMA
+    win::grid_wait();
+    restore_dkv<D, MASK, NS + 4>(a, it, max(begin, tile_tok(0)), min(L, tile_tok(n - 1) + a.tok));
   }
   if (warp == 0) {
     tc::after_sync();

@@ -44,6 +44,7 @@
 #include "device.cuh"
 #include "internal.h"
 #include "masks.cuh"
+#include "pairs.cuh"
 
 namespace pisa {
 
@@ -78,7 +79,8 @@ struct FwdArgs {
   int P, lp, tok;          // heads of a tile (P = 2^lp), tokens of a tile (128 / P)
   int n_tiles, n_heads, n_items;   // token tile pairs, (b, kv, head set) combinations
   int splits;              // CTAs of an item (SPLIT)
-  win::DocRows docs;       // documents (MASK)
+  win::DocRows docs;       // documents (MASK), and what they attend
+  const __nv_bfloat16 *Q, *K, *V;
 };
 
 // Work item w: 2 x tok tokens of P heads.
@@ -121,6 +123,37 @@ __device__ __forceinline__ win::Item fwd_item(const FwdArgs& a, int w) {
   it.last[0] = r0.last;
   it.last[1] = r1.last;
   return it;
+}
+
+// Documents: the warp's 32 rows of row tile t of an item once more, those that values which they do not see have made NaN.
+template <int D, int MASK>
+__device__ __forceinline__ void restore_rows(const FwdArgs& a, const win::Item& it, int t, int lane) {
+  const WinDims& s = a.s;
+  const int r = threadIdx.x & 127, p = it.t0 + t * a.tok + (r >> a.lp), h = it.h0 + (r & (a.P - 1)), last = t ? it.last[1] : it.last[0];
+  const float lse = p < s.Nq ? a.lse[static_cast<int64_t>(h) * s.Nq + p] : neg_inf();
+  const bool bad = p < s.Nq && isfinite(lse) && win::row_not_finite<D>(a.O + (static_cast<int64_t>(p) * s.Hq + h) * D);
+  const __nv_bfloat16 *K = a.K + it.kv * D, *V = a.V + it.kv * D;
+  const int first_key = it.lo + 128 * (t ? it.first[1] : it.first[0]), end_key = min(it.lo + 128 * (last + 1), it.L);
+  for (uint32_t left = __ballot_sync(0xffffffffu, bad); left; left &= left - 1) {
+    const int src = __ffs(left) - 1, i = __shfl_sync(0xffffffffu, p, src), hq = __shfl_sync(0xffffffffu, h, src);
+    const float l2 = __shfl_sync(0xffffffffu, lse, src) * kLog2e;
+    const win::DocSpan<MASK> span(a.docs, i);
+    if (!win::rows_not_finite<D>(V, s.vs, first_key, min(span.lo, end_key)) &&
+        !win::rows_not_finite<D>(V, s.vs, max(first_key, span.hi + 1), end_key))
+      continue;                                              // it sees them itself
+    const __nv_bfloat16* q = a.Q + i * s.qs + hq * D;
+    const float slope = MASK & win::kBias ? __ldg(a.docs.slopes + hq) * kLog2e : 0.f;
+    win::RowSum<D> o;
+#pragma unroll 1
+    for (int j0 = span.lo; j0 <= span.hi; j0 += 32) {
+      const int j = j0 + lane;
+      float w = 0.f, back;
+      if (j <= span.hi)
+        w = tc::ex2(win::pair_score<MASK>(win::row_product<D>(q, K + j * s.ks), s.scale, a.docs.cap, slope, i - j, back) - l2);
+      o.add(w, V + j0 * s.vs, s.vs, min(32, span.hi + 1 - j0));
+    }
+    o.store(a.O + (static_cast<int64_t>(i) * s.Hq + hq) * D, 1.f);
+  }
 }
 
 // SPLIT: one item per cluster of a.splits CTAs; otherwise a.splits is 1 and the CTAs are persistent.
@@ -369,6 +402,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     const win::Scores<CAP> scores(s.scale, CAP ? a.docs.cap : 0.f);
     win::Distance dist;
     int n_s = 0, n_kv = 0;                     // key tiles done by this row tile; stages used by earlier items
+    bool spoiled = false;                      // a row came out as it may not be
     int i = 0;
     for (int n = 0;; ++i, n_kv += 2 * n) {
       const win::Item it = get(i);
@@ -543,6 +577,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
       const float inv = 1.f / l;                             // l = 0: an empty row, whose output is 0
       unsigned char* stg = sm + M::oStage + warp * M::STG;
       const int tk = it.t0 + t * a.tok + ((warp & 3) * 32 >> a.lp);   // the warp's first token
+      win::Watch out;
 #pragma unroll 1
       for (int kb = 0; kb < M::KB; ++kb) {
         uint32_t u[32];
@@ -553,6 +588,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
             tc::tmem_ld32(tO + 64 * kb + 32 * q, y);
 #pragma unroll
             for (int c = 0; c < 16; ++c) u[16 * q + c] = l == 0.f ? 0u : pack_bf16(y[2 * c] * inv, y[2 * c + 1] * inv);
+            if (MASK != win::kWindow) out.add(y);
           }
           if (kb == M::KB - 1) {
             tc::before_sync();
@@ -575,8 +611,17 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
           tc::bulk_commit();
         }
       }
+      if (MASK != win::kWindow) spoiled |= out.bad();
     }
     if (lane == 0) tc::bulk_wait<0>();
+    if (MASK != win::kWindow && __any_sync(0xffffffffu, spoiled) && !__any_sync(0xffffffffu, aborted())) {
+      win::fence_async_global();                             // O went out by TMA
+      for (int k = 0; k < win::rounds_of(a.n_items); ++k) {
+        const int64_t w = win::item_of(k, a.n_items);
+        if (w < 0) break;
+        restore_rows<D, MASK>(a, fwd_item<MASK>(a, static_cast<int>(w)), t, lane);
+      }
+    }
     if (!SPLIT && aborted()) {                               // the rows of the item at hand and of those left
       for (; i < win::rounds_of(a.n_items); ++i) {
         const int64_t w = win::item_of(i, a.n_items);

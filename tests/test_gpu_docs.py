@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import pyramid_top_selection_gb300 as pisa
-from _docs_ref import doc_attention
+from _docs_ref import doc_attention, doc_mask
 from _window_ref import check
 
 pytestmark = pytest.mark.gpu
@@ -381,3 +381,80 @@ def test_starts_in_no_order_are_survived_with_biased_scores(seed, cap):
     _run(Q, K, V, dO, _ints(starts), _ints(prefix), _slopes(64), cap, max_len=T // 8)
     for t in _run(Q, K, V, dO, _ints([0, T]), None, _slopes(64), cap).values():
         assert bool(t.isfinite().all())
+
+
+def _reached(see, G, bad):
+    """Where the definition's results are not finite, from where Q, K (NaN), V, dO (NaN or infinite) are not: a sum over visible
+    pairs is not finite where one of its terms is not."""
+    T, Hq, d = bad["Q"].shape
+    Hkv = Hq // G
+    some = lambda m, x: (m.double() @ x.double()) > 0                       # noqa: E731 (any over the inner dimension)
+    out = {n: torch.zeros(T, h, d, dtype=torch.bool, device=see.device) for n, h in (("O", Hq), ("dQ", Hq), ("dK", Hkv), ("dV", Hkv))}
+    out["lse"] = torch.zeros(Hq, T, dtype=torch.bool, device=see.device)
+    for h in range(Hq):
+        q, k, v, g = bad["Q"][:, h], bad["K"][:, h // G], bad["V"][:, h // G], bad["dO"][:, h]
+        row = (see & (q.any(1)[:, None] | k.any(1)[None])).any(1)
+        o = row[:, None] | some(see, v)
+        D = (g | o).any(1)
+        dP = g.any(1)[:, None] | v.any(1)[None]
+        dS = see & (row[:, None] | D[:, None] | dP)
+        out["lse"][h], out["O"][:, h] = row, o
+        out["dQ"][:, h] = dS.any(1)[:, None] | some(see, k)
+        out["dK"][:, h // G] |= dS.any(0)[:, None] | some(see.T, q)
+        out["dV"][:, h // G] |= (see & row[:, None]).any(0)[:, None] | some(see.T, g)
+    return out
+
+
+SPOILED = {  # T, Hq, Hkv, d, starts, prefix, cap, slopes, fused, max_len
+    "three documents": (420, 4, 2, 64, [0, 150, 290, 420], None, 0.0, False, True, 0),
+    "short documents": (300, 8, 2, 128, [3, 40, 77, 130, 131, 180, 290], None, 0.0, False, False, 0),
+    "long documents, prefixes": (900, 4, 1, 128, [0, 500, 890], [30, 200], 0.0, False, False, 0),
+    "capped": (600, 4, 2, 64, [0, 310, 600], None, 5.0, False, False, 0),
+    "biased": (600, 6, 2, 128, [0, 310, 600], None, 0.0, True, True, 0),
+    "capped and biased, in runs": (700, 2, 2, 64, [0, 600, 700], None, 5.0, True, False, 0),
+    "many items": (1300, 40, 20, 64, [0, 100, 700, 1290], None, 0.0, False, False, 0),
+    "many items, capped": (1300, 40, 20, 128, [0, 100, 700, 1290], None, 5.0, False, False, 300),
+}
+
+
+@pytest.mark.parametrize("where", ["Q", "K", "V", "dO", "all"])
+@pytest.mark.parametrize("name", SPOILED)
+def test_what_is_not_finite_reaches_what_sees_it_and_nothing_else(name, where):
+    T, Hq, Hkv, d, starts, prefix, cap, biased, fused, max_len = SPOILED[name]
+    pad = torch.ones(T, dtype=torch.bool, device="cuda")
+    pad[starts[0]:starts[-1]] = False
+    x = dict(zip(("Q", "K", "V", "dO"), _inputs(T, Hq, Hkv, d, fused, len(name), padding=pad)))
+    clean = {n: torch.where(pad[:, None, None], 0.0, t.double()).to(bf16) for n, t in x.items()}
+    r = random.Random(len(name) + len(where))
+    bad = {n: torch.zeros(t.shape, dtype=torch.bool, device="cuda") for n, t in x.items()}
+    for n in (x if where == "all" else [where]):
+        for _ in range(3):                                             # (the last document but one holds most of them)
+            t = r.randrange(starts[-3], starts[-2])
+            t, h, c = r.choice([t, starts[-3], starts[-2] - 1, starts[-2]]), r.randrange(x[n].shape[1]), r.randrange(d)
+            value = math.nan if n in "QK" else r.choice([math.nan, math.inf, -math.inf])
+            x[n][t, h, c], bad[n][t, h, c] = value, True
+    slopes = _slopes(Hq) if biased else None
+    got = _run(x["Q"], x["K"], x["V"], x["dO"], _ints(starts), None if prefix is None else _ints(prefix), slopes, cap, max_len=max_len)
+    for n in x:
+        clean[n][bad[n]] = 0.0
+    want, tol = doc_attention(clean["Q"], clean["K"], clean["V"], starts, prefix, slopes, cap, dO=clean["dO"])
+    reached = _reached(doc_mask(T, starts, prefix, "cuda"), Hq // Hkv, bad)
+    for n in want:
+        assert torch.equal(got[n].isfinite() | (got[n] == -math.inf) & (n == "lse"), ~reached[n]), n
+        check(n, torch.where(reached[n], want[n], got[n].double()), want[n], tol[n])
+
+
+def test_a_batch_of_nothing_but_nan_ends():
+    # the most that can be taken pair by pair: every value but the first document's is NaN, and ends no later for it than in seconds
+    T, d = 6000, 64
+    Q, K, V, dO = _inputs(T, 16, 4, d, seed=21)
+    clean = [t.clone() for t in (Q, K, V, dO)]
+    for t in (Q, K, V, dO):
+        t[100:] = math.nan
+    got = _run(Q, K, V, dO, _ints([0, 100, 3000, T]))
+    for n, t in got.items():
+        t = t.T if n == "lse" else t
+        assert bool(t[100:].isnan().all()), n
+    want, tol = doc_attention(*(t[:100] for t in clean[:3]), [0, 100], dO=clean[3][:100])
+    for n in want:
+        check(n, got[n][:, :100] if n == "lse" else got[n][:100], want[n], tol[n])
