@@ -498,8 +498,8 @@ int pisa_paged_workspace_size(const pisa_paged_shape_t* shape, size_t* bytes);
  *   len device [B] int32: tokens in the cache, the new ones included; clamped to [0, max_pages*page], with
  *   PISA_STATUS_POS_RANGE where that changes it. A page outside [0, n_pages) sets the same bit and its keys are not
  *   seen. q [B,nq,Hq,d] bf16, slopes [Hq] fp32 or NULL (read); o [B,nq,Hq,d] bf16, lse [B,nq,Hq] fp32 (may be
- *   NULL) (written). What lies in slots behind a sequence's end is never used, whatever it is; values at the newest
- *   nq - 1 keys have to be finite for the queries that do not see them.
+ *   NULL) (written). What lies in slots behind a sequence's end is never used, whatever it is; keys and values that are not
+ *   finite reach the queries that see them, as the definition has it, and no others.
  * The order of the sums follows the lengths and the GPU's SM count only.
  * Nothing written (o, lse, the workspace) may overlap anything that is read, nor one another. */
 int pisa_paged_attn(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const int32_t* table,

@@ -222,7 +222,9 @@ struct Part {
   int unit, head, tail, first;
 };
 
-template <int D, bool FOUR, int NT>
+// DRAFTS: more than one token a sequence (a variant of its own, for what only they need cost one token of 32 sequences in 4 bits
+// 1.9 of 72 us, although it was not run).
+template <int D, bool FOUR, int NT, bool DRAFTS>
 __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kernel(const PagedArgs a) {
   using M = Plan<D, FOUR, NT>;
   constexpr int CH = M::CH, SUB = CH / 16, KS = D / 16;
@@ -667,6 +669,60 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
               pb[t][1] = transpose8(pack_bf16(x[t][k][2], x[t][k][3]));
             }
           }
+          // Values that are not finite, of a drafted token that earlier queries do not see: their weights of 0 would make NaN of them. Added
+          // here to those that see them, and left out of the product. Bits of `odd`: the 16 tokens, in 4 bits for the lane's group of channels.
+          uint32_t odd = 0;
+          if (DRAFTS && !full) {
+            const int drafted = max(0, con.n - s.nq + 1 - (v0 + 16 * k));        // the first token that not all queries see
+            const uint32_t v_at = at + M::HALF + 16 * k * M::ROW;
+            if (drafted < 16) {
+              if constexpr (FOUR) {
+                for (int u = drafted; u < 16; ++u)
+                  odd |= static_cast<uint32_t>(v0 + 16 * k + u < con.n && !((bad >> k) & 1) &&
+                                               (lds8(at + M::HALF + CH * M::ROW + (16 * k + u) * M::SROW + v_grp) & 0x7fu) == 0x7fu) << u;
+              } else {
+                bool not_finite = false;
+                for (int c = lane >> 4; c < D / 8; c += 2) {
+                  const uint4 v = lds128(v_at + piece(lane & 15, c));
+                  const uint32_t m = 0x7fff7fffu, top = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+                  not_finite |= (top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u;
+                }
+                const uint32_t b = __ballot_sync(0xffffffffu, not_finite);
+                odd = (b | b >> 16) & 0xffffu & ~((1u << drafted) - 1);
+              }
+            }
+#pragma unroll 1
+            for (uint32_t left = __reduce_or_sync(0xffffffffu, odd); left; left &= left - 1) {
+              const int u = __ffs(left) - 1, row = FOUR ? (D == 128 ? u ^ ((u >> 1) & 1) : u ^ ((u >> 2) & 1)) & 7 : u & 7;   // S's row of token u
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float lo = __shfl_sync(0xffffffffu, x[t][k][e], 4 * row + p2), hi = __shfl_sync(0xffffffffu, x[t][k][e + 2], 4 * row + p2);
+                  const float P = u < 8 ? lo : hi;
+                  if (v0 + 16 * k + u > pos[t][e]) continue;
+#pragma unroll
+                  for (int c = 0; c < KS; ++c)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                      float v = __int_as_float(0x7fc00000);
+                      if constexpr (!FOUR) {
+                        const int ch = 16 * c + g + 8 * y;
+                        v = __uint_as_float(lds16(v_at + piece(u, ch >> 3) + 2 * (ch & 7)) << 16);
+                      } else if (!((odd >> u) & 1)) {
+                        continue;
+                      }
+                      o[t][c][e + 2 * y] += P * v;
+                    }
+                }
+              if constexpr (!FOUR) {
+                __syncwarp();
+                for (int c = lane; c < D / 8; c += 32)
+                  asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + piece(u, c)), "r"(0) : "memory");
+                __syncwarp();
+              }
+            }
+          }
           if constexpr (FOUR) {
             // the lane's codes of the tokens of slots 2 p2 (a) and 2 p2 + 1 (b), and of those 8 slots on
             uint32_t va[2][D / 64], vb[2][D / 64], f[2];
@@ -685,6 +741,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 2 ? 2 : 3) paged_attn_kerne
               if (!full) {                                         // what is behind the end, or was not copied
                 if (v0 + 16 * k + 8 * h + tok_a >= con.n || (bad >> k) & 1) sa = 0;
                 if (v0 + 16 * k + 8 * h + tok_b >= con.n || (bad >> k) & 1) sb = 0;
+                if ((odd >> (8 * h + tok_a)) & 1) sa = 0;
+                if ((odd >> (8 * h + tok_b)) & 1) sb = 0;
               }
               f[h] = scales_of(sa | sb << 8);
             }
@@ -930,17 +988,17 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(const PagedArgs a, 
 
 int cols_of(const PagedDims& s) { return s.G * s.nq <= 8 ? 8 : 16; }
 
-template <int D, bool FOUR, int NT>
+template <int D, bool FOUR, int NT, bool DRAFTS>
 int attn_launch(PagedArgs& a, cudaStream_t st) {
   using M = Plan<D, FOUR, NT>;
   static win::Ready ready;
   static std::atomic<int> known[64];                               // CTAs an SM holds + 1, per device
   int dev = 0;
-  if (int e = ready(paged_attn_kernel<D, FOUR, NT>, M::bytes)) return e;
+  if (int e = ready(paged_attn_kernel<D, FOUR, NT, DRAFTS>, M::bytes)) return e;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   int held = dev < 64 ? known[dev].load(std::memory_order_relaxed) - 1 : -1;
   if (held < 0) {
-    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, paged_attn_kernel<D, FOUR, NT>, 32 * kWarps, M::bytes)) return e;
+    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, paged_attn_kernel<D, FOUR, NT, DRAFTS>, 32 * kWarps, M::bytes)) return e;
     if (held < 1) return cudaErrorInvalidConfiguration;
     if (dev < 64) known[dev].store(held + 1, std::memory_order_relaxed);
   }
@@ -951,7 +1009,7 @@ int attn_launch(PagedArgs& a, cudaStream_t st) {
     ProfScope ps(st, "paged_attn");
     const win::Behind b(dim3(ctas), 32 * kWarps, M::bytes, st);
     const PagedArgs& ca = a;
-    if (cudaError_t e = cudaLaunchKernelEx(&b.cfg, paged_attn_kernel<D, FOUR, NT>, ca)) return e;
+    if (cudaError_t e = cudaLaunchKernelEx(&b.cfg, paged_attn_kernel<D, FOUR, NT, DRAFTS>, ca)) return e;
   }
   ProfScope ps(st, "paged_join");
   // a unit a block where they are fewer than the CTAs, with more threads where they have many parts each
@@ -967,7 +1025,8 @@ int attn_launch(PagedArgs& a, cudaStream_t st) {
 
 template <int D, bool FOUR>
 int by_rows(PagedArgs& a, cudaStream_t st) {
-  return cols_of(a.s) == 8 ? attn_launch<D, FOUR, 1>(a, st) : attn_launch<D, FOUR, 2>(a, st);
+  if (a.s.nq > 1) return cols_of(a.s) == 8 ? attn_launch<D, FOUR, 1, true>(a, st) : attn_launch<D, FOUR, 2, true>(a, st);
+  return cols_of(a.s) == 8 ? attn_launch<D, FOUR, 1, false>(a, st) : attn_launch<D, FOUR, 2, false>(a, st);
 }
 
 constexpr size_t kFlags = 256, kParts = kFlags + (win::kPlanSms * kMaxCtas * 4 + 255) / 256 * 256;

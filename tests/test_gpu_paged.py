@@ -753,3 +753,43 @@ def test_append_of_more_tokens_than_one_look_up(bits):
         old[page_of, :, slot] = c[..., 0] | c[..., 1] << 4
         old_s.view(torch.uint8)[page_of, :, slot] = scales.float().to(torch.float8_e4m3fn).view(torch.uint8)
         assert torch.equal(t, old) and torch.equal(sc.view(torch.uint8), old_s.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("B,nq,Hq,Hkv,d,page", [(5, 4, 8, 2, 128, 16), (4, 16, 4, 2, 64, 32), (3, 2, 12, 2, 64, 16), (2, 9, 8, 2, 128, 64), (60, 3, 20, 4, 128, 16)])
+def test_drafted_tokens_that_are_not_finite_reach_the_queries_that_see_them(B, nq, Hq, Hkv, d, page, bits):
+    g = _gen(34 + nq)
+    lens = [(700, 33, nq, 48 + nq, 2)[b % 5] + b for b in range(B)]
+    table, pool = _table(g, lens, page)
+    shape = pisa.make_paged_shape(B, Hq, Hkv, d, pool, page, table.shape[1], bits, nq)
+    cache = _filled(g, shape)
+    q = _randn(g, B, nq, Hq, d)
+    k, v = _keys(cache, table, lens, page)
+    want, tol = paged_attention(q, k, v, lens)                         # (what is reached is left out of the comparison)
+    reached = torch.zeros(B, nq, Hq, d, dtype=torch.bool, device="cuda")
+    lost = torch.zeros(B, nq, Hq, dtype=torch.bool, device="cuda")
+    G = Hq // Hkv
+    for b, n in enumerate(lens):
+        for back in range(min(n, nq)):
+            if (b + back) % 3 == 2:
+                continue
+            p, kv, c = n - 1 - back, (b + back) % Hkv, (5 * b + 11 * back) % d
+            pg, slot = table[b, p // page].long(), p % page
+            sees = torch.arange(nq, device="cuda") >= nq - 1 - back
+            if (b + back) % 4 == 3:                                    # a key: every query that sees it
+                if bits == 16:
+                    cache.k[pg, kv, slot, c] = math.nan
+                else:
+                    cache.k_scale.view(torch.uint8)[pg, kv, slot, c // 16] = 0x7f
+                lost[b, :, kv * G:(kv + 1) * G] |= sees[:, None]
+            elif bits == 16:
+                cache.v[pg, kv, slot, c] = (math.inf, -math.inf, math.nan)[back % 3]
+                reached[b, :, kv * G:(kv + 1) * G, c] |= sees[:, None]
+            else:
+                cache.v_scale.view(torch.uint8)[pg, kv, slot, c // 16] = 0x7f if back % 2 else 0xff
+                reached[b, :, kv * G:(kv + 1) * G, c // 16 * 16:c // 16 * 16 + 16] |= sees[:, None, None]
+    o, lse = pisa.paged_attn(shape, cache, table, _ints(lens), q)
+    reached |= lost[..., None]
+    assert torch.equal(~o.isfinite(), reached) and torch.equal(lse.isnan(), lost)
+    check("o", torch.where(reached, want["O"], o.double()), want["O"], tol["O"])
+    check("lse", torch.where(lost, want["lse"], lse.double()), want["lse"], tol["lse"])
