@@ -484,7 +484,7 @@ typedef struct {
  *   is not below B, whose pos is outside [0, max_pages*page) or whose page is outside [0, n_pages), and the status
  *   word then gets PISA_STATUS_POS_RANGE ORed in.
  * Nothing written (cache, Qr, status) may overlap anything else; Qr may be a contiguous Q itself.
- * shape->nq is not looked at. */
+ * shape->nq is not looked at. T*(Hq + 2 Hkv) < 2^31. */
 int pisa_paged_append(const pisa_paged_shape_t* shape, const pisa_paged_cache_t* cache, const pisa_rope_shape_t* tokens,
                       const void* Q, const void* K, const void* V, int32_t v_stride, const float* inv_freq,
                       const float* q_weight, const float* k_weight, const int32_t* table, const int32_t* seq,

@@ -63,7 +63,7 @@ struct AppendArgs {
   int32_t* status;
   int32_t q_steps, steps;        // a token's steps: its queries' (0 without), then its keys' and values'
   int32_t per, parts;            // steps of a unit of work, units of a token
-  int32_t units;                 // < 2^31 - 32 (warps of the grid): see the launch
+  int32_t units;                 // all tokens' (< 2^31, see the launch: the step to the next one is taken only where there is one)
 };
 
 // A step of a token: rows [h, end) of its queries (part 0), or of its keys and values (part 1: row r is key r, or value
@@ -326,7 +326,7 @@ int launch_paged_append(const PagedDims& s, const PagedCache& c, const RopeDims&
     a.per = per;
     a.parts = (a.steps + per - 1) / per;
   }
-  a.units = static_cast<int>(tokens * a.parts);          // parts: at most half of Hq + 2 Hkv, or 1; and T (Hq + 2 Hkv) < 2^31
+  a.units = static_cast<int>(tokens * a.parts);          // parts <= steps < Hq + 2 Hkv (a step of queries holds one at least, one of keys and values two), and T (Hq + 2 Hkv) < 2^31
   const int blocks = static_cast<int>(std::min<int64_t>((static_cast<int64_t>(a.units) + kWarps - 1) / kWarps, room));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s.d == 128) return s.bits == 4 ? by_kind<128, true>(a, blocks, st) : by_kind<128, false>(a, blocks, st);

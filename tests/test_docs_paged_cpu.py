@@ -300,3 +300,10 @@ def test_codes_by_comparing_with_every_one():
     tied = (off == off.amin(-1, keepdim=True)).sum(-1) > 1
     assert int(tied.sum()) > 50 and bool((got[tied] % 2 == 0).all())
     assert torch.equal(codes >= 8, torch.signbit(x))
+
+
+def test_append_of_more_rows_than_32_bits_is_refused():
+    # queries, keys and values of all tokens together: 180M tokens of 4 + 2 x 4 heads, which the norm and rotation would take (4 + 4)
+    tensors, rest, _, append, _, _, _ = _paged_calls(16)
+    far = {n: A + (k << 28) for k, n in enumerate(tensors + rest)}
+    _said(append(far, pisa.make_rope_shape(1, 180_000_000, 4, 4, 64, 64)), pisa._pisa.PISA_EUNSUPPORTED, "2Hkv")
