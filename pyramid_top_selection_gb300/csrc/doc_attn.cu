@@ -6,10 +6,10 @@
 // document up (16 bytes a token), sorts the token tiles by their keys, the most first, and clears the status word; the
 // attention's kernel is launched behind it while it runs.
 //
-// Bound by the window kernel's MMA warp where scores are as they are, by the softmax warps' arithmetic where they are capped
-// (masks.cuh). Six prompts of 1500 to 8192 tokens, 16 heads over 2, d = 128: 434 us (1.48 PFLOP/s of what tokens see), biased
-// 480, capped 681 (944 TFLOP/s), both 732; with scores beyond the polynomial's range 846. 35K tokens in 60 documents of
-// 64 to 2048, 16 heads over 4: 186 us, a fifth of whose tiles' area is not seen.
+// Bound by the window kernel's MMA warp where scores are as they are, by the softmax warps' chain where they are capped
+// (masks.cuh). Six prompts of 1500 to 8192 tokens, 16 heads over 2, d = 128: 423 us (1.52 PFLOP/s of what tokens see), biased
+// 480-494, capped 685-692 (935 TFLOP/s), both 722; with scores beyond the polynomial's range (a cap of 10) 841. 35K tokens in 60
+// documents of 64 to 2048, 16 heads over 4: 189 us, a fifth of whose tiles' area is not seen; biased 213, capped 293.
 #include <algorithm>
 
 #include "doc_rows.cuh"

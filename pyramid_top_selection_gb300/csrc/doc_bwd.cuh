@@ -3,7 +3,8 @@
 // The window's backward kernels (window_bwd.cuh) with documents' ends, behind the kernel that lays the rows out. D = dO . O takes O
 // as bf16 has it where a row tile sees more than two key tiles: with peaked scores that rounding adds a tenth to the gradients'
 // error (0.0024 to 0.0026 of their size, rms), and would take a second pass over the keys to avoid.
-// 8192 tokens, 16 heads over 2, d = 128, one document: dQ 274 us, dK and dV 393, their partial sums 12; capped 299 and 537.
+// 8192 tokens, 16 heads over 2, d = 128, one document: dQ 268 us, dK and dV 389, their partial sums 18; capped 303 and 529, biased
+// 285 and 478, both 393 and 638.
 // 35K tokens in 60 documents of 64 to 2048, 16 heads over 4: 256 and 271 (288 with key tiles in the order of their keys: those that
 // many tokens see come first).
 #pragma once

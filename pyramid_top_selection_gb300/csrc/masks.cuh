@@ -98,7 +98,9 @@ struct DocSeen {
 //   is a polynomial of (k x)^2 on the FMA units (minimax, within 2.7e-7 in fp32), its coefficients taken times k^2i and
 //   scale log2 e: 6 operations; else 1 - 2 / (1 + e^(2 k x)) (within 2.5e-7): 3 of the FMA units and two special
 //   functions, of which the reciprocal alone takes as long as the 6 (16 a cycle and SM).
-// Not hidden by the products: the FMA units are these operations' bound, 128 a cycle and SM, packed or not.
+// Not hidden by the products, though no unit is full (in the capped forward FMA 21-23 %, ALU 20 %, special functions 21 %, issue slots 40-43
+// %): they lengthen a tile's chain from tensor memory over the cap, the maximum and the exponentials to P, and two softmax warps a
+// scheduler do not hide it.
 template <bool CAP>
 struct Scores {
   float k, cap2, back2;    // scale / cap, cap log2 e, -1 / (cap log2 e)^2

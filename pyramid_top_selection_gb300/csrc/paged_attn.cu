@@ -1,7 +1,9 @@
 // Attention of the last tokens of every sequence over a paged cache in 16 or 4 bits.
 //
-// o = softmax over the visible keys of the scores times V, per query head; bound by HBM: every cached key and value
-// is read once (4 d bytes per KV head and token, 1.125 d in 4 bits) for the group's heads and drafted tokens. 32 sequences of up
+// o = softmax over the visible keys of the scores times V, per query head; bound by HBM: the cached keys and values of a KV head
+// are read once (4 d bytes a token, 1.125 d in 4 bits) for up to 16 rows, heads of the group times drafted tokens. More rows are
+// sets of 16, units of their own that read them again at another time: one token of 32 sequences of up to 16384, 32 heads
+// over 4, takes 94 us (46 in 4 bits), two drafts 101 (63), four, which are two sets, 180 (107). 32 sequences of up
 // to 16384 tokens, 32 heads over 8, d = 128, pages of 64: 172 us in 16 bits (6.48 TB/s), 72 in 4 bits (4.35 TB/s: there each
 // of 12 warps an SM issues an instruction every five cycles, 620 for a chunk of 4.6 KB, of which 260 turn and
 // scale codes; with 128 registers and 16 warps 76 us, with a ring of four stages 72.6). One sequence of 131072 tokens in 4
@@ -15,7 +17,7 @@
 // crosses CTAs. All sums are in the list's order.
 //
 // S^T = K Q^T and O^T += V^T P^T on m16n8k16 MMAs with tokens (then channels) as the 16 rows and the rows of the unit (heads
-// x drafted tokens) as the 8 columns; tcgen05's 128-row tiles would be 94 % padding. Keys and values come by cp.async
+// x drafted tokens) as the 8 or 16 columns; tcgen05's 128-row tiles would be 94 % padding. Keys and values come by cp.async
 // into each warp's ring.
 //   16 bits: chunks of 16 tokens, fragments by ldmatrix.
 //   4 bits: chunks of 32 tokens; codes become halves in registers (a code times its scale is exact in fp16: 2 and 4

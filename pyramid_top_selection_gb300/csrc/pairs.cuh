@@ -4,10 +4,10 @@
 // NaN is NaN. So one document's bad token would reach its neighbours', and a row the ones behind it, wherever they share a tile.
 // The kernels therefore look at what they put out (a multiply-add for two values); where that is not finite and something that
 // the row does not see is not finite either, a warp forms the row again from the pairs that it does see, before the kernel
-// ends. Nothing of this runs where values are finite; its code and the look at the outputs cost the capped forward 1.3 % (six
-// prompts 677 -> 686 us), the others and the backward no more than 1 %. With one infinity a forward of six prompts takes 44 ms
-// instead of 0.7, and a training pass of 60 documents of up to 2048 tokens 3.8 instead of 0.8; with a channel of infinities 262
-// and 98.
+// ends. Nothing of this runs where values are finite; its code and the look at the outputs cost the capped forward 1.3 to 2.6 %
+// (six prompts 677 -> 687 us, 60 documents 286 -> 293), the others and the backward 1 % at most. With one infinity a forward of
+// six prompts takes 44 ms instead of 0.7, and a training pass of 60 documents of up to 2048 tokens 3.8 instead of 0.8; with a
+// channel of infinities 262 and 98.
 #pragma once
 
 #include "device.cuh"

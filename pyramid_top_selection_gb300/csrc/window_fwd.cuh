@@ -26,7 +26,7 @@
 // P is rounded to bf16 for the product (2^-8 relative at most); the sum l takes it unrounded.
 // Bound: the MMA warp, whose four groups of products a step are issued in some 2000 cycles and then
 // waited for; the softmax is not (the time stays without any exponential). 65536 rows of 16 heads over 2, d =
-// 128, a window of 4096: 1.44-1.45 ms a call in rows of calls, which run into the power limit (1.47-1.48 PFLOP/s,
+// 128, a window of 4096: 1.43-1.47 ms a call in rows of calls, which run into the power limit (1.45-1.49 PFLOP/s,
 // 78 % of a large library product's burst rate). An item's first S between the last products of the item before saves some
 // 2 us an item (1.50-1.52 ms with all of an item's products before the next one's); documents of 64 to 2048 tokens
 // lose 1 % by it, 6 prompts of up to 8192 gain 6 % (capped 3 %). S in two halves,
