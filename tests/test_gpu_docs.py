@@ -414,6 +414,8 @@ SPOILED = {  # T, Hq, Hkv, d, starts, prefix, cap, slopes, fused, max_len
     "capped and biased, in runs": (700, 2, 2, 64, [0, 600, 700], None, 5.0, True, False, 0),
     "many items": (1300, 40, 20, 64, [0, 100, 700, 1290], None, 0.0, False, False, 0),
     "many items, capped": (1300, 40, 20, 128, [0, 100, 700, 1290], None, 5.0, False, False, 300),
+    "many items, biased": (1500, 64, 32, 64, [7, 60, 800, 1100, 1500], [3, 0, 250, 9], 0.0, True, True, 200),
+    "group of 64": (260, 64, 1, 64, [0, 100, 190, 260], [20, 0, 7], 0.0, True, False, 0),
 }
 
 
@@ -458,3 +460,38 @@ def test_a_batch_of_nothing_but_nan_ends():
     want, tol = doc_attention(*(t[:100] for t in clean[:3]), [0, 100], dO=clean[3][:100])
     for n in want:
         check(n, got[n][:, :100] if n == "lse" else got[n][:100], want[n], tol[n])
+
+
+def test_what_is_not_finite_in_a_graph():
+    # the same bits in every call, captured or not, and nothing is left behind for finite values
+    Q, K, V, dO = _inputs(1300, 40, 20, 64, seed=22)
+    clean = [t.clone() for t in (Q, K, V, dO)]
+    starts = _ints([0, 300, 900, 1300])
+    s = pisa.doc_shape_of(Q, K, V, starts)
+    ws, wb = (pisa.doc_workspace(s, op, Q.device) for op in (pisa.DOC_FWD, pisa.DOC_BWD))
+
+    def step():
+        O, lse = pisa.doc_attn_fwd(Q, K, V, starts, s, ws=ws)
+        return O, lse, *pisa.doc_attn_bwd(Q, K, V, O, lse, dO, starts, s, ws=wb)
+
+    want = [[t.clone() for t in step()]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for t, at in ((Q, (310, 3)), (K, (500, 7)), (V, (880, 1)), (dO, (301, 39))):
+        t[at][5] = math.nan
+    want.append([t.clone() for t in step()])
+    for k in (1, 1, 0, 1):
+        for t, c in zip((Q, K, V, dO), clean):
+            bad = [(310, 3), (500, 7), (880, 1), (301, 39)]
+            for at in bad:
+                if at[1] < t.shape[1]:
+                    t[at] = c[at]
+        if k:
+            for t, at in ((Q, (310, 3)), (K, (500, 7)), (V, (880, 1)), (dO, (301, 39))):
+                t[at][5] = math.nan
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[k]):
+            assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(nan=9e9), b.nan_to_num(nan=9e9))
+    assert pisa.workspace_status(ws) == 0 and pisa.workspace_status(wb) == 0
