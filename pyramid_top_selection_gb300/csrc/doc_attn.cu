@@ -8,8 +8,8 @@
 //
 // Bound by the window kernel's MMA warp where scores are as they are, by the softmax warps' chain where they are capped
 // (masks.cuh). Six prompts of 1500 to 8192 tokens, 16 heads over 2, d = 128: 423 us (1.52 PFLOP/s of what tokens see), biased
-// 480-494, capped 685-692 (935 TFLOP/s), both 722; with scores beyond the polynomial's range (a cap of 10) 841. 35K tokens in 60
-// documents of 64 to 2048, 16 heads over 4: 189 us, a fifth of whose tiles' area is not seen; biased 213, capped 293.
+// 480-494, capped 680 (945 TFLOP/s), both 722; with scores beyond the polynomial's range (a cap of 10) 831. 35K tokens in 60
+// documents of 64 to 2048, 16 heads over 4: 190 us, a fifth of whose tiles' area is not seen; biased 211, capped 290.
 #include <algorithm>
 
 #include "doc_rows.cuh"

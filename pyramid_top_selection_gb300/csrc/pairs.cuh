@@ -4,10 +4,9 @@
 // NaN is NaN. So one document's bad token would reach its neighbours', and a row the ones behind it, wherever they share a tile.
 // The kernels therefore look at what they put out (a multiply-add for two values); where that is not finite and something that
 // the row does not see is not finite either, a warp forms the row again from the pairs that it does see, before the kernel
-// ends. Nothing of this runs where values are finite; its code and the look at the outputs cost the capped forward 1.3 to 2.6 %
-// (six prompts 677 -> 687 us, 60 documents 286 -> 293), the others and the backward 1 % at most. With one infinity a forward of
-// six prompts takes 44 ms instead of 0.7, and a training pass of 60 documents of up to 2048 tokens 3.8 instead of 0.8; with a
-// channel of infinities 262 and 98.
+// ends. Nothing of this runs where values are finite; its code and the look at the outputs cost no more than 1.5 % (six prompts capped
+// 677 -> 680 us, 60 documents capped 286 -> 290, not capped 187 -> 190). With one infinity a forward of six prompts takes 23 ms instead
+// of 0.7, and a training pass of 60 documents of up to 2048 tokens 3.7 instead of 0.8; with a channel of infinities 124 and 63.
 #pragma once
 
 #include "device.cuh"
@@ -71,7 +70,7 @@ __device__ __forceinline__ bool rows_not_finite(const __nv_bfloat16* rows, int64
 template <int D>
 __device__ __forceinline__ float row_product(const __nv_bfloat16* a, const __nv_bfloat16* b) {
   float s = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int c = 0; c < D / 8; ++c) {
     const uint4 x = ldg_u4(a + 8 * c), y = ldg_u4(b + 8 * c);
     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
@@ -96,7 +95,7 @@ struct RowSum {
   // lane k's weight times row k (stride elements apart), k < n
   __device__ __forceinline__ void add(float weight, const __nv_bfloat16* rows, int64_t stride, int n) {
     const __nv_bfloat16* at = rows + E * (threadIdx.x & 31);
-#pragma unroll 1
+#pragma unroll 4
     for (int k = 0; k < n; ++k, at += stride) {
       const float w = __shfl_sync(0xffffffffu, weight, k);
       uint32_t u[E / 2];

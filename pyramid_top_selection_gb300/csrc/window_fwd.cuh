@@ -405,7 +405,7 @@ window_fwd_kernel(const FwdArgs a, const __grid_constant__ CUtensorMap qmap, con
     win::Distance dist;
     int n_s = 0, n_kv = 0;                     // key tiles done by this row tile; stages used by earlier items
     // Whether a row came out as it may not be: in a register where scores are capped, in shared memory where not, which the compiler's
-    // registers in the loop want so (six prompts capped 687 us and 739 the other way, uncapped 424 and 445).
+    // registers in the loop want so (six prompts capped 680 us and 739 the other way, uncapped 422 and 445).
     bool spoiled = false;
     int i = 0;
     for (int n = 0;; ++i, n_kv += 2 * n) {
